@@ -329,6 +329,179 @@ size_t ll_linear_workspace_size(int32_t m, int32_t n, int32_t k);
 int ll_linear(const void* x, const void* w, void* y, int32_t m, int32_t n, int32_t k,
               void* workspace, size_t workspace_bytes, int32_t* status, void* stream);
 
+/* ---- Operators around the cache that the layer does not fuse.  The pages name
+ * the steps (RotaryEmbedding, the paged cache and its quantisation); the forms
+ * below (frequency scaling, scales per block, block copies) are this library's. */
+
+#define LL_BF16 0
+#define LL_F32 1
+
+#define LL_ROPE_HALF 0         /* pair i is elements (i, i + rotary_dim / 2) */
+#define LL_ROPE_INTERLEAVED 1  /* pair i is elements (2 i, 2 i + 1) */
+
+#define LL_ROPE_FORWARD 0
+#define LL_ROPE_BACKWARD 1     /* the gradient: the transposed rotation */
+
+/* Inverse frequencies w_i = theta^(-2 i / rotary_dim), i < rotary_dim / 2, and
+ * how a table scales them for contexts beyond the trained one: */
+#define LL_ROPE_PLAIN 0        /* w */
+#define LL_ROPE_LINEAR 1       /* w / factor */
+#define LL_ROPE_NTK 2          /* w with theta * factor^(rotary_dim / (rotary_dim - 2)) */
+#define LL_ROPE_BANDED 3       /* pairs that turn >= high_turns times over original_max_position keep w, those
+                                * that turn <= low_turns times get w / factor, linear in the turns between */
+#define LL_ROPE_YARN 4         /* the same two ends, linear in the pair index between the pairs (rounded
+                                * outwards) that turn high_turns and low_turns times; cos and sin times
+                                * attention_factor (0: 0.1 ln(factor) + 1) */
+
+/* rotary_dim even, 2 .. 1024; theta > 1; factor >= 1 unless plain.  The fields
+ * from original_max_position on are read for BANDED and YARN only
+ * (attention_factor for YARN only): 0 < low_turns < high_turns. */
+typedef struct {
+    int32_t rotary_dim;
+    int32_t scaling;
+    float theta;
+    float factor;
+    int32_t original_max_position;
+    float low_turns, high_turns;
+    float attention_factor;
+} ll_rope_config;
+
+/* Bytes of a cos/sin table of max_position positions (0 if cfg is invalid). */
+size_t ll_rope_table_size(const ll_rope_config* cfg, int32_t max_position);
+
+/* Fills `table` (device, 16-byte aligned): float32 [max_position][rotary_dim / 2]
+ * pairs (cos, sin) of position * frequency, computed in float64.  Setup-time
+ * call, asynchronous on `stream`. */
+int ll_rope_table(const ll_rope_config* cfg, int32_t max_position, void* table, size_t table_bytes, void* stream);
+
+/* The same table into packed weights (ll_pack_weights of `cfg`), in place of the
+ * plain one: every layer call with `packed` then rotates by the scaled
+ * frequencies.  rope->rotary_dim must be cfg->head_dim (the layer rotates whole
+ * heads, half-split).  Must not run while a layer call reads `packed`. */
+int ll_pack_rope(const ll_config* cfg, const ll_rope_config* rope, void* packed, size_t packed_bytes, void* stream);
+
+/* Rotary positions: q [tokens, n_heads, head_dim] and k [tokens, n_kv_heads,
+ * head_dim] of `dtype` (LL_BF16 or LL_F32), rows of tokens q_stride and k_stride
+ * elements apart (views of a merged QKV output).  Pair i of every head turns by
+ * the angle of table[positions[t]][i]: (a, b) -> (a c - b s, b c + a s), float32
+ * arithmetic, rounded once; LL_ROPE_BACKWARD is the transpose (s -> -s), the
+ * gradient of the forward call.  Elements from rotary_dim on are copied.  Either
+ * of q and k may be left out (its head count 0).  An output may be its input
+ * (same pointer and stride); otherwise it must not overlap the inputs or the other
+ * output.  A token whose position is outside 0 .. max_position - 1 sets
+ * LL_DEV_BAD_POSITION and its rows are not written.  head_dim <= 1024. */
+int ll_rope(const void* q, const void* k, int32_t dtype, const int32_t* positions, int32_t tokens, int32_t n_heads,
+            int32_t n_kv_heads, int32_t head_dim, int32_t rotary_dim, int32_t layout, int32_t direction, int64_t q_stride,
+            int64_t k_stride, const void* table, int32_t max_position, void* q_out, void* k_out, int64_t q_out_stride,
+            int64_t k_out_stride, int32_t* status, void* stream);
+
+/* A KV pool of 8-bit floating-point codes (e4m3, largest 448) with one float32
+ * scale per block of tokens and KV head.  A cached row reads back as code *
+ * scale.  ll_append_to_cache_f8 writes powers of two as scales; the attention
+ * takes any finite scales >= 0 (0: the block's rows are zeros). */
+typedef struct {
+    void* k;              /* e4m3 [num_blocks, n_kv_heads, block_size, head_dim] */
+    void* v;              /* same shape */
+    float* k_scale;       /* float32 [num_blocks, n_kv_heads] */
+    float* v_scale;       /* same shape */
+    int32_t num_blocks;
+} ll_kv_pool_f8;
+
+/* Appends new tokens' K and V (after RoPE) to an e4m3 cache.  k, v BF16 [tokens,
+ * n_kv_heads, head_dim], rows of tokens k_stride and v_stride elements apart
+ * (multiples of 8).  Sequence b's new tokens are rows cu_new[b] .. cu_new[b+1]-1
+ * (int32 [batch + 1], device; none where equal, at most max_new) and take
+ * positions context_lens[b] - n .. context_lens[b] - 1 of its block table row
+ * (context_lens counts them).  cu_new NULL: one new token per sequence (tokens =
+ * batch, max_new = 1).
+ * Per block and KV head the scale is the smallest power of two s >= 2^-117 with
+ * |x| <= 448 s for every finite value in the block so far (0 while all are zeros):
+ * a call that writes a block's first token starts the block afresh, a later one
+ * keeps s' = max(s, scale of its rows) and, where that is larger, rounds the
+ * block's earlier rows again to e4m3(code * s / s').  New codes are e4m3(x / s'),
+ * nearest even; infinities saturate, NaN stays NaN.  Bit-exact.  Rows behind the
+ * last new token, and blocks that get no token, keep their bytes.
+ * Two sequences of a call must not append to the same physical block (fork it
+ * with ll_copy_blocks first): its contents would be unspecified.
+ * Counts that do not fit together (n < 0, n > max_new, n > context_lens[b], rows
+ * beyond `tokens`, a context beyond the table) set LL_DEV_BAD_POSITION and skip
+ * the sequence; a bad block sets LL_DEV_BAD_BLOCK and is skipped.  Limits as
+ * ll_paged_attention_decode_f8. */
+int ll_append_to_cache_f8(const void* k, const void* v, int64_t k_stride, int64_t v_stride, const int32_t* cu_new,
+                          int32_t tokens, const int32_t* context_lens, int32_t batch, int32_t max_new, int32_t n_kv_heads,
+                          int32_t head_dim, int32_t block_size, const ll_kv_pool_f8* pool, const int32_t* block_table,
+                          int32_t max_blocks, int32_t* status, void* stream);
+
+/* Workspace bytes for ll_paged_attention_decode_f8 (independent of the context
+ * lengths and of the table's width). */
+size_t ll_attention_decode_f8_workspace_size(int32_t batch, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim);
+
+/* ll_paged_attention_decode over an e4m3 cache: q BF16 [batch, n_heads, head_dim],
+ * one query per sequence over positions 0 .. context_lens[b] - 1, softmax(q k^T *
+ * scale) v; zero rows where there is no key (context length 0, or no valid block).
+ * Whatever lies in the cache behind a context, NaN too, is not read into the
+ * result.  head_dim 64 or 128, n_heads / n_kv_heads <= 16, block_size a power of
+ * two in [16, 256], batch <= 65535, max_blocks * block_size <= 2^30, scale finite
+ * and >= 0.  The workspace needs no initial contents; calls that may overlap on
+ * the GPU (other streams, graphs replayed at once) need one each. */
+int ll_paged_attention_decode_f8(const void* q, const ll_kv_pool_f8* pool, const int32_t* block_table, int32_t max_blocks,
+                                 const int32_t* context_lens, int32_t batch, int32_t n_heads, int32_t n_kv_heads,
+                                 int32_t head_dim, int32_t block_size, float scale, void* out, void* workspace,
+                                 size_t workspace_bytes, int32_t* status, void* stream);
+
+/* Workspace bytes for ll_paged_attention_prefill_f8. */
+size_t ll_attention_prefill_f8_workspace_size(int32_t batch, int32_t tokens, int32_t max_new, int32_t n_heads,
+                                              int32_t n_kv_heads, int32_t head_dim);
+
+/* Causal attention of a ragged batch of new tokens over an e4m3 cache that already
+ * holds them (ll_append_to_cache_f8 with the same cu_new and context_lens): q and
+ * out BF16 [tokens, n_heads, head_dim]; row cu_new[b] + i sits at position p =
+ * context_lens[b] - n + i and attends over positions 0 .. p of its sequence.
+ * Covers prompts, chunks behind a cached prefix and a few tokens per sequence.
+ * Rows of `out` that belong to no sequence, or to one whose counts do not fit
+ * together (LL_DEV_BAD_POSITION, as ll_append_to_cache_f8), are not written.
+ * What lies in the cache behind a sequence's context is not read into the result;
+ * a NaN among the new tokens' V may reach earlier rows of the call.  Limits and
+ * workspace rule as ll_paged_attention_decode_f8. */
+int ll_paged_attention_prefill_f8(const void* q, const int32_t* cu_new, int32_t tokens, const ll_kv_pool_f8* pool,
+                                  const int32_t* block_table, int32_t max_blocks, const int32_t* context_lens,
+                                  int32_t batch, int32_t max_new, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,
+                                  int32_t block_size, float scale, void* out, void* workspace, size_t workspace_bytes,
+                                  int32_t* status, void* stream);
+
+/* One tensor of a pool whose first dimension is the physical block: K or V codes,
+ * or their scales, of one layer. */
+typedef struct {
+    void* data;           /* device, [num_blocks][block_bytes], 4-byte aligned (16: faster) */
+    int64_t block_bytes;  /* a multiple of 4, at most 2^30 */
+} ll_block_tensor;
+
+/* Copies blocks in all tensors at once (the pools of every layer share their block
+ * ids): block pairs[i][0] to block pairs[i][1] (int32 [max_pairs][2], device, 8-byte
+ * aligned), for i below *n_pairs (device int32; NULL: max_pairs; at most max_pairs
+ * are done).  `tensors` is a HOST array, read before the call returns.  A pair (-1,
+ * -1) is skipped; any other id outside 0 .. num_blocks - 1 sets LL_DEV_BAD_BLOCK and
+ * skips the pair.  No block may be the destination of two pairs, or the destination
+ * of one and the source of another: its contents would be unspecified. */
+int ll_copy_blocks(const ll_block_tensor* tensors, int32_t n_tensors, int32_t num_blocks, const int32_t* pairs,
+                   int32_t max_pairs, const int32_t* n_pairs, int32_t* status, void* stream);
+
+/* The plan that packs the blocks in use to the front of a pool.  In use are the
+ * ids >= 0 in block_table [rows, max_blocks]; a block that several rows share
+ * counts once.  With U of them, every block in use at or behind place U moves, in
+ * ascending order, to the free places before U: the fewest moves, and no source is
+ * a destination.  Writes, all int32 on the device:
+ *   new_table [rows, max_blocks]  the table after the moves (may be block_table);
+ *                                 negative entries stay as they are
+ *   pairs [num_blocks / 2][2]     the moves (from, to), then (-1, -1)
+ *   counts [2]                    U and the number of moves
+ *   block_map [num_blocks]        each block's new id, -1 where not in use
+ * An id >= num_blocks sets LL_DEV_BAD_BLOCK and stays as it is.  Then
+ * ll_copy_blocks(tensors, ..., pairs, num_blocks / 2, counts + 1, ...) moves the
+ * contents.  num_blocks <= 524288. */
+int ll_compact_blocks(const int32_t* block_table, int32_t rows, int32_t max_blocks, int32_t num_blocks, int32_t* new_table,
+                      int32_t* pairs, int32_t* counts, int32_t* block_map, int32_t* status, void* stream);
+
 /* Launch tracing, for measurement (off by default).  ll_trace_begin creates
  * 2 * capacity CUDA events on the current device; until ll_trace_end, each
  * kernel launch the library makes is bracketed by two of them, recorded on

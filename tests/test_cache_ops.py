@@ -1,0 +1,266 @@
+"""Host side of the operators around the cache: the oracle's pins, and what the library and the
+binding refuse (CPU)."""
+import ctypes
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import cache_ops as C
+from transformer_decoder_layer_llama_gb300 import api, synth
+
+NULL = ctypes.c_void_p(0)
+FAKE = 1 << 20                      # a non-null, 256-byte-aligned address that nothing on the host reads
+INVALID, UNSUPPORTED, WORKSPACE = api.LL_ERR_INVALID_ARG, api.LL_ERR_UNSUPPORTED, api.LL_ERR_WORKSPACE
+
+
+# ---------------------------------------------------------------- oracle pins
+
+def test_e4m3_codes_against_torch():
+    x = np.concatenate([np.linspace(-500, 500, 4001), np.linspace(-0.1, 0.1, 4001), C.E4M3[:127]])
+    t = torch.from_numpy(np.clip(x, -448, 448)).to(torch.float32)
+    want = t.to(torch.float8_e4m3fn).view(torch.uint8).numpy()
+    assert (C.e4m3_codes(t.double().numpy()) == want).all()
+    assert C.e4m3_codes(np.array([np.inf, -np.inf, 449.0])).tolist() == [0x7E, 0xFE, 0x7E]
+    assert C.E4M3[C.e4m3_codes(np.array([np.nan]))[0]] != C.E4M3[C.e4m3_codes(np.array([np.nan]))[0]]
+
+
+def test_block_scale_is_the_smallest_power_of_two():
+    for amax in (448.0, 448.1, 1e-30, 1.0, 3.0e38, 1e-45):
+        s = C.block_scale(amax)
+        assert amax <= 448 * s and (s == 2.0 ** -117 or amax > 448 * s / 2)
+        assert math.frexp(s)[0] == 0.5
+    assert C.block_scale(0.0) == 0.0
+
+
+def test_append_in_steps_and_at_once_agree_up_to_subnormals():
+    rng = np.random.default_rng(3)
+    n, H, bs, d = 37, 2, 16, 8
+    k, v = rng.normal(size=(2, n, H, d))
+    table = np.array([[2, 0, 1]])
+    mk = lambda: C.PoolF8(np.full((3, H, bs, d), 0x7F, np.uint8), np.full((3, H, bs, d), 0x7F, np.uint8),  # noqa: E731
+                          np.full((3, H), np.nan), np.full((3, H), np.nan))
+    a, b = mk(), mk()
+    a.append(k, v, table, [n], [0, n])
+    for i in range(n):
+        b.append(k[i:i + 1], v[i:i + 1], table, [i + 1], [0, 1])
+    for h in range(H):
+        ka, va, _ = a.rows(table[0], n, h)
+        kb, vb, _ = b.rows(table[0], n, h)
+        assert (a.k_scale[2] == b.k_scale[2]).all()
+        # a code is off by at most half a step, 2^-4 of the value; at most twice in two roundings
+        assert (np.abs(ka - k[:, h]) <= 2 ** -4 * np.abs(k[:, h]) + 2.0 ** -10 * a.k_scale.max()).all()
+        assert (np.abs(kb - k[:, h]) <= 2 ** -4 * np.abs(k[:, h]) + 2.0 ** -9 * b.k_scale.max()).all()
+        assert np.isfinite(va).all() and np.isfinite(vb).all()
+    assert (a.k[1, :, n - 32:] == 0x7F).all()          # rows behind the last token keep their bytes
+
+
+def test_oracle_rope_turns_keep_lengths_and_transpose():
+    rng = np.random.default_rng(1)
+    x, y = rng.normal(size=(2, 5, 3, 12))
+    pos = np.array([0, 1, 7, 100, 131071])
+    for layout in ("half", "interleaved"):
+        f, m = C.inv_freq(8)
+        r = C.rope(x, pos, f, m, layout)
+        assert np.allclose(np.linalg.norm(r, axis=-1), np.linalg.norm(x, axis=-1))
+        assert (r[0] == x[0]).all() and (r[..., 8:] == x[..., 8:]).all()
+        assert np.isclose((r * y).sum(), (x * C.rope(y, pos, f, m, layout, backward=True)).sum())
+    for scaling in ("linear", "ntk", "banded", "yarn"):
+        f, m = C.inv_freq(128, scaling=scaling, factor=8.0, original=4096)
+        w, _ = C.inv_freq(128)
+        assert (f <= w * (1 + 1e-12)).all() and (f >= w / 8 * (1 - 1e-12)).all()
+        assert np.isclose(f[-1], w[-1] / 8) and (scaling == "linear" or np.isclose(f[0], w[0]))
+
+
+def test_oracle_attention_is_the_plain_softmax():
+    rng = np.random.default_rng(2)
+    H, Hkv, d, bs, ctx = 4, 2, 8, 16, 21
+    pool = C.PoolF8(*(np.zeros((4, Hkv, bs, d), np.uint8) for _ in range(2)), *(np.zeros((4, Hkv)) for _ in range(2)))
+    k, v = rng.normal(size=(2, ctx, Hkv, d))
+    pool.append(k, v, [[3, 1]], [ctx], [0, ctx])
+    q = rng.normal(size=(2, H, d))
+    out, _, _ = C.attention_f8(q, pool, [[3, 1]], [ctx], [0, 2], 0.3)
+    for t in range(2):
+        for h in range(H):
+            kk, vv, _ = pool.rows([3, 1], ctx - 1 + t, h // 2)
+            s = kk @ q[t, h] * 0.3
+            p = np.exp(s - s.max())
+            assert np.allclose(out[t, h], p @ vv / p.sum())
+
+
+def test_oracle_compaction_is_minimal():
+    new, moves, U, m = C.compact(np.array([[7, 2, -1], [9, 7, 0]]), 12)
+    assert U == 4 and moves == [(7, 1), (9, 3)]
+    assert new.tolist() == [[1, 2, -1], [3, 1, 0]]
+    assert m.tolist() == [0, -1, 2, -1, -1, -1, -1, 1, -1, 3, -1, -1]
+
+
+# ---------------------------------------------------------------- refusals of the library
+
+def rope_cfg(**kw):
+    return api.make_rope_config(**{"rotary_dim": 64, **kw})
+
+
+@pytest.mark.parametrize("bad", [dict(rotary_dim=0), dict(rotary_dim=7), dict(theta=1.0), dict(theta=math.inf),
+                                 dict(scaling="linear", factor=0.5), dict(scaling="linear", factor=math.nan),
+                                 dict(scaling="ntk", factor=2.0, rotary_dim=2),
+                                 dict(scaling="banded", factor=2.0),
+                                 dict(scaling="yarn", factor=2.0, original_max_position=4096, low_turns=8, high_turns=8),
+                                 dict(scaling="yarn", factor=2.0, original_max_position=4096, attention_factor=-1.0)])
+def test_rope_config_refusals(bad):
+    c = rope_cfg(**bad)
+    assert api.lib.ll_rope_table_size(ctypes.byref(c), 16) == 0
+    assert api.lib.ll_rope_table(ctypes.byref(c), 16, FAKE, 1 << 20, NULL) == INVALID
+
+
+def test_rope_table_sizes_and_refusals():
+    c = rope_cfg()
+    assert api.lib.ll_rope_table_size(ctypes.byref(c), 100) == 100 * 32 * 8
+    assert api.lib.ll_rope_table_size(ctypes.byref(c), 0) == 0
+    f = lambda *a: api.lib.ll_rope_table(ctypes.byref(c), *a, NULL)  # noqa: E731
+    assert f(100, NULL, 1 << 20) == INVALID and f(100, FAKE + 4, 1 << 20) == INVALID
+    assert f(100, FAKE, 100 * 32 * 8 - 1) == INVALID
+    big = rope_cfg(rotary_dim=2048)
+    assert api.lib.ll_rope_table(ctypes.byref(big), 1, FAKE, 1 << 20, NULL) == UNSUPPORTED
+    layer = api.make_config(synth.DIMS_7B, 128)
+    n = api.packed_weights_size(layer)
+    assert api.lib.ll_pack_rope(ctypes.byref(layer), ctypes.byref(c), FAKE, n, NULL) == INVALID   # 64 of 128
+    whole = rope_cfg(rotary_dim=128)
+    assert api.lib.ll_pack_rope(ctypes.byref(layer), ctypes.byref(whole), FAKE, n - 1, NULL) == INVALID
+    with pytest.raises(ValueError):
+        rope_cfg(scaling="cubic")
+
+
+ROPE = dict(q=FAKE, k=2 * FAKE, dtype=0, positions=FAKE, tokens=4, n_heads=2, n_kv_heads=1, head_dim=64, rotary_dim=64,
+            layout=0, direction=0, q_stride=128, k_stride=64, table=FAKE, max_position=16, q_out=3 * FAKE,
+            k_out=4 * FAKE, q_out_stride=128, k_out_stride=64, status=FAKE)
+
+
+@pytest.mark.parametrize("bad,code", [(dict(dtype=2), INVALID), (dict(layout=2), INVALID), (dict(direction=2), INVALID),
+                                      (dict(positions=0), INVALID), (dict(table=0), INVALID), (dict(table=FAKE + 8), INVALID),
+                                      (dict(status=0), INVALID), (dict(tokens=-1), INVALID),
+                                      (dict(n_heads=0, n_kv_heads=0), INVALID), (dict(n_heads=-1), INVALID),
+                                      (dict(rotary_dim=66), INVALID), (dict(rotary_dim=63), INVALID),
+                                      (dict(rotary_dim=0), INVALID), (dict(q=0), INVALID), (dict(k_out=0), INVALID),
+                                      (dict(q_stride=127), INVALID), (dict(k_out_stride=63), INVALID),
+                                      (dict(q=FAKE + 1), INVALID), (dict(max_position=0), INVALID),
+                                      (dict(head_dim=2048, q_stride=4096, k_stride=2048, q_out_stride=4096,
+                                            k_out_stride=2048), UNSUPPORTED),
+                                      (dict(q_out=FAKE + 128), INVALID), (dict(q_out=2 * FAKE + 2), INVALID),
+                                      (dict(k_out=FAKE + 64), INVALID), (dict(tokens=1 << 25), UNSUPPORTED),
+                                      (dict(q_out=FAKE, q_out_stride=256), INVALID)])
+def test_rope_refusals(bad, code):
+    assert api.lib.ll_rope(*{**ROPE, **bad}.values(), NULL) == code
+
+
+def test_rope_without_tokens_launches_nothing():
+    assert api.lib.ll_rope(*{**ROPE, "tokens": 0}.values(), NULL) == api.LL_OK
+
+
+def pool_f8(**kw):
+    return api.ll_kv_pool_f8(*{**dict(k=FAKE, v=FAKE, k_scale=FAKE, v_scale=FAKE, num_blocks=8), **kw}.values())
+
+
+SHAPES = [(dict(head_dim=96), UNSUPPORTED), (dict(block_size=24), UNSUPPORTED), (dict(block_size=8), UNSUPPORTED),
+          (dict(block_size=512), UNSUPPORTED), (dict(batch=0), INVALID), (dict(max_blocks=0), INVALID),
+          (dict(n_kv_heads=0), INVALID), (dict(block_table=0), INVALID), (dict(context_lens=0), INVALID),
+          (dict(status=0), INVALID), (dict(max_blocks=1 << 27), UNSUPPORTED),
+          (dict(pool=pool_f8(k=0)), INVALID), (dict(pool=pool_f8(v_scale=0)), INVALID),
+          (dict(pool=pool_f8(num_blocks=0)), INVALID), (dict(pool=pool_f8(k=FAKE + 8)), INVALID),
+          (dict(pool=pool_f8(k_scale=FAKE + 2)), INVALID), (dict(pool=pool_f8(num_blocks=1 << 27)), UNSUPPORTED)]
+
+APPEND = dict(k=FAKE, v=FAKE, k_stride=256, v_stride=256, cu_new=FAKE, tokens=4, context_lens=FAKE, batch=2, max_new=4,
+              n_kv_heads=2, head_dim=128, block_size=16, pool=pool_f8(), block_table=FAKE, max_blocks=4, status=FAKE)
+
+
+@pytest.mark.parametrize("bad,code", SHAPES + [(dict(k=0), INVALID), (dict(v=FAKE + 8), INVALID), (dict(k_stride=252), INVALID),
+                                               (dict(v_stride=248), INVALID), (dict(max_new=0), INVALID),
+                                               (dict(cu_new=0), INVALID), (dict(cu_new=0, max_new=1), INVALID),
+                                               (dict(tokens=-1), INVALID), (dict(batch=1 << 17), UNSUPPORTED)])
+def test_append_refusals(bad, code):
+    a = {**APPEND, **bad}
+    a["pool"] = ctypes.byref(a["pool"])
+    assert api.lib.ll_append_to_cache_f8(*a.values(), NULL) == code
+
+
+DECODE = dict(q=FAKE, pool=pool_f8(), block_table=FAKE, max_blocks=4, context_lens=FAKE, batch=2, n_heads=4, n_kv_heads=2,
+              head_dim=128, block_size=16, scale=0.1, out=FAKE, workspace=FAKE, workspace_bytes=1 << 30, status=FAKE)
+PREFILL = dict(q=FAKE, cu_new=FAKE, tokens=4, pool=pool_f8(), block_table=FAKE, max_blocks=4, context_lens=FAKE, batch=2,
+               max_new=4, n_heads=4, n_kv_heads=2, head_dim=128, block_size=16, scale=0.1, out=FAKE, workspace=FAKE,
+               workspace_bytes=1 << 40, status=FAKE)
+ATTN = SHAPES + [(dict(q=0), INVALID), (dict(q=FAKE + 2), INVALID), (dict(out=0), INVALID), (dict(scale=-1.0), INVALID),
+                 (dict(scale=math.nan), INVALID), (dict(scale=math.inf), INVALID), (dict(n_heads=5), UNSUPPORTED),
+                 (dict(n_heads=34), UNSUPPORTED), (dict(workspace=0), WORKSPACE), (dict(workspace=FAKE + 8), WORKSPACE),
+                 (dict(workspace_bytes=0), WORKSPACE)]
+
+
+@pytest.mark.parametrize("bad,code", ATTN)
+def test_decode_f8_refusals(bad, code):
+    a = {**DECODE, **bad}
+    a["pool"] = ctypes.byref(a["pool"])
+    assert api.lib.ll_paged_attention_decode_f8(*a.values(), NULL) == code
+
+
+@pytest.mark.parametrize("bad,code", ATTN + [(dict(cu_new=0), INVALID), (dict(max_new=0), INVALID), (dict(tokens=-1), INVALID)])
+def test_prefill_f8_refusals(bad, code):
+    a = {**PREFILL, **bad}
+    a["pool"] = ctypes.byref(a["pool"])
+    assert api.lib.ll_paged_attention_prefill_f8(*a.values(), NULL) == code
+
+
+def test_f8_workspace_sizes():
+    assert api.attention_decode_f8_workspace_size(4, 32, 8, 128) > 0
+    assert api.attention_decode_f8_workspace_size(4, 32, 5, 128) == 0
+    assert api.attention_decode_f8_workspace_size(4, 32, 8, 96) == 0
+    assert api.attention_decode_f8_workspace_size(0, 32, 8, 128) == 0
+    assert api.attention_prefill_f8_workspace_size(4, 100, 50, 32, 8, 128) > 0
+    assert api.attention_prefill_f8_workspace_size(4, 100, 0, 32, 8, 128) == 0
+
+
+def test_copy_blocks_refusals():
+    def call(tensors, nb=8, pairs=FAKE, n=4, status=FAKE):
+        arr = (api.ll_block_tensor * max(len(tensors), 1))(*tensors)
+        return api.lib.ll_copy_blocks(arr, len(tensors), nb, pairs, n, NULL, status, NULL)
+    ok = (FAKE, 64)
+    assert call([]) == INVALID and call([ok], nb=0) == INVALID and call([ok], pairs=0) == INVALID
+    assert call([ok], n=-1) == INVALID and call([ok], status=0) == INVALID and call([ok], pairs=FAKE + 4) == INVALID
+    assert call([(0, 64)]) == INVALID and call([(FAKE, 0)]) == INVALID and call([(FAKE, 6)]) == INVALID
+    assert call([(FAKE + 2, 64)]) == INVALID and call([ok, (FAKE, 1 << 31)]) == UNSUPPORTED
+    assert call([ok], n=0) == api.LL_OK
+    assert api.lib.ll_copy_blocks(None, 1, 8, FAKE, 1, NULL, FAKE, NULL) == INVALID
+
+
+def test_compact_blocks_refusals():
+    base = dict(table=FAKE, rows=4, max_blocks=8, nb=16, new=FAKE, pairs=FAKE, counts=FAKE, map=FAKE, status=FAKE)
+    call = lambda **kw: api.lib.ll_compact_blocks(*{**base, **kw}.values(), NULL)  # noqa: E731
+    for bad in (dict(table=0), dict(rows=-1), dict(max_blocks=-1), dict(nb=0), dict(new=0), dict(pairs=0), dict(counts=0),
+                dict(map=0), dict(status=0), dict(pairs=FAKE + 4), dict(new=FAKE + 8)):
+        assert call(**bad) == INVALID, bad
+    assert call(nb=(1 << 19) + 1) == UNSUPPORTED
+
+
+def test_binding_refuses_cpu_tensors_and_wrong_types():
+    x = torch.zeros(2, 4, 64, dtype=torch.bfloat16)
+    pos = torch.zeros(2, dtype=torch.int32)
+    tab = torch.zeros(8, 32, 2)
+    with pytest.raises(ValueError, match="GPU"):
+        api.rope(x, x, pos, tab)
+    with pytest.raises(TypeError):
+        api.rope(x.half(), None, pos, tab)
+    with pytest.raises(ValueError, match="layout"):
+        api.rope(x, None, pos, tab, layout="other")
+    with pytest.raises(ValueError):
+        api.rope(None, None, pos, tab)
+    codes = torch.zeros(4, 2, 16, 64, dtype=torch.uint8)
+    with pytest.raises(TypeError):
+        api.PoolF8(codes, codes, torch.zeros(4, 2), torch.zeros(4, 2))
+    f8 = codes.view(torch.float8_e4m3fn)
+    with pytest.raises(ValueError, match="GPU"):
+        api.PoolF8(f8, f8, torch.zeros(4, 2), torch.zeros(4, 2))
+    with pytest.raises(ValueError):
+        api.BlockSet([])
+    with pytest.raises(ValueError):
+        api.BlockSet([codes])
+    with pytest.raises(ValueError, match="GPU"):
+        api.compact_blocks(torch.zeros(2, 2, dtype=torch.int32), 8)

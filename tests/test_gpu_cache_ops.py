@@ -1,0 +1,643 @@
+"""The operators around the cache against their float64 definitions on a GPU.
+
+Tolerances.  Rounding errors relative to the value: BF16 2^-8, FP16 2^-11, float32 2^-24, counted once
+for each rounding on the way:
+* rope: c and s come from a float32 table (2^-24 each), each product and the sum round once in float32:
+  4 * 2^-24 * magnitude * (|a| + |b|) covers them, then one rounding to the output's type.
+* attention: a probability enters P V as FP16 (2^-11 relative; below 2^-14 of its base FP16 is
+  subnormal, an absolute 2^-25, and the base is at most 2^8 above the row's largest and 2^6 shifted, so
+  2^-30 of the largest |v| per key at most, in fact far less in sum), its exponent carries the score's
+  float32 error (d products and sums on the tensor core, which may cut instead of round: 2^-23 each of
+  sum |q k| scale, and 2^-22 of the score for the factor), exp2 itself 2^-21, and the sums of n weights
+  and products in float32 cut n / 16 + n / 128 times 2^-23.  Weighted by sum p |v|.
+  Then one rounding to BF16.
+* codes, scales, tables of ids and copied bytes are exact.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import cache_ops as C
+from tests.helpers import f64
+from transformer_decoder_layer_llama_gb300 import synth
+
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    from transformer_decoder_layer_llama_gb300 import api
+
+F8 = torch.float8_e4m3fn
+UNIT = {torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 ** -24}
+
+
+def dev(x, dtype=torch.int32):
+    return torch.as_tensor(np.asarray(x), dtype=dtype).cuda()
+
+
+def status():
+    return api.new_status()
+
+
+def check(st, want=0):
+    torch.cuda.synchronize()
+    assert int(st.item()) == want
+
+
+# ---------------------------------------------------------------- rope
+
+def rope_bound(x, freq, magnitude, layout, dtype, ref):
+    half = len(freq)
+    pair = np.zeros_like(x)
+    i0 = np.arange(half) if layout == "half" else 2 * np.arange(half)
+    i1 = i0 + half if layout == "half" else i0 + 1
+    s = np.abs(x[..., i0]) + np.abs(x[..., i1])
+    pair[..., i0] = pair[..., i1] = s * magnitude
+    return 4 * 2.0 ** -24 * pair + (UNIT[dtype] * np.abs(ref) if dtype != torch.float32 else 0) + 2.0 ** -140
+
+
+ROPE_CASES = [  # tokens, heads, kv_heads, dim, rot, scaling
+    (1, 1, 1, 64, 64, "plain"), (7, 4, 2, 128, 128, "plain"), (33, 5, 1, 128, 64, "linear"), (3, 8, 8, 64, 10, "ntk"),
+    (64, 32, 32, 128, 128, "banded"), (5, 3, 2, 96, 34, "yarn"), (129, 64, 8, 128, 128, "yarn"), (2, 2, 0, 24, 8, "plain"),
+    (1025, 64, 8, 128, 32, "banded"), (9, 1, 3, 256, 256, "plain"), (4, 2, 1, 80, 2, "plain")]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("backward", [False, True])
+@pytest.mark.parametrize("case", ROPE_CASES)
+def test_rope_matches_the_definition(case, layout, backward, dtype):
+    T, H, Hk, d, rot, scaling = case
+    g = torch.Generator().manual_seed(T * 1000 + rot)
+    qkv = torch.randn(T, (H + 2 * Hk) * d + 8, generator=g).to(dtype).cuda()
+    q, k = qkv[:, :H * d].view(T, H, d), qkv[:, H * d:(H + Hk) * d].view(T, Hk, d)
+    before = qkv.clone()
+    maxpos = 140000
+    pos = torch.randint(0, maxpos, (T,), generator=g, dtype=torch.int32)
+    kw = dict(factor=8.0, original_max_position=4096) if scaling != "plain" else {}
+    table = api.rope_table(api.make_rope_config(rot, scaling=scaling, **kw), maxpos)
+    st = status()
+    q2, k2 = api.rope(q, k if Hk else None, pos.cuda(), table, layout=layout, backward=backward, status=st)
+    check(st)
+    f, m = C.inv_freq(rot, scaling=scaling, factor=kw.get("factor", 1.0), original=4096)
+    for x, got in ((q, q2), (k, k2)) if Hk else ((q, q2),):
+        xn = f64(x)
+        ref = C.rope(xn, pos.numpy(), f, m, layout, backward)
+        assert got.is_contiguous() and got.dtype == dtype
+        assert (np.abs(f64(got) - ref) <= rope_bound(xn, f, m, layout, dtype, ref)).all()
+        assert (f64(got)[..., rot:] == xn[..., rot:]).all()
+    assert torch.equal(qkv, before)                                      # the inputs are left alone
+    # in place, through the views: the same bits, and nothing else of the merged rows changes
+    api.rope(q, k if Hk else None, pos.cuda(), table, layout=layout, backward=backward, q_out=q,
+             k_out=k if Hk else None, status=st)
+    check(st)
+    assert torch.equal(q, q2) and (not Hk or torch.equal(k, k2))
+    assert torch.equal(qkv[:, (H + Hk) * d:], before[:, (H + Hk) * d:])
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_rope_gradient_is_the_transpose_and_the_difference_quotient(layout):
+    T, H, d, rot = 6, 3, 64, 48
+    g = torch.Generator().manual_seed(4)
+    x, y, h = (torch.randn(T, H, d, generator=g).cuda() for _ in range(3))
+    pos = dev([0, 1, 5, 99, 1000, 4095])
+    table = api.rope_table(api.make_rope_config(rot, scaling="yarn", factor=4.0, original_max_position=1024), 4096)
+    fwd = lambda t: f64(api.rope(t, None, pos, table, layout=layout)[0])  # noqa: E731
+    grad = f64(api.rope(y, None, pos, table, layout=layout, backward=True)[0])
+    # <R(x), y> is linear in x, so its difference along h is <grad, h> but for rounding
+    diff = ((fwd(x + h) - fwd(x)) * f64(y)).sum()
+    bound = 2.0 ** -20 * (np.abs(f64(x)) + np.abs(f64(h))).sum() * np.abs(f64(y)).max()
+    assert abs(diff - (grad * f64(h)).sum()) <= bound
+    assert abs((fwd(x) * f64(y)).sum() - (f64(x) * grad).sum()) <= bound
+
+
+def test_rope_bad_positions_are_flagged_and_left():
+    q = torch.randn(5, 2, 64).bfloat16().cuda()
+    table = api.rope_table(api.make_rope_config(64), 16)
+    out = torch.full_like(q, 7.0)
+    for stride_view in (False, True):
+        st = status()
+        api.rope(q, None, dev([0, -1, 15, 16, 3]), table, q_out=out, status=st)
+        check(st, api.LL_DEV_BAD_POSITION)
+        assert (out[[1, 3]] == 7).all() and torch.equal(out[0], q[0]) and not (out[[2, 4]] == 7).all()
+    with pytest.raises(api.LayerError):                                  # shifted onto its own input
+        flat = torch.zeros(5 * 128 + 64, dtype=torch.bfloat16, device="cuda")
+        api.rope(flat[:640].view(5, 2, 64), None, dev([0] * 5), table, q_out=flat[64:].view(5, 2, 64))
+    with pytest.raises(ValueError):
+        api.rope(q, None, dev([0] * 5), table, q_out=out[:, :1])
+    with pytest.raises(ValueError):
+        api.rope(q.transpose(0, 1), None, dev([0] * 2), table)
+
+
+def test_rope_special_values_and_empty():
+    table = api.rope_table(api.make_rope_config(4), 4)
+    q = torch.tensor([[[float("inf"), 1.0, 2.0, float("nan"), 3.0, -0.0, 5.0, 6.0]]]).cuda()
+    out, _ = api.rope(q, None, dev([0]), table)                          # position 0: c = 1, s = 0
+    assert torch.isinf(out[0, 0, 0]) and torch.isnan(out[0, 0, 3]) and torch.isnan(out[0, 0, 2])
+    assert torch.equal(out[0, 0, 4:], q[0, 0, 4:])
+    e, _ = api.rope(q[:0], None, dev([]), table)
+    assert e.shape == (0, 1, 8)
+
+
+def test_pack_rope_rescales_the_layer():
+    """The plain configuration packs the table that ll_pack_weights made; under interpolation by 2 position 2 p
+    turns as p did."""
+    d = synth.DIMS_TINY
+    W = {k: v.cuda() for k, v in synth.make_weights(d, 0.02, seed=1).items()}
+    cfg = api.make_config(d, max_position=64)
+    base = api.pack_weights(cfg, W)
+    same = base.clone()
+    api.pack_rope(cfg, api.make_rope_config(d.head_dim, theta=d.rope_theta), same)
+    assert torch.equal(base, same)
+    api.pack_rope(cfg, api.make_rope_config(d.head_dim, theta=d.rope_theta, scaling="linear", factor=2.0), same)
+    x = synth.make_x(8, d.hidden, seed=2).cuda()
+    kp, vp = (t.cuda() for t in synth.make_pool(8, d, seed=3))
+    table = dev([[0, 1, 2, 3]])
+    q = []
+    for packed, step in ((base, 1), (same, 2)):
+        ws = api.new_workspace(cfg, 8, 4)
+        api.layer_prefill(cfg, packed, x, dev(np.arange(8) * step), 1, 8, kp, vp, table, workspace=ws)
+        torch.cuda.synchronize()
+        q.append(api.checkpoints(cfg, ws, 8, 4, 8)["q"].clone())
+    assert torch.equal(q[0], q[1])
+
+
+# ---------------------------------------------------------------- the e4m3 cache
+
+def make_cache(rng, ctx, Hkv, d, bs, extra=2, poison=True, spread=0.5):
+    """(oracle pool, table) of cached contexts: values of differing size, blocks in random order, -1 behind a
+    sequence's blocks, NaN codes in every row that holds no token."""
+    need = [-(-c // bs) for c in ctx]
+    nb = sum(need) + extra
+    table = np.full((len(ctx), max(need + [1]) + 1), -1, np.int32)
+    perm = rng.permutation(nb).astype(np.int32)
+    at = 0
+    for b, n in enumerate(need):
+        table[b, :n] = perm[at:at + n]
+        at += n
+    fill = 0x7F if poison else 0
+    pool = C.PoolF8(*(np.full((nb, Hkv, bs, d), fill, np.uint8) for _ in range(2)), *(np.full((nb, Hkv), np.nan) for _ in range(2)))
+    size = np.exp(spread * rng.normal(size=(1, Hkv, 1)))
+    T = int(sum(ctx))
+    k, v = (bf16(rng.normal(size=(T, Hkv, d)) * size) for _ in range(2))
+    cu = np.concatenate([[0], np.cumsum(ctx)]).astype(int)
+    pool.append(k, v, table, ctx, cu)
+    return pool, table
+
+
+def bf16(x):
+    return torch.as_tensor(x).bfloat16().double().numpy()
+
+
+def to_gpu(pool):
+    return api.PoolF8(*(torch.from_numpy(c.copy()).cuda().view(F8) for c in (pool.k, pool.v)),
+                      *(torch.from_numpy(s.astype(np.float32)).cuda() for s in (pool.k_scale, pool.v_scale)))
+
+
+def copy_pool(p):
+    return C.PoolF8(p.k.copy(), p.v.copy(), p.k_scale.copy(), p.v_scale.copy())
+
+
+def assert_pool(gpu, ref):
+    for name in ("k", "v"):
+        got = getattr(gpu, name).view(torch.uint8).cpu().numpy()
+        want = getattr(ref, name)
+        # -0 and +0 are the same value
+        bad = (got != want) & ~(((got | want) & 0x7F) == 0)
+        assert not bad.any(), (name, int(bad.sum()), np.argwhere(bad)[:4], got[bad][:4], want[bad][:4])
+        s = getattr(gpu, name + "_scale").cpu().numpy().astype(np.float64)
+        assert np.array_equal(s, getattr(ref, name + "_scale"), equal_nan=True)
+
+
+APPEND_CASES = [  # block, kv_heads, dim, contexts before, new tokens
+    (16, 1, 64, [0], [1]), (16, 2, 128, [0, 5, 15, 16, 17], [1, 1, 1, 1, 1]), (256, 3, 128, [255, 256, 100, 0], [1, 1, 1, 1]),
+    (64, 32, 128, [63, 1, 64], [1, 1, 1]), (16, 2, 64, [0, 3, 40], [100, 0, 7]), (32, 1, 128, [31, 32], [1, 33]),
+    (64, 2, 128, [10, 0, 130], [300, 64, 63]), (128, 4, 64, [127, 5], [2, 250]), (128, 2, 128, [1, 128], [127, 128]),
+    (256, 2, 128, [3, 255], [600, 2]), (256, 1, 64, [100], [400])]
+
+
+@pytest.mark.parametrize("case", APPEND_CASES)
+def test_append_matches_the_definition(case):
+    bs, Hkv, d, before, new = case
+    rng = np.random.default_rng(bs + Hkv + sum(new))
+    ctx = [b + n for b, n in zip(before, new)]
+    cu = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    T = int(cu[-1])
+    ref, table = make_cache(rng, ctx, Hkv, d, bs)      # every block of the contexts is in the table
+    old, _ = make_cache(rng, before, Hkv, d, bs, extra=len(ref.k) - sum(-(-b // bs) for b in before))
+    ref = copy_pool(old)
+    # lay the earlier rows where the table has them, with their scales
+    ref.k[:], ref.v[:], ref.k_scale[:], ref.v_scale[:] = 0x7F, 0x7F, np.nan, np.nan
+    kb, vb = (bf16(0.1 * rng.normal(size=(sum(before), Hkv, d))) for _ in range(2))
+    ref.append(kb, vb, table, before, np.concatenate([[0], np.cumsum(before)]).astype(int))
+    gpu = to_gpu(ref)
+    # magnitudes that make some blocks grow and others not; zeros, huge and tiny values, both infinities, NaN
+    k, v = (rng.normal(size=(T, Hkv, d)) * np.exp(2 * rng.normal(size=(T, Hkv, 1))) for _ in range(2))
+    if T > 4:
+        k[0], v[1, 0], k[2, 0, 0], v[2, -1, 1], k[3, 0, 2] = 0.0, 1e-37, np.inf, -np.inf, np.nan
+        v[3, 0, 3] = 3.3e38
+    k, v = bf16(k), bf16(v)
+    wide = torch.zeros(T, 2 * Hkv * d + 8, dtype=torch.bfloat16, device="cuda")
+    kt, vt = wide[:, :Hkv * d].view(T, Hkv, d), wide[:, Hkv * d:2 * Hkv * d].view(T, Hkv, d)
+    kt.copy_(torch.from_numpy(k))
+    vt.copy_(torch.from_numpy(v))
+    ref.append(k, v, table, ctx, cu)
+    st = status()
+    one = all(n == 1 for n in new)
+    for cu_arg in ([None] if one else []) + [dev(cu)]:   # one token each: both ways to say it
+        pool = api.PoolF8(gpu.k.clone(), gpu.v.clone(), gpu.k_scale.clone(), gpu.v_scale.clone())
+        api.append_to_cache_f8(kt, vt, pool, dev(table), dev(ctx), cu_new=cu_arg, max_new=max(new), status=st)
+        check(st)
+        assert_pool(pool, ref)
+
+
+def test_append_zeros_then_values_and_a_fresh_start():
+    """A block of zeros has scale 0; a call that writes offset 0 forgets what the block held."""
+    ref = C.PoolF8(*(np.full((2, 1, 16, 64), 0x55, np.uint8) for _ in range(2)), *(np.full((2, 1), 2.0 ** 60) for _ in range(2)))
+    pool, table = to_gpu(ref), [[1, 0]]
+    st = status()
+    rng = np.random.default_rng(0)
+    for ctx, x in ((1, 0.0), (2, 0.0), (3, 1.0), (4, 1000.0), (5, 1e-3)):
+        k = bf16(rng.normal(size=(1, 1, 64)) * x)
+        ref.append(k, -k, table, [ctx], [0, 1])
+        t = torch.from_numpy(k).bfloat16().cuda()
+        api.append_to_cache_f8(t, -t, pool, dev(table), dev([ctx]), status=st)
+        check(st)
+        assert_pool(pool, ref)
+
+
+def test_append_flags_bad_counts_and_blocks():
+    rng = np.random.default_rng(5)
+    ref, table = make_cache(rng, [20, 20, 20], 2, 64, 16)
+    T = 9
+    k = bf16(rng.normal(size=(T, 2, 64)))
+    t = torch.from_numpy(k).bfloat16().cuda()
+    bad_table = table.copy()
+    bad_table[1, 1], bad_table[2, 1] = len(ref.k), -1
+    for cu, ctx, mx, tab, want in (([0, 3, 3, 3], [2, 20, 20], 3, table, api.LL_DEV_BAD_POSITION),       # n > context
+                                   ([0, 0, 4, 4], [20, 20, 20], 3, table, api.LL_DEV_BAD_POSITION),      # n > max_new
+                                   ([0, 0, 0, 12], [20, 20, 20], 20, table, api.LL_DEV_BAD_POSITION),    # beyond tokens
+                                   ([5, 5, 5, 2], [20, 20, 20], 9, table, api.LL_DEV_BAD_POSITION),      # n < 0
+                                   ([-1, 1, 1, 1], [20, 20, 20], 9, table, api.LL_DEV_BAD_POSITION),
+                                   ([0, 3, 3, 3], [1000, 20, 20], 3, table, api.LL_DEV_BAD_POSITION),    # beyond the table
+                                   ([0, 0, 3, 6], [20, 20, 20], 3, bad_table, api.LL_DEV_BAD_BLOCK)):
+        gpu = to_gpu(ref)
+        st = status()
+        api.append_to_cache_f8(t, t, gpu, dev(tab), dev(ctx), cu_new=dev(cu), max_new=mx, status=st)
+        check(st, want)
+        assert_pool(gpu, ref)                                            # nothing was written
+    gpu = to_gpu(ref)
+    st = status()
+    api.append_to_cache_f8(t[:3], t[:3], gpu, dev(bad_table), dev([0, 20, 20]), status=st)
+    check(st, api.LL_DEV_BAD_BLOCK | api.LL_DEV_BAD_POSITION)
+    assert_pool(gpu, ref)
+
+
+# ---------------------------------------------------------------- attention over it
+
+def attention_bound(ref, weight, info, d):
+    mag, n, vmax = info[..., :1], info[..., 1:2], info[..., 2:]
+    score = 2.0 ** -23 * (d + 4) * mag
+    rel = 2.0 ** -11 + score + 2.0 ** -20 + (n / 16 + n / 128 + 8) * 2.0 ** -23
+    return 2.0 ** -8 * np.abs(ref) + 1.01 * rel * weight + (n + 1) * 2.0 ** -31 * vmax
+
+
+def assert_attention(got, ref, weight, info, d):
+    got = f64(got)
+    bad = ~(np.abs(got - ref) <= attention_bound(ref, weight, info, d))
+    assert not bad.any(), (int(bad.sum()), np.argwhere(bad)[:4], got[bad][:4], ref[bad][:4])
+
+
+DECODE_CASES = [  # block, heads, kv_heads, dim, contexts
+    (16, 4, 2, 64, [1]), (16, 4, 2, 64, [0, 1, 15, 16, 17, 63, 64, 65, 200]), (128, 32, 32, 128, [700, 3, 129]),
+    (128, 64, 8, 128, [1, 2000, 1024]), (64, 16, 1, 128, [777]), (256, 10, 2, 128, [256, 257, 600]),
+    (32, 7, 1, 64, [0, 0, 33]), (16, 12, 4, 128, [5, 100]), (16, 9, 1, 128, [130, 64]), (32, 16, 1, 64, [500, 31]),
+    (128, 2, 2, 128, [5000]), (16, 1, 1, 64, [3000, 0, 7])]
+
+
+@pytest.mark.parametrize("case", DECODE_CASES)
+def test_decode_matches_the_definition(case):
+    bs, H, Hkv, d, ctx = case
+    rng = np.random.default_rng(bs + H + sum(ctx))
+    ref_pool, table = make_cache(rng, ctx, Hkv, d, bs)
+    pool = to_gpu(ref_pool)
+    q = torch.from_numpy(rng.normal(size=(len(ctx), H, d)) * np.exp(rng.normal(size=(len(ctx), H, 1)))).bfloat16()
+    scale = d ** -0.5
+    want = C.attention_f8(f64(q), ref_pool, table, ctx, np.arange(len(ctx) + 1), scale)
+    st = status()
+    ws = torch.full((api.attention_decode_f8_workspace_size(len(ctx), H, Hkv, d),), 0xFF, dtype=torch.uint8, device="cuda")
+    out = torch.full((len(ctx), H, d), float("nan"), dtype=torch.bfloat16, device="cuda")
+    first = None
+    for _ in range(3):                                                   # the same workspace, whatever it holds
+        api.paged_attention_decode_f8(q.cuda(), pool, dev(table), dev(ctx), scale, out=out, workspace=ws, status=st)
+        check(st)
+        assert_attention(out, *want, d)
+        first = out.clone() if first is None else first
+        assert torch.equal(out, first)                                   # the same bits every time
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_decode_scales_of_every_size(d):
+    """Blocks whose scales lie far apart, scale 0, scales that are no powers of two, large and tiny queries."""
+    rng = np.random.default_rng(d)
+    ctx, bs, H, Hkv = [160, 96], 16, 6, 2
+    ref_pool, table = make_cache(rng, ctx, Hkv, d, bs)
+    live = ref_pool.k_scale == ref_pool.k_scale
+    sizes = np.array([1.0, 0.37, 2.0 ** -12, 0.0, 1.9, 2.0 ** -20])
+    for s in (ref_pool.k_scale, ref_pool.v_scale):
+        s[live] = (rng.choice(sizes, size=s.shape) * 2.0 ** -6)[live]
+    ref_pool.k_scale[live] = np.float32(ref_pool.k_scale[live]).astype(np.float64)
+    ref_pool.v_scale[live] = np.float32(ref_pool.v_scale[live]).astype(np.float64)
+    for size in (1.0, 1e-20, 30.0):
+        q = torch.from_numpy(rng.normal(size=(2, H, d)) * size).bfloat16()
+        ref, weight, info = C.attention_f8(f64(q), ref_pool, table, ctx, [0, 1, 2], 0.1)
+        st = status()
+        out = api.paged_attention_decode_f8(q.cuda(), to_gpu(ref_pool), dev(table), dev(ctx), 0.1, status=st)
+        pre = api.paged_attention_prefill_f8(q.cuda(), dev([0, 1, 2]), to_gpu(ref_pool), dev(table), dev(ctx), 0.1,
+                                             max_new=1, status=st)
+        check(st)
+        # a scale that is no power of two costs one more FP16 rounding, of the block's V (prefill) or of P (decode)
+        extra = 2.0 ** -11 * weight
+        for got in (out, pre):
+            assert (np.abs(f64(got) - ref) <= attention_bound(ref, weight, info, d) + extra).all()
+
+
+def test_decode_of_a_tiny_cache_keeps_its_size():
+    """V of 1e-30 next to nothing larger comes back at its own size."""
+    rng = np.random.default_rng(7)
+    pool, table = make_cache(rng, [40], 1, 64, 16)
+    live = pool.v_scale == pool.v_scale
+    pool.v_scale[live] *= 2.0 ** -100
+    q = torch.from_numpy(rng.normal(size=(1, 2, 64))).bfloat16()
+    want = C.attention_f8(f64(q), pool, table, [40], [0, 1], 0.1)
+    for got in (api.paged_attention_decode_f8(q.cuda(), to_gpu(pool), dev(table), dev([40]), 0.1),
+                api.paged_attention_prefill_f8(q.cuda(), dev([0, 1]), to_gpu(pool), dev(table), dev([40]), 0.1, max_new=1)):
+        assert_attention(got, *want, 64)
+
+
+def test_attention_bad_blocks_and_contexts():
+    rng = np.random.default_rng(11)
+    pool, table = make_cache(rng, [100, 50, 16], 2, 64, 16)
+    gpu = to_gpu(pool)
+    table[0, 2], table[0, 4], table[2, 0] = -1, len(pool.k) + 5, -7      # holes, and a sequence without any block
+    q = torch.from_numpy(rng.normal(size=(3, 4, 64))).bfloat16()
+    want = C.attention_f8(f64(q), pool, table, [100, 50, 16], [0, 1, 2, 3], 0.1)
+    for call in (lambda st, ctx: api.paged_attention_decode_f8(q.cuda(), gpu, dev(table), dev(ctx), 0.1, status=st),
+                 lambda st, ctx: api.paged_attention_prefill_f8(q.cuda(), dev([0, 1, 2, 3]), gpu, dev(table), dev(ctx), 0.1,
+                                                                max_new=1, out=torch.zeros_like(q, device="cuda"), status=st)):
+        st = status()
+        got = call(st, [100, 50, 16])
+        check(st, api.LL_DEV_BAD_BLOCK)
+        assert_attention(got, *want, 64)
+        assert (got[2] == 0).all()
+        st = status()
+        got = call(st, [-5, 50, 10 ** 6])
+        torch.cuda.synchronize()
+        assert int(st.item()) & api.LL_DEV_BAD_POSITION
+        assert_attention(got[1:2], *(w[1:2] for w in want), 64)
+        assert (got[0] == 0).all()
+
+
+PREFILL_CASES = [  # block, heads, kv_heads, dim, contexts before, new tokens
+    (16, 4, 2, 64, [0], [1]), (16, 4, 2, 64, [0, 10, 0], [64, 5, 17]), (128, 4, 4, 128, [0], [300]),
+    (128, 16, 2, 128, [100, 0, 1], [129, 1, 40]), (64, 16, 1, 128, [500], [33]), (256, 5, 1, 128, [0, 255], [128, 2]),
+    (32, 3, 1, 64, [0, 0, 7], [0, 130, 0]), (16, 7, 7, 128, [2000], [3]), (16, 14, 2, 64, [129], [255]),
+    (128, 9, 1, 128, [30], [60]), (32, 8, 8, 64, [0, 96], [127, 128])]
+
+
+@pytest.mark.parametrize("case", PREFILL_CASES)
+def test_prefill_matches_the_definition(case):
+    bs, H, Hkv, d, before, new = case
+    ctx = [b + n for b, n in zip(before, new)]
+    rng = np.random.default_rng(bs + H + sum(ctx))
+    ref_pool, table = make_cache(rng, ctx, Hkv, d, bs)
+    cu = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    T = int(cu[-1])
+    q = torch.from_numpy(rng.normal(size=(T + 3, H, d)) * np.exp(rng.normal(size=(T + 3, H, 1)))).bfloat16()
+    scale = d ** -0.5
+    want = C.attention_f8(f64(q[:T]), ref_pool, table, ctx, cu, scale)
+    st = status()
+    out = torch.full((T + 3, H, d), 5.0, dtype=torch.bfloat16, device="cuda")
+    pool = to_gpu(ref_pool)
+    first = None
+    for mx in (max(new), max(new) + 200):                                # max_new is an upper bound
+        api.paged_attention_prefill_f8(q.cuda(), dev(cu), pool, dev(table), dev(ctx), scale, max_new=mx, out=out, status=st)
+        check(st)
+        assert_attention(out[:T], *want, d)
+        assert (out[T:] == 5).all()                                      # rows behind the last sequence
+        first = out.clone() if first is None else first
+    again = api.paged_attention_prefill_f8(q.cuda(), dev(cu), pool, dev(table), dev(ctx), scale, max_new=max(new), status=st)
+    assert torch.equal(again[:T], first[:T])
+
+
+def test_prefill_flags_bad_counts():
+    rng = np.random.default_rng(5)
+    pool, table = make_cache(rng, [20, 20], 2, 64, 16)
+    gpu = to_gpu(pool)
+    q = torch.from_numpy(rng.normal(size=(9, 4, 64))).bfloat16().cuda()
+    for cu, ctx, mx in (([0, 3, 3], [2, 20], 3), ([0, 0, 4], [20, 20], 3), ([0, 0, 12], [20, 20], 20), ([5, 5, 2], [20, 20], 9),
+                        ([-1, 1, 1], [20, 20], 9), ([0, 3, 3], [1000, 20], 3)):
+        st = status()
+        out = torch.full_like(q, 5.0)
+        api.paged_attention_prefill_f8(q, dev(cu), gpu, dev(table), dev(ctx), 0.1, max_new=mx, out=out, status=st)
+        check(st, api.LL_DEV_BAD_POSITION)
+        assert (out == 5).all()
+
+
+def test_attention_offsets_beyond_32_bits():
+    """A pool of more than 2^32 bytes: blocks at both ends of it."""
+    nb, Hkv, bs, d = 5000, 32, 256, 128                                  # 5.2 GB of codes per tensor
+    pool = api.PoolF8.empty(nb, Hkv, bs, d)
+    table = np.array([[nb - 1, 0, nb - 2]], np.int32)
+    rng = np.random.default_rng(1)
+    ctx, H = [600], 32
+    k, v = (bf16(rng.normal(size=(600, Hkv, d))) for _ in range(2))
+    st = status()
+    kt, vt = (torch.from_numpy(x).bfloat16().cuda() for x in (k, v))
+    api.append_to_cache_f8(kt, vt, pool, dev(table), dev(ctx), cu_new=dev([0, 600]), max_new=600, status=st)
+    small = C.PoolF8(*(np.zeros((3, Hkv, bs, d), np.uint8) for _ in range(2)), *(np.zeros((3, Hkv)) for _ in range(2)))
+    small.append(k, v, [[0, 1, 2]], ctx, [0, 600])
+    q = torch.from_numpy(rng.normal(size=(1, H, d))).bfloat16()
+    want = C.attention_f8(f64(q), small, [[0, 1, 2]], ctx, [0, 1], d ** -0.5)
+    assert_attention(api.paged_attention_decode_f8(q.cuda(), pool, dev(table), dev(ctx), d ** -0.5, status=st), *want, d)
+    assert_attention(api.paged_attention_prefill_f8(q.cuda(), dev([0, 1]), pool, dev(table), dev(ctx), d ** -0.5, max_new=1,
+                                                    status=st), *want, d)
+    blocks = api.BlockSet(pool.tensors())
+    api.copy_blocks(blocks, dev([[nb - 1, 17], [0, nb - 3]]), status=st)
+    check(st)
+    assert torch.equal(pool.k.view(torch.uint8)[17], pool.k.view(torch.uint8)[nb - 1])
+    assert torch.equal(pool.v.view(torch.uint8)[nb - 3], pool.v.view(torch.uint8)[0])
+    assert torch.equal(pool.k_scale[17], pool.k_scale[nb - 1])
+
+
+# ---------------------------------------------------------------- blocks
+
+@pytest.mark.parametrize("n_tensors,inner,dtype", [(1, (4,), torch.uint8), (3, (2, 16, 64), torch.bfloat16), (2, (5,), torch.float32),
+                                                   (130, (33,), torch.int32), (4, (8, 128, 128), torch.uint8)])
+@pytest.mark.parametrize("n", [1, 7])
+def test_copy_blocks(n_tensors, inner, dtype, n):
+    nb = 24
+    g = torch.Generator().manual_seed(n)
+    ts = [torch.randint(0, 100, (nb, *inner), generator=g).to(dtype).cuda() for _ in range(n_tensors)]
+    want = [t.clone() for t in ts]
+    perm = torch.randperm(nb, generator=g)[:2 * n].view(n, 2)
+    for t in want:
+        t[perm[:, 1].cuda()] = t[perm[:, 0].cuda()]
+    pad = torch.full((3, 2), -1)
+    pairs = torch.cat((pad, perm, pad)).int().cuda()
+    blocks = api.BlockSet(ts)
+    st = status()
+    api.copy_blocks(blocks, pairs, n_pairs=dev([0]), status=st)
+    api.copy_blocks(blocks, pairs[:0], status=st)
+    api.copy_blocks(blocks, pairs[3:], n_pairs=dev([n]), status=st)
+    check(st)
+    assert all(torch.equal(a, b) for a, b in zip(ts, want))
+    api.copy_blocks(blocks, pairs, status=st)                            # the padding is skipped
+    check(st)
+    assert all(torch.equal(a, b) for a, b in zip(ts, want))
+    api.copy_blocks(blocks, dev([[0, nb], [-1, 3], [-5, 0], [nb + 7, 2], [4, 4]]), status=st)
+    check(st, api.LL_DEV_BAD_BLOCK)
+    assert all(torch.equal(a, b) for a, b in zip(ts, want))
+
+
+def test_copy_blocks_of_tensors_off_16_bytes():
+    raw = torch.randint(0, 255, (4 + 12 * 20 + 16 * 20,), dtype=torch.uint8).cuda()
+    a, b = raw[4:4 + 240].view(20, 12), raw[244:244 + 320].view(20, 16)  # 4-byte aligned only
+    want_a, want_b = a.clone(), b.clone()
+    want_a[7], want_b[7] = a[3], b[3]
+    st = status()
+    api.copy_blocks(api.BlockSet([a, b]), dev([[3, 7]]), status=st)
+    check(st)
+    assert torch.equal(a, want_a) and torch.equal(b, want_b)
+
+
+@pytest.mark.parametrize("nb,rows,wide,used", [(1, 1, 1, 1), (2, 1, 1, 1), (33, 4, 8, 20), (33, 4, 9, 33), (100, 7, 20, 0),
+                                               (1000, 16, 64, 700), (100003, 64, 200, 9000), (524288, 1, 5000, 5000)])
+def test_compact_blocks(nb, rows, wide, used):
+    rng = np.random.default_rng(nb)
+    ids = rng.permutation(nb)[:used].astype(np.int32)
+    table = np.full(rows * wide, -1, np.int32)
+    table[rng.permutation(rows * wide)[:used]] = ids
+    if used > 4:
+        table[rng.integers(0, rows * wide, size=used // 4)] = rng.choice(ids, used // 4)    # shared blocks
+    table = table.reshape(rows, wide)
+    new, moves, U, block_map = C.compact(table, nb)
+    st = status()
+    t = dev(table)
+    got, pairs, counts, bm = api.compact_blocks(t, nb, status=st)
+    check(st)
+    want = np.full((nb // 2, 2), -1, np.int32)
+    want[:len(moves)] = np.array(moves, np.int32).reshape(-1, 2)
+    assert counts.tolist() == [U, len(moves)] and (pairs.cpu().numpy() == want).all()
+    assert (got.cpu().numpy() == new).all() and (bm.cpu().numpy() == block_map).all()
+    assert (t.cpu().numpy() == table).all()
+    api.compact_blocks(t, nb, new_table=t, status=st)                    # in place
+    check(st)
+    assert (t.cpu().numpy() == new).all()
+
+
+def test_compact_blocks_bad_ids_and_no_rows():
+    st = status()
+    got, pairs, counts, _ = api.compact_blocks(dev([[9, -3, 5, 8]]), 8, status=st)
+    check(st, api.LL_DEV_BAD_BLOCK)
+    assert got.tolist() == [[9, -3, 0, 8]] and counts.tolist() == [1, 1] and pairs[0].tolist() == [5, 0]
+    st = status()
+    _, pairs, counts, bm = api.compact_blocks(torch.empty(0, 4, dtype=torch.int32, device="cuda"), 6, status=st)
+    check(st)
+    assert counts.tolist() == [0, 0] and (pairs == -1).all() and (bm == -1).all()
+
+
+# ---------------------------------------------------------------- together
+
+def test_a_served_batch_from_prompt_to_compaction():
+    """Prompts through rope, the cache write and the prefill attention; a fork; decode steps replayed as one CUDA
+    graph on a stream of its own; compaction; the same answers from the packed pool."""
+    H, Hkv, d, bs, nb = 8, 2, 64, 16, 40
+    rng = np.random.default_rng(21)
+    freq = dict(scaling="banded", factor=4.0, original_max_position=64)
+    tab = api.rope_table(api.make_rope_config(d, **freq), 256)
+    f, mag = C.inv_freq(d, scaling="banded", factor=4.0, original=64)
+    pool = api.PoolF8.empty(nb, Hkv, bs, d)
+    blocks = api.BlockSet(pool.tensors())
+    ref = C.PoolF8(*(np.zeros((nb, Hkv, bs, d), np.uint8) for _ in range(2)), *(np.zeros((nb, Hkv)) for _ in range(2)))
+    table = np.full((3, 8), -1, np.int32)
+    table[0, :4], table[1, :3] = [30, 7, 39, 2], [11, 25, 38]
+    new, ctx = [50, 33], [50, 33]
+    cu = np.array([0, 50, 83], np.int32)
+    st = status()
+
+    def inputs(T):
+        return torch.from_numpy(rng.normal(size=(T, (H + 2 * Hkv) * d))).bfloat16().cuda()
+
+    def split(x):
+        T = x.shape[0]
+        return x[:, :H * d].view(T, H, d), x[:, H * d:(H + Hkv) * d].view(T, Hkv, d), x[:, (H + Hkv) * d:].view(T, Hkv, d)
+
+    def oracle(x, pos, table, ctx, cu):
+        q, k, v = (f64(t) for t in split(x))
+        q, k = bf16(C.rope(q, pos, f, mag, "half")), bf16(C.rope(k, pos, f, mag, "half"))
+        return q, k, v
+
+    # the prompts; the oracle's cache takes the device's K, since a BF16 rounding may fall either way
+    x = inputs(83)
+    pos = np.concatenate([np.arange(50), np.arange(33)]).astype(np.int32)
+    q, k, v = split(x)
+    q1, k1 = api.rope(q, k, dev(pos), tab, status=st)
+    qo, ko, vo = oracle(x, pos, table, ctx, cu)
+    assert (np.abs(f64(k1) - ko) <= 2.0 ** -7 * np.abs(ko) + 1e-6).all()
+    api.append_to_cache_f8(k1, v, pool, dev(table[:2]), dev(ctx), cu_new=dev(cu), max_new=50, status=st)
+    ref.append(f64(k1), vo, table, ctx, cu)
+    out = api.paged_attention_prefill_f8(q1, dev(cu), pool, dev(table[:2]), dev(ctx), d ** -0.5, max_new=50, status=st)
+    check(st)
+    assert_pool(pool, ref)
+    assert_attention(out, *C.attention_f8(f64(q1), ref, table, ctx, cu, d ** -0.5), d)
+    # sequence 2 forks from sequence 0: full blocks shared, the last one copied
+    table[2, :4] = [30, 7, 39, 17]
+    api.copy_blocks(blocks, dev([[2, 17]]), status=st)
+    for t in (ref.k, ref.v, ref.k_scale, ref.v_scale):
+        t[17] = t[2]
+    table[0, 4], table[1, 3], table[2, 4] = 5, 19, 33
+    ctx = [50, 33, 50]
+    # decode steps: one graph, replayed with new inputs
+    xs, ctx_d, pos_d, table_d = inputs(3), dev(ctx), dev(ctx), dev(table)
+    ws = torch.empty(api.attention_decode_f8_workspace_size(3, H, Hkv, d), dtype=torch.uint8, device="cuda")
+    y = torch.empty(3, H, d, dtype=torch.bfloat16, device="cuda")
+    qd, kd = torch.empty(3, H, d, dtype=torch.bfloat16, device="cuda"), torch.empty(3, Hkv, d, dtype=torch.bfloat16, device="cuda")
+
+    def step():
+        q, k, v = split(xs)
+        api.rope(q, k, pos_d, tab, q_out=qd, k_out=kd, status=st)
+        api.append_to_cache_f8(kd, v, pool, table_d, ctx_d, status=st)
+        api.paged_attention_decode_f8(qd, pool, table_d, ctx_d, d ** -0.5, out=y, workspace=ws, status=st)
+
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=stream):
+        step()
+    for i in range(20):
+        xn = inputs(3)
+        ctx = [c + 1 for c in ctx]
+        xs.copy_(xn)
+        ctx_d.copy_(dev(ctx))
+        pos_d.copy_(dev([c - 1 for c in ctx]))
+        g.replay()
+        check(st)
+        _, _, vo = oracle(xn, np.array(ctx) - 1, table, ctx, None)
+        ref.append(f64(kd), vo, table, ctx, [0, 1, 2, 3])
+        assert_attention(y, *C.attention_f8(f64(qd), ref, table, ctx, [0, 1, 2, 3], d ** -0.5), d)
+    assert_pool(pool, ref)
+    # sequence 1 ends: its blocks are free; the rest is packed
+    y0 = y.clone()
+    table[1] = -1
+    table_d.copy_(dev(table))
+    new_table, pairs, counts, _ = api.compact_blocks(table_d, nb, status=st)
+    api.copy_blocks(blocks, pairs, n_pairs=counts[1:], status=st)
+    want, moves, U, _ = C.compact(table, nb)
+    check(st)
+    assert counts.tolist() == [U, len(moves)] and (new_table.cpu().numpy() == want).all() and want.max() == U - 1
+    ctx_d[1] = 0
+    z = api.paged_attention_decode_f8(qd, pool, new_table, ctx_d, d ** -0.5, status=st)
+    check(st)
+    for b, w in ((0, y0[0]), (2, y0[2])):
+        assert (np.abs(f64(z[b]) - f64(w)) <= 2.0 ** -7 * np.abs(f64(w)) + 1e-3).all()
+    assert (z[1] == 0).all()

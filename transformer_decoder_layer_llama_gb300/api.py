@@ -23,6 +23,14 @@ LL_ERR_CUDA = 4
 LL_MODE_FUSED = 0
 LL_MODE_STEP_BY_STEP = 1
 
+LL_BF16 = 0
+LL_F32 = 1
+
+LL_ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+LL_ROPE_FORWARD = 0
+LL_ROPE_BACKWARD = 1
+LL_ROPE_SCALINGS = {"plain": 0, "linear": 1, "ntk": 2, "banded": 3, "yarn": 4}
+
 LL_DEV_BAD_BLOCK = 1
 LL_DEV_BAD_SLOT = 2
 LL_DEV_BAD_POSITION = 4
@@ -37,6 +45,10 @@ EXPORTED = [
     "ll_workspace_checkpoints", "ll_reshape_and_cache_q8", "ll_paged_attention_decode_q8",
     "ll_layer_decode_step_q8", "ll_workspace_size_mode", "ll_workspace_step_checkpoints",
     "ll_layer_prefill_mode", "ll_layer_decode_step_mode", "ll_set_prefill_attention_ctas",
+    "ll_rope_table_size", "ll_rope_table", "ll_pack_rope", "ll_rope", "ll_append_to_cache_f8",
+    "ll_attention_decode_f8_workspace_size", "ll_paged_attention_decode_f8",
+    "ll_attention_prefill_f8_workspace_size", "ll_paged_attention_prefill_f8", "ll_copy_blocks",
+    "ll_compact_blocks",
 ]
 
 
@@ -63,6 +75,22 @@ class ll_kv_pool_q8(ctypes.Structure):
                 ("v_scale", ctypes.c_void_p), ("num_blocks", ctypes.c_int32)]
 
 
+class ll_rope_config(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("scaling", ctypes.c_int32), ("theta", ctypes.c_float),
+                ("factor", ctypes.c_float), ("original_max_position", ctypes.c_int32),
+                ("low_turns", ctypes.c_float), ("high_turns", ctypes.c_float),
+                ("attention_factor", ctypes.c_float)]
+
+
+class ll_kv_pool_f8(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("num_blocks", ctypes.c_int32)]
+
+
+class ll_block_tensor(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("block_bytes", ctypes.c_int64)]
+
+
 class ll_checkpoints(ctypes.Structure):
     _fields_ = [("x_hat", ctypes.c_size_t), ("q", ctypes.c_size_t), ("o", ctypes.c_size_t),
                 ("h", ctypes.c_size_t), ("h_hat", ctypes.c_size_t), ("a", ctypes.c_size_t)]
@@ -80,6 +108,9 @@ def _load():
     P, S, I32 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int32
     cfgp = ctypes.POINTER(ll_config)
     poolp = ctypes.POINTER(ll_kv_pool)
+    poolf8 = ctypes.POINTER(ll_kv_pool_f8)
+    ropep = ctypes.POINTER(ll_rope_config)
+    I64 = ctypes.c_int64
     sig = {
         "ll_strerror": (ctypes.c_char_p, [ctypes.c_int]),
         "ll_last_error": (ctypes.c_char_p, []),
@@ -114,6 +145,21 @@ def _load():
         "ll_workspace_step_checkpoints": (ctypes.c_int, [cfgp, I32, I32, ctypes.POINTER(ll_step_checkpoints)]),
         "ll_layer_prefill_mode": (ctypes.c_int, [cfgp, P, P, P, I32, I32, poolp, P, I32, P, P, S, P, I32, P]),
         "ll_layer_decode_step_mode": (ctypes.c_int, [cfgp, P, P, poolp, P, I32, P, I32, P, P, S, P, I32, P]),
+        "ll_rope_table_size": (S, [ropep, I32]),
+        "ll_rope_table": (ctypes.c_int, [ropep, I32, P, S, P]),
+        "ll_pack_rope": (ctypes.c_int, [cfgp, ropep, P, S, P]),
+        "ll_rope": (ctypes.c_int, [P, P, I32, P, I32, I32, I32, I32, I32, I32, I32, I64, I64, P, I32, P, P, I64, I64,
+                                   P, P]),
+        "ll_append_to_cache_f8": (ctypes.c_int, [P, P, I64, I64, P, I32, P, I32, I32, I32, I32, I32, poolf8, P, I32,
+                                                 P, P]),
+        "ll_attention_decode_f8_workspace_size": (S, [I32, I32, I32, I32]),
+        "ll_paged_attention_decode_f8": (ctypes.c_int, [P, poolf8, P, I32, P, I32, I32, I32, I32, I32,
+                                                        ctypes.c_float, P, P, S, P, P]),
+        "ll_attention_prefill_f8_workspace_size": (S, [I32, I32, I32, I32, I32, I32]),
+        "ll_paged_attention_prefill_f8": (ctypes.c_int, [P, P, I32, poolf8, P, I32, P, I32, I32, I32, I32, I32, I32,
+                                                         ctypes.c_float, P, P, S, P, P]),
+        "ll_copy_blocks": (ctypes.c_int, [ctypes.POINTER(ll_block_tensor), I32, I32, P, I32, P, P, P]),
+        "ll_compact_blocks": (ctypes.c_int, [P, I32, I32, I32, P, P, P, P, P, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -468,6 +514,312 @@ def paged_attention_decode_noalloc(q, k_pool, v_pool, block_table, context_lens,
         Hq, k_pool.shape[1], d, k_pool.shape[2], float(scale), _ptr(out), _ptr(status),
         _stream(stream)))
     return out
+
+
+# ---------------------------------------------------------------- operators around the cache
+
+def _rows3(t, name, dtype):
+    """Checks a [tokens, heads, head_dim] tensor whose heads are contiguous within a token; returns the
+    elements between tokens."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must live on the GPU")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens, heads, head_dim]")
+    T, H, d = t.shape
+    if T == 0:
+        return H * d
+    if (d > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != d) or (T > 1 and t.stride(0) < H * d):
+        raise ValueError(f"{name} must hold each token's heads contiguously")
+    return t.stride(0) if T > 1 else H * d
+
+
+def _on(*tensors):
+    """The device that all the tensors share."""
+    dev = tensors[0].device
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors on {dev} and {t.device}: one device is needed")
+    return dev
+
+
+def _call(name, dev, stream, *args):
+    """Calls the library on `stream` (default: the device's current one) with `dev` as the current device."""
+    fn = getattr(lib, name)
+    if dev.index == torch.cuda.current_device():
+        s = stream if stream is not None else torch.cuda.current_stream()
+        _check(name, fn(*args, s.cuda_stream))
+        return
+    with torch.cuda.device(dev):
+        s = stream if stream is not None else torch.cuda.current_stream()
+        _check(name, fn(*args, s.cuda_stream))
+
+
+def make_rope_config(rotary_dim, theta=10000.0, scaling="plain", factor=1.0, original_max_position=0, low_turns=1.0,
+                     high_turns=None, attention_factor=0.0) -> ll_rope_config:
+    """ll_rope_config.  scaling: "plain", "linear", "ntk", "banded" or "yarn"; high_turns defaults to 4
+    (banded) or 32 (yarn), attention_factor 0 to 0.1 ln(factor) + 1 (yarn)."""
+    if scaling not in LL_ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(LL_ROPE_SCALINGS)}, got {scaling!r}")
+    if high_turns is None:
+        high_turns = 32.0 if scaling == "yarn" else 4.0
+    return ll_rope_config(int(rotary_dim), LL_ROPE_SCALINGS[scaling], float(theta), float(factor),
+                          int(original_max_position), float(low_turns), float(high_turns), float(attention_factor))
+
+
+def rope_table(rope: ll_rope_config, max_position: int, device=None, stream=None) -> torch.Tensor:
+    """ll_rope_table: a new float32 table [max_position, rotary_dim / 2, 2] of (cos, sin)."""
+    n = lib.ll_rope_table_size(ctypes.byref(rope), int(max_position))
+    if n == 0:
+        raise LayerError("ll_rope_table_size", LL_ERR_INVALID_ARG)
+    table = torch.empty(int(max_position), rope.rotary_dim // 2, 2, dtype=torch.float32, device=device or "cuda")
+    _call("ll_rope_table", table.device, stream, ctypes.byref(rope), int(max_position), table.data_ptr(), n)
+    return table
+
+
+def pack_rope(cfg: ll_config, rope: ll_rope_config, packed: torch.Tensor, stream=None) -> None:
+    """ll_pack_rope: the layer calls with `packed` rotate by the scaled frequencies from here on."""
+    _need(packed, "packed", torch.uint8)
+    _call("ll_pack_rope", packed.device, stream, ctypes.byref(cfg), ctypes.byref(rope), packed.data_ptr(),
+          packed.numel())
+
+
+def rope(q, k, positions, table, layout="half", backward=False, q_out=None, k_out=None, status=None, stream=None):
+    """ll_rope: q [tokens, n_heads, head_dim] and k [tokens, n_kv_heads, head_dim], BF16 or float32, heads
+    contiguous within a token (views of a merged QKV output will do); either may be None.  `table` is
+    rope_table()'s.  Pass q_out=q (k_out=k) to rotate in place.  Returns (q_out, k_out)."""
+    x = q if q is not None else k
+    if x is None:
+        raise ValueError("q and k are both None")
+    if not isinstance(x, torch.Tensor) or x.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("q and k must be bfloat16 or float32 tensors")
+    if layout not in LL_ROPE_LAYOUTS:
+        raise ValueError(f"layout must be one of {sorted(LL_ROPE_LAYOUTS)}, got {layout!r}")
+    qs = _rows3(q, "q", x.dtype) if q is not None else 0
+    ks = _rows3(k, "k", x.dtype) if k is not None else 0
+    T, d = x.shape[0], x.shape[2]
+    if q is not None and k is not None and (k.shape[0] != T or k.shape[2] != d):
+        raise ValueError(f"k must be [{T}, n_kv_heads, {d}], got {tuple(k.shape)}")
+    _need(positions, "positions", torch.int32, shape=(T,))
+    _need(table, "table", torch.float32)
+    if table.dim() != 3 or table.shape[2] != 2 or not 2 <= 2 * table.shape[1] <= d:
+        raise ValueError("table must be [max_position, rotary_dim / 2, 2] with rotary_dim <= head_dim")
+    qos = kos = 0
+    if q is not None:
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        qos = _rows3(q_out, "q_out", x.dtype)
+        if q_out.shape != q.shape:
+            raise ValueError(f"q_out must have shape {tuple(q.shape)}, got {tuple(q_out.shape)}")
+    if k is not None:
+        if k_out is None:
+            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        kos = _rows3(k_out, "k_out", x.dtype)
+        if k_out.shape != k.shape:
+            raise ValueError(f"k_out must have shape {tuple(k.shape)}, got {tuple(k_out.shape)}")
+    if status is None:
+        status = new_status(x.device)
+    dev = _on(x, q, k, q_out if q is not None else None, k_out if k is not None else None, positions, table, status)
+    _call("ll_rope", dev, stream, q.data_ptr() if q is not None else None, k.data_ptr() if k is not None else None,
+          LL_F32 if x.dtype == torch.float32 else LL_BF16, positions.data_ptr(), T,
+          q.shape[1] if q is not None else 0, k.shape[1] if k is not None else 0, d, 2 * table.shape[1],
+          LL_ROPE_LAYOUTS[layout], LL_ROPE_BACKWARD if backward else LL_ROPE_FORWARD, qs, ks, table.data_ptr(),
+          table.shape[0], q_out.data_ptr() if q is not None else None, k_out.data_ptr() if k is not None else None,
+          qos, kos, status.data_ptr())
+    return (q_out if q is not None else None), (k_out if k is not None else None)
+
+
+class PoolF8:
+    """An e4m3 KV pool on the GPU: codes k, v float8_e4m3fn [num_blocks, n_kv_heads, block_size, head_dim]
+    and float32 scales k_scale, v_scale [num_blocks, n_kv_heads]."""
+
+    def __init__(self, k, v, k_scale, v_scale):
+        _need(k, "k codes", torch.float8_e4m3fn)
+        _need(v, "v codes", torch.float8_e4m3fn, shape=tuple(k.shape))
+        if k.dim() != 4:
+            raise ValueError("codes must be [num_blocks, n_kv_heads, block_size, head_dim]")
+        _need(k_scale, "k_scale", torch.float32, shape=tuple(k.shape[:2]))
+        _need(v_scale, "v_scale", torch.float32, shape=tuple(k.shape[:2]))
+        self.device = _on(k, v, k_scale, v_scale)
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self._c = ll_kv_pool_f8(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), k.shape[0])
+
+    @classmethod
+    def empty(cls, num_blocks, n_kv_heads, block_size, head_dim, device="cuda"):
+        shape = (num_blocks, n_kv_heads, block_size, head_dim)
+        codes = [torch.zeros(shape, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn) for _ in range(2)]
+        return cls(*codes, *(torch.zeros(shape[:2], dtype=torch.float32, device=device) for _ in range(2)))
+
+    @property
+    def block_size(self):
+        return self.k.shape[2]
+
+    def tensors(self):
+        """The pool's tensors, block first, as a BlockSet takes them."""
+        return [self.k, self.v, self.k_scale, self.v_scale]
+
+    def c(self):
+        return self._c
+
+
+def _f8_batch(pool, block_table, context_lens):
+    _need(context_lens, "context_lens", torch.int32)
+    if context_lens.dim() != 1:
+        raise ValueError("context_lens must be [batch]")
+    _need(block_table, "block_table", torch.int32)
+    if block_table.dim() != 2 or block_table.shape[0] < context_lens.shape[0]:
+        raise ValueError("block_table must be [batch, max_blocks]")
+    return context_lens.shape[0]
+
+
+def append_to_cache_f8(k, v, pool: PoolF8, block_table, context_lens, cu_new=None, max_new=1, status=None, stream=None):
+    """ll_append_to_cache_f8: k, v BF16 [tokens, n_kv_heads, head_dim] (heads contiguous within a token)
+    into `pool` at the last positions of each sequence.  cu_new int32 [batch + 1] with at most max_new
+    tokens per sequence; None: one token each.  Returns the status word."""
+    ks, vs = _rows3(k, "k", torch.bfloat16), _rows3(v, "v", torch.bfloat16)
+    if v.shape != k.shape or k.shape[1] != pool.k.shape[1] or k.shape[2] != pool.k.shape[3]:
+        raise ValueError(f"k and v must both be [tokens, {pool.k.shape[1]}, {pool.k.shape[3]}]")
+    B = _f8_batch(pool, block_table, context_lens)
+    if cu_new is not None:
+        _need(cu_new, "cu_new", torch.int32, shape=(B + 1,))
+    if status is None:
+        status = new_status(k.device)
+    dev = _on(k, v, pool.k, block_table, context_lens, cu_new, status)
+    _call("ll_append_to_cache_f8", dev, stream, k.data_ptr(), v.data_ptr(), ks, vs,
+          cu_new.data_ptr() if cu_new is not None else None, k.shape[0], context_lens.data_ptr(), B, int(max_new),
+          k.shape[1], k.shape[2], pool.block_size, ctypes.byref(pool.c()), block_table.data_ptr(),
+          block_table.shape[1], status.data_ptr())
+    return status
+
+
+def attention_decode_f8_workspace_size(batch, n_heads, n_kv_heads, head_dim):
+    return lib.ll_attention_decode_f8_workspace_size(int(batch), int(n_heads), int(n_kv_heads), int(head_dim))
+
+
+def attention_prefill_f8_workspace_size(batch, tokens, max_new, n_heads, n_kv_heads, head_dim):
+    return lib.ll_attention_prefill_f8_workspace_size(int(batch), int(tokens), int(max_new), int(n_heads),
+                                                      int(n_kv_heads), int(head_dim))
+
+
+def _f8_attention(q, pool, out, workspace, status, size):
+    """Checks q, out and the workspace of an attention call; makes what was not passed."""
+    _need(q, "q", torch.bfloat16)
+    if q.dim() != 3 or q.shape[2] != pool.k.shape[3]:
+        raise ValueError(f"q must be [rows, n_heads, {pool.k.shape[3]}], got {tuple(q.shape)}")
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _need(out, "out", torch.bfloat16, shape=tuple(q.shape))
+    if workspace is None:
+        workspace = torch.empty(max(size(), 16), dtype=torch.uint8, device=q.device)
+    else:
+        _need(workspace, "workspace", torch.uint8)
+    if status is None:
+        status = new_status(q.device)
+    return out, workspace, status
+
+
+def paged_attention_decode_f8(q, pool: PoolF8, block_table, context_lens, scale, out=None, workspace=None, status=None,
+                              stream=None):
+    """ll_paged_attention_decode_f8: q BF16 [batch, n_heads, head_dim] over an e4m3 pool.  Returns out."""
+    B = _f8_batch(pool, block_table, context_lens)
+    Hkv = pool.k.shape[1]
+    out, workspace, status = _f8_attention(
+        q, pool, out, workspace, status, lambda: attention_decode_f8_workspace_size(B, q.shape[1], Hkv, q.shape[2]))
+    if q.shape[0] != B:
+        raise ValueError(f"q must have {B} rows, one per sequence")
+    dev = _on(q, pool.k, block_table, context_lens, out, workspace, status)
+    _call("ll_paged_attention_decode_f8", dev, stream, q.data_ptr(), ctypes.byref(pool.c()), block_table.data_ptr(),
+          block_table.shape[1], context_lens.data_ptr(), B, q.shape[1], Hkv, q.shape[2], pool.block_size, float(scale),
+          out.data_ptr(), workspace.data_ptr(), workspace.numel(), status.data_ptr())
+    return out
+
+
+def paged_attention_prefill_f8(q, cu_new, pool: PoolF8, block_table, context_lens, scale, max_new, out=None,
+                               workspace=None, status=None, stream=None):
+    """ll_paged_attention_prefill_f8: q BF16 [tokens, n_heads, head_dim], sequence b's new tokens in rows
+    cu_new[b] .. cu_new[b + 1] - 1 (at most max_new), already in the pool.  Returns out."""
+    B = _f8_batch(pool, block_table, context_lens)
+    _need(cu_new, "cu_new", torch.int32, shape=(B + 1,))
+    Hkv = pool.k.shape[1]
+    out, workspace, status = _f8_attention(
+        q, pool, out, workspace, status,
+        lambda: attention_prefill_f8_workspace_size(B, q.shape[0], max_new, q.shape[1], Hkv, q.shape[2]))
+    dev = _on(q, pool.k, cu_new, block_table, context_lens, out, workspace, status)
+    _call("ll_paged_attention_prefill_f8", dev, stream, q.data_ptr(), cu_new.data_ptr(), q.shape[0],
+          ctypes.byref(pool.c()), block_table.data_ptr(), block_table.shape[1], context_lens.data_ptr(), B,
+          int(max_new), q.shape[1], Hkv, q.shape[2], pool.block_size, float(scale), out.data_ptr(),
+          workspace.data_ptr(), workspace.numel(), status.data_ptr())
+    return out
+
+
+class BlockSet:
+    """Tensors [num_blocks, ...] that share their block ids (K and V pools of every layer, and their
+    scales), for copy_blocks.  Keeps the tensors and the array that the library reads."""
+
+    def __init__(self, tensors):
+        self.tensors = list(tensors)
+        if not self.tensors:
+            raise ValueError("a BlockSet needs a tensor")
+        for t in self.tensors:
+            if not isinstance(t, torch.Tensor) or not t.is_cuda or not t.is_contiguous() or t.dim() < 1:
+                raise ValueError("a BlockSet takes contiguous GPU tensors [num_blocks, ...]")
+            if t.shape[0] != self.tensors[0].shape[0]:
+                raise ValueError("the tensors of a BlockSet have the same number of blocks")
+        self.device = _on(*self.tensors)
+        self.num_blocks = self.tensors[0].shape[0]
+        self._c = (ll_block_tensor * len(self.tensors))(
+            *((t.data_ptr(), t.numel() // max(self.num_blocks, 1) * t.element_size()) for t in self.tensors))
+
+
+def copy_blocks(blocks: BlockSet, pairs, n_pairs=None, status=None, stream=None):
+    """ll_copy_blocks: block pairs[i, 0] to block pairs[i, 1] (int32 [n, 2], on the GPU) in every tensor of
+    the set; n_pairs: a GPU int32 tensor of one element with the number of pairs, None for all.  Returns
+    the status word."""
+    _need(pairs, "pairs", torch.int32)
+    if pairs.dim() != 2 or pairs.shape[1] != 2:
+        raise ValueError("pairs must be [n, 2]")
+    if n_pairs is not None:
+        _need(n_pairs, "n_pairs", torch.int32)
+        if n_pairs.numel() != 1:
+            raise ValueError("n_pairs must hold one number")
+    if status is None:
+        status = new_status(blocks.device)
+    dev = _on(blocks.tensors[0], pairs, n_pairs, status)
+    _call("ll_copy_blocks", dev, stream, blocks._c, len(blocks.tensors), blocks.num_blocks, pairs.data_ptr(),
+          pairs.shape[0], n_pairs.data_ptr() if n_pairs is not None else None, status.data_ptr())
+    return status
+
+
+def compact_blocks(block_table, num_blocks, new_table=None, pairs=None, counts=None, block_map=None, status=None,
+                   stream=None):
+    """ll_compact_blocks: the plan that packs the blocks of block_table to the front of a pool of num_blocks.
+    Returns (new_table, pairs [num_blocks // 2, 2], counts [2], block_map [num_blocks]); move the
+    contents with copy_blocks(blocks, pairs, n_pairs=counts[1:])."""
+    num_blocks = int(num_blocks)
+    _need(block_table, "block_table", torch.int32)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [rows, max_blocks]")
+    dev = block_table.device
+    new = lambda *shape: torch.empty(shape, dtype=torch.int32, device=dev)  # noqa: E731
+    new_table = new(*block_table.shape) if new_table is None else new_table
+    pairs = new(num_blocks // 2, 2) if pairs is None else pairs
+    counts = new(2) if counts is None else counts
+    block_map = new(num_blocks) if block_map is None else block_map
+    _need(new_table, "new_table", torch.int32, shape=tuple(block_table.shape))
+    _need(pairs, "pairs", torch.int32, shape=(num_blocks // 2, 2))
+    _need(counts, "counts", torch.int32, shape=(2,))
+    _need(block_map, "block_map", torch.int32, shape=(num_blocks,))
+    if status is None:
+        status = new_status(dev)
+    dev = _on(block_table, new_table, pairs, counts, block_map, status)
+    _call("ll_compact_blocks", dev, stream, block_table.data_ptr(), block_table.shape[0], block_table.shape[1],
+          num_blocks, new_table.data_ptr(), pairs.data_ptr(), counts.data_ptr(), block_map.data_ptr(),
+          status.data_ptr())
+    return new_table, pairs, counts, block_map
 
 
 def set_prefill_attention_ctas(n: int) -> None:

@@ -24,6 +24,7 @@
 #include <vector>
 
 #include "../../include/llama_layer.h"
+#include "api_util.h"
 #include "kernels.h"
 
 using ll::EpiParams;
@@ -31,15 +32,10 @@ using ll::GemmProblem;
 
 namespace {
 
-constexpr size_t kAlign = 256;
-
-size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-// The decode attention loads K/V in boxes of min(block_size, 64) rows that must
-// tile a 64-key span exactly and keep the 1024-byte swizzle alignment.
-bool block_size_ok(int bs) { return bs >= 16 && bs <= 256 && (bs & (bs - 1)) == 0; }
+using ll::align_up;
+using ll::aligned16;
+using ll::block_size_ok;
+using ll::cuda_rc;
 
 bool config_ok(const ll_config* c) {
     if (!c) return false;
@@ -147,8 +143,6 @@ WsLayout ws_layout(const ll_config* c, int T, int max_blocks, int mode = LL_MODE
 }
 
 bool mode_ok(int mode) { return mode == LL_MODE_FUSED || mode == LL_MODE_STEP_BY_STEP; }
-
-int cuda_rc(cudaError_t e) { return e == cudaSuccess ? LL_OK : LL_ERR_CUDA; }
 
 thread_local char g_last_error[512];
 
@@ -633,6 +627,16 @@ int ll_pack_weights(const ll_config* cfg, const ll_weights* w, void* packed, siz
                                    (double)cfg->rope_theta, s)) != cudaSuccess)
         return LL_ERR_CUDA;
     return cuda_rc(ll::record(cudaStreamSynchronize(s), "cudaStreamSynchronize(pack)"));
+}
+
+int ll_pack_rope(const ll_config* cfg, const ll_rope_config* rope, void* packed, size_t packed_bytes, void* stream) {
+    ll::clear_last_error();
+    const int rc = config_supported(cfg);
+    if (rc != LL_OK) return rc;
+    const PackedLayout L = packed_layout(cfg);
+    if (!rope || !packed || !aligned16(packed) || packed_bytes < L.total || rope->rotary_dim != cfg->head_dim)
+        return LL_ERR_INVALID_ARG;
+    return ll_rope_table(rope, cfg->max_position, static_cast<uint8_t*>(packed) + L.rope, L.total - L.rope, stream);
 }
 
 size_t ll_workspace_size(const ll_config* cfg, int32_t max_tokens, int32_t max_blocks) {

@@ -1,0 +1,654 @@
+// Decode attention over a paged cache of e4m3 codes with one scale per block and KV head:
+// one query token per sequence, softmax(q k^T scale) v with k = code * k_scale[block][head] and
+// v = code * v_scale[block][head].
+//
+// Bound by memory: every code of the contexts is read once, one byte per element.  The work is cut
+// along the key axis into equal shares whatever the batch: all (sequence, KV head, 64-key tile)
+// triples of the actual contexts form one list, and each CTA of a grid that fills the GPU once takes
+// an equal run of it.  A CTA that holds all tiles of a (sequence, KV head) writes its output; one
+// that shares them leaves a float32 partial (at most two per CTA), which the join kernel merges by
+// the log-sum-exp.
+//
+// A CTA is four consumer warps and a producer warp.  The producer brings each tile's codes in by TMA
+// (three stages) with the scales of its blocks, reading the block table and scales a batch of tiles
+// ahead.  Each consumer warp owns 16 keys of a tile (they lie in one block, so its scales are scalars):
+// S^T = K Q^T and O^T += V^T P^T by mma.sync with the keys, and the head dims, as the 16 rows of A
+// and up to 8 (or 16) query heads of the KV head as columns, so a single query head wastes 7 of 8
+// columns instead of 15 of 16 rows.  The tensor pipe has the room: per SM 23 cache bytes a clock
+// arrive, and a tile's MMAs take about a quarter of its load time.
+//
+// Precision.  Codes become FP16 exactly.  A query row is scaled by a power of two so that its largest
+// element lies in [2^14, 2^15) before it becomes FP16: BF16 has fewer bits, so only elements below
+// 2^-28 of the row's largest are rounded.  Scores, the running maximum and sums are float32.  A
+// probability enters P V as one FP16 (11 significant bits, relative error 2^-11, an eighth of the BF16
+// output's half step), times its block's V scale relative to the largest exponent E that the warp has
+// met, times 2^6: at most 2^15, and still exact to 2^-31 of the largest term.  When E grows the
+// accumulator is scaled down by the (exact) power of two.
+#include <algorithm>
+
+#include "common.cuh"
+#include "f8.cuh"
+#include "kernels.h"
+
+namespace ll {
+
+namespace {
+
+constexpr float kLog2eF8 = 1.4426950408889634f;
+constexpr int kF8Tile = 64;              // keys per tile
+constexpr int kF8Stages = 3;
+constexpr int kF8Threads = 160;
+constexpr int kF8Shift = 6;              // probabilities enter P V times 2^6
+constexpr int kF8MaxCtasPerSm = 4;
+
+LL_DEVINL int f8_context(const AttnF8Args& a, int b, bool flag) {
+    const int cap = a.max_blocks * a.block_size;
+    const int ctx = a.context_lens[b];
+    if (ctx < 0 || ctx > cap) {
+        if (flag) flag_status(a.status, LL_DEV_BAD_POSITION);
+        return min(max(ctx, 0), cap);
+    }
+    return ctx;
+}
+LL_DEVINL int f8_tiles(int ctx) { return (ctx + kF8Tile - 1) / kF8Tile; }
+
+// Share c of P equal runs of n tiles: the first n % P shares are one tile longer.
+LL_DEVINL long long share_begin(long long n, int P, int c) {
+    const long long q = n / P, r = n - q * P;
+    return q * c + min((long long)c, r);
+}
+LL_DEVINL int share_of(long long n, int P, long long t) {
+    const long long q = n / P, r = n - q * P;
+    return (int)(t < r * (q + 1) ? t / (q + 1) : r + (t - r * (q + 1)) / q);
+}
+
+// Byte offset of the 16-byte chunk that holds byte `at` of key row r in a tile of D-byte rows that TMA
+// wrote as 128-byte lines with the 128-byte swizzle (two rows per line where D = 64).
+template <int D>
+LL_DEVINL uint32_t f8_chunk(int r, int at) {
+    const int byte = r * D + at;
+    const int line = byte >> 7, c = (byte >> 4) & 7;
+    return (uint32_t)(line * 128 + ((c ^ (line & 7)) << 4));
+}
+
+// Where in the list of tiles a share begins: the sequence, and the tile's place in the sequence's part.
+struct F8Start {
+    long long total;     // tiles of all sequences and KV heads
+    int b;
+    long long at;        // tile within the Hkv * tiles(b) tiles of sequence b
+};
+
+// All threads of a CTA of nt threads (a multiple of 32, at most 160): sums the contexts, finds the place
+// of tile share_begin(total, P, c).
+LL_DEVINL void f8_find_start(const AttnF8Args& a, int P, int c, int nt, bool flag, long long* sums, F8Start* out) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (a.batch + nt - 1) / nt;
+    const int b0 = min(tid * per, a.batch), b1 = min(b0 + per, a.batch);
+    long long mine = 0;
+    for (int b = b0; b < b1; ++b) mine += f8_tiles(f8_context(a, b, flag));
+    long long x = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) sums[warp] = x;
+    __syncthreads();
+    long long before = x - mine, total = 0;
+    for (int w = 0; w < nt / 32; ++w) {
+        if (w < warp) before += sums[w];
+        total += sums[w];
+    }
+    total *= a.n_kv_heads;
+    before *= a.n_kv_heads;
+    const long long t0 = share_begin(total, P, c);
+    if (tid == 0) out->total = total;
+    if (t0 < total && t0 >= before && t0 < before + mine * a.n_kv_heads) {
+        int b = b0;
+        for (;; ++b) {
+            const long long n = (long long)f8_tiles(f8_context(a, b, false)) * a.n_kv_heads;
+            if (t0 < before + n) break;
+            before += n;
+        }
+        out->b = b;
+        out->at = t0 - before;
+    }
+    __syncthreads();
+}
+
+// A run of tiles of one (sequence, KV head).
+struct F8Segment {
+    int b, hk, kt0, kt1, n_kt, ctx;
+};
+
+// Walks a share segment by segment.
+struct F8Walk {
+    int b;
+    long long at;        // tile within sequence b
+    long long left;      // tiles of the share still to do
+    LL_DEVINL bool next(const AttnF8Args& a, F8Segment& s) {
+        while (left > 0) {
+            const int ctx = f8_context(a, b, false);
+            const int n = f8_tiles(ctx);
+            if (at >= (long long)n * a.n_kv_heads) {
+                at = 0;
+                ++b;
+                continue;
+            }
+            s.b = b;
+            s.ctx = ctx;
+            s.n_kt = n;
+            s.hk = (int)(at / n);
+            s.kt0 = (int)(at - (long long)s.hk * n);
+            s.kt1 = (int)min((long long)n, s.kt0 + left);
+            at += s.kt1 - s.kt0;
+            left -= s.kt1 - s.kt0;
+            return true;
+        }
+        return false;
+    }
+};
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kF8Threads, NT == 1 ? 4 : 2)
+    attn_decode_f8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                          const AttnF8Args a) {
+    constexpr int BN = kF8Tile, STAGES = kF8Stages, NCONS = 128;
+    constexpr int TILE = BN * D;
+    constexpr int W = D / 16;                              // words of a key row per lane, MMA steps along D
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* sbase = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* sk = sbase;                                   // [STAGES][TILE]
+    uint8_t* sv = sk + STAGES * TILE;                      // [STAGES][TILE]
+    float* s_acc = reinterpret_cast<float*>(sv + STAGES * TILE);   // [4 warps][G][D], merged at a segment's end
+    __shared__ uint64_t full_bar[STAGES], empty_bar[STAGES];
+    __shared__ unsigned long long valid_s[STAGES];         // per stage: bit k = key k of the tile is cached
+    __shared__ float2 scale_s[STAGES][4];                  // per stage and 16 keys: K and V scale
+    __shared__ float2 s_ml[4][16];                         // per warp and query head: max, sum
+    __shared__ int s_exp[4];                               // per warp: exponent of its accumulator
+    __shared__ long long s_sums[kF8Threads / 32];
+    __shared__ F8Start s_start;
+    __shared__ int abort_s;
+
+    const int G = a.n_heads / a.n_kv_heads;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int P = gridDim.x, cta = blockIdx.x;
+    if (threadIdx.x == 0) {
+        for (int st = 0; st < STAGES; ++st) {
+            mbar_init(&full_bar[st], 1);
+            mbar_init(&empty_bar[st], 4);
+        }
+        abort_s = 0;
+        fence_mbar_init();
+    }
+    pdl_wait();
+    pdl_trigger();
+    f8_find_start(a, P, cta, kF8Threads, cta == 0, s_sums, &s_start);
+    const long long total = s_start.total;
+    const long long t_begin = share_begin(total, P, cta), t_end = share_begin(total, P, cta + 1);
+    if (t_begin >= t_end) return;
+    F8Walk walk{s_start.b, s_start.at, t_end - t_begin};
+    F8Segment seg;
+
+    if (warp == 4) {
+        // ------------------------------------------------ producer
+        // Lane i looks after 16-to-64-key box i % spt of tile i / spt of a batch of 32 / spt tiles: its
+        // block and scales are loaded one batch ahead of its TMA loads.
+        const int kt_rows = min(a.block_size, BN);
+        const int spt = BN / kt_rows, tpb = 32 / spt;
+        const int my_tile = lane / spt, sb = lane % spt;
+        if (lane == 0) {
+            tma_prefetch_desc(&tmK);
+            tma_prefetch_desc(&tmV);
+        }
+        uint32_t issued = 0, parity = 0;                   // per stage: a load was issued; parity of the loads
+        int it = 0;                                        // tiles of the share so far
+        bool ok = true;
+        while (ok && walk.next(a, seg)) {
+            const int32_t* table_row = a.block_table + (size_t)seg.b * a.max_blocks;
+            int blk_n = -1;
+            float ks_n = 0.f, vs_n = 0.f;
+            auto fetch = [&](int kt) {                     // box of tile kt + my_tile: block and scales
+                const int p = (kt + my_tile) * BN + sb * kt_rows;
+                blk_n = -1;
+                if (kt + my_tile < seg.kt1 && p < seg.ctx) {
+                    const int v = table_row[p / a.block_size];
+                    if (v >= 0 && v < a.num_blocks) {
+                        blk_n = v;
+                        ks_n = a.k_scale[(size_t)v * a.n_kv_heads + seg.hk];
+                        vs_n = a.v_scale[(size_t)v * a.n_kv_heads + seg.hk];
+                    } else {
+                        flag_status(a.status, LL_DEV_BAD_BLOCK);
+                    }
+                }
+            };
+            fetch(seg.kt0);
+            for (int kb = seg.kt0; kb < seg.kt1 && ok; kb += tpb) {
+                const int blk = blk_n;
+                const float ks = ks_n, vs = vs_n;
+                if (kb + tpb < seg.kt1) fetch(kb + tpb);
+                const int nt = min(tpb, seg.kt1 - kb);
+                for (int t = 0; t < nt; ++t, ++it) {
+                    const int st = it % STAGES;
+                    const uint32_t ph = (uint32_t)(it / STAGES) & 1u;
+                    bool go = true;
+                    if (lane == 0) go = mbar_wait_bounded(&empty_bar[st], ph ^ 1u, &abort_s, a.status);
+                    ok = __shfl_sync(0xffffffffu, (int)go, 0) != 0;
+                    if (!ok) break;
+                    const bool mine = my_tile == t;
+                    const uint32_t have = __ballot_sync(0xffffffffu, mine && blk >= 0);
+                    const int p = (kb + t) * BN + sb * kt_rows;
+                    unsigned long long valid = 0;
+                    if (mine && blk >= 0) {
+                        const int nk = min(kt_rows, seg.ctx - p);
+                        valid = (nk == 64 ? ~0ull : ((1ull << nk) - 1ull)) << (sb * kt_rows);
+                    }
+                    const uint32_t vlo = __reduce_or_sync(0xffffffffu, (uint32_t)valid);
+                    const uint32_t vhi = __reduce_or_sync(0xffffffffu, (uint32_t)(valid >> 32));
+                    if (mine)
+                        for (int i = 0; i < kt_rows / 16; ++i)
+                            scale_s[st][sb * (kt_rows / 16) + i] = blk >= 0 ? make_float2(ks, vs) : make_float2(0.f, 0.f);
+                    if (lane == 0) valid_s[st] = ((unsigned long long)vhi << 32) | vlo;
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive_expect_tx(&full_bar[st], (uint32_t)__popc(have) * 2u * (uint32_t)(kt_rows * D));
+                    __syncwarp();
+                    if (mine && blk >= 0) {
+                        const long long row = ((long long)blk * a.n_kv_heads + seg.hk) * a.block_size + (p % a.block_size);
+                        const int line = (int)(row * D / 128);
+                        const uint32_t off = (uint32_t)(st * TILE + sb * kt_rows * D);
+                        tma_load_2d(sk + off, &tmK, 0, line, &full_bar[st]);
+                        tma_load_2d(sv + off, &tmV, 0, line, &full_bar[st]);
+                    }
+                    issued |= 1u << st;
+                    parity ^= 1u << st;
+                }
+            }
+        }
+        __syncwarp();
+        if (lane == 0 && abort_s) {
+            // wait (bounded) for the copies in flight before the CTA leaves
+            volatile int never = 0;
+            for (int st = 0; st < STAGES; ++st)
+                if ((issued >> st) & 1u) mbar_wait_bounded(&full_bar[st], ((parity >> st) & 1u) ^ 1u, &never, nullptr);
+        }
+        __syncwarp();
+        return;
+    }
+
+    // ---------------------------------------------------- consumers (warps 0-3)
+    const int g = lane >> 2, cq = lane & 3;
+    const float sl2 = a.scale * kLog2eF8;
+    int it = 0;
+    bool dead = false;
+    while (walk.next(a, seg)) {
+        // B fragments of Q^T, column g of tile nt = query head 8 nt + g.  The head dims are permuted alike
+        // in Q and K: MMA step s gives k indices 2 cq + e and 2 cq + 8 + e (e = 0, 1) the dims
+        // (D / 4) cq + 4 s + e and + 2 + e, so that lane cq reads D / 4 consecutive code bytes of a key.
+        uint2 qf[NT][W];
+        float qs[NT][2];                                   // per own column 2 cq + e: sl2 times the row's power of two
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int r = 8 * nt + g;
+            uint2 w[W];
+            uint32_t m = 0;
+#pragma unroll
+            for (int s = 0; s < W; ++s) {
+                w[s] = make_uint2(0u, 0u);
+                if (r < G)
+                    w[s] = *reinterpret_cast<const uint2*>(a.q + ((size_t)seg.b * a.n_heads + seg.hk * G + r) * D +
+                                                           (D / 4) * cq + 4 * s);
+                m = max(m, max(max(w[s].x & 0x7fffu, (w[s].x >> 16) & 0x7fffu),
+                               max(w[s].y & 0x7fffu, (w[s].y >> 16) & 0x7fffu)));
+            }
+            m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+            m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+            // exponent of the row's largest element; a row of zeros, or with an infinity or NaN, stays as it is
+            int ex = (int)(m >> 7) - 127;
+            if (m == 0u || m >= 0x7f80u) ex = 14;
+            // two powers of two, since their product may leave float32's range
+            const int e0 = (14 - ex) / 2, e1 = 14 - ex - e0;
+            const float up0 = __uint_as_float((uint32_t)(e0 + 127) << 23), up1 = __uint_as_float((uint32_t)(e1 + 127) << 23);
+#pragma unroll
+            for (int s = 0; s < W; ++s) {
+                qf[nt][s].x = pack_f16x2(bf16_lo(w[s].x) * up0 * up1, bf16_hi(w[s].x) * up0 * up1);
+                qf[nt][s].y = pack_f16x2(bf16_lo(w[s].y) * up0 * up1, bf16_hi(w[s].y) * up0 * up1);
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int exc = __shfl_sync(0xffffffffu, ex, 4 * (2 * cq + e));   // of query row 8 nt + 2 cq + e
+                qs[nt][e] = scalbnf(sl2, exc - 14);
+            }
+        }
+        // O^T: row r of tile t is head dim (D / 8)(r & 7) + 2 t + (r >> 3), column n of tile nt query head
+        // 8 nt + n; per query column the running max m (the exponent base) and the lane's part of the sum l.
+        float acc[NT][W][4];
+        float m[NT][2], l[NT][2];
+        int E = -1000;                                     // exponent of the accumulator
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int t = 0; t < W; ++t) acc[nt][t][0] = acc[nt][t][1] = acc[nt][t][2] = acc[nt][t][3] = 0.f;
+            m[nt][0] = m[nt][1] = -INFINITY;
+            l[nt][0] = l[nt][1] = 0.f;
+        }
+        for (int kt = seg.kt0; kt < seg.kt1 && !dead; ++kt, ++it) {
+            const int st = it % STAGES;
+            const uint32_t ph = (uint32_t)(it / STAGES) & 1u;
+            if (!__all_sync(0xffffffffu, mbar_wait_bounded(&full_bar[st], ph, &abort_s, a.status))) {
+                dead = true;
+                break;
+            }
+            const uint32_t okmask = (uint32_t)(valid_s[st] >> (warp * 16)) & 0xffffu;
+            if (okmask) {
+                const uint8_t* ktile = sk + st * TILE;
+                const uint8_t* vtile = sv + st * TILE;
+                const float2 kv = scale_s[st][warp];
+                // S^T = K Q^T: A rows g and g + 8 are the warp's keys g and g + 8.  Keys that are not cached
+                // hold whatever was there; their scores are masked below.
+                uint32_t kw[2][W];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int R = warp * 16 + j * 8 + g;
+#pragma unroll
+                    for (int c = 0; c < W / 4; ++c) {
+                        const uint4 w = *reinterpret_cast<const uint4*>(ktile + f8_chunk<D>(R, cq * (D / 4) + 16 * c));
+                        kw[j][4 * c] = w.x; kw[j][4 * c + 1] = w.y; kw[j][4 * c + 2] = w.z; kw[j][4 * c + 3] = w.w;
+                    }
+                }
+                float s[NT][4];
+                {
+                    float sp[NT][2][4];                    // two accumulators halve the MMA chain
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) sp[nt][h][0] = sp[nt][h][1] = sp[nt][h][2] = sp[nt][h][3] = 0.f;
+#pragma unroll
+                    for (int ks = 0; ks < W; ++ks) {
+                        uint32_t af[4];
+                        e4m3x4_to_f16x4(kw[0][ks], af[0], af[2]);
+                        e4m3x4_to_f16x4(kw[1][ks], af[1], af[3]);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) mma_f16_16816(sp[nt][ks & 1], af, qf[nt][ks].x, qf[nt][ks].y);
+                    }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) s[nt][j] = sp[nt][0][j] + sp[nt][1][j];
+                }
+                // lane: keys g (s[.][0..1]) and g + 8 (s[.][2..3]) of query columns 2 cq and 2 cq + 1
+                const bool v0 = (okmask >> g) & 1u, v1 = (okmask >> (g + 8)) & 1u;
+                float mx[NT][2];
+                bool grow = false;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float f = qs[nt][e] * kv.x;
+                        s[nt][e] = v0 ? s[nt][e] * f : -INFINITY;
+                        s[nt][2 + e] = v1 ? s[nt][2 + e] * f : -INFINITY;
+                        mx[nt][e] = fmaxf(s[nt][e], s[nt][2 + e]);
+#pragma unroll
+                        for (int o = 4; o <= 16; o <<= 1) mx[nt][e] = fmaxf(mx[nt][e], __shfl_xor_sync(0xffffffffu, mx[nt][e], o));
+                        grow = grow || mx[nt][e] > m[nt][e] + 8.f;
+                    }
+                }
+                // The exponent base of a column moves only when its max grows by more than 2^8, so that
+                // probabilities stay below 2^8; otherwise the running sums need no rescaling.
+                if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float mn = mx[nt][e] > m[nt][e] + 8.f ? mx[nt][e] : m[nt][e];
+                            const float al = mn == m[nt][e] ? 1.f : ex2_approx(m[nt][e] - mn);
+                            l[nt][e] *= al;
+#pragma unroll
+                            for (int t = 0; t < W; ++t) {
+                                acc[nt][t][e] *= al;
+                                acc[nt][t][e + 2] *= al;
+                            }
+                            m[nt][e] = mn;
+                        }
+                }
+                // the block's V scale relative to the accumulator's exponent
+                const uint32_t vbits = __float_as_uint(kv.y);
+                const int ev = (int)(vbits >> 23) - 127;
+                if (kv.y > 0.f && ev > E) {
+                    if (E > -1000) {
+                        const float down = E - ev < -126 ? 0.f : __uint_as_float((uint32_t)(E - ev + 127) << 23);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int t = 0; t < W; ++t)
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) acc[nt][t][j] *= down;
+                    }
+                    E = ev;
+                }
+                const float vr = kv.y > 0.f ? scalbnf(kv.y, kF8Shift - E) : kv.y;
+                uint32_t pb[NT][2];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const float b0 = (m[nt][0] == -INFINITY) ? 0.f : m[nt][0];
+                    const float b1 = (m[nt][1] == -INFINITY) ? 0.f : m[nt][1];
+                    const float p00 = ex2_approx(s[nt][0] - b0), p01 = ex2_approx(s[nt][1] - b1);
+                    const float p10 = ex2_approx(s[nt][2] - b0), p11 = ex2_approx(s[nt][3] - b1);
+                    l[nt][0] += p00 + p10;
+                    l[nt][1] += p01 + p11;
+                    pb[nt][0] = movmatrix_trans(pack_f16x2(p00 * vr, p01 * vr));     // keys 0-7
+                    pb[nt][1] = movmatrix_trans(pack_f16x2(p10 * vr, p11 * vr));     // keys 8-15
+                }
+                // O^T += V^T P^T: lane g reads D / 8 consecutive code bytes (dims) of each of its key rows
+                // 2 cq, 2 cq + 1, 2 cq + 8, 2 cq + 9 and byte-interleaves the rows of a key pair: word i gives
+                // tiles 2 i and 2 i + 1.  Rows without a cached key count as zeros: 0 * NaN is not 0.
+                uint32_t vw[4][W / 2];
+#pragma unroll
+                for (int q4 = 0; q4 < 4; ++q4) {
+                    const int key = 2 * cq + (q4 & 1) + (q4 >> 1) * 8;
+                    const int R = warp * 16 + key;
+                    if constexpr (D == 128) {
+                        const uint4 w = *reinterpret_cast<const uint4*>(vtile + f8_chunk<D>(R, 16 * g));
+                        vw[q4][0] = w.x; vw[q4][1] = w.y; vw[q4][2] = w.z; vw[q4][3] = w.w;
+                    } else {
+                        const uint2 w = *reinterpret_cast<const uint2*>(vtile + f8_chunk<D>(R, 8 * g) + (g & 1) * 8);
+                        vw[q4][0] = w.x; vw[q4][1] = w.y;
+                    }
+                    if (okmask != 0xffffu && !((okmask >> key) & 1u)) {
+#pragma unroll
+                        for (int i = 0; i < W / 2; ++i) vw[q4][i] = 0u;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < W / 2; ++i) {
+                    uint32_t x01, y01, x23, y23;
+                    asm("prmt.b32 %0, %1, %2, 0x5140;" : "=r"(x01) : "r"(vw[0][i]), "r"(vw[1][i]));
+                    asm("prmt.b32 %0, %1, %2, 0x7362;" : "=r"(y01) : "r"(vw[0][i]), "r"(vw[1][i]));
+                    asm("prmt.b32 %0, %1, %2, 0x5140;" : "=r"(x23) : "r"(vw[2][i]), "r"(vw[3][i]));
+                    asm("prmt.b32 %0, %1, %2, 0x7362;" : "=r"(y23) : "r"(vw[2][i]), "r"(vw[3][i]));
+                    uint32_t at0[4], at1[4];
+                    e4m3x4_to_f16x4(x01, at0[0], at0[1]);
+                    e4m3x4_to_f16x4(x23, at0[2], at0[3]);
+                    e4m3x4_to_f16x4(y01, at1[0], at1[1]);
+                    e4m3x4_to_f16x4(y23, at1[2], at1[3]);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        mma_f16_16816(acc[nt][2 * i], at0, pb[nt][0], pb[nt][1]);
+                        mma_f16_16816(acc[nt][2 * i + 1], at1, pb[nt][0], pb[nt][1]);
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty_bar[st]);
+        }
+        // ------------------------------------------------ the segment's end: merge the four warps
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int o = 4; o <= 16; o <<= 1) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], o);
+        asm volatile("bar.sync 1, 128;" ::: "memory");         // the buffer's last readers are done
+        if (lane == 0) s_exp[warp] = E;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            if (g == 0) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) s_ml[warp][8 * nt + 2 * cq + e] = make_float2(m[nt][e], l[nt][e]);
+            }
+#pragma unroll
+            for (int t = 0; t < W; ++t)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int r = 8 * nt + 2 * cq + (j & 1);
+                    if (r < G) s_acc[(warp * G + r) * D + (D / 8) * g + 2 * t + (j >> 1)] = acc[nt][t][j];
+                }
+        }
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        int Em = -1000;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) Em = max(Em, s_exp[w]);
+        const bool whole = seg.kt0 == 0 && seg.kt1 == seg.n_kt;
+        // slot 0: the segment holds the share's first tile; 1: it is the share's last one
+        const int slot = 2 * cta + (it == (int)(t_end - t_begin) && it > seg.kt1 - seg.kt0 ? 1 : 0);
+        for (int i = threadIdx.x; i < G * D; i += NCONS) {
+            const int r = i / D, col = i % D;
+            float M = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) M = fmaxf(M, s_ml[w][r].x);
+            const float base = (M == -INFINITY) ? 0.f : M;
+            float num = 0.f, den = 0.f;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const float2 ml = s_ml[w][r];
+                const float e = exp2f(ml.x - base);
+                const int de = s_exp[w] - Em;
+                num += e * (de < -126 ? 0.f : __uint_as_float((uint32_t)(de + 127) << 23)) * s_acc[(w * G + r) * D + col];
+                den += e * ml.y;
+            }
+            // no valid key: zeros
+            const float o = den == 0.f ? 0.f : scalbnf(num / den, Em > -1000 ? Em - kF8Shift : 0);
+            if (whole) {
+                a.out[((size_t)seg.b * a.n_heads + (size_t)seg.hk * G + r) * D + col] = __float2bfloat16_rn(o);
+            } else {
+                a.part_o[((size_t)slot * G + r) * D + col] = o;
+                if (col == 0) a.part_ml[(size_t)slot * G + r] = make_float2(M, den);
+            }
+        }
+    }
+}
+
+// Joins the partials of each (sequence, KV head) whose tiles several CTAs of the grid of P shared, and
+// writes zeros for sequences without a key.  Grid (KV head, sequence).
+__global__ void __launch_bounds__(128) attn_decode_f8_join_kernel(const AttnF8Args a, int P) {
+    __shared__ long long s_sums[4], s_before;
+    pdl_wait();
+    pdl_trigger();
+    const int hk = blockIdx.x, b = blockIdx.y;
+    const int G = a.n_heads / a.n_kv_heads, D = a.head_dim;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    long long all = 0, before = 0;
+    for (int i = threadIdx.x; i < a.batch; i += 128) {
+        const int n = f8_tiles(f8_context(a, i, false));
+        all += n;
+        if (i < b) before += n;
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) {
+        all += __shfl_xor_sync(0xffffffffu, all, o);
+        before += __shfl_xor_sync(0xffffffffu, before, o);
+    }
+    if (lane == 0) s_sums[warp] = all;
+    if (threadIdx.x == 0) s_before = 0;
+    __syncthreads();
+    all = s_sums[0] + s_sums[1] + s_sums[2] + s_sums[3];
+    if (lane == 0) atomicAdd(reinterpret_cast<unsigned long long*>(&s_before), (unsigned long long)before);
+    __syncthreads();
+    const int n = f8_tiles(f8_context(a, b, false));
+    __nv_bfloat16* out = a.out + ((size_t)b * a.n_heads + (size_t)hk * G) * D;
+    if (n == 0) {
+        for (int i = threadIdx.x; i < G * D; i += 128) out[i] = __float2bfloat16_rn(0.f);
+        return;
+    }
+    const long long total = all * a.n_kv_heads;
+    const long long u0 = s_before * a.n_kv_heads + (long long)hk * n, u1 = u0 + n;
+    const int c0 = share_of(total, P, u0), c1 = share_of(total, P, u1 - 1);
+    if (c0 == c1) return;                                  // one CTA had them all
+    // partial of CTA c: its slot 0 where the tiles reach the share's first, else its slot 1
+    auto slot = [&](int c) { return 2 * c + (share_begin(total, P, c) >= u0 ? 0 : 1); };
+    for (int i = threadIdx.x; i < G * D; i += 128) {
+        const int r = i / D, col = i % D;
+        float M = -INFINITY;
+        for (int c = c0; c <= c1; ++c) M = fmaxf(M, a.part_ml[(size_t)slot(c) * G + r].x);
+        const float base = (M == -INFINITY) ? 0.f : M;
+        float num = 0.f, den = 0.f;
+        for (int c = c0; c <= c1; ++c) {
+            const size_t pr = (size_t)slot(c) * G + r;
+            const float2 ml = a.part_ml[pr];
+            const float w = exp2f(ml.x - base) * ml.y;
+            num += w * a.part_o[pr * D + col];
+            den += w;
+        }
+        out[i] = __float2bfloat16_rn(den == 0.f ? 0.f : num / den);
+    }
+}
+
+int f8_ctas_per_sm(int G, int D) {
+    const size_t smem = (size_t)2 * kF8Stages * kF8Tile * D + (size_t)4 * G * D * 4 + 1024;
+    return std::min(G <= 8 ? kF8MaxCtasPerSm : 2, (int)((220 * 1024) / (smem + 2048)));
+}
+
+template <int D, int NT>
+cudaError_t decode_f8_for(const AttnF8Args& a, cudaStream_t stream) {
+    const int G = a.n_heads / a.n_kv_heads;
+    const size_t smem = (size_t)2 * kF8Stages * kF8Tile * D + (size_t)4 * G * D * 4 + 1024;
+    const size_t smem_max = (size_t)2 * kF8Stages * kF8Tile * D + (size_t)4 * 8 * NT * D * 4 + 1024;
+    const void* kernel = (const void*)attn_decode_f8_kernel<D, NT>;
+    cudaError_t e = ensure_func_attr(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_max,
+                                     "cudaFuncSetAttribute(attn_decode_f8_kernel)");
+    if (e == cudaSuccess)
+        e = ensure_func_attr(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, (int)cudaSharedmemCarveoutMaxShared,
+                             "cudaFuncSetAttribute(attn_decode_f8_kernel carveout)");
+    if (e != cudaSuccess) return e;
+    const int sms = std::min(device_sm_count(), kF8MaxSms);
+    if (sms <= 0) return record(cudaErrorNoDevice, "attn_decode_f8");
+    const long long most = (long long)a.batch * a.n_kv_heads *
+                           (((long long)a.max_blocks * a.block_size + kF8Tile - 1) / kF8Tile);
+    const int P = (int)std::min<long long>(most, (long long)sms * f8_ctas_per_sm(G, D));
+    CUtensorMap tmK, tmV;
+    const uint64_t lines = (uint64_t)a.num_blocks * a.n_kv_heads * a.block_size * D / 128;
+    const uint32_t box = (uint32_t)(std::min(a.block_size, kF8Tile) * D / 128);
+    if (!make_tmap_u8_sw128(&tmK, a.k_pool, lines, box) || !make_tmap_u8_sw128(&tmV, a.v_pool, lines, box))
+        return cudaErrorInvalidValue;
+    trace_before("attn_decode_f8", stream);
+    e = launch_pdl(attn_decode_f8_kernel<D, NT>, dim3((unsigned)P), dim3(kF8Threads), smem, stream, 1, tmK, tmV, a);
+    trace_after(stream);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    if (e != cudaSuccess) return record(e, "attn_decode_f8_kernel launch");
+    trace_before("attn_decode_f8_join", stream);
+    e = launch_pdl(attn_decode_f8_join_kernel, dim3((unsigned)a.n_kv_heads, (unsigned)a.batch), dim3(128), 0, stream, 1, a, P);
+    trace_after(stream);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    return record(e, "attn_decode_f8_join_kernel launch");
+}
+
+}  // namespace
+
+// Two partials per CTA, G rows each; the bound takes the largest grid on any device.
+size_t attn_decode_f8_scratch_bytes(int batch, int n_heads, int n_kv_heads, int head_dim) {
+    const int G = n_heads / n_kv_heads;
+    const size_t rows = (size_t)2 * kF8MaxSms * f8_ctas_per_sm(G, head_dim) * G;
+    (void)batch;
+    return rows * head_dim * sizeof(float) + rows * sizeof(float2);
+}
+
+cudaError_t launch_attn_decode_f8(AttnF8Args a, void* workspace, cudaStream_t stream) {
+    const int G = a.n_heads / a.n_kv_heads, D = a.head_dim;
+    const size_t rows = (size_t)2 * kF8MaxSms * f8_ctas_per_sm(G, D) * G;
+    a.part_o = static_cast<float*>(workspace);
+    a.part_ml = reinterpret_cast<float2*>(a.part_o + rows * D);
+    if (D == 128) return G <= 8 ? decode_f8_for<128, 1>(a, stream) : decode_f8_for<128, 2>(a, stream);
+    return G <= 8 ? decode_f8_for<64, 1>(a, stream) : decode_f8_for<64, 2>(a, stream);
+}
+
+}  // namespace ll

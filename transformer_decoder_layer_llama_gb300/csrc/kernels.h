@@ -185,6 +185,87 @@ cudaError_t launch_attn_decode(const AttnDecodeArgs& a, cudaStream_t stream);
 // Decode attention over an INT8 pool (k_q8/v_q8 + scales; head_dim 128).
 cudaError_t launch_attn_decode_q8(const AttnDecodeArgs& a, cudaStream_t stream);
 
+// Rotary positions as an operator (rope.cu): q [tokens][n_heads][head_dim] and k
+// [tokens][n_kv_heads][head_dim] with strides between tokens in elements.
+struct RopeArgs {
+    const void *q, *k;
+    void *q_out, *k_out;
+    long long q_stride, k_stride, q_out_stride, k_out_stride;
+    const int32_t* positions;
+    const float2* table;           // [max_position][rotary_dim / 2] (cos, sin)
+    int tokens, n_heads, n_kv_heads, head_dim, rotary_dim, max_position;
+    bool interleaved, backward;
+    bool copy_tail;                // elements from rotary_dim on are copied (not in place)
+    int32_t* status;
+};
+cudaError_t launch_rope(const RopeArgs& a, bool f32, cudaStream_t stream);
+
+// Scaled frequencies of a cos/sin table (see rope.cu); ramp_lo and ramp_width in pairs.
+struct RopeTableArgs {
+    int rotary_dim, scaling;       // scaling: LL_ROPE_PLAIN ...
+    double theta, factor, original, low, high, ramp_lo, ramp_width, magnitude;
+};
+cudaError_t launch_rope_scaled_table(float2* cs, int max_position, const RopeTableArgs& f, cudaStream_t stream);
+
+// A cache of e4m3 codes [num_blocks][n_kv_heads][block_size][head_dim] with scales
+// [num_blocks][n_kv_heads] (kv_f8.cu writes it, attn_f8.cu and attn_f8_tc.cu read it).
+struct AppendArgs {
+    const __nv_bfloat16 *k, *v;    // [tokens][n_kv_heads][head_dim], strides between tokens in elements
+    long long k_stride, v_stride;
+    const int32_t* cu_new;         // [batch + 1] first row of each sequence's new tokens, or null: one each
+    const int32_t* context_lens;   // [batch] including the new tokens
+    const int32_t* block_table;
+    uint8_t *k_pool, *v_pool;
+    float *k_scale, *v_scale;
+    int tokens, batch, max_new, n_kv_heads, head_dim, block_size, num_blocks, max_blocks;
+    int32_t* status;
+};
+cudaError_t launch_append_f8(const AppendArgs& a, cudaStream_t stream);
+
+struct AttnF8Args {
+    const __nv_bfloat16* q;        // [tokens][n_heads][head_dim]
+    const uint8_t *k_pool, *v_pool;
+    const float *k_scale, *v_scale;
+    const int32_t* cu_new;         // prefill
+    const int32_t* context_lens;
+    const int32_t* block_table;
+    int tokens, batch, max_new, max_blocks, num_blocks, block_size, n_heads, n_kv_heads, head_dim;
+    float scale;
+    __nv_bfloat16* out;            // [tokens][n_heads][head_dim]
+    float* part_o;                 // scratch: partial rows [rows][head_dim]
+    float2* part_ml;               //          and their (max, sum) [rows]
+    int32_t* status;
+};
+constexpr int kF8MaxSms = 160;     // grids and scratch are sized for at most this many SMs
+size_t attn_decode_f8_scratch_bytes(int batch, int n_heads, int n_kv_heads, int head_dim);
+cudaError_t launch_attn_decode_f8(AttnF8Args a, void* workspace, cudaStream_t stream);
+size_t attn_prefill_f8_scratch_bytes(int batch, int tokens, int max_new, int n_heads, int n_kv_heads, int head_dim);
+cudaError_t launch_attn_prefill_f8(const AttnF8Args& a, void* workspace, cudaStream_t stream);
+
+// Copies blocks src -> dst of `pairs` in every tensor [num_blocks][bytes] (blocks.cu).
+constexpr int kCopyMaxTensors = 128;   // per launch
+struct CopyBlocksArgs {
+    void* data[kCopyMaxTensors];
+    long long bytes[kCopyMaxTensors];          // of one block
+    int pieces[kCopyMaxTensors + 1];           // running count of pieces; [n_tensors]: per pair
+    int n_tensors, num_blocks, max_pairs;
+    const int32_t* pairs;                      // [max_pairs][2]
+    const int32_t* n_pairs;                    // device count, or null: max_pairs
+    int32_t* status;
+};
+int copy_blocks_piece_bytes();
+cudaError_t launch_copy_blocks(const CopyBlocksArgs& a, cudaStream_t stream);
+
+constexpr int kCompactMaxBlocks = 1 << 19;
+struct CompactArgs {
+    const int32_t* table;
+    long long entries;
+    int num_blocks, pair_rows;
+    int32_t *new_table, *pairs, *counts, *block_map;
+    int32_t* status;
+};
+cudaError_t launch_compact_plan(const CompactArgs& a, cudaStream_t stream);
+
 // Step-by-step operators (each one kernel; arithmetic as in the fused epilogues).
 // RotaryEmbedding of the merged QKV Linear output (float32, packed column order) into
 // q, k (rotated) and v, BF16 [tokens][heads * head_dim] in element order.
