@@ -1,22 +1,21 @@
 // Prefill attention over a paged cache of e4m3 codes with one scale per block and KV head, on the
 // tcgen05 tensor cores: a ragged batch of new tokens, each attending causally to its own sequence.
 //
-// A work item is one KV head of one sequence and a tile of 128 query rows: floor(128 / G) consecutive
-// tokens times the G query heads that share the KV head, so that a tile of keys is brought in and
-// converted once for the whole group.  One CTA per item, 128 keys at a time up to the tile's last
-// position, items with the most keys first.  Two CTAs share an SM (256 TMEM columns and 98 KB of shared
-// memory each): while one computes its softmax the other has the tensor core, and one's start and end
-// hide behind the other.
+// A work item is one KV head of one sequence and two tiles (A, B) of 128 query rows each: a tile is
+// floor(128 / G) consecutive tokens times the G query heads that share the KV head, so a tile of keys is
+// brought in and converted once for 256 rows.  One CTA per SM and item, 128 keys at a time up to the
+// item's last position, items with the most keys first.
 //
-// Roles (288 threads):
-//  * warps 0-3, softmax: one thread per query row.  First they stage Q in shared memory as FP16.  Per key
-//    tile they read S from TMEM twice (row maximum; then probabilities), write P over S as FP16 and, where
-//    the maximum has grown by more than 2^8, scale the running O in TMEM.  At the end O / l goes out.
-//  * warps 4-7, keys and values: the codes come straight from global memory into registers, one tile
-//    ahead (L2 mostly, since all row tiles of a KV head read the same codes), become FP16 and are stored as
-//    the 128-byte-swizzled operand tiles.  There is one K and one V buffer: K of the next tile is stored
-//    while the softmax works, V while the next S is computed.
-//  * warp 8, one thread: S = Q K^T (both from shared memory), O += P V (P from TMEM).
+// Roles (416 threads):
+//  * warps 0-3 and 4-7, softmax of tile A and B: one thread per query row.  First they stage Q in shared
+//    memory as FP16.  Per key tile: the row of S from TMEM into registers, its maximum, probabilities
+//    written over S as FP16; where the maximum has grown by more than 2^8 the running O in TMEM is scaled.
+//    At the end O / l goes out.
+//  * warps 8-11, keys and values: the codes come straight from global memory into registers, a tile
+//    ahead (L2 mostly, since all items of a KV head read the same codes), become FP16 and are stored as the
+//    128-byte-swizzled operand tiles, two buffers each for K and V.  Block ids are read two tiles ahead.
+//  * warp 12, one thread: S = Q K^T (both from shared memory), O += P V (P from TMEM), alternating
+//    between A and B, so that the tensor core works for one tile while the other's softmax runs.
 //
 // Precision.  Codes are exact in FP16.  A query row is scaled by a power of two so that its largest element
 // lies in [2^14, 2^15); its factor and the block's K scale multiply the float32 score, 16 keys at a time
@@ -35,10 +34,11 @@ namespace ll {
 
 namespace {
 
-constexpr int kPfThreads = 288;
-constexpr int kPfRows = 128;             // query rows per item
+constexpr int kPfThreads = 512;         // four groups of 128: the register split is set per group
+constexpr int kPfRows = 128;             // query rows per tile
 constexpr int kPfKeys = 128;             // keys per tile
 constexpr int kPfChunks = kPfKeys / 16;
+constexpr int kPfMeta = 4;               // tiles whose scales are kept
 constexpr float kPfLog2e = 1.4426950408889634f;
 constexpr int kPfShift = 6;              // V enters P V times 2^6
 constexpr float kPfBase = 6.f;           // and P times 2^6
@@ -46,8 +46,9 @@ constexpr float kPfBase = 6.f;           // and P times 2^6
 template <int D>
 struct PfLayout {
     static constexpr uint32_t TILE = kPfRows * D * 2;       // [D / 64][128 rows][128 B] FP16
-    static constexpr uint32_t OFF_Q = 0, OFF_K = TILE, OFF_V = 2 * TILE, TOTAL = 3 * TILE;
-    static constexpr uint32_t TMEM_S = 0, TMEM_O = 128, TMEM_COLS = 256;
+    static constexpr uint32_t OFF_Q = 0;                    // A, B
+    static constexpr uint32_t OFF_K = 2 * TILE, OFF_V = 4 * TILE, TOTAL = 6 * TILE;   // two buffers each
+    static constexpr uint32_t TMEM_S = 0, TMEM_O = 256, TMEM_COLS = 512;              // A, B 128 columns on
 };
 
 // kind::f16 instruction descriptor, FP16 A and B, float32 D; b_mn: B is MN-major.
@@ -75,25 +76,33 @@ LL_DEVINL uint32_t pf_off(int r, int c) {
 
 LL_DEVINL void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-LL_DEVINL void tmem_ld32(uint32_t taddr, float (&v)[32]) {
-    uint32_t r[32];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr)
-        : "memory");
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+// Two float32 operations in one instruction.
+LL_DEVINL float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%6, %7};\n"
+        " fma.rn.f32x2 x, x, y, z;\n mov.b64 {%0, %1}, x;\n}\n"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+LL_DEVINL float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n .reg .b64 x, y;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n add.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}\n"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+LL_DEVINL float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
 }
 
-// What a work item covers: new tokens t0 .. t0 + nt - 1 of sequence b (rows tok0 + t of q), the first at
-// position pos0; keys 0 .. kv_end - 1.
+// What a work item covers: new tokens t0 .. of sequence b (rows tok0 + t of q), the first at position pos0;
+// nt_a and nt_b tokens in the tiles, which see keys 0 .. end_a - 1 and 0 .. end_b - 1 (0: no tile B).
 struct PfItem {
-    int b, hk, tok0, nt, pos0, kv_end;
+    int b, hk, tok0, pos0, tt;
+    int nt_a, nt_b, end_a, end_b;
 };
 
 LL_DEVINL bool pf_item(const AttnF8Args& a, int n_mt, int tt, bool flag, PfItem& it) {
@@ -110,40 +119,49 @@ LL_DEVINL bool pf_item(const AttnF8Args& a, int n_mt, int tt, bool flag, PfItem&
         if (flag) flag_status(a.status, LL_DEV_BAD_POSITION);
         return false;
     }
-    const int t0 = mt * tt;
+    const int t0 = mt * 2 * tt;
     if (t0 >= n) return false;
+    const int left = (int)n - t0;
+    it.tt = tt;
     it.tok0 = c0 + t0;
-    it.nt = min(tt, (int)n - t0);
-    it.pos0 = ctx - (int)n + t0;
-    it.kv_end = it.pos0 + it.nt;
+    it.pos0 = ctx - left;
+    it.nt_a = min(tt, left);
+    it.nt_b = min(tt, left - it.nt_a);
+    it.end_a = it.pos0 + it.nt_a;
+    it.end_b = it.nt_b ? it.end_a + it.nt_b : 0;
     return true;
 }
 
 template <int D>
-__global__ void __launch_bounds__(kPfThreads, 2) attn_prefill_f8_kernel(const AttnF8Args a, int n_mt, int tt) {
+__global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const AttnF8Args a, int n_mt, int tt) {
     using L = PfLayout<D>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    // per key tile j.  k_ready has a barrier per parity because the softmax threads wait for it too, and
-    // tile j + 1 may be ready before the last of them has looked at tile j.
-    __shared__ uint64_t q_ready, k_ready[2], v_ready, s_full, p_ready, pv_done, o_done, drain;
+    // Per query tile x and key tile j (parity j & 1): S computed, P stored.  Per key buffer: K or V stored
+    // (ready), read by both query tiles (empty).  Scales of key tile j sit in slot j & 3: slot and barrier
+    // are written again for tile j + 4, after the S of tile j + 2, which waits for the P of tile j + 1.
+    __shared__ uint64_t q_ready[2], s_full[2], p_ready[2], o_done[2], k_ready[2], k_empty[2], v_ready[2], v_empty[2];
+    __shared__ uint64_t meta_ready[kPfMeta], drain;
     __shared__ uint32_t tmem_base_s;
     __shared__ int abort_s;
-    __shared__ float ks_s[2][kPfChunks];                    // per parity and 16-key chunk: K scale
-    __shared__ uint32_t ok_s[2];                            // per parity: bit c = chunk c is backed by a valid block
+    __shared__ __align__(16) float ks_s[kPfMeta][kPfChunks];   // per 16-key chunk: K scale
+    __shared__ uint32_t ok_s[kPfMeta];                      // bit c = chunk c is backed by a valid block
     __shared__ int vexp_w[4], vexp_s;                       // exponent of the item's largest V scale
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int32_t* status = a.status;
     if (threadIdx.x == 0) {
-        mbar_init(&q_ready, 128);
-        mbar_init(&k_ready[0], 128);
-        mbar_init(&k_ready[1], 128);
-        mbar_init(&v_ready, 128);
-        mbar_init(&s_full, 1);
-        mbar_init(&p_ready, 128);
-        mbar_init(&pv_done, 1);
-        mbar_init(&o_done, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&q_ready[i], 4);
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_ready[i], 4);
+            mbar_init(&o_done[i], 1);
+            mbar_init(&k_ready[i], 4);
+            mbar_init(&k_empty[i], 1);
+            mbar_init(&v_ready[i], 4);
+            mbar_init(&v_empty[i], 1);
+        }
+        for (int i = 0; i < kPfMeta; ++i) mbar_init(&meta_ready[i], 1);
         mbar_init(&drain, 1);
         abort_s = 0;
         fence_mbar_init();
@@ -152,7 +170,7 @@ __global__ void __launch_bounds__(kPfThreads, 2) attn_prefill_f8_kernel(const At
     pdl_trigger();
     PfItem it;
     if (!pf_item(a, n_mt, tt, threadIdx.x == 0, it)) return;
-    if (warp == 8) {
+    if (warp == 12) {
         tmem_alloc(&tmem_base_s, L::TMEM_COLS);
         tmem_relinquish();
     }
@@ -161,161 +179,197 @@ __global__ void __launch_bounds__(kPfThreads, 2) attn_prefill_f8_kernel(const At
     tc_fence_after();
     const uint32_t tmem = tmem_base_s;
     const int G = a.n_heads / a.n_kv_heads;
-    const int n_kt = (it.kv_end + kPfKeys - 1) / kPfKeys;
+    const int n_a = (it.end_a + kPfKeys - 1) / kPfKeys, n_b = (it.end_b + kPfKeys - 1) / kPfKeys;
+    const int n_kt = max(n_a, n_b), kv_end = max(it.end_a, it.end_b);
 
-    if (warp == 8) {
-        if (lane == 0) {
-            // ------------------------------------------------ MMA issuer
+    if (warp >= 12) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        if (warp == 12 && lane == 0) {
+            // ------------------------------------------------ MMA issuer (warps 13-15 are idle)
             const uint32_t id_s = idesc_f16(kPfRows, kPfKeys, false);
             const uint32_t id_o = idesc_f16(kPfRows, D, true);
             const uint32_t sq = smem_u32(smem + L::OFF_Q), sk = smem_u32(smem + L::OFF_K), sv = smem_u32(smem + L::OFF_V);
-            bool ok = mbar_wait_bounded(&q_ready, 0, &abort_s, status);
-            for (int j = 0; j < n_kt && ok; ++j) {
-                if (!mbar_wait_bounded(&k_ready[j & 1], (uint32_t)(j >> 1) & 1u, &abort_s, status)) break;
+            // S_x of key tile j; it overwrites P_x of tile j - 1 (MMAs of one thread run in order)
+            auto issue_s = [&](int x, int j) -> bool {
+                if (!mbar_wait_bounded(&k_ready[j & 1], (uint32_t)(j >> 1) & 1u, &abort_s, status)) return false;
+                if (j == 0 && !mbar_wait_bounded(&q_ready[x], 0, &abort_s, status)) return false;
                 tc_fence_after();
-                // S overwrites P of tile j - 1: MMAs of one thread run in order
+                uint64_t dq = umma_desc_sw128(sq + (uint32_t)x * L::TILE);
+                uint64_t dk = umma_desc_sw128(sk + (uint32_t)(j & 1) * L::TILE);
+                asm volatile("" : "+l"(dq), "+l"(dk));      // else every step's descriptors are kept, in local memory
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t off = (uint32_t)(kk >> 2) * (kPfRows * 128) + (uint32_t)(kk & 3) * 32;
-                    tc_mma_bf16(tmem + L::TMEM_S, umma_desc_sw128(sq + off), umma_desc_sw128(sk + off), id_s, kk > 0 ? 1u : 0u);
+                    // the descriptor's address field counts 16 bytes
+                    const uint32_t off = ((uint32_t)(kk >> 2) * (kPfRows * 128) + (uint32_t)(kk & 3) * 32) >> 4;
+                    tc_mma_bf16(tmem + L::TMEM_S + (uint32_t)x * 128u, dq + off, dk + off, id_s, kk > 0 ? 1u : 0u);
                 }
-                tc_commit(&s_full);
-                if (!mbar_wait_bounded(&v_ready, (uint32_t)j & 1u, &abort_s, status)) break;
-                if (!mbar_wait_bounded(&p_ready, (uint32_t)j & 1u, &abort_s, status)) break;
+                tc_commit(&s_full[x]);
+                return true;
+            };
+            auto issue_pv = [&](int x, int j) -> bool {
+                if (!mbar_wait_bounded(&v_ready[j & 1], (uint32_t)(j >> 1) & 1u, &abort_s, status)) return false;
+                if (!mbar_wait_bounded(&p_ready[x], (uint32_t)j & 1u, &abort_s, status)) return false;
                 tc_fence_after();
+                uint64_t dv = pf_desc_mn(sv + (uint32_t)(j & 1) * L::TILE, kPfRows * 128);
+                asm volatile("" : "+l"(dv));
 #pragma unroll
                 for (int kk = 0; kk < kPfKeys / 16; ++kk)
-                    tc_mma_bf16_ts(tmem + L::TMEM_O, tmem + L::TMEM_S + (uint32_t)kk * 8u,
-                                   pf_desc_mn(sv + (uint32_t)kk * 2048u, kPfRows * 128), id_o, (j > 0 || kk > 0) ? 1u : 0u);
-                tc_commit(&pv_done);
+                    tc_mma_bf16_ts(tmem + L::TMEM_O + (uint32_t)x * 128u, tmem + L::TMEM_S + (uint32_t)x * 128u + (uint32_t)kk * 8u,
+                                   dv + (uint32_t)(kk * 2048 >> 4), id_o, (j > 0 || kk > 0) ? 1u : 0u);
+                return true;
+            };
+            bool ok = (n_a == 0 || issue_s(0, 0)) && (n_b == 0 || issue_s(1, 0));
+            if (ok) tc_commit(&k_empty[0]);
+            for (int j = 0; j < n_kt && ok; ++j) {
+                if (j < n_a) {
+                    ok = issue_pv(0, j);
+                    if (ok && j + 1 == n_a) tc_commit(&o_done[0]);
+                    if (ok && j + 1 < n_a) ok = issue_s(0, j + 1);
+                }
+                if (ok && j < n_b) ok = issue_pv(1, j);
+                if (!ok) break;
+                tc_commit(&v_empty[j & 1]);
+                if (j + 1 == n_b) tc_commit(&o_done[1]);
+                if (j + 1 < n_b) ok = issue_s(1, j + 1);
+                if (ok && j + 1 < n_kt) tc_commit(&k_empty[(j + 1) & 1]);
             }
-            tc_commit(&o_done);
             tc_commit(&drain);
             volatile int never = 0;
             mbar_wait_bounded(&drain, 0, &never, status);
         }
         __syncwarp();
-    } else if (warp >= 4) {
-        // ---------------------------------------------------- keys and values (warps 4-7)
+    } else if (warp >= 8) {
+        // ---------------------------------------------------- keys and values (warps 8-11)
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
         constexpr int LANES = D / 16, ROWS = 128 / LANES, PER = kPfKeys / ROWS;   // lanes per row, rows per step, steps
-        const int tid = threadIdx.x - 128;
-        const int c16 = tid % LANES, rsub = tid / LANES;
+        const int tid = threadIdx.x - 256;
+        // Eight lanes that store together cover four 16-code pieces of two rows: their 16-byte chunks are 0, 2,
+        // 4, 6 of an even and an odd row, which the swizzle puts on different banks.
+        const int c16 = D == 128 ? (tid & 3) | ((tid >> 1) & 4) : tid & 3;
+        const int rsub = D == 128 ? ((tid >> 2) & 1) | ((tid >> 3) & ~1) : tid >> 2;
         const int32_t* table_row = a.block_table + (size_t)it.b * a.max_blocks;
-        // lane c < 8 of each warp looks after 16-key chunk c of a tile: its block (-1: none) and scales
-        auto block_of = [&](int j) {
-            const int key = j * kPfKeys + (lane & 7) * 16;
-            int blk = -1;
-            if (key < it.kv_end) {
-                blk = table_row[key / a.block_size];
-                if (blk < 0 || blk >= a.num_blocks) {
-                    flag_status(status, LL_DEV_BAD_BLOCK);
-                    blk = -1;
-                }
-            }
-            return blk;
+        const int my_key = (lane & 7) * 16;                 // lane c < 8 looks after 16-key chunk c of a tile
+        auto entry_of = [&](int j) {                        // its table entry (-1 past the keys)
+            const int key = j * kPfKeys + my_key;
+            return j < n_kt && key < kv_end ? table_row[key / a.block_size] : -1;
         };
-        auto scale_of = [&](const float* scales, int blk) {
-            return blk >= 0 ? scales[(size_t)blk * a.n_kv_heads + it.hk] : 0.f;
+        auto row_of = [&](int j, int entry) {               // its first pool row (-1: no valid block)
+            const int key = j * kPfKeys + my_key;
+            const bool want = j < n_kt && key < kv_end;
+            if (want && (entry < 0 || entry >= a.num_blocks)) flag_status(status, LL_DEV_BAD_BLOCK);
+            return want && entry >= 0 && entry < a.num_blocks
+                       ? (entry * a.n_kv_heads + it.hk) * a.block_size + key % a.block_size : -1;
         };
-        auto load = [&](const uint8_t* pool, int j, int blk_lane, uint4 (&w)[PER]) {
-#pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                const int r = i * ROWS + rsub, key = j * kPfKeys + r;
-                const int blk = __shfl_sync(0xffffffffu, blk_lane, r >> 4);
-                w[i] = make_uint4(0u, 0u, 0u, 0u);         // also rows that hold no key: 0 * stale stays 0
-                if (blk >= 0 && key < it.kv_end)
-                    w[i] = *reinterpret_cast<const uint4*>(
-                        pool + (((size_t)blk * a.n_kv_heads + it.hk) * a.block_size + (key % a.block_size)) * D + c16 * 16);
-            }
+        auto scale_of = [&](const float* scales, int row) {
+            return row >= 0 ? scales[(row / a.block_size)] : 0.f;
         };
-        auto store = [&](uint8_t* tile, const uint4 (&w)[PER], bool scaled, float ratio_lane) {
+        auto load = [&](const uint8_t* pool, int j, int row_lane, uint4 (&w)[PER]) {
+            const int left = kv_end - j * kPfKeys;          // keys of the tile
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
                 const int r = i * ROWS + rsub;
+                const int row = __shfl_sync(0xffffffffu, row_lane, r >> 4);
+                w[i] = make_uint4(0u, 0u, 0u, 0u);         // also rows that hold no key: 0 * stale stays 0
+                if (row >= 0 && r < left)
+                    w[i] = *reinterpret_cast<const uint4*>(pool + (size_t)(uint32_t)(row + (r & 15)) * D + c16 * 16);
+            }
+        };
+        const uint32_t st0 = pf_off(rsub, 2 * c16), st1 = pf_off(rsub, 2 * c16 + 1);
+        auto store = [&](uint8_t* tile, const uint4 (&w)[PER], bool scaled, float ratio_lane) {
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
                 uint32_t h[8];
                 e4m3x4_to_f16x4(w[i].x, h[0], h[1]);
                 e4m3x4_to_f16x4(w[i].y, h[2], h[3]);
                 e4m3x4_to_f16x4(w[i].z, h[4], h[5]);
                 e4m3x4_to_f16x4(w[i].w, h[6], h[7]);
                 if (scaled) {
-                    const __half2 f = __float2half2_rn(__shfl_sync(0xffffffffu, ratio_lane, r >> 4));
+                    const __half2 f = __float2half2_rn(__shfl_sync(0xffffffffu, ratio_lane, (i * ROWS + rsub) >> 4));
 #pragma unroll
                     for (int x = 0; x < 8; ++x) {
                         const __half2 p = __hmul2(*reinterpret_cast<const __half2*>(&h[x]), f);
                         h[x] = *reinterpret_cast<const uint32_t*>(&p);
                     }
                 }
-                // the two 16-byte chunks, the upper half of the head dims starting with its second one: the
-                // two halves' tiles share their banks
-                const int c = 2 * c16, odd = (c >> 3) & 1;
-                const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
-                *reinterpret_cast<uint4*>(tile + pf_off(r, c + odd)) = odd ? hi : lo;
-                *reinterpret_cast<uint4*>(tile + pf_off(r, c + 1 - odd)) = odd ? lo : hi;
+                *reinterpret_cast<uint4*>(tile + st0 + i * ROWS * 128) = make_uint4(h[0], h[1], h[2], h[3]);
+                *reinterpret_cast<uint4*>(tile + st1 + i * ROWS * 128) = make_uint4(h[4], h[5], h[6], h[7]);
             }
             fence_async_smem();
+            __syncwarp();
         };
         uint4 kw[PER], vw[PER];
-        int blk = block_of(0);
-        load(a.k_pool, 0, blk, kw);
-        load(a.v_pool, 0, blk, vw);
-        float ks = scale_of(a.k_scale, blk), vs = scale_of(a.v_scale, blk);
+        const int entry0 = entry_of(0);
+        int entry = entry_of(1);                            // of the tile after the one in registers
+        int row = row_of(0, entry0);
+        load(a.k_pool, 0, row, kw);
+        load(a.v_pool, 0, row, vw);
+        float ks = scale_of(a.k_scale, row), vs = scale_of(a.v_scale, row);
         int E = 0;
         for (int j = 0; j < n_kt; ++j) {
-            const int blk_next = j + 1 < n_kt ? block_of(j + 1) : -1;
+            const int entry2 = entry_of(j + 2);
             // (whole warps leave: the loads below shuffle)
-            if (j > 0 && !__all_sync(0xffffffffu, mbar_wait_bounded(&s_full, (uint32_t)(j - 1) & 1u, &abort_s, status))) break;
-            if (warp == 4) {
-                const uint32_t m = __ballot_sync(0xffffffffu, blk >= 0);
-                if (lane < kPfChunks) ks_s[j & 1][lane] = ks;
-                if (lane == 0) ok_s[j & 1] = m & ((1u << kPfChunks) - 1u);
+            if (j > 1 && !__all_sync(0xffffffffu, mbar_wait_bounded(&k_empty[j & 1], (uint32_t)((j - 2) >> 1) & 1u, &abort_s, status)))
+                break;
+            store(smem + L::OFF_K + (uint32_t)(j & 1) * L::TILE, kw, false, 0.f);
+            if (warp == 8) {
+                const uint32_t m = __ballot_sync(0xffffffffu, row >= 0);
+                if (lane < kPfChunks) ks_s[j & (kPfMeta - 1)][lane] = ks;
+                if (lane == 0) ok_s[j & (kPfMeta - 1)] = m & ((1u << kPfChunks) - 1u);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&meta_ready[j & (kPfMeta - 1)]);
             }
-            __syncwarp();
-            store(smem + L::OFF_K, kw, false, 0.f);
-            mbar_arrive(&k_ready[j & 1]);
-            if (j + 1 < n_kt) load(a.k_pool, j + 1, blk_next, kw);
+            if (lane == 0) mbar_arrive(&k_ready[j & 1]);
+            const int row2 = row_of(j + 1, entry);
+            load(a.k_pool, j + 1, row2, kw);
+            const float ks2 = scale_of(a.k_scale, row2), vs2 = scale_of(a.v_scale, row2);
             if (j == 0) {
                 // exponent of the largest V scale of the item's keys
-                const int n = (it.kv_end + a.block_size - 1) / a.block_size;
+                const int n = (kv_end + a.block_size - 1) / a.block_size;
                 float top = 0.f;
                 for (int i = tid; i < n; i += 128) {
                     const int x = table_row[i];
                     if (x >= 0 && x < a.num_blocks) top = fmaxf(top, a.v_scale[(size_t)x * a.n_kv_heads + it.hk]);
                 }
                 const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
-                if (lane == 0) vexp_w[warp - 4] = (int)(bits >> 23) - 127;
+                if (lane == 0) vexp_w[warp - 8] = (int)(bits >> 23) - 127;
                 asm volatile("bar.sync 1, 128;" ::: "memory");
                 E = max(max(vexp_w[0], vexp_w[1]), max(vexp_w[2], vexp_w[3]));
                 if (tid == 0) vexp_s = E;
             }
-            if (j > 0 && !__all_sync(0xffffffffu, mbar_wait_bounded(&pv_done, (uint32_t)(j - 1) & 1u, &abort_s, status))) break;
-            store(smem + L::OFF_V, vw, true, scalbnf(vs, kPfShift - E));
-            mbar_arrive(&v_ready);
-            if (j + 1 < n_kt) {
-                load(a.v_pool, j + 1, blk_next, vw);
-                ks = scale_of(a.k_scale, blk_next);
-                vs = scale_of(a.v_scale, blk_next);
-                blk = blk_next;
-            }
+            if (j > 1 && !__all_sync(0xffffffffu, mbar_wait_bounded(&v_empty[j & 1], (uint32_t)((j - 2) >> 1) & 1u, &abort_s, status)))
+                break;
+            store(smem + L::OFF_V + (uint32_t)(j & 1) * L::TILE, vw, true, scalbnf(vs, kPfShift - E));
+            if (lane == 0) mbar_arrive(&v_ready[j & 1]);
+            load(a.v_pool, j + 1, row2, vw);
+            row = row2;
+            entry = entry2;
+            ks = ks2;
+            vs = vs2;
         }
         __syncwarp();
     } else {
-        // ---------------------------------------------------- softmax (warps 0-3)
-        const int r = threadIdx.x;                          // query row = TMEM lane
-        const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
+        // ---------------------------------------------------- softmax (warps 0-3: tile A, 4-7: tile B)
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+        const int x = warp >> 2;
+        const int r = threadIdx.x & 127;                    // query row = TMEM lane
+        const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
         const int tok = r / G, head = it.hk * G + r % G;
-        const bool live = tok < it.nt;
-        const size_t row = ((size_t)it.tok0 + tok) * a.n_heads + head;
-        float qf;                                           // score factor but for the K scale
-        {
+        const int n_x = x ? n_b : n_a;
+        const bool live = tok < (x ? it.nt_b : it.nt_a);
+        const size_t qrow = ((size_t)it.tok0 + x * it.tt + tok) * a.n_heads + head;
+        float qf = 0.f;                                     // score factor but for the K scale
+        if (n_x > 0) {
             uint4 w[D / 8];
             uint32_t m = 0;
 #pragma unroll
             for (int c = 0; c < D / 8; ++c) {
                 w[c] = make_uint4(0u, 0u, 0u, 0u);
-                if (live) w[c] = *reinterpret_cast<const uint4*>(a.q + row * D + c * 8);
+                if (live) w[c] = *reinterpret_cast<const uint4*>(a.q + qrow * D + c * 8);
+            }
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c)
                 m = max(m, max(max(max(w[c].x & 0x7fffu, (w[c].x >> 16) & 0x7fffu), max(w[c].y & 0x7fffu, (w[c].y >> 16) & 0x7fffu)),
                                max(max(w[c].z & 0x7fffu, (w[c].z >> 16) & 0x7fffu), max(w[c].w & 0x7fffu, (w[c].w >> 16) & 0x7fffu))));
-            }
             int ex = (int)(m >> 7) - 127;                   // zeros, infinities and NaN: as they are
             if (m == 0u || m >= 0x7f80u) ex = 14;
             const int e0 = (14 - ex) / 2, e1 = 14 - ex - e0;
@@ -327,118 +381,130 @@ __global__ void __launch_bounds__(kPfThreads, 2) attn_prefill_f8_kernel(const At
                 o.y = pack_f16x2(bf16_lo(w[c].y) * u0 * u1, bf16_hi(w[c].y) * u0 * u1);
                 o.z = pack_f16x2(bf16_lo(w[c].z) * u0 * u1, bf16_hi(w[c].z) * u0 * u1);
                 o.w = pack_f16x2(bf16_lo(w[c].w) * u0 * u1, bf16_hi(w[c].w) * u0 * u1);
-                *reinterpret_cast<uint4*>(smem + L::OFF_Q + pf_off(r, c)) = o;
+                *reinterpret_cast<uint4*>(smem + L::OFF_Q + (uint32_t)x * L::TILE + pf_off(r, c)) = o;
             }
             qf = scalbnf(a.scale * kPfLog2e, ex - 14);
             fence_async_smem();
-            mbar_arrive(&q_ready);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&q_ready[x]);
         }
-        const int my_pos = it.pos0 + tok;                   // rows beyond the tokens mask nothing that is kept
-        float m_used = -INFINITY, l = 0.f;
+        const int my_pos = it.pos0 + x * it.tt + tok;       // rows beyond the tokens mask nothing that is kept
+        const uint32_t ts = tmem + lane_base + L::TMEM_S + (uint32_t)x * 128u;
+        const uint32_t to = tmem + lane_base + L::TMEM_O + (uint32_t)x * 128u;
+        float m_used = -INFINITY;
+        float2 l2 = make_float2(0.f, 0.f);
         bool ok = true;
-        for (int j = 0; j < n_kt; ++j) {
-            ok = mbar_wait_bounded(&k_ready[j & 1], (uint32_t)(j >> 1) & 1u, &abort_s, status) &&
-                 mbar_wait_bounded(&s_full, (uint32_t)j & 1u, &abort_s, status);
+        for (int j = 0; j < n_x; ++j) {
+            const int slot = j & (kPfMeta - 1);
+            ok = mbar_wait_bounded(&meta_ready[slot], (uint32_t)(j / kPfMeta) & 1u, &abort_s, status) &&
+                 mbar_wait_bounded(&s_full[x], (uint32_t)j & 1u, &abort_s, status);
             ok = __all_sync(0xffffffffu, ok);               // the TMEM accesses are warp-collective
             if (!ok) break;
             tc_fence_after();
-            const uint32_t ts = tmem + lane_base + L::TMEM_S;
-            const uint32_t chunks = ok_s[j & 1];
+            const uint32_t chunks = ok_s[slot];
             const int last = my_pos - j * kPfKeys;          // last key of the tile that this row sees
-            const bool full = __all_sync(0xffffffffu, last >= kPfKeys - 1 && chunks == (1u << kPfChunks) - 1u);
+            float f[kPfChunks];
+            {
+                const float4 f0 = *reinterpret_cast<const float4*>(&ks_s[slot][0]);
+                const float4 f1 = *reinterpret_cast<const float4*>(&ks_s[slot][4]);
+                f[0] = f0.x * qf; f[1] = f0.y * qf; f[2] = f0.z * qf; f[3] = f0.w * qf;
+                f[4] = f1.x * qf; f[5] = f1.y * qf; f[6] = f1.z * qf; f[7] = f1.w * qf;
+            }
+            float s[128];
+            {
+                float s0[64], s1[64];
+                tmem_ld64(ts, s0);
+                tmem_ld64(ts + 64u, s1);
+#pragma unroll
+                for (int i = 0; i < 64; ++i) {
+                    s[i] = s0[i];
+                    s[64 + i] = s1[i];
+                }
+            }
+            if (!__all_sync(0xffffffffu, last >= kPfKeys - 1 && chunks == (1u << kPfChunks) - 1u)) {
+#pragma unroll
+                for (int c = 0; c < kPfChunks; ++c) {
+                    const int lim = (chunks >> c) & 1u ? last - c * 16 : -1;
+                    f[c] = lim < 0 ? 1.f : f[c];            // (no 0 * -inf)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) s[16 * c + i] = i <= lim ? s[16 * c + i] : -INFINITY;
+                }
+            }
             float mx = -INFINITY;
 #pragma unroll
-            for (int c = 0; c < kPfKeys / 32; ++c) {
-                float s[32];
-                tmem_ld32(ts + (uint32_t)c * 32u, s);
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int ch = 2 * c + h;
-                    float mc = -INFINITY;
-                    if (full) {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) mc = fmaxf(mc, s[16 * h + i]);
-                    } else {
-                        const int lim = (chunks >> ch) & 1u ? last - ch * 16 : -1;
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) mc = i <= lim ? fmaxf(mc, s[16 * h + i]) : mc;
-                    }
-                    // factor >= 0; a row without a key here keeps -inf (0 * -inf would be NaN)
-                    mx = fmaxf(mx, mc == -INFINITY ? mc : mc * (qf * ks_s[j & 1][ch]));
-                }
+            for (int c = 0; c < kPfChunks; ++c) {
+                float m0 = max3(s[16 * c], s[16 * c + 1], s[16 * c + 2]), m1 = max3(s[16 * c + 3], s[16 * c + 4], s[16 * c + 5]);
+                m0 = max3(m0, s[16 * c + 6], s[16 * c + 7]);
+                m1 = max3(m1, s[16 * c + 8], s[16 * c + 9]);
+                m0 = max3(m0, s[16 * c + 10], s[16 * c + 11]);
+                m1 = max3(m1, s[16 * c + 12], s[16 * c + 13]);
+                m0 = max3(m0, s[16 * c + 14], s[16 * c + 15]);
+                // factor >= 0; a row without a key here keeps -inf (0 * -inf would be NaN)
+                const float mc = fmaxf(m0, m1);
+                mx = fmaxf(mx, mc == -INFINITY ? mc : mc * f[c]);
             }
             const bool move = mx > m_used + 8.f;            // false while the row has no key
             if (__any_sync(0xffffffffu, move)) {
-                const float f = move ? ex2_approx(m_used - mx) : 1.f;
+                const float dn = move ? ex2_approx(m_used - mx) : 1.f;
                 if (j > 0) {
                     // S of this tile is complete, so P V of the tile before is in O
-                    const uint32_t to = tmem + lane_base + L::TMEM_O;
 #pragma unroll
                     for (int c = 0; c < D; c += 16) {
                         float v[16];
                         uint32_t w[16];
                         tmem_ld16(to + (uint32_t)c, v);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(v[i] * f);
+                        for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(v[i] * dn);
                         tmem_st16(to + (uint32_t)c, w);
                     }
                 }
                 if (move) {
-                    l *= f;
+                    l2.x *= dn;
+                    l2.y *= dn;
                     m_used = mx;
                 }
             }
             const float base = (m_used == -INFINITY ? 0.f : m_used) - kPfBase;
-            float rs = 0.f;
+            const float2 nb = make_float2(-base, -base);
+            uint32_t p0[32], p1[32];
 #pragma unroll
-            for (int c = 0; c < kPfKeys / 32; ++c) {
-                float s[32];
-                tmem_ld32(ts + (uint32_t)c * 32u, s);
-                uint32_t p[16];
+            for (int c = 0; c < kPfChunks; ++c) {
+                const float2 ff = make_float2(f[c], f[c]);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int ch = 2 * c + h;
-                    const float f = qf * ks_s[j & 1][ch];
-                    const int lim = (chunks >> ch) & 1u ? last - ch * 16 : -1;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        float p0 = ex2_approx(fmaf(s[16 * h + 2 * i], f, -base));
-                        float p1 = ex2_approx(fmaf(s[16 * h + 2 * i + 1], f, -base));
-                        if (!full) {
-                            p0 = 2 * i <= lim ? p0 : 0.f;
-                            p1 = 2 * i + 1 <= lim ? p1 : 0.f;
-                        }
-                        rs += p0 + p1;
-                        p[8 * h + i] = pack_f16x2(p0, p1);
-                    }
+                for (int i = 0; i < 8; ++i) {
+                    float2 e = fma2(make_float2(s[16 * c + 2 * i], s[16 * c + 2 * i + 1]), ff, nb);
+                    e.x = ex2_approx(e.x);
+                    e.y = ex2_approx(e.y);
+                    l2 = add2(l2, e);
+                    const uint32_t h = pack_f16x2(e.x, e.y);
+                    if (c < 4) p0[8 * c + i] = h;
+                    else p1[8 * (c - 4) + i] = h;
                 }
-                tmem_st16(ts + (uint32_t)c * 16u, p);       // over columns of S already read
             }
-            l += rs;
+            tmem_st32x2(ts, p0, ts + 32u, p1);              // over S
             tc_fence_before();
-            mbar_arrive(&p_ready);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_ready[x]);
         }
-        ok = __all_sync(0xffffffffu, ok && mbar_wait_bounded(&o_done, 0, &abort_s, status));
-        if (ok) {
+        ok = __all_sync(0xffffffffu, ok && (n_x == 0 || mbar_wait_bounded(&o_done[x], 0, &abort_s, status)));
+        if (ok && n_x > 0) {
             tc_fence_after();
             // vexp_s was written before v_ready of tile 0, which the P V behind o_done waited for
+            const float l = l2.x + l2.y;
             const float inv = l == 0.f ? 0.f : 1.f / l;
             const int E = *const_cast<volatile int*>(&vexp_s) - kPfShift;
             const float up = E < -126 ? 0.f : __uint_as_float((uint32_t)(E + 127) << 23);
 #pragma unroll
             for (int c = 0; c < D; c += 16) {
                 float v[16];
-                tmem_ld16(tmem + lane_base + L::TMEM_O + (uint32_t)c, v);
+                tmem_ld16(to + (uint32_t)c, v);
                 if (live) {
-                    uint4 o[2];
-                    uint32_t x[8];
+                    uint32_t y[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) x[i] = pack_bf16x2(v[2 * i] * inv * up, v[2 * i + 1] * inv * up);
-                    o[0] = make_uint4(x[0], x[1], x[2], x[3]);
-                    o[1] = make_uint4(x[4], x[5], x[6], x[7]);
-                    uint4* dst = reinterpret_cast<uint4*>(a.out + row * D + c);
-                    dst[0] = o[0];
-                    dst[1] = o[1];
+                    for (int i = 0; i < 8; ++i) y[i] = pack_bf16x2(v[2 * i] * inv * up, v[2 * i + 1] * inv * up);
+                    uint4* dst = reinterpret_cast<uint4*>(a.out + qrow * D + c);
+                    dst[0] = make_uint4(y[0], y[1], y[2], y[3]);
+                    dst[1] = make_uint4(y[4], y[5], y[6], y[7]);
                 }
             }
         }
@@ -446,7 +512,7 @@ __global__ void __launch_bounds__(kPfThreads, 2) attn_prefill_f8_kernel(const At
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 8) tmem_dealloc(tmem, L::TMEM_COLS);
+    if (warp == 12) tmem_dealloc(tmem, L::TMEM_COLS);
 }
 
 template <int D>
@@ -460,8 +526,8 @@ cudaError_t prefill_f8_for(const AttnF8Args& a, cudaStream_t stream) {
         e = ensure_func_attr(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, (int)cudaSharedmemCarveoutMaxShared,
                              "cudaFuncSetAttribute(attn_prefill_f8_kernel carveout)");
     if (e != cudaSuccess) return e;
-    const int tt = kPfRows / (a.n_heads / a.n_kv_heads);    // tokens per item
-    const int n_mt = (a.max_new + tt - 1) / tt;
+    const int tt = kPfRows / (a.n_heads / a.n_kv_heads);    // tokens per query tile
+    const int n_mt = (a.max_new + 2 * tt - 1) / (2 * tt);
     const long long items = (long long)a.batch * n_mt * a.n_kv_heads;
     if (items > (1LL << 30)) {
         set_last_error("attn_prefill_f8", "too many (sequence, KV head, query tile) items");
