@@ -14,8 +14,9 @@
 //  * warps 8-11, keys and values: the codes come straight from global memory into registers, a tile
 //    ahead (L2 mostly, since all items of a KV head read the same codes), become FP16 and are stored as the
 //    128-byte-swizzled operand tiles, two buffers each for K and V.  Block ids are read two tiles ahead.
-//  * warp 12, one thread: S = Q K^T (both from shared memory), O += P V (P from TMEM), alternating
-//    between A and B, so that the tensor core works for one tile while the other's softmax runs.
+//  * warps 12 and 13, one thread each: S = Q K^T (both from shared memory) and O += P V (P from TMEM) of
+//    tile A and B, so that the tensor core works for one tile while the other's softmax runs.  (One thread
+//    for both spent as long between its groups of MMAs as in them.)
 //
 // Precision.  Codes are exact in FP16.  A query row is scaled by a power of two so that its largest element
 // lies in [2^14, 2^15); its factor and the block's K scale multiply the float32 score, 16 keys at a time
@@ -76,6 +77,63 @@ LL_DEVINL uint32_t pf_off(int r, int c) {
 
 LL_DEVINL void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
+// 64 consecutive 32-bit TMEM columns of this thread's lane (warp-collective), without waiting; the values may
+// be used behind tmem_wait_ld, which takes them through its operands so that no use can move before it.
+LL_DEVINL void tmem_ld64_issue(uint32_t taddr, uint32_t (&r)[64]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+          "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
+          "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+          "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+          "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+        : "r"(taddr)
+        : "memory");
+}
+LL_DEVINL void tmem_wait_ld(uint32_t (&r)[64]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+        : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+          "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+          "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+          "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]),
+          "+r"(r[32]), "+r"(r[33]), "+r"(r[34]), "+r"(r[35]), "+r"(r[36]), "+r"(r[37]), "+r"(r[38]), "+r"(r[39]),
+          "+r"(r[40]), "+r"(r[41]), "+r"(r[42]), "+r"(r[43]), "+r"(r[44]), "+r"(r[45]), "+r"(r[46]), "+r"(r[47]),
+          "+r"(r[48]), "+r"(r[49]), "+r"(r[50]), "+r"(r[51]), "+r"(r[52]), "+r"(r[53]), "+r"(r[54]), "+r"(r[55]),
+          "+r"(r[56]), "+r"(r[57]), "+r"(r[58]), "+r"(r[59]), "+r"(r[60]), "+r"(r[61]), "+r"(r[62]), "+r"(r[63])
+        :
+        : "memory");
+}
+// 16 columns, stored without waiting; tmem_wait_st waits for all of the thread's stores.
+LL_DEVINL void tmem_st16_issue(uint32_t taddr, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+LL_DEVINL void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// This thread's lane, 8 columns of TMEM times f (warp-collective).
+LL_DEVINL void tmem_scale8(uint32_t taddr, float f) {
+    asm volatile(
+        "{\n .reg .f32 a<8>;\n .reg .b32 r<8>;\n"
+        " tcgen05.ld.sync.aligned.32x32b.x8.b32 {r0,r1,r2,r3,r4,r5,r6,r7}, [%0];\n"
+        " tcgen05.wait::ld.sync.aligned;\n"
+        " mov.b32 a0, r0; mov.b32 a1, r1; mov.b32 a2, r2; mov.b32 a3, r3;\n"
+        " mov.b32 a4, r4; mov.b32 a5, r5; mov.b32 a6, r6; mov.b32 a7, r7;\n"
+        " mul.f32 a0, a0, %1; mul.f32 a1, a1, %1; mul.f32 a2, a2, %1; mul.f32 a3, a3, %1;\n"
+        " mul.f32 a4, a4, %1; mul.f32 a5, a5, %1; mul.f32 a6, a6, %1; mul.f32 a7, a7, %1;\n"
+        " mov.b32 r0, a0; mov.b32 r1, a1; mov.b32 r2, a2; mov.b32 r3, a3;\n"
+        " mov.b32 r4, a4; mov.b32 r5, a5; mov.b32 r6, a6; mov.b32 r7, a7;\n"
+        " tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {r0,r1,r2,r3,r4,r5,r6,r7};\n"
+        " tcgen05.wait::st.sync.aligned;\n}\n" ::"r"(taddr),
+        "f"(f)
+        : "memory");
+}
+
 // Two float32 operations in one instruction.
 LL_DEVINL float2 fma2(float2 a, float2 b, float2 c) {
     float2 d;
@@ -97,6 +155,39 @@ LL_DEVINL float max3(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
+
+// 16 bytes of global memory that no kernel running now writes, or zeros: predicated, so that a run of such
+// loads issues without branches.
+LL_DEVINL uint4 load16_if(const void* p, bool take) {
+    uint4 v;
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.u32 p, %5, 0;\n mov.b32 %0, 0;\n mov.b32 %1, 0;\n mov.b32 %2, 0;\n mov.b32 %3, 0;\n"
+        " @p ld.global.v4.u32 {%0, %1, %2, %3}, [%4];\n}\n"
+        : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+        : "l"(p), "r"((uint32_t)take)
+        : "memory");
+    return v;
+}
+
+// The two issuing threads take turns on the tensor core (bounded as the barrier waits are); a turn is P V of
+// a key tile with the S of the next.  Interleaved, or in smaller turns, both tiles' S are ready together: both
+// softmaxes run at once and the tensor core waits for them.
+LL_DEVINL bool turn_take(int* turn, volatile int* abort, int32_t* status) {
+    uint64_t t0 = 0;
+    for (uint32_t it = 1; atomicCAS_block(turn, 0, 1) != 0; ++it) {
+        if ((it & 255u) == 0) {
+            if (*abort) return false;
+            if (t0 == 0) t0 = global_timer_ns();
+            if (global_timer_ns() - t0 > kWaitLimitNs) {
+                *abort = 1;
+                flag_status(status, LL_DEV_TIMEOUT);
+                return false;
+            }
+        }
+    }
+    return true;
+}
+LL_DEVINL void turn_leave(int* turn) { atomicExch_block(turn, 0); }
 
 // What a work item covers: new tokens t0 .. of sequence b (rows tok0 + t of q), the first at position pos0;
 // nt_a and nt_b tokens in the tiles, which see keys 0 .. end_a - 1 and 0 .. end_b - 1 (0: no tile B).
@@ -141,9 +232,9 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
     // (ready), read by both query tiles (empty).  Scales of key tile j sit in slot j & 3: slot and barrier
     // are written again for tile j + 4, after the S of tile j + 2, which waits for the P of tile j + 1.
     __shared__ uint64_t q_ready[2], s_full[2], p_ready[2], o_done[2], k_ready[2], k_empty[2], v_ready[2], v_empty[2];
-    __shared__ uint64_t meta_ready[kPfMeta], drain;
+    __shared__ uint64_t meta_ready[kPfMeta], drain[2];
     __shared__ uint32_t tmem_base_s;
-    __shared__ int abort_s;
+    __shared__ int abort_s, turn_s;
     __shared__ __align__(16) float ks_s[kPfMeta][kPfChunks];   // per 16-key chunk: K scale
     __shared__ uint32_t ok_s[kPfMeta];                      // bit c = chunk c is backed by a valid block
     __shared__ int vexp_w[4], vexp_s;                       // exponent of the item's largest V scale
@@ -157,13 +248,14 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
             mbar_init(&p_ready[i], 4);
             mbar_init(&o_done[i], 1);
             mbar_init(&k_ready[i], 4);
-            mbar_init(&k_empty[i], 1);
+            mbar_init(&k_empty[i], 2);
+            mbar_init(&drain[i], 1);
             mbar_init(&v_ready[i], 4);
-            mbar_init(&v_empty[i], 1);
+            mbar_init(&v_empty[i], 2);
         }
         for (int i = 0; i < kPfMeta; ++i) mbar_init(&meta_ready[i], 1);
-        mbar_init(&drain, 1);
         abort_s = 0;
+        turn_s = 0;
         fence_mbar_init();
     }
     pdl_wait();
@@ -183,64 +275,77 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
     const int n_kt = max(n_a, n_b), kv_end = max(it.end_a, it.end_b);
 
     if (warp >= 12) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-        if (warp == 12 && lane == 0) {
-            // ------------------------------------------------ MMA issuer (warps 13-15 are idle)
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+        if (warp < 14 && lane == 0) {
+            // ------------------------------------------------ MMA issuers: warp 12 for tile A, 13 for B
+            const int x = warp - 12;
+            const int n_x = x ? n_b : n_a;
             const uint32_t id_s = idesc_f16(kPfRows, kPfKeys, false);
             const uint32_t id_o = idesc_f16(kPfRows, D, true);
-            const uint32_t sq = smem_u32(smem + L::OFF_Q), sk = smem_u32(smem + L::OFF_K), sv = smem_u32(smem + L::OFF_V);
-            // S_x of key tile j; it overwrites P_x of tile j - 1 (MMAs of one thread run in order)
-            auto issue_s = [&](int x, int j) -> bool {
-                if (!mbar_wait_bounded(&k_ready[j & 1], (uint32_t)(j >> 1) & 1u, &abort_s, status)) return false;
-                if (j == 0 && !mbar_wait_bounded(&q_ready[x], 0, &abort_s, status)) return false;
-                tc_fence_after();
-                uint64_t dq = umma_desc_sw128(sq + (uint32_t)x * L::TILE);
+            const uint32_t sq = smem_u32(smem + L::OFF_Q) + (uint32_t)x * L::TILE;
+            const uint32_t sk = smem_u32(smem + L::OFF_K), sv = smem_u32(smem + L::OFF_V);
+            const uint32_t t_s = tmem + L::TMEM_S + (uint32_t)x * 128u, t_o = tmem + L::TMEM_O + (uint32_t)x * 128u;
+            bool ok = n_x == 0 || mbar_wait_bounded(&q_ready[x], 0, &abort_s, status);
+            auto k_wait = [&](int j) { return mbar_wait_bounded(&k_ready[j & 1], (uint32_t)(j >> 1) & 1u, &abort_s, status); };
+            auto v_wait = [&](int j) { return mbar_wait_bounded(&v_ready[j & 1], (uint32_t)(j >> 1) & 1u, &abort_s, status); };
+            // S of key tile j, over P of tile j - 1 (MMAs of one thread run in order)
+            auto issue_s = [&](int j) {
+                uint64_t dq = umma_desc_sw128(sq);
                 uint64_t dk = umma_desc_sw128(sk + (uint32_t)(j & 1) * L::TILE);
                 asm volatile("" : "+l"(dq), "+l"(dk));      // else every step's descriptors are kept, in local memory
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                     // the descriptor's address field counts 16 bytes
                     const uint32_t off = ((uint32_t)(kk >> 2) * (kPfRows * 128) + (uint32_t)(kk & 3) * 32) >> 4;
-                    tc_mma_bf16(tmem + L::TMEM_S + (uint32_t)x * 128u, dq + off, dk + off, id_s, kk > 0 ? 1u : 0u);
+                    tc_mma_bf16(t_s, dq + off, dk + off, id_s, kk > 0 ? 1u : 0u);
                 }
                 tc_commit(&s_full[x]);
-                return true;
             };
-            auto issue_pv = [&](int x, int j) -> bool {
-                if (!mbar_wait_bounded(&v_ready[j & 1], (uint32_t)(j >> 1) & 1u, &abort_s, status)) return false;
-                if (!mbar_wait_bounded(&p_ready[x], (uint32_t)j & 1u, &abort_s, status)) return false;
-                tc_fence_after();
+            auto issue_pv = [&](int j) {
                 uint64_t dv = pf_desc_mn(sv + (uint32_t)(j & 1) * L::TILE, kPfRows * 128);
                 asm volatile("" : "+l"(dv));
 #pragma unroll
                 for (int kk = 0; kk < kPfKeys / 16; ++kk)
-                    tc_mma_bf16_ts(tmem + L::TMEM_O + (uint32_t)x * 128u, tmem + L::TMEM_S + (uint32_t)x * 128u + (uint32_t)kk * 8u,
-                                   dv + (uint32_t)(kk * 2048 >> 4), id_o, (j > 0 || kk > 0) ? 1u : 0u);
-                return true;
+                    tc_mma_bf16_ts(t_o, t_s + (uint32_t)kk * 8u, dv + (uint32_t)(kk * 2048 >> 4), id_o, (j > 0 || kk > 0) ? 1u : 0u);
             };
-            bool ok = (n_a == 0 || issue_s(0, 0)) && (n_b == 0 || issue_s(1, 0));
-            if (ok) tc_commit(&k_empty[0]);
-            for (int j = 0; j < n_kt && ok; ++j) {
-                if (j < n_a) {
-                    ok = issue_pv(0, j);
-                    if (ok && j + 1 == n_a) tc_commit(&o_done[0]);
-                    if (ok && j + 1 < n_a) ok = issue_s(0, j + 1);
+            if (ok && n_x > 0) {
+                ok = k_wait(0) && turn_take(&turn_s, &abort_s, status);
+                if (ok) {
+                    tc_fence_after();
+                    issue_s(0);
+                    turn_leave(&turn_s);
+                    tc_commit(&k_empty[0]);
                 }
-                if (ok && j < n_b) ok = issue_pv(1, j);
-                if (!ok) break;
-                tc_commit(&v_empty[j & 1]);
-                if (j + 1 == n_b) tc_commit(&o_done[1]);
-                if (j + 1 < n_b) ok = issue_s(1, j + 1);
-                if (ok && j + 1 < n_kt) tc_commit(&k_empty[(j + 1) & 1]);
             }
-            tc_commit(&drain);
+            for (int j = 0; j < n_x && ok; ++j) {
+                // (what is usually there already is waited for first, beside the softmax)
+                const bool more = j + 1 < n_x;
+                ok = v_wait(j) && (!more || k_wait(j + 1)) && mbar_wait_bounded(&p_ready[x], (uint32_t)j & 1u, &abort_s, status) &&
+                     turn_take(&turn_s, &abort_s, status);
+                if (!ok) break;
+                tc_fence_after();
+                issue_pv(j);
+                if (more) issue_s(j + 1);
+                turn_leave(&turn_s);
+                tc_commit(&v_empty[j & 1]);
+                if (more) tc_commit(&k_empty[(j + 1) & 1]);
+                else tc_commit(&o_done[x]);
+            }
+            // past its own last tile a query tile still takes part in the buffers' turns
+            for (int j = n_x; j < n_kt && ok; ++j) {
+                ok = k_wait(j);
+                if (ok) mbar_arrive(&k_empty[j & 1]);
+                ok = ok && v_wait(j);
+                if (ok) mbar_arrive(&v_empty[j & 1]);
+            }
+            tc_commit(&drain[x]);
             volatile int never = 0;
-            mbar_wait_bounded(&drain, 0, &never, status);
+            mbar_wait_bounded(&drain[x], 0, &never, status);
         }
         __syncwarp();
     } else if (warp >= 8) {
         // ---------------------------------------------------- keys and values (warps 8-11)
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
         constexpr int LANES = D / 16, ROWS = 128 / LANES, PER = kPfKeys / ROWS;   // lanes per row, rows per step, steps
         const int tid = threadIdx.x - 256;
         // Eight lanes that store together cover four 16-code pieces of two rows: their 16-byte chunks are 0, 2,
@@ -249,29 +354,30 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
         const int rsub = D == 128 ? ((tid >> 2) & 1) | ((tid >> 3) & ~1) : tid >> 2;
         const int32_t* table_row = a.block_table + (size_t)it.b * a.max_blocks;
         const int my_key = (lane & 7) * 16;                 // lane c < 8 looks after 16-key chunk c of a tile
+        const int bs_log2 = 31 - __clz(a.block_size);       // (a power of two: no divisions on this path)
         auto entry_of = [&](int j) {                        // its table entry (-1 past the keys)
             const int key = j * kPfKeys + my_key;
-            return j < n_kt && key < kv_end ? table_row[key / a.block_size] : -1;
+            return j < n_kt && key < kv_end ? table_row[key >> bs_log2] : -1;
         };
         auto row_of = [&](int j, int entry) {               // its first pool row (-1: no valid block)
             const int key = j * kPfKeys + my_key;
             const bool want = j < n_kt && key < kv_end;
             if (want && (entry < 0 || entry >= a.num_blocks)) flag_status(status, LL_DEV_BAD_BLOCK);
             return want && entry >= 0 && entry < a.num_blocks
-                       ? (entry * a.n_kv_heads + it.hk) * a.block_size + key % a.block_size : -1;
+                       ? ((entry * a.n_kv_heads + it.hk) << bs_log2) + (key & (a.block_size - 1)) : -1;
         };
         auto scale_of = [&](const float* scales, int row) {
-            return row >= 0 ? scales[(row / a.block_size)] : 0.f;
+            return row >= 0 ? scales[row >> bs_log2] : 0.f;
         };
         auto load = [&](const uint8_t* pool, int j, int row_lane, uint4 (&w)[PER]) {
             const int left = kv_end - j * kPfKeys;          // keys of the tile
+            int row[PER];
+#pragma unroll
+            for (int i = 0; i < PER; ++i) row[i] = __shfl_sync(0xffffffffu, row_lane, (i * ROWS + rsub) >> 4);
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
-                const int r = i * ROWS + rsub;
-                const int row = __shfl_sync(0xffffffffu, row_lane, r >> 4);
-                w[i] = make_uint4(0u, 0u, 0u, 0u);         // also rows that hold no key: 0 * stale stays 0
-                if (row >= 0 && r < left)
-                    w[i] = *reinterpret_cast<const uint4*>(pool + (size_t)(uint32_t)(row + (r & 15)) * D + c16 * 16);
+                const int r = i * ROWS + rsub;             // rows that hold no key become zeros: 0 * stale stays 0
+                w[i] = load16_if(pool + (size_t)(uint32_t)(row[i] + (r & 15)) * D + c16 * 16, row[i] >= 0 && r < left);
             }
         };
         const uint32_t st0 = pf_off(rsub, 2 * c16), st1 = pf_off(rsub, 2 * c16 + 1);
@@ -304,9 +410,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
         load(a.k_pool, 0, row, kw);
         load(a.v_pool, 0, row, vw);
         float ks = scale_of(a.k_scale, row), vs = scale_of(a.v_scale, row);
-        int E = 0;
+        float up0 = 0.f, up1 = 0.f;                         // 2^(6 - E) as two factors
         for (int j = 0; j < n_kt; ++j) {
-            const int entry2 = entry_of(j + 2);
             // (whole warps leave: the loads below shuffle)
             if (j > 1 && !__all_sync(0xffffffffu, mbar_wait_bounded(&k_empty[j & 1], (uint32_t)((j - 2) >> 1) & 1u, &abort_s, status)))
                 break;
@@ -319,12 +424,15 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
                 if (lane == 0) mbar_arrive(&meta_ready[j & (kPfMeta - 1)]);
             }
             if (lane == 0) mbar_arrive(&k_ready[j & 1]);
-            const int row2 = row_of(j + 1, entry);
-            load(a.k_pool, j + 1, row2, kw);
-            const float ks2 = scale_of(a.k_scale, row2), vs2 = scale_of(a.v_scale, row2);
+            // Each value is loaded into the variable whose last use is behind it: a copy at the loop's end
+            // would wait for the load.
+            row = row_of(j + 1, entry);
+            entry = entry_of(j + 2);
+            load(a.k_pool, j + 1, row, kw);
+            ks = scale_of(a.k_scale, row);
             if (j == 0) {
                 // exponent of the largest V scale of the item's keys
-                const int n = (kv_end + a.block_size - 1) / a.block_size;
+                const int n = (kv_end + a.block_size - 1) >> bs_log2;
                 float top = 0.f;
                 for (int i = tid; i < n; i += 128) {
                     const int x = table_row[i];
@@ -333,18 +441,18 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
                 const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
                 if (lane == 0) vexp_w[warp - 8] = (int)(bits >> 23) - 127;
                 asm volatile("bar.sync 1, 128;" ::: "memory");
-                E = max(max(vexp_w[0], vexp_w[1]), max(vexp_w[2], vexp_w[3]));
+                const int E = max(max(vexp_w[0], vexp_w[1]), max(vexp_w[2], vexp_w[3]));
                 if (tid == 0) vexp_s = E;
+                const int e0 = (kPfShift - E) / 2, e1 = kPfShift - E - e0;
+                up0 = __uint_as_float((uint32_t)(e0 + 127) << 23);
+                up1 = __uint_as_float((uint32_t)(e1 + 127) << 23);
             }
             if (j > 1 && !__all_sync(0xffffffffu, mbar_wait_bounded(&v_empty[j & 1], (uint32_t)((j - 2) >> 1) & 1u, &abort_s, status)))
                 break;
-            store(smem + L::OFF_V + (uint32_t)(j & 1) * L::TILE, vw, true, scalbnf(vs, kPfShift - E));
+            store(smem + L::OFF_V + (uint32_t)(j & 1) * L::TILE, vw, true, vs * up0 * up1);
             if (lane == 0) mbar_arrive(&v_ready[j & 1]);
-            load(a.v_pool, j + 1, row2, vw);
-            row = row2;
-            entry = entry2;
-            ks = ks2;
-            vs = vs2;
+            load(a.v_pool, j + 1, row, vw);
+            vs = scale_of(a.v_scale, row);
         }
         __syncwarp();
     } else {
@@ -412,13 +520,15 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
             }
             float s[128];
             {
-                float s0[64], s1[64];
-                tmem_ld64(ts, s0);
-                tmem_ld64(ts + 64u, s1);
+                uint32_t s0[64], s1[64];
+                tmem_ld64_issue(ts, s0);
+                tmem_ld64_issue(ts + 64u, s1);
+                tmem_wait_ld(s0);
+                tmem_wait_ld(s1);
 #pragma unroll
                 for (int i = 0; i < 64; ++i) {
-                    s[i] = s0[i];
-                    s[64 + i] = s1[i];
+                    s[i] = __uint_as_float(s0[i]);
+                    s[64 + i] = __uint_as_float(s1[i]);
                 }
             }
             if (!__all_sync(0xffffffffu, last >= kPfKeys - 1 && chunks == (1u << kPfChunks) - 1u)) {
@@ -448,15 +558,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
                 const float dn = move ? ex2_approx(m_used - mx) : 1.f;
                 if (j > 0) {
                     // S of this tile is complete, so P V of the tile before is in O
-#pragma unroll
-                    for (int c = 0; c < D; c += 16) {
-                        float v[16];
-                        uint32_t w[16];
-                        tmem_ld16(to + (uint32_t)c, v);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(v[i] * dn);
-                        tmem_st16(to + (uint32_t)c, w);
-                    }
+                    for (int c = 0; c < D; c += 8) tmem_scale8(to + (uint32_t)c, dn);
                 }
                 if (move) {
                     l2.x *= dn;
@@ -466,22 +568,25 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
             }
             const float base = (m_used == -INFINITY ? 0.f : m_used) - kPfBase;
             const float2 nb = make_float2(-base, -base);
-            uint32_t p0[32], p1[32];
 #pragma unroll
-            for (int c = 0; c < kPfChunks; ++c) {
-                const float2 ff = make_float2(f[c], f[c]);
+            for (int c2 = 0; c2 < kPfChunks; c2 += 2) {     // 32 keys: 16 columns of P, over S
+                uint32_t p[16];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    float2 e = fma2(make_float2(s[16 * c + 2 * i], s[16 * c + 2 * i + 1]), ff, nb);
-                    e.x = ex2_approx(e.x);
-                    e.y = ex2_approx(e.y);
-                    l2 = add2(l2, e);
-                    const uint32_t h = pack_f16x2(e.x, e.y);
-                    if (c < 4) p0[8 * c + i] = h;
-                    else p1[8 * (c - 4) + i] = h;
+                for (int h = 0; h < 2; ++h) {
+                    const int c = c2 + h;
+                    const float2 ff = make_float2(f[c], f[c]);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        float2 e = fma2(make_float2(s[16 * c + 2 * i], s[16 * c + 2 * i + 1]), ff, nb);
+                        e.x = ex2_approx(e.x);
+                        e.y = ex2_approx(e.y);
+                        l2 = add2(l2, e);
+                        p[8 * h + i] = pack_f16x2(e.x, e.y);
+                    }
                 }
+                tmem_st16_issue(ts + (uint32_t)c2 * 8u, p);
             }
-            tmem_st32x2(ts, p0, ts + 32u, p1);              // over S
+            tmem_wait_st();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&p_ready[x]);
