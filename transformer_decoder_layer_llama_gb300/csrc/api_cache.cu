@@ -259,8 +259,7 @@ size_t ll_attention_prefill_f8_workspace_size(int32_t batch, int32_t tokens, int
     if (batch <= 0 || tokens < 0 || max_new <= 0 || n_heads <= 0 || n_kv_heads <= 0 || n_heads % n_kv_heads != 0 ||
         n_heads / n_kv_heads > 16 || (head_dim != 64 && head_dim != 128))
         return 0;
-    return align_up(std::max<size_t>(
-        1, ll::attn_prefill_f8_scratch_bytes(batch, tokens, std::min(max_new, std::max(tokens, 1)), n_heads, n_kv_heads, head_dim)));
+    return align_up(ll::attn_prefill_f8_scratch_bytes(head_dim));
 }
 
 int ll_paged_attention_prefill_f8(const void* q, const int32_t* cu_new, int32_t tokens, const ll_kv_pool_f8* pool,

@@ -239,8 +239,8 @@ struct AttnF8Args {
 constexpr int kF8MaxSms = 160;     // grids and scratch are sized for at most this many SMs
 size_t attn_decode_f8_scratch_bytes(int batch, int n_heads, int n_kv_heads, int head_dim);
 cudaError_t launch_attn_decode_f8(AttnF8Args a, void* workspace, cudaStream_t stream);
-size_t attn_prefill_f8_scratch_bytes(int batch, int tokens, int max_new, int n_heads, int n_kv_heads, int head_dim);
-cudaError_t launch_attn_prefill_f8(const AttnF8Args& a, void* workspace, cudaStream_t stream);
+size_t attn_prefill_f8_scratch_bytes(int head_dim);
+cudaError_t launch_attn_prefill_f8(AttnF8Args a, void* workspace, cudaStream_t stream);
 
 // Copies blocks src -> dst of `pairs` in every tensor [num_blocks][bytes] (blocks.cu).
 constexpr int kCopyMaxTensors = 128;   // per launch
