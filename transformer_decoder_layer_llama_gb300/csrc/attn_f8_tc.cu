@@ -2,23 +2,19 @@
 // tcgen05 tensor cores: a ragged batch of new tokens, each attending causally to its own sequence.
 //
 // A work item is one KV head of one sequence and two tiles (A, B) of 128 query rows each: a tile is
-// floor(128 / G) consecutive tokens times the G query heads that share the KV head, so a tile of 128 keys is
-// brought in and converted once for 256 rows.  The key tiles of all items form one list; each CTA of a
-// persistent grid, one per SM, takes an equal run of it, whatever the lengths: a run that ends inside an item
-// leaves a float32 partial (at most two per CTA), which the join kernel merges by the log-sum-exp.  So a
-// single chunk behind a long prefix fills the GPU, and no SM waits for the longest item.
+// floor(128 / G) consecutive tokens times the G query heads that share the KV head, so a tile of keys is
+// brought in and converted once for 256 rows.  One CTA per SM and item, 128 keys at a time up to the
+// item's last position, items with the most keys first.
 //
-// Roles (512 threads):
-//  * warps 0-3 and 4-7, softmax of tile A and B: one thread per query row.  They stage the item's Q in shared
-//    memory as FP16 (the next item's before the output of the one before).  Per key tile: the row of S from
-//    TMEM into registers, its maximum, probabilities written over S as FP16; where the maximum has grown by
-//    more than 2^8 the running O in TMEM is scaled.  At the end O / l goes out.
+// Roles (416 threads):
+//  * warps 0-3 and 4-7, softmax of tile A and B: one thread per query row.  First they stage Q in shared
+//    memory as FP16.  Per key tile: the row of S from TMEM into registers, its maximum, probabilities
+//    written over S as FP16; where the maximum has grown by more than 2^8 the running O in TMEM is scaled.
+//    At the end O / l goes out.
 //  * warps 8-11, keys and values: the codes come straight from global memory into registers, a tile
 //    ahead (L2 mostly, since all items of a KV head read the same codes), become FP16 and are stored as the
 //    128-byte-swizzled operand tiles, two buffers each for K and V.  Block ids are read two tiles ahead.
-//  * warp 14, one thread: writes the run's segments (a run of key tiles of one item) to a ring that the other
-//    roles read.
-//  * warps 12 and 13, one thread each: S = Q K^T (both from shared memory) and O += P V (P from TMEM) of
+//  * warps 12 and 13, one lane each: S = Q K^T (both from shared memory) and O += P V (P from TMEM) of
 //    tile A and B, so that the tensor core works for one tile while the other's softmax runs.  (One thread
 //    for both spent as long between its groups of MMAs as in them.)
 //
@@ -27,7 +23,7 @@
 // (a block holds whole 16-key chunks), so they cost nothing per element but the multiply-add there already
 // is.  P is one FP16 (relative error 2^-11, an eighth of the BF16 output's half step), relative to an
 // exponent base that keeps it below 2^14.  V carries its block's scale relative to the largest scale of the
-// run's keys, times 2^6: exact for powers of two down to 2^-21 of that scale (values below about 2^-31 of
+// item's keys, times 2^6: exact for powers of two down to 2^-21 of that scale (values below about 2^-31 of
 // the largest are lost).  Row maxima, sums, S and O are float32.
 #include <algorithm>
 
@@ -44,7 +40,6 @@ constexpr int kPfRows = 128;             // query rows per tile
 constexpr int kPfKeys = 128;             // keys per tile
 constexpr int kPfChunks = kPfKeys / 16;
 constexpr int kPfMeta = 4;               // tiles whose scales are kept
-constexpr int kPfSegs = 4;               // segments in the ring
 constexpr float kPfLog2e = 1.4426950408889634f;
 constexpr int kPfShift = 6;              // V enters P V times 2^6
 constexpr float kPfBase = 6.f;           // and P times 2^6
@@ -111,11 +106,13 @@ LL_DEVINL void tmem_wait_ld(uint32_t (&r)[64]) {
         :
         : "memory");
 }
-// 8 columns, stored without waiting; tmem_wait_st waits for all of the thread's stores.
-LL_DEVINL void tmem_st8_issue(uint32_t taddr, const uint32_t (&v)[8]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]), "r"(v[1]),
-                 "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                 : "memory");
+// 16 columns, stored without waiting; tmem_wait_st waits for all of the thread's stores.
+LL_DEVINL void tmem_st16_issue(uint32_t taddr, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
 }
 LL_DEVINL void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -213,290 +210,99 @@ LL_DEVINL bool turn_take(int* turn, volatile int* abort, int32_t* status) {
 }
 LL_DEVINL void turn_leave(int* turn) { atomicExch_block(turn, 0); }
 
-// A whole 32-byte sector per thread.
-LL_DEVINL void store32(void* p, const uint32_t (&v)[8]) {
-    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]),
-                 "r"(v[5]), "r"(v[6]), "r"(v[7])
-                 : "memory");
-}
-
-// sum of floor((a i + b) / m) over i = 0 .. n - 1, by the Euclidean recurrence; a n + b < 2^32
-LL_DEVINL long long floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
-    long long sum = 0;
-    while (n > 0) {
-        sum += (long long)((unsigned long long)n * (n - 1) / 2) * (a / m) + (long long)n * (b / m);
-        a %= m;
-        b %= m;
-        const uint32_t y = a * n + b;
-        if (y < m) break;
-        n = y / m;
-        b = y % m;
-        const uint32_t t = m;
-        m = a;
-        a = t;
-    }
-    return sum;
-}
-
-// One sequence's new tokens: rows c0 .. c0 + n - 1 of q at positions ctx - n .. ctx - 1 (n = 0 where there
-// are none, or where the counts do not fit together: flagged).  With step tokens per item, item mt sees
-// keys below pos0 + min((mt + 1) step, n).
-struct PfSeq {
-    int c0, n, pos0;
-};
-LL_DEVINL PfSeq pf_seq(const AttnF8Args& a, int b, bool flag) {
-    PfSeq s;
-    s.c0 = a.cu_new[b];
-    const int c1 = a.cu_new[b + 1], ctx = a.context_lens[b];
-    const long long n = (long long)c1 - s.c0;
-    const bool bad = s.c0 < 0 || n < 0 || c1 > a.tokens || n > a.max_new || n > ctx || ctx > a.max_blocks * a.block_size;
-    if (bad && n != 0 && flag) flag_status(a.status, LL_DEV_BAD_POSITION);
-    s.n = bad ? 0 : (int)n;
-    s.pos0 = ctx - s.n;
-    return s;
-}
-LL_DEVINL int pf_items(const PfSeq& s, int step) { return (s.n + step - 1) / step; }
-// key tiles of the items before item mt (mt <= items); all items but the last are full
-LL_DEVINL long long pf_tiles_before(const PfSeq& s, int step, int mt) {
-    const int full = min(mt, s.n / step);
-    long long t = floor_sum((uint32_t)full, kPfKeys, (uint32_t)step, (uint32_t)(s.pos0 + step + kPfKeys - 1));
-    if (mt > full) t += (s.pos0 + s.n + kPfKeys - 1) / kPfKeys;
-    return t;
-}
-
-// A place in the list of key tiles: items in the order sequence, KV head, query tiles.
-struct PfPlace {
-    int b, hk, mt, j;
+// What a work item covers: new tokens t0 .. of sequence b (rows tok0 + t of q), the first at position pos0;
+// nt_a and nt_b tokens in the tiles, which see keys 0 .. end_a - 1 and 0 .. end_b - 1 (0: no tile B).
+struct PfItem {
+    int b, hk, tok0, pos0, tt;
+    int nt_a, nt_b, end_a, end_b;
 };
 
-struct PfRun {
-    PfPlace at, to;          // where the run begins and ends (valid where that is before the list's end)
-    long long begin, end, total;
-};
-
-// Key tiles of an item's edge that a run does not split off: a few tiles more or less cost less than a partial.
-constexpr int kPfSnap = 2;
-
-// The run of CTA c of P, found by a whole block of nt threads (a multiple of 32, at most 512): the runs are
-// equal but for the snap to item edges.
-LL_DEVINL void pf_find_run(const AttnF8Args& a, int step, int P, int c, int nt, bool flag, PfRun* out) {
-    __shared__ long long sums[16];
-    __shared__ PfPlace place[2];
-    __shared__ long long place_t[2];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int per = (a.batch + nt - 1) / nt;
-    const int b0 = min(tid * per, a.batch), b1 = min(b0 + per, a.batch);
-    long long mine = 0;
-    for (int b = b0; b < b1; ++b) {
-        const PfSeq s = pf_seq(a, b, flag);
-        mine += pf_tiles_before(s, step, pf_items(s, step));
-    }
-    long long x = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-    }
-    if (lane == 31) sums[warp] = x;
-    if (tid < 2) place_t[tid] = -1;
-    __syncthreads();
-    long long before = x - mine, total = 0;
-    for (int w = 0; w < nt / 32; ++w) {
-        if (w < warp) before += sums[w];
-        total += sums[w];
-    }
-    before *= a.n_kv_heads;
-    total *= a.n_kv_heads;
-    const long long q = total / P, r = total - q * P;
-    for (int e = 0; e < 2; ++e) {
-        const long long t = q * (c + e) + min((long long)(c + e), r);   // the boundary, before the snap
-        if (t >= total) {
-            if (tid == 0) place_t[e] = total;
-        } else if (t >= before && t < before + mine * a.n_kv_heads) {
-            long long at = before;
-            for (int b = b0; b < b1; ++b) {
-                const PfSeq s = pf_seq(a, b, false);
-                const int items = pf_items(s, step);
-                const long long per_head = pf_tiles_before(s, step, items);
-                if (t >= at + per_head * a.n_kv_heads) {
-                    at += per_head * a.n_kv_heads;
-                    continue;
-                }
-                PfPlace p;
-                p.b = b;
-                p.hk = (int)((t - at) / per_head);
-                const long long rest = t - at - (long long)p.hk * per_head;
-                int lo = 0, hi = items;                    // the item: last one that begins at or before rest
-                while (hi - lo > 1) {
-                    const int mid = (lo + hi) >> 1;
-                    if (pf_tiles_before(s, step, mid) <= rest) lo = mid;
-                    else hi = mid;
-                }
-                p.mt = lo;
-                p.j = (int)(rest - pf_tiles_before(s, step, lo));
-                const int n_kt = (s.pos0 + min((lo + 1) * step, s.n) + kPfKeys - 1) / kPfKeys;
-                long long snapped = t;
-                if (p.j <= kPfSnap) {
-                    snapped -= p.j;
-                    p.j = 0;
-                } else if (n_kt - p.j <= kPfSnap) {
-                    snapped += n_kt - p.j;
-                    p.j = n_kt;                            // (the walk goes on to the next item)
-                }
-                place[e] = p;
-                place_t[e] = snapped;
-                break;
-            }
-        }
-    }
-    __syncthreads();
-    if (tid == 0) {
-        out->at = place[0];
-        out->to = place[1];
-        out->begin = place_t[0];
-        out->end = place_t[1];
-        out->total = total;
-    }
-    __syncthreads();
-}
-
-// A run of key tiles j0 .. j1 - 1 (of n_kt) of one item: nt_a and nt_b tokens in the query tiles (rows tok0 + t
-// of q, the first at position pos0), which see keys 0 .. end_a - 1 and 0 .. end_b - 1 (0: no tile B).
-struct PfSegment {
-    int b;                   // -1: the run is over
-    int hk, tok0, pos0, nt_a, nt_b, end_a, end_b, j0, j1, n_kt;
-};
-
-struct PfWalk {
-    PfPlace at;
-    long long left;          // key tiles of the run still to do
-    LL_DEVINL bool next(const AttnF8Args& a, int tt, PfSegment& g) {
-        while (left > 0) {
-            const PfSeq s = pf_seq(a, at.b, false);
-            const int t0 = at.mt * 2 * tt;
-            if (t0 >= s.n) {                  // past the sequence's items: the next head, or sequence
-                at.mt = 0;
-                at.j = 0;
-                if (s.n == 0 || ++at.hk == a.n_kv_heads) {
-                    at.hk = 0;
-                    ++at.b;
-                }
-                continue;
-            }
-            const int rest = s.n - t0;
-            g.b = at.b;
-            g.hk = at.hk;
-            g.tok0 = s.c0 + t0;
-            g.pos0 = s.pos0 + t0;
-            g.nt_a = min(tt, rest);
-            g.nt_b = min(tt, rest - g.nt_a);
-            g.end_a = g.pos0 + g.nt_a;
-            g.end_b = g.nt_b ? g.end_a + g.nt_b : 0;
-            g.n_kt = (max(g.end_a, g.end_b) + kPfKeys - 1) / kPfKeys;
-            if (at.j >= g.n_kt) {
-                at.j = 0;
-                ++at.mt;
-                continue;
-            }
-            g.j0 = at.j;
-            g.j1 = (int)min((long long)g.n_kt, g.j0 + left);
-            left -= g.j1 - g.j0;
-            at.j = g.j1;
-            return true;
-        }
+LL_DEVINL bool pf_item(const AttnF8Args& a, int n_mt, int tt, bool flag, PfItem& it) {
+    // latest tiles (the most keys) first, KV heads fastest
+    int i = blockIdx.x;
+    it.hk = i % a.n_kv_heads;
+    i /= a.n_kv_heads;
+    it.b = i % a.batch;
+    const int mt = n_mt - 1 - i / a.batch;
+    const int c0 = a.cu_new[it.b], c1 = a.cu_new[it.b + 1], ctx = a.context_lens[it.b];
+    const long long n = (long long)c1 - c0;
+    if (n == 0) return false;
+    if (c0 < 0 || n < 0 || c1 > a.tokens || n > a.max_new || n > ctx || ctx > a.max_blocks * a.block_size) {
+        if (flag) flag_status(a.status, LL_DEV_BAD_POSITION);
         return false;
     }
-};
-// one past the last key tile of the segment that query tile x works on
-LL_DEVINL int pf_end(const PfSegment& g, int x) {
-    return min(g.j1, ((x ? g.end_b : g.end_a) + kPfKeys - 1) / kPfKeys);
+    const int t0 = mt * 2 * tt;
+    if (t0 >= n) return false;
+    const int left = (int)n - t0;
+    it.tt = tt;
+    it.tok0 = c0 + t0;
+    it.pos0 = ctx - left;
+    it.nt_a = min(tt, left);
+    it.nt_b = min(tt, left - it.nt_a);
+    it.end_a = it.pos0 + it.nt_a;
+    it.end_b = it.nt_b ? it.end_a + it.nt_b : 0;
+    return true;
 }
 
 template <int D>
-__global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const AttnF8Args a, int tt) {
+__global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const AttnF8Args a, int n_mt, int tt) {
     using L = PfLayout<D>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    // Per query tile x, counted over the key tiles it works on: S computed, P stored; over its segments: Q
-    // staged, O complete, O read.  Per key buffer, counted over all key tiles: K or V stored (ready), read by
-    // both query tiles (empty).  The scales of key tile i of the run sit in slot i & 3: slot and barrier are
-    // written again for tile i + 4, after the S of tile i + 2, which waits for the P of tile i + 1.
-    __shared__ uint64_t q_ready[2], s_full[2], p_ready[2], o_done[2], o_free[2], k_ready[2], k_empty[2], v_ready[2], v_empty[2];
+    // Per query tile x and key tile j (parity j & 1): S computed, P stored.  Per key buffer: K or V stored
+    // (ready), read by both query tiles (empty).  Scales of key tile j sit in slot j & 3: slot and barrier
+    // are written again for tile j + 4, after the S of tile j + 2, which waits for the P of tile j + 1.
+    __shared__ uint64_t q_ready[2], s_full[2], p_ready[2], o_done[2], k_ready[2], k_empty[2], v_ready[2], v_empty[2];
     __shared__ uint64_t meta_ready[kPfMeta], drain[2];
     __shared__ uint32_t tmem_base_s;
     __shared__ int abort_s, turn_s;
     __shared__ __align__(16) float ks_s[kPfMeta][kPfChunks];   // per 16-key chunk: K scale
     __shared__ uint32_t ok_s[kPfMeta];                      // bit c = chunk c is backed by a valid block
-    __shared__ int vexp_s[kPfMeta], vexp_w[2][4];           // exponent of the segment's largest V scale
-    __shared__ PfRun run_s;
-    __shared__ uint64_t seg_ready[kPfSegs], seg_empty[kPfSegs];
-    __shared__ PfSegment seg_s[kPfSegs];
-    __shared__ struct {
-        long long row0;      // q and out row of the tile's first query row
-        int nt, part;        // tokens; partial slot (-1: the whole item)
-        int exp, next;       // exponent of V; the run's key tile that the query tile goes on with
-    } out_s[8];              // per softmax warp
+    __shared__ int vexp_w[4], vexp_s;                       // exponent of the item's largest V scale
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int32_t* status = a.status;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kPfSegs; ++i) {
-            mbar_init(&seg_ready[i], 1);
-            mbar_init(&seg_empty[i], 14);                   // 8 softmax warps, 4 for keys and values, 2 issuers
-        }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&q_ready[i], 4);
             mbar_init(&s_full[i], 1);
             mbar_init(&p_ready[i], 4);
             mbar_init(&o_done[i], 1);
-            mbar_init(&o_free[i], 4);
             mbar_init(&k_ready[i], 4);
             mbar_init(&k_empty[i], 2);
+            mbar_init(&drain[i], 1);
             mbar_init(&v_ready[i], 4);
             mbar_init(&v_empty[i], 2);
-            mbar_init(&drain[i], 1);
         }
         for (int i = 0; i < kPfMeta; ++i) mbar_init(&meta_ready[i], 1);
         abort_s = 0;
         turn_s = 0;
         fence_mbar_init();
     }
+    pdl_wait();
+    pdl_trigger();
+    PfItem it;
+    if (!pf_item(a, n_mt, tt, threadIdx.x == 0, it)) return;
     if (warp == 12) {
         tmem_alloc(&tmem_base_s, L::TMEM_COLS);
         tmem_relinquish();
     }
-    pdl_wait();
-    pdl_trigger();
-    pf_find_run(a, 2 * tt, (int)gridDim.x, (int)blockIdx.x, kPfThreads, blockIdx.x == 0, &run_s);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_base_s;
     const int G = a.n_heads / a.n_kv_heads;
-    // segment k of the run; false after a timeout
-    auto seg_wait = [&](int k) {
-        return mbar_wait_bounded(&seg_ready[k & (kPfSegs - 1)], (uint32_t)(k / kPfSegs) & 1u, &abort_s, status);
-    };
+    const int n_a = (it.end_a + kPfKeys - 1) / kPfKeys, n_b = (it.end_b + kPfKeys - 1) / kPfKeys;
+    const int n_kt = max(n_a, n_b), kv_end = max(it.end_a, it.end_b);
 
     if (warp >= 12) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
-        if (warp == 14 && lane == 0) {
-            // ------------------------------------------------ segments of the run
-            PfWalk walk{run_s.at, run_s.end - run_s.begin};
-            for (int k = 0;; ++k) {
-                PfSegment& g = seg_s[k & (kPfSegs - 1)];
-                if (k >= kPfSegs && !mbar_wait_bounded(&seg_empty[k & (kPfSegs - 1)], (uint32_t)(k / kPfSegs - 1) & 1u, &abort_s, status))
-                    break;
-                const bool some = walk.next(a, tt, g);
-                if (!some) g.b = -1;
-                mbar_arrive(&seg_ready[k & (kPfSegs - 1)]);
-                if (!some) break;
-            }
-        } else if (warp < 14) {
+        if (warp < 14) {
             // ------------------------------------------------ MMA issuers: warp 12 for tile A, 13 for B
             // The whole warp walks along, one lane issues: addresses stay in uniform registers.  (One thread on a
             // path of its own took twice an MMA's time to issue the next.)
             const int x = warp - 12;
+            const int n_x = x ? n_b : n_a;
             constexpr uint32_t id_s = idesc_f16(kPfRows, kPfKeys, false), id_o = idesc_f16(kPfRows, D, true);
             const uint64_t dq = umma_desc_sw128(smem_u32(smem + L::OFF_Q) + (uint32_t)x * L::TILE);
             const uint64_t dk = umma_desc_sw128(smem_u32(smem + L::OFF_K));
@@ -504,7 +310,6 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
             const uint32_t q_lo = (uint32_t)dq, q_hi = (uint32_t)(dq >> 32), k_lo = (uint32_t)dk, k_hi = (uint32_t)(dk >> 32);
             const uint32_t v_lo = (uint32_t)dv, v_hi = (uint32_t)(dv >> 32);
             const uint32_t t_s = tmem + L::TMEM_S + (uint32_t)x * 128u, t_o = tmem + L::TMEM_O + (uint32_t)x * 128u;
-            // key tile i of the run
             auto k_wait = [&](int i) { return mbar_wait_bounded(&k_ready[i & 1], (uint32_t)(i >> 1) & 1u, &abort_s, status); };
             auto v_wait = [&](int i) { return mbar_wait_bounded(&v_ready[i & 1], (uint32_t)(i >> 1) & 1u, &abort_s, status); };
             auto take = [&](bool good) {                    // (all lanes' waits went well, and the turn is the warp's)
@@ -531,55 +336,38 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
                 for (int kk = 0; kk < kPfKeys / 16; ++kk)
                     pf_mma_ts(t_o, t_s + (uint32_t)kk * 8u, b + (uint32_t)(kk * 2048 >> 4), v_hi, id_o, !first || kk > 0 ? 1u : 0u);
             };
-            int i = 0;                                      // key tiles of the run so far
-            uint32_t p_par = 0;                             // parity of this query tile's key tiles
-            int segs = 0;                                   // and its segments
             bool ok = true;
-            for (int k = 0;; ++k) {
-                ok = __all_sync(0xffffffffu, seg_wait(k));
-                const PfSegment& seg = seg_s[k & (kPfSegs - 1)];
-                if (!ok || seg.b < 0) break;
-                const int n = max(pf_end(seg, x) - seg.j0, 0), pass = seg.j1 - seg.j0 - n;
+            if (n_x > 0) {
+                ok = take(mbar_wait_bounded(&q_ready[x], 0, &abort_s, status) && k_wait(0));
+                if (ok && elect_one()) {
+                    issue_s(0);
+                    turn_leave(&turn_s);
+                    tc_commit(&k_empty[0]);
+                }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&seg_empty[k & (kPfSegs - 1)]);   // (its numbers are taken)
-                if (n > 0) {
-                    ok = take(mbar_wait_bounded(&q_ready[x], (uint32_t)segs & 1u, &abort_s, status) && k_wait(i));
-                    if (!ok) break;
-                    if (elect_one()) {
-                        issue_s(i);
-                        turn_leave(&turn_s);
-                        tc_commit(&k_empty[i & 1]);
-                    }
-                    __syncwarp();
-                }
-                // the segment before this one has been read out of O: before O is overwritten, and before buffers
-                // pass on unseen by this tile
-                ok = segs == 0 || __all_sync(0xffffffffu, mbar_wait_bounded(&o_free[x], (uint32_t)(segs - 1) & 1u, &abort_s, status));
-                for (int j = 0; j < n && ok; ++j, ++i, p_par ^= 1u) {
-                    // (what is usually there already is waited for first, beside the softmax)
-                    const bool more = j + 1 < n;
-                    ok = take(v_wait(i) && (!more || k_wait(i + 1)) && mbar_wait_bounded(&p_ready[x], p_par, &abort_s, status));
-                    if (!ok) break;
-                    if (elect_one()) {
-                        issue_pv(i, j == 0);
-                        if (more) issue_s(i + 1);
-                        turn_leave(&turn_s);
-                        tc_commit(&v_empty[i & 1]);
-                        if (more) tc_commit(&k_empty[(i + 1) & 1]);
-                        else tc_commit(&o_done[x]);
-                    }
-                    __syncwarp();
-                }
-                // key tiles that only the other query tile works on
-                for (int j = 0; j < pass && ok; ++j, ++i) {
-                    ok = __all_sync(0xffffffffu, k_wait(i) && v_wait(i));
-                    if (ok && lane == 0) {
-                        mbar_arrive(&k_empty[i & 1]);
-                        mbar_arrive(&v_empty[i & 1]);
-                    }
-                }
+            }
+            for (int j = 0; j < n_x && ok; ++j) {
+                // (what is usually there already is waited for first, beside the softmax)
+                const bool more = j + 1 < n_x;
+                ok = take(v_wait(j) && (!more || k_wait(j + 1)) && mbar_wait_bounded(&p_ready[x], (uint32_t)j & 1u, &abort_s, status));
                 if (!ok) break;
-                if (n > 0) ++segs;
+                if (elect_one()) {
+                    issue_pv(j, j == 0);
+                    if (more) issue_s(j + 1);
+                    turn_leave(&turn_s);
+                    tc_commit(&v_empty[j & 1]);
+                    if (more) tc_commit(&k_empty[(j + 1) & 1]);
+                    else tc_commit(&o_done[x]);
+                }
+                __syncwarp();
+            }
+            // past its own last tile a query tile still takes part in the buffers' turns
+            for (int j = n_x; j < n_kt && ok; ++j) {
+                ok = __all_sync(0xffffffffu, k_wait(j) && v_wait(j));
+                if (ok && lane == 0) {
+                    mbar_arrive(&k_empty[j & 1]);
+                    mbar_arrive(&v_empty[j & 1]);
+                }
             }
             if (elect_one()) {
                 tc_commit(&drain[x]);
@@ -597,20 +385,19 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
         // 4, 6 of an even and an odd row, which the swizzle puts on different banks.
         const int c16 = D == 128 ? (tid & 3) | ((tid >> 1) & 4) : tid & 3;
         const int rsub = D == 128 ? ((tid >> 2) & 1) | ((tid >> 3) & ~1) : tid >> 2;
+        const int32_t* table_row = a.block_table + (size_t)it.b * a.max_blocks;
         const int my_key = (lane & 7) * 16;                 // lane c < 8 looks after 16-key chunk c of a tile
         const int bs_log2 = 31 - __clz(a.block_size);       // (a power of two: no divisions on this path)
-        const int32_t* table_row = nullptr;
-        int kv_end = 0, hk = 0, j1 = 0;                     // of the segment
         auto entry_of = [&](int j) {                        // its table entry (-1 past the keys)
             const int key = j * kPfKeys + my_key;
-            return j < j1 && key < kv_end ? table_row[key >> bs_log2] : -1;
+            return j < n_kt && key < kv_end ? table_row[key >> bs_log2] : -1;
         };
         auto row_of = [&](int j, int entry) {               // its first pool row (-1: no valid block)
             const int key = j * kPfKeys + my_key;
-            const bool want = j < j1 && key < kv_end;
+            const bool want = j < n_kt && key < kv_end;
             if (want && (entry < 0 || entry >= a.num_blocks)) flag_status(status, LL_DEV_BAD_BLOCK);
             return want && entry >= 0 && entry < a.num_blocks
-                       ? ((entry * a.n_kv_heads + hk) << bs_log2) + (key & (a.block_size - 1)) : -1;
+                       ? ((entry * a.n_kv_heads + it.hk) << bs_log2) + (key & (a.block_size - 1)) : -1;
         };
         auto scale_of = [&](const float* scales, int row) {
             return row >= 0 ? scales[row >> bs_log2] : 0.f;
@@ -649,68 +436,56 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
             fence_async_smem();
             __syncwarp();
         };
-        int i = 0;                                          // key tiles of the run so far
-        bool ok = true;
-        for (int k = 0; ok; ++k) {
-            ok = __all_sync(0xffffffffu, seg_wait(k));
-            const PfSegment& seg = seg_s[k & (kPfSegs - 1)];
-            if (!ok || seg.b < 0) break;
-            table_row = a.block_table + (size_t)seg.b * a.max_blocks;
-            kv_end = max(seg.end_a, seg.end_b);
-            hk = seg.hk;
-            const int j0 = seg.j0;
-            j1 = seg.j1;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&seg_empty[k & (kPfSegs - 1)]);
-            uint4 kw[PER], vw[PER];
-            int row = row_of(j0, entry_of(j0));
-            int entry = entry_of(j0 + 1);               // of the tile after the one in registers
-            load(a.k_pool, j0, row, kw);
-            load(a.v_pool, j0, row, vw);
-            float ks = scale_of(a.k_scale, row), vs = scale_of(a.v_scale, row);
-            // exponent of the largest V scale of the segment's keys
-            float top = 0.f;
-            const int e1 = (min(j1 * kPfKeys, kv_end) + a.block_size - 1) >> bs_log2;
-            for (int e = (j0 * kPfKeys >> bs_log2) + tid; e < e1; e += 128) {
-                const int x = table_row[e];
-                if (x >= 0 && x < a.num_blocks) top = fmaxf(top, a.v_scale[(size_t)x * a.n_kv_heads + hk]);
+        uint4 kw[PER], vw[PER];
+        const int entry0 = entry_of(0);
+        int entry = entry_of(1);                            // of the tile after the one in registers
+        int row = row_of(0, entry0);
+        load(a.k_pool, 0, row, kw);
+        load(a.v_pool, 0, row, vw);
+        float ks = scale_of(a.k_scale, row), vs = scale_of(a.v_scale, row);
+        float up0 = 0.f, up1 = 0.f;                         // 2^(6 - E) as two factors
+        for (int j = 0; j < n_kt; ++j) {
+            // (whole warps leave: the loads below shuffle)
+            if (j > 1 && !__all_sync(0xffffffffu, mbar_wait_bounded(&k_empty[j & 1], (uint32_t)((j - 2) >> 1) & 1u, &abort_s, status)))
+                break;
+            store(smem + L::OFF_K + (uint32_t)(j & 1) * L::TILE, kw, false, 0.f);
+            if (warp == 8) {
+                const uint32_t m = __ballot_sync(0xffffffffu, row >= 0);
+                if (lane < kPfChunks) ks_s[j & (kPfMeta - 1)][lane] = ks;
+                if (lane == 0) ok_s[j & (kPfMeta - 1)] = m & ((1u << kPfChunks) - 1u);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&meta_ready[j & (kPfMeta - 1)]);
             }
-            const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
-            if (lane == 0) vexp_w[k & 1][warp - 8] = (int)(bits >> 23) - 127;
-            asm volatile("bar.sync 1, 128;" ::: "memory");
-            const int E = max(max(vexp_w[k & 1][0], vexp_w[k & 1][1]), max(vexp_w[k & 1][2], vexp_w[k & 1][3]));
-            const int h0 = (kPfShift - E) / 2, h1 = kPfShift - E - h0;
-            const float up0 = __uint_as_float((uint32_t)(h0 + 127) << 23), up1 = __uint_as_float((uint32_t)(h1 + 127) << 23);
-            for (int j = j0; j < j1; ++j, ++i) {
-                // (whole warps leave: the loads below shuffle)
-                ok = i < 2 || __all_sync(0xffffffffu, mbar_wait_bounded(&k_empty[i & 1], (uint32_t)((i - 2) >> 1) & 1u, &abort_s, status));
-                if (!ok) break;
-                store(smem + L::OFF_K + (uint32_t)(i & 1) * L::TILE, kw, false, 0.f);
-                if (warp == 8) {
-                    const int slot = i & (kPfMeta - 1);
-                    const uint32_t m = __ballot_sync(0xffffffffu, row >= 0);
-                    if (lane < kPfChunks) ks_s[slot][lane] = ks;
-                    if (lane == 0) {
-                        ok_s[slot] = m & ((1u << kPfChunks) - 1u);
-                        vexp_s[slot] = E;
-                    }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&meta_ready[slot]);
+            if (lane == 0) mbar_arrive(&k_ready[j & 1]);
+            // Each value is loaded into the variable whose last use is behind it: a copy at the loop's end
+            // would wait for the load.
+            row = row_of(j + 1, entry);
+            entry = entry_of(j + 2);
+            load(a.k_pool, j + 1, row, kw);
+            ks = scale_of(a.k_scale, row);
+            if (j == 0) {
+                // exponent of the largest V scale of the item's keys
+                const int n = (kv_end + a.block_size - 1) >> bs_log2;
+                float top = 0.f;
+                for (int i = tid; i < n; i += 128) {
+                    const int x = table_row[i];
+                    if (x >= 0 && x < a.num_blocks) top = fmaxf(top, a.v_scale[(size_t)x * a.n_kv_heads + it.hk]);
                 }
-                if (lane == 0) mbar_arrive(&k_ready[i & 1]);
-                // Each value is loaded into the variable whose last use is behind it: a copy at the loop's end
-                // would wait for the load.
-                row = row_of(j + 1, entry);
-                entry = entry_of(j + 2);
-                load(a.k_pool, j + 1, row, kw);
-                ks = scale_of(a.k_scale, row);
-                ok = i < 2 || __all_sync(0xffffffffu, mbar_wait_bounded(&v_empty[i & 1], (uint32_t)((i - 2) >> 1) & 1u, &abort_s, status));
-                if (!ok) break;
-                store(smem + L::OFF_V + (uint32_t)(i & 1) * L::TILE, vw, true, vs * up0 * up1);
-                if (lane == 0) mbar_arrive(&v_ready[i & 1]);
-                load(a.v_pool, j + 1, row, vw);
-                vs = scale_of(a.v_scale, row);
+                const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
+                if (lane == 0) vexp_w[warp - 8] = (int)(bits >> 23) - 127;
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+                const int E = max(max(vexp_w[0], vexp_w[1]), max(vexp_w[2], vexp_w[3]));
+                if (tid == 0) vexp_s = E;
+                const int e0 = (kPfShift - E) / 2, e1 = kPfShift - E - e0;
+                up0 = __uint_as_float((uint32_t)(e0 + 127) << 23);
+                up1 = __uint_as_float((uint32_t)(e1 + 127) << 23);
             }
+            if (j > 1 && !__all_sync(0xffffffffu, mbar_wait_bounded(&v_empty[j & 1], (uint32_t)((j - 2) >> 1) & 1u, &abort_s, status)))
+                break;
+            store(smem + L::OFF_V + (uint32_t)(j & 1) * L::TILE, vw, true, vs * up0 * up1);
+            if (lane == 0) mbar_arrive(&v_ready[j & 1]);
+            load(a.v_pool, j + 1, row, vw);
+            vs = scale_of(a.v_scale, row);
         }
         __syncwarp();
     } else {
@@ -719,28 +494,26 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
         const int x = warp >> 2;
         const int r = threadIdx.x & 127;                    // query row = TMEM lane
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t per_g = 65536u / (uint32_t)G + 1u;   // r / G = r * per_g >> 16 for r < 128
-        const uint32_t ts = tmem + lane_base + L::TMEM_S + (uint32_t)x * 128u;
-        const uint32_t to = tmem + lane_base + L::TMEM_O + (uint32_t)x * 128u;
-        uint8_t* const sq = smem + L::OFF_Q + (uint32_t)x * L::TILE;
-        // The warp's 32 rows of an item's Q on their way to their places in shared memory, as they are: D / 8 lanes
-        // take a row, 16 bytes each.  (Rolled loops here, in scale_q and at the output: code that runs once per
-        // item displaces the loop that matters.)
-        auto fetch_q = [&](const PfSegment& g) {
-            constexpr int QL = D / 8, QR = 32 / QL;         // lanes per row, rows per step
-            const int c = lane % QL, nt = x ? g.nt_b : g.nt_a;
-            const size_t row0 = ((size_t)g.tok0 + x * tt) * a.n_heads + g.hk * G;
+        const int tok = r / G, head = it.hk * G + r % G;
+        const int n_x = x ? n_b : n_a;
+        const bool live = tok < (x ? it.nt_b : it.nt_a);
+        const size_t qrow = ((size_t)it.tok0 + x * it.tt + tok) * a.n_heads + head;
+        float qf = 0.f;                                     // score factor but for the K scale
+        if (n_x > 0) {
+            // The warp's 32 rows to their places in shared memory, D / 8 lanes to a row, 16 bytes each; then each thread
+            // turns its own row into FP16 there.  (Rolled loops here and at the output: code that runs once per item
+            // displaces the loop that matters.)
+            constexpr int QL = D / 8, QR = 32 / QL;
+            uint8_t* const sq = smem + L::OFF_Q + (uint32_t)x * L::TILE;
+            const uint32_t per_g = 65536u / (uint32_t)G + 1u;   // row / G = row * per_g >> 16 for row < 128
+            const int c0 = lane % QL, nt = x ? it.nt_b : it.nt_a;
+            const size_t row0 = ((size_t)it.tok0 + x * it.tt) * a.n_heads + it.hk * G;
 #pragma unroll 4
             for (int rr = (warp & 3) * 32 + lane / QL; rr < (warp & 3) * 32 + 32; rr += QR) {
-                const int tok = (int)((uint32_t)rr * per_g >> 16);
-                const bool take = tok < nt;
-                cp_async16(sq + pf_off(rr, c), a.q + (take ? (row0 + (size_t)tok * a.n_heads + (rr - tok * G)) * D + c * 8 : 0), take);
+                const int t = (int)((uint32_t)rr * per_g >> 16);
+                cp_async16(sq + pf_off(rr, c0), a.q + (t < nt ? (row0 + (size_t)t * a.n_heads + (rr - t * G)) * D + c0 * 8 : 0), t < nt);
             }
             cp_async_commit();
-        };
-        // Then each thread turns its own row into FP16, scaled so that its largest element lies in [2^14, 2^15).
-        // Returns the row's score factor, but for the K scale.
-        auto scale_q = [&]() {
             cp_async_wait<0>();
             __syncwarp();
             uint32_t m = 0;
@@ -765,256 +538,133 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
                 o.w = pack_f16x2(bf16_lo(w.w) * u0 * u1, bf16_hi(w.w) * u0 * u1);
                 *at = o;
             }
+            qf = scalbnf(a.scale * kPfLog2e, ex - 14);
             fence_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&q_ready[x]);
-            return scalbnf(a.scale * kPfLog2e, ex - 14);
-        };
-        int i = 0, k = 0;                                   // key tile of the run, segment in hand
-        uint32_t s_par = 0, o_par = 0;                      // parity of this query tile's key tiles and segments
-        bool more = false, ok = true;
-        auto done_with = [&](int kk) {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&seg_empty[kk & (kPfSegs - 1)]);
-        };
-        // on to segment k, and past those that this query tile has no keys in; i: its first key tile
-        auto find = [&]() {
-            for (;; ++k) {
-                ok = ok && __all_sync(0xffffffffu, seg_wait(k));
-                const PfSegment& g = seg_s[k & (kPfSegs - 1)];
-                more = ok && g.b >= 0;
-                if (!more || pf_end(g, x) > g.j0) return;
-                // (a segment without keys for tile A is the end of an item: it still owes a partial)
-                if ((x ? g.nt_b : g.nt_a) > 0)
-                    a.part_ml[(size_t)(2 * (int)blockIdx.x + (i > 0 ? 1 : 0)) * 2 * kPfRows + x * kPfRows + r] = make_float2(-INFINITY, 0.f);
-                i += g.j1 - g.j0;
-                done_with(k);
-            }
-        };
-        find();
-        float qf = 0.f;
-        if (more) {
-            fetch_q(seg_s[k & (kPfSegs - 1)]);
-            qf = scale_q();
         }
-        while (more && ok) {
-            int last, left;                                 // last key of the tile that this row sees; tiles after this one
-            bool first = true;
+        const int my_pos = it.pos0 + x * it.tt + tok;       // rows beyond the tokens mask nothing that is kept
+        const uint32_t ts = tmem + lane_base + L::TMEM_S + (uint32_t)x * 128u;
+        const uint32_t to = tmem + lane_base + L::TMEM_O + (uint32_t)x * 128u;
+        float m_used = -INFINITY;
+        float2 l2 = make_float2(0.f, 0.f);
+        bool ok = true;
+        for (int j = 0; j < n_x; ++j) {
+            const int slot = j & (kPfMeta - 1);
+            ok = mbar_wait_bounded(&meta_ready[slot], (uint32_t)(j / kPfMeta) & 1u, &abort_s, status) &&
+                 mbar_wait_bounded(&s_full[x], (uint32_t)j & 1u, &abort_s, status);
+            ok = __all_sync(0xffffffffu, ok);               // the TMEM accesses are warp-collective
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t chunks = ok_s[slot];
+            const int last = my_pos - j * kPfKeys;          // last key of the tile that this row sees
+            float f[kPfChunks];
             {
-                // (rows beyond the tokens mask nothing that is kept)
-                const PfSegment& g = seg_s[k & (kPfSegs - 1)];
-                last = g.pos0 + x * tt + (int)((uint32_t)r * per_g >> 16) - g.j0 * kPfKeys;
-                left = pf_end(g, x) - g.j0 - 1;
-                __syncwarp();
-                // slot 0 of the CTA: the segment holds the run's first key tile; slot 1: its last
-                if (lane == 0) out_s[warp].part = g.j0 == 0 && g.j1 == g.n_kt ? -1 : 2 * (int)blockIdx.x + (i > 0 ? 1 : 0);
+                const float4 f0 = *reinterpret_cast<const float4*>(&ks_s[slot][0]);
+                const float4 f1 = *reinterpret_cast<const float4*>(&ks_s[slot][4]);
+                f[0] = f0.x * qf; f[1] = f0.y * qf; f[2] = f0.z * qf; f[3] = f0.w * qf;
+                f[4] = f1.x * qf; f[5] = f1.y * qf; f[6] = f1.z * qf; f[7] = f1.w * qf;
             }
-            float m_used = -INFINITY;
-            float2 l2 = make_float2(0.f, 0.f);
-            for (; left >= 0; --left, ++i, last -= kPfKeys, first = false) {
-                const int slot = i & (kPfMeta - 1);
-                ok = mbar_wait_bounded(&meta_ready[slot], (uint32_t)(i / kPfMeta) & 1u, &abort_s, status) &&
-                     mbar_wait_bounded(&s_full[x], s_par, &abort_s, status);
-                ok = __all_sync(0xffffffffu, ok);           // the TMEM accesses are warp-collective
-                if (!ok) break;
-                s_par ^= 1u;
-                tc_fence_after();
-                if (left == 0) {
-                    // The item's last S is there, so its Q is no longer needed: the next one's is fetched beside this
-                    // tile's softmax.  What the output needs of the segment is kept aside.
-                    const PfSegment& g = seg_s[k & (kPfSegs - 1)];
-                    if (lane == 0) {
-                        out_s[warp].row0 = ((long long)g.tok0 + x * tt) * a.n_heads + g.hk * G;
-                        out_s[warp].nt = x ? g.nt_b : g.nt_a;
-                        out_s[warp].exp = vexp_s[slot];
-                    }
-                    const int here = i;
-                    i += 1 + g.j1 - pf_end(g, x);
-                    done_with(k);
-                    ++k;
-                    find();
-                    if (lane == 0) out_s[warp].next = i;
-                    i = here;
-                    if (!ok) break;
-                    if (more) fetch_q(seg_s[k & (kPfSegs - 1)]);
-                }
-                const uint32_t chunks = ok_s[slot];
-                // score factor of chunk c, kept above 0: times a masked score of -inf it has to stay -inf
-                const auto factor = [&](int c) { return fmaxf(ks_s[slot][c] * qf, 1.2e-38f); };
-                float s[128];
-                {
-                    uint32_t s0[64], s1[64];
-                    tmem_ld64_issue(ts, s0);
-                    tmem_ld64_issue(ts + 64u, s1);
-                    tmem_wait_ld(s0);
-                    tmem_wait_ld(s1);
+            float s[128];
+            {
+                uint32_t s0[64], s1[64];
+                tmem_ld64_issue(ts, s0);
+                tmem_ld64_issue(ts + 64u, s1);
+                tmem_wait_ld(s0);
+                tmem_wait_ld(s1);
 #pragma unroll
-                    for (int e = 0; e < 64; ++e) {
-                        s[e] = __uint_as_float(s0[e]);
-                        s[64 + e] = __uint_as_float(s1[e]);
-                    }
+                for (int i = 0; i < 64; ++i) {
+                    s[i] = __uint_as_float(s0[i]);
+                    s[64 + i] = __uint_as_float(s1[i]);
                 }
-                if (!__all_sync(0xffffffffu, last >= kPfKeys - 1 && chunks == (1u << kPfChunks) - 1u)) {
-#pragma unroll
-                    for (int c = 0; c < kPfChunks; ++c) {
-                        const int lim = (chunks >> c) & 1u ? last - c * 16 : -1;
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) s[16 * c + e] = e <= lim ? s[16 * c + e] : -INFINITY;
-                    }
-                }
-                float mx = -INFINITY;
+            }
+            if (!__all_sync(0xffffffffu, last >= kPfKeys - 1 && chunks == (1u << kPfChunks) - 1u)) {
 #pragma unroll
                 for (int c = 0; c < kPfChunks; ++c) {
-                    float m0 = max3(s[16 * c], s[16 * c + 1], s[16 * c + 2]), m1 = max3(s[16 * c + 3], s[16 * c + 4], s[16 * c + 5]);
-                    m0 = max3(m0, s[16 * c + 6], s[16 * c + 7]);
-                    m1 = max3(m1, s[16 * c + 8], s[16 * c + 9]);
-                    m0 = max3(m0, s[16 * c + 10], s[16 * c + 11]);
-                    m1 = max3(m1, s[16 * c + 12], s[16 * c + 13]);
-                    m0 = max3(m0, s[16 * c + 14], s[16 * c + 15]);
-                    mx = fmaxf(mx, fmaxf(m0, m1) * factor(c));
+                    const int lim = (chunks >> c) & 1u ? last - c * 16 : -1;
+                    f[c] = lim < 0 ? 1.f : f[c];            // (no 0 * -inf)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) s[16 * c + i] = i <= lim ? s[16 * c + i] : -INFINITY;
                 }
-                const bool move = mx > m_used + 8.f;        // false while the row has no key
-                if (__any_sync(0xffffffffu, move)) {
-                    const float dn = move ? ex2_approx(m_used - mx) : 1.f;
-                    if (!first) {
-                        // S of this tile is complete, so P V of the tile before is in O
+            }
+            float mx = -INFINITY;
 #pragma unroll
-                        for (int c = 0; c < D; c += 8) tmem_scale8(to + (uint32_t)c, dn);
-                    }
-                    if (move) {
-                        l2.x *= dn;
-                        l2.y *= dn;
-                        m_used = mx;
-                    }
+            for (int c = 0; c < kPfChunks; ++c) {
+                float m0 = max3(s[16 * c], s[16 * c + 1], s[16 * c + 2]), m1 = max3(s[16 * c + 3], s[16 * c + 4], s[16 * c + 5]);
+                m0 = max3(m0, s[16 * c + 6], s[16 * c + 7]);
+                m1 = max3(m1, s[16 * c + 8], s[16 * c + 9]);
+                m0 = max3(m0, s[16 * c + 10], s[16 * c + 11]);
+                m1 = max3(m1, s[16 * c + 12], s[16 * c + 13]);
+                m0 = max3(m0, s[16 * c + 14], s[16 * c + 15]);
+                // factor >= 0; a row without a key here keeps -inf (0 * -inf would be NaN)
+                const float mc = fmaxf(m0, m1);
+                mx = fmaxf(mx, mc == -INFINITY ? mc : mc * f[c]);
+            }
+            const bool move = mx > m_used + 8.f;            // false while the row has no key
+            if (__any_sync(0xffffffffu, move)) {
+                const float dn = move ? ex2_approx(m_used - mx) : 1.f;
+                if (j > 0) {
+                    // S of this tile is complete, so P V of the tile before is in O
+                    for (int c = 0; c < D; c += 8) tmem_scale8(to + (uint32_t)c, dn);
                 }
-                const float base = (m_used == -INFINITY ? 0.f : m_used) - kPfBase;
-                const float2 nb = make_float2(-base, -base);
+                if (move) {
+                    l2.x *= dn;
+                    l2.y *= dn;
+                    m_used = mx;
+                }
+            }
+            const float base = (m_used == -INFINITY ? 0.f : m_used) - kPfBase;
+            const float2 nb = make_float2(-base, -base);
 #pragma unroll
-                for (int c = 0; c < kPfChunks; ++c) {       // 16 keys: 8 columns of P, over S
-                    uint32_t p[8];
-                    const float fc = factor(c);
-                    const float2 ff = make_float2(fc, fc);
+            for (int c2 = 0; c2 < kPfChunks; c2 += 2) {     // 32 keys: 16 columns of P, over S
+                uint32_t p[16];
 #pragma unroll
-                    for (int e2 = 0; e2 < 8; ++e2) {
-                        float2 e = fma2(make_float2(s[16 * c + 2 * e2], s[16 * c + 2 * e2 + 1]), ff, nb);
+                for (int h = 0; h < 2; ++h) {
+                    const int c = c2 + h;
+                    const float2 ff = make_float2(f[c], f[c]);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        float2 e = fma2(make_float2(s[16 * c + 2 * i], s[16 * c + 2 * i + 1]), ff, nb);
                         e.x = ex2_approx(e.x);
                         e.y = ex2_approx(e.y);
                         l2 = add2(l2, e);
-                        p[e2] = pack_f16x2(e.x, e.y);
+                        p[8 * h + i] = pack_f16x2(e.x, e.y);
                     }
-                    tmem_st8_issue(ts + (uint32_t)c * 8u, p);
                 }
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&p_ready[x]);
+                tmem_st16_issue(ts + (uint32_t)c2 * 8u, p);
             }
-            if (!ok) break;
+            tmem_wait_st();
+            tc_fence_before();
             __syncwarp();
-            i = out_s[warp].next;
-            // the next item's Q before this one's output, so that its S runs beside that
-            if (more) qf = scale_q();
-            ok = __all_sync(0xffffffffu, mbar_wait_bounded(&o_done[x], o_par, &abort_s, status));
-            if (!ok) break;
-            o_par ^= 1u;
+            if (lane == 0) mbar_arrive(&p_ready[x]);
+        }
+        ok = __all_sync(0xffffffffu, ok && (n_x == 0 || mbar_wait_bounded(&o_done[x], 0, &abort_s, status)));
+        if (ok && n_x > 0) {
             tc_fence_after();
+            // vexp_s was written before v_ready of tile 0, which the P V behind o_done waited for
             const float l = l2.x + l2.y;
-            const int E6 = out_s[warp].exp - kPfShift;
-            const float up = E6 < -126 ? 0.f : __uint_as_float((uint32_t)(E6 + 127) << 23);
             const float inv = l == 0.f ? 0.f : 1.f / l;
-            const float f = inv * up;
-            const int tok = (int)((uint32_t)r * per_g >> 16), part = out_s[warp].part;
-            const bool live = tok < out_s[warp].nt;
-            const size_t qrow = (size_t)out_s[warp].row0 + (size_t)tok * a.n_heads + (r - tok * G);
-            const size_t prow = (size_t)max(part, 0) * 2 * kPfRows + x * kPfRows + r;
+            const int E = *const_cast<volatile int*>(&vexp_s) - kPfShift;
+            const float up = E < -126 ? 0.f : __uint_as_float((uint32_t)(E + 127) << 23);
 #pragma unroll 1
             for (int c = 0; c < D; c += 16) {
                 float v[16];
                 tmem_ld16(to + (uint32_t)c, v);
-#pragma unroll
-                for (int e = 0; e < 16; ++e) v[e] *= f;
-                if (live && part < 0) {
+                if (live) {
                     uint32_t y[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) y[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
+                    for (int i = 0; i < 8; ++i) y[i] = pack_bf16x2(v[2 * i] * inv * up, v[2 * i + 1] * inv * up);
                     uint4* dst = reinterpret_cast<uint4*>(a.out + qrow * D + c);
                     dst[0] = make_uint4(y[0], y[1], y[2], y[3]);
                     dst[1] = make_uint4(y[4], y[5], y[6], y[7]);
-                } else if (live) {
-                    uint32_t y[8], z[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        y[e] = __float_as_uint(v[e]);
-                        z[e] = __float_as_uint(v[8 + e]);
-                    }
-                    store32(a.part_o + prow * D + c, y);
-                    store32(a.part_o + prow * D + c + 8, z);
                 }
             }
-            if (live && part >= 0) a.part_ml[prow] = make_float2(m_used, l);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&o_free[x]);
         }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     if (warp == 12) tmem_dealloc(tmem, L::TMEM_COLS);
-}
-
-// Joins the partials of one item: that of boundary c = blockIdx.x + 1 between the grid's P runs, if it lies
-// inside an item and is the first one there.  blockIdx.y takes 32 of the item's 256 query rows; a row's D / 4
-// lanes hold four head dims each.
-constexpr int kPfJoinThreads = 256;
-constexpr int kPfJoinRows = 32;
-__global__ void __launch_bounds__(kPfJoinThreads) attn_prefill_f8_join_kernel(const AttnF8Args a, int tt, int P) {
-    __shared__ PfRun run_s;
-    pdl_wait();
-    pdl_trigger();
-    const int c = blockIdx.x + 1, D = a.head_dim, step = 2 * tt;
-    pf_find_run(a, step, P, c - 1, kPfJoinThreads, false, &run_s);
-    if (run_s.end >= run_s.total) return;
-    const PfPlace at = run_s.to;
-    const PfSeq s = pf_seq(a, at.b, false);
-    const int n_kt = (s.pos0 + min((at.mt + 1) * step, s.n) + kPfKeys - 1) / kPfKeys;
-    if (at.j == 0 || at.j >= n_kt) return;
-    const long long t0 = run_s.end - at.j, t1 = t0 + n_kt;
-    if (run_s.begin > t0) return;                          // not the first inside
-    const long long q = run_s.total / P, rem = run_s.total - q * P;
-    const auto boundary = [&](int k) { return q * k + min((long long)k, rem); };    // before the snap
-    const int first_slot = 2 * (c - 1) + (run_s.begin == t0 ? 0 : 1);
-    int last = c;                                          // the last run with tiles of the item
-    while (last + 1 < P && boundary(last + 1) < t1 - kPfSnap) ++last;
-    const int G = a.n_heads / a.n_kv_heads;
-    const int lanes = D / 4, rows_at_once = kPfJoinThreads / lanes, lane = threadIdx.x % lanes;
-    const int row0 = (int)blockIdx.y * kPfJoinRows;
-    for (int i = threadIdx.x / lanes; i < kPfJoinRows; i += rows_at_once) {
-        const int row = row0 + i, x = row / kPfRows, r = row % kPfRows;
-        const int tok = at.mt * step + x * tt + r / G;
-        if (r / G >= tt || tok >= s.n) continue;
-        float M = -INFINITY;
-        for (int k = c - 1; k <= last; ++k)
-            M = fmaxf(M, a.part_ml[(size_t)(k < c ? first_slot : 2 * k) * 2 * kPfRows + row].x);
-        const float base = M == -INFINITY ? 0.f : M;
-        float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
-        float den = 0.f;
-        for (int k = c - 1; k <= last; ++k) {
-            const size_t pr = (size_t)(k < c ? first_slot : 2 * k) * 2 * kPfRows + row;
-            const float2 ml = a.part_ml[pr];
-            if (ml.y == 0.f) continue;                     // no key there; its row may not be written
-            const float w = exp2f(ml.x - base) * ml.y;
-            const float4 o = *reinterpret_cast<const float4*>(a.part_o + pr * D + lane * 4);
-            num.x += w * o.x;
-            num.y += w * o.y;
-            num.z += w * o.z;
-            num.w += w * o.w;
-            den += w;
-        }
-        const float inv = den == 0.f ? 0.f : 1.f / den;
-        *reinterpret_cast<uint2*>(a.out + ((size_t)(s.c0 + tok) * a.n_heads + (size_t)at.hk * G + r % G) * D + lane * 4) =
-            make_uint2(pack_bf16x2(num.x * inv, num.y * inv), pack_bf16x2(num.z * inv, num.w * inv));
-    }
 }
 
 template <int D>
@@ -1028,34 +678,27 @@ cudaError_t prefill_f8_for(const AttnF8Args& a, cudaStream_t stream) {
         e = ensure_func_attr(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, (int)cudaSharedmemCarveoutMaxShared,
                              "cudaFuncSetAttribute(attn_prefill_f8_kernel carveout)");
     if (e != cudaSuccess) return e;
-    const int sms = std::min(device_sm_count(), kF8MaxSms);
-    if (sms <= 0) return record(cudaErrorNoDevice, "attn_prefill_f8");
     const int tt = kPfRows / (a.n_heads / a.n_kv_heads);    // tokens per query tile
+    const int n_mt = (a.max_new + 2 * tt - 1) / (2 * tt);
+    const long long items = (long long)a.batch * n_mt * a.n_kv_heads;
+    if (items > (1LL << 30)) {
+        set_last_error("attn_prefill_f8", "too many (sequence, KV head, query tile) items");
+        return cudaErrorInvalidValue;
+    }
     trace_before("attn_prefill_f8", stream);
-    e = launch_pdl(attn_prefill_f8_kernel<D>, dim3((unsigned)sms), dim3(kPfThreads), smem, stream, 1, a, tt);
+    e = launch_pdl(attn_prefill_f8_kernel<D>, dim3((unsigned)items), dim3(kPfThreads), smem, stream, 1, a, n_mt, tt);
     trace_after(stream);
     if (e == cudaSuccess) e = cudaGetLastError();
-    if (e != cudaSuccess) return record(e, "attn_prefill_f8_kernel launch");
-    if (sms == 1) return cudaSuccess;
-    trace_before("attn_prefill_f8_join", stream);
-    e = launch_pdl(attn_prefill_f8_join_kernel, dim3((unsigned)(sms - 1), 2 * kPfRows / kPfJoinRows), dim3(kPfJoinThreads), 0,
-                   stream, 1, a, tt, sms);
-    trace_after(stream);
-    if (e == cudaSuccess) e = cudaGetLastError();
-    return record(e, "attn_prefill_f8_join_kernel launch");
+    return record(e, "attn_prefill_f8_kernel launch");
 }
 
 }  // namespace
 
-// Two partials of 256 rows per CTA; sized for the largest grid on any device.
-size_t attn_prefill_f8_scratch_bytes(int head_dim) {
-    return (size_t)2 * kF8MaxSms * 2 * kPfRows * (head_dim * sizeof(float) + sizeof(float2));
-}
+size_t attn_prefill_f8_scratch_bytes(int) { return 16; }
 
 cudaError_t launch_attn_prefill_f8(AttnF8Args a, void* workspace, cudaStream_t stream) {
+    (void)workspace;
     if (a.tokens <= 0) return cudaSuccess;
-    a.part_o = static_cast<float*>(workspace);
-    a.part_ml = reinterpret_cast<float2*>(a.part_o + (size_t)2 * kF8MaxSms * 2 * kPfRows * a.head_dim);
     return a.head_dim == 128 ? prefill_f8_for<128>(a, stream) : prefill_f8_for<64>(a, stream);
 }
 
