@@ -190,26 +190,6 @@ LL_DEVINL void pf_mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t b_hi, u
         "r"(a), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate));
 }
 
-// The two issuing warps take turns on the tensor core (bounded as the barrier waits are); a turn is P V of
-// a key tile with the S of the next.  Interleaved, or in smaller turns, both tiles' S are ready together: both
-// softmaxes run at once and the tensor core waits for them.
-LL_DEVINL bool turn_take(int* turn, volatile int* abort, int32_t* status) {
-    uint64_t t0 = 0;
-    for (uint32_t it = 1; atomicCAS_block(turn, 0, 1) != 0; ++it) {
-        if ((it & 255u) == 0) {
-            if (*abort) return false;
-            if (t0 == 0) t0 = global_timer_ns();
-            if (global_timer_ns() - t0 > kWaitLimitNs) {
-                *abort = 1;
-                flag_status(status, LL_DEV_TIMEOUT);
-                return false;
-            }
-        }
-    }
-    return true;
-}
-LL_DEVINL void turn_leave(int* turn) { atomicExch_block(turn, 0); }
-
 // What a work item covers: new tokens t0 .. of sequence b (rows tok0 + t of q), the first at position pos0;
 // nt_a and nt_b tokens in the tiles, which see keys 0 .. end_a - 1 and 0 .. end_b - 1 (0: no tile B).
 struct PfItem {
@@ -252,10 +232,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
     // Per query tile x and key tile j (parity j & 1): S computed, P stored.  Per key buffer: K or V stored
     // (ready), read by both query tiles (empty).  Scales of key tile j sit in slot j & 3: slot and barrier
     // are written again for tile j + 4, after the S of tile j + 2, which waits for the P of tile j + 1.
-    __shared__ uint64_t q_ready[2], s_full[2], p_ready[2], o_done[2], k_ready[2], k_empty[2], v_ready[2], v_empty[2];
+    __shared__ uint64_t q_ready[2], s_full[2], p_ready[2][2], turn_done[2], o_done[2], k_ready[2], k_empty[2], v_ready[2], v_empty[2];
     __shared__ uint64_t meta_ready[kPfMeta], drain[2];
     __shared__ uint32_t tmem_base_s;
-    __shared__ int abort_s, turn_s;
+    __shared__ int abort_s;
     __shared__ __align__(16) float ks_s[kPfMeta][kPfChunks];   // per 16-key chunk: K scale
     __shared__ uint32_t ok_s[kPfMeta];                      // bit c = chunk c is backed by a valid block
     __shared__ int vexp_w[4], vexp_s;                       // exponent of the item's largest V scale
@@ -266,7 +246,9 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
         for (int i = 0; i < 2; ++i) {
             mbar_init(&q_ready[i], 4);
             mbar_init(&s_full[i], 1);
-            mbar_init(&p_ready[i], 4);
+            mbar_init(&p_ready[i][0], 4);
+            mbar_init(&p_ready[i][1], 4);
+            mbar_init(&turn_done[i], 1);
             mbar_init(&o_done[i], 1);
             mbar_init(&k_ready[i], 4);
             mbar_init(&k_empty[i], 2);
@@ -276,7 +258,6 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
         }
         for (int i = 0; i < kPfMeta; ++i) mbar_init(&meta_ready[i], 1);
         abort_s = 0;
-        turn_s = 0;
         fence_mbar_init();
     }
     pdl_wait();
@@ -312,12 +293,11 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
             const uint32_t t_s = tmem + L::TMEM_S + (uint32_t)x * 128u, t_o = tmem + L::TMEM_O + (uint32_t)x * 128u;
             auto k_wait = [&](int i) { return mbar_wait_bounded(&k_ready[i & 1], (uint32_t)(i >> 1) & 1u, &abort_s, status); };
             auto v_wait = [&](int i) { return mbar_wait_bounded(&v_ready[i & 1], (uint32_t)(i >> 1) & 1u, &abort_s, status); };
-            auto take = [&](bool good) {                    // (all lanes' waits went well, and the turn is the warp's)
-                good = __all_sync(0xffffffffu, good);
-                if (good && lane == 0) good = turn_take(&turn_s, &abort_s, status);
-                good = __all_sync(0xffffffffu, good);
-                tc_fence_after();
-                return good;
+            // The two warps take turns, A before B: a turn is P V of a key tile with the S of the next.  Interleaved,
+            // both tiles' S would be ready together: both softmaxes would run at once and the tensor core wait for them.
+            auto my_turn = [&](int j) {
+                const int before = x ? j : j - 1;           // the other's turn, if it has one
+                return before < 0 || before >= (x ? n_a : n_b) || mbar_wait_bounded(&turn_done[x ^ 1], (uint32_t)before & 1u, &abort_s, status);
             };
             // S of a key tile, over P of the one before (MMAs of one thread run in order); by the elected lane
             auto issue_s = [&](int i) {
@@ -330,38 +310,48 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
                 }
                 tc_commit(&s_full[x]);
             };
-            auto issue_pv = [&](int i, bool first) {
-                const uint32_t b = v_lo + (uint32_t)(i & 1) * (L::TILE >> 4);
+            // 64 keys of O += P V
+            auto issue_pv = [&](int i, int half, bool first) {
+                const uint32_t b = v_lo + (uint32_t)(i & 1) * (L::TILE >> 4) + (uint32_t)(half * 4 * 2048 >> 4);
 #pragma unroll
-                for (int kk = 0; kk < kPfKeys / 16; ++kk)
-                    pf_mma_ts(t_o, t_s + (uint32_t)kk * 8u, b + (uint32_t)(kk * 2048 >> 4), v_hi, id_o, !first || kk > 0 ? 1u : 0u);
+                for (int kk = 0; kk < 4; ++kk)
+                    pf_mma_ts(t_o, t_s + (uint32_t)half * 32u + (uint32_t)kk * 8u, b + (uint32_t)(kk * 2048 >> 4), v_hi, id_o,
+                              !first || kk > 0 ? 1u : 0u);
             };
             bool ok = true;
             if (n_x > 0) {
-                ok = take(mbar_wait_bounded(&q_ready[x], 0, &abort_s, status) && k_wait(0));
+                ok = __all_sync(0xffffffffu, mbar_wait_bounded(&q_ready[x], 0, &abort_s, status) && k_wait(0));
+                tc_fence_after();
                 if (ok && elect_one()) {
                     issue_s(0);
-                    turn_leave(&turn_s);
                     tc_commit(&k_empty[0]);
                 }
                 __syncwarp();
             }
             for (int j = 0; j < n_x && ok; ++j) {
-                // (what is usually there already is waited for first, beside the softmax)
+                // (what is usually there already is waited for first, beside the softmax; P comes in halves of 64 keys,
+                // so that P V of the first runs while the second is computed)
                 const bool more = j + 1 < n_x;
-                ok = take(v_wait(j) && (!more || k_wait(j + 1)) && mbar_wait_bounded(&p_ready[x], (uint32_t)j & 1u, &abort_s, status));
+                ok = __all_sync(0xffffffffu, v_wait(j) && (!more || k_wait(j + 1)) && my_turn(j) &&
+                                                 mbar_wait_bounded(&p_ready[x][0], (uint32_t)j & 1u, &abort_s, status));
                 if (!ok) break;
+                tc_fence_after();
+                if (elect_one()) issue_pv(j, 0, j == 0);
+                __syncwarp();
+                ok = __all_sync(0xffffffffu, mbar_wait_bounded(&p_ready[x][1], (uint32_t)j & 1u, &abort_s, status));
+                if (!ok) break;
+                tc_fence_after();
                 if (elect_one()) {
-                    issue_pv(j, j == 0);
+                    issue_pv(j, 1, false);
                     if (more) issue_s(j + 1);
-                    turn_leave(&turn_s);
+                    mbar_arrive(&turn_done[x]);
                     tc_commit(&v_empty[j & 1]);
                     if (more) tc_commit(&k_empty[(j + 1) & 1]);
                     else tc_commit(&o_done[x]);
                 }
                 __syncwarp();
             }
-            // past its own last tile a query tile still takes part in the buffers' turns
+            // past its own last tile a query tile still takes part in the buffers' rounds
             for (int j = n_x; j < n_kt && ok; ++j) {
                 ok = __all_sync(0xffffffffu, k_wait(j) && v_wait(j));
                 if (ok && lane == 0) {
@@ -632,11 +622,13 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
                     }
                 }
                 tmem_st16_issue(ts + (uint32_t)c2 * 8u, p);
+                if (c2 % 4 == 2) {                          // 64 keys are there
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&p_ready[x][c2 / 4]);
+                }
             }
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&p_ready[x]);
         }
         ok = __all_sync(0xffffffffu, ok && (n_x == 0 || mbar_wait_bounded(&o_done[x], 0, &abort_s, status)));
         if (ok && n_x > 0) {
