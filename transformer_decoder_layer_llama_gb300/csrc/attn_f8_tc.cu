@@ -4,7 +4,10 @@
 // A work item is one KV head of one sequence and two tiles (A, B) of 128 query rows each: a tile is
 // floor(128 / G) consecutive tokens times the G query heads that share the KV head, so a tile of keys is
 // brought in and converted once for 256 rows.  One CTA per SM and item, 128 keys at a time up to the
-// item's last position, items with the most keys first.
+// item's last position, items with the most keys first.  Where there are at most half as many items as SMs,
+// several CTAs share an item's keys and a second kernel joins their float32 partials by the log-sum-exp.
+// (A persistent grid with equal shares of all key tiles was slower: 7B prefill 80 us and 27 for the join against
+// 50, 70B-shaped chunks 605 against 551.  Its roles need registers for the walk, and a partial is 128 KB.)
 //
 // Roles (416 threads):
 //  * warps 0-3 and 4-7, softmax of tile A and B: one thread per query row.  First they stage Q in shared
@@ -195,11 +198,11 @@ LL_DEVINL void pf_mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t b_hi, u
 struct PfItem {
     int b, hk, tok0, pos0, tt;
     int nt_a, nt_b, end_a, end_b;
+    int n_kt;                // key tiles
 };
 
-LL_DEVINL bool pf_item(const AttnF8Args& a, int n_mt, int tt, bool flag, PfItem& it) {
+LL_DEVINL bool pf_item(const AttnF8Args& a, int i, int n_mt, int tt, bool flag, PfItem& it) {
     // latest tiles (the most keys) first, KV heads fastest
-    int i = blockIdx.x;
     it.hk = i % a.n_kv_heads;
     i /= a.n_kv_heads;
     it.b = i % a.batch;
@@ -221,11 +224,17 @@ LL_DEVINL bool pf_item(const AttnF8Args& a, int n_mt, int tt, bool flag, PfItem&
     it.nt_b = min(tt, left - it.nt_a);
     it.end_a = it.pos0 + it.nt_a;
     it.end_b = it.nt_b ? it.end_a + it.nt_b : 0;
+    it.n_kt = (max(it.end_a, it.end_b) + kPfKeys - 1) / kPfKeys;
     return true;
 }
 
+// Where there are fewer items than SMs, ns CTAs share an item's key tiles, each at least kPfLeast of them, and leave
+// partials for the join kernel.
+constexpr int kPfLeast = 3;
+LL_DEVINL int pf_splits(int ns, int n_kt) { return max(1, min(ns, n_kt / kPfLeast)); }
+
 template <int D>
-__global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const AttnF8Args a, int n_mt, int tt) {
+__global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const AttnF8Args a, int n_mt, int tt, int ns) {
     using L = PfLayout<D>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -263,7 +272,12 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
     pdl_wait();
     pdl_trigger();
     PfItem it;
-    if (!pf_item(a, n_mt, tt, threadIdx.x == 0, it)) return;
+    const int item = (int)blockIdx.x / ns, split = (int)blockIdx.x - item * ns;
+    if (!pf_item(a, item, n_mt, tt, threadIdx.x == 0 && split == 0, it)) return;
+    const int splits = pf_splits(ns, it.n_kt);
+    if (split >= splits) return;
+    const int first = (int)((long long)it.n_kt * split / splits);   // the CTA's first key tile; tiles are counted from it
+    const int n_kt = (int)((long long)it.n_kt * (split + 1) / splits) - first;
     if (warp == 12) {
         tmem_alloc(&tmem_base_s, L::TMEM_COLS);
         tmem_relinquish();
@@ -273,8 +287,9 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
     tc_fence_after();
     const uint32_t tmem = tmem_base_s;
     const int G = a.n_heads / a.n_kv_heads;
-    const int n_a = (it.end_a + kPfKeys - 1) / kPfKeys, n_b = (it.end_b + kPfKeys - 1) / kPfKeys;
-    const int n_kt = max(n_a, n_b), kv_end = max(it.end_a, it.end_b);
+    const int n_a = min(max((it.end_a + kPfKeys - 1) / kPfKeys - first, 0), n_kt);
+    const int n_b = min(max((it.end_b + kPfKeys - 1) / kPfKeys - first, 0), n_kt);
+    const int kv_end = max(it.end_a, it.end_b) - first * kPfKeys;   // keys, and table entries, from there too
 
     if (warp >= 12) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
@@ -376,18 +391,19 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
         const int c16 = D == 128 ? (tid & 3) | ((tid >> 1) & 4) : tid & 3;
         const int rsub = D == 128 ? ((tid >> 2) & 1) | ((tid >> 3) & ~1) : tid >> 2;
         const int32_t* table_row = a.block_table + (size_t)it.b * a.max_blocks;
+        const int key0 = first * kPfKeys;
         const int my_key = (lane & 7) * 16;                 // lane c < 8 looks after 16-key chunk c of a tile
         const int bs_log2 = 31 - __clz(a.block_size);       // (a power of two: no divisions on this path)
         auto entry_of = [&](int j) {                        // its table entry (-1 past the keys)
             const int key = j * kPfKeys + my_key;
-            return j < n_kt && key < kv_end ? table_row[key >> bs_log2] : -1;
+            return j < n_kt && key < kv_end ? table_row[(key0 + key) >> bs_log2] : -1;
         };
         auto row_of = [&](int j, int entry) {               // its first pool row (-1: no valid block)
             const int key = j * kPfKeys + my_key;
             const bool want = j < n_kt && key < kv_end;
             if (want && (entry < 0 || entry >= a.num_blocks)) flag_status(status, LL_DEV_BAD_BLOCK);
             return want && entry >= 0 && entry < a.num_blocks
-                       ? ((entry * a.n_kv_heads + it.hk) << bs_log2) + (key & (a.block_size - 1)) : -1;
+                       ? ((entry * a.n_kv_heads + it.hk) << bs_log2) + ((key0 + key) & (a.block_size - 1)) : -1;
         };
         auto scale_of = [&](const float* scales, int row) {
             return row >= 0 ? scales[row >> bs_log2] : 0.f;
@@ -454,10 +470,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
             load(a.k_pool, j + 1, row, kw);
             ks = scale_of(a.k_scale, row);
             if (j == 0) {
-                // exponent of the largest V scale of the item's keys
-                const int n = (kv_end + a.block_size - 1) >> bs_log2;
+                // exponent of the largest V scale of the CTA's keys
+                const int n = (key0 + min(kv_end, n_kt * kPfKeys) + a.block_size - 1) >> bs_log2;
                 float top = 0.f;
-                for (int i = tid; i < n; i += 128) {
+                for (int i = (key0 >> bs_log2) + tid; i < n; i += 128) {
                     const int x = table_row[i];
                     if (x >= 0 && x < a.num_blocks) top = fmaxf(top, a.v_scale[(size_t)x * a.n_kv_heads + it.hk]);
                 }
@@ -533,7 +549,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
             __syncwarp();
             if (lane == 0) mbar_arrive(&q_ready[x]);
         }
-        const int my_pos = it.pos0 + x * it.tt + tok;       // rows beyond the tokens mask nothing that is kept
+        const int my_pos = it.pos0 + x * it.tt + tok - first * kPfKeys;   // rows beyond the tokens mask nothing that is kept
         const uint32_t ts = tmem + lane_base + L::TMEM_S + (uint32_t)x * 128u;
         const uint32_t to = tmem + lane_base + L::TMEM_O + (uint32_t)x * 128u;
         float m_used = -INFINITY;
@@ -630,6 +646,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
                 }
             }
         }
+        const size_t prow = (size_t)blockIdx.x * 2 * kPfRows + x * kPfRows + r;
         ok = __all_sync(0xffffffffu, ok && (n_x == 0 || mbar_wait_bounded(&o_done[x], 0, &abort_s, status)));
         if (ok && n_x > 0) {
             tc_fence_after();
@@ -642,21 +659,68 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
             for (int c = 0; c < D; c += 16) {
                 float v[16];
                 tmem_ld16(to + (uint32_t)c, v);
-                if (live) {
+                if (live && splits == 1) {
                     uint32_t y[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) y[i] = pack_bf16x2(v[2 * i] * inv * up, v[2 * i + 1] * inv * up);
                     uint4* dst = reinterpret_cast<uint4*>(a.out + qrow * D + c);
                     dst[0] = make_uint4(y[0], y[1], y[2], y[3]);
                     dst[1] = make_uint4(y[4], y[5], y[6], y[7]);
+                } else if (live) {
+                    float4* dst = reinterpret_cast<float4*>(a.part_o + prow * D + c);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        dst[i] = make_float4(v[4 * i] * inv * up, v[4 * i + 1] * inv * up, v[4 * i + 2] * inv * up, v[4 * i + 3] * inv * up);
                 }
             }
+            if (live && splits > 1) a.part_ml[prow] = make_float2(m_used, l);
+        } else if (ok && live && splits > 1) {
+            a.part_ml[prow] = make_float2(-INFINITY, 0.f);  // no key here
         }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     if (warp == 12) tmem_dealloc(tmem, L::TMEM_COLS);
+}
+
+// Joins the partials of item blockIdx.x; blockIdx.y takes 32 of its 256 query rows, D / 4 lanes to a row.
+constexpr int kPfJoinThreads = 256;
+constexpr int kPfJoinRows = 32;
+__global__ void __launch_bounds__(kPfJoinThreads) attn_prefill_f8_join_kernel(const AttnF8Args a, int n_mt, int tt, int ns) {
+    pdl_wait();
+    pdl_trigger();
+    PfItem it;
+    if (!pf_item(a, blockIdx.x, n_mt, tt, false, it)) return;
+    const int splits = pf_splits(ns, it.n_kt);
+    if (splits == 1) return;
+    const int D = a.head_dim, G = a.n_heads / a.n_kv_heads;
+    const int lanes = D / 4, lane = threadIdx.x % lanes;
+    for (int i = threadIdx.x / lanes; i < kPfJoinRows; i += kPfJoinThreads / lanes) {
+        const int row = (int)blockIdx.y * kPfJoinRows + i, x = row / kPfRows, r = row % kPfRows;
+        if (r / G >= (x ? it.nt_b : it.nt_a)) continue;
+        const size_t pr = (size_t)blockIdx.x * ns * 2 * kPfRows + row;
+        float M = -INFINITY;
+        for (int k = 0; k < splits; ++k) M = fmaxf(M, a.part_ml[pr + (size_t)k * 2 * kPfRows].x);
+        const float base = M == -INFINITY ? 0.f : M;
+        float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+        float den = 0.f;
+        for (int k = 0; k < splits; ++k) {
+            const size_t pk = pr + (size_t)k * 2 * kPfRows;
+            const float2 ml = a.part_ml[pk];
+            if (ml.y == 0.f) continue;                     // no key there; its row may not be written
+            const float w = exp2f(ml.x - base) * ml.y;
+            const float4 o = *reinterpret_cast<const float4*>(a.part_o + pk * D + lane * 4);
+            num.x += w * o.x;
+            num.y += w * o.y;
+            num.z += w * o.z;
+            num.w += w * o.w;
+            den += w;
+        }
+        const float inv = den == 0.f ? 0.f : 1.f / den;
+        *reinterpret_cast<uint2*>(a.out + (((size_t)it.tok0 + x * tt + r / G) * a.n_heads + (size_t)it.hk * G + r % G) * D + lane * 4) =
+            make_uint2(pack_bf16x2(num.x * inv, num.y * inv), pack_bf16x2(num.z * inv, num.w * inv));
+    }
 }
 
 template <int D>
@@ -677,20 +741,35 @@ cudaError_t prefill_f8_for(const AttnF8Args& a, cudaStream_t stream) {
         set_last_error("attn_prefill_f8", "too many (sequence, KV head, query tile) items");
         return cudaErrorInvalidValue;
     }
+    const int sms = std::min(device_sm_count(), kF8MaxSms);
+    if (sms <= 0) return record(cudaErrorNoDevice, "attn_prefill_f8");
+    // Fewer items than half the SMs (a short chunk behind a long prefix): several CTAs per item.
+    const int ns = (int)std::max<long long>(1, sms / items);
     trace_before("attn_prefill_f8", stream);
-    e = launch_pdl(attn_prefill_f8_kernel<D>, dim3((unsigned)items), dim3(kPfThreads), smem, stream, 1, a, n_mt, tt);
+    e = launch_pdl(attn_prefill_f8_kernel<D>, dim3((unsigned)(items * ns)), dim3(kPfThreads), smem, stream, 1, a, n_mt, tt, ns);
     trace_after(stream);
     if (e == cudaSuccess) e = cudaGetLastError();
-    return record(e, "attn_prefill_f8_kernel launch");
+    if (e != cudaSuccess) return record(e, "attn_prefill_f8_kernel launch");
+    if (ns == 1) return cudaSuccess;
+    trace_before("attn_prefill_f8_join", stream);
+    e = launch_pdl(attn_prefill_f8_join_kernel, dim3((unsigned)items, 2 * kPfRows / kPfJoinRows), dim3(kPfJoinThreads), 0, stream, 1,
+                   a, n_mt, tt, ns);
+    trace_after(stream);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    return record(e, "attn_prefill_f8_join_kernel launch");
 }
 
 }  // namespace
 
-size_t attn_prefill_f8_scratch_bytes(int) { return 16; }
+// One partial of 256 rows per CTA of a grid of at most as many CTAs as SMs; sized for the largest on any device.
+size_t attn_prefill_f8_scratch_bytes(int head_dim) {
+    return (size_t)kF8MaxSms * 2 * kPfRows * (head_dim * sizeof(float) + sizeof(float2));
+}
 
 cudaError_t launch_attn_prefill_f8(AttnF8Args a, void* workspace, cudaStream_t stream) {
-    (void)workspace;
     if (a.tokens <= 0) return cudaSuccess;
+    a.part_o = static_cast<float*>(workspace);
+    a.part_ml = reinterpret_cast<float2*>(a.part_o + (size_t)kF8MaxSms * 2 * kPfRows * a.head_dim);
     return a.head_dim == 128 ? prefill_f8_for<128>(a, stream) : prefill_f8_for<64>(a, stream);
 }
 
