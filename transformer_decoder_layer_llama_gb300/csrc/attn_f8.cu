@@ -324,7 +324,8 @@ __global__ void __launch_bounds__(kF8Threads, NT == 1 ? 4 : 2)
         // 8 nt + n; per query column the running max m (the exponent base) and the lane's part of the sum l.
         float acc[NT][W][4];
         float m[NT][2], l[NT][2];
-        int E = -1000;                                     // exponent of the accumulator
+        int E = -1000;                                     // exponent of the accumulator, and 2^(6 - E) as two factors
+        float up0 = 1.f, up1 = 1.f;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -377,30 +378,40 @@ __global__ void __launch_bounds__(kF8Threads, NT == 1 ? 4 : 2)
                         for (int j = 0; j < 4; ++j) s[nt][j] = sp[nt][0][j] + sp[nt][1][j];
                 }
                 // lane: keys g (s[.][0..1]) and g + 8 (s[.][2..3]) of query columns 2 cq and 2 cq + 1
-                const bool v0 = (okmask >> g) & 1u, v1 = (okmask >> (g + 8)) & 1u;
-                float mx[NT][2];
-                bool grow = false;
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const float f = qs[nt][e] * kv.x;
-                        s[nt][e] = v0 ? s[nt][e] * f : -INFINITY;
-                        s[nt][2 + e] = v1 ? s[nt][2 + e] * f : -INFINITY;
-                        mx[nt][e] = fmaxf(s[nt][e], s[nt][2 + e]);
-#pragma unroll
-                        for (int o = 4; o <= 16; o <<= 1) mx[nt][e] = fmaxf(mx[nt][e], __shfl_xor_sync(0xffffffffu, mx[nt][e], o));
-                        grow = grow || mx[nt][e] > m[nt][e] + 8.f;
+                        s[nt][e] *= f;
+                        s[nt][2 + e] *= f;
                     }
+                if (okmask != 0xffffu) {
+                    const bool v0 = (okmask >> g) & 1u, v1 = (okmask >> (g + 8)) & 1u;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            s[nt][e] = v0 ? s[nt][e] : -INFINITY;
+                            s[nt][2 + e] = v1 ? s[nt][2 + e] : -INFINITY;
+                        }
                 }
-                // The exponent base of a column moves only when its max grows by more than 2^8, so that
-                // probabilities stay below 2^8; otherwise the running sums need no rescaling.
+                // The exponent base of a column moves only when a score exceeds it by more than 2^8, so that
+                // probabilities stay below 2^8.  So the column's maximum over the lanes is looked for only then.
+                bool grow = false;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) grow = grow || fmaxf(s[nt][e], s[nt][2 + e]) > m[nt][e] + 8.f;
                 if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            const float mn = mx[nt][e] > m[nt][e] + 8.f ? mx[nt][e] : m[nt][e];
+                            float mx = fmaxf(s[nt][e], s[nt][2 + e]);
+#pragma unroll
+                            for (int o = 4; o <= 16; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                            const float mn = mx > m[nt][e] + 8.f ? mx : m[nt][e];
                             const float al = mn == m[nt][e] ? 1.f : ex2_approx(m[nt][e] - mn);
                             l[nt][e] *= al;
 #pragma unroll
@@ -425,8 +436,11 @@ __global__ void __launch_bounds__(kF8Threads, NT == 1 ? 4 : 2)
                                 for (int j = 0; j < 4; ++j) acc[nt][t][j] *= down;
                     }
                     E = ev;
+                    const int h0 = (kF8Shift - E) / 2, h1 = kF8Shift - E - h0;
+                    up0 = __uint_as_float((uint32_t)(h0 + 127) << 23);
+                    up1 = __uint_as_float((uint32_t)(h1 + 127) << 23);
                 }
-                const float vr = kv.y > 0.f ? scalbnf(kv.y, kF8Shift - E) : kv.y;
+                const float vr = kv.y * up0 * up1;
                 uint32_t pb[NT][2];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
@@ -539,16 +553,18 @@ __global__ void __launch_bounds__(kF8Threads, NT == 1 ? 4 : 2)
 }
 
 // Joins the partials of each (sequence, KV head) whose tiles several CTAs of the grid of P shared, and
-// writes zeros for sequences without a key.  Grid (KV head, sequence).
-__global__ void __launch_bounds__(128) attn_decode_f8_join_kernel(const AttnF8Args a, int P) {
-    __shared__ long long s_sums[4], s_before;
-    pdl_wait();
-    pdl_trigger();
+// writes zeros for sequences without a key.  Grid (KV head, sequence); a thread has four head dims of a query
+// head, and takes the partials four at a time, so that their loads are in flight together.
+constexpr int kF8JoinThreads = 256;
+__global__ void __launch_bounds__(kF8JoinThreads) attn_decode_f8_join_kernel(const AttnF8Args a, int P) {
+    __shared__ long long s_all[kF8JoinThreads / 32], s_before[kF8JoinThreads / 32];
+    // The context lengths are no output of the kernel before this one, which itself waited for their writers
+    // before it let this one start: they are read beside its end.
     const int hk = blockIdx.x, b = blockIdx.y;
     const int G = a.n_heads / a.n_kv_heads, D = a.head_dim;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     long long all = 0, before = 0;
-    for (int i = threadIdx.x; i < a.batch; i += 128) {
+    for (int i = threadIdx.x; i < a.batch; i += kF8JoinThreads) {
         const int n = f8_tiles(f8_context(a, i, false));
         all += n;
         if (i < b) before += n;
@@ -558,38 +574,62 @@ __global__ void __launch_bounds__(128) attn_decode_f8_join_kernel(const AttnF8Ar
         all += __shfl_xor_sync(0xffffffffu, all, o);
         before += __shfl_xor_sync(0xffffffffu, before, o);
     }
-    if (lane == 0) s_sums[warp] = all;
-    if (threadIdx.x == 0) s_before = 0;
-    __syncthreads();
-    all = s_sums[0] + s_sums[1] + s_sums[2] + s_sums[3];
-    if (lane == 0) atomicAdd(reinterpret_cast<unsigned long long*>(&s_before), (unsigned long long)before);
-    __syncthreads();
-    const int n = f8_tiles(f8_context(a, b, false));
-    __nv_bfloat16* out = a.out + ((size_t)b * a.n_heads + (size_t)hk * G) * D;
-    if (n == 0) {
-        for (int i = threadIdx.x; i < G * D; i += 128) out[i] = __float2bfloat16_rn(0.f);
-        return;
+    if (lane == 0) {
+        s_all[warp] = all;
+        s_before[warp] = before;
     }
+    __syncthreads();
+    all = before = 0;
+#pragma unroll
+    for (int w = 0; w < kF8JoinThreads / 32; ++w) {
+        all += s_all[w];
+        before += s_before[w];
+    }
+    const int n = f8_tiles(f8_context(a, b, false));
     const long long total = all * a.n_kv_heads;
-    const long long u0 = s_before * a.n_kv_heads + (long long)hk * n, u1 = u0 + n;
-    const int c0 = share_of(total, P, u0), c1 = share_of(total, P, u1 - 1);
-    if (c0 == c1) return;                                  // one CTA had them all
-    // partial of CTA c: its slot 0 where the tiles reach the share's first, else its slot 1
-    auto slot = [&](int c) { return 2 * c + (share_begin(total, P, c) >= u0 ? 0 : 1); };
-    for (int i = threadIdx.x; i < G * D; i += 128) {
-        const int r = i / D, col = i % D;
-        float M = -INFINITY;
-        for (int c = c0; c <= c1; ++c) M = fmaxf(M, a.part_ml[(size_t)slot(c) * G + r].x);
-        const float base = (M == -INFINITY) ? 0.f : M;
-        float num = 0.f, den = 0.f;
-        for (int c = c0; c <= c1; ++c) {
-            const size_t pr = (size_t)slot(c) * G + r;
-            const float2 ml = a.part_ml[pr];
-            const float w = exp2f(ml.x - base) * ml.y;
-            num += w * a.part_o[pr * D + col];
-            den += w;
+    const long long u0 = before * a.n_kv_heads + (long long)hk * n, u1 = u0 + n;
+    const int c0 = n ? share_of(total, P, u0) : 0, c1 = n ? share_of(total, P, u1 - 1) : 0;
+    // partial of CTA c: its slot 0 where the tiles reach the share's first, else its slot 1 (only the first CTA)
+    const int slot0 = n ? 2 * c0 + (share_begin(total, P, c0) >= u0 ? 0 : 1) : 0;
+    pdl_wait();
+    pdl_trigger();
+    if (n > 0 && c0 == c1) return;                         // one CTA had them all
+    __nv_bfloat16* out = a.out + ((size_t)b * a.n_heads + (size_t)hk * G) * D;
+    for (int i = threadIdx.x; i < G * D / 4; i += kF8JoinThreads) {
+        const int r = i / (D / 4), col = (i - r * (D / 4)) * 4;
+        float M = -INFINITY, den = 0.f;
+        float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c = c0; c <= c1 && n > 0; c += 4) {
+            float2 ml[4];
+            float4 o[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const size_t pr = (size_t)(c + k == c0 ? slot0 : 2 * min(c + k, c1)) * G + r;
+                ml[k] = c + k <= c1 ? a.part_ml[pr] : make_float2(-INFINITY, 0.f);
+                o[k] = *reinterpret_cast<const float4*>(a.part_o + pr * D + col);
+            }
+            const float mn = fmaxf(M, fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)));
+            const float base = mn == -INFINITY ? 0.f : mn, old = exp2f(M - base);
+            num.x *= old;
+            num.y *= old;
+            num.z *= old;
+            num.w *= old;
+            den *= old;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (c + k > c1) break;
+                const float w = exp2f(ml[k].x - base) * ml[k].y;
+                num.x += w * o[k].x;
+                num.y += w * o[k].y;
+                num.z += w * o[k].z;
+                num.w += w * o[k].w;
+                den += w;
+            }
+            M = mn;
         }
-        out[i] = __float2bfloat16_rn(den == 0.f ? 0.f : num / den);
+        const float inv = den == 0.f ? 0.f : 1.f / den;
+        *reinterpret_cast<uint2*>(out + (size_t)r * D + col) =
+            make_uint2(pack_bf16x2(num.x * inv, num.y * inv), pack_bf16x2(num.z * inv, num.w * inv));
     }
 }
 
@@ -626,7 +666,8 @@ cudaError_t decode_f8_for(const AttnF8Args& a, cudaStream_t stream) {
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) return record(e, "attn_decode_f8_kernel launch");
     trace_before("attn_decode_f8_join", stream);
-    e = launch_pdl(attn_decode_f8_join_kernel, dim3((unsigned)a.n_kv_heads, (unsigned)a.batch), dim3(128), 0, stream, 1, a, P);
+    e = launch_pdl(attn_decode_f8_join_kernel, dim3((unsigned)a.n_kv_heads, (unsigned)a.batch), dim3(kF8JoinThreads), 0, stream, 1,
+                   a, P);
     trace_after(stream);
     if (e == cudaSuccess) e = cudaGetLastError();
     return record(e, "attn_decode_f8_join_kernel launch");
