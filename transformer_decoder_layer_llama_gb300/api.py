@@ -527,35 +527,41 @@ def _rows3(t, name, dtype):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must live on the GPU")
-    if t.dim() != 3:
+    shape = t.shape
+    if len(shape) != 3:
         raise ValueError(f"{name} must be [tokens, heads, head_dim]")
-    T, H, d = t.shape
+    T, H, d = shape
     if T == 0:
         return H * d
-    if (d > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != d) or (T > 1 and t.stride(0) < H * d):
+    st, sh, sd = t.stride()
+    if (d > 1 and sd != 1) or (H > 1 and sh != d) or (T > 1 and st < H * d):
         raise ValueError(f"{name} must hold each token's heads contiguously")
-    return t.stride(0) if T > 1 else H * d
+    return st if T > 1 else H * d
 
 
-def _on(*tensors):
-    """The device that all the tensors share."""
-    dev = tensors[0].device
+def _on(first, *tensors):
+    """The index of the device that all the tensors share (None among them is passed over)."""
+    dev = first.get_device()
     for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors on {dev} and {t.device}: one device is needed")
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensors on {first.device} and {t.device}: one device is needed")
     return dev
 
 
-def _call(name, dev, stream, *args):
-    """Calls the library on `stream` (default: the device's current one) with `dev` as the current device."""
-    fn = getattr(lib, name)
-    if dev.index == torch.cuda.current_device():
-        s = stream if stream is not None else torch.cuda.current_stream()
-        _check(name, fn(*args, s.cuda_stream))
-        return
-    with torch.cuda.device(dev):
-        s = stream if stream is not None else torch.cuda.current_stream()
-        _check(name, fn(*args, s.cuda_stream))
+# the current stream of a device as a number, without the Stream object around it (3 us a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _call(name, fn, dev, stream, *args):
+    """Calls the library on `stream` (default: the device's current one) with device index `dev` current."""
+    if dev == torch.cuda.current_device():
+        rc = fn(*args, stream.cuda_stream if stream is not None else _raw_stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, stream.cuda_stream if stream is not None else _raw_stream(dev))
+    if rc != LL_OK:
+        raise LayerError(name, rc)
 
 
 def make_rope_config(rotary_dim, theta=10000.0, scaling="plain", factor=1.0, original_max_position=0, low_turns=1.0,
@@ -576,14 +582,14 @@ def rope_table(rope: ll_rope_config, max_position: int, device=None, stream=None
     if n == 0:
         raise LayerError("ll_rope_table_size", LL_ERR_INVALID_ARG)
     table = torch.empty(int(max_position), rope.rotary_dim // 2, 2, dtype=torch.float32, device=device or "cuda")
-    _call("ll_rope_table", table.device, stream, ctypes.byref(rope), int(max_position), table.data_ptr(), n)
+    _call("ll_rope_table", lib.ll_rope_table, table.get_device(), stream, ctypes.byref(rope), int(max_position), table.data_ptr(), n)
     return table
 
 
 def pack_rope(cfg: ll_config, rope: ll_rope_config, packed: torch.Tensor, stream=None) -> None:
     """ll_pack_rope: the layer calls with `packed` rotate by the scaled frequencies from here on."""
     _need(packed, "packed", torch.uint8)
-    _call("ll_pack_rope", packed.device, stream, ctypes.byref(cfg), ctypes.byref(rope), packed.data_ptr(),
+    _call("ll_pack_rope", lib.ll_pack_rope, packed.get_device(), stream, ctypes.byref(cfg), ctypes.byref(rope), packed.data_ptr(),
           packed.numel())
 
 
@@ -598,38 +604,43 @@ def rope(q, k, positions, table, layout="half", backward=False, q_out=None, k_ou
         raise TypeError("q and k must be bfloat16 or float32 tensors")
     if layout not in LL_ROPE_LAYOUTS:
         raise ValueError(f"layout must be one of {sorted(LL_ROPE_LAYOUTS)}, got {layout!r}")
-    qs = _rows3(q, "q", x.dtype) if q is not None else 0
-    ks = _rows3(k, "k", x.dtype) if k is not None else 0
-    T, d = x.shape[0], x.shape[2]
-    if q is not None and k is not None and (k.shape[0] != T or k.shape[2] != d):
-        raise ValueError(f"k must be [{T}, n_kv_heads, {d}], got {tuple(k.shape)}")
+    T = d = None
+    ends = []                      # per tensor: data, heads, stride, output data, output stride
+    outs = []
+    for t, out, name in ((q, q_out, "q"), (k, k_out, "k")):
+        if t is None:
+            ends.append((None, 0, 0, None, 0))
+            outs.append(None)
+            continue
+        stride = _rows3(t, name, x.dtype)
+        shape = t.shape
+        if T is None:
+            T, _, d = shape
+        elif shape[0] != T or shape[2] != d:
+            raise ValueError(f"k must be [{T}, n_kv_heads, {d}], got {tuple(shape)}")
+        if out is None:
+            out = t.new_empty(shape)
+            out_stride = shape[1] * d
+        else:
+            out_stride = _rows3(out, name + "_out", x.dtype)
+            if out.shape != shape:
+                raise ValueError(f"{name}_out must have shape {tuple(shape)}, got {tuple(out.shape)}")
+        ends.append((t.data_ptr(), shape[1], stride, out.data_ptr(), out_stride))
+        outs.append(out)
     _need(positions, "positions", torch.int32, shape=(T,))
     _need(table, "table", torch.float32)
-    if table.dim() != 3 or table.shape[2] != 2 or not 2 <= 2 * table.shape[1] <= d:
+    rows = table.shape
+    if len(rows) != 3 or rows[2] != 2 or not 2 <= 2 * rows[1] <= d:
         raise ValueError("table must be [max_position, rotary_dim / 2, 2] with rotary_dim <= head_dim")
-    qos = kos = 0
-    if q is not None:
-        if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        qos = _rows3(q_out, "q_out", x.dtype)
-        if q_out.shape != q.shape:
-            raise ValueError(f"q_out must have shape {tuple(q.shape)}, got {tuple(q_out.shape)}")
-    if k is not None:
-        if k_out is None:
-            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-        kos = _rows3(k_out, "k_out", x.dtype)
-        if k_out.shape != k.shape:
-            raise ValueError(f"k_out must have shape {tuple(k.shape)}, got {tuple(k_out.shape)}")
     if status is None:
         status = new_status(x.device)
-    dev = _on(x, q, k, q_out if q is not None else None, k_out if k is not None else None, positions, table, status)
-    _call("ll_rope", dev, stream, q.data_ptr() if q is not None else None, k.data_ptr() if k is not None else None,
-          LL_F32 if x.dtype == torch.float32 else LL_BF16, positions.data_ptr(), T,
-          q.shape[1] if q is not None else 0, k.shape[1] if k is not None else 0, d, 2 * table.shape[1],
-          LL_ROPE_LAYOUTS[layout], LL_ROPE_BACKWARD if backward else LL_ROPE_FORWARD, qs, ks, table.data_ptr(),
-          table.shape[0], q_out.data_ptr() if q is not None else None, k_out.data_ptr() if k is not None else None,
-          qos, kos, status.data_ptr())
-    return (q_out if q is not None else None), (k_out if k is not None else None)
+    dev = _on(x, k, outs[0], outs[1], positions, table, status)
+    (qp, n_heads, qs, qo, qos), (kp, n_kv_heads, ks, ko, kos) = ends
+    _call("ll_rope", lib.ll_rope, dev, stream, qp, kp, LL_F32 if x.dtype == torch.float32 else LL_BF16,
+          positions.data_ptr(), T, n_heads, n_kv_heads, d, 2 * rows[1], LL_ROPE_LAYOUTS[layout],
+          LL_ROPE_BACKWARD if backward else LL_ROPE_FORWARD, qs, ks, table.data_ptr(), rows[0], qo, ko, qos, kos,
+          status.data_ptr())
+    return outs[0], outs[1]
 
 
 class PoolF8:
@@ -643,7 +654,8 @@ class PoolF8:
             raise ValueError("codes must be [num_blocks, n_kv_heads, block_size, head_dim]")
         _need(k_scale, "k_scale", torch.float32, shape=tuple(k.shape[:2]))
         _need(v_scale, "v_scale", torch.float32, shape=tuple(k.shape[:2]))
-        self.device = _on(k, v, k_scale, v_scale)
+        _on(k, v, k_scale, v_scale)
+        self.device = k.device
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self._c = ll_kv_pool_f8(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), k.shape[0])
 
@@ -688,7 +700,7 @@ def append_to_cache_f8(k, v, pool: PoolF8, block_table, context_lens, cu_new=Non
     if status is None:
         status = new_status(k.device)
     dev = _on(k, v, pool.k, block_table, context_lens, cu_new, status)
-    _call("ll_append_to_cache_f8", dev, stream, k.data_ptr(), v.data_ptr(), ks, vs,
+    _call("ll_append_to_cache_f8", lib.ll_append_to_cache_f8, dev, stream, k.data_ptr(), v.data_ptr(), ks, vs,
           cu_new.data_ptr() if cu_new is not None else None, k.shape[0], context_lens.data_ptr(), B, int(max_new),
           k.shape[1], k.shape[2], pool.block_size, ctypes.byref(pool.c()), block_table.data_ptr(),
           block_table.shape[1], status.data_ptr())
@@ -732,7 +744,7 @@ def paged_attention_decode_f8(q, pool: PoolF8, block_table, context_lens, scale,
     if q.shape[0] != B:
         raise ValueError(f"q must have {B} rows, one per sequence")
     dev = _on(q, pool.k, block_table, context_lens, out, workspace, status)
-    _call("ll_paged_attention_decode_f8", dev, stream, q.data_ptr(), ctypes.byref(pool.c()), block_table.data_ptr(),
+    _call("ll_paged_attention_decode_f8", lib.ll_paged_attention_decode_f8, dev, stream, q.data_ptr(), ctypes.byref(pool.c()), block_table.data_ptr(),
           block_table.shape[1], context_lens.data_ptr(), B, q.shape[1], Hkv, q.shape[2], pool.block_size, float(scale),
           out.data_ptr(), workspace.data_ptr(), workspace.numel(), status.data_ptr())
     return out
@@ -749,7 +761,7 @@ def paged_attention_prefill_f8(q, cu_new, pool: PoolF8, block_table, context_len
         q, pool, out, workspace, status,
         lambda: attention_prefill_f8_workspace_size(B, q.shape[0], max_new, q.shape[1], Hkv, q.shape[2]))
     dev = _on(q, pool.k, cu_new, block_table, context_lens, out, workspace, status)
-    _call("ll_paged_attention_prefill_f8", dev, stream, q.data_ptr(), cu_new.data_ptr(), q.shape[0],
+    _call("ll_paged_attention_prefill_f8", lib.ll_paged_attention_prefill_f8, dev, stream, q.data_ptr(), cu_new.data_ptr(), q.shape[0],
           ctypes.byref(pool.c()), block_table.data_ptr(), block_table.shape[1], context_lens.data_ptr(), B,
           int(max_new), q.shape[1], Hkv, q.shape[2], pool.block_size, float(scale), out.data_ptr(),
           workspace.data_ptr(), workspace.numel(), status.data_ptr())
@@ -769,7 +781,8 @@ class BlockSet:
                 raise ValueError("a BlockSet takes contiguous GPU tensors [num_blocks, ...]")
             if t.shape[0] != self.tensors[0].shape[0]:
                 raise ValueError("the tensors of a BlockSet have the same number of blocks")
-        self.device = _on(*self.tensors)
+        _on(*self.tensors)
+        self.device = self.tensors[0].device
         self.num_blocks = self.tensors[0].shape[0]
         self._c = (ll_block_tensor * len(self.tensors))(
             *((t.data_ptr(), t.numel() // max(self.num_blocks, 1) * t.element_size()) for t in self.tensors))
@@ -789,7 +802,7 @@ def copy_blocks(blocks: BlockSet, pairs, n_pairs=None, status=None, stream=None)
     if status is None:
         status = new_status(blocks.device)
     dev = _on(blocks.tensors[0], pairs, n_pairs, status)
-    _call("ll_copy_blocks", dev, stream, blocks._c, len(blocks.tensors), blocks.num_blocks, pairs.data_ptr(),
+    _call("ll_copy_blocks", lib.ll_copy_blocks, dev, stream, blocks._c, len(blocks.tensors), blocks.num_blocks, pairs.data_ptr(),
           pairs.shape[0], n_pairs.data_ptr() if n_pairs is not None else None, status.data_ptr())
     return status
 
@@ -816,7 +829,7 @@ def compact_blocks(block_table, num_blocks, new_table=None, pairs=None, counts=N
     if status is None:
         status = new_status(dev)
     dev = _on(block_table, new_table, pairs, counts, block_map, status)
-    _call("ll_compact_blocks", dev, stream, block_table.data_ptr(), block_table.shape[0], block_table.shape[1],
+    _call("ll_compact_blocks", lib.ll_compact_blocks, dev, stream, block_table.data_ptr(), block_table.shape[0], block_table.shape[1],
           num_blocks, new_table.data_ptr(), pairs.data_ptr(), counts.data_ptr(), block_map.data_ptr(),
           status.data_ptr())
     return new_table, pairs, counts, block_map
