@@ -28,19 +28,37 @@ LL_DEVINL void unpack8(const uint4& w, float (&v)[8]) {
     v[4] = bf16_lo(w.z); v[5] = bf16_hi(w.z); v[6] = bf16_lo(w.w); v[7] = bf16_hi(w.w);
 }
 
-// largest finite magnitude of 8 BF16: as integers, |x| of a pair at a time; infinities and NaN count 0
-LL_DEVINL uint32_t amax8(const uint4& w) {
-    uint32_t m = 0;
-    const uint32_t p[4] = {w.x, w.y, w.z, w.w};
+// Magnitudes of 16 bits in each half: the larger of each (a NaN loses to a number).
+LL_DEVINL uint32_t max_abs2(uint32_t m, uint32_t x) {
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(m), "r"(x & 0x7fff7fffu));
+    return r;
+}
+// Largest finite magnitude among the N loads, as BF16 bits.  The plain maximum, unless that is an infinity:
+// then the infinities are left out one by one.
+template <int N>
+LL_DEVINL uint32_t amax(const uint4 (&w)[N]) {
+    uint32_t m2 = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t a = p[i] & 0x7fffu, b = (p[i] >> 16) & 0x7fffu;
-        m = max(m, a < 0x7f80u ? a : 0u);
-        m = max(m, b < 0x7f80u ? b : 0u);
+    for (int i = 0; i < N; ++i) m2 = max_abs2(max_abs2(max_abs2(max_abs2(m2, w[i].x), w[i].y), w[i].z), w[i].w);
+    uint32_t m = max(m2 & 0xffffu, m2 >> 16);
+    if (m >= 0x7f80u) {
+        m = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const uint32_t p[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t a = p[j] & 0x7fffu, b = (p[j] >> 16) & 0x7fffu;
+                m = max(m, max(a < 0x7f80u ? a : 0u, b < 0x7f80u ? b : 0u));
+            }
+        }
     }
-    return m;                                           // BF16 bits without the sign
+    return m;
 }
 
+// The codes of x / scale.  A power of two (every scale but one that somebody else wrote) is divided by
+// exactly by a multiplication; IEEE divisions took the chunk kernel twice its time.
 LL_DEVINL uint2 codes8(const uint4& w, float scale) {
     float v[8];
     unpack8(w, v);
@@ -49,8 +67,15 @@ LL_DEVINL uint2 codes8(const uint4& w, float scale) {
         for (int i = 0; i < 8; ++i) v[i] = v[i] != v[i] ? v[i] : 0.f;
         return make_uint2(f32x4_to_e4m3x4(v[0], v[1], v[2], v[3]), f32x4_to_e4m3x4(v[4], v[5], v[6], v[7]));
     }
+    const uint32_t u = __float_as_uint(scale);
+    if ((u & 0x7fffffu) == 0u && (u >> 23) < 254u) {       // 2^e: times 2^-e (both normal)
+        const float inv = __uint_as_float((254u - (u >> 23)) << 23);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __fdiv_rn(v[i], scale);
+        for (int i = 0; i < 8; ++i) v[i] *= inv;
+    } else {
+#pragma unroll 1
+        for (int i = 0; i < 8; ++i) v[i] = __fdiv_rn(v[i], scale);
+    }
     return make_uint2(f32x4_to_e4m3x4(v[0], v[1], v[2], v[3]), f32x4_to_e4m3x4(v[4], v[5], v[6], v[7]));
 }
 
@@ -109,7 +134,8 @@ __global__ void __launch_bounds__(kAppendThreads) append_step_kernel(const Appen
             const size_t bhk = (size_t)blk * a.n_kv_heads + h;
             float* sp = (which ? a.v_scale : a.k_scale) + bhk;
             const float old = off ? *sp : 0.f;
-            uint32_t m = amax8(w);
+            const uint4 one[1] = {w};
+            uint32_t m = amax(one);
             const uint32_t mask = 0xffffu << (threadIdx.x & 16);
 #pragma unroll
             for (int o = 8; o >= 1; o >>= 1) m = max(m, __shfl_xor_sync(mask, m, o));
@@ -159,27 +185,25 @@ __global__ void __launch_bounds__(kAppendThreads) append_chunk_kernel(const Appe
     const int lo = max(s.p0 - j * bs, 0), hi = min(s.p0 + s.n - j * bs, bs);   // its new rows
     if (lo >= hi) return;
     const int blk = a.block_table[(size_t)b * a.max_blocks + j];
-    if (blk < 0 || blk >= a.num_blocks) {
-        if (threadIdx.x == 0 && blockIdx.y == 0) flag_status(a.status, LL_DEV_BAD_BLOCK);
-        return;
-    }
     const long long stride = which ? a.v_stride : a.k_stride;
     const int l = threadIdx.x % LANES, r0 = threadIdx.x / LANES;
     // row r of the block is token start + (j bs + r - p0)
     const __nv_bfloat16* x = (which ? a.v : a.k) + ((long long)s.start + (long long)j * bs - s.p0) * stride +
                              (size_t)h * D + l * 8;
-    const size_t bhk = (size_t)blk * a.n_kv_heads + h;
-    float* sp = (which ? a.v_scale : a.k_scale) + bhk;
-    const float old = lo ? *sp : 0.f;
     uint4 w[PASSES];
 #pragma unroll
     for (int i = 0; i < PASSES; ++i) {
         const int r = lo + r0 + i * ROWS;
         w[i] = r < hi ? *reinterpret_cast<const uint4*>(x + (long long)r * stride) : make_uint4(0, 0, 0, 0);
     }
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < PASSES; ++i) m = max(m, amax8(w[i]));
+    if (blk < 0 || blk >= a.num_blocks) {                   // (looked at behind the loads, which do not need it)
+        if (threadIdx.x == 0 && blockIdx.y == 0) flag_status(a.status, LL_DEV_BAD_BLOCK);
+        return;
+    }
+    const size_t bhk = (size_t)blk * a.n_kv_heads + h;
+    float* sp = (which ? a.v_scale : a.k_scale) + bhk;
+    const float old = lo ? *sp : 0.f;
+    uint32_t m = amax(w);
     m = __reduce_max_sync(0xffffffffu, m);
     if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = m;
     __syncthreads();                                        // also: every thread has read the old scale

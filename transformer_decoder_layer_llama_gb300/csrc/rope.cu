@@ -217,12 +217,15 @@ cudaError_t rope_for(const RopeArgs& a, cudaStream_t stream) {
     if (vec) {
         const int lanes_rot = a.interleaved ? a.rotary_dim / N : a.rotary_dim / (2 * N);
         const int lanes = lanes_rot + (a.copy_tail ? (a.head_dim - a.rotary_dim) / N : 0);
-        const int rows = std::min(kRopeThreads / lanes, H);
-        const int threads = (rows * lanes + 31) / 32 * 32;
         // Few tokens: one head per thread spreads them over the most CTAs.  Many: four heads per
         // thread keep more loads in flight and read each table row less often.
         const bool wide = (long long)a.tokens * H * lanes > 4LL * 2048 * std::max(1, device_sm_count());
-        const dim3 grid((unsigned)a.tokens, (unsigned)((H + rows * (wide ? 4 : 1) - 1) / (rows * (wide ? 4 : 1))));
+        // head rows of a CTA: as even a split of the heads as the CTA's threads allow
+        const int u = wide ? 4 : 1, most = std::max(1, kRopeThreads / lanes);
+        const int parts = (H + u * most - 1) / (u * most);
+        const int rows = (H + u * parts - 1) / (u * parts);
+        const int threads = (rows * lanes + 31) / 32 * 32;
+        const dim3 grid((unsigned)a.tokens, (unsigned)parts);
         if (a.interleaved)
             e = wide ? launch_pdl(rope_vec_kernel<T, false, 4>, grid, dim3(threads), 0, stream, 1, a, lanes_rot, lanes, rows)
                      : launch_pdl(rope_vec_kernel<T, false, 1>, grid, dim3(threads), 0, stream, 1, a, lanes_rot, lanes, rows);
