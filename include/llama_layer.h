@@ -469,6 +469,26 @@ int ll_paged_attention_prefill_f8(const void* q, const int32_t* cu_new, int32_t 
                                   int32_t block_size, float scale, void* out, void* workspace, size_t workspace_bytes,
                                   int32_t* status, void* stream);
 
+/* Workspace bytes for layer calls over an e4m3 pool (max_tokens and max_blocks as
+ * for ll_workspace_size; the checkpoints of ll_workspace_checkpoints hold in it). */
+size_t ll_workspace_size_f8(const ll_config* cfg, int32_t max_tokens, int32_t max_blocks);
+
+/* ll_layer_prefill over an e4m3 pool: every sequence's seq_len new tokens take its
+ * last positions, context_lens[b] - seq_len .. context_lens[b] - 1 (a prompt, a
+ * chunk behind a cached prefix, or a few tokens).  Their K and V go into the pool
+ * as ll_append_to_cache_f8 does, the attention is ll_paged_attention_prefill_f8's.
+ * x and y as ll_layer_prefill. */
+int ll_layer_prefill_f8(const ll_config* cfg, const void* packed, const void* x, const int32_t* context_lens, int32_t batch,
+                        int32_t seq_len, const ll_kv_pool_f8* pool, const int32_t* block_table, int32_t max_blocks, void* y,
+                        void* workspace, size_t workspace_bytes, int32_t* status, void* stream);
+
+/* ll_layer_decode_step over an e4m3 pool (ll_append_to_cache_f8 and
+ * ll_paged_attention_decode_f8); the other arguments as there, workspace from
+ * ll_workspace_size_f8. */
+int ll_layer_decode_step_f8(const ll_config* cfg, const void* packed, const void* x, const ll_kv_pool_f8* pool,
+                            const int32_t* block_table, int32_t max_blocks, const int32_t* context_lens, int32_t batch,
+                            void* y, void* workspace, size_t workspace_bytes, int32_t* status, void* stream);
+
 /* One tensor of a pool whose first dimension is the physical block: K or V codes,
  * or their scales, of one layer. */
 typedef struct {

@@ -264,3 +264,72 @@ def test_binding_refuses_cpu_tensors_and_wrong_types():
         api.BlockSet([codes])
     with pytest.raises(ValueError, match="GPU"):
         api.compact_blocks(torch.zeros(2, 2, dtype=torch.int32), 8)
+
+
+# ---------------------------------------------------------------- the serving side
+
+def test_shared_blocks_are_freed_with_their_last_holder():
+    from transformer_decoder_layer_llama_gb300.serving import BlockAllocator
+    a = BlockAllocator(8, seed=1)
+    x = a.alloc(3)
+    a.share(x[:2])
+    assert [a.holders(b) for b in x] == [2, 2, 1]
+    a.free(x)
+    assert a.free_count() == 6 and a.holders(x[0]) == 1
+    a.free(x[:2])
+    assert a.free_count() == 8
+    with pytest.raises(ValueError):
+        a.share([x[0]])
+    with pytest.raises(ValueError):
+        a.free([x[0]])
+
+
+def test_fork_retire_and_compaction_keep_the_books():
+    from transformer_decoder_layer_llama_gb300.serving import BlockAllocator, Scheduler
+    nb, bs = 30, 16
+    sch = Scheduler(4, bs, 6, BlockAllocator(nb, seed=3), seed=1)
+    sch.start_resident(0, 40)
+    sch.start_resident(1, 32)
+    pairs = sch.fork(0, 2)                   # 2 full blocks shared, the third copied
+    r0, r2 = sch.slots[0], sch.slots[2]
+    assert r2.blocks[:2] == r0.blocks[:2] and pairs == [(r0.blocks[2], r2.blocks[2])] and r2.ctx == 40
+    assert sch.fork(1, 3) == []              # 32 = 2 full blocks: nothing is filling
+    assert sch.alloc.free_count() == nb - 6
+    with pytest.raises(ValueError):
+        sch.fork(0, 1)
+    sch.retire(0)
+    assert sch.alloc.free_count() == nb - 5 and sch.alloc.holders(r2.blocks[0]) == 1 and (sch.table[0] == -1).all()
+    with pytest.raises(ValueError):
+        sch.fork(0, 0)
+    new, moves, U, block_map = C.compact(sch.table, nb)
+    sch.apply_map(block_map)
+    assert (sch.table == new).all() and U == 5
+    used = {b for r in sch.slots if r is not None for b in r.blocks}
+    assert used == set(range(5)) and sch.alloc.alloc(1) == [5]
+    assert sch.alloc.holders(sch.slots[1].blocks[0]) == 2
+
+
+LAYER_F8 = dict(cfg=None, packed=FAKE, x=FAKE, ctx=FAKE, batch=2, seq_len=4, pool=pool_f8(), table=FAKE, max_blocks=4,
+                y=2 * FAKE, ws=FAKE, ws_bytes=1 << 40, status=FAKE)
+
+
+@pytest.mark.parametrize("bad,code", [(dict(packed=0), INVALID), (dict(x=0), INVALID), (dict(ctx=0), INVALID),
+                                      (dict(table=0), INVALID), (dict(y=0), INVALID), (dict(y=FAKE), INVALID),
+                                      (dict(status=0), INVALID), (dict(batch=0), INVALID), (dict(seq_len=0), INVALID),
+                                      (dict(pool=pool_f8(k_scale=0)), INVALID), (dict(pool=pool_f8(v=FAKE + 4)), INVALID),
+                                      (dict(batch=70000), UNSUPPORTED), (dict(max_blocks=1 << 27), UNSUPPORTED),
+                                      (dict(seq_len=1 << 24), UNSUPPORTED), (dict(ws=0), WORKSPACE), (dict(ws_bytes=100), WORKSPACE)])
+def test_layer_f8_refusals(bad, code):
+    cfg = api.make_config(synth.DIMS_TINY, 128)
+    a = {**LAYER_F8, **bad, "cfg": ctypes.byref(cfg)}
+    a["pool"] = ctypes.byref(a["pool"])
+    assert api.lib.ll_layer_prefill_f8(*a.values(), NULL) == code
+    if "seq_len" not in bad:
+        order = ("cfg", "packed", "x", "pool", "table", "max_blocks", "ctx", "batch", "y", "ws", "ws_bytes", "status")
+        assert api.lib.ll_layer_decode_step_f8(*(a[k] for k in order), NULL) == code
+
+
+def test_layer_f8_workspace_holds_the_fused_one():
+    cfg = api.make_config(synth.DIMS_70B, 4096)
+    assert api.lib.ll_workspace_size_f8(ctypes.byref(cfg), 64, 16) > api.workspace_size(cfg, 64, 16)
+    assert api.lib.ll_workspace_size_f8(ctypes.byref(cfg), 0, 16) == 0

@@ -18,7 +18,8 @@ import pytest
 import torch
 
 from oracle import cache_ops as C
-from tests.helpers import f64
+from oracle import llama_layer as O
+from tests.helpers import assert_close, bits, f64
 from transformer_decoder_layer_llama_gb300 import synth
 
 pytestmark = pytest.mark.gpu
@@ -401,7 +402,8 @@ PREFILL_CASES = [  # block, heads, kv_heads, dim, contexts before, new tokens
     (16, 4, 2, 64, [0], [1]), (16, 4, 2, 64, [0, 10, 0], [64, 5, 17]), (128, 4, 4, 128, [0], [300]),
     (128, 16, 2, 128, [100, 0, 1], [129, 1, 40]), (64, 16, 1, 128, [500], [33]), (256, 5, 1, 128, [0, 255], [128, 2]),
     (32, 3, 1, 64, [0, 0, 7], [0, 130, 0]), (16, 7, 7, 128, [2000], [3]), (16, 14, 2, 64, [129], [255]),
-    (128, 9, 1, 128, [30], [60]), (32, 8, 8, 64, [0, 96], [127, 128])]
+    (128, 9, 1, 128, [30], [60]), (32, 8, 8, 64, [0, 96], [127, 128]), (16, 1, 1, 128, [1000], [200]),
+    (256, 16, 1, 64, [3000], [5]), (128, 8, 2, 128, [1500, 0], [1, 700]), (64, 2, 2, 64, [2500], [257])]
 
 
 @pytest.mark.parametrize("case", PREFILL_CASES)
@@ -641,3 +643,125 @@ def test_a_served_batch_from_prompt_to_compaction():
     for b, w in ((0, y0[0]), (2, y0[2])):
         assert (np.abs(f64(z[b]) - f64(w)) <= 2.0 ** -7 * np.abs(f64(w)) + 1e-3).all()
     assert (z[1] == 0).all()
+
+
+# ---------------------------------------------------------------- the layer and the stack over it
+
+DIMS_128 = synth.LayerDims(512, 8, 2, 128, 1024, 32)
+
+
+@pytest.mark.parametrize("d", [synth.DIMS_TINY, DIMS_128])
+def test_layer_over_an_e4m3_pool(d):
+    """A prompt, a chunk behind it and decode steps: codes and scales exact for the layer's own K and V (a BF16
+    pool fed the same tokens holds them), the attention within its bound of the definition on the layer's q and
+    codes, the output within the layer's bound of the definition from there."""
+    B, nb, mb = 3, 40, 8
+    W = synth.make_weights(d, 0.02, seed=11)
+    Wn = {k: f64(v) for k, v in W.items()}
+    cfg = api.make_config(d, max_position=mb * d.block_size)
+    packed = api.pack_weights(cfg, {k: v.cuda() for k, v in W.items()})
+    table = np.random.default_rng(5).permutation(nb)[:B * mb].reshape(B, mb).astype(np.int32)
+    pool = api.PoolF8.empty(nb, d.n_kv_heads, d.block_size, d.head_dim)
+    kp, vp = (t.cuda() for t in synth.make_pool(nb, d, seed=3))
+    ref = C.PoolF8(*(np.zeros(tuple(pool.k.shape), np.uint8) for _ in range(2)),
+                   *(np.zeros(tuple(pool.k_scale.shape)) for _ in range(2)))
+    st, done = status(), 0
+    for n in (37, 20, 1, 1):
+        ctx = [done + n] * B
+        T = B * n
+        x = synth.make_x(T, d.hidden, seed=100 + done).cuda()
+        pos = np.tile(np.arange(done, done + n), B)
+        api.layer_prefill(cfg, packed, x, dev(pos), B, n, kp, vp, dev(table), status=st)
+        ws = api.new_workspace_f8(cfg, T, mb)
+        if n == 1:
+            y = api.layer_decode_step_f8(cfg, packed, x, pool, dev(table), dev(ctx), workspace=ws, status=st)
+        else:
+            y = api.layer_prefill_f8(cfg, packed, x, pool, dev(table), dev(ctx), n, workspace=ws, status=st)
+        check(st)
+        cp = api.checkpoints(cfg, ws, T, mb, T)
+        cu = np.arange(B + 1) * n
+        at = table[np.repeat(np.arange(B), n), pos // d.block_size]
+        k, v = (f64(t)[at, :, pos % d.block_size] for t in (kp, vp))
+        ref.append(k, v, table, ctx, cu)
+        assert_pool(pool, ref)
+        q = f64(cp["q"]).reshape(T, d.n_heads, d.head_dim)
+        assert_attention(cp["o"].view(T, d.n_heads, d.head_dim), *C.attention_f8(q, ref, table, ctx, cu, d.head_dim ** -0.5),
+                         d.head_dim)
+        h = f64(x) + f64(cp["o"]) @ Wn["w_o"].T
+        hh = O.bf16_round(O.rmsnorm(h, Wn["g_ffn"], d.rms_eps))
+        a = O.bf16_round(O.silu(hh @ Wn["w_gate"].T) * (hh @ Wn["w_up"].T))
+        assert_close(f64(y), h + a @ Wn["w_down"].T, f"after {done + n} tokens")
+        done += n
+
+
+def test_layer_f8_flags_contexts_shorter_than_the_new_tokens():
+    d, B = synth.DIMS_TINY, 2
+    cfg = api.make_config(d, max_position=64)
+    packed = api.pack_weights(cfg, {k: v.cuda() for k, v in synth.make_weights(d, 0.02, seed=1).items()})
+    pool = api.PoolF8.empty(8, d.n_kv_heads, d.block_size, d.head_dim)
+    before = pool.k.view(torch.uint8).clone()
+    x = synth.make_x(B * 4, d.hidden, seed=2).cuda()
+    st = status()
+    api.layer_prefill_f8(cfg, packed, x, pool, dev([[0, 1], [2, 3]]), dev([3, 4]), 4, status=st)
+    torch.cuda.synchronize()
+    assert int(st.item()) & api.LL_DEV_BAD_POSITION
+    assert torch.equal(pool.k.view(torch.uint8)[:2], before[:2]) and (pool.k_scale[2] > 0).all()
+    # a context beyond the RoPE table is not written either
+    st = status()
+    api.layer_decode_step_f8(cfg, packed, x[:2], pool, dev([[4, 5, 6, 7, 0], [4, 5, 6, 7, 1]]), dev([65, 0]), status=st)
+    torch.cuda.synchronize()
+    assert int(st.item()) & api.LL_DEV_BAD_POSITION and (pool.k_scale[:2] == 0).all()
+    with pytest.raises(ValueError):
+        api.layer_prefill_f8(cfg, packed, x, api.PoolF8.empty(8, d.n_kv_heads, 32, d.head_dim), dev([[0, 1], [2, 3]]), dev([4, 4]), 4)
+
+
+@pytest.mark.parametrize("f8", [False, True])
+def test_stack_forks_and_compacts(f8):
+    """A two-layer stack: a forked request answers as its parent does, and packing the pools changes no answer."""
+    from transformer_decoder_layer_llama_gb300.serving import BlockAllocator, Scheduler, StackEngine
+    d, L, nb, mb, slots, prompt = synth.DIMS_TINY, 2, 40, 8, 3, 24
+    cfg = api.make_config(d, max_position=mb * d.block_size)
+    packed = [api.pack_weights(cfg, {k: v.cuda() for k, v in synth.make_weights(d, 0.02, seed=100 + l).items()}) for l in range(L)]
+    pools = [api.PoolF8.empty(nb, d.n_kv_heads, d.block_size, d.head_dim) if f8 else
+             tuple(t.cuda() for t in synth.make_pool(nb, d, seed=l)) for l in range(L)]
+    sch = Scheduler(slots, d.block_size, mb, BlockAllocator(nb, seed=5), seed=6, prompt_len=prompt)
+    eng = StackEngine(api, [cfg] * L, packed, pools, slots, mb, slots * prompt)
+    stream = torch.cuda.Stream()
+    torch.cuda.set_stream(stream)
+    try:
+        for s in (0, 1):
+            sch.start_resident(s, prompt)
+        eng.pf_table[:2].copy_(torch.from_numpy(sch.table[:2]))
+        eng.pf_ctx[:2].copy_(dev([prompt, prompt]))
+        eng.pf_pos[:2 * prompt].copy_(dev(np.tile(np.arange(prompt), 2)))
+        eng.pf_x[:2 * prompt].copy_(synth.make_x(2 * prompt, d.hidden, seed=1))
+        eng.prefill(2, prompt, stream)
+        eng.copy_blocks(sch.fork(0, 2), stream)
+
+        def step(seed):
+            ctx = sch.grow_for_decode()
+            x = synth.make_x(slots, d.hidden, seed=seed)
+            x[2] = x[0]
+            eng.table.copy_(torch.from_numpy(sch.table))
+            eng.ctx.copy_(torch.from_numpy(ctx))
+            eng.x.copy_(x)
+            return eng.decode(stream).clone()
+
+        for i in range(12):                   # over a block's end
+            y = step(10 + i)
+            assert torch.equal(y[0], y[2]) and not torch.equal(y[0], y[1])
+        sch.retire(1)
+        sch.start_resident(1, 5)              # leaves holes behind
+        sch.retire(1)
+        moved = eng.compact(sch, stream)
+        sch.start_resident(1, 1)
+        live = [b for s in (0, 2) for b in sch.slots[s].blocks]
+        assert moved > 0 and max(live) < len(set(live)) and sorted(set(live)) == list(range(len(set(live))))
+        eng.table.copy_(torch.from_numpy(sch.table))
+        eng.ctx[1] = 1
+        again = eng.decode(stream)            # the same step once more, from the packed pool
+        assert torch.equal(again[0], y[0]) and torch.equal(again[2], y[2])
+        torch.cuda.synchronize()
+        assert int(eng.status.item()) == 0
+    finally:
+        torch.cuda.set_stream(torch.cuda.default_stream())

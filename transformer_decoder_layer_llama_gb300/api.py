@@ -48,7 +48,7 @@ EXPORTED = [
     "ll_rope_table_size", "ll_rope_table", "ll_pack_rope", "ll_rope", "ll_append_to_cache_f8",
     "ll_attention_decode_f8_workspace_size", "ll_paged_attention_decode_f8",
     "ll_attention_prefill_f8_workspace_size", "ll_paged_attention_prefill_f8", "ll_copy_blocks",
-    "ll_compact_blocks",
+    "ll_compact_blocks", "ll_workspace_size_f8", "ll_layer_prefill_f8", "ll_layer_decode_step_f8",
 ]
 
 
@@ -158,6 +158,9 @@ def _load():
         "ll_attention_prefill_f8_workspace_size": (S, [I32, I32, I32, I32, I32, I32]),
         "ll_paged_attention_prefill_f8": (ctypes.c_int, [P, P, I32, poolf8, P, I32, P, I32, I32, I32, I32, I32, I32,
                                                          ctypes.c_float, P, P, S, P, P]),
+        "ll_workspace_size_f8": (S, [cfgp, I32, I32]),
+        "ll_layer_prefill_f8": (ctypes.c_int, [cfgp, P, P, P, I32, I32, poolf8, P, I32, P, P, S, P, P]),
+        "ll_layer_decode_step_f8": (ctypes.c_int, [cfgp, P, P, poolf8, P, I32, P, I32, P, P, S, P, P]),
         "ll_copy_blocks": (ctypes.c_int, [ctypes.POINTER(ll_block_tensor), I32, I32, P, I32, P, P, P]),
         "ll_compact_blocks": (ctypes.c_int, [P, I32, I32, I32, P, P, P, P, P, P]),
     }
@@ -766,6 +769,56 @@ def paged_attention_prefill_f8(q, cu_new, pool: PoolF8, block_table, context_len
           int(max_new), q.shape[1], Hkv, q.shape[2], pool.block_size, float(scale), out.data_ptr(),
           workspace.data_ptr(), workspace.numel(), status.data_ptr())
     return out
+
+
+def new_workspace_f8(cfg, max_tokens, max_blocks, device=None):
+    """A workspace for layer calls over an e4m3 pool of up to max_tokens tokens."""
+    n = lib.ll_workspace_size_f8(ctypes.byref(cfg), int(max_tokens), int(max_blocks))
+    if n == 0:
+        raise LayerError("ll_workspace_size_f8", LL_ERR_INVALID_ARG)
+    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def _layer_f8(cfg, packed, x, pool, block_table, context_lens, tokens, y, workspace, status):
+    _need(packed, "packed", torch.uint8)
+    _need(x, "x", torch.bfloat16, shape=(tokens, cfg.hidden))
+    if tuple(pool.k.shape[1:]) != (cfg.n_kv_heads, cfg.block_size, cfg.head_dim):
+        raise ValueError(f"the pool must be [num_blocks, {cfg.n_kv_heads}, {cfg.block_size}, {cfg.head_dim}]")
+    if y is None:
+        y = torch.empty_like(x)
+    else:
+        _need(y, "y", torch.bfloat16, shape=(tokens, cfg.hidden))
+    if workspace is None:
+        workspace = new_workspace_f8(cfg, tokens, block_table.shape[1], x.device)
+    else:
+        _need(workspace, "workspace", torch.uint8)
+    if status is None:
+        status = new_status(x.device)
+    return y, workspace, status, _on(x, packed, pool.k, block_table, context_lens, y, workspace, status)
+
+
+def layer_prefill_f8(cfg, packed, x, pool: PoolF8, block_table, context_lens, seq_len, y=None, workspace=None,
+                     status=None, stream=None):
+    """ll_layer_prefill_f8: x BF16 [batch * seq_len, hidden], each sequence's seq_len new tokens at its last
+    positions.  Returns y."""
+    B = _f8_batch(pool, block_table, context_lens)
+    y, workspace, status, dev = _layer_f8(cfg, packed, x, pool, block_table, context_lens, B * int(seq_len), y,
+                                          workspace, status)
+    _call("ll_layer_prefill_f8", lib.ll_layer_prefill_f8, dev, stream, ctypes.byref(cfg), packed.data_ptr(),
+          x.data_ptr(), context_lens.data_ptr(), B, int(seq_len), ctypes.byref(pool.c()), block_table.data_ptr(),
+          block_table.shape[1], y.data_ptr(), workspace.data_ptr(), workspace.numel(), status.data_ptr())
+    return y
+
+
+def layer_decode_step_f8(cfg, packed, x, pool: PoolF8, block_table, context_lens, y=None, workspace=None, status=None,
+                         stream=None):
+    """ll_layer_decode_step_f8: x BF16 [batch, hidden], one new token per sequence.  Returns y."""
+    B = _f8_batch(pool, block_table, context_lens)
+    y, workspace, status, dev = _layer_f8(cfg, packed, x, pool, block_table, context_lens, B, y, workspace, status)
+    _call("ll_layer_decode_step_f8", lib.ll_layer_decode_step_f8, dev, stream, ctypes.byref(cfg), packed.data_ptr(),
+          x.data_ptr(), ctypes.byref(pool.c()), block_table.data_ptr(), block_table.shape[1], context_lens.data_ptr(),
+          B, y.data_ptr(), workspace.data_ptr(), workspace.numel(), status.data_ptr())
+    return y
 
 
 class BlockSet:

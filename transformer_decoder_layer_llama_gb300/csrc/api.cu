@@ -142,6 +142,26 @@ WsLayout ws_layout(const ll_config* c, int T, int max_blocks, int mode = LL_MODE
     return L;
 }
 
+// Workspace of a layer call over an e4m3 pool: the fused layer's, then the attention's partials and the new
+// tokens' positions and row offsets.
+struct WsF8Layout {
+    WsLayout base;
+    size_t attn, pos, cu, total;
+};
+
+WsF8Layout ws_f8_layout(const ll_config* c, int T, int max_blocks) {
+    WsF8Layout L{};
+    L.base = ws_layout(c, T, max_blocks);
+    size_t at = L.base.total;
+    L.attn = at;
+    at = align_up(at + std::max(ll::attn_decode_f8_scratch_bytes(T, c->n_heads, c->n_kv_heads, c->head_dim),
+                                ll::attn_prefill_f8_scratch_bytes(c->head_dim)));
+    L.pos = at; at = align_up(at + (size_t)T * 4);
+    L.cu = at;  at = align_up(at + ((size_t)T + 1) * 4);
+    L.total = at;
+    return L;
+}
+
 bool mode_ok(int mode) { return mode == LL_MODE_FUSED || mode == LL_MODE_STEP_BY_STEP; }
 
 thread_local char g_last_error[512];
@@ -154,9 +174,10 @@ int run_layer(const ll_config* cfg, const void* packed, const void* x, const int
               const int32_t* context_lens, int T, int seq_len, int batch, const ll_kv_pool* pool,
               const int32_t* block_table, int max_blocks, void* y, void* workspace,
               size_t workspace_bytes, int32_t* status, cudaStream_t stream, bool decode,
-              const ll_kv_pool_q8* pq8 = nullptr) {
+              const ll_kv_pool_q8* pq8 = nullptr, const ll_kv_pool_f8* pf8 = nullptr) {
     WsLayout L = ws_layout(cfg, T, max_blocks);
-    if (!workspace || workspace_bytes < L.total || !aligned16(workspace)) return LL_ERR_WORKSPACE;
+    const WsF8Layout LF = pf8 ? ws_f8_layout(cfg, T, max_blocks) : WsF8Layout{};
+    if (!workspace || workspace_bytes < (pf8 ? LF.total : L.total) || !aligned16(workspace)) return LL_ERR_WORKSPACE;
     Packed P = packed_view(cfg, packed);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     auto* xh = reinterpret_cast<__nv_bfloat16*>(ws + L.xh);
@@ -173,8 +194,15 @@ int run_layer(const ll_config* cfg, const void* packed, const void* x, const int
     const int nq = cfg->n_heads * d;
     const int nqkv = (cfg->n_heads + 2 * cfg->n_kv_heads) * d;
 
-    cudaError_t e = ll::launch_rmsnorm(xb, P.g_attn, xh, T, H, cfg->rms_eps, counters,
-                                       4 * L.counter_words, stream);
+    cudaError_t e;
+    int32_t* cu_new = nullptr;
+    if (pf8 && !decode) {
+        auto* pos = reinterpret_cast<int32_t*>(ws + LF.pos);
+        cu_new = reinterpret_cast<int32_t*>(ws + LF.cu);
+        if ((e = ll::launch_f8_positions(context_lens, batch, seq_len, pos, cu_new, stream)) != cudaSuccess) return LL_ERR_CUDA;
+        positions = pos;
+    }
+    e = ll::launch_rmsnorm(xb, P.g_attn, xh, T, H, cfg->rms_eps, counters, 4 * L.counter_words, stream);
     if (e != cudaSuccess) return LL_ERR_CUDA;
 
     GemmProblem g{};
@@ -198,12 +226,12 @@ int run_layer(const ll_config* cfg, const void* packed, const void* x, const int
     g.ep.block_table = block_table;
     g.ep.max_blocks = max_blocks;
     g.ep.seq_len = seq_len;
-    if (pq8) {
-        // K/V go to staging rows, then into the INT8 pool with their scales
+    if (pq8 || pf8) {
+        // K/V go to staging rows, then into the 8-bit pool with their scales
         g.ep.kv_stage = 1;
         g.ep.k_pool = reinterpret_cast<__nv_bfloat16*>(ws + L.kst);
         g.ep.v_pool = reinterpret_cast<__nv_bfloat16*>(ws + L.vst);
-        g.ep.num_blocks = pq8->num_blocks;
+        g.ep.num_blocks = pq8 ? pq8->num_blocks : pf8->num_blocks;
         g.ep.block_size = 1;
     } else {
         g.ep.k_pool = static_cast<__nv_bfloat16*>(pool->k);
@@ -225,9 +253,55 @@ int run_layer(const ll_config* cfg, const void* packed, const void* x, const int
                                              pq8->num_blocks, status, stream)) != cudaSuccess)
         return LL_ERR_CUDA;
 
-    // attention
     const float scale = 1.0f / std::sqrt((float)d);
-    if (!decode) {
+    if (pf8) {
+        // cache write, then attention
+        ll::AppendArgs ap{};
+        ap.k = g.ep.k_pool;
+        ap.v = g.ep.v_pool;
+        ap.k_stride = ap.v_stride = (long long)cfg->n_kv_heads * d;
+        ap.cu_new = cu_new;
+        ap.context_lens = context_lens;
+        ap.block_table = block_table;
+        ap.k_pool = static_cast<uint8_t*>(pf8->k);
+        ap.v_pool = static_cast<uint8_t*>(pf8->v);
+        ap.k_scale = pf8->k_scale;
+        ap.v_scale = pf8->v_scale;
+        ap.tokens = T;
+        ap.batch = batch;
+        ap.max_new = seq_len;
+        ap.n_kv_heads = cfg->n_kv_heads;
+        ap.head_dim = d;
+        ap.block_size = cfg->block_size;
+        ap.num_blocks = pf8->num_blocks;
+        ap.max_blocks = max_blocks;
+        ap.max_context = std::min(max_blocks * cfg->block_size, cfg->max_position);
+        ap.status = status;
+        if ((e = ll::launch_append_f8(ap, stream)) != cudaSuccess) return LL_ERR_CUDA;
+        ll::AttnF8Args at{};
+        at.q = q;
+        at.k_pool = ap.k_pool;
+        at.v_pool = ap.v_pool;
+        at.k_scale = ap.k_scale;
+        at.v_scale = ap.v_scale;
+        at.cu_new = cu_new;
+        at.context_lens = context_lens;
+        at.block_table = block_table;
+        at.tokens = T;
+        at.batch = batch;
+        at.max_new = seq_len;
+        at.max_blocks = max_blocks;
+        at.num_blocks = pf8->num_blocks;
+        at.block_size = cfg->block_size;
+        at.n_heads = cfg->n_heads;
+        at.n_kv_heads = cfg->n_kv_heads;
+        at.head_dim = d;
+        at.scale = scale;
+        at.out = o;
+        at.status = status;
+        e = decode ? ll::launch_attn_decode_f8(at, ws + LF.attn, stream) : ll::launch_attn_prefill_f8(at, ws + LF.attn, stream);
+        if (e != cudaSuccess) return LL_ERR_CUDA;
+    } else if (!decode) {
         ll::AttnPrefillArgs at{};
         at.q = q;
         at.k_pool = g.ep.k_pool;
@@ -776,6 +850,49 @@ int ll_layer_decode_step_q8(const ll_config* cfg, const void* packed, const void
     if (!aligned16(packed) || !aligned16(x) || !aligned16(y)) return LL_ERR_INVALID_ARG;
     return run_layer(cfg, packed, x, nullptr, context_lens, batch, 1, batch, nullptr, block_table, max_blocks, y,
                      workspace, workspace_bytes, status, static_cast<cudaStream_t>(stream), true, pool);
+}
+
+size_t ll_workspace_size_f8(const ll_config* cfg, int32_t max_tokens, int32_t max_blocks) {
+    if (config_supported(cfg) != LL_OK || max_tokens <= 0 || max_blocks <= 0) return 0;
+    return ws_f8_layout(cfg, max_tokens, max_blocks).total;
+}
+
+namespace {
+int layer_f8_args(const ll_config* cfg, const void* packed, const void* x, const int32_t* context_lens, int32_t batch,
+                  int32_t seq_len, const ll_kv_pool_f8* pool, const int32_t* block_table, int32_t max_blocks, const void* y,
+                  const int32_t* status) {
+    const int rc = config_supported(cfg);
+    if (rc != LL_OK) return rc;
+    if (!packed || !x || !context_lens || !block_table || !y || !status || !pool || !pool->k || !pool->v ||
+        !pool->k_scale || !pool->v_scale || pool->num_blocks <= 0 || !aligned16(pool->k) || !aligned16(pool->v))
+        return LL_ERR_INVALID_ARG;
+    if (batch <= 0 || seq_len <= 0 || max_blocks <= 0 || x == y) return LL_ERR_INVALID_ARG;
+    if (!aligned16(packed) || !aligned16(x) || !aligned16(y)) return LL_ERR_INVALID_ARG;
+    if ((long long)batch * seq_len > (1 << 24) || batch > 65535 || cfg->n_kv_heads > 32767) return LL_ERR_UNSUPPORTED;
+    if ((long long)max_blocks * cfg->block_size > (1LL << 30)) return LL_ERR_UNSUPPORTED;
+    if ((long long)pool->num_blocks * cfg->n_kv_heads * cfg->block_size > (1LL << 31) - 1) return LL_ERR_UNSUPPORTED;
+    return LL_OK;
+}
+}  // namespace
+
+int ll_layer_prefill_f8(const ll_config* cfg, const void* packed, const void* x, const int32_t* context_lens, int32_t batch,
+                        int32_t seq_len, const ll_kv_pool_f8* pool, const int32_t* block_table, int32_t max_blocks, void* y,
+                        void* workspace, size_t workspace_bytes, int32_t* status, void* stream) {
+    ll::clear_last_error();
+    const int rc = layer_f8_args(cfg, packed, x, context_lens, batch, seq_len, pool, block_table, max_blocks, y, status);
+    if (rc != LL_OK) return rc;
+    return run_layer(cfg, packed, x, nullptr, context_lens, batch * seq_len, seq_len, batch, nullptr, block_table, max_blocks,
+                     y, workspace, workspace_bytes, status, static_cast<cudaStream_t>(stream), false, nullptr, pool);
+}
+
+int ll_layer_decode_step_f8(const ll_config* cfg, const void* packed, const void* x, const ll_kv_pool_f8* pool,
+                            const int32_t* block_table, int32_t max_blocks, const int32_t* context_lens, int32_t batch,
+                            void* y, void* workspace, size_t workspace_bytes, int32_t* status, void* stream) {
+    ll::clear_last_error();
+    const int rc = layer_f8_args(cfg, packed, x, context_lens, batch, 1, pool, block_table, max_blocks, y, status);
+    if (rc != LL_OK) return rc;
+    return run_layer(cfg, packed, x, nullptr, context_lens, batch, 1, batch, nullptr, block_table, max_blocks, y, workspace,
+                     workspace_bytes, status, static_cast<cudaStream_t>(stream), true, nullptr, pool);
 }
 
 int ll_paged_attention_decode(const void* q, const ll_kv_pool* pool, const int32_t* block_table,

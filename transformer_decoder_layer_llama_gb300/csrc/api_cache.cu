@@ -224,6 +224,7 @@ int ll_append_to_cache_f8(const void* k, const void* v, int64_t k_stride, int64_
     a.block_size = block_size;
     a.num_blocks = pool->num_blocks;
     a.max_blocks = max_blocks;
+    a.max_context = max_blocks * block_size;
     a.status = status;
     return cuda_rc(ll::launch_append_f8(a, static_cast<cudaStream_t>(stream)));
 }

@@ -218,9 +218,13 @@ struct AppendArgs {
     uint8_t *k_pool, *v_pool;
     float *k_scale, *v_scale;
     int tokens, batch, max_new, n_kv_heads, head_dim, block_size, num_blocks, max_blocks;
+    int max_context;               // contexts beyond it count as bad
     int32_t* status;
 };
 cudaError_t launch_append_f8(const AppendArgs& a, cudaStream_t stream);
+// Positions of seq_len new tokens at each context's end, and their cu_new [batch + 1].
+cudaError_t launch_f8_positions(const int32_t* context_lens, int batch, int seq_len, int32_t* positions, int32_t* cu_new,
+                                cudaStream_t stream);
 
 struct AttnF8Args {
     const __nv_bfloat16* q;        // [tokens][n_heads][head_dim]

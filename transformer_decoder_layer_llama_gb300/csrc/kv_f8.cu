@@ -91,7 +91,7 @@ LL_DEVINL bool append_span(const AppendArgs& a, int b, bool flag, AppendSpan& s)
     s.start = c0;
     s.n = 0;
     if (n == 0) return false;
-    if (c0 < 0 || n < 0 || c1 > a.tokens || n > a.max_new || n > ctx || ctx > a.max_blocks * a.block_size) {
+    if (c0 < 0 || n < 0 || c1 > a.tokens || n > a.max_new || n > ctx || ctx > a.max_context) {
         if (flag) flag_status(a.status, LL_DEV_BAD_POSITION);
         return false;
     }
@@ -230,6 +230,17 @@ __global__ void __launch_bounds__(kAppendThreads) append_chunk_kernel(const Appe
     }
 }
 
+__global__ void f8_positions_kernel(const int32_t* context_lens, int batch, int seq_len, int32_t* positions, int32_t* cu_new) {
+    pdl_wait();
+    pdl_trigger();
+    const int t = (int)(blockIdx.x * blockDim.x + threadIdx.x);
+    if (t < batch * seq_len) {
+        const int b = t / seq_len;
+        positions[t] = context_lens[b] - seq_len + (t - b * seq_len);
+    }
+    if (t <= batch) cu_new[t] = t * seq_len;
+}
+
 template <int D>
 cudaError_t append_for(const AppendArgs& a, cudaStream_t stream) {
     cudaError_t e;
@@ -256,6 +267,17 @@ cudaError_t append_for(const AppendArgs& a, cudaStream_t stream) {
 }
 
 }  // namespace
+
+cudaError_t launch_f8_positions(const int32_t* context_lens, int batch, int seq_len, int32_t* positions, int32_t* cu_new,
+                                cudaStream_t stream) {
+    const int n = std::max(batch * seq_len, batch + 1);
+    trace_before("f8_positions", stream);
+    cudaError_t e = launch_pdl(f8_positions_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, stream, 1, context_lens,
+                               batch, seq_len, positions, cu_new);
+    trace_after(stream);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    return record(e, "f8_positions_kernel launch");
+}
 
 cudaError_t launch_append_f8(const AppendArgs& a, cudaStream_t stream) {
     if (a.batch <= 0 || a.tokens <= 0) return cudaSuccess;

@@ -20,6 +20,12 @@ step for every slot through all layers (one decode call per layer; this part
 can be captured once as a CUDA graph and replayed with the tables updated in
 place).  Every computation runs in the library's kernels; this module only
 moves indices.
+
+Requests can share blocks: a fork shares its parent's full blocks (each block
+counts its holders, and returns to the free list when the last one lets go) and
+copies the block that is still filling, in the pools of every layer at once.
+After many admissions and retirements the blocks in use can be packed to the
+front of the pools.
 """
 from __future__ import annotations
 
@@ -32,31 +38,55 @@ from . import synth
 
 
 class BlockAllocator:
-    """LIFO free list of physical KV blocks (seeded initial order)."""
+    """LIFO free list of physical KV blocks (seeded initial order), with the number of holders of each
+    block in use."""
 
     def __init__(self, num_blocks: int, seed: int):
         g = torch.Generator()
         g.manual_seed(int(seed))
         self.num_blocks = int(num_blocks)
         self._free = torch.randperm(self.num_blocks, generator=g).tolist()
-        self._used = set()
+        self._used = {}
 
     def free_count(self) -> int:
         return len(self._free)
+
+    def holders(self, block: int) -> int:
+        return self._used.get(block, 0)
 
     def alloc(self, n: int) -> list:
         if n > len(self._free):
             raise MemoryError(f"KV pool exhausted: need {n} blocks, {len(self._free)} free")
         out = [self._free.pop() for _ in range(n)]
-        self._used.update(out)
+        self._used.update((b, 1) for b in out)
         return out
 
+    def share(self, blocks) -> None:
+        """One more holder for each of the blocks."""
+        blocks = list(blocks)
+        for b in blocks:
+            if b not in self._used:
+                raise ValueError(f"block {b} is not in use")
+        for b in blocks:
+            self._used[b] += 1
+
     def free(self, blocks) -> None:
+        """One holder less; a block without any returns to the free list."""
         for b in blocks:
             if b not in self._used:
                 raise ValueError(f"block {b} freed twice or never allocated")
-            self._used.remove(b)
-            self._free.append(b)
+            self._used[b] -= 1
+            if self._used[b] == 0:
+                del self._used[b]
+                self._free.append(b)
+
+    def apply_map(self, block_map) -> None:
+        """Renames the blocks in use as compact_blocks' block_map says (old id -> new id, -1: not in use)."""
+        moved = {int(block_map[b]): n for b, n in self._used.items()}
+        if len(moved) != len(self._used) or any(not 0 <= b < self.num_blocks for b in moved):
+            raise ValueError("the map does not name every block in use")
+        self._used = moved
+        self._free = [b for b in range(self.num_blocks - 1, -1, -1) if b not in moved]
 
 
 @dataclasses.dataclass
@@ -115,6 +145,39 @@ class Scheduler:
             admitted.append(s)
         return admitted
 
+    def retire(self, slot: int) -> None:
+        """Ends the request in a slot now: its blocks are let go, the slot is empty."""
+        r = self.slots[slot]
+        if r is None:
+            raise ValueError(f"slot {slot} is empty")
+        self.alloc.free(r.blocks)
+        self.slots[slot] = None
+        self.table[slot, :] = -1
+
+    def fork(self, src: int, dst: int) -> list:
+        """A copy of the request in slot `src` for the empty slot `dst`: full blocks are shared, the one that is
+        still filling is copied.  Returns the (from, to) block pairs to copy in every pool before either
+        request goes on."""
+        r = self.slots[src]
+        if r is None or self.slots[dst] is not None:
+            raise ValueError(f"a fork goes from a request to an empty slot, not from slot {src} to {dst}")
+        full = r.ctx // self.bs
+        last = self.alloc.alloc(1) if r.ctx % self.bs else []
+        self.alloc.share(r.blocks[:full])
+        nr = Request(self.next_rid, r.ctx, r.budget, r.blocks[:full] + last)
+        self.next_rid += 1
+        self.slots[dst] = nr
+        self._set_blocks(dst, nr.blocks)
+        return [(r.blocks[full], last[0])] if last else []
+
+    def apply_map(self, block_map) -> None:
+        """Renames every block as compact_blocks' block_map says."""
+        self.alloc.apply_map(block_map)
+        for s, r in enumerate(self.slots):
+            if r is not None:
+                r.blocks = [int(block_map[b]) for b in r.blocks]
+                self._set_blocks(s, r.blocks)
+
     def grow_for_decode(self) -> np.ndarray:
         """Every slot appends one token: a block is added when the new position starts one.
         Returns context_lens (int32) including the appended token."""
@@ -131,7 +194,8 @@ class Scheduler:
 
 
 class StackEngine:
-    """The GPU side: L layers (packed weights, K/V pools) and device copies of the tables."""
+    """The GPU side: L layers (packed weights, K/V pools) and device copies of the tables.  A layer's pool is
+    a (K, V) pair of BF16 tensors or an api.PoolF8; all layers have the same kind."""
 
     def __init__(self, api, cfgs, packed, pools, n_slots, max_blocks, max_prefill_tokens,
                  device="cuda"):
@@ -142,7 +206,10 @@ class StackEngine:
         self.H = cfg.hidden
         self.table = torch.full((n_slots, max_blocks), -1, dtype=torch.int32, device=device)
         self.ctx = torch.zeros(n_slots, dtype=torch.int32, device=device)
-        self.ws = api.new_workspace(cfg, max(n_slots, max_prefill_tokens), max_blocks, device)
+        self.f8 = isinstance(pools[0], api.PoolF8)
+        self.ws = (api.new_workspace_f8 if self.f8 else api.new_workspace)(cfg, max(n_slots, max_prefill_tokens),
+                                                                           max_blocks, device)
+        self.blocks = api.BlockSet([t for p in pools for t in (p.tensors() if self.f8 else p)])
         self.status = api.new_status(device)
         self.x = torch.zeros(n_slots, self.H, dtype=torch.bfloat16, device=device)
         self.bufs = [torch.empty(n_slots, self.H, dtype=torch.bfloat16, device=device) for _ in range(2)]
@@ -151,16 +218,26 @@ class StackEngine:
                         for _ in range(2)]
         self.pf_pos = torch.empty(max_prefill_tokens, dtype=torch.int32, device=device)
         self.pf_table = torch.full((n_slots, max_blocks), -1, dtype=torch.int32, device=device)
+        self.pf_ctx = torch.zeros(n_slots, dtype=torch.int32, device=device)
         self.graph = None
         self.y = None
+        # the buffers are filled on the stream that is current here, and used on the caller's from now on
+        torch.cuda.current_stream(self.table.device).synchronize()
 
     def prefill(self, n_req, prompt_len, stream):
         """All layers over the n_req requests whose rows are in pf_table[:n_req] and whose
-        inputs are in pf_x[:n_req * prompt_len]."""
+        inputs are in pf_x[:n_req * prompt_len]; their positions in pf_pos (BF16 pools) or their
+        context lengths, which count the prompt, in pf_ctx (e4m3 pools)."""
         T = n_req * prompt_len
         src = self.pf_x[:T]
         for l in range(len(self.cfgs)):
             dst = self.pf_bufs[l & 1][:T]
+            if self.f8:
+                self.api.layer_prefill_f8(self.cfgs[l], self.packed[l], src, self.pools[l], self.pf_table[:n_req],
+                                          self.pf_ctx[:n_req], prompt_len, y=dst, workspace=self.ws,
+                                          status=self.status, stream=stream)
+                src = dst
+                continue
             k, v = self.pools[l]
             self.api.layer_prefill(self.cfgs[l], self.packed[l], src, self.pf_pos[:T], n_req, prompt_len,
                                    k, v, self.pf_table[:n_req], y=dst, workspace=self.ws,
@@ -172,11 +249,37 @@ class StackEngine:
         src = self.x
         for l in range(len(self.cfgs)):
             dst = self.bufs[l & 1]
+            if self.f8:
+                self.api.layer_decode_step_f8(self.cfgs[l], self.packed[l], src, self.pools[l], self.table, self.ctx,
+                                              y=dst, workspace=self.ws, status=self.status, stream=stream)
+                src = dst
+                continue
             k, v = self.pools[l]
             self.api.layer_decode_step(self.cfgs[l], self.packed[l], src, k, v, self.table, self.ctx,
                                        y=dst, workspace=self.ws, status=self.status, stream=stream)
             src = dst
         return src
+
+    def copy_blocks(self, pairs, stream):
+        """Copies blocks (from, to), as Scheduler.fork names them, in the pools of every layer."""
+        if pairs:
+            t = torch.tensor(pairs, dtype=torch.int32, device=self.table.device)
+            stream.wait_stream(torch.cuda.current_stream())
+            t.record_stream(stream)
+            self.api.copy_blocks(self.blocks, t, status=self.status, stream=stream)
+
+    def compact(self, scheduler: Scheduler, stream) -> int:
+        """Packs the blocks of the scheduler's requests to the front of every pool, and renames them in the
+        scheduler and in the device table.  Waits for the stream; returns the number of blocks moved."""
+        self.table.copy_(torch.from_numpy(scheduler.table))
+        stream.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(stream):
+            _, pairs, counts, block_map = self.api.compact_blocks(self.table, self.blocks.num_blocks,
+                                                                  new_table=self.table, status=self.status)
+            self.api.copy_blocks(self.blocks, pairs, n_pairs=counts[1:], status=self.status)
+            block_map, counts = block_map.cpu().numpy(), counts.tolist()
+        scheduler.apply_map(block_map)
+        return counts[1]
 
     def capture_decode(self, stream):
         """Records the all-layer decode step once as a CUDA graph (replayed by decode())."""
