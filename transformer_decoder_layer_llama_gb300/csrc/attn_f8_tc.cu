@@ -172,6 +172,27 @@ LL_DEVINL uint4 load16_if(const void* p, bool take) {
     return v;
 }
 
+// The larger magnitude in each half (a NaN loses to a number).
+LL_DEVINL uint32_t max_abs_bf16x2(uint32_t m, uint32_t x) {
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(m), "r"(x & 0x7fff7fffu));
+    return r;
+}
+
+// Two BF16 times the power of two in both halves of up2 (exact), as FP16.
+LL_DEVINL uint32_t scaled_f16x2(uint32_t x, uint32_t up2) {
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(up2));
+    return pack_f16x2(bf16_lo(r), bf16_hi(r));
+}
+
+// A whole 32-byte sector per thread.
+LL_DEVINL void store32(void* p, const uint32_t (&v)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]),
+                 "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
 // One lane of the (converged) warp, always the same.
 LL_DEVINL bool elect_one() {
     uint32_t r;
@@ -522,27 +543,23 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
             cp_async_commit();
             cp_async_wait<0>();
             __syncwarp();
-            uint32_t m = 0;
+            uint32_t m2 = 0;                                // largest magnitudes of the even and odd elements
 #pragma unroll 4
             for (int c = 0; c < D / 8; ++c) {
                 const uint4 w = *reinterpret_cast<const uint4*>(sq + pf_off(r, c));
-                m = max(m, max(max(max(w.x & 0x7fffu, (w.x >> 16) & 0x7fffu), max(w.y & 0x7fffu, (w.y >> 16) & 0x7fffu)),
-                               max(max(w.z & 0x7fffu, (w.z >> 16) & 0x7fffu), max(w.w & 0x7fffu, (w.w >> 16) & 0x7fffu))));
+                m2 = max_abs_bf16x2(max_abs_bf16x2(max_abs_bf16x2(max_abs_bf16x2(m2, w.x), w.y), w.z), w.w);
             }
-            int ex = (int)(m >> 7) - 127;                   // zeros, infinities and NaN: as they are
+            const uint32_t m = max(m2 & 0xffffu, m2 >> 16);
+            // exponent of the largest; zeros, infinities (and NaN alone) stay as they are; below 2^-112 the row is
+            // scaled as if at 2^-112, so that the factor is one BF16
+            int ex = max((int)(m >> 7) - 127, -112);
             if (m == 0u || m >= 0x7f80u) ex = 14;
-            const int e0 = (14 - ex) / 2, e1 = 14 - ex - e0;
-            const float u0 = __uint_as_float((uint32_t)(e0 + 127) << 23), u1 = __uint_as_float((uint32_t)(e1 + 127) << 23);
+            const uint32_t up = (uint32_t)(14 - ex + 127) << 7, up2 = up << 16 | up;
 #pragma unroll 4
             for (int c = 0; c < D / 8; ++c) {
                 uint4* at = reinterpret_cast<uint4*>(sq + pf_off(r, c));
                 const uint4 w = *at;
-                uint4 o;
-                o.x = pack_f16x2(bf16_lo(w.x) * u0 * u1, bf16_hi(w.x) * u0 * u1);
-                o.y = pack_f16x2(bf16_lo(w.y) * u0 * u1, bf16_hi(w.y) * u0 * u1);
-                o.z = pack_f16x2(bf16_lo(w.z) * u0 * u1, bf16_hi(w.z) * u0 * u1);
-                o.w = pack_f16x2(bf16_lo(w.w) * u0 * u1, bf16_hi(w.w) * u0 * u1);
-                *at = o;
+                *at = make_uint4(scaled_f16x2(w.x, up2), scaled_f16x2(w.y, up2), scaled_f16x2(w.z, up2), scaled_f16x2(w.w, up2));
             }
             qf = scalbnf(a.scale * kPfLog2e, ex - 14);
             fence_async_smem();
@@ -656,21 +673,25 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
             const int E = *const_cast<volatile int*>(&vexp_s) - kPfShift;
             const float up = E < -126 ? 0.f : __uint_as_float((uint32_t)(E + 127) << 23);
 #pragma unroll 1
-            for (int c = 0; c < D; c += 16) {
-                float v[16];
-                tmem_ld16(to + (uint32_t)c, v);
-                if (live && splits == 1) {
-                    uint32_t y[8];
+            for (int c = 0; c < D; c += 64) {
+                uint32_t v[64];
+                tmem_ld64_issue(to + (uint32_t)c, v);
+                tmem_wait_ld(v);
+                if (!live) continue;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) y[i] = pack_bf16x2(v[2 * i] * inv * up, v[2 * i + 1] * inv * up);
-                    uint4* dst = reinterpret_cast<uint4*>(a.out + qrow * D + c);
-                    dst[0] = make_uint4(y[0], y[1], y[2], y[3]);
-                    dst[1] = make_uint4(y[4], y[5], y[6], y[7]);
-                } else if (live) {
-                    float4* dst = reinterpret_cast<float4*>(a.part_o + prow * D + c);
+                for (int i = 0; i < 64; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * inv * up);
+                if (splits == 1) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        dst[i] = make_float4(v[4 * i] * inv * up, v[4 * i + 1] * inv * up, v[4 * i + 2] * inv * up, v[4 * i + 3] * inv * up);
+                    for (int i = 0; i < 64; i += 8)
+                        *reinterpret_cast<uint4*>(a.out + qrow * D + c + i) = make_uint4(
+                            pack_bf16x2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), pack_bf16x2(__uint_as_float(v[i + 2]), __uint_as_float(v[i + 3])),
+                            pack_bf16x2(__uint_as_float(v[i + 4]), __uint_as_float(v[i + 5])), pack_bf16x2(__uint_as_float(v[i + 6]), __uint_as_float(v[i + 7])));
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 64; i += 8) {
+                        const uint32_t y[8] = {v[i], v[i + 1], v[i + 2], v[i + 3], v[i + 4], v[i + 5], v[i + 6], v[i + 7]};
+                        store32(a.part_o + prow * D + c + i, y);
+                    }
                 }
             }
             if (live && splits > 1) a.part_ml[prow] = make_float2(m_used, l);
