@@ -222,25 +222,76 @@ struct PfItem {
     int n_kt;                // key tiles
 };
 
+// One sequence's new tokens: rows c0 .. c0 + n - 1 of q at positions pos0 .. (n = 0 where there are none, or where
+// the counts do not fit together: flagged).
+struct PfSeq {
+    int c0, n, pos0;
+};
+LL_DEVINL PfSeq pf_seq(const AttnF8Args& a, int b, bool flag) {
+    PfSeq s;
+    s.c0 = a.cu_new[b];
+    const int c1 = a.cu_new[b + 1], ctx = a.context_lens[b];
+    const long long n = (long long)c1 - s.c0;
+    const bool bad = s.c0 < 0 || n < 0 || c1 > a.tokens || n > a.max_new || n > ctx || ctx > a.max_blocks * a.block_size;
+    if (bad && n != 0 && flag) flag_status(a.status, LL_DEV_BAD_POSITION);
+    s.n = bad ? 0 : (int)n;
+    s.pos0 = ctx - s.n;
+    return s;
+}
+
+// Item i of the grid, KV heads fastest; called by whole warps.  Items with the most keys come first, so that the
+// last ones to start are short: in a batch of up to 32 sequences the item's place in that order is found by a
+// search over the number of key tiles, a lane per sequence; in larger batches the order is by query tile alone
+// (latest first).  Ragged 70B-shaped chunks: 529 -> 485 us.
 LL_DEVINL bool pf_item(const AttnF8Args& a, int i, int n_mt, int tt, bool flag, PfItem& it) {
-    // latest tiles (the most keys) first, KV heads fastest
+    const int step = 2 * tt;
     it.hk = i % a.n_kv_heads;
-    i /= a.n_kv_heads;
-    it.b = i % a.batch;
-    const int mt = n_mt - 1 - i / a.batch;
-    const int c0 = a.cu_new[it.b], c1 = a.cu_new[it.b + 1], ctx = a.context_lens[it.b];
-    const long long n = (long long)c1 - c0;
-    if (n == 0) return false;
-    if (c0 < 0 || n < 0 || c1 > a.tokens || n > a.max_new || n > ctx || ctx > a.max_blocks * a.block_size) {
-        if (flag) flag_status(a.status, LL_DEV_BAD_POSITION);
-        return false;
+    const int k = i / a.n_kv_heads;
+    int mt;
+    PfSeq s;
+    if (a.batch == 1 || a.batch > 32) {
+        it.b = k % a.batch;
+        mt = n_mt - 1 - k / a.batch;
+        s = pf_seq(a, it.b, flag);
+        if (mt * step >= s.n) return false;
+    } else {
+        const int lane = threadIdx.x & 31;
+        PfSeq mine{0, 0, 0};
+        if (lane < a.batch) mine = pf_seq(a, lane, flag && i == 0);
+        const int items = (mine.n + step - 1) / step;
+        // this lane's items with more than t key tiles: those whose last key lies beyond 128 t
+        const auto longer = [&](int t) {
+            const int x = t * kPfKeys - mine.pos0;
+            return x < 0 ? items : x >= mine.n ? 0 : items - x / step;
+        };
+        int lo = 0;                                         // (longer than lo - 1: more than k items, or lo = 0)
+        int hi = __reduce_max_sync(0xffffffffu, mine.n ? (mine.pos0 + mine.n + kPfKeys - 1) / kPfKeys : 0);
+        if (k >= __reduce_add_sync(0xffffffffu, items)) return false;
+        while (lo < hi) {                                   // the smallest t that at most k items exceed: item k's key tiles
+            const int mid = (lo + hi) >> 1;
+            if (__reduce_add_sync(0xffffffffu, longer(mid)) <= k) hi = mid;
+            else lo = mid + 1;
+        }
+        const int more = longer(lo), same = longer(lo - 1) - more;
+        const int p = k - __reduce_add_sync(0xffffffffu, more);      // its place among the items as long
+        int before = same;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, before, o);
+            if (lane >= o) before += y;
+        }
+        before -= same;
+        const uint32_t who = __ballot_sync(0xffffffffu, p >= before && p < before + same);
+        it.b = __ffs(who) - 1;
+        mt = __shfl_sync(0xffffffffu, items - more - 1 - (p - before), it.b);
+        s.c0 = __shfl_sync(0xffffffffu, mine.c0, it.b);
+        s.n = __shfl_sync(0xffffffffu, mine.n, it.b);
+        s.pos0 = __shfl_sync(0xffffffffu, mine.pos0, it.b);
     }
-    const int t0 = mt * 2 * tt;
-    if (t0 >= n) return false;
-    const int left = (int)n - t0;
+    const int t0 = mt * step, left = s.n - t0;
     it.tt = tt;
-    it.tok0 = c0 + t0;
-    it.pos0 = ctx - left;
+    it.tok0 = s.c0 + t0;
+    it.pos0 = s.pos0 + t0;
     it.nt_a = min(tt, left);
     it.nt_b = min(tt, left - it.nt_a);
     it.end_a = it.pos0 + it.nt_a;
@@ -294,7 +345,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
     pdl_trigger();
     PfItem it;
     const int item = (int)blockIdx.x / ns, split = (int)blockIdx.x - item * ns;
-    if (!pf_item(a, item, n_mt, tt, threadIdx.x == 0 && split == 0, it)) return;
+    if (!pf_item(a, item, n_mt, tt, warp == 0 && split == 0, it)) return;
     const int splits = pf_splits(ns, it.n_kt);
     if (split >= splits) return;
     const int first = (int)((long long)it.n_kt * split / splits);   // the CTA's first key tile; tiles are counted from it
