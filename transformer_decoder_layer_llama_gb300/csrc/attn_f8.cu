@@ -10,7 +10,7 @@
 // the log-sum-exp.
 //
 // A CTA is four consumer warps and a producer warp.  The producer brings each tile's codes in by TMA
-// (three stages) with the scales of its blocks, reading the block table and scales a batch of tiles
+// (four stages) with the scales of its blocks, reading the block table and scales a batch of tiles
 // ahead.  Each consumer warp owns 16 keys of a tile (they lie in one block, so its scales are scalars):
 // S^T = K Q^T and O^T += V^T P^T by mma.sync with the keys, and the head dims, as the 16 rows of A
 // and up to 8 (or 16) query heads of the KV head as columns, so a single query head wastes 7 of 8
@@ -36,10 +36,13 @@ namespace {
 
 constexpr float kLog2eF8 = 1.4426950408889634f;
 constexpr int kF8Tile = 64;              // keys per tile
-constexpr int kF8Stages = 3;
+constexpr int kF8Stages = 4;
 constexpr int kF8Threads = 160;
 constexpr int kF8Shift = 6;              // probabilities enter P V times 2^6
-constexpr int kF8MaxCtasPerSm = 4;
+// Up to 8 query heads per KV head: three CTAs per SM of four stages each (192 KB of codes per SM at D = 128).
+// 7B shapes 201 us, 70B shapes 102; with three stages and four (7B) or three CTAs 201 and 110,
+// with four CTAs throughout 217 and 108, for their 96 registers spill.
+constexpr int kF8MaxCtasPerSm = 3;
 
 LL_DEVINL int f8_context(const AttnF8Args& a, int b, bool flag) {
     const int cap = a.max_blocks * a.block_size;
@@ -150,7 +153,7 @@ struct F8Walk {
 };
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kF8Threads, NT == 1 ? 4 : 2)
+__global__ void __launch_bounds__(kF8Threads, NT == 1 ? kF8MaxCtasPerSm : 2)
     attn_decode_f8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                           const AttnF8Args a) {
     constexpr int BN = kF8Tile, STAGES = kF8Stages, NCONS = 128;
@@ -160,7 +163,7 @@ __global__ void __launch_bounds__(kF8Threads, NT == 1 ? 4 : 2)
     uint8_t* sbase = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sk = sbase;                                   // [STAGES][TILE]
     uint8_t* sv = sk + STAGES * TILE;                      // [STAGES][TILE]
-    float* s_acc = reinterpret_cast<float*>(sv + STAGES * TILE);   // [4 warps][G][D], merged at a segment's end
+    float* s_acc = reinterpret_cast<float*>(sv + STAGES * TILE);   // [4 warps][G][32], for merging at a segment's end
     __shared__ uint64_t full_bar[STAGES], empty_bar[STAGES];
     __shared__ unsigned long long valid_s[STAGES];         // per stage: bit k = key k of the tile is cached
     __shared__ float2 scale_s[STAGES][4];                  // per stage and 16 keys: K and V scale
@@ -502,51 +505,67 @@ __global__ void __launch_bounds__(kF8Threads, NT == 1 ? 4 : 2)
             for (int e = 0; e < 2; ++e)
 #pragma unroll
                 for (int o = 4; o <= 16; o <<= 1) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], o);
-        asm volatile("bar.sync 1, 128;" ::: "memory");         // the buffer's last readers are done
+        asm volatile("bar.sync 1, 128;" ::: "memory");         // the last segment's readers of s_ml are done
         if (lane == 0) s_exp[warp] = E;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
+        for (int nt = 0; nt < NT; ++nt)
             if (g == 0) {
 #pragma unroll
                 for (int e = 0; e < 2; ++e) s_ml[warp][8 * nt + 2 * cq + e] = make_float2(m[nt][e], l[nt][e]);
             }
-#pragma unroll
-            for (int t = 0; t < W; ++t)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int r = 8 * nt + 2 * cq + (j & 1);
-                    if (r < G) s_acc[(warp * G + r) * D + (D / 8) * g + 2 * t + (j >> 1)] = acc[nt][t][j];
-                }
-        }
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-        int Em = -1000;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) Em = max(Em, s_exp[w]);
         const bool whole = seg.kt0 == 0 && seg.kt1 == seg.n_kt;
         // slot 0: the segment holds the share's first tile; 1: it is the share's last one
         const int slot = 2 * cta + (it == (int)(t_end - t_begin) && it > seg.kt1 - seg.kt0 ? 1 : 0);
-        for (int i = threadIdx.x; i < G * D; i += NCONS) {
-            const int r = i / D, col = i % D;
-            float M = -INFINITY;
+        // 32 head dims at a time, four of each lane group g, so that the buffer leaves room for four stages in three CTAs per SM
 #pragma unroll
-            for (int w = 0; w < 4; ++w) M = fmaxf(M, s_ml[w][r].x);
-            const float base = (M == -INFINITY) ? 0.f : M;
-            float num = 0.f, den = 0.f;
+        for (int rd = 0; rd < W / 2; ++rd) {
+            if (rd > 0) asm volatile("bar.sync 1, 128;" ::: "memory");
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                const float2 ml = s_ml[w][r];
-                const float e = exp2f(ml.x - base);
-                const int de = s_exp[w] - Em;
-                num += e * (de < -126 ? 0.f : __uint_as_float((uint32_t)(de + 127) << 23)) * s_acc[(w * G + r) * D + col];
-                den += e * ml.y;
-            }
-            // no valid key: zeros
-            const float o = den == 0.f ? 0.f : scalbnf(num / den, Em > -1000 ? Em - kF8Shift : 0);
-            if (whole) {
-                a.out[((size_t)seg.b * a.n_heads + (size_t)seg.hk * G + r) * D + col] = __float2bfloat16_rn(o);
-            } else {
-                a.part_o[((size_t)slot * G + r) * D + col] = o;
-                if (col == 0) a.part_ml[(size_t)slot * G + r] = make_float2(M, den);
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int r = 8 * nt + 2 * cq + (j & 1);
+                        if (r < G) s_acc[(warp * G + r) * 32 + 4 * g + 2 * t + (j >> 1)] = acc[nt][2 * rd + t][j];
+                    }
+            asm volatile("bar.sync 1, 128;" ::: "memory");
+            int Em = -1000;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) Em = max(Em, s_exp[w]);
+            for (int i = threadIdx.x; i < G * 8; i += NCONS) {
+                const int r = i >> 3, gg = i & 7, col = (D / 8) * gg + 4 * rd;
+                float M = -INFINITY;
+#pragma unroll
+                for (int w = 0; w < 4; ++w) M = fmaxf(M, s_ml[w][r].x);
+                const float base = (M == -INFINITY) ? 0.f : M;
+                float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+                float den = 0.f;
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    const float2 ml = s_ml[w][r];
+                    const float e = exp2f(ml.x - base);
+                    const int de = s_exp[w] - Em;
+                    const float f = e * (de < -126 ? 0.f : __uint_as_float((uint32_t)(de + 127) << 23));
+                    const float4 x = *reinterpret_cast<const float4*>(&s_acc[(w * G + r) * 32 + 4 * gg]);
+                    num.x += f * x.x;
+                    num.y += f * x.y;
+                    num.z += f * x.z;
+                    num.w += f * x.w;
+                    den += e * ml.y;
+                }
+                // no valid key: zeros.  2^(Em - 6) as two factors
+                const int ex = Em > -1000 ? Em - kF8Shift : 0, h0 = ex / 2, h1 = ex - h0;
+                const float u0 = __uint_as_float((uint32_t)(h0 + 127) << 23), u1 = __uint_as_float((uint32_t)(h1 + 127) << 23);
+                const float inv = den == 0.f ? 0.f : 1.f / den;
+                const float4 o = make_float4(num.x * inv * u0 * u1, num.y * inv * u0 * u1, num.z * inv * u0 * u1, num.w * inv * u0 * u1);
+                if (whole) {
+                    *reinterpret_cast<uint2*>(a.out + ((size_t)seg.b * a.n_heads + (size_t)seg.hk * G + r) * D + col) =
+                        make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+                } else {
+                    *reinterpret_cast<float4*>(a.part_o + ((size_t)slot * G + r) * D + col) = o;
+                    if (col == 0) a.part_ml[(size_t)slot * G + r] = make_float2(M, den);
+                }
             }
         }
     }
@@ -634,15 +653,16 @@ __global__ void __launch_bounds__(kF8JoinThreads) attn_decode_f8_join_kernel(con
 }
 
 int f8_ctas_per_sm(int G, int D) {
-    const size_t smem = (size_t)2 * kF8Stages * kF8Tile * D + (size_t)4 * G * D * 4 + 1024;
-    return std::min(G <= 8 ? kF8MaxCtasPerSm : 2, (int)((220 * 1024) / (smem + 2048)));
+    const size_t smem = (size_t)2 * kF8Stages * kF8Tile * D + (size_t)4 * G * 32 * 4 + 1024;
+    // an SM has 228 KB, a CTA takes 2 KB more for its static part and the system's
+    return std::min(G <= 8 ? kF8MaxCtasPerSm : 2, (int)((228 * 1024) / (smem + 2048)));
 }
 
 template <int D, int NT>
 cudaError_t decode_f8_for(const AttnF8Args& a, cudaStream_t stream) {
     const int G = a.n_heads / a.n_kv_heads;
-    const size_t smem = (size_t)2 * kF8Stages * kF8Tile * D + (size_t)4 * G * D * 4 + 1024;
-    const size_t smem_max = (size_t)2 * kF8Stages * kF8Tile * D + (size_t)4 * 8 * NT * D * 4 + 1024;
+    const size_t smem = (size_t)2 * kF8Stages * kF8Tile * D + (size_t)4 * G * 32 * 4 + 1024;
+    const size_t smem_max = (size_t)2 * kF8Stages * kF8Tile * D + (size_t)4 * 8 * NT * 32 * 4 + 1024;
     const void* kernel = (const void*)attn_decode_f8_kernel<D, NT>;
     cudaError_t e = ensure_func_attr(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_max,
                                      "cudaFuncSetAttribute(attn_decode_f8_kernel)");
