@@ -765,3 +765,26 @@ def test_stack_forks_and_compacts(f8):
         assert int(eng.status.item()) == 0
     finally:
         torch.cuda.set_stream(torch.cuda.default_stream())
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_attention_of_zero_keys_and_a_zero_scale(d):
+    """Blocks whose keys are all zeros (scale 0) that end inside a tile, or whose last keys the causal mask hides;
+    scale 0: every visible key counts alike."""
+    rng = np.random.default_rng(3 * d)
+    ctx, bs, H, Hkv = [5, 150, 40], 16, 6, 2
+    ref_pool, table = make_cache(rng, ctx, Hkv, d, bs)
+    for blk in (table[0][0], table[1][8], table[1][9], table[2][1]):     # the last blocks of each
+        ref_pool.k[blk], ref_pool.k_scale[blk] = 0, 0.0
+    pool = to_gpu(ref_pool)
+    new = [5, 60, 1]
+    cu = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    q = torch.from_numpy(rng.normal(size=(int(cu[-1]), H, d))).bfloat16()
+    st = status()
+    for scale in (d ** -0.5, 0.0):
+        want = C.attention_f8(f64(q), ref_pool, table, ctx, cu, scale)
+        assert_attention(api.paged_attention_prefill_f8(q.cuda(), dev(cu), pool, dev(table), dev(ctx), scale, max_new=60,
+                                                        status=st), *want, d)
+        want = C.attention_f8(f64(q[:3]), ref_pool, table, ctx, np.arange(4), scale)
+        assert_attention(api.paged_attention_decode_f8(q[:3].cuda(), pool, dev(table), dev(ctx), scale, status=st), *want, d)
+    check(st)

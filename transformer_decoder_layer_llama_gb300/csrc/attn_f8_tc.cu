@@ -656,7 +656,9 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
 #pragma unroll
                 for (int c = 0; c < kPfChunks; ++c) {
                     const int lim = (chunks >> c) & 1u ? last - c * 16 : -1;
-                    f[c] = lim < 0 ? 1.f : f[c];            // (no 0 * -inf)
+                    // -inf times the factor stays -inf: a factor of 0 (a block of zeros, or scale 0) becomes 2^-126,
+                    // which leaves of a sum S (below 2^31) at most 2^-95
+                    f[c] = lim < 0 ? 1.f : fmaxf(f[c], 1.17549435e-38f);
 #pragma unroll
                     for (int i = 0; i < 16; ++i) s[16 * c + i] = i <= lim ? s[16 * c + i] : -INFINITY;
                 }
