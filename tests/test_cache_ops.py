@@ -154,6 +154,23 @@ def test_rope_refusals(bad, code):
     assert api.lib.ll_rope(*{**ROPE, **bad}.values(), NULL) == code
 
 
+# q and k as the columns of one buffer of 384-element rows: 0 .. 127 and 128 .. 191
+MERGED = dict(q=FAKE, k=FAKE + 256, q_stride=384, k_stride=384, q_out_stride=384, k_out_stride=384)
+
+
+@pytest.mark.parametrize("out", [dict(q_out=FAKE, k_out=FAKE),                       # k over q, which is rotated in place
+                                 dict(q_out=FAKE, k_out=FAKE + 254),
+                                 dict(q_out=FAKE + 200, k_out=FAKE + 256),           # q over its own columns
+                                 dict(q_out=FAKE + 512, k_out=FAKE + 512 + 128),     # the outputs over each other
+                                 dict(q_out=FAKE + 384, k_out=FAKE + 384 + 768),     # a row later is the same columns
+                                 dict(q_out=FAKE + 640, k_out=FAKE + 256),           # q over the next row's start
+                                 dict(q_out=8 * FAKE, k_out=8 * FAKE + 255 * 2, q_out_stride=256),   # strides that differ
+                                 dict(q_out=8 * FAKE, k_out=8 * FAKE),
+                                 dict(k=FAKE, q_out=FAKE, k_out=8 * FAKE)])          # k is read while q is rotated
+def test_rope_refuses_outputs_that_share_memory(out):
+    assert api.lib.ll_rope(*{**ROPE, **MERGED, **out}.values(), NULL) == INVALID
+
+
 def test_rope_without_tokens_launches_nothing():
     assert api.lib.ll_rope(*{**ROPE, "tokens": 0}.values(), NULL) == api.LL_OK
 

@@ -864,7 +864,8 @@ int layer_f8_args(const ll_config* cfg, const void* packed, const void* x, const
     const int rc = config_supported(cfg);
     if (rc != LL_OK) return rc;
     if (!packed || !x || !context_lens || !block_table || !y || !status || !pool || !pool->k || !pool->v ||
-        !pool->k_scale || !pool->v_scale || pool->num_blocks <= 0 || !aligned16(pool->k) || !aligned16(pool->v))
+        !pool->k_scale || !pool->v_scale || pool->num_blocks <= 0 || !aligned16(pool->k) || !aligned16(pool->v) ||
+        ((reinterpret_cast<uintptr_t>(pool->k_scale) | reinterpret_cast<uintptr_t>(pool->v_scale)) & 3u) != 0)
         return LL_ERR_INVALID_ARG;
     if (batch <= 0 || seq_len <= 0 || max_blocks <= 0 || x == y) return LL_ERR_INVALID_ARG;
     if (!aligned16(packed) || !aligned16(x) || !aligned16(y)) return LL_ERR_INVALID_ARG;

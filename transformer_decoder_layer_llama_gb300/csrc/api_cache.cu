@@ -23,6 +23,23 @@ bool overlap(const void* a, size_t an, const void* b, size_t bn) {
     return x < y + bn && y < x + an;
 }
 
+// `tokens` rows of `width` elements, `stride` elements apart.
+struct Rows {
+    const void* p;
+    int64_t stride, width;
+};
+// Whether two such tensors may share a byte.  Rows of one buffer at the same stride (the heads of a merged QKV
+// output) do not where their columns lie apart; other strides that meet count as sharing.
+bool rows_overlap(const Rows& a, const Rows& b, int64_t tokens, int64_t esz) {
+    const auto bytes = [&](const Rows& r) { return (size_t)(((tokens - 1) * r.stride + r.width) * esz); };
+    if (!overlap(a.p, bytes(a), b.p, bytes(b))) return false;
+    if (a.stride != b.stride || tokens == 1) return true;
+    const int64_t step = a.stride * esz;
+    const int64_t apart = (static_cast<const char*>(b.p) - static_cast<const char*>(a.p)) % step;
+    const int64_t at = apart < 0 ? apart + step : apart;        // b's column in a's rows
+    return at < a.width * esz || at + b.width * esz > step;
+}
+
 int rope_config_ok(const ll_rope_config* c) {
     if (!c || c->rotary_dim < 2 || c->rotary_dim % 2 != 0 || !(c->theta > 1.f) || !std::isfinite(c->theta))
         return LL_ERR_INVALID_ARG;
@@ -149,24 +166,22 @@ int ll_rope(const void* q, const void* k, int32_t dtype, const int32_t* position
     const int64_t qw = (int64_t)n_heads * head_dim, kw = (int64_t)n_kv_heads * head_dim;
     if (n_heads > 0 && (!q || !q_out || q_stride < qw || q_out_stride < qw)) return LL_ERR_INVALID_ARG;
     if (n_kv_heads > 0 && (!k || !k_out || k_stride < kw || k_out_stride < kw)) return LL_ERR_INVALID_ARG;
-    const int64_t big = 1LL << 40;
+    const int64_t big = 1LL << 34;                    // (2^24 rows of 4-byte elements: byte offsets stay in 64 bits)
     if (q_stride > big || k_stride > big || q_out_stride > big || k_out_stride > big) return LL_ERR_UNSUPPORTED;
     const void* ptrs[4] = {n_heads ? q : nullptr, n_kv_heads ? k : nullptr, n_heads ? q_out : nullptr,
                            n_kv_heads ? k_out : nullptr};
     for (const void* p : ptrs)
         if (reinterpret_cast<uintptr_t>(p) % esz != 0) return LL_ERR_INVALID_ARG;
     // an output is its input itself (same rows), or shares no byte with either input or the other output
-    const auto span = [&](int64_t stride, int64_t width) { return (size_t)((tokens - 1) * stride + width) * esz; };
+    const Rows in[2] = {{q, q_stride, qw}, {k, k_stride, kw}}, out[2] = {{q_out, q_out_stride, qw}, {k_out, k_out_stride, kw}};
     const bool q_in = n_heads > 0 && q == q_out && q_stride == q_out_stride;
     const bool k_in = n_kv_heads > 0 && k == k_out && k_stride == k_out_stride;
-    if (n_heads > 0 && !q_in) {
-        if (overlap(q_out, span(q_out_stride, qw), q, span(q_stride, qw))) return LL_ERR_INVALID_ARG;
-        if (n_kv_heads > 0 && overlap(q_out, span(q_out_stride, qw), k, span(k_stride, kw))) return LL_ERR_INVALID_ARG;
-    }
-    if (n_kv_heads > 0 && !k_in) {
-        if (overlap(k_out, span(k_out_stride, kw), k, span(k_stride, kw))) return LL_ERR_INVALID_ARG;
-        if (n_heads > 0 && overlap(k_out, span(k_out_stride, kw), q, span(q_stride, qw))) return LL_ERR_INVALID_ARG;
-    }
+    const bool here[2] = {n_heads > 0, n_kv_heads > 0}, own[2] = {q_in, k_in};
+    for (int i = 0; i < 2; ++i)
+        for (int j = 0; j < 2; ++j)
+            if (here[i] && here[j] &&
+                ((!(i == j && own[i]) && rows_overlap(out[i], in[j], tokens, esz)) || (i < j && rows_overlap(out[i], out[j], tokens, esz))))
+                return LL_ERR_INVALID_ARG;
     ll::RopeArgs a{};
     a.q = q;
     a.k = k;
