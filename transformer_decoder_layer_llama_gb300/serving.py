@@ -271,9 +271,9 @@ class StackEngine:
     def compact(self, scheduler: Scheduler, stream) -> int:
         """Packs the blocks of the scheduler's requests to the front of every pool, and renames them in the
         scheduler and in the device table.  Waits for the stream; returns the number of blocks moved."""
-        self.table.copy_(torch.from_numpy(scheduler.table))
         stream.wait_stream(torch.cuda.current_stream())
-        with torch.cuda.stream(stream):
+        with torch.cuda.stream(stream):                       # behind the steps that still read the table
+            self.table.copy_(torch.from_numpy(scheduler.table))
             _, pairs, counts, block_map = self.api.compact_blocks(self.table, self.blocks.num_blocks,
                                                                   new_table=self.table, status=self.status)
             self.api.copy_blocks(self.blocks, pairs, n_pairs=counts[1:], status=self.status)
