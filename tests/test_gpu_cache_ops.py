@@ -788,3 +788,176 @@ def test_attention_of_zero_keys_and_a_zero_scale(d):
         want = C.attention_f8(f64(q[:3]), ref_pool, table, ctx, np.arange(4), scale)
         assert_attention(api.paged_attention_decode_f8(q[:3].cuda(), pool, dev(table), dev(ctx), scale, status=st), *want, d)
     check(st)
+
+
+def test_rope_into_columns_of_one_buffer():
+    """q, k, v and the rotated q and k all in one buffer: rows interleave, columns do not."""
+    T, H, Hkv, d = 37, 4, 2, 64
+    rng = np.random.default_rng(4)
+    w = (2 * H + 3 * Hkv) * d
+    x = torch.from_numpy(rng.normal(size=(T, w))).bfloat16().cuda()
+    col = lambda at, n: x[:, at * d:(at + n) * d].view(T, n, d)  # noqa: E731
+    q, k, v, q1, k1 = col(0, H), col(H, Hkv), col(H + Hkv, Hkv), col(H + 2 * Hkv, H), col(2 * H + 2 * Hkv, Hkv)
+    tab = api.rope_table(api.make_rope_config(d), 64)
+    pos = dev(np.arange(T))
+    want = api.rope(q.contiguous(), k.contiguous(), pos, tab)
+    kept = [t.clone() for t in (q, k, v)]
+    api.rope(q, k, pos, tab, q_out=q1, k_out=k1)
+    assert torch.equal(q1, want[0]) and torch.equal(k1, want[1])
+    assert all(torch.equal(a, b) for a, b in zip((q, k, v), kept))
+    api.rope(q, k, pos, tab, q_out=q, k_out=k)
+    assert torch.equal(q, want[0]) and torch.equal(k, want[1]) and torch.equal(v, kept[2])
+
+
+# ---------------------------------------------------------------- many sequences, other streams, graphs
+
+def test_many_sequences():
+    """More sequences than the lanes of a warp (40) and than CTAs of a wave (700): prompts, then single tokens."""
+    rng = np.random.default_rng(9)
+    bs, H, Hkv, d = 16, 8, 2, 64
+    before, new = rng.integers(0, 60, 40), rng.integers(0, 70, 40)
+    new[[0, 7, 39]], before[[3, 7]] = 0, 0
+    ctx = before + new
+    ref, table = make_cache(rng, list(ctx), Hkv, d, bs)
+    cu = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    q = torch.from_numpy(rng.normal(size=(int(cu[-1]) + 2, H, d))).bfloat16()
+    st = status()
+    out = torch.full(tuple(q.shape), 5.0, dtype=torch.bfloat16, device="cuda")
+    api.paged_attention_prefill_f8(q.cuda(), dev(cu), to_gpu(ref), dev(table), dev(ctx), d ** -0.5, max_new=int(new.max()),
+                                   out=out, status=st)
+    check(st)
+    assert_attention(out[:cu[-1]], *C.attention_f8(f64(q[:cu[-1]]), ref, table, ctx, cu, d ** -0.5), d)
+    assert (out[cu[-1]:] == 5).all()
+    B = 700
+    ctx = rng.integers(0, 50, B)
+    ctx[[1, 699]] = 0
+    ref, table = make_cache(rng, list(ctx), Hkv, d, bs, extra=B + 2)
+    free = iter(np.setdiff1d(np.arange(len(ref.k)), table[table >= 0]))
+    table = np.concatenate([table, np.full((B, 1), -1, np.int32)], 1)
+    for b in range(B):                        # a block for the token that starts one
+        if ctx[b] % bs == 0:
+            table[b, ctx[b] // bs] = next(free)
+    gpu, ctx = to_gpu(ref), ctx + 1
+    k, v = (bf16(rng.normal(size=(B, Hkv, d))) for _ in range(2))
+    ref.append(k, v, table, ctx, np.arange(B + 1))
+    api.append_to_cache_f8(*(torch.from_numpy(t).bfloat16().cuda() for t in (k, v)), gpu, dev(table), dev(ctx), status=st)
+    q = torch.from_numpy(rng.normal(size=(B, H, d))).bfloat16()
+    out = api.paged_attention_decode_f8(q.cuda(), gpu, dev(table), dev(ctx), d ** -0.5, status=st)
+    check(st)
+    assert_pool(gpu, ref)
+    assert_attention(out, *C.attention_f8(f64(q), ref, table, ctx, np.arange(B + 1), d ** -0.5), d)
+
+
+def small_batch(seed, d=64, bs=16, H=4, Hkv=2):
+    """Inputs of one run of the cache operators, and the run: name -> result.  Three sequences, 40 new tokens."""
+    rng = np.random.default_rng(seed)
+    ctx, new = [50, 20, 33], [20, 20, 0]
+    ref, table = make_cache(rng, ctx, Hkv, d, bs, poison=False)
+    cu = np.array([0, 20, 40, 40], np.int32)
+    x = dict(q=torch.from_numpy(rng.normal(size=(40, H, d))).bfloat16().cuda(), pool=to_gpu(ref),
+             k=torch.from_numpy(rng.normal(size=(40, Hkv, d))).bfloat16().cuda(), table=dev(table), ctx=dev(ctx), cu=dev(cu),
+             pos=dev(np.concatenate([np.arange(30, 50), np.arange(20)])), rope=api.rope_table(api.make_rope_config(d), 64),
+             pairs=dev([[int(table[0, 0]), len(ref.k) - 1]]), spare=api.PoolF8.empty(len(ref.k), Hkv, bs, d))
+    return x
+
+
+def run_small(x, **kw):
+    """Every operator once, everything that may be left out left out."""
+    q, k = api.rope(x["q"], x["k"], x["pos"], x["rope"], **kw)
+    yield api.append_to_cache_f8(k, x["k"], x["pool"], x["table"], x["ctx"], cu_new=x["cu"], max_new=20, **kw)
+    yield q
+    yield api.paged_attention_prefill_f8(q, x["cu"], x["pool"], x["table"], x["ctx"], 0.125, max_new=20, **kw)
+    yield api.paged_attention_decode_f8(q[:3], x["pool"], x["table"], x["ctx"], 0.125, **kw)
+    yield api.copy_blocks(api.BlockSet(x["pool"].tensors()), x["pairs"], **kw)
+    new_table, _, counts, block_map = api.compact_blocks(x["table"], len(x["pool"].k), **kw)
+    yield from (new_table, counts, block_map)
+    yield from (t.view(torch.uint8) for t in (x["pool"].k, x["pool"].v))
+
+
+def test_calls_on_a_stream_that_is_not_the_current_one():
+    """What a call makes itself is made on the current stream, which is busy here; the call's stream waits for it."""
+    want = [t.clone() for t in run_small(small_batch(1))]
+    x = small_batch(1)
+    bad = dev([[99, 0]])
+    blocks = api.BlockSet(x["spare"].tensors())
+    torch.cuda.synchronize()
+    stream = torch.cuda.Stream()
+    torch.cuda._sleep(100_000_000)                                       # about 50 ms
+    got = list(run_small(x, stream=stream))
+    st = api.copy_blocks(blocks, bad, stream=stream)
+    stream.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert int(st.item()) == api.LL_DEV_BAD_BLOCK                        # not cleared behind the kernel that set it
+    torch.cuda.synchronize()
+
+
+def test_captured_runs_replayed_side_by_side():
+    """Two captured runs of all operators, each with its own memory, replayed at once on two streams and with new
+    inputs: the results of the plain calls."""
+    sets, graphs, outs, streams = [small_batch(1), small_batch(2)], [], [], [torch.cuda.Stream() for _ in range(2)]
+    first = [{n: t.clone() for n, t in zip("kv", (x["pool"].k.view(torch.uint8), x["pool"].v.view(torch.uint8)))} for x in sets]
+    scales = [[x["pool"].k_scale.clone(), x["pool"].v_scale.clone()] for x in sets]
+    for x, s in zip(sets, streams):
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            outs.append(list(run_small(x)))
+        graphs.append(g)
+
+    def reset():
+        for x, f, sc in zip(sets, first, scales):
+            x["pool"].k.view(torch.uint8).copy_(f["k"])
+            x["pool"].v.view(torch.uint8).copy_(f["v"])
+            x["pool"].k_scale.copy_(sc[0])
+            x["pool"].v_scale.copy_(sc[1])
+
+    for turn in range(3):
+        if turn:
+            for x in sets:
+                x["q"].mul_(-0.5)
+                x["k"].mul_(1.5)
+        reset()
+        want = [[t.clone() for t in run_small(x)] for x in sets]
+        reset()
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for o, w in zip(outs, want):
+            assert all(torch.equal(a, b) for a, b in zip(o, w))
+
+
+def test_stack_compaction_waits_for_the_step_that_reads_the_table():
+    from transformer_decoder_layer_llama_gb300.serving import BlockAllocator, Scheduler, StackEngine
+    d, nb, mb, slots = synth.DIMS_TINY, 24, 4, 2
+    cfg = api.make_config(d, max_position=mb * d.block_size)
+    packed = [api.pack_weights(cfg, {k: v.cuda() for k, v in synth.make_weights(d, 0.02, seed=7).items()})]
+    pools = [api.PoolF8.empty(nb, d.n_kv_heads, d.block_size, d.head_dim)]
+    sch = Scheduler(slots, d.block_size, mb, BlockAllocator(nb, seed=5), seed=6, prompt_len=9)
+    eng = StackEngine(api, [cfg], packed, pools, slots, mb, slots * 9)
+    stream = torch.cuda.Stream()
+    for s in range(slots):
+        sch.start_resident(s, 9)
+    eng.pf_table.copy_(torch.from_numpy(sch.table))
+    eng.pf_ctx.fill_(9)
+    eng.pf_x.copy_(synth.make_x(slots * 9, d.hidden, seed=1))
+    torch.cuda.synchronize()
+    eng.prefill(slots, 9, stream)
+    eng.ctx.fill_(9)                          # the last position once more: the same codes and the same answer
+    eng.x.copy_(synth.make_x(slots, d.hidden, seed=2))
+    eng.table.copy_(torch.from_numpy(sch.table))
+    torch.cuda.synchronize()
+    eng.decode(stream)
+    stream.synchronize()
+    want = eng.decode(stream)
+    stream.synchronize()
+    want = want.clone()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(stream):
+        torch.cuda._sleep(100_000_000)
+    y = eng.decode(stream)
+    sch.retire(1)
+    eng.compact(sch, stream)                  # returns when the stream is done
+    assert torch.equal(y, want)
+    assert int(eng.status.item()) == 0

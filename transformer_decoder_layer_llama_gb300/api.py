@@ -567,6 +567,17 @@ def _call(name, fn, dev, stream, *args):
         raise LayerError(name, rc)
 
 
+def _made(stream, dev, *tensors):
+    """Tensors made here, on the device's current stream, for a call on `stream`: it waits for that stream, and
+    their memory is not handed out again before the call is done.  (None among them is passed over.)"""
+    current = torch.cuda.current_stream(dev)
+    tensors = [t for t in tensors if t is not None]
+    if tensors and stream != current:
+        stream.wait_stream(current)
+        for t in tensors:
+            t.record_stream(stream)
+
+
 def make_rope_config(rotary_dim, theta=10000.0, scaling="plain", factor=1.0, original_max_position=0, low_turns=1.0,
                      high_turns=None, attention_factor=0.0) -> ll_rope_config:
     """ll_rope_config.  scaling: "plain", "linear", "ntk", "banded" or "yarn"; high_turns defaults to 4
@@ -585,6 +596,8 @@ def rope_table(rope: ll_rope_config, max_position: int, device=None, stream=None
     if n == 0:
         raise LayerError("ll_rope_table_size", LL_ERR_INVALID_ARG)
     table = torch.empty(int(max_position), rope.rotary_dim // 2, 2, dtype=torch.float32, device=device or "cuda")
+    if stream is not None:
+        _made(stream, table.get_device(), table)
     _call("ll_rope_table", lib.ll_rope_table, table.get_device(), stream, ctypes.byref(rope), int(max_position), table.data_ptr(), n)
     return table
 
@@ -635,9 +648,13 @@ def rope(q, k, positions, table, layout="half", backward=False, q_out=None, k_ou
     rows = table.shape
     if len(rows) != 3 or rows[2] != 2 or not 2 <= 2 * rows[1] <= d:
         raise ValueError("table must be [max_position, rotary_dim / 2, 2] with rotary_dim <= head_dim")
-    if status is None:
+    own_status = status is None
+    if own_status:
         status = new_status(x.device)
     dev = _on(x, k, outs[0], outs[1], positions, table, status)
+    if stream is not None:
+        _made(stream, dev, outs[0] if q_out is None else None, outs[1] if k_out is None else None,
+              status if own_status else None)
     (qp, n_heads, qs, qo, qos), (kp, n_kv_heads, ks, ko, kos) = ends
     _call("ll_rope", lib.ll_rope, dev, stream, qp, kp, LL_F32 if x.dtype == torch.float32 else LL_BF16,
           positions.data_ptr(), T, n_heads, n_kv_heads, d, 2 * rows[1], LL_ROPE_LAYOUTS[layout],
@@ -700,9 +717,12 @@ def append_to_cache_f8(k, v, pool: PoolF8, block_table, context_lens, cu_new=Non
     B = _f8_batch(pool, block_table, context_lens)
     if cu_new is not None:
         _need(cu_new, "cu_new", torch.int32, shape=(B + 1,))
-    if status is None:
+    own_status = status is None
+    if own_status:
         status = new_status(k.device)
     dev = _on(k, v, pool.k, block_table, context_lens, cu_new, status)
+    if stream is not None and own_status:
+        _made(stream, dev, status)
     _call("ll_append_to_cache_f8", lib.ll_append_to_cache_f8, dev, stream, k.data_ptr(), v.data_ptr(), ks, vs,
           cu_new.data_ptr() if cu_new is not None else None, k.shape[0], context_lens.data_ptr(), B, int(max_new),
           k.shape[1], k.shape[2], pool.block_size, ctypes.byref(pool.c()), block_table.data_ptr(),
@@ -719,8 +739,9 @@ def attention_prefill_f8_workspace_size(batch, tokens, max_new, n_heads, n_kv_he
                                                       int(n_kv_heads), int(head_dim))
 
 
-def _f8_attention(q, pool, out, workspace, status, size):
+def _f8_attention(q, pool, out, workspace, status, size, stream):
     """Checks q, out and the workspace of an attention call; makes what was not passed."""
+    given = out, workspace, status
     _need(q, "q", torch.bfloat16)
     if q.dim() != 3 or q.shape[2] != pool.k.shape[3]:
         raise ValueError(f"q must be [rows, n_heads, {pool.k.shape[3]}], got {tuple(q.shape)}")
@@ -734,6 +755,8 @@ def _f8_attention(q, pool, out, workspace, status, size):
         _need(workspace, "workspace", torch.uint8)
     if status is None:
         status = new_status(q.device)
+    if stream is not None:
+        _made(stream, q.get_device(), *(t if g is None else None for g, t in zip(given, (out, workspace, status))))
     return out, workspace, status
 
 
@@ -743,7 +766,8 @@ def paged_attention_decode_f8(q, pool: PoolF8, block_table, context_lens, scale,
     B = _f8_batch(pool, block_table, context_lens)
     Hkv = pool.k.shape[1]
     out, workspace, status = _f8_attention(
-        q, pool, out, workspace, status, lambda: attention_decode_f8_workspace_size(B, q.shape[1], Hkv, q.shape[2]))
+        q, pool, out, workspace, status, lambda: attention_decode_f8_workspace_size(B, q.shape[1], Hkv, q.shape[2]),
+        stream)
     if q.shape[0] != B:
         raise ValueError(f"q must have {B} rows, one per sequence")
     dev = _on(q, pool.k, block_table, context_lens, out, workspace, status)
@@ -762,7 +786,7 @@ def paged_attention_prefill_f8(q, cu_new, pool: PoolF8, block_table, context_len
     Hkv = pool.k.shape[1]
     out, workspace, status = _f8_attention(
         q, pool, out, workspace, status,
-        lambda: attention_prefill_f8_workspace_size(B, q.shape[0], max_new, q.shape[1], Hkv, q.shape[2]))
+        lambda: attention_prefill_f8_workspace_size(B, q.shape[0], max_new, q.shape[1], Hkv, q.shape[2]), stream)
     dev = _on(q, pool.k, cu_new, block_table, context_lens, out, workspace, status)
     _call("ll_paged_attention_prefill_f8", lib.ll_paged_attention_prefill_f8, dev, stream, q.data_ptr(), cu_new.data_ptr(), q.shape[0],
           ctypes.byref(pool.c()), block_table.data_ptr(), block_table.shape[1], context_lens.data_ptr(), B,
@@ -779,7 +803,8 @@ def new_workspace_f8(cfg, max_tokens, max_blocks, device=None):
     return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
 
 
-def _layer_f8(cfg, packed, x, pool, block_table, context_lens, tokens, y, workspace, status):
+def _layer_f8(cfg, packed, x, pool, block_table, context_lens, tokens, y, workspace, status, stream):
+    given = y, workspace, status
     _need(packed, "packed", torch.uint8)
     _need(x, "x", torch.bfloat16, shape=(tokens, cfg.hidden))
     if tuple(pool.k.shape[1:]) != (cfg.n_kv_heads, cfg.block_size, cfg.head_dim):
@@ -794,7 +819,10 @@ def _layer_f8(cfg, packed, x, pool, block_table, context_lens, tokens, y, worksp
         _need(workspace, "workspace", torch.uint8)
     if status is None:
         status = new_status(x.device)
-    return y, workspace, status, _on(x, packed, pool.k, block_table, context_lens, y, workspace, status)
+    dev = _on(x, packed, pool.k, block_table, context_lens, y, workspace, status)
+    if stream is not None:
+        _made(stream, dev, *(t if g is None else None for g, t in zip(given, (y, workspace, status))))
+    return y, workspace, status, dev
 
 
 def layer_prefill_f8(cfg, packed, x, pool: PoolF8, block_table, context_lens, seq_len, y=None, workspace=None,
@@ -803,7 +831,7 @@ def layer_prefill_f8(cfg, packed, x, pool: PoolF8, block_table, context_lens, se
     positions.  Returns y."""
     B = _f8_batch(pool, block_table, context_lens)
     y, workspace, status, dev = _layer_f8(cfg, packed, x, pool, block_table, context_lens, B * int(seq_len), y,
-                                          workspace, status)
+                                          workspace, status, stream)
     _call("ll_layer_prefill_f8", lib.ll_layer_prefill_f8, dev, stream, ctypes.byref(cfg), packed.data_ptr(),
           x.data_ptr(), context_lens.data_ptr(), B, int(seq_len), ctypes.byref(pool.c()), block_table.data_ptr(),
           block_table.shape[1], y.data_ptr(), workspace.data_ptr(), workspace.numel(), status.data_ptr())
@@ -814,7 +842,8 @@ def layer_decode_step_f8(cfg, packed, x, pool: PoolF8, block_table, context_lens
                          stream=None):
     """ll_layer_decode_step_f8: x BF16 [batch, hidden], one new token per sequence.  Returns y."""
     B = _f8_batch(pool, block_table, context_lens)
-    y, workspace, status, dev = _layer_f8(cfg, packed, x, pool, block_table, context_lens, B, y, workspace, status)
+    y, workspace, status, dev = _layer_f8(cfg, packed, x, pool, block_table, context_lens, B, y, workspace, status,
+                                          stream)
     _call("ll_layer_decode_step_f8", lib.ll_layer_decode_step_f8, dev, stream, ctypes.byref(cfg), packed.data_ptr(),
           x.data_ptr(), ctypes.byref(pool.c()), block_table.data_ptr(), block_table.shape[1], context_lens.data_ptr(),
           B, y.data_ptr(), workspace.data_ptr(), workspace.numel(), status.data_ptr())
@@ -852,9 +881,12 @@ def copy_blocks(blocks: BlockSet, pairs, n_pairs=None, status=None, stream=None)
         _need(n_pairs, "n_pairs", torch.int32)
         if n_pairs.numel() != 1:
             raise ValueError("n_pairs must hold one number")
-    if status is None:
+    own_status = status is None
+    if own_status:
         status = new_status(blocks.device)
     dev = _on(blocks.tensors[0], pairs, n_pairs, status)
+    if stream is not None and own_status:
+        _made(stream, dev, status)
     _call("ll_copy_blocks", lib.ll_copy_blocks, dev, stream, blocks._c, len(blocks.tensors), blocks.num_blocks, pairs.data_ptr(),
           pairs.shape[0], n_pairs.data_ptr() if n_pairs is not None else None, status.data_ptr())
     return status
@@ -871,6 +903,7 @@ def compact_blocks(block_table, num_blocks, new_table=None, pairs=None, counts=N
         raise ValueError("block_table must be [rows, max_blocks]")
     dev = block_table.device
     new = lambda *shape: torch.empty(shape, dtype=torch.int32, device=dev)  # noqa: E731
+    given = new_table, pairs, counts, block_map, status
     new_table = new(*block_table.shape) if new_table is None else new_table
     pairs = new(num_blocks // 2, 2) if pairs is None else pairs
     counts = new(2) if counts is None else counts
@@ -882,6 +915,8 @@ def compact_blocks(block_table, num_blocks, new_table=None, pairs=None, counts=N
     if status is None:
         status = new_status(dev)
     dev = _on(block_table, new_table, pairs, counts, block_map, status)
+    if stream is not None:
+        _made(stream, dev, *(t if g is None else None for g, t in zip(given, (new_table, pairs, counts, block_map, status))))
     _call("ll_compact_blocks", lib.ll_compact_blocks, dev, stream, block_table.data_ptr(), block_table.shape[0], block_table.shape[1],
           num_blocks, new_table.data_ptr(), pairs.data_ptr(), counts.data_ptr(), block_map.data_ptr(),
           status.data_ptr())
