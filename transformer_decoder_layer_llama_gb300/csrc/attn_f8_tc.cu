@@ -51,7 +51,9 @@ template <int D>
 struct PfLayout {
     static constexpr uint32_t TILE = kPfRows * D * 2;       // [D / 64][128 rows][128 B] FP16
     static constexpr uint32_t OFF_Q = 0;                    // A, B
-    static constexpr uint32_t OFF_K = 2 * TILE, OFF_V = 4 * TILE, TOTAL = 6 * TILE;   // two buffers each
+    static constexpr uint32_t OFF_K = 2 * TILE, OFF_V = 4 * TILE;   // two buffers each
+    static constexpr uint32_t CODES = kPfKeys * D;          // a tile of codes as it lies in the pool
+    static constexpr uint32_t OFF_CK = 6 * TILE, OFF_CV = OFF_CK + CODES, TOTAL = OFF_CV + CODES;
     static constexpr uint32_t TMEM_S = 0, TMEM_O = 256, TMEM_COLS = 512;              // A, B 128 columns on
 };
 
@@ -157,19 +159,6 @@ LL_DEVINL float max3(float a, float b, float c) {
     float d;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
-}
-
-// 16 bytes of global memory that no kernel running now writes, or zeros: predicated, so that a run of such
-// loads issues without branches.
-LL_DEVINL uint4 load16_if(const void* p, bool take) {
-    uint4 v;
-    asm volatile(
-        "{\n .reg .pred p;\n setp.ne.u32 p, %5, 0;\n mov.b32 %0, 0;\n mov.b32 %1, 0;\n mov.b32 %2, 0;\n mov.b32 %3, 0;\n"
-        " @p ld.global.v4.u32 {%0, %1, %2, %3}, [%4];\n}\n"
-        : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
-        : "l"(p), "r"((uint32_t)take)
-        : "memory");
-    return v;
 }
 
 // The larger magnitude in each half (a NaN loses to a number).
@@ -314,10 +303,12 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
     // (ready), read by both query tiles (empty).  Scales of key tile j sit in slot j & 3: slot and barrier
     // are written again for tile j + 4, after the S of tile j + 2, which waits for the P of tile j + 1.
     __shared__ uint64_t q_ready[2], s_full[2], p_ready[2][2], turn_done[2], o_done[2], k_ready[2], k_empty[2], v_ready[2], v_empty[2];
-    __shared__ uint64_t meta_ready[kPfMeta], drain[2];
+    // Codes of a key tile: brought in (full), read by the converters (empty).
+    __shared__ uint64_t meta_ready[kPfMeta], drain[2], c_full[2], c_empty[2];
     __shared__ uint32_t tmem_base_s;
     __shared__ int abort_s;
     __shared__ __align__(16) float ks_s[kPfMeta][kPfChunks];   // per 16-key chunk: K scale
+    __shared__ float vs_s[kPfMeta][kPfChunks];              // and V scale
     __shared__ uint32_t ok_s[kPfMeta];                      // bit c = chunk c is backed by a valid block
     __shared__ int vexp_w[4], vexp_s;                       // exponent of the item's largest V scale
 
@@ -336,6 +327,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
             mbar_init(&drain[i], 1);
             mbar_init(&v_ready[i], 4);
             mbar_init(&v_empty[i], 2);
+            mbar_init(&c_full[i], 1);
+            mbar_init(&c_empty[i], 4);
         }
         for (int i = 0; i < kPfMeta; ++i) mbar_init(&meta_ready[i], 1);
         abort_s = 0;
@@ -451,6 +444,60 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
                 volatile int never = 0;
                 mbar_wait_bounded(&drain[x], 0, &never, status);
             }
+        } else if (warp == 14) {
+            // ------------------------------------------------ codes and scales
+            const int32_t* table_row = a.block_table + (size_t)it.b * a.max_blocks;
+            const int key0 = first * kPfKeys;
+            const int my_key = (lane & 7) * 16;                 // lane c < 8 looks after 16-key chunk c of a tile
+            const int bs_log2 = 31 - __clz(a.block_size);       // (a power of two: no divisions on this path)
+            auto entry_of = [&](int j) {                        // its table entry (-1 past the keys)
+                const int key = j * kPfKeys + my_key;
+                return j < n_kt && key < kv_end ? table_row[(key0 + key) >> bs_log2] : -1;
+            };
+            auto row_of = [&](int j, int entry) {               // its first pool row (-1: no valid block)
+                const int key = j * kPfKeys + my_key;
+                const bool want = j < n_kt && key < kv_end;
+                if (want && (entry < 0 || entry >= a.num_blocks)) flag_status(status, LL_DEV_BAD_BLOCK);
+                return want && entry >= 0 && entry < a.num_blocks
+                           ? ((entry * a.n_kv_heads + it.hk) << bs_log2) + ((key0 + key) & (a.block_size - 1)) : -1;
+            };
+            auto scale_of = [&](const float* scales, int row) {
+                return row >= 0 ? scales[row >> bs_log2] : 0.f;
+            };
+            auto bring = [&](int which, const uint8_t* pool, int j, int row, uint32_t mask) {
+                if (lane == 0) mbar_arrive_expect_tx(&c_full[which], (uint32_t)__popc(mask) * 16u * D);
+                __syncwarp();
+                if (lane < kPfChunks && row >= 0)
+                    bulk_load(smem + (which ? L::OFF_CV : L::OFF_CK) + lane * 16 * D, pool + (size_t)(uint32_t)row * D, 16u * D,
+                              &c_full[which]);
+            };
+            auto taken = [&](int which, int j) {            // by the converters: the codes of the tile before
+                return j == 0 || __all_sync(0xffffffffu, mbar_wait_bounded(&c_empty[which], (uint32_t)(j - 1) & 1u, &abort_s, status));
+            };
+            int entry = entry_of(0), k_at = -1, v_at = -1;
+            for (int j = 0; j < n_kt; ++j) {
+                const int row = row_of(j, entry), slot = j & (kPfMeta - 1);
+                const float ks = scale_of(a.k_scale, row), vs = scale_of(a.v_scale, row);
+                entry = entry_of(j + 1);
+                const uint32_t mask = __ballot_sync(0xffffffffu, lane < kPfChunks && row >= 0);
+                if (!taken(0, j)) break;
+                if (lane < kPfChunks) {
+                    ks_s[slot][lane] = ks;
+                    vs_s[slot][lane] = vs;
+                }
+                if (lane == 0) ok_s[slot] = mask;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&meta_ready[slot]);
+                bring(0, a.k_pool, j, row, mask);
+                k_at = j;
+                if (!taken(1, j)) break;
+                bring(1, a.v_pool, j, row, mask);
+                v_at = j;
+            }
+            // no copy is in flight when the CTA leaves
+            volatile int never = 0;
+            if (k_at >= 0) mbar_wait_bounded(&c_full[0], (uint32_t)k_at & 1u, &never, status);
+            if (v_at >= 0) mbar_wait_bounded(&c_full[1], (uint32_t)v_at & 1u, &never, status);
         }
         __syncwarp();
     } else if (warp >= 8) {
@@ -458,41 +505,28 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
         asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
         constexpr int LANES = D / 16, ROWS = 128 / LANES, PER = kPfKeys / ROWS;   // lanes per row, rows per step, steps
         const int tid = threadIdx.x - 256;
-        // Eight lanes that store together cover four 16-code pieces of two rows: their 16-byte chunks are 0, 2,
-        // 4, 6 of an even and an odd row, which the swizzle puts on different banks.
-        const int c16 = D == 128 ? (tid & 3) | ((tid >> 1) & 4) : tid & 3;
-        const int rsub = D == 128 ? ((tid >> 2) & 1) | ((tid >> 3) & ~1) : tid >> 2;
-        const int32_t* table_row = a.block_table + (size_t)it.b * a.max_blocks;
-        const int key0 = first * kPfKeys;
-        const int my_key = (lane & 7) * 16;                 // lane c < 8 looks after 16-key chunk c of a tile
-        const int bs_log2 = 31 - __clz(a.block_size);       // (a power of two: no divisions on this path)
-        auto entry_of = [&](int j) {                        // its table entry (-1 past the keys)
-            const int key = j * kPfKeys + my_key;
-            return j < n_kt && key < kv_end ? table_row[(key0 + key) >> bs_log2] : -1;
-        };
-        auto row_of = [&](int j, int entry) {               // its first pool row (-1: no valid block)
-            const int key = j * kPfKeys + my_key;
-            const bool want = j < n_kt && key < kv_end;
-            if (want && (entry < 0 || entry >= a.num_blocks)) flag_status(status, LL_DEV_BAD_BLOCK);
-            return want && entry >= 0 && entry < a.num_blocks
-                       ? ((entry * a.n_kv_heads + it.hk) << bs_log2) + ((key0 + key) & (a.block_size - 1)) : -1;
-        };
-        auto scale_of = [&](const float* scales, int row) {
-            return row >= 0 ? scales[row >> bs_log2] : 0.f;
-        };
-        auto load = [&](const uint8_t* pool, int j, int row_lane, uint4 (&w)[PER]) {
-            const int left = kv_end - j * kPfKeys;          // keys of the tile
-            int row[PER];
-#pragma unroll
-            for (int i = 0; i < PER; ++i) row[i] = __shfl_sync(0xffffffffu, row_lane, (i * ROWS + rsub) >> 4);
-#pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                const int r = i * ROWS + rsub;             // rows that hold no key become zeros: 0 * stale stays 0
-                w[i] = load16_if(pool + (size_t)(uint32_t)(row[i] + (r & 15)) * D + c16 * 16, row[i] >= 0 && r < left);
-            }
-        };
+        // Eight lanes that load or store together: D = 128: four 16-code pieces of an even row and the other four of
+        // the row behind it; D = 64: two rows.  So the codes' chunks are on different banks, and so are the operand's:
+        // 0, 2, 4, 6 of an even and an odd row, which the swizzle tells apart.
+        const int c16 = D == 128 ? (tid & 3) | (((tid ^ (tid >> 1)) & 4)) : tid & 3;
+        const int rsub = D == 128 ? ((tid >> 3) & ~1) | ((tid >> 2) & 1) : tid >> 2;
         const uint32_t st0 = pf_off(rsub, 2 * c16), st1 = pf_off(rsub, 2 * c16 + 1);
-        auto store = [&](uint8_t* tile, const uint4 (&w)[PER], bool scaled, float ratio_lane) {
+        // Tile j from its codes to the operand tile; rows that hold no key become zeros: 0 * stale stays 0.
+        auto convert = [&](uint8_t* tile, const uint8_t* codes, int j, uint64_t* done, bool scaled, float up0, float up1) {
+            const int slot = j & (kPfMeta - 1), left = kv_end - j * kPfKeys;
+            const uint32_t chunks = ok_s[slot];
+            uint4 w[PER];
+#pragma unroll
+            for (int i = 0; i < PER; ++i) w[i] = *reinterpret_cast<const uint4*>(codes + (i * ROWS + rsub) * D + c16 * 16);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(done);
+            if (left < kPfKeys || chunks != (1u << kPfChunks) - 1u) {
+#pragma unroll
+                for (int i = 0; i < PER; ++i) {
+                    const int r = i * ROWS + rsub;
+                    if (r >= left || !((chunks >> (r >> 4)) & 1u)) w[i] = make_uint4(0u, 0u, 0u, 0u);
+                }
+            }
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
                 uint32_t h[8];
@@ -501,7 +535,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
                 e4m3x4_to_f16x4(w[i].z, h[4], h[5]);
                 e4m3x4_to_f16x4(w[i].w, h[6], h[7]);
                 if (scaled) {
-                    const __half2 f = __float2half2_rn(__shfl_sync(0xffffffffu, ratio_lane, (i * ROWS + rsub) >> 4));
+                    const __half2 f = __float2half2_rn(vs_s[slot][(i * ROWS + rsub) >> 4] * up0 * up1);
 #pragma unroll
                     for (int x = 0; x < 8; ++x) {
                         const __half2 p = __hmul2(*reinterpret_cast<const __half2*>(&h[x]), f);
@@ -514,35 +548,18 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
             fence_async_smem();
             __syncwarp();
         };
-        uint4 kw[PER], vw[PER];
-        const int entry0 = entry_of(0);
-        int entry = entry_of(1);                            // of the tile after the one in registers
-        int row = row_of(0, entry0);
-        load(a.k_pool, 0, row, kw);
-        load(a.v_pool, 0, row, vw);
-        float ks = scale_of(a.k_scale, row), vs = scale_of(a.v_scale, row);
         float up0 = 0.f, up1 = 0.f;                         // 2^(6 - E) as two factors
         for (int j = 0; j < n_kt; ++j) {
-            // (whole warps leave: the loads below shuffle)
-            if (j > 1 && !__all_sync(0xffffffffu, mbar_wait_bounded(&k_empty[j & 1], (uint32_t)((j - 2) >> 1) & 1u, &abort_s, status)))
-                break;
-            store(smem + L::OFF_K + (uint32_t)(j & 1) * L::TILE, kw, false, 0.f);
-            if (warp == 8) {
-                const uint32_t m = __ballot_sync(0xffffffffu, row >= 0);
-                if (lane < kPfChunks) ks_s[j & (kPfMeta - 1)][lane] = ks;
-                if (lane == 0) ok_s[j & (kPfMeta - 1)] = m & ((1u << kPfChunks) - 1u);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&meta_ready[j & (kPfMeta - 1)]);
-            }
+            // (whole warps leave)
+            bool ok = (j < 2 || mbar_wait_bounded(&k_empty[j & 1], (uint32_t)((j - 2) >> 1) & 1u, &abort_s, status)) &&
+                      mbar_wait_bounded(&c_full[0], (uint32_t)j & 1u, &abort_s, status);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            convert(smem + L::OFF_K + (uint32_t)(j & 1) * L::TILE, smem + L::OFF_CK, j, &c_empty[0], false, 0.f, 0.f);
             if (lane == 0) mbar_arrive(&k_ready[j & 1]);
-            // Each value is loaded into the variable whose last use is behind it: a copy at the loop's end
-            // would wait for the load.
-            row = row_of(j + 1, entry);
-            entry = entry_of(j + 2);
-            load(a.k_pool, j + 1, row, kw);
-            ks = scale_of(a.k_scale, row);
             if (j == 0) {
                 // exponent of the largest V scale of the CTA's keys
+                const int32_t* table_row = a.block_table + (size_t)it.b * a.max_blocks;
+                const int key0 = first * kPfKeys, bs_log2 = 31 - __clz(a.block_size);
                 const int n = (key0 + min(kv_end, n_kt * kPfKeys) + a.block_size - 1) >> bs_log2;
                 float top = 0.f;
                 for (int i = (key0 >> bs_log2) + tid; i < n; i += 128) {
@@ -558,12 +575,11 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
                 up0 = __uint_as_float((uint32_t)(e0 + 127) << 23);
                 up1 = __uint_as_float((uint32_t)(e1 + 127) << 23);
             }
-            if (j > 1 && !__all_sync(0xffffffffu, mbar_wait_bounded(&v_empty[j & 1], (uint32_t)((j - 2) >> 1) & 1u, &abort_s, status)))
-                break;
-            store(smem + L::OFF_V + (uint32_t)(j & 1) * L::TILE, vw, true, vs * up0 * up1);
+            ok = (j < 2 || mbar_wait_bounded(&v_empty[j & 1], (uint32_t)((j - 2) >> 1) & 1u, &abort_s, status)) &&
+                 mbar_wait_bounded(&c_full[1], (uint32_t)j & 1u, &abort_s, status);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            convert(smem + L::OFF_V + (uint32_t)(j & 1) * L::TILE, smem + L::OFF_CV, j, &c_empty[1], true, up0, up1);
             if (lane == 0) mbar_arrive(&v_ready[j & 1]);
-            load(a.v_pool, j + 1, row, vw);
-            vs = scale_of(a.v_scale, row);
         }
         __syncwarp();
     } else {
