@@ -707,6 +707,12 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
             }
             const float base = (m_used == -INFINITY ? 0.f : m_used) - kPfBase;
             const float2 nb = make_float2(-base, -base);
+            auto hand_over = [&](int half) {                // what is stored of P, to the tensor core
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_ready[x][half]);
+            };
 #pragma unroll
             for (int c2 = 0; c2 < kPfChunks; c2 += 2) {     // 32 keys: 16 columns of P, over S
                 uint32_t p[16];
@@ -723,13 +729,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
                         p[8 * h + i] = pack_f16x2(e.x, e.y);
                     }
                 }
+                // the first 64 keys are waited for beside the work on the 32 behind them
+                if (c2 == 4) hand_over(0);
                 tmem_st16_issue(ts + (uint32_t)c2 * 8u, p);
-                if (c2 % 4 == 2) {                          // 64 keys are there
-                    tmem_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&p_ready[x][c2 / 4]);
-                }
+                if (c2 == 6) hand_over(1);
             }
         }
         const size_t prow = (size_t)blockIdx.x * 2 * kPfRows + x * kPfRows + r;
