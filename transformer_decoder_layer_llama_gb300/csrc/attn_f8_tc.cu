@@ -247,11 +247,14 @@ LL_DEVINL bool pf_item(const AttnF8Args& a, int i, int n_mt, int tt, bool flag, 
         const int lane = threadIdx.x & 31;
         PfSeq mine{0, 0, 0};
         if (lane < a.batch) mine = pf_seq(a, lane, flag && i == 0);
-        const int items = (mine.n + step - 1) / step;
+        // x / step for 0 <= x < 2^30, exactly: step <= 256, so x times what 2^38 / step is rounded up by stays below 2^38
+        const unsigned long long per = (1ull << 38) / (unsigned)step + 1;
+        const auto steps_of = [&](int x) { return (int)((unsigned long long)x * per >> 38); };
+        const int items = steps_of(mine.n + step - 1);
         // this lane's items with more than t key tiles: those whose last key lies beyond 128 t
         const auto longer = [&](int t) {
             const int x = t * kPfKeys - mine.pos0;
-            return x < 0 ? items : x >= mine.n ? 0 : items - x / step;
+            return x < 0 ? items : x >= mine.n ? 0 : items - steps_of(x);
         };
         int lo = 0;                                         // (longer than lo - 1: more than k items, or lo = 0)
         int hi = __reduce_max_sync(0xffffffffu, mine.n ? (mine.pos0 + mine.n + kPfKeys - 1) / kPfKeys : 0);
@@ -502,7 +505,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
         __syncwarp();
     } else if (warp >= 8) {
         // ---------------------------------------------------- keys and values (warps 8-11)
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
         constexpr int LANES = D / 16, ROWS = 128 / LANES, PER = kPfKeys / ROWS;   // lanes per row, rows per step, steps
         const int tid = threadIdx.x - 256;
         // Eight lanes that load or store together: D = 128: four 16-code pieces of an even row and the other four of
@@ -584,7 +587,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
         __syncwarp();
     } else {
         // ---------------------------------------------------- softmax (warps 0-3: tile A, 4-7: tile B)
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
         const int x = warp >> 2;
         const int r = threadIdx.x & 127;                    // query row = TMEM lane
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
