@@ -18,6 +18,7 @@ namespace ll {
 namespace {
 
 constexpr int kRopeThreads = 256;
+constexpr int kRopeHeads = 4;               // of a thread
 
 template <typename T>
 struct Vec;   // 16 bytes of T as float32
@@ -217,21 +218,16 @@ cudaError_t rope_for(const RopeArgs& a, cudaStream_t stream) {
     if (vec) {
         const int lanes_rot = a.interleaved ? a.rotary_dim / N : a.rotary_dim / (2 * N);
         const int lanes = lanes_rot + (a.copy_tail ? (a.head_dim - a.rotary_dim) / N : 0);
-        // Few tokens: one head per thread spreads them over the most CTAs.  Many: four heads per
-        // thread keep more loads in flight and read each table row less often.
-        const bool wide = (long long)a.tokens * H * lanes > 4LL * 2048 * std::max(1, device_sm_count());
-        // head rows of a CTA: as even a split of the heads as the CTA's threads allow
-        const int u = wide ? 4 : 1, most = std::max(1, kRopeThreads / lanes);
-        const int parts = (H + u * most - 1) / (u * most);
-        const int rows = (H + u * parts - 1) / (u * parts);
+        // Four heads per thread keep their loads in flight together and read a table row once (16384 tokens of 40
+        // heads: 57 us, with one head per thread 61; up to 2048 tokens there is no difference).  Head rows of a CTA:
+        // as even a split of the heads as the CTA's threads allow.
+        const int most = std::max(1, kRopeThreads / lanes);
+        const int parts = (H + kRopeHeads * most - 1) / (kRopeHeads * most);
+        const int rows = (H + kRopeHeads * parts - 1) / (kRopeHeads * parts);
         const int threads = (rows * lanes + 31) / 32 * 32;
         const dim3 grid((unsigned)a.tokens, (unsigned)parts);
-        if (a.interleaved)
-            e = wide ? launch_pdl(rope_vec_kernel<T, false, 4>, grid, dim3(threads), 0, stream, 1, a, lanes_rot, lanes, rows)
-                     : launch_pdl(rope_vec_kernel<T, false, 1>, grid, dim3(threads), 0, stream, 1, a, lanes_rot, lanes, rows);
-        else
-            e = wide ? launch_pdl(rope_vec_kernel<T, true, 4>, grid, dim3(threads), 0, stream, 1, a, lanes_rot, lanes, rows)
-                     : launch_pdl(rope_vec_kernel<T, true, 1>, grid, dim3(threads), 0, stream, 1, a, lanes_rot, lanes, rows);
+        e = a.interleaved ? launch_pdl(rope_vec_kernel<T, false, kRopeHeads>, grid, dim3(threads), 0, stream, 1, a, lanes_rot, lanes, rows)
+                          : launch_pdl(rope_vec_kernel<T, true, kRopeHeads>, grid, dim3(threads), 0, stream, 1, a, lanes_rot, lanes, rows);
     } else {
         const long long units = (long long)H * (a.rotary_dim / 2 + (a.copy_tail ? a.head_dim - a.rotary_dim : 0));
         const unsigned y = (unsigned)std::min<long long>(16, (units + kRopeThreads - 1) / kRopeThreads);
