@@ -780,9 +780,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
     if (warp == 12) tmem_dealloc(tmem, L::TMEM_COLS);
 }
 
-// Joins the partials of item blockIdx.x; blockIdx.y takes 32 of its 256 query rows, D / 4 lanes to a row.
+// Joins the partials of item blockIdx.x: D / 4 lanes to a query row, as many rows per CTA as its threads allow.  A thread
+// takes the partials four at a time, so that their loads are in flight together (one after the other, and four rows
+// to a thread, 16 tokens behind 32768 of a 70B-shaped layer took 36 us here).
 constexpr int kPfJoinThreads = 256;
-constexpr int kPfJoinRows = 32;
 __global__ void __launch_bounds__(kPfJoinThreads) attn_prefill_f8_join_kernel(const AttnF8Args a, int n_mt, int tt, int ns) {
     pdl_wait();
     pdl_trigger();
@@ -791,32 +792,43 @@ __global__ void __launch_bounds__(kPfJoinThreads) attn_prefill_f8_join_kernel(co
     const int splits = pf_splits(ns, it.n_kt);
     if (splits == 1) return;
     const int D = a.head_dim, G = a.n_heads / a.n_kv_heads;
-    const int lanes = D / 4, lane = threadIdx.x % lanes;
-    for (int i = threadIdx.x / lanes; i < kPfJoinRows; i += kPfJoinThreads / lanes) {
-        const int row = (int)blockIdx.y * kPfJoinRows + i, x = row / kPfRows, r = row % kPfRows;
-        if (r / G >= (x ? it.nt_b : it.nt_a)) continue;
-        const size_t pr = (size_t)blockIdx.x * ns * 2 * kPfRows + row;
-        float M = -INFINITY;
-        for (int k = 0; k < splits; ++k) M = fmaxf(M, a.part_ml[pr + (size_t)k * 2 * kPfRows].x);
-        const float base = M == -INFINITY ? 0.f : M;
-        float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
-        float den = 0.f;
-        for (int k = 0; k < splits; ++k) {
-            const size_t pk = pr + (size_t)k * 2 * kPfRows;
-            const float2 ml = a.part_ml[pk];
-            if (ml.y == 0.f) continue;                     // no key there; its row may not be written
-            const float w = exp2f(ml.x - base) * ml.y;
-            const float4 o = *reinterpret_cast<const float4*>(a.part_o + pk * D + lane * 4);
-            num.x += w * o.x;
-            num.y += w * o.y;
-            num.z += w * o.z;
-            num.w += w * o.w;
+    const int lanes = D / 4, col = (int)threadIdx.x % lanes * 4;
+    const int row = (int)blockIdx.y * (kPfJoinThreads / lanes) + (int)threadIdx.x / lanes, x = row / kPfRows, r = row % kPfRows;
+    if (r / G >= (x ? it.nt_b : it.nt_a)) return;
+    const size_t pr = (size_t)blockIdx.x * ns * 2 * kPfRows + row;
+    float M = -INFINITY, den = 0.f;
+    float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < splits; k += 4) {
+        float2 ml[4];
+        float4 o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const size_t pk = pr + (size_t)min(k + i, splits - 1) * 2 * kPfRows;
+            ml[i] = k + i < splits ? a.part_ml[pk] : make_float2(-INFINITY, 0.f);
+            o[i] = *reinterpret_cast<const float4*>(a.part_o + pk * D + col);
+        }
+        const float mn = fmaxf(M, fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)));
+        const float base = mn == -INFINITY ? 0.f : mn, old = exp2f(M - base);
+        num.x *= old;
+        num.y *= old;
+        num.z *= old;
+        num.w *= old;
+        den *= old;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (ml[i].y == 0.f) continue;                  // no key there: what was read may be anything
+            const float w = exp2f(ml[i].x - base) * ml[i].y;
+            num.x += w * o[i].x;
+            num.y += w * o[i].y;
+            num.z += w * o[i].z;
+            num.w += w * o[i].w;
             den += w;
         }
-        const float inv = den == 0.f ? 0.f : 1.f / den;
-        *reinterpret_cast<uint2*>(a.out + (((size_t)it.tok0 + x * tt + r / G) * a.n_heads + (size_t)it.hk * G + r % G) * D + lane * 4) =
-            make_uint2(pack_bf16x2(num.x * inv, num.y * inv), pack_bf16x2(num.z * inv, num.w * inv));
+        M = mn;
     }
+    const float inv = den == 0.f ? 0.f : 1.f / den;
+    *reinterpret_cast<uint2*>(a.out + (((size_t)it.tok0 + x * tt + r / G) * a.n_heads + (size_t)it.hk * G + r % G) * D + col) =
+        make_uint2(pack_bf16x2(num.x * inv, num.y * inv), pack_bf16x2(num.z * inv, num.w * inv));
 }
 
 template <int D>
@@ -848,7 +860,7 @@ cudaError_t prefill_f8_for(const AttnF8Args& a, cudaStream_t stream) {
     if (e != cudaSuccess) return record(e, "attn_prefill_f8_kernel launch");
     if (ns == 1) return cudaSuccess;
     trace_before("attn_prefill_f8_join", stream);
-    e = launch_pdl(attn_prefill_f8_join_kernel, dim3((unsigned)items, 2 * kPfRows / kPfJoinRows), dim3(kPfJoinThreads), 0, stream, 1,
+    e = launch_pdl(attn_prefill_f8_join_kernel, dim3((unsigned)items, 2 * kPfRows * (D / 4) / kPfJoinThreads), dim3(kPfJoinThreads), 0, stream, 1,
                    a, n_mt, tt, ns);
     trace_after(stream);
     if (e == cudaSuccess) e = cudaGetLastError();
