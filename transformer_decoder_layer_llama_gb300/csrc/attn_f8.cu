@@ -15,7 +15,9 @@
 // S^T = K Q^T and O^T += V^T P^T by mma.sync with the keys, and the head dims, as the 16 rows of A
 // and up to 8 (or 16) query heads of the KV head as columns, so a single query head wastes 7 of 8
 // columns instead of 15 of 16 rows.  The tensor pipe has the room: per SM 23 cache bytes a clock
-// arrive, and a tile's MMAs take about a quarter of its load time.
+// arrive, and a tile's MMAs take about a quarter of its load time.  7B shapes, 64 sequences of 512 to 4096 keys
+// (1.2 GB): 201 us, 6.0 TB/s (88% of the copy bandwidth); 70B shapes, 16 of 4096 to 32768 (0.6 GB): 102 us,
+// 5.9 TB/s.
 //
 // Precision.  Codes become FP16 exactly.  A query row is scaled by a power of two so that its largest
 // element lies in [2^14, 2^15) before it becomes FP16: BF16 has fewer bits, so only elements below

@@ -5,21 +5,29 @@
 // floor(128 / G) consecutive tokens times the G query heads that share the KV head, so a tile of keys is
 // brought in and converted once for 256 rows.  One CTA per SM and item, 128 keys at a time up to the
 // item's last position, items with the most keys first.  Where there are at most half as many items as SMs,
-// several CTAs share an item's keys and a second kernel joins their float32 partials by the log-sum-exp.
-// (A persistent grid with equal shares of all key tiles was slower: 7B prefill 80 us and 27 for the join against
-// 50, 70B-shaped chunks 605 against 551.  Its roles need registers for the walk, and a partial is 128 KB.)
+// several CTAs share an item's keys and a second kernel joins their float32 partials by the log-sum-exp:
+// 16 tokens behind 32768 (64 heads over 8) take 45 us so, 382 with one CTA per item.  (A persistent grid with
+// equal shares of all key tiles was slower: its roles need registers for the walk, and a partial is 128 KB.)
 //
-// Roles (416 threads):
+// Roles (512 threads in four groups of four warps, the registers split by setmaxnreg):
 //  * warps 0-3 and 4-7, softmax of tile A and B: one thread per query row.  First they stage Q in shared
 //    memory as FP16.  Per key tile: the row of S from TMEM into registers, its maximum, probabilities
 //    written over S as FP16; where the maximum has grown by more than 2^8 the running O in TMEM is scaled.
 //    At the end O / l goes out.
-//  * warps 8-11, keys and values: the codes come straight from global memory into registers, a tile
-//    ahead (L2 mostly, since all items of a KV head read the same codes), become FP16 and are stored as the
-//    128-byte-swizzled operand tiles, two buffers each for K and V.  Block ids are read two tiles ahead.
-//  * warps 12 and 13, one lane each: S = Q K^T (both from shared memory) and O += P V (P from TMEM) of
-//    tile A and B, so that the tensor core works for one tile while the other's softmax runs.  (One thread
-//    for both spent as long between its groups of MMAs as in them.)
+//  * warps 8-11, converters: the codes of a key tile, as they lie in the pool, become FP16 in the
+//    128-byte-swizzled operand tiles, two buffers each for K and V.
+//  * warp 14: brings codes (bulk copies of 16 keys) and scales a tile ahead.  (Loaded straight into the converters'
+//    registers they were what the rest waited for: the little L1 that this much shared memory leaves cannot
+//    keep a tile's loads in flight.)
+//  * warps 12 and 13, one elected lane each: S = Q K^T (both from shared memory) and O += P V (P from TMEM) of
+//    tile A and B.  The two tiles take turns, so that the tensor core works for one while the other's softmax runs.
+//
+// Bound by the chain of one query tile: S out of TMEM, maximum, 128 exponentials per row, P back, P V and the next
+// S, about 3100 clocks a key tile of which the tensor core works 1024 for each of the two query tiles.  Ragged
+// 70B-shaped chunks (589 GFLOP): 429 us, 1.37 PFLOP/s, 74% of the measured BF16 burst; 7B prompt of 2048
+// tokens (34 GFLOP, 256 items of 2 to 16 key tiles, of which an SM's one or two start with 5 us of fetching and
+// staging): 49.7 us.  Two threads per row (768 threads, 96 registers for the softmax) took 475 us in place
+// of 434, more tries before a wait looks at the clock 479.
 //
 // Precision.  Codes are exact in FP16.  A query row is scaled by a power of two so that its largest element
 // lies in [2^14, 2^15); its factor and the block's K scale multiply the float32 score, 16 keys at a time

