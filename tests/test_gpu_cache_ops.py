@@ -961,3 +961,25 @@ def test_stack_compaction_waits_for_the_step_that_reads_the_table():
     eng.compact(sch, stream)                  # returns when the stream is done
     assert torch.equal(y, want)
     assert int(eng.status.item()) == 0
+
+
+@pytest.mark.parametrize("case", [(16, 14, 2, 64, [129], [255]), (16, 7, 7, 128, [129], [255]), (128, 8, 2, 128, [300, 0], [100, 257])])
+def test_prefill_gives_the_same_bits_every_time(case):
+    """Items of a few key tiles, whose codes follow each other into the same shared memory, 300 times."""
+    bs, H, Hkv, d, before, new = case
+    ctx = [b + n for b, n in zip(before, new)]
+    rng = np.random.default_rng(sum(ctx))
+    ref_pool, table = make_cache(rng, ctx, Hkv, d, bs)
+    cu = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    q = torch.from_numpy(rng.normal(size=(int(cu[-1]), H, d))).bfloat16()
+    pool, st = to_gpu(ref_pool), status()
+    args = (q.cuda(), dev(cu), pool, dev(table), dev(ctx), d ** -0.5)
+    first = api.paged_attention_prefill_f8(*args, max_new=max(new), status=st)
+    assert_attention(first, *C.attention_f8(f64(q), ref_pool, table, ctx, cu, d ** -0.5), d)
+    out, differ = torch.empty_like(first), torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(300):
+        out.fill_(5.0)
+        api.paged_attention_prefill_f8(*args, max_new=max(new), out=out, status=st)
+        differ += (out != first).any()
+    check(st)
+    assert int(differ.item()) == 0

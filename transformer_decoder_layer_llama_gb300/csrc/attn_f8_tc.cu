@@ -529,8 +529,6 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
             uint4 w[PER];
 #pragma unroll
             for (int i = 0; i < PER; ++i) w[i] = *reinterpret_cast<const uint4*>(codes + (i * ROWS + rsub) * D + c16 * 16);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(done);
             if (left < kPfKeys || chunks != (1u << kPfChunks) - 1u) {
 #pragma unroll
                 for (int i = 0; i < PER; ++i) {
@@ -558,8 +556,27 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
             }
             fence_async_smem();
             __syncwarp();
+            // Only now may the codes be overwritten: every lane has stored what it loaded.  (An arrive right behind the loads
+            // can be seen before they have read.)
+            if (lane == 0) mbar_arrive(done);
         };
-        float up0 = 0.f, up1 = 0.f;                         // 2^(6 - E) as two factors
+        // exponent of the largest V scale of the CTA's keys
+        const int32_t* table_row = a.block_table + (size_t)it.b * a.max_blocks;
+        const int key0 = first * kPfKeys, bs_log2 = 31 - __clz(a.block_size);
+        const int n = (key0 + min(kv_end, n_kt * kPfKeys) + a.block_size - 1) >> bs_log2;
+        float top = 0.f;
+        for (int i = (key0 >> bs_log2) + tid; i < n; i += 128) {
+            const int x = table_row[i];
+            if (x >= 0 && x < a.num_blocks) top = fmaxf(top, a.v_scale[(size_t)x * a.n_kv_heads + it.hk]);
+        }
+        const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
+        if (lane == 0) vexp_w[warp - 8] = (int)(bits >> 23) - 127;
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        const int E = max(max(vexp_w[0], vexp_w[1]), max(vexp_w[2], vexp_w[3]));
+        if (tid == 0) vexp_s = E;
+        const int e0 = (kPfShift - E) / 2, e1 = kPfShift - E - e0;
+        const float up0 = __uint_as_float((uint32_t)(e0 + 127) << 23);   // 2^(6 - E) as two factors
+        const float up1 = __uint_as_float((uint32_t)(e1 + 127) << 23);
         for (int j = 0; j < n_kt; ++j) {
             // (whole warps leave)
             bool ok = (j < 2 || mbar_wait_bounded(&k_empty[j & 1], (uint32_t)((j - 2) >> 1) & 1u, &abort_s, status)) &&
@@ -567,25 +584,6 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
             if (!__all_sync(0xffffffffu, ok)) break;
             convert(smem + L::OFF_K + (uint32_t)(j & 1) * L::TILE, smem + L::OFF_CK, j, &c_empty[0], false, 0.f, 0.f);
             if (lane == 0) mbar_arrive(&k_ready[j & 1]);
-            if (j == 0) {
-                // exponent of the largest V scale of the CTA's keys
-                const int32_t* table_row = a.block_table + (size_t)it.b * a.max_blocks;
-                const int key0 = first * kPfKeys, bs_log2 = 31 - __clz(a.block_size);
-                const int n = (key0 + min(kv_end, n_kt * kPfKeys) + a.block_size - 1) >> bs_log2;
-                float top = 0.f;
-                for (int i = (key0 >> bs_log2) + tid; i < n; i += 128) {
-                    const int x = table_row[i];
-                    if (x >= 0 && x < a.num_blocks) top = fmaxf(top, a.v_scale[(size_t)x * a.n_kv_heads + it.hk]);
-                }
-                const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
-                if (lane == 0) vexp_w[warp - 8] = (int)(bits >> 23) - 127;
-                asm volatile("bar.sync 1, 128;" ::: "memory");
-                const int E = max(max(vexp_w[0], vexp_w[1]), max(vexp_w[2], vexp_w[3]));
-                if (tid == 0) vexp_s = E;
-                const int e0 = (kPfShift - E) / 2, e1 = kPfShift - E - e0;
-                up0 = __uint_as_float((uint32_t)(e0 + 127) << 23);
-                up1 = __uint_as_float((uint32_t)(e1 + 127) << 23);
-            }
             ok = (j < 2 || mbar_wait_bounded(&v_empty[j & 1], (uint32_t)((j - 2) >> 1) & 1u, &abort_s, status)) &&
                  mbar_wait_bounded(&c_full[1], (uint32_t)j & 1u, &abort_s, status);
             if (!__all_sync(0xffffffffu, ok)) break;
