@@ -983,3 +983,44 @@ def test_prefill_gives_the_same_bits_every_time(case):
         differ += (out != first).any()
     check(st)
     assert int(differ.item()) == 0
+
+
+def test_stack_over_e4m3_pools_replays_its_captured_step():
+    """The captured all-layer step, replayed with other tables, contexts and inputs, against the plain calls."""
+    from transformer_decoder_layer_llama_gb300.serving import BlockAllocator, Scheduler, StackEngine
+    d, L, nb, mb, slots, prompt = synth.DIMS_TINY, 2, 40, 8, 3, 20
+    cfg = api.make_config(d, max_position=mb * d.block_size)
+    packed = [api.pack_weights(cfg, {k: v.cuda() for k, v in synth.make_weights(d, 0.02, seed=50 + l).items()}) for l in range(L)]
+    results, stream = [], torch.cuda.Stream()
+    for captured in (False, True):
+        pools = [api.PoolF8.empty(nb, d.n_kv_heads, d.block_size, d.head_dim) for _ in range(L)]
+        sch = Scheduler(slots, d.block_size, mb, BlockAllocator(nb, seed=5), seed=6, prompt_len=prompt)
+        eng = StackEngine(api, [cfg] * L, packed, pools, slots, mb, slots * prompt)
+        for s in range(slots):
+            sch.start_resident(s, prompt)
+        if captured:                          # with every slot empty: nothing is written
+            torch.cuda.synchronize()
+            eng.capture_decode(stream)
+            stream.synchronize()
+            eng.status.zero_()                # an empty context holds no room for the step's token: flagged
+            assert all((p.k_scale == 0).all() and (p.v_scale == 0).all() for p in pools)
+        eng.pf_table.copy_(torch.from_numpy(sch.table))
+        eng.pf_ctx.fill_(prompt)
+        eng.pf_x.copy_(synth.make_x(slots * prompt, d.hidden, seed=1))
+        torch.cuda.synchronize()
+        eng.prefill(slots, prompt, stream)
+        ys = []
+        for i in range(20):
+            stream.synchronize()
+            ctx = sch.grow_for_decode()
+            eng.table.copy_(torch.from_numpy(sch.table))
+            eng.ctx.copy_(torch.from_numpy(ctx))
+            eng.x.copy_(synth.make_x(slots, d.hidden, seed=10 + i))
+            torch.cuda.synchronize()
+            y = eng.decode(stream)
+            stream.synchronize()
+            ys.append(y.clone())
+        torch.cuda.synchronize()
+        assert int(eng.status.item()) == 0
+        results.append(ys + [t.view(torch.uint8) for p in pools for t in (p.k, p.v)] + [t for p in pools for t in (p.k_scale, p.v_scale)])
+    assert all(torch.equal(a, b) for a, b in zip(*results))

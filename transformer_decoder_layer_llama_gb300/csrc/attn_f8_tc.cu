@@ -22,9 +22,10 @@
 //  * warps 12 and 13, one elected lane each: S = Q K^T (both from shared memory) and O += P V (P from TMEM) of
 //    tile A and B.  The two tiles take turns, so that the tensor core works for one while the other's softmax runs.
 //
-// Bound by the chain of one query tile: S out of TMEM, maximum, 128 exponentials per row, P back, P V and the next
-// S, about 3100 clocks a key tile of which the tensor core works 1024 for each of the two query tiles.  Ragged
-// 70B-shaped chunks (589 GFLOP): 429 us, 1.37 PFLOP/s, 74% of the measured BF16 burst; 7B prompt of 2048
+// Bound by the chain of one query tile (S out of TMEM, maximum, 128 exponentials per row, P back, P V and the next
+// S: about 3100 clocks a key tile, of which the tensor core works 1024 for each of the two query tiles) together with
+// the conversion, which shares shared memory with it: leaving out any one of them gains 3 to 10%.  Ragged
+// 70B-shaped chunks (589 GFLOP): 432 us, 1.36 PFLOP/s, 73% of the measured BF16 burst; 7B prompt of 2048
 // tokens (34 GFLOP, 256 items of 2 to 16 key tiles, of which an SM's one or two start with 5 us of fetching and
 // staging): 49.7 us.  Two threads per row (768 threads, 96 registers for the softmax) took 475 us in place
 // of 434, more tries before a wait looks at the clock 479.
