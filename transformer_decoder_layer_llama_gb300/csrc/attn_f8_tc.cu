@@ -312,8 +312,9 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     // Per query tile x and key tile j (parity j & 1): S computed, P stored.  Per key buffer: K or V stored
-    // (ready), read by both query tiles (empty).  Scales of key tile j sit in slot j & 3: slot and barrier
-    // are written again for tile j + 4, after the S of tile j + 2, which waits for the P of tile j + 1.
+    // (ready), read by both query tiles (empty).  Scales of key tile j sit in slot j & 3: slot and barrier are
+    // written again for tile j + 4, when K of tile j + 3 is converted, whose buffer was free after the S of tile
+    // j + 1, which waited for the P of tile j.
     __shared__ uint64_t q_ready[2], s_full[2], p_ready[2][2], turn_done[2], o_done[2], k_ready[2], k_empty[2], v_ready[2], v_empty[2];
     // Codes of a key tile: brought in (full), read by the converters (empty).
     __shared__ uint64_t meta_ready[kPfMeta], drain[2], c_full[2], c_empty[2];
