@@ -387,8 +387,8 @@ int ll_pack_rope(const ll_config* cfg, const ll_rope_config* rope, void* packed,
  * arithmetic, rounded once; LL_ROPE_BACKWARD is the transpose (s -> -s), the
  * gradient of the forward call.  Elements from rotary_dim on are copied.  Either
  * of q and k may be left out (its head count 0).  An output may be its input
- * (same pointer and stride); otherwise it must not overlap the inputs or the other
- * output.  A token whose position is outside 0 .. max_position - 1 sets
+ * (same pointer and stride); otherwise it must share no byte with the inputs or the
+ * other output (columns of one buffer at the same stride do not).  A token whose position is outside 0 .. max_position - 1 sets
  * LL_DEV_BAD_POSITION and its rows are not written.  head_dim <= 1024. */
 int ll_rope(const void* q, const void* k, int32_t dtype, const int32_t* positions, int32_t tokens, int32_t n_heads,
             int32_t n_kv_heads, int32_t head_dim, int32_t rotary_dim, int32_t layout, int32_t direction, int64_t q_stride,
