@@ -191,6 +191,21 @@ LL_DEVINL void store32(void* p, const uint32_t (&v)[8]) {
                  : "memory");
 }
 
+// Waits for the phase with the given parity for at most two seconds, and no longer once *abort is set; false, and
+// *abort set, if it did not come.  (mbar_wait_bounded in fewer instructions: twenty of them share this kernel's
+// instruction cache.  The kernel's end flags the status.)
+LL_DEVINL bool pf_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+    if (mbar_try_wait(bar, parity)) return true;
+    uint32_t t0, t;
+    asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t0));
+    do {
+        if (mbar_try_wait(bar, parity)) return true;
+        asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+    } while (*abort == 0 && t - t0 < 2000000000u);
+    *abort = 1;
+    return false;
+}
+
 // One lane of the (converged) warp, always the same.
 LL_DEVINL bool elect_one() {
     uint32_t r;
@@ -384,13 +399,13 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
             const uint32_t q_lo = (uint32_t)dq, q_hi = (uint32_t)(dq >> 32), k_lo = (uint32_t)dk, k_hi = (uint32_t)(dk >> 32);
             const uint32_t v_lo = (uint32_t)dv, v_hi = (uint32_t)(dv >> 32);
             const uint32_t t_s = tmem + L::TMEM_S + (uint32_t)x * 128u, t_o = tmem + L::TMEM_O + (uint32_t)x * 128u;
-            auto k_wait = [&](int i) { return mbar_wait_bounded(&k_ready[i & 1], (uint32_t)(i >> 1) & 1u, &abort_s, status); };
-            auto v_wait = [&](int i) { return mbar_wait_bounded(&v_ready[i & 1], (uint32_t)(i >> 1) & 1u, &abort_s, status); };
+            auto k_wait = [&](int i) { return pf_wait(&k_ready[i & 1], (uint32_t)(i >> 1) & 1u, &abort_s); };
+            auto v_wait = [&](int i) { return pf_wait(&v_ready[i & 1], (uint32_t)(i >> 1) & 1u, &abort_s); };
             // The two warps take turns, A before B: a turn is P V of a key tile with the S of the next.  Interleaved,
             // both tiles' S would be ready together: both softmaxes would run at once and the tensor core wait for them.
             auto my_turn = [&](int j) {
                 const int before = x ? j : j - 1;           // the other's turn, if it has one
-                return before < 0 || before >= (x ? n_a : n_b) || mbar_wait_bounded(&turn_done[x ^ 1], (uint32_t)before & 1u, &abort_s, status);
+                return before < 0 || before >= (x ? n_a : n_b) || pf_wait(&turn_done[x ^ 1], (uint32_t)before & 1u, &abort_s);
             };
             // S of a key tile, over P of the one before (MMAs of one thread run in order); by the elected lane
             auto issue_s = [&](int i) {
@@ -413,7 +428,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
             };
             bool ok = true;
             if (n_x > 0) {
-                ok = __all_sync(0xffffffffu, mbar_wait_bounded(&q_ready[x], 0, &abort_s, status) && k_wait(0));
+                ok = __all_sync(0xffffffffu, pf_wait(&q_ready[x], 0, &abort_s) && k_wait(0));
                 tc_fence_after();
                 if (ok && elect_one()) {
                     issue_s(0);
@@ -421,17 +436,18 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
                 }
                 __syncwarp();
             }
+#pragma unroll 1
             for (int j = 0; j < n_x && ok; ++j) {
                 // (what is usually there already is waited for first, beside the softmax; P comes in halves of 64 keys,
                 // so that P V of the first runs while the second is computed)
                 const bool more = j + 1 < n_x;
                 ok = __all_sync(0xffffffffu, v_wait(j) && (!more || k_wait(j + 1)) && my_turn(j) &&
-                                                 mbar_wait_bounded(&p_ready[x][0], (uint32_t)j & 1u, &abort_s, status));
+                                                 pf_wait(&p_ready[x][0], (uint32_t)j & 1u, &abort_s));
                 if (!ok) break;
                 tc_fence_after();
                 if (elect_one()) issue_pv(j, 0, j == 0);
                 __syncwarp();
-                ok = __all_sync(0xffffffffu, mbar_wait_bounded(&p_ready[x][1], (uint32_t)j & 1u, &abort_s, status));
+                ok = __all_sync(0xffffffffu, pf_wait(&p_ready[x][1], (uint32_t)j & 1u, &abort_s));
                 if (!ok) break;
                 tc_fence_after();
                 if (elect_one()) {
@@ -445,6 +461,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
                 __syncwarp();
             }
             // past its own last tile a query tile still takes part in the buffers' rounds
+#pragma unroll 1
             for (int j = n_x; j < n_kt && ok; ++j) {
                 ok = __all_sync(0xffffffffu, k_wait(j) && v_wait(j));
                 if (ok && lane == 0) {
@@ -455,7 +472,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
             if (elect_one()) {
                 tc_commit(&drain[x]);
                 volatile int never = 0;
-                mbar_wait_bounded(&drain[x], 0, &never, status);
+                pf_wait(&drain[x], 0, &never);
             }
         } else if (warp == 14) {
             // ------------------------------------------------ codes and scales
@@ -485,9 +502,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
                               &c_full[which]);
             };
             auto taken = [&](int which, int j) {            // by the converters: the codes of the tile before
-                return j == 0 || __all_sync(0xffffffffu, mbar_wait_bounded(&c_empty[which], (uint32_t)(j - 1) & 1u, &abort_s, status));
+                return j == 0 || __all_sync(0xffffffffu, pf_wait(&c_empty[which], (uint32_t)(j - 1) & 1u, &abort_s));
             };
             int entry = entry_of(0), k_at = -1, v_at = -1;
+#pragma unroll 1
             for (int j = 0; j < n_kt; ++j) {
                 const int row = row_of(j, entry), slot = j & (kPfMeta - 1);
                 const float ks = scale_of(a.k_scale, row), vs = scale_of(a.v_scale, row);
@@ -509,8 +527,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
             }
             // no copy is in flight when the CTA leaves
             volatile int never = 0;
-            if (k_at >= 0) mbar_wait_bounded(&c_full[0], (uint32_t)k_at & 1u, &never, status);
-            if (v_at >= 0) mbar_wait_bounded(&c_full[1], (uint32_t)v_at & 1u, &never, status);
+            if (k_at >= 0) pf_wait(&c_full[0], (uint32_t)k_at & 1u, &never);
+            if (v_at >= 0) pf_wait(&c_full[1], (uint32_t)v_at & 1u, &never);
         }
         __syncwarp();
     } else if (warp >= 8) {
@@ -567,6 +585,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
         const int key0 = first * kPfKeys, bs_log2 = 31 - __clz(a.block_size);
         const int n = (key0 + min(kv_end, n_kt * kPfKeys) + a.block_size - 1) >> bs_log2;
         float top = 0.f;
+#pragma unroll 1
         for (int i = (key0 >> bs_log2) + tid; i < n; i += 128) {
             const int x = table_row[i];
             if (x >= 0 && x < a.num_blocks) top = fmaxf(top, a.v_scale[(size_t)x * a.n_kv_heads + it.hk]);
@@ -579,15 +598,16 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
         const int e0 = (kPfShift - E) / 2, e1 = kPfShift - E - e0;
         const float up0 = __uint_as_float((uint32_t)(e0 + 127) << 23);   // 2^(6 - E) as two factors
         const float up1 = __uint_as_float((uint32_t)(e1 + 127) << 23);
+#pragma unroll 1
         for (int j = 0; j < n_kt; ++j) {
             // (whole warps leave)
-            bool ok = (j < 2 || mbar_wait_bounded(&k_empty[j & 1], (uint32_t)((j - 2) >> 1) & 1u, &abort_s, status)) &&
-                      mbar_wait_bounded(&c_full[0], (uint32_t)j & 1u, &abort_s, status);
+            bool ok = (j < 2 || pf_wait(&k_empty[j & 1], (uint32_t)((j - 2) >> 1) & 1u, &abort_s)) &&
+                      pf_wait(&c_full[0], (uint32_t)j & 1u, &abort_s);
             if (!__all_sync(0xffffffffu, ok)) break;
             convert(smem + L::OFF_K + (uint32_t)(j & 1) * L::TILE, smem + L::OFF_CK, j, &c_empty[0], false, 0.f, 0.f);
             if (lane == 0) mbar_arrive(&k_ready[j & 1]);
-            ok = (j < 2 || mbar_wait_bounded(&v_empty[j & 1], (uint32_t)((j - 2) >> 1) & 1u, &abort_s, status)) &&
-                 mbar_wait_bounded(&c_full[1], (uint32_t)j & 1u, &abort_s, status);
+            ok = (j < 2 || pf_wait(&v_empty[j & 1], (uint32_t)((j - 2) >> 1) & 1u, &abort_s)) &&
+                 pf_wait(&c_full[1], (uint32_t)j & 1u, &abort_s);
             if (!__all_sync(0xffffffffu, ok)) break;
             convert(smem + L::OFF_V + (uint32_t)(j & 1) * L::TILE, smem + L::OFF_CV, j, &c_empty[1], true, up0, up1);
             if (lane == 0) mbar_arrive(&v_ready[j & 1]);
@@ -650,10 +670,11 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
         float m_used = -INFINITY;
         float2 l2 = make_float2(0.f, 0.f);
         bool ok = true;
+#pragma unroll 1
         for (int j = 0; j < n_x; ++j) {
             const int slot = j & (kPfMeta - 1);
-            ok = mbar_wait_bounded(&meta_ready[slot], (uint32_t)(j / kPfMeta) & 1u, &abort_s, status) &&
-                 mbar_wait_bounded(&s_full[x], (uint32_t)j & 1u, &abort_s, status);
+            ok = pf_wait(&meta_ready[slot], (uint32_t)(j / kPfMeta) & 1u, &abort_s) &&
+                 pf_wait(&s_full[x], (uint32_t)j & 1u, &abort_s);
             ok = __all_sync(0xffffffffu, ok);               // the TMEM accesses are warp-collective
             if (!ok) break;
             tc_fence_after();
@@ -708,6 +729,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
                 const float dn = move ? ex2_approx(m_used - mx) : 1.f;
                 if (j > 0) {
                     // S of this tile is complete, so P V of the tile before is in O
+#pragma unroll 1
                     for (int c = 0; c < D; c += 8) tmem_scale8(to + (uint32_t)c, dn);
                 }
                 if (move) {
@@ -747,7 +769,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
             }
         }
         const size_t prow = (size_t)blockIdx.x * 2 * kPfRows + x * kPfRows + r;
-        ok = __all_sync(0xffffffffu, ok && (n_x == 0 || mbar_wait_bounded(&o_done[x], 0, &abort_s, status)));
+        ok = __all_sync(0xffffffffu, ok && (n_x == 0 || pf_wait(&o_done[x], 0, &abort_s)));
         if (ok && n_x > 0) {
             tc_fence_after();
             // vexp_s was written before v_ready of tile 0, which the P V behind o_done waited for
@@ -785,6 +807,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (threadIdx.x == 0 && *const_cast<volatile int*>(&abort_s)) flag_status(status, LL_DEV_TIMEOUT);
     if (warp == 12) tmem_dealloc(tmem, L::TMEM_COLS);
 }
 
