@@ -10,8 +10,8 @@
 // equal shares of all key tiles was slower: its roles need registers for the walk, and a partial is 128 KB.)
 //
 // Roles (512 threads in four groups of four warps, the registers split by setmaxnreg):
-//  * warps 0-3 and 4-7, softmax of tile A and B: one thread per query row.  First they stage Q in shared
-//    memory as FP16.  Per key tile: the row of S from TMEM into registers, its maximum, probabilities
+//  * warps 0-3 and 4-7, softmax of tile A and B: one thread per query row.  First they bring Q to shared
+//    memory and turn it into FP16 there.  Per key tile: the row of S from TMEM into registers, its maximum, probabilities
 //    written over S as FP16; where the maximum has grown by more than 2^8 the running O in TMEM is scaled.
 //    At the end O / l goes out.
 //  * warps 8-11, converters: the codes of a key tile, as they lie in the pool, become FP16 in the
@@ -25,10 +25,11 @@
 // Bound by the chain of one query tile (S out of TMEM, maximum, 128 exponentials per row, P back, P V and the next
 // S: about 3100 clocks a key tile, of which the tensor core works 1024 for each of the two query tiles) together with
 // the conversion, which shares shared memory with it: leaving out any one of them gains 3 to 10%.  Ragged
-// 70B-shaped chunks (589 GFLOP): 432 us, 1.36 PFLOP/s, 73% of the measured BF16 burst; 7B prompt of 2048
+// 70B-shaped chunks (589 GFLOP): 424 us, 1.39 PFLOP/s, 74% of the measured BF16 burst; 7B prompt of 2048
 // tokens (34 GFLOP, 256 items of 2 to 16 key tiles, of which an SM's one or two start with 5 us of fetching and
-// staging): 49.7 us.  Two threads per row (768 threads, 96 registers for the softmax) took 475 us in place
-// of 434, more tries before a wait looks at the clock 479.
+// staging): 44.8 us.  The code of all roles shares the instruction cache: waits in half the instructions and loops
+// that are not unrolled took the prompt from 49.2 to 44.7 us.  Two threads per row (768 threads, 96 registers
+// for the softmax) took 475 us in place of 434.
 //
 // Precision.  Codes are exact in FP16.  A query row is scaled by a power of two so that its largest element
 // lies in [2^14, 2^15); its factor and the block's K scale multiply the float32 score, 16 keys at a time
@@ -371,6 +372,48 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
     if (split >= splits) return;
     const int first = (int)((long long)it.n_kt * split / splits);   // the CTA's first key tile; tiles are counted from it
     const int n_kt = (int)((long long)it.n_kt * (split + 1) / splits) - first;
+    const int G = a.n_heads / a.n_kv_heads;
+    const int kv_end = max(it.end_a, it.end_b) - first * kPfKeys;   // keys, and table entries, from the CTA's first tile too
+    const int32_t* table_row = a.block_table + (size_t)it.b * a.max_blocks;
+    const int key0 = first * kPfKeys;
+    const int my_key = (lane & 7) * 16;                 // lane c < 8 looks after 16-key chunk c of a tile
+    const int bs_log2 = 31 - __clz(a.block_size);       // (a power of two: no divisions on this path)
+    auto entry_of = [&](int j) {                        // its table entry (-1 past the keys)
+        const int key = j * kPfKeys + my_key;
+        return j < n_kt && key < kv_end ? table_row[(key0 + key) >> bs_log2] : -1;
+    };
+    auto row_of = [&](int j, int entry) {               // its first pool row (-1: no valid block)
+        const int key = j * kPfKeys + my_key;
+        const bool want = j < n_kt && key < kv_end;
+        if (want && (entry < 0 || entry >= a.num_blocks)) flag_status(status, LL_DEV_BAD_BLOCK);
+        return want && entry >= 0 && entry < a.num_blocks
+                   ? ((entry * a.n_kv_heads + it.hk) << bs_log2) + ((key0 + key) & (a.block_size - 1)) : -1;
+    };
+    auto scale_of = [&](const float* scales, int row) {
+        return row >= 0 ? scales[row >> bs_log2] : 0.f;
+    };
+    if (warp < 8) {                                         // Q of tile A (warps 0-3) and B, as it is, to its place
+        // a warp's 32 rows, D / 8 lanes to a row, 16 bytes each
+        constexpr int QL = D / 8, QR = 32 / QL;
+        const int x = warp >> 2, c0 = lane % QL, nt = x ? it.nt_b : it.nt_a;
+        const uint32_t per_g = 65536u / (uint32_t)G + 1u;   // row / G = row * per_g >> 16 for row < 128
+        const size_t row0 = ((size_t)it.tok0 + x * it.tt) * a.n_heads + it.hk * G;
+#pragma unroll 4
+        for (int rr = (warp & 3) * 32 + lane / QL; rr < (warp & 3) * 32 + 32; rr += QR) {
+            const int t = (int)((uint32_t)rr * per_g >> 16);
+            cp_async16(smem + L::OFF_Q + (uint32_t)x * L::TILE + pf_off(rr, c0),
+                       a.q + (t < nt ? (row0 + (size_t)t * a.n_heads + (rr - t * G)) * D + c0 * 8 : 0), t < nt);
+        }
+        cp_async_commit();
+    }
+    int entry = -1, row = -1;                               // of the producer: the next tile's table entry, the tile's row
+    float ks = 0.f, vs = 0.f;
+    if (warp == 14) {                                       // (what takes a while is on its way before the barrier)
+        row = row_of(0, entry_of(0));
+        ks = scale_of(a.k_scale, row);
+        vs = scale_of(a.v_scale, row);
+        entry = entry_of(1);
+    }
     if (warp == 12) {
         tmem_alloc(&tmem_base_s, L::TMEM_COLS);
         tmem_relinquish();
@@ -379,10 +422,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_base_s;
-    const int G = a.n_heads / a.n_kv_heads;
     const int n_a = min(max((it.end_a + kPfKeys - 1) / kPfKeys - first, 0), n_kt);
     const int n_b = min(max((it.end_b + kPfKeys - 1) / kPfKeys - first, 0), n_kt);
-    const int kv_end = max(it.end_a, it.end_b) - first * kPfKeys;   // keys, and table entries, from there too
 
     if (warp >= 12) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
@@ -476,24 +517,6 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
             }
         } else if (warp == 14) {
             // ------------------------------------------------ codes and scales
-            const int32_t* table_row = a.block_table + (size_t)it.b * a.max_blocks;
-            const int key0 = first * kPfKeys;
-            const int my_key = (lane & 7) * 16;                 // lane c < 8 looks after 16-key chunk c of a tile
-            const int bs_log2 = 31 - __clz(a.block_size);       // (a power of two: no divisions on this path)
-            auto entry_of = [&](int j) {                        // its table entry (-1 past the keys)
-                const int key = j * kPfKeys + my_key;
-                return j < n_kt && key < kv_end ? table_row[(key0 + key) >> bs_log2] : -1;
-            };
-            auto row_of = [&](int j, int entry) {               // its first pool row (-1: no valid block)
-                const int key = j * kPfKeys + my_key;
-                const bool want = j < n_kt && key < kv_end;
-                if (want && (entry < 0 || entry >= a.num_blocks)) flag_status(status, LL_DEV_BAD_BLOCK);
-                return want && entry >= 0 && entry < a.num_blocks
-                           ? ((entry * a.n_kv_heads + it.hk) << bs_log2) + ((key0 + key) & (a.block_size - 1)) : -1;
-            };
-            auto scale_of = [&](const float* scales, int row) {
-                return row >= 0 ? scales[row >> bs_log2] : 0.f;
-            };
             auto bring = [&](int which, const uint8_t* pool, int j, int row, uint32_t mask) {
                 if (lane == 0) mbar_arrive_expect_tx(&c_full[which], (uint32_t)__popc(mask) * 16u * D);
                 __syncwarp();
@@ -504,23 +527,28 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
             auto taken = [&](int which, int j) {            // by the converters: the codes of the tile before
                 return j == 0 || __all_sync(0xffffffffu, pf_wait(&c_empty[which], (uint32_t)(j - 1) & 1u, &abort_s));
             };
-            int entry = entry_of(0), k_at = -1, v_at = -1;
+            int k_at = -1, v_at = -1;
 #pragma unroll 1
             for (int j = 0; j < n_kt; ++j) {
-                const int row = row_of(j, entry), slot = j & (kPfMeta - 1);
-                const float ks = scale_of(a.k_scale, row), vs = scale_of(a.v_scale, row);
-                entry = entry_of(j + 1);
+                const int slot = j & (kPfMeta - 1);
+                if (j) {
+                    row = row_of(j, entry);
+                    ks = scale_of(a.k_scale, row);
+                    vs = scale_of(a.v_scale, row);
+                    entry = entry_of(j + 1);
+                }
                 const uint32_t mask = __ballot_sync(0xffffffffu, lane < kPfChunks && row >= 0);
                 if (!taken(0, j)) break;
+                if (lane == 0) ok_s[slot] = mask;
+                __syncwarp();
+                bring(0, a.k_pool, j, row, mask);
+                k_at = j;
                 if (lane < kPfChunks) {
                     ks_s[slot][lane] = ks;
                     vs_s[slot][lane] = vs;
                 }
-                if (lane == 0) ok_s[slot] = mask;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&meta_ready[slot]);
-                bring(0, a.k_pool, j, row, mask);
-                k_at = j;
                 if (!taken(1, j)) break;
                 bring(1, a.v_pool, j, row, mask);
                 v_at = j;
@@ -581,8 +609,6 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
             if (lane == 0) mbar_arrive(done);
         };
         // exponent of the largest V scale of the CTA's keys
-        const int32_t* table_row = a.block_table + (size_t)it.b * a.max_blocks;
-        const int key0 = first * kPfKeys, bs_log2 = 31 - __clz(a.block_size);
         const int n = (key0 + min(kv_end, n_kt * kPfKeys) + a.block_size - 1) >> bs_log2;
         float top = 0.f;
 #pragma unroll 1
@@ -624,23 +650,12 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
         const bool live = tok < (x ? it.nt_b : it.nt_a);
         const size_t qrow = ((size_t)it.tok0 + x * it.tt + tok) * a.n_heads + head;
         float qf = 0.f;                                     // score factor but for the K scale
+        cp_async_wait<0>();
+        __syncwarp();
         if (n_x > 0) {
-            // The warp's 32 rows to their places in shared memory, D / 8 lanes to a row, 16 bytes each; then each thread
-            // turns its own row into FP16 there.  (Rolled loops here and at the output: code that runs once per item
-            // displaces the loop that matters.)
-            constexpr int QL = D / 8, QR = 32 / QL;
+            // Each thread turns its own row into FP16 in its place.  (Rolled loops here and at the output: code that runs
+            // once per item displaces the loop that matters.)
             uint8_t* const sq = smem + L::OFF_Q + (uint32_t)x * L::TILE;
-            const uint32_t per_g = 65536u / (uint32_t)G + 1u;   // row / G = row * per_g >> 16 for row < 128
-            const int c0 = lane % QL, nt = x ? it.nt_b : it.nt_a;
-            const size_t row0 = ((size_t)it.tok0 + x * it.tt) * a.n_heads + it.hk * G;
-#pragma unroll 4
-            for (int rr = (warp & 3) * 32 + lane / QL; rr < (warp & 3) * 32 + 32; rr += QR) {
-                const int t = (int)((uint32_t)rr * per_g >> 16);
-                cp_async16(sq + pf_off(rr, c0), a.q + (t < nt ? (row0 + (size_t)t * a.n_heads + (rr - t * G)) * D + c0 * 8 : 0), t < nt);
-            }
-            cp_async_commit();
-            cp_async_wait<0>();
-            __syncwarp();
             uint32_t m2 = 0;                                // largest magnitudes of the even and odd elements
 #pragma unroll 4
             for (int c = 0; c < D / 8; ++c) {
@@ -704,11 +719,12 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
 #pragma unroll
                 for (int c = 0; c < kPfChunks; ++c) {
                     const int lim = (chunks >> c) & 1u ? last - c * 16 : -1;
+                    const uint32_t see = lim < 0 ? 0u : 0xffffu >> (15 - min(lim, 15));   // the keys that this row sees
                     // -inf times the factor stays -inf: a factor of 0 (a block of zeros, or scale 0) becomes 2^-126,
                     // which leaves of a sum S (below 2^31) at most 2^-95
                     f[c] = lim < 0 ? 1.f : fmaxf(f[c], 1.17549435e-38f);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) s[16 * c + i] = i <= lim ? s[16 * c + i] : -INFINITY;
+                    for (int i = 0; i < 16; ++i) s[16 * c + i] = (see >> i) & 1u ? s[16 * c + i] : -INFINITY;
                 }
             }
             float mx = -INFINITY;
