@@ -6,7 +6,7 @@
 // brought in and converted once for 256 rows.  One CTA per SM and item, 128 keys at a time up to the
 // item's last position, items with the most keys first.  Where there are at most half as many items as SMs,
 // several CTAs share an item's keys and a second kernel joins their float32 partials by the log-sum-exp:
-// 16 tokens behind 32768 (64 heads over 8) take 45 us so, 382 with one CTA per item.  (A persistent grid with
+// 16 tokens behind 32768 (64 heads over 8) take 41 us so, 382 with one CTA per item.  (A persistent grid with
 // equal shares of all key tiles was slower: its roles need registers for the walk, and a partial is 128 KB.)
 //
 // Roles (512 threads in four groups of four warps, the registers split by setmaxnreg):
@@ -25,9 +25,9 @@
 // Bound by the chain of one query tile (S out of TMEM, maximum, 128 exponentials per row, P back, P V and the next
 // S: about 3100 clocks a key tile, of which the tensor core works 1024 for each of the two query tiles) together with
 // the conversion, which shares shared memory with it: leaving out any one of them gains 3 to 10%.  Ragged
-// 70B-shaped chunks (589 GFLOP): 424 us, 1.39 PFLOP/s, 74% of the measured BF16 burst; 7B prompt of 2048
+// 70B-shaped chunks (589 GFLOP): 423 us, 1.39 PFLOP/s, 75% of the measured BF16 burst; 7B prompt of 2048
 // tokens (34 GFLOP, 256 items of 2 to 16 key tiles, of which an SM's one or two start with 5 us of fetching and
-// staging): 44.8 us.  The code of all roles shares the instruction cache: waits in half the instructions and loops
+// staging): 44.5 us.  The code of all roles shares the instruction cache: waits in half the instructions and loops
 // that are not unrolled took the prompt from 49.2 to 44.7 us.  Two threads per row (768 threads, 96 registers
 // for the softmax) took 475 us in place of 434.
 //
