@@ -1024,3 +1024,25 @@ def test_stack_over_e4m3_pools_replays_its_captured_step():
         assert int(eng.status.item()) == 0
         results.append(ys + [t.view(torch.uint8) for p in pools for t in (p.k, p.v)] + [t for p in pools for t in (p.k_scale, p.v_scale)])
     assert all(torch.equal(a, b) for a, b in zip(*results))
+
+
+def test_largest_batch():
+    """65535 sequences of one token: the answer is the cached V row itself."""
+    B, Hkv, d, bs = 65535, 1, 64, 16
+    pool, st = api.PoolF8.empty(B, Hkv, bs, d), status()
+    table = torch.randperm(B, device="cuda", generator=torch.Generator("cuda").manual_seed(1)).to(torch.int32).view(B, 1)
+    ctx, cu = torch.ones(B, dtype=torch.int32, device="cuda"), torch.arange(B + 1, dtype=torch.int32, device="cuda")
+    g = torch.Generator("cuda").manual_seed(2)
+    k, v = (torch.randn(B, Hkv, d, device="cuda", generator=g).bfloat16() for _ in range(2))
+    q = torch.randn(B, 2, d, device="cuda", generator=g).bfloat16()
+    api.append_to_cache_f8(k, v, pool, table, ctx, status=st)
+    row = pool.v[table[:, 0].long(), :, 0].float() * pool.v_scale[table[:, 0].long()][..., None]
+    want = row.expand(B, 2, d)                                           # codes times powers of two: exact in BF16
+    assert (want - v.float()).abs().max() <= 2.0 ** -4 * v.float().abs().max()
+    for out in (api.paged_attention_decode_f8(q, pool, table, ctx, 0.125, status=st),
+                api.paged_attention_prefill_f8(q, cu, pool, table, ctx, 0.125, max_new=1, status=st)):
+        assert ((out.float() - want).abs() <= 2.0 ** -8 * want.abs()).all()
+    check(st)
+    with pytest.raises(api.LayerError):
+        api.append_to_cache_f8(torch.cat([k, k[:1]]), torch.cat([v, v[:1]]), pool, torch.cat([table, table[:1]]),
+                               torch.ones(B + 1, dtype=torch.int32, device="cuda"), status=st)
