@@ -573,48 +573,12 @@ __global__ void __launch_bounds__(kF8Threads, NT == 1 ? kF8MaxCtasPerSm : 2)
     }
 }
 
-// Joins the partials of each (sequence, KV head) whose tiles several CTAs of the grid of P shared, and
-// writes zeros for sequences without a key.  Grid (KV head, sequence); a thread has four head dims of a query
-// head, and takes the partials four at a time, so that their loads are in flight together.
+// The partials of the CTAs c0 .. c1 that share the n tiles of (sequence b, KV head hk), joined by the log-sum-exp; zeros
+// where n = 0.  A thread has four head dims of a query head, and takes the partials four at a time, so that their
+// loads are in flight together.
 constexpr int kF8JoinThreads = 256;
-__global__ void __launch_bounds__(kF8JoinThreads) attn_decode_f8_join_kernel(const AttnF8Args a, int P) {
-    __shared__ long long s_all[kF8JoinThreads / 32], s_before[kF8JoinThreads / 32];
-    // The context lengths are no output of the kernel before this one, which itself waited for their writers
-    // before it let this one start: they are read beside its end.
-    const int hk = blockIdx.x, b = blockIdx.y;
+LL_DEVINL void f8_join(const AttnF8Args& a, int b, int hk, int n, int c0, int c1, int slot0) {
     const int G = a.n_heads / a.n_kv_heads, D = a.head_dim;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    long long all = 0, before = 0;
-    for (int i = threadIdx.x; i < a.batch; i += kF8JoinThreads) {
-        const int n = f8_tiles(f8_context(a, i, false));
-        all += n;
-        if (i < b) before += n;
-    }
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) {
-        all += __shfl_xor_sync(0xffffffffu, all, o);
-        before += __shfl_xor_sync(0xffffffffu, before, o);
-    }
-    if (lane == 0) {
-        s_all[warp] = all;
-        s_before[warp] = before;
-    }
-    __syncthreads();
-    all = before = 0;
-#pragma unroll
-    for (int w = 0; w < kF8JoinThreads / 32; ++w) {
-        all += s_all[w];
-        before += s_before[w];
-    }
-    const int n = f8_tiles(f8_context(a, b, false));
-    const long long total = all * a.n_kv_heads;
-    const long long u0 = before * a.n_kv_heads + (long long)hk * n, u1 = u0 + n;
-    const int c0 = n ? share_of(total, P, u0) : 0, c1 = n ? share_of(total, P, u1 - 1) : 0;
-    // partial of CTA c: its slot 0 where the tiles reach the share's first, else its slot 1 (only the first CTA)
-    const int slot0 = n ? 2 * c0 + (share_begin(total, P, c0) >= u0 ? 0 : 1) : 0;
-    pdl_wait();
-    pdl_trigger();
-    if (n > 0 && c0 == c1) return;                         // one CTA had them all
     __nv_bfloat16* out = a.out + ((size_t)b * a.n_heads + (size_t)hk * G) * D;
     for (int i = threadIdx.x; i < G * D / 4; i += kF8JoinThreads) {
         const int r = i / (D / 4), col = (i - r * (D / 4)) * 4;
@@ -654,6 +618,91 @@ __global__ void __launch_bounds__(kF8JoinThreads) attn_decode_f8_join_kernel(con
     }
 }
 
+// Joins what several CTAs of the grid of P shared, and writes zeros for sequences without a key.  Grid (KV head,
+// sequence).
+__global__ void __launch_bounds__(kF8JoinThreads) attn_decode_f8_join_kernel(const AttnF8Args a, int P) {
+    __shared__ long long s_all[kF8JoinThreads / 32], s_before[kF8JoinThreads / 32];
+    // The context lengths are no output of the kernel before this one, which itself waited for their writers
+    // before it let this one start: they are read beside its end.
+    const int hk = blockIdx.x, b = blockIdx.y;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    long long all = 0, before = 0;
+    for (int i = threadIdx.x; i < a.batch; i += kF8JoinThreads) {
+        const int n = f8_tiles(f8_context(a, i, false));
+        all += n;
+        if (i < b) before += n;
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) {
+        all += __shfl_xor_sync(0xffffffffu, all, o);
+        before += __shfl_xor_sync(0xffffffffu, before, o);
+    }
+    if (lane == 0) {
+        s_all[warp] = all;
+        s_before[warp] = before;
+    }
+    __syncthreads();
+    all = before = 0;
+#pragma unroll
+    for (int w = 0; w < kF8JoinThreads / 32; ++w) {
+        all += s_all[w];
+        before += s_before[w];
+    }
+    const int n = f8_tiles(f8_context(a, b, false));
+    const long long total = all * a.n_kv_heads;
+    const long long u0 = before * a.n_kv_heads + (long long)hk * n, u1 = u0 + n;
+    const int c0 = n ? share_of(total, P, u0) : 0, c1 = n ? share_of(total, P, u1 - 1) : 0;
+    // partial of CTA c: its slot 0 where the tiles reach the share's first, else its slot 1 (only the first CTA)
+    const int slot0 = n ? 2 * c0 + (share_begin(total, P, c0) >= u0 ? 0 : 1) : 0;
+    pdl_wait();
+    pdl_trigger();
+    if (n > 0 && c0 == c1) return;                         // one CTA had them all
+    f8_join(a, b, hk, n, c0, c1, slot0);
+}
+
+// The same for more than 1024 sequences: every CTA adds up all contexts, so it takes a run of the sequences (65535 of
+// them: 3.4 ms -> 0.16; for the 7B and 70B shapes this form costs 2 us more).
+constexpr int kF8JoinRuns = 1024;
+__global__ void __launch_bounds__(kF8JoinThreads) attn_decode_f8_join_runs_kernel(const AttnF8Args a, int P) {
+    __shared__ long long s_all[kF8JoinThreads / 32], s_before[kF8JoinThreads / 32];
+    const int hk = blockIdx.x, per = (a.batch + (int)gridDim.y - 1) / (int)gridDim.y;
+    const int b0 = (int)blockIdx.y * per, b1 = min(b0 + per, a.batch);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    long long all = 0, before = 0;
+    for (int i = threadIdx.x; i < a.batch; i += kF8JoinThreads) {
+        const int n = f8_tiles(f8_context(a, i, false));
+        all += n;
+        if (i < b0) before += n;
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) {
+        all += __shfl_xor_sync(0xffffffffu, all, o);
+        before += __shfl_xor_sync(0xffffffffu, before, o);
+    }
+    if (lane == 0) {
+        s_all[warp] = all;
+        s_before[warp] = before;
+    }
+    __syncthreads();
+    all = before = 0;
+#pragma unroll
+    for (int w = 0; w < kF8JoinThreads / 32; ++w) {
+        all += s_all[w];
+        before += s_before[w];
+    }
+    const long long total = all * a.n_kv_heads;
+    pdl_wait();
+    pdl_trigger();
+    for (int b = b0; b < b1; ++b) {
+        const int n = f8_tiles(f8_context(a, b, false));
+        const long long u0 = before * a.n_kv_heads + (long long)hk * n, u1 = u0 + n;
+        const int c0 = n ? share_of(total, P, u0) : 0, c1 = n ? share_of(total, P, u1 - 1) : 0;
+        const int slot0 = n ? 2 * c0 + (share_begin(total, P, c0) >= u0 ? 0 : 1) : 0;
+        before += n;
+        if (n == 0 || c0 != c1) f8_join(a, b, hk, n, c0, c1, slot0);
+    }
+}
+
 int f8_ctas_per_sm(int G, int D) {
     const size_t smem = (size_t)2 * kF8Stages * kF8Tile * D + (size_t)4 * G * 32 * 4 + 1024;
     // an SM has 228 KB, a CTA takes 2 KB more for its static part and the system's
@@ -688,8 +737,9 @@ cudaError_t decode_f8_for(const AttnF8Args& a, cudaStream_t stream) {
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) return record(e, "attn_decode_f8_kernel launch");
     trace_before("attn_decode_f8_join", stream);
-    e = launch_pdl(attn_decode_f8_join_kernel, dim3((unsigned)a.n_kv_heads, (unsigned)a.batch), dim3(kF8JoinThreads), 0, stream, 1,
-                   a, P);
+    const dim3 grid((unsigned)a.n_kv_heads, (unsigned)std::min(a.batch, kF8JoinRuns));
+    e = launch_pdl(a.batch > kF8JoinRuns ? attn_decode_f8_join_runs_kernel : attn_decode_f8_join_kernel, grid, dim3(kF8JoinThreads), 0,
+                   stream, 1, a, P);
     trace_after(stream);
     if (e == cudaSuccess) e = cudaGetLastError();
     return record(e, "attn_decode_f8_join_kernel launch");
