@@ -350,3 +350,38 @@ def test_layer_f8_workspace_holds_the_fused_one():
     cfg = api.make_config(synth.DIMS_70B, 4096)
     assert api.lib.ll_workspace_size_f8(ctypes.byref(cfg), 64, 16) > api.workspace_size(cfg, 64, 16)
     assert api.lib.ll_workspace_size_f8(ctypes.byref(cfg), 0, 16) == 0
+
+
+def engine_without_a_gpu(nb):
+    """A StackEngine whose every GPU call fails the test."""
+    from transformer_decoder_layer_llama_gb300.serving import StackEngine
+    eng = StackEngine.__new__(StackEngine)
+    for name in ("api", "blocks", "table", "pf_table", "status"):
+        setattr(eng, name, None)                       # (any use of them raises AttributeError)
+    return eng
+
+
+@pytest.mark.parametrize("how", ["a prefix of a request that is gone", "a prefix of one that runs", "blocks of no request"])
+def test_compaction_refuses_blocks_held_outside_the_requests_before_it_moves_any(how):
+    from transformer_decoder_layer_llama_gb300.serving import BlockAllocator, Scheduler
+    sch = Scheduler(3, 16, 6, BlockAllocator(30, seed=3), seed=1)
+    for s in range(3):
+        sch.start_resident(s, 40)
+    if how == "blocks of no request":
+        kept = sch.alloc.alloc(2)
+    else:
+        kept = sch.slots[0].blocks[:2]
+        sch.alloc.share(kept)
+        if how == "a prefix of a request that is gone":
+            sch.retire(0)
+    assert sch.held_outside() == sorted(kept)
+    before = sch.table.copy(), [list(r.blocks) if r else None for r in sch.slots], dict(sch.alloc._used), list(sch.alloc._free)
+    stream = None                                      # (waiting on it raises AttributeError)
+    with pytest.raises(ValueError, match="held outside"):
+        engine_without_a_gpu(30).compact(sch, stream)
+    after = sch.table.copy(), [list(r.blocks) if r else None for r in sch.slots], dict(sch.alloc._used), list(sch.alloc._free)
+    assert (before[0] == after[0]).all() and before[1:] == after[1:]
+    sch.alloc.free(kept)
+    assert sch.held_outside() == []
+    sch.fork(1, 0) if sch.slots[0] is None else None   # shared between requests: theirs
+    assert sch.held_outside() == []

@@ -1,0 +1,45 @@
+"""The operators around the cache where they can go wrong: what a serving program does between steps,
+batches of very different sequences, values that a row does not see.  Tolerances are those of
+test_gpu_cache_ops.py."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import cache_ops as C
+from tests.helpers import f64
+from tests.test_gpu_cache_ops import assert_attention, assert_pool, bf16, check, dev, make_cache, status, to_gpu
+from transformer_decoder_layer_llama_gb300 import synth
+
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    from transformer_decoder_layer_llama_gb300 import api
+
+
+def test_compaction_renames_a_prefill_that_is_staged():
+    """Requests whose rows lie in pf_table when the pools are packed: the prefill writes their new blocks."""
+    from transformer_decoder_layer_llama_gb300.serving import BlockAllocator, Scheduler, StackEngine
+    d, nb, mb, slots, n = synth.DIMS_TINY, 24, 4, 3, 20
+    cfg = api.make_config(d, max_position=mb * d.block_size)
+    packed = [api.pack_weights(cfg, {k: v.cuda() for k, v in synth.make_weights(d, 0.02, seed=7).items()})]
+    pools = [api.PoolF8.empty(nb, d.n_kv_heads, d.block_size, d.head_dim)]
+    sch = Scheduler(slots, d.block_size, mb, BlockAllocator(nb, seed=5), seed=6, prompt_len=n)
+    eng = StackEngine(api, [cfg], packed, pools, slots, mb, slots * n)
+    stream = torch.cuda.Stream()
+    for s in range(slots):
+        sch.start_resident(s, n)
+    eng.pf_table.copy_(torch.from_numpy(sch.table))
+    eng.pf_table[1, 2] = 10 ** 6                       # an id of no pool stays
+    eng.pf_ctx.fill_(n)
+    eng.pf_x.copy_(synth.make_x(slots * n, d.hidden, seed=1))
+    sch.retire(2)
+    torch.cuda.synchronize()
+    assert eng.compact(sch, stream) > 0
+    got = eng.pf_table.cpu().numpy()
+    assert got[1, 2] == 10 ** 6 and (got[2] == -1).all()
+    got[1, 2] = -1
+    assert (got[:2] == sch.table[:2]).all() and set(got[got >= 0]) == set(range(4))
+    eng.prefill(2, n, stream)
+    torch.cuda.synchronize()
+    assert int(eng.status.item()) == 0
+    assert (pools[0].k_scale[:4] > 0).all() and (pools[0].k_scale[4:] == 0).all()

@@ -54,6 +54,9 @@ class BlockAllocator:
     def holders(self, block: int) -> int:
         return self._used.get(block, 0)
 
+    def in_use(self) -> list:
+        return list(self._used)
+
     def alloc(self, n: int) -> list:
         if n > len(self._free):
             raise MemoryError(f"KV pool exhausted: need {n} blocks, {len(self._free)} free")
@@ -170,6 +173,15 @@ class Scheduler:
         self._set_blocks(dst, nr.blocks)
         return [(r.blocks[full], last[0])] if last else []
 
+    def held_outside(self) -> list:
+        """Blocks in use that somebody besides the requests in the slots holds (a prefix kept with share, blocks
+        from alloc): a renaming reaches the requests' ids only."""
+        mine = {}
+        for r in self.slots:
+            for b in r.blocks if r is not None else ():
+                mine[b] = mine.get(b, 0) + 1
+        return sorted(b for b in self.alloc.in_use() if self.alloc.holders(b) != mine.get(b, 0))
+
     def apply_map(self, block_map) -> None:
         """Renames every block as compact_blocks' block_map says."""
         self.alloc.apply_map(block_map)
@@ -270,13 +282,21 @@ class StackEngine:
 
     def compact(self, scheduler: Scheduler, stream) -> int:
         """Packs the blocks of the scheduler's requests to the front of every pool, and renames them in the
-        scheduler and in the device table.  Waits for the stream; returns the number of blocks moved."""
+        scheduler and in the device tables (a row of pf_table that belongs to no request any more becomes -1).
+        Waits for the stream; returns the number of blocks moved.  A block that somebody besides the requests
+        holds raises ValueError before anything is moved: to the plan it would be free, or its id would go stale."""
+        held = scheduler.held_outside()
+        if held:
+            raise ValueError(f"blocks {held[:8]} are held outside the requests: free them before packing")
         stream.wait_stream(torch.cuda.current_stream())
         with torch.cuda.stream(stream):                       # behind the steps that still read the table
             self.table.copy_(torch.from_numpy(scheduler.table))
             _, pairs, counts, block_map = self.api.compact_blocks(self.table, self.blocks.num_blocks,
                                                                   new_table=self.table, status=self.status)
             self.api.copy_blocks(self.blocks, pairs, n_pairs=counts[1:], status=self.status)
+            old = self.pf_table
+            known = (old >= 0) & (old < self.blocks.num_blocks)
+            old.copy_(torch.where(known, block_map[torch.where(known, old, 0).long()], old))
             block_map, counts = block_map.cpu().numpy(), counts.tolist()
         scheduler.apply_map(block_map)
         return counts[1]
