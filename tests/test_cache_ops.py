@@ -385,3 +385,21 @@ def test_compaction_refuses_blocks_held_outside_the_requests_before_it_moves_any
     assert sch.held_outside() == []
     sch.fork(1, 0) if sch.slots[0] is None else None   # shared between requests: theirs
     assert sch.held_outside() == []
+
+
+def test_a_step_with_an_empty_slot_changes_no_request():
+    from transformer_decoder_layer_llama_gb300.serving import BlockAllocator, Scheduler
+    sch = Scheduler(3, 16, 6, BlockAllocator(30, seed=3), seed=1, prompt_len=20)
+    for s in range(3):
+        sch.start_resident(s, 32)                      # the next token starts a block
+    sch.retire(1)
+    books = lambda: [(r.ctx, r.budget, list(r.blocks)) if r else None for r in sch.slots]  # noqa: E731
+    before, free, table = books(), sch.alloc.free_count(), sch.table.copy()
+    with pytest.raises(ValueError, match="empty"):
+        sch.grow_for_decode()
+    assert books() == before and sch.alloc.free_count() == free and (sch.table == table).all()
+    sch.fork(2, 1)
+    assert sch.grow_for_decode().tolist() == [33, 33, 33]
+    sch.retire(0)
+    assert sch.retire_and_admit() == [0]               # an empty slot takes the next request
+    assert sch.grow_for_decode().tolist() == [21, 34, 34]

@@ -149,7 +149,8 @@ class Scheduler:
         return admitted
 
     def retire(self, slot: int) -> None:
-        """Ends the request in a slot now: its blocks are let go, the slot is empty."""
+        """Ends the request in a slot now: its blocks are let go, the slot is empty until the next fork into it,
+        start_resident or retire_and_admit."""
         r = self.slots[slot]
         if r is None:
             raise ValueError(f"slot {slot} is empty")
@@ -192,7 +193,12 @@ class Scheduler:
 
     def grow_for_decode(self) -> np.ndarray:
         """Every slot appends one token: a block is added when the new position starts one.
-        Returns context_lens (int32) including the appended token."""
+        Returns context_lens (int32) including the appended token.  A decode step has a request in every slot
+        (fork, start_resident or retire_and_admit fill one that retire left empty): with an empty one, ValueError
+        and no request is changed."""
+        empty = [s for s, r in enumerate(self.slots) if r is None]
+        if empty:
+            raise ValueError(f"slots {empty} are empty")
         ctx = np.empty(self.n_slots, np.int32)
         for s, r in enumerate(self.slots):
             pos = r.ctx                       # position of the appended token
