@@ -403,3 +403,16 @@ def test_a_step_with_an_empty_slot_changes_no_request():
     sch.retire(0)
     assert sch.retire_and_admit() == [0]               # an empty slot takes the next request
     assert sch.grow_for_decode().tolist() == [21, 34, 34]
+
+
+@pytest.mark.parametrize("nb,width,error", [(7, 6, MemoryError), (30, 2, ValueError)])
+def test_a_step_without_room_changes_no_request(nb, width, error):
+    from transformer_decoder_layer_llama_gb300.serving import BlockAllocator, Scheduler
+    sch = Scheduler(3, 16, width, BlockAllocator(nb, seed=3), seed=1)
+    for s in range(3):
+        sch.start_resident(s, 32)                      # two blocks each; the next token starts another
+    books = lambda: [(r.ctx, r.budget, list(r.blocks)) for r in sch.slots]  # noqa: E731
+    before, free, table = books(), sch.alloc.free_count(), sch.table.copy()
+    with pytest.raises(error):
+        sch.grow_for_decode()
+    assert books() == before and sch.alloc.free_count() == free and (sch.table == table).all()

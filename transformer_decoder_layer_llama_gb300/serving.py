@@ -194,17 +194,20 @@ class Scheduler:
     def grow_for_decode(self) -> np.ndarray:
         """Every slot appends one token: a block is added when the new position starts one.
         Returns context_lens (int32) including the appended token.  A decode step has a request in every slot
-        (fork, start_resident or retire_and_admit fill one that retire left empty): with an empty one, ValueError
-        and no request is changed."""
+        (fork, start_resident or retire_and_admit fill one that retire left empty): with an empty one ValueError, with
+        too few free blocks MemoryError, and no request is changed."""
         empty = [s for s, r in enumerate(self.slots) if r is None]
         if empty:
             raise ValueError(f"slots {empty} are empty")
+        new = [s for s, r in enumerate(self.slots) if r.ctx % self.bs == 0 and r.ctx // self.bs >= len(r.blocks)]
+        if any(len(self.slots[s].blocks) >= self.max_blocks for s in new):
+            raise ValueError("request outgrew the block table width")
+        for s, b in zip(new, self.alloc.alloc(len(new))):
+            r = self.slots[s]
+            r.blocks.append(b)
+            self._set_blocks(s, r.blocks)
         ctx = np.empty(self.n_slots, np.int32)
         for s, r in enumerate(self.slots):
-            pos = r.ctx                       # position of the appended token
-            if pos % self.bs == 0 and pos // self.bs >= len(r.blocks):
-                r.blocks += self.alloc.alloc(1)
-                self._set_blocks(s, r.blocks)
             r.ctx += 1
             r.budget -= 1
             ctx[s] = r.ctx
