@@ -416,3 +416,13 @@ def test_a_step_without_room_changes_no_request(nb, width, error):
     with pytest.raises(error):
         sch.grow_for_decode()
     assert books() == before and sch.alloc.free_count() == free and (sch.table == table).all()
+
+
+@pytest.mark.parametrize("cls,names", [("PoolF8", ("k", "v", "k_scale", "v_scale", "device")), ("BlockSet", ("tensors", "device", "num_blocks"))])
+def test_the_tensors_of_a_pool_cannot_be_replaced(cls, names):
+    """The library is given the addresses that were checked; a tensor put in their place would pass the checks and
+    not be used."""
+    obj = object.__new__(getattr(api, cls))
+    for name in names:
+        with pytest.raises(AttributeError):
+            setattr(obj, name, torch.zeros(2))

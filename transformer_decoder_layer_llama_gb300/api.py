@@ -665,7 +665,8 @@ def rope(q, k, positions, table, layout="half", backward=False, q_out=None, k_ou
 
 class PoolF8:
     """An e4m3 KV pool on the GPU: codes k, v float8_e4m3fn [num_blocks, n_kv_heads, block_size, head_dim]
-    and float32 scales k_scale, v_scale [num_blocks, n_kv_heads]."""
+    and float32 scales k_scale, v_scale [num_blocks, n_kv_heads].  The tensors were checked together: they
+    cannot be replaced (another set is another pool)."""
 
     def __init__(self, k, v, k_scale, v_scale):
         _need(k, "k codes", torch.float8_e4m3fn)
@@ -675,8 +676,7 @@ class PoolF8:
         _need(k_scale, "k_scale", torch.float32, shape=tuple(k.shape[:2]))
         _need(v_scale, "v_scale", torch.float32, shape=tuple(k.shape[:2]))
         _on(k, v, k_scale, v_scale)
-        self.device = k.device
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self._tensors = k, v, k_scale, v_scale
         self._c = ll_kv_pool_f8(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), k.shape[0])
 
     @classmethod
@@ -685,13 +685,22 @@ class PoolF8:
         codes = [torch.zeros(shape, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn) for _ in range(2)]
         return cls(*codes, *(torch.zeros(shape[:2], dtype=torch.float32, device=device) for _ in range(2)))
 
+    k = property(lambda self: self._tensors[0])
+    v = property(lambda self: self._tensors[1])
+    k_scale = property(lambda self: self._tensors[2])
+    v_scale = property(lambda self: self._tensors[3])
+
+    @property
+    def device(self):
+        return self.k.device
+
     @property
     def block_size(self):
         return self.k.shape[2]
 
     def tensors(self):
         """The pool's tensors, block first, as a BlockSet takes them."""
-        return [self.k, self.v, self.k_scale, self.v_scale]
+        return list(self._tensors)
 
     def c(self):
         return self._c
@@ -852,10 +861,15 @@ def layer_decode_step_f8(cfg, packed, x, pool: PoolF8, block_table, context_lens
 
 class BlockSet:
     """Tensors [num_blocks, ...] that share their block ids (K and V pools of every layer, and their
-    scales), for copy_blocks.  Keeps the tensors and the array that the library reads."""
+    scales), for copy_blocks.  Keeps the tensors and the array that the library reads; they cannot be
+    replaced (another set of tensors is another BlockSet)."""
+
+    tensors = property(lambda self: self._tensors)
+    device = property(lambda self: self._tensors[0].device)
+    num_blocks = property(lambda self: self._tensors[0].shape[0])
 
     def __init__(self, tensors):
-        self.tensors = list(tensors)
+        self._tensors = tuple(tensors)
         if not self.tensors:
             raise ValueError("a BlockSet needs a tensor")
         for t in self.tensors:
@@ -864,8 +878,6 @@ class BlockSet:
             if t.shape[0] != self.tensors[0].shape[0]:
                 raise ValueError("the tensors of a BlockSet have the same number of blocks")
         _on(*self.tensors)
-        self.device = self.tensors[0].device
-        self.num_blocks = self.tensors[0].shape[0]
         self._c = (ll_block_tensor * len(self.tensors))(
             *((t.data_ptr(), t.numel() // max(self.num_blocks, 1) * t.element_size()) for t in self.tensors))
 
