@@ -356,7 +356,7 @@ def engine_without_a_gpu(nb):
     """A StackEngine whose every GPU call fails the test."""
     from transformer_decoder_layer_llama_gb300.serving import StackEngine
     eng = StackEngine.__new__(StackEngine)
-    for name in ("api", "blocks", "table", "pf_table", "status"):
+    for name in ("api", "pools", "_blocks", "table", "pf_table", "status"):
         setattr(eng, name, None)                       # (any use of them raises AttributeError)
     return eng
 

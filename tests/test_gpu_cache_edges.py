@@ -43,3 +43,37 @@ def test_compaction_renames_a_prefill_that_is_staged():
     torch.cuda.synchronize()
     assert int(eng.status.item()) == 0
     assert (pools[0].k_scale[:4] > 0).all() and (pools[0].k_scale[4:] == 0).all()
+
+
+@pytest.mark.parametrize("f8", [False, True])
+def test_a_stack_whose_pools_have_different_numbers_of_blocks(f8):
+    """Each layer's call takes its own pool; only copies of blocks in all of them need as many everywhere."""
+    from transformer_decoder_layer_llama_gb300.serving import BlockAllocator, Scheduler, StackEngine
+    d, mb, slots, n = synth.DIMS_TINY, 4, 2, 20
+    cfg = api.make_config(d, max_position=mb * d.block_size)
+    packed = [api.pack_weights(cfg, {k: v.cuda() for k, v in synth.make_weights(d, 0.02, seed=7 + l).items()}) for l in range(2)]
+    ys = []
+    for blocks in ((12, 12), (12, 20)):
+        pools = [api.PoolF8.empty(nb, d.n_kv_heads, d.block_size, d.head_dim) if f8 else
+                 tuple(t.cuda() for t in synth.make_pool(nb, d, seed=3)) for nb in blocks]
+        sch = Scheduler(slots, d.block_size, mb, BlockAllocator(12, seed=5), seed=6, prompt_len=n)
+        eng = StackEngine(api, [cfg] * 2, packed, pools, slots, mb, slots * n)
+        for s in range(slots):
+            sch.start_resident(s, n)
+        eng.pf_table.copy_(torch.from_numpy(sch.table))
+        eng.pf_ctx.fill_(n)
+        eng.pf_pos.copy_(dev(np.tile(np.arange(n), slots)))
+        eng.pf_x.copy_(synth.make_x(slots * n, d.hidden, seed=1))
+        stream = torch.cuda.current_stream()
+        ys.append(eng.prefill(slots, n, stream).clone())
+        ctx = sch.grow_for_decode()
+        eng.table.copy_(torch.from_numpy(sch.table))
+        eng.ctx.copy_(torch.from_numpy(ctx))
+        eng.x.copy_(synth.make_x(slots, d.hidden, seed=2))
+        ys.append(eng.decode(stream).clone())
+        check(eng.status)
+    assert torch.equal(ys[0], ys[2]) and torch.equal(ys[1], ys[3])
+    before = sch.table.copy(), [list(r.blocks) for r in sch.slots]
+    with pytest.raises(ValueError, match="number of blocks"):
+        eng.compact(sch, stream)
+    assert (sch.table == before[0]).all() and [r.blocks for r in sch.slots] == before[1]

@@ -230,7 +230,7 @@ class StackEngine:
         self.f8 = isinstance(pools[0], api.PoolF8)
         self.ws = (api.new_workspace_f8 if self.f8 else api.new_workspace)(cfg, max(n_slots, max_prefill_tokens),
                                                                            max_blocks, device)
-        self.blocks = api.BlockSet([t for p in pools for t in (p.tensors() if self.f8 else p)])
+        self._blocks = None
         self.status = api.new_status(device)
         self.x = torch.zeros(n_slots, self.H, dtype=torch.bfloat16, device=device)
         self.bufs = [torch.empty(n_slots, self.H, dtype=torch.bfloat16, device=device) for _ in range(2)]
@@ -281,6 +281,14 @@ class StackEngine:
             src = dst
         return src
 
+    @property
+    def blocks(self):
+        """Every layer's pool as one BlockSet, for copy_blocks and compact: the pools then have as many blocks each.
+        (The layer calls take each layer's own pool, of any number of blocks.)"""
+        if self._blocks is None:
+            self._blocks = self.api.BlockSet([t for p in self.pools for t in (p.tensors() if self.f8 else p)])
+        return self._blocks
+
     def copy_blocks(self, pairs, stream):
         """Copies blocks (from, to), as Scheduler.fork names them, in the pools of every layer."""
         if pairs:
@@ -297,14 +305,15 @@ class StackEngine:
         held = scheduler.held_outside()
         if held:
             raise ValueError(f"blocks {held[:8]} are held outside the requests: free them before packing")
+        blocks = self.blocks
         stream.wait_stream(torch.cuda.current_stream())
         with torch.cuda.stream(stream):                       # behind the steps that still read the table
             self.table.copy_(torch.from_numpy(scheduler.table))
-            _, pairs, counts, block_map = self.api.compact_blocks(self.table, self.blocks.num_blocks,
+            _, pairs, counts, block_map = self.api.compact_blocks(self.table, blocks.num_blocks,
                                                                   new_table=self.table, status=self.status)
-            self.api.copy_blocks(self.blocks, pairs, n_pairs=counts[1:], status=self.status)
+            self.api.copy_blocks(blocks, pairs, n_pairs=counts[1:], status=self.status)
             old = self.pf_table
-            known = (old >= 0) & (old < self.blocks.num_blocks)
+            known = (old >= 0) & (old < blocks.num_blocks)
             old.copy_(torch.where(known, block_map[torch.where(known, old, 0).long()], old))
             block_map, counts = block_map.cpu().numpy(), counts.tolist()
         scheduler.apply_map(block_map)
