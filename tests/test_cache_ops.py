@@ -426,3 +426,27 @@ def test_the_tensors_of_a_pool_cannot_be_replaced(cls, names):
     for name in names:
         with pytest.raises(AttributeError):
             setattr(obj, name, torch.zeros(2))
+
+
+def test_the_stack_waits_for_the_stream_of_its_own_device(monkeypatch):
+    """copy_blocks and compact wait for the current stream of the tables' device, whichever device is current."""
+    from types import SimpleNamespace
+
+    from transformer_decoder_layer_llama_gb300.serving import BlockAllocator, Scheduler
+    eng = engine_without_a_gpu(8)
+    eng.table, eng.pf_table = torch.zeros(2, 2, dtype=torch.int32), torch.zeros(2, 2, dtype=torch.int32)
+    eng._blocks = SimpleNamespace(num_blocks=8)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: ("the stream of", device))
+
+    class Waited(Exception):
+        pass
+
+    class Stream:
+        def wait_stream(self, other):
+            raise Waited(other)
+
+    for call in (lambda: eng.copy_blocks([(0, 1)], Stream()),
+                 lambda: eng.compact(Scheduler(2, 16, 2, BlockAllocator(8, seed=1), seed=1), Stream())):
+        with pytest.raises(Waited) as e:
+            call()
+        assert e.value.args == (("the stream of", eng.table.device),)

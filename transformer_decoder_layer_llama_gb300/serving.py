@@ -293,7 +293,7 @@ class StackEngine:
         """Copies blocks (from, to), as Scheduler.fork names them, in the pools of every layer."""
         if pairs:
             t = torch.tensor(pairs, dtype=torch.int32, device=self.table.device)
-            stream.wait_stream(torch.cuda.current_stream())
+            stream.wait_stream(torch.cuda.current_stream(self.table.device))
             t.record_stream(stream)
             self.api.copy_blocks(self.blocks, t, status=self.status, stream=stream)
 
@@ -306,7 +306,7 @@ class StackEngine:
         if held:
             raise ValueError(f"blocks {held[:8]} are held outside the requests: free them before packing")
         blocks = self.blocks
-        stream.wait_stream(torch.cuda.current_stream())
+        stream.wait_stream(torch.cuda.current_stream(self.table.device))
         with torch.cuda.stream(stream):                       # behind the steps that still read the table
             self.table.copy_(torch.from_numpy(scheduler.table))
             _, pairs, counts, block_map = self.api.compact_blocks(self.table, blocks.num_blocks,
