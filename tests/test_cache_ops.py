@@ -450,3 +450,13 @@ def test_the_stack_waits_for_the_stream_of_its_own_device(monkeypatch):
         with pytest.raises(Waited) as e:
             call()
         assert e.value.args == (("the stream of", eng.table.device),)
+
+
+def test_rope_refuses_to_lose_a_gradient():
+    x, pos, tab = torch.zeros(2, 4, 64), torch.zeros(2, dtype=torch.int32), torch.zeros(8, 32, 2)
+    g = x.clone().requires_grad_()
+    for q, k in ((g, None), (None, g), (x, g), (g * 2, x)):
+        with pytest.raises(ValueError, match="autograd"):
+            api.rope(q, k, pos, tab)
+        with torch.no_grad(), pytest.raises(ValueError, match="GPU"):      # as for any other tensor
+            api.rope(q, k, pos, tab)

@@ -612,7 +612,9 @@ def pack_rope(cfg: ll_config, rope: ll_rope_config, packed: torch.Tensor, stream
 def rope(q, k, positions, table, layout="half", backward=False, q_out=None, k_out=None, status=None, stream=None):
     """ll_rope: q [tokens, n_heads, head_dim] and k [tokens, n_kv_heads, head_dim], BF16 or float32, heads
     contiguous within a token (views of a merged QKV output will do); either may be None.  `table` is
-    rope_table()'s.  Pass q_out=q (k_out=k) to rotate in place.  Returns (q_out, k_out)."""
+    rope_table()'s.  Pass q_out=q (k_out=k) to rotate in place.  The call is not recorded by autograd: the
+    gradient is the call with backward=True, and a tensor that requires one is refused unless gradients are
+    off (torch.no_grad()).  Returns (q_out, k_out)."""
     x = q if q is not None else k
     if x is None:
         raise ValueError("q and k are both None")
@@ -620,6 +622,8 @@ def rope(q, k, positions, table, layout="half", backward=False, q_out=None, k_ou
         raise TypeError("q and k must be bfloat16 or float32 tensors")
     if layout not in LL_ROPE_LAYOUTS:
         raise ValueError(f"layout must be one of {sorted(LL_ROPE_LAYOUTS)}, got {layout!r}")
+    if torch.is_grad_enabled() and (getattr(q, "requires_grad", False) or getattr(k, "requires_grad", False)):
+        raise ValueError("rope is not recorded by autograd: use torch.no_grad(), and backward=True for the gradient")
     T = d = None
     ends = []                      # per tensor: data, heads, stride, output data, output stride
     outs = []
