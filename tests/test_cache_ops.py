@@ -460,3 +460,10 @@ def test_rope_refuses_to_lose_a_gradient():
             api.rope(q, k, pos, tab)
         with torch.no_grad(), pytest.raises(ValueError, match="GPU"):      # as for any other tensor
             api.rope(q, k, pos, tab)
+
+
+def test_a_banded_table_does_not_look_at_the_attention_factor():
+    kw = dict(factor=2.0, original_max_position=4096, high_turns=4.0)
+    for factor in (-1.0, math.nan, math.inf):
+        assert api.lib.ll_rope_table_size(ctypes.byref(rope_cfg(scaling="banded", attention_factor=factor, **kw)), 16) == 16 * 32 * 8
+        assert api.lib.ll_rope_table_size(ctypes.byref(rope_cfg(scaling="yarn", attention_factor=factor, **kw)), 16) == 0

@@ -52,8 +52,9 @@ int rope_config_ok(const ll_rope_config* c) {
         if (c->original_max_position <= 0 || !(c->low_turns > 0.f) || !(c->high_turns > c->low_turns) ||
             !std::isfinite(c->high_turns))
             return LL_ERR_INVALID_ARG;
-        if (!(c->attention_factor >= 0.f) || !std::isfinite(c->attention_factor)) return LL_ERR_INVALID_ARG;
     }
+    if (c->scaling == LL_ROPE_YARN && (!(c->attention_factor >= 0.f) || !std::isfinite(c->attention_factor)))
+        return LL_ERR_INVALID_ARG;
     return LL_OK;
 }
 
