@@ -426,7 +426,8 @@ typedef struct {
  * Counts that do not fit together (n < 0, n > max_new, n > context_lens[b], rows
  * beyond `tokens`, a context beyond the table) set LL_DEV_BAD_POSITION and skip
  * the sequence; a bad block sets LL_DEV_BAD_BLOCK and is skipped.  Limits as
- * ll_paged_attention_decode_f8. */
+ * ll_paged_attention_decode_f8, and n_kv_heads times the blocks that max_new tokens
+ * can touch below 2^30. */
 int ll_append_to_cache_f8(const void* k, const void* v, int64_t k_stride, int64_t v_stride, const int32_t* cu_new,
                           int32_t tokens, const int32_t* context_lens, int32_t batch, int32_t max_new, int32_t n_kv_heads,
                           int32_t head_dim, int32_t block_size, const ll_kv_pool_f8* pool, const int32_t* block_table,
@@ -462,7 +463,9 @@ size_t ll_attention_prefill_f8_workspace_size(int32_t batch, int32_t tokens, int
  * together (LL_DEV_BAD_POSITION, as ll_append_to_cache_f8), are not written.
  * What lies in the cache behind a sequence's context is not read into the result;
  * a NaN among the new tokens' V may reach earlier rows of the call.  Limits and
- * workspace rule as ll_paged_attention_decode_f8. */
+ * workspace rule as ll_paged_attention_decode_f8, and batch * n_kv_heads times the
+ * pairs of query tiles of max_new tokens (floor(128 n_kv_heads / n_heads) tokens a
+ * tile) at most 2^30. */
 int ll_paged_attention_prefill_f8(const void* q, const int32_t* cu_new, int32_t tokens, const ll_kv_pool_f8* pool,
                                   const int32_t* block_table, int32_t max_blocks, const int32_t* context_lens,
                                   int32_t batch, int32_t max_new, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,

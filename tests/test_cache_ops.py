@@ -467,3 +467,15 @@ def test_a_banded_table_does_not_look_at_the_attention_factor():
     for factor in (-1.0, math.nan, math.inf):
         assert api.lib.ll_rope_table_size(ctypes.byref(rope_cfg(scaling="banded", attention_factor=factor, **kw)), 16) == 16 * 32 * 8
         assert api.lib.ll_rope_table_size(ctypes.byref(rope_cfg(scaling="yarn", attention_factor=factor, **kw)), 16) == 0
+
+
+def test_sizes_beyond_the_grids_are_refused_as_such():
+    a = {**PREFILL, **dict(n_heads=128, n_kv_heads=128, batch=65535, tokens=1 << 24, max_new=65535)}   # 128 * 256 * 65535 items
+    a["pool"] = ctypes.byref(pool_f8())
+    assert api.lib.ll_paged_attention_prefill_f8(*a.values(), NULL) == UNSUPPORTED
+    a["max_new"] = (1 << 31) - 1                       # an upper bound, cut to the tokens
+    assert api.lib.ll_paged_attention_prefill_f8(*a.values(), NULL) == UNSUPPORTED
+    w = 32767 * 128
+    b = {**APPEND, **dict(n_kv_heads=32767, k_stride=w, v_stride=w, tokens=(1 << 31) - 1, max_new=(1 << 31) - 1, max_blocks=1 << 16)}
+    b["pool"] = ctypes.byref(pool_f8())
+    assert api.lib.ll_append_to_cache_f8(*b.values(), NULL) == UNSUPPORTED

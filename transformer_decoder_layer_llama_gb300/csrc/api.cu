@@ -872,6 +872,9 @@ int layer_f8_args(const ll_config* cfg, const void* packed, const void* x, const
     if ((long long)batch * seq_len > (1 << 24) || batch > 65535 || cfg->n_kv_heads > 32767) return LL_ERR_UNSUPPORTED;
     if ((long long)max_blocks * cfg->block_size > (1LL << 30)) return LL_ERR_UNSUPPORTED;
     if ((long long)pool->num_blocks * cfg->n_kv_heads * cfg->block_size > (1LL << 31) - 1) return LL_ERR_UNSUPPORTED;
+    if (!ll::append_f8_fits(seq_len, cfg->n_kv_heads, cfg->block_size, max_blocks) ||
+        !ll::attn_prefill_f8_fits(batch, seq_len, cfg->n_heads, cfg->n_kv_heads))
+        return LL_ERR_UNSUPPORTED;
     return LL_OK;
 }
 }  // namespace

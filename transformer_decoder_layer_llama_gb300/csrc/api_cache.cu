@@ -220,6 +220,7 @@ int ll_append_to_cache_f8(const void* k, const void* v, int64_t k_stride, int64_
     if (!k || !v || !aligned16(k) || !aligned16(v) || k_stride % 8 != 0 || v_stride % 8 != 0 ||
         k_stride < (int64_t)n_kv_heads * head_dim || v_stride < (int64_t)n_kv_heads * head_dim)
         return LL_ERR_INVALID_ARG;
+    if (!ll::append_f8_fits(std::min(max_new, tokens), n_kv_heads, block_size, max_blocks)) return LL_ERR_UNSUPPORTED;
     ll::AppendArgs a{};
     a.k = static_cast<const __nv_bfloat16*>(k);
     a.v = static_cast<const __nv_bfloat16*>(v);
@@ -291,6 +292,7 @@ int ll_paged_attention_prefill_f8(const void* q, const int32_t* cu_new, int32_t 
     const int rc = f8_shape(batch, n_heads, n_kv_heads, head_dim, block_size, max_blocks, pool);
     if (rc != LL_OK) return rc;
     if (tokens > 0 && (!q || !out || !aligned16(q) || !aligned16(out))) return LL_ERR_INVALID_ARG;
+    if (!ll::attn_prefill_f8_fits(batch, std::min(max_new, tokens), n_heads, n_kv_heads)) return LL_ERR_UNSUPPORTED;
     const size_t need = ll_attention_prefill_f8_workspace_size(batch, tokens, max_new, n_heads, n_kv_heads, head_dim);
     if (!workspace || workspace_bytes < need || !aligned16(workspace)) return LL_ERR_WORKSPACE;
     ll::AttnF8Args a = f8_args(q, pool, block_table, max_blocks, context_lens, batch, n_heads, n_kv_heads, head_dim,

@@ -878,6 +878,9 @@ __global__ void __launch_bounds__(kPfJoinThreads) attn_prefill_f8_join_kernel(co
         make_uint2(pack_bf16x2(num.x * inv, num.y * inv), pack_bf16x2(num.z * inv, num.w * inv));
 }
 
+// Pairs of query tiles that max_new tokens of a sequence can take.
+int pf_query_tiles(int max_new, int tt) { return (int)(((long long)max_new + 2 * tt - 1) / (2 * tt)); }
+
 template <int D>
 cudaError_t prefill_f8_for(const AttnF8Args& a, cudaStream_t stream) {
     using L = PfLayout<D>;
@@ -890,12 +893,8 @@ cudaError_t prefill_f8_for(const AttnF8Args& a, cudaStream_t stream) {
                              "cudaFuncSetAttribute(attn_prefill_f8_kernel carveout)");
     if (e != cudaSuccess) return e;
     const int tt = kPfRows / (a.n_heads / a.n_kv_heads);    // tokens per query tile
-    const int n_mt = (a.max_new + 2 * tt - 1) / (2 * tt);
+    const int n_mt = pf_query_tiles(a.max_new, tt);
     const long long items = (long long)a.batch * n_mt * a.n_kv_heads;
-    if (items > (1LL << 30)) {
-        set_last_error("attn_prefill_f8", "too many (sequence, KV head, query tile) items");
-        return cudaErrorInvalidValue;
-    }
     const int sms = std::min(device_sm_count(), kF8MaxSms);
     if (sms <= 0) return record(cudaErrorNoDevice, "attn_prefill_f8");
     // Fewer items than half the SMs (a short chunk behind a long prefix): several CTAs per item.
@@ -919,6 +918,10 @@ cudaError_t prefill_f8_for(const AttnF8Args& a, cudaStream_t stream) {
 // One partial of 256 rows per CTA of a grid of at most as many CTAs as SMs; sized for the largest on any device.
 size_t attn_prefill_f8_scratch_bytes(int head_dim) {
     return (size_t)kF8MaxSms * 2 * kPfRows * (head_dim * sizeof(float) + sizeof(float2));
+}
+
+bool attn_prefill_f8_fits(int batch, int max_new, int n_heads, int n_kv_heads) {
+    return (long long)batch * pf_query_tiles(max_new, kPfRows / (n_heads / n_kv_heads)) * n_kv_heads <= 1LL << 30;
 }
 
 cudaError_t launch_attn_prefill_f8(AttnF8Args a, void* workspace, cudaStream_t stream) {

@@ -222,6 +222,8 @@ struct AppendArgs {
     int32_t* status;
 };
 cudaError_t launch_append_f8(const AppendArgs& a, cudaStream_t stream);
+// Whether the grid holds a call of these sizes.
+bool append_f8_fits(int max_new, int n_kv_heads, int block_size, int max_blocks);
 // Positions of seq_len new tokens at each context's end, and their cu_new [batch + 1].
 cudaError_t launch_f8_positions(const int32_t* context_lens, int batch, int seq_len, int32_t* positions, int32_t* cu_new,
                                 cudaStream_t stream);
@@ -245,6 +247,7 @@ size_t attn_decode_f8_scratch_bytes(int batch, int n_heads, int n_kv_heads, int 
 cudaError_t launch_attn_decode_f8(AttnF8Args a, void* workspace, cudaStream_t stream);
 size_t attn_prefill_f8_scratch_bytes(int head_dim);
 cudaError_t launch_attn_prefill_f8(AttnF8Args a, void* workspace, cudaStream_t stream);
+bool attn_prefill_f8_fits(int batch, int max_new, int n_heads, int n_kv_heads);
 
 // Copies blocks src -> dst of `pairs` in every tensor [num_blocks][bytes] (blocks.cu).
 constexpr int kCopyMaxTensors = 128;   // per launch

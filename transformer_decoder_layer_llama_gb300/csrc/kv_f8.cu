@@ -244,16 +244,15 @@ __global__ void f8_positions_kernel(const int32_t* context_lens, int batch, int 
     if (t <= batch) cu_new[t] = t * seq_len;
 }
 
+// (block, KV head, K or V) of a sequence: blocks that max_new consecutive positions can touch.
+long long append_pairs(int max_new, int n_kv_heads, int block_size, int max_blocks) {
+    return 2LL * n_kv_heads * std::min(((long long)max_new + block_size - 2) / block_size + 1, (long long)max_blocks);
+}
+
 template <int D>
 cudaError_t append_for(const AppendArgs& a, cudaStream_t stream) {
-    // (block, KV head, K or V) of a sequence: blocks that max_new consecutive positions can touch.  Heads fastest: the
-    // CTAs that run together read whole token rows (blocks fastest: 25.5 us for the 24.2 of ragged 70B-shaped chunks).
-    const int touch = std::min((a.max_new + a.block_size - 2) / a.block_size + 1, a.max_blocks);
-    const long long pairs = 2LL * a.n_kv_heads * touch;
-    if (pairs > 0x7fffffffLL) {
-        set_last_error("append_f8", "too many (block, KV head) pairs");
-        return cudaErrorInvalidValue;
-    }
+    // Heads fastest: the CTAs that run together read whole token rows (blocks fastest: 25.5 us for the 24.2 of ragged 70B-shaped chunks).
+    const long long pairs = append_pairs(a.max_new, a.n_kv_heads, a.block_size, a.max_blocks);
     cudaError_t e;
     trace_before("append_f8", stream);
     if (a.max_new == 1) {
@@ -286,6 +285,10 @@ cudaError_t launch_f8_positions(const int32_t* context_lens, int batch, int seq_
     trace_after(stream);
     if (e == cudaSuccess) e = cudaGetLastError();
     return record(e, "f8_positions_kernel launch");
+}
+
+bool append_f8_fits(int max_new, int n_kv_heads, int block_size, int max_blocks) {
+    return append_pairs(max_new, n_kv_heads, block_size, max_blocks) <= 0x7fffffffLL;
 }
 
 cudaError_t launch_append_f8(const AppendArgs& a, cudaStream_t stream) {
