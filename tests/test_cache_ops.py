@@ -479,3 +479,11 @@ def test_sizes_beyond_the_grids_are_refused_as_such():
     b = {**APPEND, **dict(n_kv_heads=32767, k_stride=w, v_stride=w, tokens=(1 << 31) - 1, max_new=(1 << 31) - 1, max_blocks=1 << 16)}
     b["pool"] = ctypes.byref(pool_f8())
     assert api.lib.ll_append_to_cache_f8(*b.values(), NULL) == UNSUPPORTED
+
+
+def test_binding_refuses_status_words_of_other_types():
+    for bad in (torch.zeros(1, dtype=torch.int64), torch.zeros(4, dtype=torch.uint8)[1:], torch.zeros(1)):
+        with pytest.raises(TypeError, match="status"):
+            api._status(bad)
+    with pytest.raises(ValueError, match="GPU"):
+        api._status(torch.zeros(1, dtype=torch.int32))

@@ -77,3 +77,33 @@ def test_a_stack_whose_pools_have_different_numbers_of_blocks(f8):
     with pytest.raises(ValueError, match="number of blocks"):
         eng.compact(sch, stream)
     assert (sch.table == before[0]).all() and [r.blocks for r in sch.slots] == before[1]
+
+
+def test_calls_refuse_status_words_that_are_no_int32():
+    """The kernels set bits of a 4-byte word: a byte tensor's address may be any."""
+    rng = np.random.default_rng(3)
+    ref, table = make_cache(rng, [20, 9], 2, 64, 16)
+    pool, t, ctx, cu = to_gpu(ref), dev(table), dev([20, 9]), dev([0, 1, 2])
+    q = torch.zeros(2, 4, 64, dtype=torch.bfloat16, device="cuda")
+    tab = api.rope_table(api.make_rope_config(64), 16)
+    d = synth.DIMS_TINY
+    cfg = api.make_config(d, max_position=64)
+    packed = api.pack_weights(cfg, {k: v.cuda() for k, v in synth.make_weights(d, 0.02, seed=1).items()})
+    layer = api.PoolF8.empty(4, d.n_kv_heads, d.block_size, d.head_dim)
+    x = synth.make_x(2, d.hidden, seed=2).cuda()
+    for bad, error in ((torch.zeros(8, dtype=torch.uint8, device="cuda")[1:], TypeError),
+                       (torch.zeros(1, dtype=torch.int64, device="cuda"), TypeError),
+                       (torch.zeros(0, dtype=torch.int32, device="cuda"), ValueError),
+                       (torch.zeros(1, dtype=torch.int32), ValueError)):
+        for call in (lambda st: api.rope(q, None, dev([0, 1]), tab, status=st),
+                     lambda st: api.append_to_cache_f8(q[:, :2].contiguous(), q[:, 2:].contiguous(), pool, t, ctx, status=st),
+                     lambda st: api.paged_attention_decode_f8(q, pool, t, ctx, 0.1, status=st),
+                     lambda st: api.paged_attention_prefill_f8(q, cu, pool, t, ctx, 0.1, max_new=1, status=st),
+                     lambda st: api.layer_decode_step_f8(cfg, packed, x, layer, dev([[0], [1]]), dev([1, 1]), status=st),
+                     lambda st: api.layer_prefill_f8(cfg, packed, x, layer, dev([[0], [1]]), dev([1, 1]), 1, status=st),
+                     lambda st: api.copy_blocks(api.BlockSet(pool.tensors()), dev([[0, 1]]), status=st),
+                     lambda st: api.compact_blocks(t, len(ref.k), status=st)):
+            with pytest.raises(error, match="status"):
+                call(bad)
+    torch.cuda.synchronize()
+    assert_pool(pool, ref)

@@ -542,6 +542,14 @@ def _rows3(t, name, dtype):
     return st if T > 1 else H * d
 
 
+def _status(t):
+    """A status word that the caller passed: the kernels set its bits as an int32."""
+    _need(t, "status", torch.int32)
+    if t.numel() < 1:
+        raise ValueError("status must hold one number")
+    return t
+
+
 def _on(first, *tensors):
     """The index of the device that all the tensors share (None among them is passed over)."""
     dev = first.get_device()
@@ -653,8 +661,7 @@ def rope(q, k, positions, table, layout="half", backward=False, q_out=None, k_ou
     if len(rows) != 3 or rows[2] != 2 or not 2 <= 2 * rows[1] <= d:
         raise ValueError("table must be [max_position, rotary_dim / 2, 2] with rotary_dim <= head_dim")
     own_status = status is None
-    if own_status:
-        status = new_status(x.device)
+    status = new_status(x.device) if own_status else _status(status)
     dev = _on(x, k, outs[0], outs[1], positions, table, status)
     if stream is not None:
         _made(stream, dev, outs[0] if q_out is None else None, outs[1] if k_out is None else None,
@@ -731,8 +738,7 @@ def append_to_cache_f8(k, v, pool: PoolF8, block_table, context_lens, cu_new=Non
     if cu_new is not None:
         _need(cu_new, "cu_new", torch.int32, shape=(B + 1,))
     own_status = status is None
-    if own_status:
-        status = new_status(k.device)
+    status = new_status(k.device) if own_status else _status(status)
     dev = _on(k, v, pool.k, block_table, context_lens, cu_new, status)
     if stream is not None and own_status:
         _made(stream, dev, status)
@@ -766,8 +772,7 @@ def _f8_attention(q, pool, out, workspace, status, size, stream):
         workspace = torch.empty(max(size(), 16), dtype=torch.uint8, device=q.device)
     else:
         _need(workspace, "workspace", torch.uint8)
-    if status is None:
-        status = new_status(q.device)
+    status = new_status(q.device) if status is None else _status(status)
     if stream is not None:
         _made(stream, q.get_device(), *(t if g is None else None for g, t in zip(given, (out, workspace, status))))
     return out, workspace, status
@@ -830,8 +835,7 @@ def _layer_f8(cfg, packed, x, pool, block_table, context_lens, tokens, y, worksp
         workspace = new_workspace_f8(cfg, tokens, block_table.shape[1], x.device)
     else:
         _need(workspace, "workspace", torch.uint8)
-    if status is None:
-        status = new_status(x.device)
+    status = new_status(x.device) if status is None else _status(status)
     dev = _on(x, packed, pool.k, block_table, context_lens, y, workspace, status)
     if stream is not None:
         _made(stream, dev, *(t if g is None else None for g, t in zip(given, (y, workspace, status))))
@@ -898,8 +902,7 @@ def copy_blocks(blocks: BlockSet, pairs, n_pairs=None, status=None, stream=None)
         if n_pairs.numel() != 1:
             raise ValueError("n_pairs must hold one number")
     own_status = status is None
-    if own_status:
-        status = new_status(blocks.device)
+    status = new_status(blocks.device) if own_status else _status(status)
     dev = _on(blocks.tensors[0], pairs, n_pairs, status)
     if stream is not None and own_status:
         _made(stream, dev, status)
@@ -928,8 +931,7 @@ def compact_blocks(block_table, num_blocks, new_table=None, pairs=None, counts=N
     _need(pairs, "pairs", torch.int32, shape=(num_blocks // 2, 2))
     _need(counts, "counts", torch.int32, shape=(2,))
     _need(block_map, "block_map", torch.int32, shape=(num_blocks,))
-    if status is None:
-        status = new_status(dev)
+    status = new_status(dev) if status is None else _status(status)
     dev = _on(block_table, new_table, pairs, counts, block_map, status)
     if stream is not None:
         _made(stream, dev, *(t if g is None else None for g, t in zip(given, (new_table, pairs, counts, block_map, status))))
