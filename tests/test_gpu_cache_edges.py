@@ -107,3 +107,75 @@ def test_calls_refuse_status_words_that_are_no_int32():
                 call(bad)
     torch.cuda.synchronize()
     assert_pool(pool, ref)
+
+
+@pytest.mark.parametrize("B,H,Hkv,d", [(1025, 4, 2, 64), (2100, 6, 3, 128), (1300, 18, 2, 64)])
+def test_decode_of_thousands_of_sequences_some_of_which_many_ctas_share(B, H, Hkv, d):
+    """Beyond 1024 sequences a CTA of the join takes a run of them: long contexts first, last and side by side in a run,
+    which are cut over several CTAs each, among short and empty ones."""
+    rng = np.random.default_rng(B)
+    bs = 16
+    ctx = rng.integers(0, 40, B)
+    ctx[[3, 4, B // 2 + 2, B - 2]] = 0
+    long = [0, B // 2, B // 2 + 1, B - 1]              # (runs of B / 1024 rounded up: 2 or 3)
+    ctx[long] = [5000, 3001, 2500, 4097]
+    ref, table = make_cache(rng, list(ctx), Hkv, d, bs)
+    q = torch.from_numpy(rng.normal(size=(B, H, d))).bfloat16()
+    want = C.attention_f8(f64(q), ref, table, ctx, np.arange(B + 1), d ** -0.5)
+    st = status()
+    ws = torch.full((api.attention_decode_f8_workspace_size(B, H, Hkv, d),), 0xFF, dtype=torch.uint8, device="cuda")
+    out = torch.full((B, H, d), float("nan"), dtype=torch.bfloat16, device="cuda")
+    api.paged_attention_decode_f8(q.cuda(), to_gpu(ref), dev(table), dev(ctx), d ** -0.5, out=out, workspace=ws, status=st)
+    check(st)
+    for some in (long, np.flatnonzero(ctx == 0)):      # (named first, so that a failure says which)
+        assert_attention(out[torch.as_tensor(some).cuda()], *(w[some] for w in want), d)
+    assert_attention(out, *want, d)
+    assert (out[torch.from_numpy(ctx == 0).cuda()] == 0).all()
+
+
+@pytest.mark.parametrize("bs,H,Hkv,d", [(16, 8, 2, 64), (128, 16, 2, 128), (64, 3, 3, 128)])
+def test_prefill_of_a_prompt_beside_single_tokens_behind_long_prefixes(bs, H, Hkv, d):
+    """Items of one query tile and of two side by side, each with its own number of key tiles; with an empty sequence,
+    a short chunk, and more than a warp's lanes of sequences."""
+    rng = np.random.default_rng(bs + H)
+    for before, new in (([0, 5000, 3000, 17, 4100, 0, 700], [600, 1, 1, 0, 1, 33, 5]),
+                        ([0] * 3 + [900] * 32, [300, 129, 0] + [1] * 32)):
+        ctx = [b + n for b, n in zip(before, new)]
+        ref, table = make_cache(rng, ctx, Hkv, d, bs)
+        cu = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+        q = torch.from_numpy(rng.normal(size=(int(cu[-1]) + 2, H, d))).bfloat16()
+        want = C.attention_f8(f64(q[:cu[-1]]), ref, table, ctx, cu, d ** -0.5)
+        st = status()
+        out = torch.full(tuple(q.shape), 5.0, dtype=torch.bfloat16, device="cuda")
+        ws = torch.full((api.attention_prefill_f8_workspace_size(len(new), len(q), max(new), H, Hkv, d),), 0xFF,
+                        dtype=torch.uint8, device="cuda")
+        for _ in range(2):
+            api.paged_attention_prefill_f8(q.cuda(), dev(cu), to_gpu(ref), dev(table), dev(ctx), d ** -0.5, max_new=max(new),
+                                           out=out, workspace=ws, status=st)
+            check(st)
+            assert_attention(out[:cu[-1]], *want, d)
+            assert (out[cu[-1]:] == 5).all()
+
+
+@pytest.mark.parametrize("rot", [64, 24])
+def test_rope_leaves_the_rows_of_bad_positions_in_views_of_merged_rows(rot):
+    """Whole 16-byte columns (64) and not (24 of 64, half-split): rows of a wider buffer, out of place and in place."""
+    T, H, Hkv, d = 6, 3, 2, 64
+    w = (H + 2 * Hkv) * d + 8
+    g = torch.Generator().manual_seed(rot)
+    x = torch.randn(T, w, generator=g).bfloat16().cuda()
+    q, k = x[:, :H * d].view(T, H, d), x[:, H * d:(H + Hkv) * d].view(T, Hkv, d)
+    tab, pos, bad = api.rope_table(api.make_rope_config(rot), 16), dev([0, -1, 15, 16, 3, 2 ** 31 - 1]), [1, 3, 5]
+    good, st = [0, 2, 4], status()
+    want = api.rope(q[good].contiguous(), k[good].contiguous(), pos[good].contiguous(), tab, status=st)
+    check(st)
+    y = torch.full_like(x, 7.0)
+    q1, k1 = y[:, :H * d].view(T, H, d), y[:, H * d:(H + Hkv) * d].view(T, Hkv, d)
+    before = x.clone()
+    for outs in ((q1, k1), (q, k)):
+        st = status()
+        api.rope(q, k, pos, tab, q_out=outs[0], k_out=outs[1], status=st)
+        check(st, api.LL_DEV_BAD_POSITION)
+        assert torch.equal(outs[0][good], want[0]) and torch.equal(outs[1][good], want[1])
+    assert (y[bad] == 7).all() and (y[:, (H + Hkv) * d:] == 7).all()
+    assert torch.equal(x[bad], before[bad]) and torch.equal(x[:, (H + Hkv) * d:], before[:, (H + Hkv) * d:])
