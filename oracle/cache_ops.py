@@ -105,7 +105,7 @@ class PoolF8:
 def attention_f8(q, pool, table, context_lens, cu, scale):
     """Causal attention of the new tokens (rows cu[b] .. cu[b+1]-1 of q float64 [tokens, heads, d]).  Returns
     (out, weight, spread): the output, sum p |v| per element, and per row (largest scale * sum |q k| over the
-    keys seen, number of keys, largest |v|)."""
+    keys seen, number of keys, largest |v| among them)."""
     T, H, d = q.shape
     Hkv = pool.k.shape[1]
     G = H // Hkv
@@ -128,8 +128,26 @@ def attention_f8(q, pool, table, context_lens, cu, scale):
                 out[cu[b]:cu[b + 1], h] = p @ v
                 weight[cu[b]:cu[b + 1], h] = p @ np.abs(v)
                 mag = np.where(seen, (np.abs(x) @ np.abs(k).T) * scale, 0.0)
-                info[cu[b]:cu[b + 1], h] = np.stack((mag.max(1), seen.sum(1), np.full(n, np.abs(v).max())), 1)
+                vmax = np.where(seen, np.abs(v).max(1)[None, :], 0.0).max(1)
+                info[cu[b]:cu[b + 1], h] = np.stack((mag.max(1), seen.sum(1), vmax), 1)
     return out, weight, info
+
+
+def largest_term(q, pool, table, context_lens, cu, scale):
+    """Per query row [tokens, heads, 1]: the largest probability times 448 times the V scale of its key, a bound on
+    any one key's share of the output."""
+    ones = PoolF8(pool.k, np.full_like(pool.v, e4m3_codes(448.0)), pool.k_scale, pool.v_scale)
+    T, H, _ = q.shape
+    Hkv, top = pool.k.shape[1], np.zeros((T, H, 1))
+    for b in range(len(context_lens)):
+        n, ctx = int(cu[b + 1] - cu[b]), int(context_lens[b])
+        for h in range(H if n else 0):
+            k, v, ok = ones.rows(table[b], ctx, h // (H // Hkv))
+            seen = (np.arange(ctx)[None, :] <= (ctx - n + np.arange(n))[:, None]) & ok[None, :]
+            s = np.where(seen, (q[cu[b]:cu[b + 1], h] @ k.T) * scale, -np.inf)
+            p = np.exp(s - np.max(s, 1, keepdims=True, initial=-1e300))
+            top[cu[b]:cu[b + 1], h, 0] = (p / np.maximum(p.sum(1, keepdims=True), 1e-300) * v[:, 0]).max(1, initial=0.0)
+    return top
 
 
 def inv_freq(rotary_dim, theta=10000.0, scaling="plain", factor=1.0, original=0, low=1.0, high=None, magnitude=0.0):

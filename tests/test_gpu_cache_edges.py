@@ -179,3 +179,92 @@ def test_rope_leaves_the_rows_of_bad_positions_in_views_of_merged_rows(rot):
         assert torch.equal(outs[0][good], want[0]) and torch.equal(outs[1][good], want[1])
     assert (y[bad] == 7).all() and (y[:, (H + Hkv) * d:] == 7).all()
     assert torch.equal(x[bad], before[bad]) and torch.equal(x[:, (H + Hkv) * d:], before[:, (H + Hkv) * d:])
+
+
+# ---------------------------------------------------------------- values that a row does not see, or hardly weighs
+
+def assert_by_terms(got, q, pool, table, ctx, cu, scale, extra=0.0):
+    """As assert_attention, with what the FP16 probabilities lose counted against the largest term that the row
+    itself sums, not the largest |v| around: a probability times its V scale enters P V relative to a base, times 2^6.
+    The base is at most 2^4 above the largest such product of the row (keys whose scales differ by less share one),
+    so where it is subnormal it is off by 2^-25 of 2^-2 of that product, and a code (448) may carry a factor below 2."""
+    d = q.shape[2]
+    ref, weight, info = C.attention_f8(f64(q), pool, table, ctx, cu, scale)
+    mag, n = info[..., :1], info[..., 1:2]
+    rel = 2.0 ** -11 + 2.0 ** -23 * (d + 4) * mag + 2.0 ** -20 + (n / 16 + n / 128 + 8) * 2.0 ** -23 + extra
+    bound = 2.0 ** -8 * np.abs(ref) + 1.01 * rel * weight + (n + 1) * 2.0 ** -26 * C.largest_term(f64(q), pool, table, ctx, cu, scale)
+    got = f64(got)
+    bad = ~(np.abs(got - ref) <= bound)
+    assert not bad.any(), (int(bad.sum()), np.argwhere(bad)[:4], got[bad][:4], ref[bad][:4])
+
+
+def one_large_value(rng, before, new, Hkv, d, bs, at, size, u=None):
+    """A cache of contexts before + new in which position at[b] of sequence b has a V `size` times as large (and, with u,
+    every position of its block the key u: a block's scale counts for each of its keys)."""
+    ctx = [b + n for b, n in zip(before, new)]
+    pool, table = make_cache(rng, ctx, Hkv, d, bs)
+    k, v = (bf16(rng.normal(size=(sum(ctx), Hkv, d))) for _ in range(2))
+    starts = np.concatenate([[0], np.cumsum(ctx)]).astype(int)
+    for b, p in enumerate(at):
+        v[starts[b] + p] *= size
+        if u is not None:
+            lo = p // bs * bs
+            k[starts[b] + lo:starts[b] + min(lo + bs, ctx[b])] = u
+    pool.append(bf16(k), bf16(v), table, ctx, starts)
+    return pool, table, ctx
+
+
+@pytest.mark.parametrize("bs,H,Hkv,d", [(16, 4, 2, 64), (128, 4, 4, 128), (32, 16, 1, 128)])
+@pytest.mark.parametrize("size", [2.0 ** 24, 2.0 ** 60])
+def test_a_large_value_does_not_reach_rows_that_do_not_see_it(bs, H, Hkv, d, size):
+    """The last new tokens have V far above the others': the rows before them answer as without it (chunks, a prompt of
+    two query tiles, and a few tokens behind a long prefix, whose keys several CTAs share)."""
+    for before, new in (([40, 0, 200], [100, 300, 2]), ([3000], [20])):
+        rng = np.random.default_rng(bs + d)
+        ctx = [b + n for b, n in zip(before, new)]
+        pool, table, ctx = one_large_value(rng, before, new, Hkv, d, bs, [c - 1 for c in ctx], size)
+        cu = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+        q = torch.from_numpy(rng.normal(size=(int(cu[-1]), H, d))).bfloat16()
+        st = status()
+        out = api.paged_attention_prefill_f8(q.cuda(), dev(cu), to_gpu(pool), dev(table), dev(ctx), d ** -0.5, max_new=max(new), status=st)
+        check(st)
+        assert_by_terms(out, q, pool, table, ctx, cu, d ** -0.5)
+
+
+@pytest.mark.parametrize("bs,H,Hkv,d", [(16, 4, 2, 64), (128, 4, 4, 128), (32, 16, 1, 128)])
+@pytest.mark.parametrize("size", [2.0 ** 24, 2.0 ** 60])
+def test_a_large_value_that_hardly_weighs_leaves_the_others_their_bits(bs, H, Hkv, d, size):
+    """A block far from every query (its probabilities about e^-150) has a V far above the others': decode and prefill."""
+    rng = np.random.default_rng(bs + d)
+    u = rng.choice([-1.0, 1.0], size=d)
+    before, new = [3000, 0, 300], [3, 300, 40]
+    pool, table, ctx = one_large_value(rng, before, new, Hkv, d, bs, [1234, 0, 177], size, u=-4 * u)
+    cu = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    T = int(cu[-1])
+    q = torch.from_numpy(4.0 * u + rng.normal(size=(T, H, d))).bfloat16()
+    scale = 150.0 / (16 * d)
+    st = status()
+    out = api.paged_attention_prefill_f8(q.cuda(), dev(cu), to_gpu(pool), dev(table), dev(ctx), scale, max_new=max(new), status=st)
+    one = api.paged_attention_decode_f8(q[:3].cuda(), to_gpu(pool), dev(table), dev(ctx), scale, status=st)
+    check(st)
+    assert_by_terms(one, q[:3], pool, table, ctx, np.arange(4), scale)
+    assert_by_terms(out, q, pool, table, ctx, cu, scale)
+
+
+@pytest.mark.parametrize("power", [-123, -110, 80])
+def test_value_scales_far_from_one(power):
+    """V scales of 2^power and a few powers above, in blocks side by side."""
+    rng = np.random.default_rng(power + 200)
+    before, new, H, Hkv, d, bs = [600, 0], [5, 130], 4, 2, 64, 16
+    ctx = [605, 130]
+    pool, table = make_cache(rng, ctx, Hkv, d, bs)
+    live = pool.v_scale == pool.v_scale
+    pool.v_scale[live] = 2.0 ** (power + rng.integers(0, 3, size=int(live.sum())))
+    cu = np.array([0, 5, 135], np.int32)
+    q = torch.from_numpy(rng.normal(size=(135, H, d))).bfloat16()
+    st = status()
+    out = api.paged_attention_prefill_f8(q.cuda(), dev(cu), to_gpu(pool), dev(table), dev(ctx), 0.125, max_new=130, status=st)
+    one = api.paged_attention_decode_f8(q[:2].cuda(), to_gpu(pool), dev(table), dev(ctx), 0.125, status=st)
+    check(st)
+    assert_by_terms(one, q[:2], pool, table, ctx, np.arange(3), 0.125)
+    assert_by_terms(out, q, pool, table, ctx, cu, 0.125)

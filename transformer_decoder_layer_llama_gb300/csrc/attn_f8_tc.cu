@@ -16,7 +16,7 @@
 //    At the end O / l goes out.
 //  * warps 8-11, converters: the codes of a key tile, as they lie in the pool, become FP16 in the
 //    128-byte-swizzled operand tiles, two buffers each for K and V.
-//  * warp 14: brings codes (bulk copies of 16 keys) and scales a tile ahead.  (Loaded straight into the converters'
+//  * warp 14: brings codes (bulk copies of 16 keys) and scales a tile ahead, and looks at how far V scales differ.  (Loaded straight into the converters'
 //    registers they were what the rest waited for: the little L1 that this much shared memory leaves cannot
 //    keep a tile's loads in flight.)
 //  * warps 12 and 13, one elected lane each: S = Q K^T (both from shared memory) and O += P V (P from TMEM) of
@@ -35,9 +35,16 @@
 // lies in [2^14, 2^15); its factor and the block's K scale multiply the float32 score, 16 keys at a time
 // (a block holds whole 16-key chunks), so they cost nothing per element but the multiply-add there already
 // is.  P is one FP16 (relative error 2^-11, an eighth of the BF16 output's half step), relative to an
-// exponent base that keeps it below 2^14.  V carries its block's scale relative to the largest scale of the
-// item's keys, times 2^6: exact for powers of two down to 2^-21 of that scale (values below about 2^-31 of
-// the largest are lost).  Row maxima, sums, S and O are float32.
+// exponent base that keeps it below 2^14.  Row maxima, sums, S and O are float32.
+//
+// V scales belong to blocks, and what a row sums is probability times V scale times code.  So P holds such
+// terms, 2^(score + log2 of the V scale - t + 6), where t is the largest term that the row itself has met: a
+// block that the row does not see, or hardly weighs, takes no bits from the others, however large its V.  The
+// sum of the probabilities has a base of its own (m); terms times one power of two per tile are probabilities.
+// Where the scales of a tile of keys differ, but by 2^4 at most, V is code times the scale's ratio to one
+// power of two for the tile (exact for powers of two), and t at most 4 too large; where they differ by more, the
+// tile takes a slower path that gives each 16 keys their own scale.  A term is lost below about 2^-27 of the
+// row's largest.
 #include <algorithm>
 
 #include "common.cuh"
@@ -54,8 +61,15 @@ constexpr int kPfKeys = 128;             // keys per tile
 constexpr int kPfChunks = kPfKeys / 16;
 constexpr int kPfMeta = 4;               // tiles whose scales are kept
 constexpr float kPfLog2e = 1.4426950408889634f;
-constexpr int kPfShift = 6;              // V enters P V times 2^6
-constexpr float kPfBase = 6.f;           // and P times 2^6
+constexpr float kPfShift = 6.f;          // P enters P V times 2^6
+constexpr float kPfFloor = 80.f;         // a V scale this far (in powers of two) below the largest term adds nothing
+
+// The V scales of a key tile: all alike; within 2^4 of each other: V enters P V as code times its scale's ratio to a
+// power of two that the whole tile has (exact for scales that are powers of two); further apart: V is the bare code,
+// and each 16 keys' probabilities carry their own scale.
+enum PfScales { kOneScale, kNearScales, kFarScales };
+constexpr float kPfSpread = 16.f;
+constexpr uint32_t kPfFar = 1u << kPfChunks;   // beside the bits of a tile's chunks
 
 template <int D>
 struct PfLayout {
@@ -337,9 +351,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
     __shared__ uint32_t tmem_base_s;
     __shared__ int abort_s;
     __shared__ __align__(16) float ks_s[kPfMeta][kPfChunks];   // per 16-key chunk: K scale
-    __shared__ float vs_s[kPfMeta][kPfChunks];              // and V scale
+    __shared__ float v_s[kPfMeta][kPfChunks];               // near scales: ratio of the V scale to the tile's; far: its log2
+    __shared__ uint2 tile_s[kPfMeta];                       // log2 of the tile's V scale; ok_s, and whether they are far apart
+    __shared__ int near_s[kPfMeta];                         // whether its V scales are near, not alike
     __shared__ uint32_t ok_s[kPfMeta];                      // bit c = chunk c is backed by a valid block
-    __shared__ int vexp_w[4], vexp_s;                       // exponent of the item's largest V scale
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int32_t* status = a.status;
@@ -528,6 +543,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
                 return j == 0 || __all_sync(0xffffffffu, pf_wait(&c_empty[which], (uint32_t)(j - 1) & 1u, &abort_s));
             };
             int k_at = -1, v_at = -1;
+            float lvr = 0.f;                                // log2 of the tile's V scale
+            uint32_t v_at_log = ~0u;                        // the scale whose log2 lvr is
 #pragma unroll 1
             for (int j = 0; j < n_kt; ++j) {
                 const int slot = j & (kPfMeta - 1);
@@ -543,9 +560,24 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
                 __syncwarp();
                 bring(0, a.k_pool, j, row, mask);
                 k_at = j;
-                if (lane < kPfChunks) {
-                    ks_s[slot][lane] = ks;
-                    vs_s[slot][lane] = vs;
+                const uint32_t vb = __float_as_uint(vs);    // (scales are not negative: ordered as integers)
+                const uint32_t hi = __reduce_max_sync(0xffffffffu, lane < kPfChunks && row >= 0 ? vb : 0u);
+                const uint32_t lo = __reduce_min_sync(0xffffffffu, lane < kPfChunks && row >= 0 ? vb : hi);
+                PfScales kind = kOneScale;
+                if (hi != v_at_log || lo != hi) {
+                    lvr = f8_log2_scale(__uint_as_float(hi));
+                    v_at_log = hi;
+                    if (lo != hi) {
+                        kind = __uint_as_float(lo) * kPfSpread >= __uint_as_float(hi) ? kNearScales : kFarScales;
+                        if (kind == kNearScales) lvr = floorf(lvr);
+                        v_at_log = ~0u;
+                        if (lane < kPfChunks) v_s[slot][lane] = kind == kNearScales ? scalbnf(vs, -(int)lvr) : f8_log2_scale(vs);
+                    }
+                }
+                if (lane < kPfChunks) ks_s[slot][lane] = ks;
+                if (lane == 0) {
+                    tile_s[slot] = make_uint2(__float_as_uint(lvr), kind == kFarScales ? mask | kPfFar : mask);
+                    near_s[slot] = kind == kNearScales;
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&meta_ready[slot]);
@@ -571,7 +603,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
         const int rsub = D == 128 ? ((tid >> 3) & ~1) | ((tid >> 2) & 1) : tid >> 2;
         const uint32_t st0 = pf_off(rsub, 2 * c16), st1 = pf_off(rsub, 2 * c16 + 1);
         // Tile j from its codes to the operand tile; rows that hold no key become zeros: 0 * stale stays 0.
-        auto convert = [&](uint8_t* tile, const uint8_t* codes, int j, uint64_t* done, bool scaled, float up0, float up1) {
+        auto convert = [&](uint8_t* tile, const uint8_t* codes, int j, uint64_t* done, bool scaled) {
             const int slot = j & (kPfMeta - 1), left = kv_end - j * kPfKeys;
             const uint32_t chunks = ok_s[slot];
             uint4 w[PER];
@@ -592,7 +624,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
                 e4m3x4_to_f16x4(w[i].z, h[4], h[5]);
                 e4m3x4_to_f16x4(w[i].w, h[6], h[7]);
                 if (scaled) {
-                    const __half2 f = __float2half2_rn(vs_s[slot][(i * ROWS + rsub) >> 4] * up0 * up1);
+                    const __half2 f = __float2half2_rn(v_s[slot][(i * ROWS + rsub) >> 4]);
 #pragma unroll
                     for (int x = 0; x < 8; ++x) {
                         const __half2 p = __hmul2(*reinterpret_cast<const __half2*>(&h[x]), f);
@@ -608,34 +640,18 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
             // can be seen before they have read.)
             if (lane == 0) mbar_arrive(done);
         };
-        // exponent of the largest V scale of the CTA's keys
-        const int n = (key0 + min(kv_end, n_kt * kPfKeys) + a.block_size - 1) >> bs_log2;
-        float top = 0.f;
-#pragma unroll 1
-        for (int i = (key0 >> bs_log2) + tid; i < n; i += 128) {
-            const int x = table_row[i];
-            if (x >= 0 && x < a.num_blocks) top = fmaxf(top, a.v_scale[(size_t)x * a.n_kv_heads + it.hk]);
-        }
-        const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
-        if (lane == 0) vexp_w[warp - 8] = (int)(bits >> 23) - 127;
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-        const int E = max(max(vexp_w[0], vexp_w[1]), max(vexp_w[2], vexp_w[3]));
-        if (tid == 0) vexp_s = E;
-        const int e0 = (kPfShift - E) / 2, e1 = kPfShift - E - e0;
-        const float up0 = __uint_as_float((uint32_t)(e0 + 127) << 23);   // 2^(6 - E) as two factors
-        const float up1 = __uint_as_float((uint32_t)(e1 + 127) << 23);
 #pragma unroll 1
         for (int j = 0; j < n_kt; ++j) {
             // (whole warps leave)
             bool ok = (j < 2 || pf_wait(&k_empty[j & 1], (uint32_t)((j - 2) >> 1) & 1u, &abort_s)) &&
                       pf_wait(&c_full[0], (uint32_t)j & 1u, &abort_s);
             if (!__all_sync(0xffffffffu, ok)) break;
-            convert(smem + L::OFF_K + (uint32_t)(j & 1) * L::TILE, smem + L::OFF_CK, j, &c_empty[0], false, 0.f, 0.f);
+            convert(smem + L::OFF_K + (uint32_t)(j & 1) * L::TILE, smem + L::OFF_CK, j, &c_empty[0], false);
             if (lane == 0) mbar_arrive(&k_ready[j & 1]);
             ok = (j < 2 || pf_wait(&v_empty[j & 1], (uint32_t)((j - 2) >> 1) & 1u, &abort_s)) &&
                  pf_wait(&c_full[1], (uint32_t)j & 1u, &abort_s);
             if (!__all_sync(0xffffffffu, ok)) break;
-            convert(smem + L::OFF_V + (uint32_t)(j & 1) * L::TILE, smem + L::OFF_CV, j, &c_empty[1], true, up0, up1);
+            convert(smem + L::OFF_V + (uint32_t)(j & 1) * L::TILE, smem + L::OFF_CV, j, &c_empty[1], near_s[j & (kPfMeta - 1)] != 0);
             if (lane == 0) mbar_arrive(&v_ready[j & 1]);
         }
         __syncwarp();
@@ -682,8 +698,77 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
         const int my_pos = it.pos0 + x * it.tt + tok - first * kPfKeys;   // rows beyond the tokens mask nothing that is kept
         const uint32_t ts = tmem + lane_base + L::TMEM_S + (uint32_t)x * 128u;
         const uint32_t to = tmem + lane_base + L::TMEM_O + (uint32_t)x * 128u;
-        float m_used = -INFINITY;
+        // The bases that the probabilities (m) and the terms, probability times V scale (t), are kept to, as powers of two;
+        // the sum of the probabilities, 2^m times l.
+        float m_used = -INFINITY, t_used = -INFINITY;
         float2 l2 = make_float2(0.f, 0.f);
+        // Moves the bases where the row's largest score and term exceed them by more than 2^8 (not while it has no key).
+        auto move_bases = [&](float mx, float tx, bool scale_o) {
+            const bool move = mx > m_used + 8.f, move_t = tx > t_used + 8.f;
+            if (__any_sync(0xffffffffu, move || move_t)) {
+                const float dn = move_t ? ex2_approx(t_used - tx) : 1.f, dm = move ? ex2_approx(m_used - mx) : 1.f;
+                if (scale_o) {
+                    // S of this tile is complete, so P V of the tile before is in O
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 8) tmem_scale8(to + (uint32_t)c, dn);
+                }
+                l2.x *= dm;
+                l2.y *= dm;
+                if (move) m_used = mx;
+                if (move_t) t_used = tx;
+            }
+        };
+        auto m_base = [&] { return m_used == -INFINITY ? 0.f : m_used; };
+        auto t_base = [&] { return (t_used == -INFINITY ? 0.f : t_used) - kPfShift; };
+        auto hand_over = [&](int half) {                    // what is stored of P, to the tensor core
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_ready[x][half]);
+        };
+        // A key tile whose V scales lie far apart: 16 keys at a time, twice out of TMEM.  In code of its own, reached from
+        // the path of masked tiles: factors of 16 keys each on the path of all tiles took the ragged chunks from 423 us to
+        // 467, a test of its own there to 455.
+        auto far_tile = [&](int slot, uint32_t chunks, int last, bool scale_o) {
+            float e[16];
+            auto load = [&](int c) {                        // scores, -inf where the row sees no key
+                const int lim = (chunks >> c) & 1u ? last - c * 16 : -1;
+                const float f = fmaxf(ks_s[slot][c] * qf, 1.17549435e-38f);
+                tmem_ld16(ts + (uint32_t)c * 16u, e);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) e[i] = i <= lim ? e[i] * f : -INFINITY;
+            };
+            float mx = -INFINITY, tx = -INFINITY;
+#pragma unroll 1
+            for (int c = 0; c < kPfChunks; ++c) {
+                load(c);
+                float mc = e[0];
+#pragma unroll
+                for (int i = 1; i < 16; ++i) mc = fmaxf(mc, e[i]);
+                mx = fmaxf(mx, mc);
+                tx = fmaxf(tx, mc + v_s[slot][c]);
+            }
+            move_bases(mx, tx, scale_o);
+            const float mb = m_base(), tb = t_base();
+#pragma unroll 1
+            for (int c2 = 0; c2 < kPfChunks; c2 += 2) {
+                uint32_t p[16];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    load(c2 + h);
+                    const float nb = v_s[slot][c2 + h] - tb;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        l2.x += ex2_approx(e[2 * i] - mb);
+                        l2.y += ex2_approx(e[2 * i + 1] - mb);
+                        p[8 * h + i] = pack_f16x2(ex2_approx(e[2 * i] + nb), ex2_approx(e[2 * i + 1] + nb));
+                    }
+                }
+                if (c2 == 4) hand_over(0);
+                tmem_st16_issue(ts + (uint32_t)c2 * 8u, p);
+            }
+            hand_over(1);
+        };
         bool ok = true;
 #pragma unroll 1
         for (int j = 0; j < n_x; ++j) {
@@ -693,7 +778,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
             ok = __all_sync(0xffffffffu, ok);               // the TMEM accesses are warp-collective
             if (!ok) break;
             tc_fence_after();
-            const uint32_t chunks = ok_s[slot];
+            const uint2 tile = tile_s[slot];
+            const uint32_t chunks = tile.y;
             const int last = my_pos - j * kPfKeys;          // last key of the tile that this row sees
             float f[kPfChunks];
             {
@@ -716,6 +802,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
                 }
             }
             if (!__all_sync(0xffffffffu, last >= kPfKeys - 1 && chunks == (1u << kPfChunks) - 1u)) {
+                if (chunks & kPfFar) {
+                    far_tile(slot, chunks, last, j > 0);
+                    continue;
+                }
 #pragma unroll
                 for (int c = 0; c < kPfChunks; ++c) {
                     const int lim = (chunks >> c) & 1u ? last - c * 16 : -1;
@@ -740,28 +830,11 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
                 const float mc = fmaxf(m0, m1);
                 mx = fmaxf(mx, mc == -INFINITY ? mc : mc * f[c]);
             }
-            const bool move = mx > m_used + 8.f;            // false while the row has no key
-            if (__any_sync(0xffffffffu, move)) {
-                const float dn = move ? ex2_approx(m_used - mx) : 1.f;
-                if (j > 0) {
-                    // S of this tile is complete, so P V of the tile before is in O
-#pragma unroll 1
-                    for (int c = 0; c < D; c += 8) tmem_scale8(to + (uint32_t)c, dn);
-                }
-                if (move) {
-                    l2.x *= dn;
-                    l2.y *= dn;
-                    m_used = mx;
-                }
-            }
-            const float base = (m_used == -INFINITY ? 0.f : m_used) - kPfBase;
-            const float2 nb = make_float2(-base, -base);
-            auto hand_over = [&](int half) {                // what is stored of P, to the tensor core
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&p_ready[x][half]);
-            };
+            const float lv = __uint_as_float(tile.x);
+            move_bases(mx, mx + lv, j > 0);
+            // A term is 2^(score + nb); terms times to_p are probabilities.
+            const float nb = fmaxf(lv, t_base() - m_base() - kPfFloor) - t_base(), to_p = ex2_approx(-m_base() - nb);
+            const float2 nb2 = make_float2(nb, nb), to_p2 = make_float2(to_p, to_p);
 #pragma unroll
             for (int c2 = 0; c2 < kPfChunks; c2 += 2) {     // 32 keys: 16 columns of P, over S
                 uint32_t p[16];
@@ -771,10 +844,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
                     const float2 ff = make_float2(f[c], f[c]);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        float2 e = fma2(make_float2(s[16 * c + 2 * i], s[16 * c + 2 * i + 1]), ff, nb);
+                        float2 e = fma2(make_float2(s[16 * c + 2 * i], s[16 * c + 2 * i + 1]), ff, nb2);
                         e.x = ex2_approx(e.x);
                         e.y = ex2_approx(e.y);
-                        l2 = add2(l2, e);
+                        l2 = fma2(e, to_p2, l2);
                         p[8 * h + i] = pack_f16x2(e.x, e.y);
                     }
                 }
@@ -788,11 +861,11 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
         ok = __all_sync(0xffffffffu, ok && (n_x == 0 || pf_wait(&o_done[x], 0, &abort_s)));
         if (ok && n_x > 0) {
             tc_fence_after();
-            // vexp_s was written before v_ready of tile 0, which the P V behind o_done waited for
             const float l = l2.x + l2.y;
             const float inv = l == 0.f ? 0.f : 1.f / l;
-            const int E = *const_cast<volatile int*>(&vexp_s) - kPfShift;
-            const float up = E < -126 ? 0.f : __uint_as_float((uint32_t)(E + 127) << 23);
+            // 2^(t - m) as two factors, exact where it is a power of two; a row has a key, so both are finite (or NaN)
+            const float ex = l == 0.f ? 0.f : t_used - kPfShift - m_used, ex0 = rintf(0.5f * ex);
+            const float up0 = exp2f(ex0), up1 = exp2f(ex - ex0);
 #pragma unroll 1
             for (int c = 0; c < D; c += 64) {
                 uint32_t v[64];
@@ -800,7 +873,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
                 tmem_wait_ld(v);
                 if (!live) continue;
 #pragma unroll
-                for (int i = 0; i < 64; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * inv * up);
+                for (int i = 0; i < 64; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * inv * up0 * up1);
                 if (splits == 1) {
 #pragma unroll
                     for (int i = 0; i < 64; i += 8)

@@ -39,6 +39,16 @@ LL_DEVINL float e4m3_scale(float amax) {
     return __uint_as_float((uint32_t)max(e, 127 - 117) << 23);
 }
 
+// log2 of a V scale, exact for powers of two.  A scale of 0 becomes 2^-160: times a code and a probability that is
+// below float32's smallest number.
+constexpr float kLog2ZeroScale = -160.f;
+LL_DEVINL float f8_log2_scale(float s) {
+    if (!(s > 0.f)) return kLog2ZeroScale;
+    const bool tiny = s < 1.17549435e-38f;                 // subnormal
+    const uint32_t u = __float_as_uint(tiny ? s * 16777216.f : s);
+    return (float)((int)(u >> 23) - 127 - (tiny ? 24 : 0)) + log2f(__uint_as_float((u & 0x7fffffu) | 0x3f800000u));
+}
+
 // Four codes requantised from scale f_old to f_new: ratio = f_old / f_new.
 LL_DEVINL uint32_t e4m3x4_rescale(uint32_t w, float ratio) {
     uint32_t lo, hi;
