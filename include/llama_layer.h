@@ -398,7 +398,9 @@ int ll_rope(const void* q, const void* k, int32_t dtype, const int32_t* position
 /* A KV pool of 8-bit floating-point codes (e4m3, largest 448) with one float32
  * scale per block of tokens and KV head.  A cached row reads back as code *
  * scale.  ll_append_to_cache_f8 writes powers of two as scales; the attention
- * takes any finite scales >= 0 (0: the block's rows are zeros). */
+ * takes any finite scales >= 0 (0: the block's rows are zeros).  A cached row counts
+ * in a query's answer down to about 2^-27 of the largest probability times V scale
+ * that the query itself sums; blocks that it does not see take no bits from the rest. */
 typedef struct {
     void* k;              /* e4m3 [num_blocks, n_kv_heads, block_size, head_dim] */
     void* v;              /* same shape */

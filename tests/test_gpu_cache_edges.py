@@ -268,3 +268,17 @@ def test_value_scales_far_from_one(power):
     check(st)
     assert_by_terms(one, q[:2], pool, table, ctx, np.arange(3), 0.125)
     assert_by_terms(out, q, pool, table, ctx, cu, 0.125)
+
+
+@pytest.mark.parametrize("bs,H,Hkv,d", [(16, 4, 2, 64), (128, 4, 2, 128), (32, 24, 2, 128)])
+def test_a_large_value_that_hardly_weighs_in_long_runs_of_keys(bs, H, Hkv, d):
+    """The same for decode where a CTA has several key tiles of a sequence, before and behind the large block."""
+    rng = np.random.default_rng(bs)
+    u = rng.choice([-1.0, 1.0], size=d)
+    B = 20
+    pool, table, ctx = one_large_value(rng, [2300] * B, list(range(B)), Hkv, d, bs, list(rng.integers(0, 2300, size=B)), 2.0 ** 40, u=-4 * u)
+    q = torch.from_numpy(4.0 * u + rng.normal(size=(B, H, d))).bfloat16()
+    st = status()
+    out = api.paged_attention_decode_f8(q.cuda(), to_gpu(pool), dev(table), dev(ctx), 150.0 / (16 * d), status=st)
+    check(st)
+    assert_by_terms(out, q, pool, table, ctx, np.arange(B + 1), 150.0 / (16 * d))

@@ -23,9 +23,10 @@
 // element lies in [2^14, 2^15) before it becomes FP16: BF16 has fewer bits, so only elements below
 // 2^-28 of the row's largest are rounded.  Scores, the running maximum and sums are float32.  A
 // probability enters P V as one FP16 (11 significant bits, relative error 2^-11, an eighth of the BF16
-// output's half step), times its block's V scale relative to the largest exponent E that the warp has
-// met, times 2^6: at most 2^15, and still exact to 2^-31 of the largest term.  When E grows the
-// accumulator is scaled down by the (exact) power of two.
+// output's half step) times its block's V scale, relative to the largest such term t that the warp has met
+// for the query, times 2^6: below 2^15, and still exact to 2^-31 of the largest term.  So a block that hardly
+// weighs takes no bits from the others, however large its V.  The sum of the probabilities has a base of its
+// own (m); terms times one power of two per block are probabilities.
 #include <algorithm>
 
 #include "common.cuh"
@@ -40,7 +41,8 @@ constexpr float kLog2eF8 = 1.4426950408889634f;
 constexpr int kF8Tile = 64;              // keys per tile
 constexpr int kF8Stages = 4;
 constexpr int kF8Threads = 160;
-constexpr int kF8Shift = 6;              // probabilities enter P V times 2^6
+constexpr float kF8Shift = 6.f;          // probabilities times V scales enter P V times 2^6
+constexpr float kF8Floor = 80.f;         // a V scale this far (in powers of two) below the largest term adds nothing
 // Up to 8 query heads per KV head: three CTAs per SM of four stages each (192 KB of codes per SM at D = 128).
 // 7B shapes 201 us, 70B shapes 102; with three stages and four (7B) or three CTAs 201 and 110,
 // with four CTAs throughout 217 and 108, for their 96 registers spill.
@@ -168,9 +170,9 @@ __global__ void __launch_bounds__(kF8Threads, NT == 1 ? kF8MaxCtasPerSm : 2)
     float* s_acc = reinterpret_cast<float*>(sv + STAGES * TILE);   // [4 warps][G][32], for merging at a segment's end
     __shared__ uint64_t full_bar[STAGES], empty_bar[STAGES];
     __shared__ unsigned long long valid_s[STAGES];         // per stage: bit k = key k of the tile is cached
-    __shared__ float2 scale_s[STAGES][4];                  // per stage and 16 keys: K and V scale
+    __shared__ float2 scale_s[STAGES][4];                  // per stage and 16 keys: K scale, log2 of the V scale
     __shared__ float2 s_ml[4][16];                         // per warp and query head: max, sum
-    __shared__ int s_exp[4];                               // per warp: exponent of its accumulator
+    __shared__ float s_t[4][16];                           // and largest term (below)
     __shared__ long long s_sums[kF8Threads / 32];
     __shared__ F8Start s_start;
     __shared__ int abort_s;
@@ -230,7 +232,7 @@ __global__ void __launch_bounds__(kF8Threads, NT == 1 ? kF8MaxCtasPerSm : 2)
             fetch(seg.kt0);
             for (int kb = seg.kt0; kb < seg.kt1 && ok; kb += tpb) {
                 const int blk = blk_n;
-                const float ks = ks_n, vs = vs_n;
+                const float ks = ks_n, lv = f8_log2_scale(vs_n);
                 if (kb + tpb < seg.kt1) fetch(kb + tpb);
                 const int nt = min(tpb, seg.kt1 - kb);
                 for (int t = 0; t < nt; ++t, ++it) {
@@ -252,7 +254,7 @@ __global__ void __launch_bounds__(kF8Threads, NT == 1 ? kF8MaxCtasPerSm : 2)
                     const uint32_t vhi = __reduce_or_sync(0xffffffffu, (uint32_t)(valid >> 32));
                     if (mine)
                         for (int i = 0; i < kt_rows / 16; ++i)
-                            scale_s[st][sb * (kt_rows / 16) + i] = blk >= 0 ? make_float2(ks, vs) : make_float2(0.f, 0.f);
+                            scale_s[st][sb * (kt_rows / 16) + i] = blk >= 0 ? make_float2(ks, lv) : make_float2(0.f, 0.f);
                     if (lane == 0) valid_s[st] = ((unsigned long long)vhi << 32) | vlo;
                     __syncwarp();
                     if (lane == 0)
@@ -326,16 +328,17 @@ __global__ void __launch_bounds__(kF8Threads, NT == 1 ? kF8MaxCtasPerSm : 2)
             }
         }
         // O^T: row r of tile t is head dim (D / 8)(r & 7) + 2 t + (r >> 3), column n of tile nt query head
-        // 8 nt + n; per query column the running max m (the exponent base) and the lane's part of the sum l.
+        // 8 nt + n; per query column the running max m of the scores and t of score + log2 of the V scale (the bases of
+        // the probabilities and of the terms that P V sums), and the lane's part of the sum l of the probabilities.
         float acc[NT][W][4];
-        float m[NT][2], l[NT][2];
-        int E = -1000;                                     // exponent of the accumulator, and 2^(6 - E) as two factors
-        float up0 = 1.f, up1 = 1.f;
+        float m[NT][2], t[NT][2], l[NT][2];
+        // A term is 2^(score + nb), terms times to_p are probabilities, for V scales of 2^lv_at.
+        float nb[NT][2], to_p[NT][2], lv_at = INFINITY;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-            for (int t = 0; t < W; ++t) acc[nt][t][0] = acc[nt][t][1] = acc[nt][t][2] = acc[nt][t][3] = 0.f;
-            m[nt][0] = m[nt][1] = -INFINITY;
+            for (int i = 0; i < W; ++i) acc[nt][i][0] = acc[nt][i][1] = acc[nt][i][2] = acc[nt][i][3] = 0.f;
+            m[nt][0] = m[nt][1] = t[nt][0] = t[nt][1] = -INFINITY;
             l[nt][0] = l[nt][1] = 0.f;
         }
         for (int kt = seg.kt0; kt < seg.kt1 && !dead; ++kt, ++it) {
@@ -401,14 +404,17 @@ __global__ void __launch_bounds__(kF8Threads, NT == 1 ? kF8MaxCtasPerSm : 2)
                             s[nt][2 + e] = v1 ? s[nt][2 + e] : -INFINITY;
                         }
                 }
-                // The exponent base of a column moves only when a score exceeds it by more than 2^8, so that
-                // probabilities stay below 2^8.  So the column's maximum over the lanes is looked for only then.
-                bool grow = false;
+                // The bases of a column move only when a score or a term exceeds its base by more than 2^8, so that
+                // terms stay below 2^8.  So the column's maximum over the lanes is looked for only then.
+                const float lv = kv.y;
+                bool grow = false, anew = lv != lv_at;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) grow = grow || fmaxf(s[nt][e], s[nt][2 + e]) > m[nt][e] + 8.f;
+                    for (int e = 0; e < 2; ++e)
+                        grow = grow || fmaxf(s[nt][e], s[nt][2 + e]) > fminf(m[nt][e], t[nt][e] - lv) + 8.f;
                 if (__any_sync(0xffffffffu, grow)) {
+                    anew = true;
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -416,47 +422,41 @@ __global__ void __launch_bounds__(kF8Threads, NT == 1 ? kF8MaxCtasPerSm : 2)
                             float mx = fmaxf(s[nt][e], s[nt][2 + e]);
 #pragma unroll
                             for (int o = 4; o <= 16; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                            const float mn = mx > m[nt][e] + 8.f ? mx : m[nt][e];
-                            const float al = mn == m[nt][e] ? 1.f : ex2_approx(m[nt][e] - mn);
-                            l[nt][e] *= al;
-#pragma unroll
-                            for (int t = 0; t < W; ++t) {
-                                acc[nt][t][e] *= al;
-                                acc[nt][t][e + 2] *= al;
+                            if (mx > m[nt][e] + 8.f) {
+                                l[nt][e] *= ex2_approx(m[nt][e] - mx);
+                                m[nt][e] = mx;
                             }
-                            m[nt][e] = mn;
+                            const float tn = mx + lv > t[nt][e] + 8.f ? mx + lv : t[nt][e];
+                            const float al = tn == t[nt][e] ? 1.f : ex2_approx(t[nt][e] - tn);
+#pragma unroll
+                            for (int i = 0; i < W; ++i) {
+                                acc[nt][i][e] *= al;
+                                acc[nt][i][e + 2] *= al;
+                            }
+                            t[nt][e] = tn;
                         }
                 }
-                // the block's V scale relative to the accumulator's exponent
-                const uint32_t vbits = __float_as_uint(kv.y);
-                const int ev = (int)(vbits >> 23) - 127;
-                if (kv.y > 0.f && ev > E) {
-                    if (E > -1000) {
-                        const float down = E - ev < -126 ? 0.f : __uint_as_float((uint32_t)(E - ev + 127) << 23);
+                if (anew) {
+                    lv_at = lv;
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
+                    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                            for (int t = 0; t < W; ++t)
-#pragma unroll
-                                for (int j = 0; j < 4; ++j) acc[nt][t][j] *= down;
-                    }
-                    E = ev;
-                    const int h0 = (kF8Shift - E) / 2, h1 = kF8Shift - E - h0;
-                    up0 = __uint_as_float((uint32_t)(h0 + 127) << 23);
-                    up1 = __uint_as_float((uint32_t)(h1 + 127) << 23);
+                        for (int e = 0; e < 2; ++e) {
+                            const float mb = m[nt][e] == -INFINITY ? 0.f : m[nt][e];
+                            const float tb = (t[nt][e] == -INFINITY ? 0.f : t[nt][e]) - kF8Shift;
+                            nb[nt][e] = fmaxf(lv, tb - mb - kF8Floor) - tb;
+                            to_p[nt][e] = ex2_approx(-mb - nb[nt][e]);
+                        }
                 }
-                const float vr = kv.y * up0 * up1;
                 uint32_t pb[NT][2];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    const float b0 = (m[nt][0] == -INFINITY) ? 0.f : m[nt][0];
-                    const float b1 = (m[nt][1] == -INFINITY) ? 0.f : m[nt][1];
-                    const float p00 = ex2_approx(s[nt][0] - b0), p01 = ex2_approx(s[nt][1] - b1);
-                    const float p10 = ex2_approx(s[nt][2] - b0), p11 = ex2_approx(s[nt][3] - b1);
-                    l[nt][0] += p00 + p10;
-                    l[nt][1] += p01 + p11;
-                    pb[nt][0] = movmatrix_trans(pack_f16x2(p00 * vr, p01 * vr));     // keys 0-7
-                    pb[nt][1] = movmatrix_trans(pack_f16x2(p10 * vr, p11 * vr));     // keys 8-15
+                    const float p00 = ex2_approx(s[nt][0] + nb[nt][0]), p01 = ex2_approx(s[nt][1] + nb[nt][1]);
+                    const float p10 = ex2_approx(s[nt][2] + nb[nt][0]), p11 = ex2_approx(s[nt][3] + nb[nt][1]);
+                    l[nt][0] += (p00 + p10) * to_p[nt][0];
+                    l[nt][1] += (p01 + p11) * to_p[nt][1];
+                    pb[nt][0] = movmatrix_trans(pack_f16x2(p00, p01));     // keys 0-7
+                    pb[nt][1] = movmatrix_trans(pack_f16x2(p10, p11));     // keys 8-15
                 }
                 // O^T += V^T P^T: lane g reads D / 8 consecutive code bytes (dims) of each of its key rows
                 // 2 cq, 2 cq + 1, 2 cq + 8, 2 cq + 9 and byte-interleaves the rows of a key pair: word i gives
@@ -508,12 +508,14 @@ __global__ void __launch_bounds__(kF8Threads, NT == 1 ? kF8MaxCtasPerSm : 2)
 #pragma unroll
                 for (int o = 4; o <= 16; o <<= 1) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], o);
         asm volatile("bar.sync 1, 128;" ::: "memory");         // the last segment's readers of s_ml are done
-        if (lane == 0) s_exp[warp] = E;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
             if (g == 0) {
 #pragma unroll
-                for (int e = 0; e < 2; ++e) s_ml[warp][8 * nt + 2 * cq + e] = make_float2(m[nt][e], l[nt][e]);
+                for (int e = 0; e < 2; ++e) {
+                    s_ml[warp][8 * nt + 2 * cq + e] = make_float2(m[nt][e], l[nt][e]);
+                    s_t[warp][8 * nt + 2 * cq + e] = t[nt][e];
+                }
             }
         const bool whole = seg.kt0 == 0 && seg.kt1 == seg.n_kt;
         // slot 0: the segment holds the share's first tile; 1: it is the share's last one
@@ -525,40 +527,37 @@ __global__ void __launch_bounds__(kF8Threads, NT == 1 ? kF8MaxCtasPerSm : 2)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
+                for (int i = 0; i < 2; ++i)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const int r = 8 * nt + 2 * cq + (j & 1);
-                        if (r < G) s_acc[(warp * G + r) * 32 + 4 * g + 2 * t + (j >> 1)] = acc[nt][2 * rd + t][j];
+                        if (r < G) s_acc[(warp * G + r) * 32 + 4 * g + 2 * i + (j >> 1)] = acc[nt][2 * rd + i][j];
                     }
             asm volatile("bar.sync 1, 128;" ::: "memory");
-            int Em = -1000;
-#pragma unroll
-            for (int w = 0; w < 4; ++w) Em = max(Em, s_exp[w]);
             for (int i = threadIdx.x; i < G * 8; i += NCONS) {
                 const int r = i >> 3, gg = i & 7, col = (D / 8) * gg + 4 * rd;
-                float M = -INFINITY;
+                float M = -INFINITY, T = -INFINITY;
 #pragma unroll
-                for (int w = 0; w < 4; ++w) M = fmaxf(M, s_ml[w][r].x);
-                const float base = (M == -INFINITY) ? 0.f : M;
+                for (int w = 0; w < 4; ++w) {
+                    M = fmaxf(M, s_ml[w][r].x);
+                    T = fmaxf(T, s_t[w][r]);
+                }
+                const float base = (M == -INFINITY) ? 0.f : M, top = (T == -INFINITY) ? 0.f : T;
                 float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
                 float den = 0.f;
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {
                     const float2 ml = s_ml[w][r];
-                    const float e = exp2f(ml.x - base);
-                    const int de = s_exp[w] - Em;
-                    const float f = e * (de < -126 ? 0.f : __uint_as_float((uint32_t)(de + 127) << 23));
+                    const float f = exp2f(s_t[w][r] - top);
                     const float4 x = *reinterpret_cast<const float4*>(&s_acc[(w * G + r) * 32 + 4 * gg]);
                     num.x += f * x.x;
                     num.y += f * x.y;
                     num.z += f * x.z;
                     num.w += f * x.w;
-                    den += e * ml.y;
+                    den += exp2f(ml.x - base) * ml.y;
                 }
-                // no valid key: zeros.  2^(Em - 6) as two factors
-                const int ex = Em > -1000 ? Em - kF8Shift : 0, h0 = ex / 2, h1 = ex - h0;
-                const float u0 = __uint_as_float((uint32_t)(h0 + 127) << 23), u1 = __uint_as_float((uint32_t)(h1 + 127) << 23);
+                // no valid key: zeros.  2^(T - M - 6) as two factors, exact where it is a power of two
+                const float ex = top - kF8Shift - base, ex0 = rintf(0.5f * ex), u0 = exp2f(ex0), u1 = exp2f(ex - ex0);
                 const float inv = den == 0.f ? 0.f : 1.f / den;
                 const float4 o = make_float4(num.x * inv * u0 * u1, num.y * inv * u0 * u1, num.z * inv * u0 * u1, num.w * inv * u0 * u1);
                 if (whole) {
@@ -705,8 +704,8 @@ __global__ void __launch_bounds__(kF8JoinThreads) attn_decode_f8_join_runs_kerne
 
 int f8_ctas_per_sm(int G, int D) {
     const size_t smem = (size_t)2 * kF8Stages * kF8Tile * D + (size_t)4 * G * 32 * 4 + 1024;
-    // an SM has 228 KB, a CTA takes 2 KB more for its static part and the system's
-    return std::min(G <= 8 ? kF8MaxCtasPerSm : 2, (int)((228 * 1024) / (smem + 2048)));
+    // an SM has 228 KB, a CTA takes 2.25 KB more for its static part and the system's
+    return std::min(G <= 8 ? kF8MaxCtasPerSm : 2, (int)((228 * 1024) / (smem + 2304)));
 }
 
 template <int D, int NT>
