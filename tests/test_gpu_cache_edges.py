@@ -251,7 +251,7 @@ def test_a_large_value_that_hardly_weighs_leaves_the_others_their_bits(bs, H, Hk
     assert_by_terms(out, q, pool, table, ctx, cu, scale)
 
 
-@pytest.mark.parametrize("power", [-123, -110, 80])
+@pytest.mark.parametrize("power", [-123, -110, 80, 117])
 def test_value_scales_far_from_one(power):
     """V scales of 2^power and a few powers above, in blocks side by side."""
     rng = np.random.default_rng(power + 200)

@@ -574,7 +574,8 @@ __global__ void __launch_bounds__(kF8Threads, NT == 1 ? kF8MaxCtasPerSm : 2)
 
 // The partials of the CTAs c0 .. c1 that share the n tiles of (sequence b, KV head hk), joined by the log-sum-exp; zeros
 // where n = 0.  A thread has four head dims of a query head, and takes the partials four at a time, so that their
-// loads are in flight together.
+// loads are in flight together.  What it keeps is their mean so far, which stays in float32's range where the sum
+// of large values would not.
 constexpr int kF8JoinThreads = 256;
 LL_DEVINL void f8_join(const AttnF8Args& a, int b, int hk, int n, int c0, int c1, int slot0) {
     const int G = a.n_heads / a.n_kv_heads, D = a.head_dim;
@@ -582,7 +583,7 @@ LL_DEVINL void f8_join(const AttnF8Args& a, int b, int hk, int n, int c0, int c1
     for (int i = threadIdx.x; i < G * D / 4; i += kF8JoinThreads) {
         const int r = i / (D / 4), col = (i - r * (D / 4)) * 4;
         float M = -INFINITY, den = 0.f;
-        float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+        float4 mean = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int c = c0; c <= c1 && n > 0; c += 4) {
             float2 ml[4];
             float4 o[4];
@@ -594,26 +595,31 @@ LL_DEVINL void f8_join(const AttnF8Args& a, int b, int hk, int n, int c0, int c1
             }
             const float mn = fmaxf(M, fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)));
             const float base = mn == -INFINITY ? 0.f : mn, old = exp2f(M - base);
-            num.x *= old;
-            num.y *= old;
-            num.z *= old;
-            num.w *= old;
-            den *= old;
+            float w[4], sum = den * old;
+            const float before = sum;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                w[k] = exp2f(ml[k].x - base) * ml[k].y;
+                sum += w[k];
+            }
+            const float inv = sum == 0.f ? 0.f : __fdividef(1.f, sum), keep = before * inv;   // (2^-22 off: the weights need no more)
+            mean.x *= keep;
+            mean.y *= keep;
+            mean.z *= keep;
+            mean.w *= keep;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 if (c + k > c1) break;
-                const float w = exp2f(ml[k].x - base) * ml[k].y;
-                num.x += w * o[k].x;
-                num.y += w * o[k].y;
-                num.z += w * o[k].z;
-                num.w += w * o[k].w;
-                den += w;
+                const float part = w[k] * inv;
+                mean.x += part * o[k].x;
+                mean.y += part * o[k].y;
+                mean.z += part * o[k].z;
+                mean.w += part * o[k].w;
             }
             M = mn;
+            den = sum;
         }
-        const float inv = den == 0.f ? 0.f : 1.f / den;
-        *reinterpret_cast<uint2*>(out + (size_t)r * D + col) =
-            make_uint2(pack_bf16x2(num.x * inv, num.y * inv), pack_bf16x2(num.z * inv, num.w * inv));
+        *reinterpret_cast<uint2*>(out + (size_t)r * D + col) = make_uint2(pack_bf16x2(mean.x, mean.y), pack_bf16x2(mean.z, mean.w));
     }
 }
 

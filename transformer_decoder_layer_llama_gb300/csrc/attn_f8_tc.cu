@@ -902,7 +902,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) attn_prefill_f8_kernel(const At
 
 // Joins the partials of item blockIdx.x: D / 4 lanes to a query row, as many rows per CTA as its threads allow.  A thread
 // takes the partials four at a time, so that their loads are in flight together (one after the other, and four rows
-// to a thread, 16 tokens behind 32768 of a 70B-shaped layer took 36 us here).
+// to a thread, 16 tokens behind 32768 of a 70B-shaped layer took 36 us here), and keeps their mean so far, which stays in
+// float32's range where the sum of large values would not.
 constexpr int kPfJoinThreads = 256;
 __global__ void __launch_bounds__(kPfJoinThreads) attn_prefill_f8_join_kernel(const AttnF8Args a, int n_mt, int tt, int ns) {
     pdl_wait();
@@ -917,7 +918,7 @@ __global__ void __launch_bounds__(kPfJoinThreads) attn_prefill_f8_join_kernel(co
     if (r / G >= (x ? it.nt_b : it.nt_a)) return;
     const size_t pr = (size_t)blockIdx.x * ns * 2 * kPfRows + row;
     float M = -INFINITY, den = 0.f;
-    float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+    float4 mean = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int k = 0; k < splits; k += 4) {
         float2 ml[4];
         float4 o[4];
@@ -929,26 +930,32 @@ __global__ void __launch_bounds__(kPfJoinThreads) attn_prefill_f8_join_kernel(co
         }
         const float mn = fmaxf(M, fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)));
         const float base = mn == -INFINITY ? 0.f : mn, old = exp2f(M - base);
-        num.x *= old;
-        num.y *= old;
-        num.z *= old;
-        num.w *= old;
-        den *= old;
+        float w[4], sum = den * old;
+        const float before = sum;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            w[i] = exp2f(ml[i].x - base) * ml[i].y;
+            sum += w[i];
+        }
+        const float inv = sum == 0.f ? 0.f : __fdividef(1.f, sum), keep = before * inv;   // (2^-22 off: the weights need no more)
+        mean.x *= keep;
+        mean.y *= keep;
+        mean.z *= keep;
+        mean.w *= keep;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             if (ml[i].y == 0.f) continue;                  // no key there: what was read may be anything
-            const float w = exp2f(ml[i].x - base) * ml[i].y;
-            num.x += w * o[i].x;
-            num.y += w * o[i].y;
-            num.z += w * o[i].z;
-            num.w += w * o[i].w;
-            den += w;
+            const float part = w[i] * inv;
+            mean.x += part * o[i].x;
+            mean.y += part * o[i].y;
+            mean.z += part * o[i].z;
+            mean.w += part * o[i].w;
         }
         M = mn;
+        den = sum;
     }
-    const float inv = den == 0.f ? 0.f : 1.f / den;
     *reinterpret_cast<uint2*>(a.out + (((size_t)it.tok0 + x * tt + r / G) * a.n_heads + (size_t)it.hk * G + r % G) * D + col) =
-        make_uint2(pack_bf16x2(num.x * inv, num.y * inv), pack_bf16x2(num.z * inv, num.w * inv));
+        make_uint2(pack_bf16x2(mean.x, mean.y), pack_bf16x2(mean.z, mean.w));
 }
 
 // Pairs of query tiles that max_new tokens of a sequence can take.
