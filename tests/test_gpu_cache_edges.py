@@ -282,3 +282,70 @@ def test_a_large_value_that_hardly_weighs_in_long_runs_of_keys(bs, H, Hkv, d):
     out = api.paged_attention_decode_f8(q.cuda(), to_gpu(pool), dev(table), dev(ctx), 150.0 / (16 * d), status=st)
     check(st)
     assert_by_terms(out, q, pool, table, ctx, np.arange(B + 1), 150.0 / (16 * d))
+
+
+@pytest.mark.parametrize("bs,H,Hkv,d", [(16, 8, 8, 64), (128, 32, 4, 128), (64, 4, 4, 128), (16, 32, 2, 64)])
+def test_decode_gives_the_same_bits_every_time(bs, H, Hkv, d):
+    """Long runs of key tiles, whose codes follow each other into the same shared memory, 300 times."""
+    rng = np.random.default_rng(bs + H)
+    B = 24
+    nb = B * (8192 // bs)
+    g = torch.Generator("cuda").manual_seed(bs)
+    codes = [torch.randint(0, 256, (nb, Hkv, bs, d), generator=g, device="cuda", dtype=torch.uint8) for _ in range(2)]
+    for c in codes:
+        c[(c & 0x7F) == 0x7F] = 0                      # no NaN
+    pool = api.PoolF8(*(c.view(torch.float8_e4m3fn) for c in codes),
+                      *(torch.exp2(torch.randint(-9, -5, (nb, Hkv), generator=g, device="cuda").float()) for _ in range(2)))
+    table = torch.randperm(nb, generator=g, device="cuda").int().view(B, -1)
+    ctx = dev(rng.integers(1, 8193, size=B))
+    q, st = torch.randn(B, H, d, generator=g, device="cuda").bfloat16(), status()
+    ws = torch.empty(api.attention_decode_f8_workspace_size(B, H, Hkv, d), dtype=torch.uint8, device="cuda")
+    first = api.paged_attention_decode_f8(q, pool, table, ctx, d ** -0.5, workspace=ws, status=st)
+    out, differ = torch.empty_like(first), torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(300):
+        out.fill_(5.0)
+        api.paged_attention_decode_f8(q, pool, table, ctx, d ** -0.5, out=out, workspace=ws, status=st)
+        differ += (out != first).any()
+    check(st)
+    assert int(differ.item()) == 0 and torch.isfinite(first).all()
+
+
+@pytest.mark.parametrize("bs,H,Hkv,d", [(16, 8, 2, 64), (128, 16, 2, 128)])
+def test_values_far_apart_give_the_same_bits_every_time(bs, H, Hkv, d):
+    """Prefill over tiles whose V scales lie far apart, among tiles whose scales are near or alike, 100 times."""
+    rng = np.random.default_rng(bs)
+    before, new = [900, 0, 3000], [150, 300, 2]
+    pool, table, ctx = one_large_value(rng, before, new, Hkv, d, bs, [200, 77, 1500], 2.0 ** 9)
+    cu = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    q, st = torch.from_numpy(rng.normal(size=(int(cu[-1]), H, d))).bfloat16(), status()
+    args = (q.cuda(), dev(cu), to_gpu(pool), dev(table), dev(ctx), d ** -0.5)
+    first = api.paged_attention_prefill_f8(*args, max_new=max(new), status=st)
+    assert_by_terms(first, q, pool, table, ctx, cu, d ** -0.5)
+    differ = torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(100):
+        differ += (api.paged_attention_prefill_f8(*args, max_new=max(new), status=st) != first).any()
+    check(st)
+    assert int(differ.item()) == 0
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_subnormal_queries_of_large_keys(d):
+    """Queries below BF16's normal range whose scores with very large keys are of ordinary size."""
+    rng = np.random.default_rng(d)
+    before, new, H, Hkv, bs = [200, 0], [4, 90], 4, 2, 16
+    ctx = [204, 90]
+    pool, table = make_cache(rng, ctx, Hkv, d, bs)
+    live = pool.k_scale == pool.k_scale
+    pool.k_scale[live] = 2.0 ** 119
+    cu = np.array([0, 4, 94], np.int32)
+    q = torch.from_numpy(rng.integers(-100, 101, size=(94, H, d)) * 2.0 ** -133).bfloat16()
+    scale = float(np.float32(16.0 / d))
+    st = status()
+    out = api.paged_attention_prefill_f8(q.cuda(), dev(cu), to_gpu(pool), dev(table), dev(ctx), scale, max_new=90, status=st)
+    one = api.paged_attention_decode_f8(q[:2].cuda(), to_gpu(pool), dev(table), dev(ctx), scale, status=st)
+    check(st)
+    # the factor of such a row, a power of two times scale * log2 e, is subnormal itself: 20 bits
+    mag = C.attention_f8(f64(q), pool, table, ctx, cu, scale)[2][..., :1]
+    assert 3 < mag.max() < 300
+    assert_by_terms(out, q, pool, table, ctx, cu, scale, extra=2.0 ** -20 * mag)
+    assert_by_terms(one, q[:2], pool, table, ctx, np.arange(3), scale, extra=2.0 ** -20 * mag[:2])

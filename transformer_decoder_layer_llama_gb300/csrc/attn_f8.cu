@@ -310,8 +310,9 @@ __global__ void __launch_bounds__(kF8Threads, NT == 1 ? kF8MaxCtasPerSm : 2)
             }
             m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
             m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-            // exponent of the row's largest element; a row of zeros, or with an infinity or NaN, stays as it is
-            int ex = (int)(m >> 7) - 127;
+            // exponent of the row's largest element; a row of zeros, or with an infinity or NaN, stays as it is.  Below 2^-112
+            // it is scaled as if at 2^-112, so that the factor taken out of it keeps 20 bits.
+            int ex = max((int)(m >> 7) - 127, -112);
             if (m == 0u || m >= 0x7f80u) ex = 14;
             // two powers of two, since their product may leave float32's range
             const int e0 = (14 - ex) / 2, e1 = 14 - ex - e0;
