@@ -421,7 +421,8 @@ typedef struct {
  * a call that writes a block's first token starts the block afresh, a later one
  * keeps s' = max(s, scale of its rows) and, where that is larger, rounds the
  * block's earlier rows again to e4m3(code * s / s').  New codes are e4m3(x / s'),
- * nearest even; infinities saturate, NaN stays NaN.  Bit-exact.  Rows behind the
+ * nearest even; infinities saturate (to 448 s', so to 0 beside zeros alone), NaN
+ * stays NaN.  Bit-exact.  Rows behind the
  * last new token, and blocks that get no token, keep their bytes.
  * Two sequences of a call must not append to the same physical block (fork it
  * with ll_copy_blocks first): its contents would be unspecified.
@@ -441,7 +442,8 @@ size_t ll_attention_decode_f8_workspace_size(int32_t batch, int32_t n_heads, int
 
 /* ll_paged_attention_decode over an e4m3 cache: q BF16 [batch, n_heads, head_dim],
  * one query per sequence over positions 0 .. context_lens[b] - 1, softmax(q k^T *
- * scale) v; zero rows where there is no key (context length 0, or no valid block).
+ * scale) v; zero rows where there is no key (context length 0, or no valid block), or
+ * where every score is -infinity (an infinity in q).
  * Whatever lies in the cache behind a context, NaN too, is not read into the
  * result.  head_dim 64 or 128, n_heads / n_kv_heads <= 16, block_size a power of
  * two in [16, 256], batch <= 65535, max_blocks * block_size <= 2^30, scale finite

@@ -14,10 +14,11 @@
 // ahead.  Each consumer warp owns 16 keys of a tile (they lie in one block, so its scales are scalars):
 // S^T = K Q^T and O^T += V^T P^T by mma.sync with the keys, and the head dims, as the 16 rows of A
 // and up to 8 (or 16) query heads of the KV head as columns, so a single query head wastes 7 of 8
-// columns instead of 15 of 16 rows.  The tensor pipe has the room: per SM 23 cache bytes a clock
+// columns instead of 15 of 16 rows.  The tensor pipe has the room: per SM about 19 cache bytes a clock
 // arrive, and a tile's MMAs take about a quarter of its load time.  7B shapes, 64 sequences of 512 to 4096 keys
-// (1.2 GB): 201 us, 6.0 TB/s (88% of the copy bandwidth); 70B shapes, 16 of 4096 to 32768 (0.6 GB): 102 us,
-// 5.9 TB/s.
+// (1.2 GB): 205 us, 5.9 TB/s (87% of the copy bandwidth); 70B shapes, 16 of 4096 to 32768 (0.6 GB): 102 us,
+// 5.9 TB/s.  The same sequences with head dim 64 take 134 and 71 us (66 and 62%: a tile's fixed work for half
+// its bytes), with 16 query heads per KV head 138 (128) and 96 (64): twice the MMAs and exponentials a tile.
 //
 // Precision.  Codes become FP16 exactly.  A query row is scaled by a power of two so that its largest
 // element lies in [2^14, 2^15) before it becomes FP16: BF16 has fewer bits, so only elements below
@@ -44,8 +45,10 @@ constexpr int kF8Threads = 160;
 constexpr float kF8Shift = 6.f;          // probabilities times V scales enter P V times 2^6
 constexpr float kF8Floor = 80.f;         // a V scale this far (in powers of two) below the largest term adds nothing
 // Up to 8 query heads per KV head: three CTAs per SM of four stages each (192 KB of codes per SM at D = 128).
-// 7B shapes 201 us, 70B shapes 102; with three stages and four (7B) or three CTAs 201 and 110,
-// with four CTAs throughout 217 and 108, for their 96 registers spill.
+// 7B shapes 201 us, 70B shapes 102 when it was chosen; with three stages and four (7B) or three CTAs 201 and 110,
+// with four CTAs throughout 217 and 108, for their 96 registers spill.  Head dim 64, calls one at a time: 145 us
+// (7B heads) and 83 (70B); with two CTAs 188 and 96, with six stages 145 and 82.  Beyond 8 heads two CTAs, for the
+// accumulators of a second column tile: 149 us (16 heads, dim 128) and 106 (64); with three 201, for spills, and 105.
 constexpr int kF8MaxCtasPerSm = 3;
 
 LL_DEVINL int f8_context(const AttnF8Args& a, int b, bool flag) {

@@ -6,7 +6,7 @@
 // brought in and converted once for 256 rows.  One CTA per SM and item, 128 keys at a time up to the
 // item's last position, items with the most keys first.  Where there are at most half as many items as SMs,
 // several CTAs share an item's keys and a second kernel joins their float32 partials by the log-sum-exp:
-// 16 tokens behind 32768 (64 heads over 8) take 41 us so, 382 with one CTA per item.  (A persistent grid with
+// 16 tokens behind 32768 (64 heads over 8) take 48 us so (L2 cold), 382 with one CTA per item.  (A persistent grid with
 // equal shares of all key tiles was slower: its roles need registers for the walk, and a partial is 128 KB.)
 //
 // Roles (512 threads in four groups of four warps, the registers split by setmaxnreg):
@@ -16,18 +16,18 @@
 //    At the end O / l goes out.
 //  * warps 8-11, converters: the codes of a key tile, as they lie in the pool, become FP16 in the
 //    128-byte-swizzled operand tiles, two buffers each for K and V.
-//  * warp 14: brings codes (bulk copies of 16 keys) and scales a tile ahead, and looks at how far V scales differ.  (Loaded straight into the converters'
-//    registers they were what the rest waited for: the little L1 that this much shared memory leaves cannot
-//    keep a tile's loads in flight.)
+//  * warp 14: brings codes (bulk copies of 16 keys) and scales a tile ahead, and looks at how far V scales differ.
+//    (Loaded straight into the converters' registers the codes were what the rest waited for: the little L1 that this
+//    much shared memory leaves cannot keep a tile's loads in flight.)
 //  * warps 12 and 13, one elected lane each: S = Q K^T (both from shared memory) and O += P V (P from TMEM) of
 //    tile A and B.  The two tiles take turns, so that the tensor core works for one while the other's softmax runs.
 //
 // Bound by the chain of one query tile (S out of TMEM, maximum, 128 exponentials per row, P back, P V and the next
 // S: about 3100 clocks a key tile, of which the tensor core works 1024 for each of the two query tiles) together with
 // the conversion, which shares shared memory with it: leaving out any one of them gains 3 to 10%.  Ragged
-// 70B-shaped chunks (589 GFLOP): 423 us, 1.39 PFLOP/s, 75% of the measured BF16 burst; 7B prompt of 2048
+// 70B-shaped chunks (589 GFLOP): 428 us, 1.38 PFLOP/s, 74% of the measured BF16 burst; 7B prompt of 2048
 // tokens (34 GFLOP, 256 items of 2 to 16 key tiles, of which an SM's one or two start with 5 us of fetching and
-// staging): 44.5 us.  The code of all roles shares the instruction cache: waits in half the instructions and loops
+// staging): 45 us.  The code of all roles shares the instruction cache: waits in half the instructions and loops
 // that are not unrolled took the prompt from 49.2 to 44.7 us.  Two threads per row (768 threads, 96 registers
 // for the softmax) took 475 us in place of 434.
 //
@@ -44,7 +44,8 @@
 // Where the scales of a tile of keys differ, but by 2^4 at most, V is code times the scale's ratio to one
 // power of two for the tile (exact for powers of two), and t at most 4 too large; where they differ by more, the
 // tile takes a slower path that gives each 16 keys their own scale.  A term is lost below about 2^-27 of the
-// row's largest.
+// row's largest.  Four chunks of 1000 tokens behind 1000 to 7000 (64 heads over 8), blocks of 16: 445 us with V scales
+// alike, 473 with scales up to 2^2 apart, 942 with scales up to 2^12 apart in every tile.
 #include <algorithm>
 
 #include "common.cuh"
@@ -331,8 +332,8 @@ LL_DEVINL bool pf_item(const AttnF8Args& a, int i, int n_mt, int tt, bool flag, 
     return true;
 }
 
-// Where there are fewer items than SMs, ns CTAs share an item's key tiles, each at least kPfLeast of them, and leave
-// partials for the join kernel.
+// Where there are at most half as many items as SMs, ns CTAs share an item's key tiles, each at least kPfLeast of them,
+// and leave partials for the join kernel.
 constexpr int kPfLeast = 3;
 LL_DEVINL int pf_splits(int ns, int n_kt) { return max(1, min(ns, n_kt / kPfLeast)); }
 

@@ -5,14 +5,7 @@
 
 namespace ll {
 
-// Two e4m3 codes (low byte first) as two FP16, exactly (NaN codes give NaN).
-LL_DEVINL uint32_t e4m3x2_to_f16x2(uint32_t two) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((unsigned short)two));
-    return r;
-}
-
-// Four codes of a word, lowest byte first, as two FP16 pairs.
+// Four codes of a word, lowest byte first, as two FP16 pairs, exactly (NaN codes give NaN).
 LL_DEVINL void e4m3x4_to_f16x4(uint32_t w, uint32_t& lo, uint32_t& hi) {
     asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}\n"
         : "=r"(lo), "=r"(hi)
