@@ -349,3 +349,46 @@ def test_subnormal_queries_of_large_keys(d):
     assert 3 < mag.max() < 300
     assert_by_terms(out, q, pool, table, ctx, cu, scale, extra=2.0 ** -20 * mag)
     assert_by_terms(one, q[:2], pool, table, ctx, np.arange(3), scale, extra=2.0 ** -20 * mag[:2])
+
+
+@pytest.mark.parametrize("B,H,Hkv,d,bs", [(40, 4, 1, 64, 16), (33, 16, 1, 128, 64), (64, 8, 1, 128, 32)])
+def test_few_tokens_of_more_sequences_than_a_warp_has_lanes_behind_prefixes_that_ctas_share(B, H, Hkv, d, bs):
+    rng = np.random.default_rng(B)
+    before, new = rng.integers(0, 1500, B), rng.integers(0, 4, B)
+    new[[2, B - 1]] = 0
+    ctx = before + new
+    pool, table = make_cache(rng, list(ctx), Hkv, d, bs)
+    cu = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    q = torch.from_numpy(rng.normal(size=(int(cu[-1]), H, d))).bfloat16()
+    st = status()
+    out = api.paged_attention_prefill_f8(q.cuda(), dev(cu), to_gpu(pool), dev(table), dev(ctx), d ** -0.5, max_new=3, status=st)
+    check(st)
+    assert_attention(out, *C.attention_f8(f64(q), pool, table, ctx, cu, d ** -0.5), d)
+
+
+def test_rows_before_the_first_sequence_and_tables_with_more_rows_than_sequences():
+    """cu_new may start behind row 0, and the table may hold rows of sequences that are not in the call."""
+    rng = np.random.default_rng(12)
+    H, Hkv, d, bs = 4, 2, 64, 16
+    before, new, ctx = [20, 7], [5, 30], [25, 37]
+    cu = np.array([3, 8, 38], np.int32)
+    T = 45
+    ref, table = make_cache(rng, ctx, Hkv, d, bs)
+    gpu = to_gpu(ref)
+    wide = dev(np.concatenate([table, np.full((2, table.shape[1]), 10 ** 6, np.int32)]))
+    k, v = (bf16(rng.normal(size=(T, Hkv, d))) for _ in range(2))
+    ref.append(k, v, table, ctx, cu)
+    st = status()
+    api.append_to_cache_f8(*(torch.from_numpy(x).bfloat16().cuda() for x in (k, v)), gpu, wide, dev(ctx), cu_new=dev(cu), max_new=30, status=st)
+    check(st)
+    assert_pool(gpu, ref)
+    q = torch.from_numpy(rng.normal(size=(T, H, d))).bfloat16()
+    out = torch.full((T, H, d), 5.0, dtype=torch.bfloat16, device="cuda")
+    api.paged_attention_prefill_f8(q.cuda(), dev(cu), gpu, wide, dev(ctx), 0.125, max_new=30, out=out, status=st)
+    check(st)
+    want = C.attention_f8(f64(q), ref, table, ctx, cu, 0.125)
+    assert_attention(out[3:38], *(w[3:38] for w in want), d)
+    assert (out[:3] == 5).all() and (out[38:] == 5).all()
+    one = api.paged_attention_decode_f8(q[:2].cuda(), gpu, wide, dev(ctx), 0.125, status=st)
+    check(st)
+    assert_attention(one, *C.attention_f8(f64(q[:2]), ref, table, ctx, np.arange(3), 0.125), d)
