@@ -395,6 +395,43 @@ int ll_rope(const void* q, const void* k, int32_t dtype, const int32_t* position
             int64_t k_stride, const void* table, int32_t max_position, void* q_out, void* k_out, int64_t q_out_stride,
             int64_t k_out_stride, int32_t* status, void* stream);
 
+/* Q or K heads of `tokens` tokens: [tokens][n_heads][head_dim], rows of tokens
+ * `stride` elements apart (views of a merged QKV output).  n_heads 0: none. */
+typedef struct {
+    void* data;
+    int64_t stride;
+    int32_t n_heads;
+} ll_head_rows;
+
+/* Norms of the Q and K heads and their rotary positions in one pass: every head row x
+ * of q and k becomes R(p) (x / sqrt(mean(x^2) + eps) * gain), R the rotation of ll_rope
+ * at the token's position (elements from rotary_dim on are normed only), float32
+ * arithmetic, rounded once to `dtype` (squares are summed in float32: heads with
+ * elements beyond 2^58 are not supported).  gains float32 [head_dim], one for all Q heads
+ * and one for all K heads; eps > 0.  Positions, table, layout and limits as ll_rope; an
+ * output may be its input (same pointer and stride), otherwise it must share no byte with
+ * the inputs or the other output.  Rows of bad positions are not written. */
+int ll_norm_rope(const ll_head_rows* q, const ll_head_rows* k, int32_t dtype, const float* q_gain, const float* k_gain,
+                 float eps, const int32_t* positions, int32_t tokens, int32_t head_dim, int32_t rotary_dim, int32_t layout,
+                 const void* table, int32_t max_position, const ll_head_rows* q_out, const ll_head_rows* k_out,
+                 int32_t* status, void* stream);
+
+/* Workspace bytes for ll_norm_rope_backward (0 if head_dim is not supported). */
+size_t ll_norm_rope_backward_workspace_size(int32_t head_dim);
+
+/* The gradient of ll_norm_rope: q and k are its inputs, dq and dk the gradients of its
+ * outputs.  Writes the gradients of the inputs (q_grad, k_grad, of `dtype`; each may be dq or
+ * dk itself, same pointer and stride, and otherwise shares no byte with any other tensor)
+ * and of the gains (float32 [head_dim], sums over all tokens and heads in float32 in a fixed
+ * order: the same bits every time; zeros for no tokens).  A token of a bad position is left
+ * out: its rows are not written and its gain terms not counted.  The workspace needs no initial
+ * contents; calls that may overlap on the GPU need one each. */
+int ll_norm_rope_backward(const ll_head_rows* dq, const ll_head_rows* dk, const ll_head_rows* q, const ll_head_rows* k,
+                          int32_t dtype, const float* q_gain, const float* k_gain, float eps, const int32_t* positions,
+                          int32_t tokens, int32_t head_dim, int32_t rotary_dim, int32_t layout, const void* table,
+                          int32_t max_position, const ll_head_rows* q_grad, const ll_head_rows* k_grad, float* q_gain_grad,
+                          float* k_gain_grad, void* workspace, size_t workspace_bytes, int32_t* status, void* stream);
+
 /* A KV pool of 8-bit floating-point codes (e4m3, largest 448) with one float32
  * scale per block of tokens and KV head.  A cached row reads back as code *
  * scale.  ll_append_to_cache_f8 writes powers of two as scales; the attention

@@ -49,6 +49,7 @@ EXPORTED = [
     "ll_attention_decode_f8_workspace_size", "ll_paged_attention_decode_f8",
     "ll_attention_prefill_f8_workspace_size", "ll_paged_attention_prefill_f8", "ll_copy_blocks",
     "ll_compact_blocks", "ll_workspace_size_f8", "ll_layer_prefill_f8", "ll_layer_decode_step_f8",
+    "ll_norm_rope", "ll_norm_rope_backward_workspace_size", "ll_norm_rope_backward",
 ]
 
 
@@ -82,6 +83,10 @@ class ll_rope_config(ctypes.Structure):
                 ("attention_factor", ctypes.c_float)]
 
 
+class ll_head_rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("stride", ctypes.c_int64), ("n_heads", ctypes.c_int32)]
+
+
 class ll_kv_pool_f8(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
                 ("v_scale", ctypes.c_void_p), ("num_blocks", ctypes.c_int32)]
@@ -110,7 +115,8 @@ def _load():
     poolp = ctypes.POINTER(ll_kv_pool)
     poolf8 = ctypes.POINTER(ll_kv_pool_f8)
     ropep = ctypes.POINTER(ll_rope_config)
-    I64 = ctypes.c_int64
+    I64, F32 = ctypes.c_int64, ctypes.c_float
+    headp = ctypes.POINTER(ll_head_rows)
     sig = {
         "ll_strerror": (ctypes.c_char_p, [ctypes.c_int]),
         "ll_last_error": (ctypes.c_char_p, []),
@@ -150,6 +156,10 @@ def _load():
         "ll_pack_rope": (ctypes.c_int, [cfgp, ropep, P, S, P]),
         "ll_rope": (ctypes.c_int, [P, P, I32, P, I32, I32, I32, I32, I32, I32, I32, I64, I64, P, I32, P, P, I64, I64,
                                    P, P]),
+        "ll_norm_rope": (ctypes.c_int, [headp, headp, I32, P, P, F32, P, I32, I32, I32, I32, P, I32, headp, headp, P, P]),
+        "ll_norm_rope_backward_workspace_size": (S, [I32]),
+        "ll_norm_rope_backward": (ctypes.c_int, [headp, headp, headp, headp, I32, P, P, F32, P, I32, I32, I32, I32, P, I32,
+                                                 headp, headp, P, P, P, S, P, P]),
         "ll_append_to_cache_f8": (ctypes.c_int, [P, P, I64, I64, P, I32, P, I32, I32, I32, I32, I32, poolf8, P, I32,
                                                  P, P]),
         "ll_attention_decode_f8_workspace_size": (S, [I32, I32, I32, I32]),
@@ -672,6 +682,118 @@ def rope(q, k, positions, table, layout="half", backward=False, q_out=None, k_ou
           LL_ROPE_BACKWARD if backward else LL_ROPE_FORWARD, qs, ks, table.data_ptr(), rows[0], qo, ko, qos, kos,
           status.data_ptr())
     return outs[0], outs[1]
+
+
+def _heads(t, name, dtype, shape=None):
+    """ll_head_rows of a [tokens, heads, head_dim] tensor (None: no heads)."""
+    if t is None:
+        return ll_head_rows(None, 0, 0)
+    stride = _rows3(t, name, dtype)
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    return ll_head_rows(t.data_ptr(), stride, t.shape[1])
+
+
+def _norm_args(q, k, q_gain, k_gain, positions, table, layout, name):
+    """Checks what norm_rope and its gradient share; returns (dtype, tokens, head_dim, ll_head_rows of q and k)."""
+    x = q if q is not None else k
+    if x is None:
+        raise ValueError("q and k are both None")
+    if not isinstance(x, torch.Tensor) or x.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("q and k must be bfloat16 or float32 tensors")
+    if layout not in LL_ROPE_LAYOUTS:
+        raise ValueError(f"layout must be one of {sorted(LL_ROPE_LAYOUTS)}, got {layout!r}")
+    if torch.is_grad_enabled() and any(getattr(t, "requires_grad", False) for t in (q, k, q_gain, k_gain)):
+        raise ValueError(f"{name} is not recorded by autograd: use torch.no_grad(), and norm_rope_backward for the gradient")
+    qh, kh = _heads(q, "q", x.dtype), _heads(k, "k", x.dtype)
+    T, _, d = x.shape
+    if k is not None and (k.shape[0] != T or k.shape[2] != d):
+        raise ValueError(f"k must be [{T}, n_kv_heads, {d}], got {tuple(k.shape)}")
+    for t, gain, n in ((q, q_gain, "q_gain"), (k, k_gain, "k_gain")):
+        if t is not None:
+            _need(gain, n, torch.float32, shape=(d,))
+    _need(positions, "positions", torch.int32, shape=(T,))
+    _need(table, "table", torch.float32)
+    rows = table.shape
+    if len(rows) != 3 or rows[2] != 2 or not 2 <= 2 * rows[1] <= d:
+        raise ValueError("table must be [max_position, rotary_dim / 2, 2] with rotary_dim <= head_dim")
+    return x.dtype, T, d, qh, kh
+
+
+def _like(t, out):
+    """`out`, or a new contiguous tensor of t's shape; None for None."""
+    return out if out is not None or t is None else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+
+
+def norm_rope(q, k, q_gain, k_gain, positions, table, eps=1e-5, layout="half", q_out=None, k_out=None, status=None,
+              stream=None):
+    """ll_norm_rope: RMS norm of every head of q [tokens, n_heads, head_dim] and k [tokens, n_kv_heads, head_dim] with
+    the gains (float32 [head_dim]), then the rotary positions of rope(), in one pass.  q and k are BF16 or float32,
+    heads contiguous within a token; either may be None (its gain too).  Pass q_out=q (k_out=k) to work in place.
+    Not recorded by autograd: norm_rope_backward is the gradient.  Returns (q_out, k_out)."""
+    dtype, T, d, qh, kh = _norm_args(q, k, q_gain, k_gain, positions, table, layout, "norm_rope")
+    given = q_out, k_out, status
+    q_out, k_out = _like(q, q_out), _like(k, k_out)
+    qo = _heads(q_out, "q_out", dtype, q.shape) if q is not None else ll_head_rows(None, 0, 0)
+    ko = _heads(k_out, "k_out", dtype, k.shape) if k is not None else ll_head_rows(None, 0, 0)
+    x = q if q is not None else k
+    status = new_status(x.device) if status is None else _status(status)
+    dev = _on(x, k, q_out, k_out, q_gain if q is not None else None, k_gain if k is not None else None, positions, table,
+              status)
+    if stream is not None:
+        _made(stream, dev, *(t if g is None else None for g, t in zip(given, (q_out, k_out, status))))
+    _call("ll_norm_rope", lib.ll_norm_rope, dev, stream, qh, kh, LL_F32 if dtype == torch.float32 else LL_BF16,
+          q_gain.data_ptr() if q is not None else None, k_gain.data_ptr() if k is not None else None, eps,
+          positions.data_ptr(), T, d, 2 * table.shape[1], LL_ROPE_LAYOUTS[layout], table.data_ptr(), table.shape[0], qo, ko,
+          status.data_ptr())
+    return (q_out if q is not None else None), (k_out if k is not None else None)
+
+
+def norm_rope_backward_workspace_size(head_dim: int) -> int:
+    return lib.ll_norm_rope_backward_workspace_size(int(head_dim))
+
+
+def norm_rope_backward(dq, dk, q, k, q_gain, k_gain, positions, table, eps=1e-5, layout="half", q_grad=None, k_grad=None,
+                       q_gain_grad=None, k_gain_grad=None, workspace=None, status=None, stream=None):
+    """ll_norm_rope_backward: the gradients of norm_rope's inputs q, k and gains, from the gradients dq, dk of its
+    outputs.  Pass q_grad=dq (k_grad=dk) to overwrite those.  Returns (q_grad, k_grad, q_gain_grad, k_gain_grad), the
+    gains' in float32; None for a tensor that is None."""
+    dtype, T, d, qh, kh = _norm_args(q, k, q_gain, k_gain, positions, table, layout, "norm_rope_backward")
+    if (dq is None) != (q is None) or (dk is None) != (k is None):
+        raise ValueError("dq and dk go with q and k")
+    given = q_grad, k_grad, q_gain_grad, k_gain_grad, workspace, status
+    none = ll_head_rows(None, 0, 0)
+    x = q if q is not None else k
+    if q is None:
+        q_grad = q_gain_grad = q_gain = None
+        dqh = qo = none
+    else:
+        q_grad, q_gain_grad = _like(q, q_grad), _like(q_gain, q_gain_grad)
+        dqh, qo = _heads(dq, "dq", dtype, q.shape), _heads(q_grad, "q_grad", dtype, q.shape)
+        _need(q_gain_grad, "q_gain_grad", torch.float32, shape=(d,))
+    if k is None:
+        k_grad = k_gain_grad = k_gain = None
+        dkh = ko = none
+    else:
+        k_grad, k_gain_grad = _like(k, k_grad), _like(k_gain, k_gain_grad)
+        dkh, ko = _heads(dk, "dk", dtype, k.shape), _heads(k_grad, "k_grad", dtype, k.shape)
+        _need(k_gain_grad, "k_gain_grad", torch.float32, shape=(d,))
+    if workspace is None:
+        workspace = torch.empty(max(norm_rope_backward_workspace_size(d), 16), dtype=torch.uint8, device=x.device)
+    else:
+        _need(workspace, "workspace", torch.uint8)
+    status = new_status(x.device) if status is None else _status(status)
+    outs = q_grad, k_grad, q_gain_grad, k_gain_grad
+    dev = _on(x, k, dq, dk, *outs, q_gain, k_gain, positions, table, workspace, status)
+    if stream is not None:
+        _made(stream, dev, *(t if g is None else None for g, t in zip(given, (*outs, workspace, status))))
+    _call("ll_norm_rope_backward", lib.ll_norm_rope_backward, dev, stream, dqh, dkh, qh, kh,
+          LL_F32 if dtype == torch.float32 else LL_BF16, q_gain.data_ptr() if q is not None else None,
+          k_gain.data_ptr() if k is not None else None, eps, positions.data_ptr(), T, d, 2 * table.shape[1],
+          LL_ROPE_LAYOUTS[layout], table.data_ptr(), table.shape[0], qo, ko,
+          q_gain_grad.data_ptr() if q is not None else None, k_gain_grad.data_ptr() if k is not None else None,
+          workspace.data_ptr(), workspace.numel(), status.data_ptr())
+    return outs
 
 
 class PoolF8:

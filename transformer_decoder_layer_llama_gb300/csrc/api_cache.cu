@@ -87,6 +87,35 @@ ll::RopeTableArgs rope_table_args(const ll_rope_config* c) {
     return f;
 }
 
+// What ll_norm_rope and its gradient check of their sizes.
+int norm_shape(const ll_head_rows* q, const ll_head_rows* k, int32_t dtype, float eps, int32_t tokens, int32_t head_dim,
+               int32_t rotary_dim, int32_t layout, const void* table, int32_t max_position, const int32_t* status) {
+    if (!q || !k || (dtype != LL_BF16 && dtype != LL_F32)) return LL_ERR_INVALID_ARG;
+    if (layout != LL_ROPE_HALF && layout != LL_ROPE_INTERLEAVED) return LL_ERR_INVALID_ARG;
+    if (!(eps > 0.f) || !std::isfinite(eps) || tokens < 0 || q->n_heads < 0 || k->n_heads < 0 ||
+        q->n_heads + (int64_t)k->n_heads <= 0 || head_dim <= 0 || max_position <= 0 || rotary_dim < 2 || rotary_dim % 2 != 0 ||
+        rotary_dim > head_dim)
+        return LL_ERR_INVALID_ARG;
+    if (head_dim > 1024 || q->n_heads > 4096 || k->n_heads > 4096 || tokens > (1 << 24)) return LL_ERR_UNSUPPORTED;
+    if (!table || !status || !aligned16(table)) return LL_ERR_INVALID_ARG;
+    return LL_OK;
+}
+
+bool gain_ok(const float* g) { return g && (reinterpret_cast<uintptr_t>(g) & 3u) == 0; }
+
+int heads_ok(const ll_head_rows* t, int32_t head_dim, int64_t esz) {
+    if (t->n_heads == 0) return LL_OK;
+    if (!t->data || reinterpret_cast<uintptr_t>(t->data) % esz != 0 || t->stride < (int64_t)t->n_heads * head_dim) return LL_ERR_INVALID_ARG;
+    return t->stride > (1LL << 34) ? LL_ERR_UNSUPPORTED : LL_OK;
+}
+
+bool same_heads(const ll_head_rows* a, const ll_head_rows* b) { return a->data == b->data && a->stride == b->stride; }
+
+bool heads_overlap(const ll_head_rows* a, const ll_head_rows* b, int64_t tokens, int64_t head_dim, int64_t esz) {
+    if (a->n_heads == 0 || b->n_heads == 0) return false;
+    return rows_overlap({a->data, a->stride, a->n_heads * head_dim}, {b->data, b->stride, b->n_heads * head_dim}, tokens, esz);
+}
+
 // The shape limits that every call over an e4m3 cache shares.
 int f8_shape(int32_t batch, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim, int32_t block_size, int32_t max_blocks,
              const ll_kv_pool_f8* pool) {
@@ -205,6 +234,132 @@ int ll_rope(const void* q, const void* k, int32_t dtype, const int32_t* position
     a.copy_tail = rotary_dim < head_dim && ((n_heads > 0 && !q_in) || (n_kv_heads > 0 && !k_in));
     a.status = status;
     return cuda_rc(ll::launch_rope(a, dtype == LL_F32, static_cast<cudaStream_t>(stream)));
+}
+
+int ll_norm_rope(const ll_head_rows* q, const ll_head_rows* k, int32_t dtype, const float* q_gain, const float* k_gain,
+                 float eps, const int32_t* positions, int32_t tokens, int32_t head_dim, int32_t rotary_dim, int32_t layout,
+                 const void* table, int32_t max_position, const ll_head_rows* q_out, const ll_head_rows* k_out,
+                 int32_t* status, void* stream) {
+    ll::clear_last_error();
+    const int rc = norm_shape(q, k, dtype, eps, tokens, head_dim, rotary_dim, layout, table, max_position, status);
+    if (rc != LL_OK) return rc;
+    if (!q_out || !k_out || q_out->n_heads != q->n_heads || k_out->n_heads != k->n_heads) return LL_ERR_INVALID_ARG;
+    if (tokens == 0) return LL_OK;
+    if (!positions || (q->n_heads > 0 && !gain_ok(q_gain)) || (k->n_heads > 0 && !gain_ok(k_gain))) return LL_ERR_INVALID_ARG;
+    const int64_t esz = dtype == LL_F32 ? 4 : 2;
+    const ll_head_rows* in[2] = {q, k};
+    const ll_head_rows* out[2] = {q_out, k_out};
+    for (int i = 0; i < 2; ++i) {
+        int bad = heads_ok(in[i], head_dim, esz);
+        if (bad == LL_OK) bad = heads_ok(out[i], head_dim, esz);
+        if (bad != LL_OK) return bad;
+    }
+    for (int i = 0; i < 2; ++i)
+        for (int j = 0; j < 2; ++j)
+            if ((!(i == j && same_heads(out[i], in[j])) && heads_overlap(out[i], in[j], tokens, head_dim, esz)) ||
+                (i < j && heads_overlap(out[i], out[j], tokens, head_dim, esz)))
+                return LL_ERR_INVALID_ARG;
+    ll::NormRopeArgs a{};
+    a.q = q->data;
+    a.k = k->data;
+    a.q_out = q_out->data;
+    a.k_out = k_out->data;
+    a.q_stride = q->stride;
+    a.k_stride = k->stride;
+    a.q_out_stride = q_out->stride;
+    a.k_out_stride = k_out->stride;
+    a.q_gain = q_gain;
+    a.k_gain = k_gain;
+    a.positions = positions;
+    a.table = static_cast<const float2*>(table);
+    a.tokens = tokens;
+    a.n_heads = q->n_heads;
+    a.n_kv_heads = k->n_heads;
+    a.head_dim = head_dim;
+    a.rotary_dim = rotary_dim;
+    a.max_position = max_position;
+    a.eps = eps;
+    a.interleaved = layout == LL_ROPE_INTERLEAVED;
+    a.status = status;
+    return cuda_rc(ll::launch_norm_rope(a, dtype == LL_F32, static_cast<cudaStream_t>(stream)));
+}
+
+size_t ll_norm_rope_backward_workspace_size(int32_t head_dim) {
+    if (head_dim <= 0 || head_dim > 1024) return 0;
+    return align_up(ll::norm_rope_grad_scratch_bytes(head_dim));
+}
+
+int ll_norm_rope_backward(const ll_head_rows* dq, const ll_head_rows* dk, const ll_head_rows* q, const ll_head_rows* k,
+                          int32_t dtype, const float* q_gain, const float* k_gain, float eps, const int32_t* positions,
+                          int32_t tokens, int32_t head_dim, int32_t rotary_dim, int32_t layout, const void* table,
+                          int32_t max_position, const ll_head_rows* q_grad, const ll_head_rows* k_grad, float* q_gain_grad,
+                          float* k_gain_grad, void* workspace, size_t workspace_bytes, int32_t* status, void* stream) {
+    ll::clear_last_error();
+    const int rc = norm_shape(q, k, dtype, eps, tokens, head_dim, rotary_dim, layout, table, max_position, status);
+    if (rc != LL_OK) return rc;
+    const ll_head_rows* x[2] = {q, k};
+    const ll_head_rows* dy[2] = {dq, dk};
+    const ll_head_rows* dx[2] = {q_grad, k_grad};
+    const float* gain[2] = {q_gain, k_gain};
+    float* dgain[2] = {q_gain_grad, k_gain_grad};
+    const int64_t esz = dtype == LL_F32 ? 4 : 2;
+    for (int i = 0; i < 2; ++i) {
+        if (!dy[i] || !dx[i] || dy[i]->n_heads != x[i]->n_heads || dx[i]->n_heads != x[i]->n_heads) return LL_ERR_INVALID_ARG;
+        if (x[i]->n_heads == 0) continue;
+        if (!gain_ok(gain[i]) || !gain_ok(dgain[i])) return LL_ERR_INVALID_ARG;
+        if (tokens == 0) continue;
+        for (const ll_head_rows* t : {x[i], dy[i], dx[i]}) {
+            const int bad = heads_ok(t, head_dim, esz);
+            if (bad != LL_OK) return bad;
+        }
+    }
+    // the gains' gradients are written last: apart from everything that is read or written
+    const size_t gain_bytes = (size_t)head_dim * 4;
+    if (q->n_heads > 0 && k->n_heads > 0 && overlap(q_gain_grad, gain_bytes, k_gain_grad, gain_bytes)) return LL_ERR_INVALID_ARG;
+    for (int i = 0; i < 2; ++i)
+        for (int j = 0; j < 2; ++j)
+            if (x[i]->n_heads > 0 && x[j]->n_heads > 0 && overlap(dgain[i], gain_bytes, gain[j], gain_bytes)) return LL_ERR_INVALID_ARG;
+    if (tokens > 0) {
+        if (!positions) return LL_ERR_INVALID_ARG;
+        for (int i = 0; i < 2; ++i)
+            for (int j = 0; j < 2; ++j)
+                if (heads_overlap(dx[i], x[j], tokens, head_dim, esz) ||
+                    (!(i == j && same_heads(dx[i], dy[j])) && heads_overlap(dx[i], dy[j], tokens, head_dim, esz)) ||
+                    (i < j && heads_overlap(dx[i], dx[j], tokens, head_dim, esz)))
+                    return LL_ERR_INVALID_ARG;
+    }
+    if (!workspace || workspace_bytes < ll_norm_rope_backward_workspace_size(head_dim) || !aligned16(workspace))
+        return LL_ERR_WORKSPACE;
+    ll::NormRopeGradArgs a{};
+    a.q = q->data;
+    a.k = k->data;
+    a.dq = dq->data;
+    a.dk = dk->data;
+    a.q_grad = q_grad->data;
+    a.k_grad = k_grad->data;
+    a.q_stride = q->stride;
+    a.k_stride = k->stride;
+    a.dq_stride = dq->stride;
+    a.dk_stride = dk->stride;
+    a.q_grad_stride = q_grad->stride;
+    a.k_grad_stride = k_grad->stride;
+    a.q_gain = q_gain;
+    a.k_gain = k_gain;
+    a.q_gain_grad = q_gain_grad;
+    a.k_gain_grad = k_gain_grad;
+    a.positions = positions;
+    a.table = static_cast<const float2*>(table);
+    a.tokens = tokens;
+    a.n_heads = q->n_heads;
+    a.n_kv_heads = k->n_heads;
+    a.head_dim = head_dim;
+    a.rotary_dim = rotary_dim;
+    a.max_position = max_position;
+    a.eps = eps;
+    a.interleaved = layout == LL_ROPE_INTERLEAVED;
+    a.partials = static_cast<float*>(workspace);
+    a.status = status;
+    return cuda_rc(ll::launch_norm_rope_grad(a, dtype == LL_F32, static_cast<cudaStream_t>(stream)));
 }
 
 int ll_append_to_cache_f8(const void* k, const void* v, int64_t k_stride, int64_t v_stride, const int32_t* cu_new,

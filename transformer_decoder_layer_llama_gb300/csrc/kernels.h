@@ -207,6 +207,40 @@ struct RopeTableArgs {
 };
 cudaError_t launch_rope_scaled_table(float2* cs, int max_position, const RopeTableArgs& f, cudaStream_t stream);
 
+// RMS norm of every head with its gain, then rotary positions (norm_rope.cu); strides between tokens in elements.
+struct NormRopeArgs {
+    const void *q, *k;
+    void *q_out, *k_out;
+    long long q_stride, k_stride, q_out_stride, k_out_stride;
+    const float *q_gain, *k_gain;  // [head_dim]
+    const int32_t* positions;
+    const float2* table;           // [max_position][rotary_dim / 2] (cos, sin)
+    int tokens, n_heads, n_kv_heads, head_dim, rotary_dim, max_position;
+    float eps;
+    bool interleaved;
+    int32_t* status;
+};
+cudaError_t launch_norm_rope(const NormRopeArgs& a, bool f32, cudaStream_t stream);
+
+struct NormRopeGradArgs {
+    const void *q, *k;             // the heads that were normed
+    const void *dq, *dk;           // gradients of the rotated heads
+    void *q_grad, *k_grad;
+    long long q_stride, k_stride, dq_stride, dk_stride, q_grad_stride, k_grad_stride;
+    const float *q_gain, *k_gain;
+    float *q_gain_grad, *k_gain_grad;
+    const int32_t* positions;
+    const float2* table;
+    int tokens, n_heads, n_kv_heads, head_dim, rotary_dim, max_position;
+    float eps;
+    bool interleaved;
+    float* partials;               // scratch [CTAs][2][head_dim]
+    int32_t* status;
+};
+constexpr int kNormGradMaxCtas = 2 * 160;
+size_t norm_rope_grad_scratch_bytes(int head_dim);
+cudaError_t launch_norm_rope_grad(const NormRopeGradArgs& a, bool f32, cudaStream_t stream);
+
 // A cache of e4m3 codes [num_blocks][n_kv_heads][block_size][head_dim] with scales
 // [num_blocks][n_kv_heads] (kv_f8.cu writes it, attn_f8.cu and attn_f8_tc.cu read it).
 struct AppendArgs {
