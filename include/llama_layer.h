@@ -533,6 +533,70 @@ int ll_layer_decode_step_f8(const ll_config* cfg, const void* packed, const void
                             const int32_t* block_table, int32_t max_blocks, const int32_t* context_lens, int32_t batch,
                             void* y, void* workspace, size_t workspace_bytes, int32_t* status, void* stream);
 
+/* ---- Attention weights, and evictions by them.  `weights` is float32 [batch,
+ * n_kv_heads, weights_width], the caller's: for each sequence, KV head and cached
+ * position the sum of the softmax probabilities that queries have given it, over the
+ * query heads of the KV head and over all calls since the caller zeroed it.  Calls that
+ * add to the same weights must not overlap on the GPU. */
+
+/* Workspace bytes for ll_paged_attention_decode_weights(_q8) (0 for sizes that these
+ * refuse).  Beside the partials it holds a float32 score for each query head and
+ * position of the table. */
+size_t ll_attention_decode_weights_workspace_size(int32_t batch, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,
+                                                  int32_t max_blocks, int32_t block_size);
+
+/* ll_paged_attention_decode (same output) that also adds each position's attention
+ * weight: weights[b][hk][p] += sum over the query heads h of hk of softmax(q_h k^T *
+ * scale)[p], for p < context_lens[b].  A position without a valid block, and a query
+ * without any score above -infinity, add nothing; positions from weights_width on set
+ * LL_DEV_BAD_POSITION and are not added.  What lies behind a context keeps its value.
+ * The sums are float32 and the same bits every time.  head_dim 64 or 128, n_heads /
+ * n_kv_heads <= 16, block_size a power of two in [16, 256], batch <= 65535, max_blocks *
+ * block_size <= 2^30, num_blocks * n_kv_heads * block_size < 2^31, scale finite and >= 0.
+ * The workspace needs no initial contents; calls that may overlap on the GPU need one each. */
+int ll_paged_attention_decode_weights(const void* q, const ll_kv_pool* pool, const int32_t* block_table, int32_t max_blocks,
+                                      const int32_t* context_lens, int32_t batch, int32_t n_heads, int32_t n_kv_heads,
+                                      int32_t head_dim, int32_t block_size, float scale, float* weights, int32_t weights_width,
+                                      void* out, void* workspace, size_t workspace_bytes, int32_t* status, void* stream);
+
+/* The same over an INT8 pool (output as ll_paged_attention_decode_q8; head_dim 128). */
+int ll_paged_attention_decode_weights_q8(const void* q, const ll_kv_pool_q8* pool, const int32_t* block_table, int32_t max_blocks,
+                                         const int32_t* context_lens, int32_t batch, int32_t n_heads, int32_t n_kv_heads,
+                                         int32_t head_dim, int32_t block_size, float scale, float* weights, int32_t weights_width,
+                                         void* out, void* workspace, size_t workspace_bytes, int32_t* status, void* stream);
+
+/* One tensor of a paged pool, by the bytes of a cached row (K or V rows, codes, scales). */
+typedef struct {
+    void* data;           /* device, [num_blocks][n_kv_heads][block_size][row_bytes], 4-byte aligned (16: faster) */
+    int64_t row_bytes;    /* a multiple of 4, at most 4096 */
+} ll_row_tensor;
+
+/* Evicts cached rows by their weights, in place and for every KV head by itself.  With n =
+ * context_lens[b] and m = min(n, keep[b]) (keep NULL: max_keep for all), each KV head of
+ * sequence b keeps m rows: the last min(recent, m), the first min(sinks, m - those), and of
+ * the rows between the ones of the largest weight (ties: the lowest position; NaN counts
+ * below every number).  The kept rows move, in order, to positions 0 .. m - 1 of the
+ * sequence's blocks in all tensors (a HOST array of 1 .. 8, read before the call returns).
+ * Writes
+ *   kept [batch, n_kv_heads, max_keep]  the position that row j had, -1 from m on (int32)
+ *   new_lens [batch]                    m (int32)
+ *   weights_out                         as weights: its rows [0, m) the kept ones', [m, n) zeros,
+ *                                       the rest as it was; weights itself or memory apart from it
+ * Blocks behind the last one that m rows need are free for the caller to reuse; a block that
+ * a moved row is written to must not be part of another sequence (fork it with ll_copy_blocks first).
+ * Cached keys keep the rotary positions they were written with: go on with positions of the
+ * uncut sequence, not with the cut length.
+ * Sizes that do not fit (n < 0 or beyond the table or weights_width, keep[b] < 0, m >
+ * max_keep) set LL_DEV_BAD_POSITION, a bad block among the n rows of a sequence that loses any sets
+ * LL_DEV_BAD_BLOCK: that sequence's kept are -1, its new_lens n, and nothing else of it is touched.
+ * The same rows every time.  max_keep >= 1, sinks, recent >= 0; block_size a power of two in [16,
+ * 256], batch <= 65535, n_kv_heads <= 32767, max_blocks * block_size <= 2^30, num_blocks *
+ * n_kv_heads * block_size < 2^31. */
+int ll_evict_rows(const ll_row_tensor* tensors, int32_t n_tensors, int32_t num_blocks, int32_t n_kv_heads, int32_t block_size,
+                  const int32_t* block_table, int32_t max_blocks, const int32_t* context_lens, int32_t batch,
+                  const float* weights, int32_t weights_width, const int32_t* keep, int32_t max_keep, int32_t sinks,
+                  int32_t recent, float* weights_out, int32_t* kept, int32_t* new_lens, int32_t* status, void* stream);
+
 /* One tensor of a pool whose first dimension is the physical block: K or V codes,
  * or their scales, of one layer. */
 typedef struct {

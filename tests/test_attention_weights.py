@@ -1,0 +1,108 @@
+"""Attention weights and evictions, without a GPU: the oracle's pins and what the library refuses."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import weight_ops as W
+from transformer_decoder_layer_llama_gb300 import api
+
+FAKE = 1 << 20
+NULL = None
+OK, INVALID, UNSUPPORTED, WORKSPACE = range(4)
+
+
+def test_probabilities():
+    rng = np.random.default_rng(1)
+    q, k = rng.normal(size=(3, 2, 8)), rng.normal(size=(5, 8))
+    p = W.probabilities(q, k, 0.3, 2)
+    assert np.allclose(p.sum(-1), 1) and (p[0, :, 3:] == 0).all() and (p[1, :, 4:] == 0).all() and (p[2] > 0).all()
+    one = np.exp(0.3 * q[0] @ k[:3].T)
+    assert np.allclose(p[0, :, :3], one / one.sum(-1, keepdims=True))
+    assert (W.probabilities(q, k[:0], 0.3, -1).shape == (3, 2, 0))
+    assert (W.probabilities(q, k, 0.3, -4) == 0).all()
+
+
+def test_kept_rows_by_hand():
+    w = np.array([5, 1, 9, 1, 0, 1, 2, 0.5])
+    assert W.keep_rows(w, 8, 0, 0).tolist() == list(range(8))
+    assert W.keep_rows(w, 3, 0, 0).tolist() == [0, 2, 6]
+    assert W.keep_rows(w, 4, 0, 0).tolist() == [0, 1, 2, 6]          # of the ones the first
+    assert W.keep_rows(w, 4, 1, 2).tolist() == [0, 2, 6, 7]
+    assert W.keep_rows(w, 2, 5, 1).tolist() == [0, 7] and W.keep_rows(w, 2, 5, 3).tolist() == [6, 7]
+    assert W.keep_rows(w, 0, 5, 3).tolist() == []
+    assert W.keep_rows(np.array([np.nan, -np.inf, 1, np.nan]), 3, 0, 0).tolist() == [0, 1, 2]
+
+
+def pool(**kw):
+    return api.ll_kv_pool(*{**dict(k=FAKE, v=FAKE, num_blocks=8), **kw}.values())
+
+
+def pool_q8(**kw):
+    return api.ll_kv_pool_q8(*{**dict(k=FAKE, v=FAKE, k_scale=FAKE, v_scale=FAKE, num_blocks=8), **kw}.values())
+
+
+DECODE = dict(q=FAKE, pool=pool(), table=FAKE, max_blocks=8, ctx=FAKE, batch=2, n_heads=4, n_kv_heads=2, head_dim=128, block=16,
+              scale=0.1, weights=FAKE, width=128, out=FAKE, ws=FAKE, ws_bytes=1 << 40, status=FAKE)
+DECODE_BAD = [(dict(q=0), INVALID), (dict(q=FAKE + 8), INVALID), (dict(table=0), INVALID), (dict(ctx=0), INVALID), (dict(batch=0), INVALID),
+              (dict(n_heads=5), UNSUPPORTED), (dict(n_heads=34), UNSUPPORTED), (dict(n_kv_heads=0), INVALID), (dict(head_dim=96), UNSUPPORTED),
+              (dict(block=24), UNSUPPORTED), (dict(block=8), UNSUPPORTED), (dict(block=512), UNSUPPORTED), (dict(scale=-1.0), INVALID),
+              (dict(scale=float("nan")), INVALID), (dict(scale=float("inf")), INVALID), (dict(weights=0), INVALID), (dict(weights=FAKE + 2), INVALID),
+              (dict(width=0), INVALID), (dict(out=0), INVALID), (dict(out=FAKE + 4), INVALID), (dict(ws=0), WORKSPACE), (dict(ws_bytes=1000), WORKSPACE),
+              (dict(ws=FAKE + 8), WORKSPACE), (dict(status=0), INVALID), (dict(batch=65536), UNSUPPORTED), (dict(max_blocks=1 << 27), UNSUPPORTED),
+              (dict(max_blocks=0), INVALID)]
+
+
+@pytest.mark.parametrize("bad,code", DECODE_BAD + [(dict(pool=pool(k=0)), INVALID), (dict(pool=pool(v=FAKE + 8)), INVALID),
+                                                   (dict(pool=pool(num_blocks=0)), INVALID), (dict(pool=pool(num_blocks=1 << 26)), UNSUPPORTED)])
+def test_decode_refusals(bad, code):
+    a = {**DECODE, **bad}
+    assert api.lib.ll_paged_attention_decode_weights(*a.values(), NULL) == code
+
+
+@pytest.mark.parametrize("bad,code", DECODE_BAD + [(dict(pool=pool_q8(k_scale=0)), INVALID), (dict(pool=pool_q8(v_scale=FAKE + 4)), INVALID),
+                                                   (dict(head_dim=64), UNSUPPORTED)])
+def test_decode_q8_refusals(bad, code):
+    a = {**DECODE, "pool": pool_q8(), **bad}
+    assert api.lib.ll_paged_attention_decode_weights_q8(*a.values(), NULL) == code
+
+
+def test_decode_workspace():
+    n = api.attention_decode_weights_workspace_size(2, 4, 2, 128, 8, 16)
+    assert n >= api.attention_workspace_size(2, 4, 128, 8, 16) + 2 * 4 * 8 * 16 * 4
+    assert api.attention_decode_weights_workspace_size(2, 4, 2, 96, 8, 16) == 0
+    assert api.attention_decode_weights_workspace_size(0, 4, 2, 128, 8, 16) == 0
+
+
+def rows(*pairs):
+    return (api.ll_row_tensor * max(len(pairs), 1))(*pairs)
+
+
+EVICT = dict(tensors=rows((FAKE, 256), (FAKE, 256)), n=2, num_blocks=8, n_kv_heads=2, block=16, table=FAKE, max_blocks=8, ctx=FAKE,
+             batch=2, weights=2 * FAKE, width=128, keep=0, max_keep=64, sinks=1, recent=2, weights_out=2 * FAKE, kept=3 * FAKE,
+             new_lens=4 * FAKE, status=FAKE)
+
+
+@pytest.mark.parametrize("bad,code", [
+    (dict(tensors=None), INVALID), (dict(n=0), INVALID), (dict(n=9), UNSUPPORTED), (dict(num_blocks=0), INVALID), (dict(n_kv_heads=0), INVALID),
+    (dict(block=24), UNSUPPORTED), (dict(table=0), INVALID), (dict(max_blocks=0), INVALID), (dict(ctx=0), INVALID), (dict(batch=0), INVALID),
+    (dict(batch=65536), UNSUPPORTED), (dict(weights=0), INVALID), (dict(weights=2 * FAKE + 1), INVALID), (dict(width=0), INVALID),
+    (dict(max_keep=0), INVALID), (dict(sinks=-1), INVALID), (dict(recent=-1), INVALID), (dict(weights_out=0), INVALID),
+    (dict(weights_out=2 * FAKE + 128), INVALID), (dict(kept=0), INVALID), (dict(kept=2 * FAKE + 256), INVALID), (dict(new_lens=0), INVALID),
+    (dict(new_lens=FAKE + 4), INVALID), (dict(new_lens=3 * FAKE + 16), INVALID), (dict(keep=4 * FAKE), INVALID), (dict(status=0), INVALID),
+    (dict(tensors=rows((FAKE, 256), (FAKE, 6))), INVALID), (dict(tensors=rows((FAKE, 256), (FAKE, 0))), INVALID),
+    (dict(tensors=rows((FAKE, 256), (0, 256))), INVALID), (dict(tensors=rows((FAKE, 256), (FAKE + 2, 256))), INVALID),
+    (dict(tensors=rows((FAKE, 256), (FAKE, 4100))), UNSUPPORTED), (dict(num_blocks=1 << 26), UNSUPPORTED), (dict(max_blocks=1 << 27), UNSUPPORTED),
+    (dict(n_kv_heads=40000), UNSUPPORTED)])
+def test_evict_refusals(bad, code):
+    assert api.lib.ll_evict_rows(*{**EVICT, **bad}.values(), NULL) == code
+
+
+def test_binding_refusals():
+    i = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    k = torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16)
+    with pytest.raises(TypeError, match="pool"):
+        api.evict_rows(k, i(1, 2), i(1), torch.zeros(1, 2, 32), 4)
+    with pytest.raises(ValueError, match="GPU"):
+        api.evict_rows((k, k), i(1, 2), i(1), torch.zeros(1, 2, 32), 4)

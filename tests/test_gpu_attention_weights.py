@@ -1,0 +1,214 @@
+"""Attention weights of cached positions against their float64 definition on a GPU.
+
+Tolerance of a weight.  A score's float32 error: d products and sums on the tensor core, which may cut instead of round,
+2^-23 each of sum |q k| scale (d + 8 of them; INT8: the code is exact, the scale's product 2^-24 more, inside that), and
+2^-22 of the score for the factors; exponentiated it is relative to the weight.  The exponentials 2^-21 each, the sum of
+n probabilities in float32 (n / 16 + 160) 2^-23 relative, the logarithm of the sum 2^-22 of itself and of the largest
+score (their difference from the score is rounded at that size).  The sum over the heads and rows adds
+(heads * rows / 8 + 16) 2^-23 relative, and the sum so far one rounding.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import llama_layer as O
+from oracle import weight_ops as W
+from tests.helpers import f64
+from transformer_decoder_layer_llama_gb300 import synth
+
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    from transformer_decoder_layer_llama_gb300 import api
+
+LOG2E = 1.4426950408889634
+
+
+def i32(x):
+    return torch.as_tensor(np.asarray(x), dtype=torch.int32).cuda()
+
+
+def check_status(st, want=0):
+    torch.cuda.synchronize()
+    assert int(st.item()) == want
+
+
+class Paged:
+    """A paged cache of some sequences: blocks in random order, garbage (NaN in BF16 pools) behind every context."""
+
+    def __init__(self, ctx, kv_heads, dim, block, seed, int8=False, spare=1):
+        g = torch.Generator().manual_seed(seed)
+        need = [-(-n // block) for n in ctx]
+        wide, nb = max(need) + spare, sum(need) + 2
+        perm = torch.randperm(nb, generator=g).tolist()
+        self.table = np.full((len(ctx), wide), -1, np.int64)
+        for b, n in enumerate(need):
+            self.table[b, :n] = [perm.pop() for _ in range(n)]
+        k, v = (torch.randn(nb, kv_heads, block, dim, generator=g).bfloat16() for _ in range(2))
+        k[..., ::max(dim // 4, 1)] *= 4
+        self.ctx, self.block, self.int8 = list(ctx), block, int8
+        if int8:
+            sets = []
+            for x in (k, v):
+                s = x.float().abs().amax(-1) / 127
+                sets += [torch.round(x.float() / s[..., None]).to(torch.int8), s]
+            self.kq, ks, vq, vs = sets
+            self.pool = api.PoolQ8(self.kq.cuda(), vq.cuda(), ks.cuda(), vs.cuda())
+            self.k_rows, self.v_rows = (c.numpy().astype(np.float64) * f64(s)[..., None] for c, s in ((self.kq, ks), (vq, vs)))
+        else:
+            self.k_rows, self.v_rows = f64(k), f64(v)
+            for b, n in enumerate(ctx):                       # NaN behind the contexts, and in blocks of nobody
+                if n % block:
+                    k[self.table[b, n // block], :, n % block:] = math.nan
+                    v[self.table[b, n // block], :, n % block:] = math.nan
+            free = sorted(set(range(nb)) - set(self.table[self.table >= 0].tolist()))
+            k[free], v[free] = math.nan, math.nan
+            self.k, self.v = k.cuda(), v.cuda()
+        self.d_table, self.d_ctx = i32(self.table), i32(ctx)
+
+    def rows(self, which, b, h, hole=()):
+        """float64 rows of sequence b and KV head h, and which positions have a block."""
+        at = np.arange(self.ctx[b])
+        blk = self.table[b, at // self.block]
+        ok = np.array([j not in hole for j in at // self.block], dtype=bool) & (blk >= 0)
+        x = (self.k_rows if which == "k" else self.v_rows)[np.where(ok, blk, 0), h, at % self.block]
+        return x, ok
+
+
+def reference(paged, q, cu, scale, base, holes={}):
+    """(weights float64, their bounds) after the rows q [tokens, heads, d] of every sequence."""
+    w, bound = f64(base), np.abs(f64(base)) * 2.0 ** -24
+    B, Hkv, width = w.shape
+    G = q.shape[1] // Hkv
+    d = q.shape[2]
+    for b, n in enumerate(paged.ctx):
+        rows = q[cu[b]:cu[b + 1]]
+        m = len(rows)
+        if not m or not n:
+            continue
+        for h in range(Hkv):
+            k, ok = paged.rows("k", b, h, holes.get(b, ()))
+            qq = rows[:, h * G:(h + 1) * G]
+            s = np.einsum("igd,md->igm", qq, k) * scale
+            size = np.einsum("igd,md->igm", np.abs(qq), np.abs(k)) * scale
+            seen = (np.arange(n)[None, None] <= (n - m + np.arange(m))[:, None, None]) & ok
+            s = np.where(seen, s, -np.inf)
+            top = s.max(-1, keepdims=True, initial=-np.inf)
+            p = np.exp(s - np.where(np.isfinite(top), top, 0))
+            tot = p.sum(-1, keepdims=True)
+            p = np.divide(p, tot, out=np.zeros_like(p), where=tot > 0)
+            largest = np.where(np.isfinite(top), np.abs(top), 0) + np.log(np.maximum(tot, 1))
+            score = (d + 8) * 2.0 ** -23 * size + 2.0 ** -22 * (np.where(seen, np.abs(s), 0) + 2 * largest)
+            # a score's error moves its own weight, and the row's normaliser by at most the largest error among its weights
+            own = score + (p * score).sum(-1, keepdims=True)
+            rel = own + 2 * 2.0 ** -21 + (n / 16 + 160) * 2.0 ** -23 + (m * G / 8 + 16) * 2.0 ** -23
+            end = min(n, width)
+            w[b, h, :end] += p.sum((0, 1))[:end]
+            bound[b, h, :end] += (p * rel).sum((0, 1))[:end] + p.sum((0, 1))[:end] * 2.0 ** -24
+    return w, bound * 1.01 + 2.0 ** -120
+
+
+def assert_weights(got, ref, bound):
+    err = np.abs(f64(got) - ref)
+    assert np.isfinite(f64(got)).all()
+    assert (err <= bound + 2.0 ** -24 * np.abs(ref)).all(), float((err / bound).max())
+
+
+DECODE = [  # contexts, heads, kv_heads, dim, block
+    ([1], 1, 1, 64, 16), ([5, 64, 65], 4, 2, 64, 16), ([1, 0, 200], 8, 8, 128, 32), ([1024, 1025, 3, 2047], 6, 2, 128, 64),
+    ([300, 77], 16, 1, 128, 128), ([129], 9, 1, 64, 256), ([4099, 31], 5, 1, 128, 256), ([2500] * 3, 14, 2, 64, 32),
+    ([9000, 100, 8193], 8, 1, 128, 128)]
+
+
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("case", DECODE)
+def test_decode(case, int8):
+    ctx, H, Hkv, d, block = case
+    if int8 and d != 128:
+        d = 128
+    c = Paged(ctx, Hkv, d, block, 7 * len(ctx) + H, int8)
+    g = torch.Generator().manual_seed(H)
+    q = torch.randn(len(ctx), H, d, generator=g).bfloat16().cuda()
+    width = c.table.shape[1] * block + 3
+    base = torch.rand(len(ctx), Hkv, width, generator=g).cuda()
+    w, st, scale = base.clone(), api.new_status(), 1 / math.sqrt(d)
+    if int8:
+        out = api.paged_attention_decode_weights_q8(q, c.pool, c.d_table, c.d_ctx, scale, w, status=st)
+        plain = api.paged_attention_decode_q8(q, c.pool, c.d_table, c.d_ctx, scale)
+    else:
+        out = api.paged_attention_decode_weights(q, c.k, c.v, c.d_table, c.d_ctx, scale, w, status=st)
+        plain = api.paged_attention_decode(q, c.k, c.v, c.d_table, c.d_ctx, scale)
+    check_status(st)
+    assert torch.equal(out, plain)                              # the output is that of the call without weights
+    ref, bound = reference(c, f64(q), list(range(len(ctx) + 1)), scale, base)
+    assert_weights(w, ref, bound)
+    for b, n in enumerate(ctx):
+        assert torch.equal(w[b, :, n:], base[b, :, n:])         # behind the context: left
+        added = f64(w[b]).sum(-1) - f64(base[b]).sum(-1)
+        assert np.allclose(added, H // Hkv if n else 0, atol=1e-3)
+    again = base.clone()
+    if not int8:
+        ws = torch.full((api.attention_decode_weights_workspace_size(len(ctx), H, Hkv, d, c.table.shape[1], block),), 255,
+                        dtype=torch.uint8, device="cuda")
+        api.paged_attention_decode_weights(q, c.k, c.v, c.d_table, c.d_ctx, scale, again, out=out, workspace=ws, status=st)
+        check_status(st)
+        assert torch.equal(again, w)                            # the same bits, whatever the workspace held
+
+
+def test_decode_edges():
+    """Bad blocks add nothing, narrow weights are flagged, bad contexts are cut, a scale of 0, an infinite query."""
+    c = Paged([40, 90, 64], 2, 64, 16, 3)
+    q = torch.randn(3, 4, 64, generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
+    table = c.table.copy()
+    table[1, 2] = 10 ** 6
+    table[2, :] = -1
+    base = torch.rand(3, 2, 112, generator=torch.Generator().manual_seed(2)).cuda()
+    w, st = base.clone(), api.new_status()
+    out = api.paged_attention_decode_weights(q, c.k, c.v, i32(table), c.d_ctx, 0.125, w, status=st)
+    check_status(st, api.LL_DEV_BAD_BLOCK)
+    ref, bound = reference(c, f64(q), [0, 1, 2, 3], 0.125, base, {1: (2,), 2: range(9)})
+    assert_weights(w, ref, bound)
+    assert torch.equal(w[1, :, 32:48], base[1, :, 32:48]) and torch.equal(w[2], base[2]) and (out[2] == 0).all()
+    w, st = base[..., :48].contiguous(), api.new_status()
+    api.paged_attention_decode_weights(q, c.k, c.v, c.d_table, c.d_ctx, 0.125, w, status=st)
+    check_status(st, api.LL_DEV_BAD_POSITION)
+    ref, bound = reference(c, f64(q), [0, 1, 2, 3], 0.125, base[..., :48])
+    assert_weights(w, ref, bound)
+    w, st = torch.zeros(3, 2, 112).cuda(), api.new_status()
+    api.paged_attention_decode_weights(q, c.k, c.v, c.d_table, c.d_ctx, 0.0, w, status=st)
+    check_status(st)
+    for b, n in enumerate(c.ctx):
+        assert np.allclose(f64(w[b, :, :n]), 2 / n, rtol=1e-5) and (w[b, :, n:] == 0).all()
+    w, st = base.clone(), api.new_status()
+    api.paged_attention_decode_weights(q, c.k, c.v, c.d_table, i32([40, -3, 5000]), 0.125, w, status=st)
+    torch.cuda.synchronize()
+    assert int(st.item()) & api.LL_DEV_BAD_POSITION and torch.equal(w[1], base[1])
+    ref, bound = reference(c, f64(q), [0, 1, 1, 1], 0.125, base)
+    assert (np.abs(f64(w[0]) - ref[0]) <= bound[0] + 2.0 ** -24 * np.abs(ref[0])).all()
+
+
+def test_decode_streams_and_graphs():
+    c = Paged([500, 1300], 2, 128, 64, 5)
+    q = torch.randn(2, 8, 128, generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
+    zero = lambda: torch.zeros(2, 2, c.table.shape[1] * 64, device="cuda")  # noqa: E731
+    want = zero()
+    out = api.paged_attention_decode_weights(q, c.k, c.v, c.d_table, c.d_ctx, 0.1, want)
+    torch.cuda.synchronize()
+    side, w = torch.cuda.Stream(), zero()
+    side.wait_stream(torch.cuda.current_stream())
+    o2 = api.paged_attention_decode_weights(q, c.k, c.v, c.d_table, c.d_ctx, 0.1, w, stream=side)
+    side.synchronize()
+    assert torch.equal(w, want) and torch.equal(o2, out)
+    w, o3, st = zero(), torch.zeros_like(out), api.new_status()
+    ws = torch.empty(api.attention_decode_weights_workspace_size(2, 8, 2, 128, c.table.shape[1], 64), dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        api.paged_attention_decode_weights(q, c.k, c.v, c.d_table, c.d_ctx, 0.1, w, out=o3, workspace=ws, status=st)
+    for step in (1, 2):
+        graph.replay()
+        check_status(st)
+        assert torch.equal(o3, out)
+        assert (f64(w) - step * f64(want) <= 2.0 ** -22 * step * f64(want)).all()

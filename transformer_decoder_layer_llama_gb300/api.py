@@ -50,6 +50,8 @@ EXPORTED = [
     "ll_attention_prefill_f8_workspace_size", "ll_paged_attention_prefill_f8", "ll_copy_blocks",
     "ll_compact_blocks", "ll_workspace_size_f8", "ll_layer_prefill_f8", "ll_layer_decode_step_f8",
     "ll_norm_rope", "ll_norm_rope_backward_workspace_size", "ll_norm_rope_backward",
+    "ll_attention_decode_weights_workspace_size", "ll_paged_attention_decode_weights",
+    "ll_paged_attention_decode_weights_q8", "ll_evict_rows",
 ]
 
 
@@ -85,6 +87,10 @@ class ll_rope_config(ctypes.Structure):
 
 class ll_head_rows(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("stride", ctypes.c_int64), ("n_heads", ctypes.c_int32)]
+
+
+class ll_row_tensor(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("row_bytes", ctypes.c_int64)]
 
 
 class ll_kv_pool_f8(ctypes.Structure):
@@ -160,6 +166,13 @@ def _load():
         "ll_norm_rope_backward_workspace_size": (S, [I32]),
         "ll_norm_rope_backward": (ctypes.c_int, [headp, headp, headp, headp, I32, P, P, F32, P, I32, I32, I32, I32, P, I32,
                                                  headp, headp, P, P, P, S, P, P]),
+        "ll_attention_decode_weights_workspace_size": (S, [I32, I32, I32, I32, I32, I32]),
+        "ll_paged_attention_decode_weights": (ctypes.c_int, [P, poolp, P, I32, P, I32, I32, I32, I32, I32, F32, P, I32, P, P,
+                                                             S, P, P]),
+        "ll_paged_attention_decode_weights_q8": (ctypes.c_int, [P, ctypes.POINTER(ll_kv_pool_q8), P, I32, P, I32, I32, I32,
+                                                                I32, I32, F32, P, I32, P, P, S, P, P]),
+        "ll_evict_rows": (ctypes.c_int, [ctypes.POINTER(ll_row_tensor), I32, I32, I32, I32, P, I32, P, I32, P, I32, P, I32, I32,
+                                         I32, P, P, P, P, P]),
         "ll_append_to_cache_f8": (ctypes.c_int, [P, P, I64, I64, P, I32, P, I32, I32, I32, I32, I32, poolf8, P, I32,
                                                  P, P]),
         "ll_attention_decode_f8_workspace_size": (S, [I32, I32, I32, I32]),
@@ -987,6 +1000,130 @@ def layer_decode_step_f8(cfg, packed, x, pool: PoolF8, block_table, context_lens
           x.data_ptr(), ctypes.byref(pool.c()), block_table.data_ptr(), block_table.shape[1], context_lens.data_ptr(),
           B, y.data_ptr(), workspace.data_ptr(), workspace.numel(), status.data_ptr())
     return y
+
+
+# ---------------------------------------------------------------- attention weights
+
+def _paged_batch(block_table, context_lens):
+    """Checks a batch over a paged cache; returns its size."""
+    _need(context_lens, "context_lens", torch.int32)
+    _need(block_table, "block_table", torch.int32)
+    if context_lens.dim() != 1 or block_table.dim() != 2 or block_table.shape[0] != context_lens.shape[0]:
+        raise ValueError("context_lens must be [batch] and block_table [batch, max_blocks]")
+    return context_lens.shape[0]
+
+
+def _weights(weights, batch, n_kv_heads):
+    _need(weights, "weights", torch.float32)
+    if weights.dim() != 3 or weights.shape[0] != batch or weights.shape[1] != n_kv_heads:
+        raise ValueError(f"weights must be [{batch}, {n_kv_heads}, width], got {tuple(weights.shape)}")
+    return weights.shape[2]
+
+
+def attention_decode_weights_workspace_size(batch, n_heads, n_kv_heads, head_dim, max_blocks, block_size):
+    return lib.ll_attention_decode_weights_workspace_size(int(batch), int(n_heads), int(n_kv_heads), int(head_dim),
+                                                          int(max_blocks), int(block_size))
+
+
+def _decode_weights(name, fn, cpool, pool_tensors, q, block_table, context_lens, scale, weights, out, workspace, status, stream):
+    given = out, workspace, status
+    k = pool_tensors[0]
+    _, Hkv, bs, d = k.shape
+    B = _paged_batch(block_table, context_lens)
+    _need(q, "q", torch.bfloat16)
+    if q.dim() != 3 or q.shape[0] != B or q.shape[2] != d:
+        raise ValueError(f"q must be [{B}, n_heads, {d}], got {tuple(q.shape)}")
+    width = _weights(weights, B, Hkv)
+    Hq, mb = q.shape[1], block_table.shape[1]
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _need(out, "out", torch.bfloat16, shape=tuple(q.shape))
+    if workspace is None:
+        workspace = torch.empty(max(attention_decode_weights_workspace_size(B, Hq, Hkv, d, mb, bs), 16), dtype=torch.uint8,
+                                device=q.device)
+    else:
+        _need(workspace, "workspace", torch.uint8)
+    status = new_status(q.device) if status is None else _status(status)
+    dev = _on(q, *pool_tensors, block_table, context_lens, weights, out, workspace, status)
+    if stream is not None:
+        _made(stream, dev, *(t if g is None else None for g, t in zip(given, (out, workspace, status))))
+    _call(name, fn, dev, stream, q.data_ptr(), cpool, block_table.data_ptr(), mb, context_lens.data_ptr(), B, Hq, Hkv, d, bs,
+          float(scale), weights.data_ptr(), width, out.data_ptr(), workspace.data_ptr(), workspace.numel(), status.data_ptr())
+    return out
+
+
+def paged_attention_decode_weights(q, k_pool, v_pool, block_table, context_lens, scale, weights, out=None, workspace=None,
+                                   status=None, stream=None):
+    """ll_paged_attention_decode_weights: paged_attention_decode that also adds every cached position's attention
+    weight to `weights` (float32 [batch, n_kv_heads, width], in place).  Returns out."""
+    return _decode_weights("ll_paged_attention_decode_weights", lib.ll_paged_attention_decode_weights, _pool(k_pool, v_pool),
+                           (k_pool, v_pool), q, block_table, context_lens, scale, weights, out, workspace, status, stream)
+
+
+def paged_attention_decode_weights_q8(q, pool: PoolQ8, block_table, context_lens, scale, weights, out=None, workspace=None,
+                                      status=None, stream=None):
+    """ll_paged_attention_decode_weights_q8: the same over an INT8 pool.  Returns out."""
+    return _decode_weights("ll_paged_attention_decode_weights_q8", lib.ll_paged_attention_decode_weights_q8, pool.c(),
+                           (pool.k, pool.v, pool.k_scale, pool.v_scale), q, block_table, context_lens, scale, weights, out,
+                           workspace, status, stream)
+
+
+def evict_rows(pool, block_table, context_lens, weights, keep, max_keep=None, sinks=0, recent=0, weights_out=None,
+               kept=None, new_lens=None, status=None, stream=None):
+    """ll_evict_rows: every sequence keeps at most `keep` cached rows for each KV head (the first `sinks`, the last
+    `recent`, and between them those of the largest weights), moved to the front of its blocks in place.
+
+    pool: a (K, V) pair of BF16 pools or a PoolQ8.  keep: a number, or an int32 tensor [batch] with max_keep the
+    largest of them.  weights float32 [batch, n_kv_heads, width] move along, in place or to weights_out.  Returns
+    (kept, new_lens): int32 [batch, n_kv_heads, max_keep], the position that each row had (-1 behind the last), and
+    int32 [batch], the new context lengths."""
+    if isinstance(pool, PoolQ8):
+        tensors = pool.k, pool.v, pool.k_scale, pool.v_scale
+    elif isinstance(pool, (tuple, list)) and len(pool) == 2:
+        _pool(*pool)
+        tensors = tuple(pool)
+    else:
+        raise TypeError("pool must be a (K, V) pair of BF16 pools or a PoolQ8")
+    nb, Hkv, bs = tensors[0].shape[:3]
+    B = _paged_batch(block_table, context_lens)
+    width = _weights(weights, B, Hkv)
+    given = kept, new_lens, status
+    if isinstance(keep, torch.Tensor):
+        _need(keep, "keep", torch.int32, shape=(B,))
+        if max_keep is None:
+            raise ValueError("a keep of each sequence needs max_keep")
+        per = keep
+    else:
+        if max_keep is not None and int(max_keep) != int(keep):
+            raise ValueError("max_keep is keep where that is a number")
+        max_keep, per = int(keep), None
+    max_keep = int(max_keep)
+    if max_keep < 1:
+        raise ValueError("keep (max_keep) must be at least 1")
+    if weights_out is None:
+        weights_out = weights
+    else:
+        _need(weights_out, "weights_out", torch.float32, shape=tuple(weights.shape))
+    if kept is None:
+        kept = torch.empty((B, Hkv, max_keep), dtype=torch.int32, device=weights.device)
+    else:
+        _need(kept, "kept", torch.int32, shape=(B, Hkv, max_keep))
+    if new_lens is None:
+        new_lens = torch.empty((B,), dtype=torch.int32, device=weights.device)
+    else:
+        _need(new_lens, "new_lens", torch.int32, shape=(B,))
+    status = new_status(weights.device) if status is None else _status(status)
+    dev = _on(weights, *tensors, block_table, context_lens, per, weights_out, kept, new_lens, status)
+    if stream is not None:
+        _made(stream, dev, *(t if g is None else None for g, t in zip(given, (kept, new_lens, status))))
+    rows = (ll_row_tensor * len(tensors))(
+        *((t.data_ptr(), t.element_size() * (t.shape[3] if t.dim() == 4 else 1)) for t in tensors))
+    _call("ll_evict_rows", lib.ll_evict_rows, dev, stream, rows, len(tensors), nb, Hkv, bs, block_table.data_ptr(),
+          block_table.shape[1], context_lens.data_ptr(), B, weights.data_ptr(), width,
+          per.data_ptr() if per is not None else None, max_keep, int(sinks), int(recent), weights_out.data_ptr(),
+          kept.data_ptr(), new_lens.data_ptr(), status.data_ptr())
+    return kept, new_lens
 
 
 class BlockSet:

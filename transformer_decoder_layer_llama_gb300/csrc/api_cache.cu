@@ -116,6 +116,54 @@ bool heads_overlap(const ll_head_rows* a, const ll_head_rows* b, int64_t tokens,
     return rows_overlap({a->data, a->stride, a->n_heads * head_dim}, {b->data, b->stride, b->n_heads * head_dim}, tokens, esz);
 }
 
+// The shape limits of the calls around attention weights.
+int paged_shape(int32_t batch, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim, int32_t block_size, int32_t max_blocks) {
+    if (batch <= 0 || n_heads <= 0 || n_kv_heads <= 0 || max_blocks <= 0 || block_size <= 0) return LL_ERR_INVALID_ARG;
+    if (head_dim != 64 && head_dim != 128) return LL_ERR_UNSUPPORTED;
+    if (!ll::block_size_ok(block_size)) return LL_ERR_UNSUPPORTED;
+    if (n_heads % n_kv_heads != 0 || n_heads / n_kv_heads > 16) return LL_ERR_UNSUPPORTED;
+    if (batch > 65535 || n_kv_heads > 32767 || (int64_t)max_blocks * block_size > kMaxPositions) return LL_ERR_UNSUPPORTED;
+    return LL_OK;
+}
+
+int decode_weights_args(ll::AttnDecodeArgs& a, const void* q, int32_t num_blocks, const int32_t* block_table, int32_t max_blocks,
+                        const int32_t* context_lens, int32_t batch, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,
+                        int32_t block_size, float scale, float* weights, int32_t weights_width, void* out, void* workspace,
+                        size_t workspace_bytes, int32_t* status) {
+    if (!q || !block_table || !context_lens || !weights || weights_width <= 0 || !out || !status || !(scale >= 0.f) ||
+        !std::isfinite(scale))
+        return LL_ERR_INVALID_ARG;
+    const int rc = paged_shape(batch, n_heads, n_kv_heads, head_dim, block_size, max_blocks);
+    if (rc != LL_OK) return rc;
+    if (!aligned16(q) || !aligned16(out) || (reinterpret_cast<uintptr_t>(weights) & 3u) != 0) return LL_ERR_INVALID_ARG;
+    // rows of the pool are TMA coordinates
+    if ((int64_t)num_blocks * n_kv_heads * block_size > (1LL << 31) - 1) return LL_ERR_UNSUPPORTED;
+    const size_t need = ll_attention_decode_weights_workspace_size(batch, n_heads, n_kv_heads, head_dim, max_blocks, block_size);
+    if (!workspace || workspace_bytes < need || !aligned16(workspace)) return LL_ERR_WORKSPACE;
+    a.q = static_cast<const __nv_bfloat16*>(q);
+    a.context_lens = context_lens;
+    a.block_table = block_table;
+    a.max_blocks = max_blocks;
+    a.num_blocks = num_blocks;
+    a.block_size = block_size;
+    a.batch = batch;
+    a.n_heads = n_heads;
+    a.n_kv_heads = n_kv_heads;
+    a.head_dim = head_dim;
+    a.scale = scale;
+    a.out = static_cast<__nv_bfloat16*>(out);
+    const size_t rows = (size_t)batch * n_heads * ll::attn_decode_max_splits(max_blocks, block_size);
+    a.part_o = static_cast<float*>(workspace);
+    a.part_ml = a.part_o + rows * head_dim;
+    a.weights = weights;
+    a.weights_width = weights_width;
+    a.scores = reinterpret_cast<float*>(static_cast<char*>(workspace) +
+                                        align_up(ll::attn_decode_scratch_bytes(batch, n_heads, head_dim, max_blocks, block_size)));
+    a.score_stride = (long long)max_blocks * block_size;
+    a.status = status;
+    return LL_OK;
+}
+
 // The shape limits that every call over an e4m3 cache shares.
 int f8_shape(int32_t batch, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim, int32_t block_size, int32_t max_blocks,
              const ll_kv_pool_f8* pool) {
@@ -401,6 +449,47 @@ int ll_append_to_cache_f8(const void* k, const void* v, int64_t k_stride, int64_
     return cuda_rc(ll::launch_append_f8(a, static_cast<cudaStream_t>(stream)));
 }
 
+size_t ll_attention_decode_weights_workspace_size(int32_t batch, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,
+                                                  int32_t max_blocks, int32_t block_size) {
+    if (paged_shape(batch, n_heads, n_kv_heads, head_dim, block_size, max_blocks) != LL_OK) return 0;
+    return align_up(ll::attn_decode_scratch_bytes(batch, n_heads, head_dim, max_blocks, block_size)) +
+           align_up((size_t)batch * n_heads * max_blocks * block_size * sizeof(float));
+}
+
+int ll_paged_attention_decode_weights(const void* q, const ll_kv_pool* pool, const int32_t* block_table, int32_t max_blocks,
+                                      const int32_t* context_lens, int32_t batch, int32_t n_heads, int32_t n_kv_heads,
+                                      int32_t head_dim, int32_t block_size, float scale, float* weights, int32_t weights_width,
+                                      void* out, void* workspace, size_t workspace_bytes, int32_t* status, void* stream) {
+    ll::clear_last_error();
+    if (!pool || !pool->k || !pool->v || pool->num_blocks <= 0 || !aligned16(pool->k) || !aligned16(pool->v)) return LL_ERR_INVALID_ARG;
+    ll::AttnDecodeArgs a{};
+    const int rc = decode_weights_args(a, q, pool->num_blocks, block_table, max_blocks, context_lens, batch, n_heads, n_kv_heads,
+                                       head_dim, block_size, scale, weights, weights_width, out, workspace, workspace_bytes, status);
+    if (rc != LL_OK) return rc;
+    a.k_pool = static_cast<const __nv_bfloat16*>(pool->k);
+    a.v_pool = static_cast<const __nv_bfloat16*>(pool->v);
+    return cuda_rc(ll::launch_attn_decode(a, static_cast<cudaStream_t>(stream)));
+}
+
+int ll_paged_attention_decode_weights_q8(const void* q, const ll_kv_pool_q8* pool, const int32_t* block_table, int32_t max_blocks,
+                                         const int32_t* context_lens, int32_t batch, int32_t n_heads, int32_t n_kv_heads,
+                                         int32_t head_dim, int32_t block_size, float scale, float* weights, int32_t weights_width,
+                                         void* out, void* workspace, size_t workspace_bytes, int32_t* status, void* stream) {
+    ll::clear_last_error();
+    if (!pool || !pool->k || !pool->v || !pool->k_scale || !pool->v_scale || pool->num_blocks <= 0) return LL_ERR_INVALID_ARG;
+    if (!aligned16(pool->k) || !aligned16(pool->v) || !aligned16(pool->k_scale) || !aligned16(pool->v_scale)) return LL_ERR_INVALID_ARG;
+    if (head_dim != 128) return LL_ERR_UNSUPPORTED;
+    ll::AttnDecodeArgs a{};
+    const int rc = decode_weights_args(a, q, pool->num_blocks, block_table, max_blocks, context_lens, batch, n_heads, n_kv_heads,
+                                       head_dim, block_size, scale, weights, weights_width, out, workspace, workspace_bytes, status);
+    if (rc != LL_OK) return rc;
+    a.k_q8 = static_cast<const int8_t*>(pool->k);
+    a.v_q8 = static_cast<const int8_t*>(pool->v);
+    a.k_scale = pool->k_scale;
+    a.v_scale = pool->v_scale;
+    return cuda_rc(ll::launch_attn_decode_q8(a, static_cast<cudaStream_t>(stream)));
+}
+
 size_t ll_attention_decode_f8_workspace_size(int32_t batch, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim) {
     if (batch <= 0 || n_heads <= 0 || n_kv_heads <= 0 || n_heads % n_kv_heads != 0 || n_heads / n_kv_heads > 16 ||
         (head_dim != 64 && head_dim != 128))
@@ -456,6 +545,57 @@ int ll_paged_attention_prefill_f8(const void* q, const int32_t* cu_new, int32_t 
     a.tokens = tokens;
     a.max_new = std::min(max_new, tokens);
     return cuda_rc(ll::launch_attn_prefill_f8(a, workspace, static_cast<cudaStream_t>(stream)));
+}
+
+int ll_evict_rows(const ll_row_tensor* tensors, int32_t n_tensors, int32_t num_blocks, int32_t n_kv_heads, int32_t block_size,
+                  const int32_t* block_table, int32_t max_blocks, const int32_t* context_lens, int32_t batch,
+                  const float* weights, int32_t weights_width, const int32_t* keep, int32_t max_keep, int32_t sinks,
+                  int32_t recent, float* weights_out, int32_t* kept, int32_t* new_lens, int32_t* status, void* stream) {
+    ll::clear_last_error();
+    if (!tensors || n_tensors <= 0 || num_blocks <= 0 || n_kv_heads <= 0 || block_size <= 0 || max_blocks <= 0 || batch <= 0 ||
+        weights_width <= 0 || max_keep <= 0 || sinks < 0 || recent < 0)
+        return LL_ERR_INVALID_ARG;
+    if (!block_table || !context_lens || !weights || !weights_out || !kept || !new_lens || !status) return LL_ERR_INVALID_ARG;
+    for (const void* p : {(const void*)weights, (const void*)weights_out, (const void*)kept, (const void*)new_lens})
+        if ((reinterpret_cast<uintptr_t>(p) & 3u) != 0) return LL_ERR_INVALID_ARG;
+    if (n_tensors > ll::kEvictMaxTensors || !ll::block_size_ok(block_size) || batch > 65535 || n_kv_heads > 32767 ||
+        (int64_t)max_blocks * block_size > kMaxPositions || (int64_t)num_blocks * n_kv_heads * block_size > (1LL << 31) - 1)
+        return LL_ERR_UNSUPPORTED;
+    const size_t rows = (size_t)batch * n_kv_heads, weight_bytes = rows * weights_width * 4, kept_bytes = rows * max_keep * 4;
+    if (weights_out != weights && overlap(weights_out, weight_bytes, weights, weight_bytes)) return LL_ERR_INVALID_ARG;
+    if (overlap(kept, kept_bytes, weights, weight_bytes) || overlap(kept, kept_bytes, weights_out, weight_bytes) ||
+        overlap(new_lens, (size_t)batch * 4, context_lens, (size_t)batch * 4) ||
+        (keep && overlap(new_lens, (size_t)batch * 4, keep, (size_t)batch * 4)) ||
+        overlap(new_lens, (size_t)batch * 4, kept, kept_bytes))
+        return LL_ERR_INVALID_ARG;
+    ll::EvictArgs a{};
+    for (int32_t t = 0; t < n_tensors; ++t) {
+        const ll_row_tensor& x = tensors[t];
+        if (!x.data || x.row_bytes <= 0 || x.row_bytes % 4 != 0 || (reinterpret_cast<uintptr_t>(x.data) & 3u) != 0) return LL_ERR_INVALID_ARG;
+        if (x.row_bytes > 4096) return LL_ERR_UNSUPPORTED;
+        a.data[t] = x.data;
+        a.row_bytes[t] = (int)x.row_bytes;
+        a.wide[t] = x.row_bytes % 16 == 0 && aligned16(x.data);
+    }
+    a.n_tensors = n_tensors;
+    a.num_blocks = num_blocks;
+    a.n_kv_heads = n_kv_heads;
+    a.block_size = block_size;
+    a.max_blocks = max_blocks;
+    a.batch = batch;
+    a.block_table = block_table;
+    a.context_lens = context_lens;
+    a.weights = weights;
+    a.weights_out = weights_out;
+    a.weights_width = weights_width;
+    a.keep = keep;
+    a.max_keep = max_keep;
+    a.sinks = sinks;
+    a.recent = recent;
+    a.kept = kept;
+    a.new_lens = new_lens;
+    a.status = status;
+    return cuda_rc(ll::launch_evict(a, static_cast<cudaStream_t>(stream)));
 }
 
 int ll_copy_blocks(const ll_block_tensor* tensors, int32_t n_tensors, int32_t num_blocks, const int32_t* pairs,

@@ -206,7 +206,9 @@ LL_DEVINL uint32_t tswz(int r, int c) {
 // Warps 0-3 consume: each owns 16 keys of every tile, multiplies the group's
 // query rows (padded to 16) with them on the tensor cores and keeps its own
 // online-softmax state; the four merge in shared memory at the end.
-template <int D>
+// SCORES: every valid key's score (times scale log2 e; -infinity where no valid block backs it) also goes to
+// a.scores, for the attention weights (attn_decode_finish_kernel).
+template <int D, bool SCORES>
 __global__ void __launch_bounds__(160, 2)
     attn_decode_split_kernel(const __grid_constant__ CUtensorMap tmK,
                              const __grid_constant__ CUtensorMap tmV, const AttnDecodeArgs a,
@@ -258,6 +260,7 @@ __global__ void __launch_bounds__(160, 2)
         if (lane == 0) {
             tma_prefetch_desc(&tmK);
             tma_prefetch_desc(&tmV);
+            const uint64_t once = SCORES ? l2_policy_evict_first() : 0;    // K and V are read once; the scores stay in L2
             uint32_t issued = 0, parity = 0;    // per stage: a load was issued; parity of the loads issued
             for (int kt = 0; kt < n_kt; ++kt) {
                 const int st = kt % STAGES;
@@ -280,8 +283,13 @@ __global__ void __launch_bounds__(160, 2)
 #pragma unroll
                     for (int h = 0; h < D / 64; ++h) {
                         const uint32_t off = (uint32_t)(st * TILE + h * (BN * 128) + sb * kt_rows * 128);
-                        tma_load_2d(sk + off, &tmK, h * 64, row, &full_bar[st]);
-                        tma_load_2d(sv + off, &tmV, h * 64, row, &full_bar[st]);
+                        if (SCORES) {
+                            tma_load_2d_hint(sk + off, &tmK, h * 64, row, &full_bar[st], once);
+                            tma_load_2d_hint(sv + off, &tmV, h * 64, row, &full_bar[st], once);
+                        } else {
+                            tma_load_2d(sk + off, &tmK, h * 64, row, &full_bar[st]);
+                            tma_load_2d(sv + off, &tmV, h * 64, row, &full_bar[st]);
+                        }
                     }
                 }
                 issued |= 1u << st;
@@ -373,6 +381,14 @@ __global__ void __launch_bounds__(160, 2)
             s[nt][3] = v1 ? s[nt][3] * sl2 : -INFINITY;
             mx0 = fmaxf(mx0, fmaxf(s[nt][0], s[nt][1]));
             mx1 = fmaxf(mx1, fmaxf(s[nt][2], s[nt][3]));
+            if (SCORES) {
+                const int p = pbase + kk;               // even, like the rows' lengths: a pair is inside or outside
+                if (p < a.score_stride) {
+                    float* to = a.scores + ((size_t)b * a.n_heads + (size_t)hk * G + g) * a.score_stride + p;
+                    if (g < G) *reinterpret_cast<float2*>(to) = make_float2(s[nt][0], s[nt][1]);
+                    if (g + 8 < G) *reinterpret_cast<float2*>(to + 8 * a.score_stride) = make_float2(s[nt][2], s[nt][3]);
+                }
+            }
         }
 #pragma unroll
         for (int o = 1; o <= 2; o <<= 1) {
@@ -505,7 +521,7 @@ LL_DEVINL int q8_merge_col(int r, int col) {
 // 6e-4, the same as exact probabilities.
 // One column tile runs four CTAs per SM (94 registers); two run two (their
 // accumulators take 64 registers).
-template <int NT>
+template <int NT, bool SCORES>
 __global__ void __launch_bounds__(160, NT == 1 ? 4 : 2)
     attn_decode_split_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                                 const AttnDecodeArgs a, int max_splits) {
@@ -558,6 +574,7 @@ __global__ void __launch_bounds__(160, NT == 1 ? 4 : 2)
         if (lane == 0) {
             tma_prefetch_desc(&tmK);
             tma_prefetch_desc(&tmV);
+            const uint64_t once = SCORES ? l2_policy_evict_first() : 0;
             uint32_t issued = 0, parity = 0;    // per stage: a load was issued; parity of the loads issued
             for (int kt = 0; kt < n_kt; ++kt) {
                 const int st = kt % STAGES;
@@ -584,8 +601,13 @@ __global__ void __launch_bounds__(160, NT == 1 ? 4 : 2)
                     }
                     const size_t row = ((size_t)blk * a.n_kv_heads + hk) * a.block_size + (p % a.block_size);
                     const uint32_t off = (uint32_t)(st * TILE + sb * kt_rows * 128);
-                    tma_load_2d(sk + off, &tmK, 0, (int)row, &full_bar[st]);
-                    tma_load_2d(sv + off, &tmV, 0, (int)row, &full_bar[st]);
+                    if (SCORES) {
+                        tma_load_2d_hint(sk + off, &tmK, 0, (int)row, &full_bar[st], once);
+                        tma_load_2d_hint(sv + off, &tmV, 0, (int)row, &full_bar[st], once);
+                    } else {
+                        tma_load_2d(sk + off, &tmK, 0, (int)row, &full_bar[st]);
+                        tma_load_2d(sv + off, &tmV, 0, (int)row, &full_bar[st]);
+                    }
                     bulk_load(ssc + (st * 2 + 0) * BN + sb * kt_rows, a.k_scale + row, (uint32_t)kt_rows * 4u,
                               &full_bar[st]);
                     bulk_load(ssc + (st * 2 + 1) * BN + sb * kt_rows, a.v_scale + row, (uint32_t)kt_rows * 4u,
@@ -706,6 +728,15 @@ __global__ void __launch_bounds__(160, NT == 1 ? 4 : 2)
             s[nt][1] = v0 ? s[nt][1] * f0 : -INFINITY;
             s[nt][2] = v1 ? s[nt][2] * f1 : -INFINITY;
             s[nt][3] = v1 ? s[nt][3] * f1 : -INFINITY;
+            if (SCORES) {
+                const int p = k_begin + kt * BN + warp * 16 + g, r = 8 * nt + 2 * cq;
+                float* to = a.scores + ((size_t)b * a.n_heads + (size_t)hk * G + r) * a.score_stride + p;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    if (r + e < G && p < a.score_stride) to[e * a.score_stride] = s[nt][e];
+                    if (r + e < G && p + 8 < a.score_stride) to[e * a.score_stride + 8] = s[nt][2 + e];
+                }
+            }
             mx[nt][0] = fmaxf(s[nt][0] + lv0, s[nt][2] + lv1);
             mx[nt][1] = fmaxf(s[nt][1] + lv0, s[nt][3] + lv1);
 #pragma unroll
@@ -861,6 +892,117 @@ __global__ void attn_decode_combine_kernel(const AttnDecodeArgs a, int max_split
     }
 }
 
+// The outputs, as attn_decode_combine_kernel (blocks x >= spans: one query head of the group each), and the
+// attention weights of 256 E cached tokens per block x < spans:
+//   weights[b][hk][p] += sum over the group's heads of 2^(score_h[p] - lse_h),  lse_h = M + log2 sum_s 2^(m_s - M) l_s.
+// The scores are float32, 4 bytes a query head and key beside the 4 head_dim bytes of a key and KV head, and mostly
+// still in L2 when they are read here.  One kernel for both, so that a step has no launch more than without weights.
+// A thread has E positions and the scores of AHEAD heads on their way at once, before the normalisers are there.
+constexpr int kFinishThreads = 256;
+
+template <int E, int AHEAD>
+__global__ void __launch_bounds__(kFinishThreads) attn_decode_finish_kernel(const AttnDecodeArgs a, int max_splits, int spans) {
+    __shared__ float s_lse[16];
+    pdl_wait();
+    pdl_trigger();
+    const int hk = blockIdx.y, b = blockIdx.z, G = a.n_heads / a.n_kv_heads, D = a.head_dim;
+    const int ctx = min(max(a.context_lens[b], 0), a.max_blocks * a.block_size);
+    const int ns = min(max_splits, (ctx + kDecodeChunk - 1) / kDecodeChunk);
+    const size_t first = ((size_t)b * a.n_heads + (size_t)hk * G) * max_splits;   // partial rows of the group's first head
+    if ((int)blockIdx.x >= spans) {
+        const int h = blockIdx.x - spans;
+        const size_t base_row = first + (size_t)h * max_splits;
+        float M = -INFINITY;
+        for (int s = 0; s < ns; ++s) M = fmaxf(M, a.part_ml[2 * (base_row + s)]);
+        const float mb = (M == -INFINITY) ? 0.f : M;
+        for (int col = threadIdx.x; col < D; col += blockDim.x) {
+            float num = 0.f, den = 0.f;
+            for (int s = 0; s < ns; ++s) {
+                const float w = exp2f(a.part_ml[2 * (base_row + s)] - mb) * a.part_ml[2 * (base_row + s) + 1];
+                num += w * a.part_o[(base_row + s) * D + col];
+                den += w;
+            }
+            a.out[((size_t)b * a.n_heads + (size_t)hk * G + h) * D + col] = __float2bfloat16_rn(den > 0.f ? num / den : 0.f);
+        }
+        return;
+    }
+    const long long span0 = (long long)blockIdx.x * (E * kFinishThreads);
+    if (span0 >= ctx) return;
+    const int p0 = (int)span0, p1 = min(ctx, p0 + E * kFinishThreads);
+    if (p1 > a.weights_width && threadIdx.x == 0) flag_status(a.status, LL_DEV_BAD_POSITION);
+    const int end = min(p1, a.weights_width);
+    const float* scores = a.scores + ((size_t)b * a.n_heads + (size_t)hk * G) * a.score_stride;
+    float* weights = a.weights + ((size_t)b * a.n_kv_heads + hk) * a.weights_width;
+    float sum[E], next[AHEAD][E];
+    const auto fetch = [&](int h, float (&v)[E]) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const int p = p0 + e * kFinishThreads + threadIdx.x;
+            v[e] = h < G && p < end ? __ldcs(scores + (size_t)h * a.score_stride + p) : -INFINITY;
+        }
+    };
+#pragma unroll
+    for (int e = 0; e < E; ++e) {                                 // the sums so far and the first heads, before the normalisers
+        const int p = p0 + e * kFinishThreads + threadIdx.x;
+        sum[e] = p < end ? weights[p] : 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j) fetch(j, next[j]);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int h = warp; h < G; h += kFinishThreads / 32) {
+        const float* ml = a.part_ml + 2 * (first + (size_t)h * max_splits);
+        float M = -INFINITY, den = 0.f;
+        for (int s = lane; s < ns; s += 32) M = fmaxf(M, ml[2 * s]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        const float mb = (M == -INFINITY) ? 0.f : M;
+        for (int s = lane; s < ns; s += 32) den += exp2f(ml[2 * s] - mb) * ml[2 * s + 1];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+        // no key at all, or scores of -infinity alone: the head adds nothing
+        if (lane == 0) s_lse[h] = den == 0.f ? INFINITY : mb + log2f(den);
+    }
+    __syncthreads();
+    float add[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) add[e] = 0.f;
+    for (int h0 = 0; h0 < G; h0 += AHEAD) {
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) {
+            const float lse = h0 + j < G ? s_lse[h0 + j] : INFINITY;
+#pragma unroll
+            for (int e = 0; e < E; ++e) add[e] += exp2f(next[j][e] - lse);
+            fetch(h0 + AHEAD + j, next[j]);
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        const int p = p0 + e * kFinishThreads + threadIdx.x;
+        if (p < end) weights[p] = sum[e] + add[e];
+    }
+}
+
+// The kernel behind the split kernel: outputs alone, or outputs and weights.
+cudaError_t launch_join(const AttnDecodeArgs& a, int max_splits, cudaStream_t stream) {
+    cudaError_t e;
+    if (a.weights) {
+        trace_before("attn_decode_finish", stream);
+        const int G = a.n_heads / a.n_kv_heads;
+        const auto finish = [&](auto kernel, int positions) {
+            const int spans = (int)((a.score_stride + positions * kFinishThreads - 1) / (positions * kFinishThreads));
+            return launch_pdl(kernel, dim3(spans + G, a.n_kv_heads, a.batch), dim3(kFinishThreads), 0, stream, 1, a, max_splits, spans);
+        };
+        e = G == 1 ? finish(attn_decode_finish_kernel<8, 1>, 8) : G == 2 ? finish(attn_decode_finish_kernel<8, 2>, 8) :
+            G <= 4 ? finish(attn_decode_finish_kernel<4, 4>, 4) : finish(attn_decode_finish_kernel<2, 8>, 2);
+    } else {
+        trace_before("attn_decode_combine", stream);
+        e = launch_pdl(attn_decode_combine_kernel, dim3(a.n_heads, a.batch), dim3(a.head_dim), 0, stream, 1, a, max_splits);
+    }
+    trace_after(stream);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    return record(e, a.weights ? "attn_decode_finish_kernel launch" : "attn_decode_combine_kernel launch");
+}
+
 // The dispatch order table sits in the scratch after the split partials (16-byte entries).
 int4* order_table(const AttnDecodeArgs& a, int max_splits) {
     const size_t rows = (size_t)a.batch * a.n_heads * max_splits;
@@ -901,6 +1043,7 @@ cudaError_t launch_order(AttnDecodeArgs& a, int max_splits, bool int8_cache, cud
 template <int D>
 cudaError_t decode_for(const AttnDecodeArgs& args, cudaStream_t stream) {
     AttnDecodeArgs a = args;
+    const auto kernel = a.weights ? attn_decode_split_kernel<D, true> : attn_decode_split_kernel<D, false>;
     const int max_splits = attn_decode_max_splits(a.max_blocks, a.block_size);
     {
         const cudaError_t eo = launch_order(a, max_splits, false, stream);
@@ -908,7 +1051,7 @@ cudaError_t decode_for(const AttnDecodeArgs& args, cudaStream_t stream) {
     }
     const size_t smem = (size_t)2 * 3 * (64 * D * 2) + 16 * D * 2 + 1024;
     {
-        const cudaError_t e = ensure_func_attr((const void*)attn_decode_split_kernel<D>,
+        const cudaError_t e = ensure_func_attr((const void*)kernel,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem,
                                                "cudaFuncSetAttribute(attn_decode_split_kernel)");
         if (e != cudaSuccess) return e;
@@ -921,23 +1064,19 @@ cudaError_t decode_for(const AttnDecodeArgs& args, cudaStream_t stream) {
         return cudaErrorInvalidValue;
     dim3 grid(max_splits, a.n_kv_heads, a.batch);
     trace_before("attn_decode_split", stream);
-    cudaError_t e = launch_pdl(attn_decode_split_kernel<D>, grid, dim3(160), smem, stream, 1, tmK, tmV, a,
+    cudaError_t e = launch_pdl(kernel, grid, dim3(160), smem, stream, 1, tmK, tmV, a,
                                max_splits);
     trace_after(stream);
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) return record(e, "attn_decode_split_kernel launch");
-    trace_before("attn_decode_combine", stream);
-    e = launch_pdl(attn_decode_combine_kernel, dim3(a.n_heads, a.batch), dim3(D), 0, stream, 1, a,
-                   max_splits);
-    trace_after(stream);
-    if (e != cudaSuccess) return record(e, "attn_decode_combine_kernel launch");
-    return record(cudaGetLastError(), "attn_decode_combine_kernel launch");
+    return launch_join(a, max_splits, stream);
 }
 
 template <int NT>
 cudaError_t decode_q8_for(const AttnDecodeArgs& args, cudaStream_t stream) {
     AttnDecodeArgs a = args;
     constexpr int D = 128, BN = 64, STAGES = 3;
+    const auto kernel = a.weights ? attn_decode_split_q8_kernel<NT, true> : attn_decode_split_q8_kernel<NT, false>;
     const int max_splits = attn_decode_max_splits(a.max_blocks, a.block_size);
     {
         const cudaError_t eo = launch_order(a, max_splits, true, stream);
@@ -945,12 +1084,12 @@ cudaError_t decode_q8_for(const AttnDecodeArgs& args, cudaStream_t stream) {
     }
     const size_t smem = (size_t)STAGES * 2 * BN * D + STAGES * 2 * BN * 4 + 16 * D * 2 + 1024;
     {
-        cudaError_t e = ensure_func_attr((const void*)attn_decode_split_q8_kernel<NT>,
+        cudaError_t e = ensure_func_attr((const void*)kernel,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem,
                                          "cudaFuncSetAttribute(attn_decode_split_q8_kernel)");
         if (e != cudaSuccess) return e;
         // four CTAs of 56 KB per SM need the whole shared-memory carveout
-        e = ensure_func_attr((const void*)attn_decode_split_q8_kernel<NT>,
+        e = ensure_func_attr((const void*)kernel,
                              cudaFuncAttributePreferredSharedMemoryCarveout, (int)cudaSharedmemCarveoutMaxShared,
                              "cudaFuncSetAttribute(attn_decode_split_q8_kernel carveout)");
         if (e != cudaSuccess) return e;
@@ -962,16 +1101,12 @@ cudaError_t decode_q8_for(const AttnDecodeArgs& args, cudaStream_t stream) {
         return cudaErrorInvalidValue;
     dim3 grid(max_splits, a.n_kv_heads, a.batch);
     trace_before("attn_decode_split", stream);
-    cudaError_t e = launch_pdl(attn_decode_split_q8_kernel<NT>, grid, dim3(160), smem, stream, 1, tmK, tmV, a,
+    cudaError_t e = launch_pdl(kernel, grid, dim3(160), smem, stream, 1, tmK, tmV, a,
                                max_splits);
     trace_after(stream);
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) return record(e, "attn_decode_split_q8_kernel launch");
-    trace_before("attn_decode_combine", stream);
-    e = launch_pdl(attn_decode_combine_kernel, dim3(a.n_heads, a.batch), dim3(D), 0, stream, 1, a, max_splits);
-    trace_after(stream);
-    if (e != cudaSuccess) return record(e, "attn_decode_combine_kernel launch");
-    return record(cudaGetLastError(), "attn_decode_combine_kernel launch");
+    return launch_join(a, max_splits, stream);
 }
 
 }  // namespace

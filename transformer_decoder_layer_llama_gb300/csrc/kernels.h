@@ -177,6 +177,10 @@ struct AttnDecodeArgs {
     const float* k_scale;          // ... and their scales [num_blocks, n_kv_heads, block_size]
     const float* v_scale;
     int4* order;                   // dispatch order of the split grid, in the scratch (set by the launcher)
+    float* weights;                // attention weights to add to, [batch][n_kv_heads][weights_width], or null
+    int weights_width;
+    float* scores;                 // with weights: scratch [batch][n_heads][score_stride]
+    long long score_stride;        // max_blocks * block_size
 };
 int attn_decode_max_splits(int max_blocks, int block_size);
 size_t attn_decode_scratch_bytes(int batch, int n_heads, int head_dim, int max_blocks,
@@ -282,6 +286,27 @@ cudaError_t launch_attn_decode_f8(AttnF8Args a, void* workspace, cudaStream_t st
 size_t attn_prefill_f8_scratch_bytes(int head_dim);
 cudaError_t launch_attn_prefill_f8(AttnF8Args a, void* workspace, cudaStream_t stream);
 bool attn_prefill_f8_fits(int batch, int max_new, int n_heads, int n_kv_heads);
+
+// Which cached rows stay, and their move to the front (evict.cu).
+constexpr int kEvictMaxTensors = 8;
+struct EvictArgs {
+    void* data[kEvictMaxTensors];              // [num_blocks][n_kv_heads][block_size][row_bytes]
+    int row_bytes[kEvictMaxTensors];
+    bool wide[kEvictMaxTensors];               // rows in pieces of 16 bytes, else 4
+    int slices[kEvictMaxTensors];              // set by the launcher
+    int n_tensors, num_blocks, n_kv_heads, block_size, max_blocks, batch;
+    const int32_t* block_table;
+    const int32_t* context_lens;
+    const float* weights;                      // [batch][n_kv_heads][weights_width]
+    float* weights_out;                        // may be weights
+    int weights_width;
+    const int32_t* keep;                       // [batch], or null: max_keep each
+    int max_keep, sinks, recent;
+    int32_t* kept;                             // [batch][n_kv_heads][max_keep]
+    int32_t* new_lens;                         // [batch]
+    int32_t* status;
+};
+cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream);
 
 // Copies blocks src -> dst of `pairs` in every tensor [num_blocks][bytes] (blocks.cu).
 constexpr int kCopyMaxTensors = 128;   // per launch

@@ -6,6 +6,7 @@
 // threads that holds a head sums its squares by shuffles, so nothing is read twice and nothing goes through shared
 // memory; a token's (cos, sin) row and the gains stay in registers for a thread's heads.
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -16,14 +17,14 @@ namespace ll {
 namespace {
 
 constexpr int kNormThreads = 256;
-constexpr int kNormHeads = 4;          // of a thread, forward
+constexpr int kNormHeads = 3;          // of a thread, forward
 constexpr int kNormGradHeads = 2;      // of a thread, gradient (x and dy of each)
 constexpr int kNormGradCtasPerSm = 2;
 constexpr int kNormAnyWarps = 4;       // of the gradient's CTA for other shapes
 
-// How the threads of a vector kernel share a token's heads: a head is `lanes` threads of a group of `width` (a power
-// of two), each with two 16-byte columns; a token is `rows` groups, each with up to U heads at a time, in `parts`
-// turns; a CTA has `slots` tokens at a time.
+// How the threads of a vector kernel share a token's heads: a head is `lanes` threads of a group of W (a power of
+// two), each with two 16-byte columns; a token is `rows` groups, each with up to U heads at a time, in `parts` turns; a
+// CTA has `slots` tokens at a time.
 struct HeadSplit {
     int lanes, width, rows, parts, slots, threads;
 };
@@ -31,7 +32,7 @@ struct HeadSplit {
 HeadSplit head_split(int head_dim, int n, int heads, int per_thread) {
     HeadSplit s;
     s.lanes = head_dim / (2 * n);
-    s.width = 1;
+    s.width = 4;
     while (s.width < s.lanes) s.width *= 2;
     const int most = kNormThreads / s.width;
     s.parts = (heads + per_thread * most - 1) / (per_thread * most);
@@ -55,49 +56,42 @@ struct Columns {
     }
 };
 
-template <int N>
-LL_DEVINL void load_angles(const float2* table, int pos, int half, int first_pair, float (&c)[N], float (&s)[N]) {
-    const float4* cs = reinterpret_cast<const float4*>(table + (size_t)pos * half + first_pair);
+// Element pairs (2 i, 2 i + 1) of a 16-byte column.
+template <typename T>
+LL_DEVINL void unpack2(const uint4& w, float2 (&v)[Vec<T>::N / 2]) {
+    float f[Vec<T>::N];
+    Vec<T>::unpack(w, f);
 #pragma unroll
-    for (int i = 0; i < N / 2; ++i) {
-        const float4 x = __ldg(cs + i);
-        c[2 * i] = x.x;
-        s[2 * i] = x.y;
-        c[2 * i + 1] = x.z;
-        s[2 * i + 1] = x.w;
+    for (int i = 0; i < Vec<T>::N / 2; ++i) v[i] = make_float2(f[2 * i], f[2 * i + 1]);
+}
+template <typename T>
+LL_DEVINL uint4 pack2(const float2 (&v)[Vec<T>::N / 2]) {
+    float f[Vec<T>::N];
+#pragma unroll
+    for (int i = 0; i < Vec<T>::N / 2; ++i) {
+        f[2 * i] = v[i].x;
+        f[2 * i + 1] = v[i].y;
+    }
+    return Vec<T>::pack(f);
+}
+
+template <int M>
+LL_DEVINL void load2(const float* p, float2 (&v)[M]) {
+#pragma unroll
+    for (int i = 0; i < M / 2; ++i) {
+        const float4 x = __ldg(reinterpret_cast<const float4*>(p) + i);
+        v[2 * i] = make_float2(x.x, x.y);
+        v[2 * i + 1] = make_float2(x.z, x.w);
     }
 }
 
-template <int N>
-LL_DEVINL void load_gains(const float* g, int e0, int e1, float (&a)[N], float (&b)[N]) {
-#pragma unroll
-    for (int i = 0; i < N / 4; ++i) {
-        const float4 x = __ldg(reinterpret_cast<const float4*>(g + e0) + i), y = __ldg(reinterpret_cast<const float4*>(g + e1) + i);
-        a[4 * i] = x.x; a[4 * i + 1] = x.y; a[4 * i + 2] = x.z; a[4 * i + 3] = x.w;
-        b[4 * i] = y.x; b[4 * i + 1] = y.y; b[4 * i + 2] = y.z; b[4 * i + 3] = y.w;
-    }
-}
+LL_DEVINL float2 swapped(float2 v) { return make_float2(v.y, v.x); }
+LL_DEVINL float2 both(float x) { return make_float2(x, x); }
 
-// The N pairs that the columns a and b hold, turned by (c, s).
-template <int N, bool HALF>
-LL_DEVINL void turn_pairs(float (&a)[N], float (&b)[N], const float (&c)[N], const float (&s)[N], float sign) {
+template <int W>
+LL_DEVINL float group_sum(float x) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        if (HALF) {
-            const float2 r = rope_rotate(a[i], b[i], c[i], sign * s[i]);
-            a[i] = r.x;
-            b[i] = r.y;
-        } else {
-            float* v = i < N / 2 ? a + 2 * i : b + 2 * i - N;
-            const float2 r = rope_rotate(v[0], v[1], c[i], sign * s[i]);
-            v[0] = r.x;
-            v[1] = r.y;
-        }
-    }
-}
-
-LL_DEVINL float group_sum(float x, int width) {
-    for (int o = width >> 1; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    for (int o = W >> 1; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
     return x;
 }
 
@@ -108,66 +102,119 @@ LL_DEVINL int norm_position(const int32_t* positions, int t, int max_position, i
     return -1;
 }
 
-template <typename T, bool HALF>
-__global__ void __launch_bounds__(kNormThreads) norm_rope_vec_kernel(const NormRopeArgs a, const HeadSplit hs) {
-    using V = Vec<T>;
-    constexpr int N = V::N, U = kNormHeads;
-    pdl_wait();
-    pdl_trigger();
-    const int group = threadIdx.x / hs.width, lane = threadIdx.x % hs.width;
-    const int slot = group / hs.rows, row = group - slot * hs.rows;
-    const int t = blockIdx.x * hs.slots + slot;
-    const bool here = slot < hs.slots && t < a.tokens;
-    const int pos = here ? norm_position(a.positions, t, a.max_position, a.status, lane == 0 && row == 0 && blockIdx.y == 0) : -1;
-    const bool live = pos >= 0 && lane < hs.lanes;      // (every thread takes part in the shuffles)
-    const Columns<N, HALF> col(lane, a.rotary_dim);
-    const int H = a.n_heads + a.n_kv_heads;
-    const int h0 = blockIdx.y * hs.rows * U + row;
-    uint4 w0[U], w1[U];
+// The (cos, sin) entries of a thread's two columns, as whole pairs of elements: half-split, c[i], s[i] belong to
+// elements 2 i and 2 i + 1 of both columns; interleaved, to pair i of the thread's N, with s = (-sin, sin).
+template <int N, bool HALF>
+struct Turn {
+    static constexpr int M = HALF ? N / 2 : N;
+    float2 c[M], s[M];
+    LL_DEVINL void load(const float2* table, int pos, int half, int e0) {
+        const float4* cs = reinterpret_cast<const float4*>(table + (size_t)pos * half + (HALF ? e0 : e0 / 2));
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int h = h0 + u * hs.rows;
-        w0[u] = w1[u] = make_uint4(0u, 0u, 0u, 0u);
-        if (live && h < H) {
-            const bool isq = h < a.n_heads;
-            const T* src = static_cast<const T*>(isq ? a.q : a.k) + (size_t)t * (isq ? a.q_stride : a.k_stride) +
-                           (size_t)(isq ? h : h - a.n_heads) * a.head_dim;
-            w0[u] = *reinterpret_cast<const uint4*>(src + col.e0);
-            w1[u] = *reinterpret_cast<const uint4*>(src + col.e1);
+        for (int i = 0; i < N / 2; ++i) {               // two pairs of the head at a time
+            const float4 x = __ldg(cs + i);
+            if (HALF) {
+                c[i] = make_float2(x.x, x.z);
+                s[i] = make_float2(x.y, x.w);
+            } else {
+                c[(2 * i) % M] = both(x.x);
+                s[(2 * i) % M] = make_float2(-x.y, x.y);
+                c[(2 * i + 1) % M] = both(x.z);
+                s[(2 * i + 1) % M] = make_float2(-x.w, x.w);
+            }
         }
     }
-    float c[N], s[N], g0[N], g1[N];
-    bool gain_q = h0 < a.n_heads;
-    if (live) {
-        if (col.turn) load_angles<N>(a.table, pos, a.rotary_dim >> 1, HALF ? col.e0 : col.e0 / 2, c, s);
-        load_gains<N>(gain_q ? a.q_gain : a.k_gain, col.e0, col.e1, g0, g1);
+};
+
+// Forward.  The gains are taken into the factors of the rotation once for a thread's U heads of a token: with a, b
+// the columns of x,  a' = r (a fa + b ga),  b' = r (b fb + a gb)  (interleaved: a' = r (a fa + swapped(a) ga), b' likewise).
+template <typename T, bool HALF, int W>
+__global__ void __launch_bounds__(kNormThreads, 3) norm_rope_vec_kernel(const NormRopeArgs a, const HeadSplit hs, float inv_d) {
+    constexpr int N = Vec<T>::N, P = N / 2, U = kNormHeads;
+    pdl_wait();
+    pdl_trigger();
+    const int group = threadIdx.x / W, lane = threadIdx.x % W;
+    const int slot = group / hs.rows, row = group - slot * hs.rows;
+    const int t = blockIdx.x * hs.slots + slot;
+    const bool here = slot < hs.slots && t < a.tokens, mine = here && lane < hs.lanes;
+    const Columns<N, HALF> col(lane, a.rotary_dim);
+    const int H = a.n_heads + a.n_kv_heads, gap = col.e1 - col.e0;
+    const int h0 = blockIdx.y * hs.rows * U + row;
+    const int pos_read = here ? a.positions[t] : 0;
+    const T* q = static_cast<const T*>(a.q) + (size_t)t * a.q_stride + col.e0;
+    const T* k = static_cast<const T*>(a.k) + (size_t)t * a.k_stride + col.e0 - (long long)a.n_heads * a.head_dim;
+    uint4 w0[U], w1[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {                       // (on their way before the position is there)
+        const int h = h0 + u * hs.rows;
+        w0[u] = w1[u] = make_uint4(0u, 0u, 0u, 0u);
+        if (mine && h < H) {
+            const T* src = (h < a.n_heads ? q : k) + (size_t)h * a.head_dim;
+            w0[u] = *reinterpret_cast<const uint4*>(src);
+            w1[u] = *reinterpret_cast<const uint4*>(src + gap);
+        }
     }
+    const bool known = pos_read >= 0 && pos_read < a.max_position;
+    if (here && !known && lane == 0 && row == 0 && blockIdx.y == 0) flag_status(a.status, LL_DEV_BAD_POSITION);
+    const bool live = known && mine;                    // (every thread takes part in the shuffles)
+    float2 fa[P], ga[P], fb[P], gb[P];
+    const auto factors = [&](const float* gain) {
+        load2<P>(gain + col.e0, fa);
+        load2<P>(gain + col.e1, fb);
+        if (!col.turn) return;
+        Turn<N, HALF> turn;
+        turn.load(a.table, pos_read, a.rotary_dim >> 1, col.e0);
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            if (HALF) {
+                ga[i] = mul2(fb[i], make_float2(-turn.s[i].x, -turn.s[i].y));
+                gb[i] = mul2(fa[i], turn.s[i]);
+                fa[i] = mul2(fa[i], turn.c[i]);
+                fb[i] = mul2(fb[i], turn.c[i]);
+            } else {
+                constexpr int M = Turn<N, HALF>::M;
+                ga[i] = mul2(swapped(fa[i]), turn.s[i]);
+                gb[i] = mul2(swapped(fb[i]), turn.s[(P + i) % M]);
+                fa[i] = mul2(fa[i], turn.c[i]);
+                fb[i] = mul2(fb[i], turn.c[(P + i) % M]);
+            }
+        }
+    };
+    bool gain_q = h0 < a.n_heads;
+    if (live) factors(gain_q ? a.q_gain : a.k_gain);
+    T* q_out = static_cast<T*>(a.q_out) + (size_t)t * a.q_out_stride + col.e0;
+    T* k_out = static_cast<T*>(a.k_out) + (size_t)t * a.k_out_stride + col.e0 - (long long)a.n_heads * a.head_dim;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int h = h0 + u * hs.rows;
-        float x[N], y[N], sum = 0.f;
-        V::unpack(w0[u], x);
-        V::unpack(w1[u], y);
+        float2 x[P], y[P], sum = make_float2(0.f, 0.f);
+        unpack2<T>(w0[u], x);
+        unpack2<T>(w1[u], y);
 #pragma unroll
-        for (int i = 0; i < N; ++i) sum += x[i] * x[i] + y[i] * y[i];
-        sum = group_sum(sum, hs.width);
+        for (int i = 0; i < P; ++i) sum = fma2(y[i], y[i], fma2(x[i], x[i], sum));
+        const float total = group_sum<W>(sum.x + sum.y);
         if (!live || h >= H) continue;
         const bool isq = h < a.n_heads;
         if (isq != gain_q) {
             gain_q = isq;
-            load_gains<N>(a.k_gain, col.e0, col.e1, g0, g1);
+            factors(a.k_gain);
         }
-        const float r = rsqrtf(sum / (float)a.head_dim + a.eps);
+        const float2 r = both(rsqrtf(total * inv_d + a.eps));
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            x[i] = x[i] * r * g0[i];
-            y[i] = y[i] * r * g1[i];
+        for (int i = 0; i < P; ++i) {
+            if (col.turn) {
+                const float2 u0 = HALF ? y[i] : swapped(x[i]), u1 = HALF ? x[i] : swapped(y[i]);
+                const float2 a0 = fma2(x[i], fa[i], mul2(u0, ga[i])), b0 = fma2(y[i], fb[i], mul2(u1, gb[i]));
+                x[i] = mul2(a0, r);
+                y[i] = mul2(b0, r);
+            } else {
+                x[i] = mul2(mul2(x[i], r), fa[i]);
+                y[i] = mul2(mul2(y[i], r), fb[i]);
+            }
         }
-        if (col.turn) turn_pairs<N, HALF>(x, y, c, s, 1.f);
-        T* dst = static_cast<T*>(isq ? a.q_out : a.k_out) + (size_t)t * (isq ? a.q_out_stride : a.k_out_stride) +
-                 (size_t)(isq ? h : h - a.n_heads) * a.head_dim;
-        *reinterpret_cast<uint4*>(dst + col.e0) = V::pack(x);
-        *reinterpret_cast<uint4*>(dst + col.e1) = V::pack(y);
+        T* dst = (isq ? q_out : k_out) + (size_t)h * a.head_dim;
+        *reinterpret_cast<uint4*>(dst) = pack2<T>(x);
+        *reinterpret_cast<uint4*>(dst + gap) = pack2<T>(y);
     }
 }
 
@@ -204,7 +251,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_rope_any_kernel(const NormR
             const float x = V::get(src + i);
             sum += x * x;
         }
-        const float r = rsqrtf(group_sum(sum, 32) / (float)a.head_dim + a.eps);
+        const float r = rsqrtf(group_sum<32>(sum) / (float)a.head_dim + a.eps);
         for (int u = lane; u < units; u += 32) {          // (a lane's elements are its own: in place is safe, the sum is done)
             int i0, i1;
             unit_elements(u, a.rotary_dim, a.interleaved, i0, i1);
@@ -223,116 +270,139 @@ __global__ void __launch_bounds__(kNormThreads) norm_rope_any_kernel(const NormR
 
 // ---------------------------------------------------------------- gradient
 
-// Tokens go round the CTAs; a thread keeps the gain gradients of its columns over all of them.  The sums of a CTA's
-// groups meet in shared memory in a fixed order, those of the CTAs in a second kernel: the same bits every time.
-template <typename T, bool HALF>
+// Head rows of one tensor (q or k).
+template <typename T>
+struct HeadRows {
+    const T *x, *dy;
+    T* dx;
+    long long x_stride, dy_stride, dx_stride;
+    const float* gain;
+    int heads;
+};
+
+// The tokens go round the CTAs of a tensor (q's, then k's); a group has U heads of a token at a time, its loads all on
+// their way before the first is used, the token's position read a turn ahead.  A thread keeps the gain gradients of its
+// columns over all its tokens.  The sums of a CTA's groups meet in shared memory in a fixed order, those of the CTAs in a
+// second kernel: the same bits every time.
+template <typename T, bool HALF, int W>
 __global__ void __launch_bounds__(kNormThreads, kNormGradCtasPerSm)
-    norm_rope_grad_vec_kernel(const NormRopeGradArgs a, const HeadSplit hs) {
-    using V = Vec<T>;
-    constexpr int N = V::N, U = kNormGradHeads;
+    norm_rope_grad_vec_kernel(const NormRopeGradArgs a, const HeadSplit q_split, const HeadSplit k_split, int q_ctas, float inv_d) {
+    constexpr int N = Vec<T>::N, P = N / 2, U = kNormGradHeads;
     extern __shared__ float s_dg[];                       // [groups][head_dim]
     pdl_wait();
     pdl_trigger();
-    const int group = threadIdx.x / hs.width, lane = threadIdx.x % hs.width;
-    const int slot = group / hs.rows, row = group - slot * hs.rows;
+    const bool isq = (int)blockIdx.x < q_ctas;
+    const int ctas = isq ? q_ctas : gridDim.x - q_ctas, cta = isq ? blockIdx.x : blockIdx.x - q_ctas;
+    HeadRows<T> m;
+    m.x = static_cast<const T*>(isq ? a.q : a.k);
+    m.dy = static_cast<const T*>(isq ? a.dq : a.dk);
+    m.dx = static_cast<T*>(isq ? a.q_grad : a.k_grad);
+    m.x_stride = isq ? a.q_stride : a.k_stride;
+    m.dy_stride = isq ? a.dq_stride : a.dk_stride;
+    m.dx_stride = isq ? a.q_grad_stride : a.k_grad_stride;
+    m.gain = isq ? a.q_gain : a.k_gain;
+    m.heads = isq ? a.n_heads : a.n_kv_heads;
+    const int rows = isq ? q_split.rows : k_split.rows, slots = isq ? q_split.slots : k_split.slots;
+    const int parts = isq ? q_split.parts : k_split.parts;
+    const int group = threadIdx.x / W, lane = threadIdx.x % W;
+    const int slot = group / rows, row = group - slot * rows;
     const Columns<N, HALF> col(lane, a.rotary_dim);
-    const int H = a.n_heads + a.n_kv_heads;
-    const bool worker = slot < hs.slots && lane < hs.lanes;
-    float dg0[2][N], dg1[2][N];                           // [q, k]
+    const int gap = col.e1 - col.e0;
+    const bool worker = slot < slots && lane < q_split.lanes;
+    float2 dg0[P], dg1[P];
 #pragma unroll
-    for (int i = 0; i < N; ++i) dg0[0][i] = dg0[1][i] = dg1[0][i] = dg1[1][i] = 0.f;
-    const float inv_d = 1.f / (float)a.head_dim;
+    for (int i = 0; i < P; ++i) dg0[i] = dg1[i] = make_float2(0.f, 0.f);
 
-    for (int t0 = blockIdx.x * hs.slots; t0 < a.tokens; t0 += gridDim.x * hs.slots) {
-        const int t = t0 + slot;
-        const bool here = slot < hs.slots && t < a.tokens;
-        const int pos = here ? norm_position(a.positions, t, a.max_position, a.status, lane == 0 && row == 0) : -1;
-        const bool live = pos >= 0 && worker;
-        float c[N], s[N];
-        if (live && col.turn) load_angles<N>(a.table, pos, a.rotary_dim >> 1, HALF ? col.e0 : col.e0 / 2, c, s);
-        for (int part = 0; part < hs.parts; ++part) {
-            const int h0 = part * hs.rows * U + row;
+    const int t_step = ctas * slots;
+    int t = cta * slots + slot;
+    int pos_next = slot < slots && t < a.tokens ? a.positions[t] : 0;
+    // (as many turns for every group of the CTA: the shuffles need whole warps)
+    for (int t0 = cta * slots; t0 < a.tokens; t0 += t_step, t += t_step) {
+        const int pos = pos_next;
+        pos_next = slot < slots && t + t_step < a.tokens ? a.positions[t + t_step] : 0;
+        const bool here = slot < slots && t < a.tokens, known = pos >= 0 && pos < a.max_position;
+        if (here && !known && lane == 0 && row == 0) flag_status(a.status, LL_DEV_BAD_POSITION);
+        const bool live = here && known && worker;
+        for (int part = 0; part < parts; ++part) {
+            const int h0 = part * rows * U + row;
             uint4 wx0[U], wx1[U], wy0[U], wy1[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int h = h0 + u * hs.rows;
+                const int h = h0 + u * rows;
                 wx0[u] = wx1[u] = wy0[u] = wy1[u] = make_uint4(0u, 0u, 0u, 0u);
-                if (live && h < H) {
-                    const bool isq = h < a.n_heads;
-                    const size_t at = (size_t)(isq ? h : h - a.n_heads) * a.head_dim;
-                    const T* x = static_cast<const T*>(isq ? a.q : a.k) + (size_t)t * (isq ? a.q_stride : a.k_stride) + at;
-                    const T* dy = static_cast<const T*>(isq ? a.dq : a.dk) + (size_t)t * (isq ? a.dq_stride : a.dk_stride) + at;
-                    wx0[u] = *reinterpret_cast<const uint4*>(x + col.e0);
-                    wx1[u] = *reinterpret_cast<const uint4*>(x + col.e1);
-                    wy0[u] = *reinterpret_cast<const uint4*>(dy + col.e0);
-                    wy1[u] = *reinterpret_cast<const uint4*>(dy + col.e1);
+                if (live && h < m.heads) {
+                    const T* x = m.x + t * m.x_stride + h * a.head_dim + col.e0;
+                    const T* dy = m.dy + t * m.dy_stride + h * a.head_dim + col.e0;
+                    wx0[u] = *reinterpret_cast<const uint4*>(x);
+                    wx1[u] = *reinterpret_cast<const uint4*>(x + gap);
+                    wy0[u] = *reinterpret_cast<const uint4*>(dy);
+                    wy1[u] = *reinterpret_cast<const uint4*>(dy + gap);
                 }
             }
+            Turn<N, HALF> turn;
+            if (live && col.turn) turn.load(a.table, pos, a.rotary_dim >> 1, col.e0);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int h = h0 + u * hs.rows;
-                const bool isq = h < a.n_heads, on = live && h < H;
-                float x0[N], x1[N], y0[N], y1[N], g0[N], g1[N];
-                V::unpack(wx0[u], x0);
-                V::unpack(wx1[u], x1);
-                V::unpack(wy0[u], y0);
-                V::unpack(wy1[u], y1);
-                float sq = 0.f, dot = 0.f;
+                const int h = h0 + u * rows;
+                const bool on = live && h < m.heads;
+                float2 x0[P], x1[P], y0[P], y1[P], g0[P], g1[P], sq = make_float2(0.f, 0.f), dot = sq;
                 if (on) {
-                    load_gains<N>(isq ? a.q_gain : a.k_gain, col.e0, col.e1, g0, g1);
-                    if (col.turn) turn_pairs<N, HALF>(y0, y1, c, s, -1.f);
+                    unpack2<T>(wx0[u], x0);
+                    unpack2<T>(wx1[u], x1);
+                    unpack2<T>(wy0[u], y0);
+                    unpack2<T>(wy1[u], y1);
+                    load2<P>(m.gain + col.e0, g0);
+                    load2<P>(m.gain + col.e1, g1);
 #pragma unroll
-                    for (int i = 0; i < N; ++i) {
-                        sq += x0[i] * x0[i] + x1[i] * x1[i];
-                        dot += y0[i] * g0[i] * x0[i] + y1[i] * g1[i] * x1[i];
+                    for (int i = 0; i < P; ++i) {
+                        if (col.turn) {                   // dn = R^T dy
+                            if (HALF) {
+                                const float2 n0 = fma2(y0[i], turn.c[i], mul2(y1[i], turn.s[i]));
+                                y1[i] = fma2(y1[i], turn.c[i], mul2(y0[i], make_float2(-turn.s[i].x, -turn.s[i].y)));
+                                y0[i] = n0;
+                            } else {                      // (s swapped is -s)
+                                constexpr int M = Turn<N, HALF>::M;
+                                y0[i] = fma2(y0[i], turn.c[i], mul2(swapped(y0[i]), swapped(turn.s[i])));
+                                y1[i] = fma2(y1[i], turn.c[(P + i) % M], mul2(swapped(y1[i]), swapped(turn.s[(P + i) % M])));
+                            }
+                        }
+                        g0[i] = mul2(y0[i], g0[i]);
+                        g1[i] = mul2(y1[i], g1[i]);
+                        sq = fma2(x1[i], x1[i], fma2(x0[i], x0[i], sq));
+                        dot = fma2(g1[i], x1[i], fma2(g0[i], x0[i], dot));
                     }
                 }
-                sq = group_sum(sq, hs.width);
-                dot = group_sum(dot, hs.width);
+                const float sum_sq = group_sum<W>(sq.x + sq.y), sum_dot = group_sum<W>(dot.x + dot.y);
                 if (!on) continue;
-                const float r = rsqrtf(sq * inv_d + a.eps), f = dot * inv_d * r * r;
-                if (isq) {
+                const float r = rsqrtf(sum_sq * inv_d + a.eps), f = -(sum_dot * inv_d * r * r);
 #pragma unroll
-                    for (int i = 0; i < N; ++i) {
-                        dg0[0][i] += y0[i] * (x0[i] * r);
-                        dg1[0][i] += y1[i] * (x1[i] * r);
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < N; ++i) {
-                        dg0[1][i] += y0[i] * (x0[i] * r);
-                        dg1[1][i] += y1[i] * (x1[i] * r);
-                    }
+                for (int i = 0; i < P; ++i) {
+                    dg0[i] = fma2(y0[i], mul2(x0[i], both(r)), dg0[i]);
+                    dg1[i] = fma2(y1[i], mul2(x1[i], both(r)), dg1[i]);
+                    x0[i] = mul2(fma2(x0[i], both(f), g0[i]), both(r));
+                    x1[i] = mul2(fma2(x1[i], both(f), g1[i]), both(r));
                 }
-#pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    x0[i] = r * (y0[i] * g0[i] - x0[i] * f);
-                    x1[i] = r * (y1[i] * g1[i] - x1[i] * f);
-                }
-                T* dst = static_cast<T*>(isq ? a.q_grad : a.k_grad) + (size_t)t * (isq ? a.q_grad_stride : a.k_grad_stride) +
-                         (size_t)(isq ? h : h - a.n_heads) * a.head_dim;
-                *reinterpret_cast<uint4*>(dst + col.e0) = V::pack(x0);
-                *reinterpret_cast<uint4*>(dst + col.e1) = V::pack(x1);
+                T* dst = m.dx + t * m.dx_stride + h * a.head_dim + col.e0;
+                *reinterpret_cast<uint4*>(dst) = pack2<T>(x0);
+                *reinterpret_cast<uint4*>(dst + gap) = pack2<T>(x1);
             }
         }
     }
-    const int groups = hs.slots * hs.rows;
+    if (worker) {
+        float2* s0 = reinterpret_cast<float2*>(s_dg + group * a.head_dim + col.e0);
+        float2* s1 = reinterpret_cast<float2*>(s_dg + group * a.head_dim + col.e1);
 #pragma unroll
-    for (int which = 0; which < 2; ++which) {
-        if (worker) {
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                s_dg[group * a.head_dim + col.e0 + i] = dg0[which][i];
-                s_dg[group * a.head_dim + col.e1 + i] = dg1[which][i];
-            }
+        for (int i = 0; i < P; ++i) {
+            s0[i] = dg0[i];
+            s1[i] = dg1[i];
         }
-        __syncthreads();
-        for (int e = threadIdx.x; e < a.head_dim; e += blockDim.x) {
-            float sum = 0.f;
-            for (int i = 0; i < groups; ++i) sum += s_dg[i * a.head_dim + e];
-            a.partials[((size_t)blockIdx.x * 2 + which) * a.head_dim + e] = sum;
-        }
-        __syncthreads();
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.head_dim; e += blockDim.x) {
+        float sum = 0.f;
+#pragma unroll 8
+        for (int i = 0; i < slots * rows; ++i) sum += s_dg[i * a.head_dim + e];
+        a.partials[(size_t)blockIdx.x * a.head_dim + e] = sum;
     }
 }
 
@@ -385,8 +455,8 @@ __global__ void __launch_bounds__(kNormAnyWarps * 32) norm_rope_grad_any_kernel(
                 }
             }
             if (turn == 0) {
-                r = rsqrtf(group_sum(sq, 32) / (float)d + a.eps);
-                f = group_sum(dot, 32) / (float)d * r * r;
+                r = rsqrtf(group_sum<32>(sq) / (float)d + a.eps);
+                f = group_sum<32>(dot) / (float)d * r * r;
             }
         }
     }
@@ -394,30 +464,47 @@ __global__ void __launch_bounds__(kNormAnyWarps * 32) norm_rope_grad_any_kernel(
     for (int i = threadIdx.x; i < 2 * d; i += blockDim.x) {
         float sum = 0.f;
         for (int w = 0; w < kNormAnyWarps; ++w) sum += s_dg[w * 2 * d + i];
-        a.partials[(size_t)blockIdx.x * 2 * d + i] = sum;
+        a.partials[((size_t)blockIdx.x + (i < d ? 0 : gridDim.x)) * d + (i < d ? i : i - d)] = sum;
     }
 }
 
-// Gain gradients: the sum of the CTAs' partials [ctas][2][head_dim], eight of them at a time per column.
-__global__ void __launch_bounds__(256) norm_rope_gains_kernel(const float* partials, int ctas, int head_dim, float* q_gain_grad,
-                                                              float* k_gain_grad) {
-    __shared__ float s_sum[8][32];
+// Gain gradients: the sums of the partials [q_rows of q, k_rows of k][head_dim], 32 of them at a time per column.
+__global__ void __launch_bounds__(1024) norm_rope_gains_kernel(const float* partials, int q_rows, int k_rows, int head_dim,
+                                                               float* q_gain_grad, float* k_gain_grad) {
+    __shared__ float s_sum[32][33];
     pdl_wait();
     pdl_trigger();
-    const int i = blockIdx.x * 32 + (threadIdx.x & 31), w = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, i = blockIdx.x * 32 + lane;
+    const bool isq = blockIdx.y == 0;
+    float* out = isq ? q_gain_grad : k_gain_grad;
+    if (!out) return;
+    if (!isq) partials += (size_t)q_rows * head_dim;
+    const int rows = isq ? q_rows : k_rows;
     float sum = 0.f;
-    if (i < 2 * head_dim)
-        for (int c = w; c < ctas; c += 8) sum += partials[(size_t)c * 2 * head_dim + i];
-    s_sum[w][threadIdx.x & 31] = sum;
+    if (i < head_dim) {
+#pragma unroll 5
+        for (int c = w; c < rows; c += 32) sum += partials[(size_t)c * head_dim + i];
+    }
+    s_sum[w][lane] = sum;
     __syncthreads();
-    if (w != 0 || i >= 2 * head_dim) return;
-    for (int j = 1; j < 8; ++j) sum += s_sum[j][threadIdx.x];
-    float* out = i < head_dim ? q_gain_grad : k_gain_grad;
-    if (out) out[i < head_dim ? i : i - head_dim] = sum;
+    const float total = group_sum<32>(s_sum[lane][w]);    // warp w: column w
+    const int e = blockIdx.x * 32 + w;
+    if (lane == 0 && e < head_dim) out[e] = total;
 }
 
 bool rows16(const void* p, long long stride, int esz) {
     return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && stride * esz % 16 == 0;
+}
+
+// f with the width of a group as a constant.
+template <typename F>
+cudaError_t for_width(int width, F&& f) {
+    switch (width) {
+        case 4: return f(std::integral_constant<int, 4>{});
+        case 8: return f(std::integral_constant<int, 8>{});
+        case 16: return f(std::integral_constant<int, 16>{});
+        default: return f(std::integral_constant<int, 32>{});
+    }
 }
 
 // 16-byte columns, two to a thread, a head within a warp: every row and the gains start on 16 bytes.
@@ -437,8 +524,10 @@ cudaError_t norm_rope_for(const NormRopeArgs& a, cudaStream_t stream) {
     if (vec) {
         const HeadSplit hs = head_split(a.head_dim, N, H, kNormHeads);
         const dim3 grid((unsigned)((a.tokens + hs.slots - 1) / hs.slots), (unsigned)hs.parts);
-        e = a.interleaved ? launch_pdl(norm_rope_vec_kernel<T, false>, grid, dim3(hs.threads), 0, stream, 1, a, hs)
-                          : launch_pdl(norm_rope_vec_kernel<T, true>, grid, dim3(hs.threads), 0, stream, 1, a, hs);
+        e = for_width(hs.width, [&](auto w) {
+            return launch_pdl(a.interleaved ? norm_rope_vec_kernel<T, false, w.value> : norm_rope_vec_kernel<T, true, w.value>, grid,
+                              dim3(hs.threads), 0, stream, 1, a, hs, 1.f / (float)a.head_dim);
+        });
     } else {
         const unsigned y = (unsigned)std::min(16, (H + kNormThreads / 32 - 1) / (kNormThreads / 32));
         e = launch_pdl(norm_rope_any_kernel<T>, dim3((unsigned)a.tokens, y), dim3(kNormThreads), 0, stream, 1, a);
@@ -451,34 +540,43 @@ cudaError_t norm_rope_for(const NormRopeArgs& a, cudaStream_t stream) {
 template <typename T>
 cudaError_t norm_rope_grad_for(const NormRopeGradArgs& a, cudaStream_t stream) {
     constexpr int N = Vec<T>::N, E = (int)sizeof(T);
-    const int H = a.n_heads + a.n_kv_heads;
     const int most = std::min(kNormGradMaxCtas, std::max(1, device_sm_count()) * kNormGradCtasPerSm);
     const bool vec = vec_shape(a.head_dim, a.rotary_dim, N) &&
                      (a.n_heads == 0 || (rows16(a.q, a.q_stride, E) && rows16(a.dq, a.dq_stride, E) && rows16(a.q_grad, a.q_grad_stride, E) && rows16(a.q_gain, 0, 4))) &&
                      (a.n_kv_heads == 0 || (rows16(a.k, a.k_stride, E) && rows16(a.dk, a.dk_stride, E) && rows16(a.k_grad, a.k_grad_stride, E) && rows16(a.k_gain, 0, 4)));
-    int ctas;
+    int q_rows = 0, k_rows = 0;                           // of partials
     cudaError_t e = cudaSuccess;
     trace_before("norm_rope_grad", stream);
     if (a.tokens == 0) {                                  // the gains' gradients are zeros
-        ctas = 0;
     } else if (vec) {
-        const HeadSplit hs = head_split(a.head_dim, N, H, kNormGradHeads);
-        ctas = std::min(most, (a.tokens + hs.slots - 1) / hs.slots);
-        const size_t smem = (size_t)hs.slots * hs.rows * a.head_dim * sizeof(float);   // at most 256 threads of 2 N columns: 16 KB
-        e = a.interleaved ? launch_pdl(norm_rope_grad_vec_kernel<T, false>, dim3(ctas), dim3(hs.threads), smem, stream, 1, a, hs)
-                          : launch_pdl(norm_rope_grad_vec_kernel<T, true>, dim3(ctas), dim3(hs.threads), smem, stream, 1, a, hs);
+        // CTAs for q and for k, as many as their tokens ask for, in proportion to their heads up to what runs at once
+        const HeadSplit qs = head_split(a.head_dim, N, std::max(a.n_heads, 1), kNormGradHeads);
+        const HeadSplit ks = head_split(a.head_dim, N, std::max(a.n_kv_heads, 1), kNormGradHeads);
+        q_rows = a.n_heads ? (a.tokens + qs.slots - 1) / qs.slots : 0;
+        k_rows = a.n_kv_heads ? (a.tokens + ks.slots - 1) / ks.slots : 0;
+        if (q_rows + k_rows > most) {
+            const int q_part = a.n_heads == 0 ? 0 : a.n_kv_heads == 0 ? most :
+                std::min(most - 1, std::max(1, (int)((long long)most * a.n_heads / (a.n_heads + a.n_kv_heads))));
+            q_rows = std::min(q_rows, q_part);
+            k_rows = std::min(k_rows, most - q_rows);
+        }
+        const size_t smem = (size_t)std::max(qs.slots * qs.rows, ks.slots * ks.rows) * a.head_dim * sizeof(float);   // at most 16 KB
+        e = for_width(qs.width, [&](auto w) {
+            return launch_pdl(a.interleaved ? norm_rope_grad_vec_kernel<T, false, w.value> : norm_rope_grad_vec_kernel<T, true, w.value>,
+                              dim3(q_rows + k_rows), dim3(kNormThreads), smem, stream, 1, a, qs, ks, q_rows, 1.f / (float)a.head_dim);
+        });
     } else {
-        const long long rows = (long long)a.tokens * H;
-        ctas = (int)std::min<long long>(most, (rows + kNormAnyWarps - 1) / kNormAnyWarps);
+        const long long rows = (long long)a.tokens * (a.n_heads + a.n_kv_heads);
+        q_rows = k_rows = (int)std::min<long long>(most, (rows + kNormAnyWarps - 1) / kNormAnyWarps);
         const size_t smem = (size_t)kNormAnyWarps * 2 * a.head_dim * sizeof(float);    // 32 KB at head_dim 1024
-        e = launch_pdl(norm_rope_grad_any_kernel<T>, dim3(ctas), dim3(kNormAnyWarps * 32), smem, stream, 1, a);
+        e = launch_pdl(norm_rope_grad_any_kernel<T>, dim3(q_rows), dim3(kNormAnyWarps * 32), smem, stream, 1, a);
     }
     trace_after(stream);
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) return record(e, "norm_rope_grad launch");
     trace_before("norm_rope_gains", stream);
-    e = launch_pdl(norm_rope_gains_kernel, dim3((2 * a.head_dim + 31) / 32), dim3(256), 0, stream, 1, (const float*)a.partials, ctas,
-                   a.head_dim, a.n_heads ? a.q_gain_grad : nullptr, a.n_kv_heads ? a.k_gain_grad : nullptr);
+    e = launch_pdl(norm_rope_gains_kernel, dim3((a.head_dim + 31) / 32, 2), dim3(1024), 0, stream, 1, (const float*)a.partials, q_rows,
+                   k_rows, a.head_dim, a.n_heads ? a.q_gain_grad : nullptr, a.n_kv_heads ? a.k_gain_grad : nullptr);
     trace_after(stream);
     if (e == cudaSuccess) e = cudaGetLastError();
     return record(e, "norm_rope_gains launch");
