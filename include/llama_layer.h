@@ -565,6 +565,26 @@ int ll_paged_attention_decode_weights_q8(const void* q, const ll_kv_pool_q8* poo
                                          int32_t head_dim, int32_t block_size, float scale, float* weights, int32_t weights_width,
                                          void* out, void* workspace, size_t workspace_bytes, int32_t* status, void* stream);
 
+/* Workspace bytes for ll_paged_attention_weights (0 for sizes that it refuses). */
+size_t ll_attention_weights_workspace_size(int32_t batch, int32_t tokens, int32_t max_new, int32_t n_heads, int32_t n_kv_heads,
+                                           int32_t head_dim, int32_t max_blocks, int32_t block_size);
+
+/* The weights alone, of a ragged batch of query rows (a whole prompt, a chunk, or the last
+ * rows of each context): q BF16 [tokens, n_heads, head_dim] after RoPE, sequence b's rows
+ * cu_new[b] .. cu_new[b+1]-1 (int32 [batch + 1], device; at most max_new), row i of n at
+ * position context_lens[b] - n + i, seeing positions 0 .. that one of the K pool (BF16), which
+ * already holds them.  Adds to weights as ll_paged_attention_decode_weights, summed over the
+ * rows too (the same bits every time); a row of NaN scores gives NaN to what it sees.
+ * Sequences whose counts do not fit together (n < 0, n > max_new, n > context_lens[b], rows
+ * beyond `tokens`, a context beyond the table) set LL_DEV_BAD_POSITION and add nothing.
+ * Limits and workspace rule as ll_paged_attention_decode_weights, and batch * n_kv_heads
+ * times the CTAs that max_new rows ask for below 2^31 (LL_ERR_UNSUPPORTED). */
+int ll_paged_attention_weights(const void* q, const int32_t* cu_new, int32_t tokens, const void* k_pool, int32_t num_blocks,
+                               const int32_t* block_table, int32_t max_blocks, const int32_t* context_lens, int32_t batch,
+                               int32_t max_new, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim, int32_t block_size,
+                               float scale, float* weights, int32_t weights_width, void* workspace, size_t workspace_bytes,
+                               int32_t* status, void* stream);
+
 /* One tensor of a paged pool, by the bytes of a cached row (K or V rows, codes, scales). */
 typedef struct {
     void* data;           /* device, [num_blocks][n_kv_heads][block_size][row_bytes], 4-byte aligned (16: faster) */

@@ -106,3 +106,20 @@ def test_binding_refusals():
         api.evict_rows(k, i(1, 2), i(1), torch.zeros(1, 2, 32), 4)
     with pytest.raises(ValueError, match="GPU"):
         api.evict_rows((k, k), i(1, 2), i(1), torch.zeros(1, 2, 32), 4)
+
+
+OBSERVE = dict(q=FAKE, cu=FAKE, tokens=16, k=FAKE, num_blocks=8, table=FAKE, max_blocks=8, ctx=FAKE, batch=2, max_new=8, n_heads=4,
+               n_kv_heads=2, head_dim=128, block=16, scale=0.1, weights=FAKE, width=128, ws=FAKE, ws_bytes=1 << 40, status=FAKE)
+
+
+@pytest.mark.parametrize("bad,code", [
+    (dict(q=0), INVALID), (dict(q=FAKE + 8), INVALID), (dict(cu=0), INVALID), (dict(tokens=-1), INVALID), (dict(k=0), INVALID),
+    (dict(k=FAKE + 8), INVALID), (dict(num_blocks=0), INVALID), (dict(num_blocks=1 << 26), UNSUPPORTED), (dict(table=0), INVALID),
+    (dict(max_blocks=0), INVALID), (dict(max_blocks=1 << 27), UNSUPPORTED), (dict(ctx=0), INVALID), (dict(batch=0), INVALID),
+    (dict(batch=65536), UNSUPPORTED), (dict(max_new=0), INVALID), (dict(n_heads=6, n_kv_heads=4), UNSUPPORTED), (dict(n_heads=34), UNSUPPORTED),
+    (dict(head_dim=96), UNSUPPORTED), (dict(block=48), UNSUPPORTED), (dict(scale=-0.1), INVALID), (dict(scale=float("nan")), INVALID),
+    (dict(weights=0), INVALID), (dict(weights=FAKE + 1), INVALID), (dict(width=0), INVALID), (dict(ws=0), WORKSPACE),
+    (dict(ws_bytes=16), WORKSPACE), (dict(status=0), INVALID),
+    (dict(batch=65535, n_kv_heads=128, n_heads=128, tokens=1 << 24, max_new=1 << 24), UNSUPPORTED)])
+def test_observe_refusals(bad, code):
+    assert api.lib.ll_paged_attention_weights(*{**OBSERVE, **bad}.values(), NULL) == code

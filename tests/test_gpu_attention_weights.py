@@ -212,3 +212,116 @@ def test_decode_streams_and_graphs():
         check_status(st)
         assert torch.equal(o3, out)
         assert (f64(w) - step * f64(want) <= 2.0 ** -22 * step * f64(want)).all()
+
+
+# ---------------------------------------------------------------- prompts, chunks, last rows
+
+PROMPT = [  # contexts, new rows, heads, kv_heads, dim, block
+    ([1], [1], 1, 1, 64, 16), ([5, 64, 65], [5, 3, 65], 4, 2, 64, 16), ([200, 17, 130], [1, 0, 130], 8, 8, 128, 32),
+    ([700], [700], 2, 2, 128, 128), ([300, 77], [64, 77], 16, 1, 128, 128), ([129, 500], [40, 31], 9, 1, 64, 256),
+    ([1100], [259], 5, 1, 128, 256), ([600] * 3, [32] * 3, 14, 2, 64, 32), ([2100, 100, 1025], [33, 100, 2], 8, 1, 128, 64),
+    ([4000], [17], 6, 2, 128, 128), ([1300], [1300], 3, 1, 64, 64)]
+
+
+def prompt(case, seed=0):
+    ctx, new, H, Hkv, d, block = case
+    c = Paged(ctx, Hkv, d, block, 11 * len(ctx) + H + seed)
+    g = torch.Generator().manual_seed(H + seed)
+    cu = [sum(new[:i]) for i in range(len(new) + 1)]
+    q = torch.randn(cu[-1], H, d, generator=g).bfloat16().cuda()
+    base = torch.rand(len(ctx), Hkv, c.table.shape[1] * block + 3, generator=g).cuda()
+    return c, q, cu, base
+
+
+@pytest.mark.parametrize("case", PROMPT)
+def test_prompt(case):
+    ctx, new, H, Hkv, d, block = case
+    c, q, cu, base = prompt(case)
+    w, st, scale = base.clone(), api.new_status(), 1 / math.sqrt(d)
+    got = api.paged_attention_weights(q, i32(cu), c.k, c.d_table, c.d_ctx, scale, w, max(new), status=st)
+    check_status(st)
+    assert got is w
+    ref, bound = reference(c, f64(q), cu, scale, base)
+    assert_weights(w, ref, bound)
+    for b, n in enumerate(ctx):
+        end = n if new[b] else 0
+        assert torch.equal(w[b, :, end:], base[b, :, end:])
+    # the same bits again, whatever the workspace held; an upper bound of the rows may split them otherwise
+    for more in (max(new), max(new) + 50):
+        again = base.clone()
+        ws = torch.full((api.attention_weights_workspace_size(len(ctx), cu[-1], more, H, Hkv, d, c.table.shape[1], block),), 255,
+                        dtype=torch.uint8, device="cuda")
+        api.paged_attention_weights(q, i32(cu), c.k, c.d_table, c.d_ctx, scale, again, more, workspace=ws, status=st)
+        check_status(st)
+        assert_weights(again, ref, bound)
+        assert more > max(new) or torch.equal(again, w)
+
+
+def test_prompt_equals_its_single_tokens():
+    """A chunk's weights are those of its rows as decode steps, but for rounding."""
+    case = ([150, 90], [7, 3], 8, 2, 128, 32)
+    c, q, cu, base = prompt(case)
+    w = api.paged_attention_weights(q, i32(cu), c.k, c.d_table, c.d_ctx, 0.09, base.clone(), 7)
+    steps = base.clone()
+    for i in range(7):
+        ctx = [150 - 7 + i + 1, 90 - 3 + i + 1 if i < 3 else 0]
+        rows = torch.stack([q[i], q[7 + min(i, 2)]])
+        api.paged_attention_decode_weights(rows, c.k, c.v, c.d_table, i32(ctx), 0.09, steps)
+    ref, bound = reference(c, f64(q), cu, 0.09, base)
+    assert_weights(w, ref, bound)
+    assert (np.abs(f64(w) - f64(steps)) <= 2 * bound + 2.0 ** -20 * np.abs(ref)).all()
+
+
+def test_prompt_edges():
+    """Counts that do not fit, bad blocks, rows of nobody (NaN), narrow weights, no rows."""
+    case = ([60, 50, 90, 40], [20, 10, 30, 5], 4, 2, 64, 16)
+    c, q, cu, base = prompt(case)
+    pad = torch.full((9, 4, 64), math.nan).bfloat16().cuda()
+    wide = torch.cat([pad, q, pad])
+    cu9 = [x + 9 for x in cu]
+    table = c.table.copy()
+    table[2, 1] = 10 ** 6
+    w, st = base.clone(), api.new_status()
+    api.paged_attention_weights(wide, i32(cu9), c.k, i32(table), i32([60, 8, 90, 40]), 0.125, w, 30, status=st)     # 8 < 10 rows
+    check_status(st, api.LL_DEV_BAD_POSITION | api.LL_DEV_BAD_BLOCK)
+    ref, bound = reference(c, f64(q), cu, 0.125, base, {2: (1,)})
+    for b in (0, 2, 3):
+        assert (np.abs(f64(w[b]) - ref[b]) <= bound[b] + 2.0 ** -24 * np.abs(ref[b])).all()
+    assert torch.equal(w[1], base[1]) and torch.equal(w[2, :, 16:32], base[2, :, 16:32])
+    for bad in (dict(max_new=29), dict(cu=[9, 29, 25, 69, 74]), dict(cu=[9, 29, 39, 69, 200]), dict(cu=[-1, 29, 39, 69, 74])):
+        w, st = base.clone(), api.new_status()
+        api.paged_attention_weights(wide, i32(bad.get("cu", cu9)), c.k, c.d_table, c.d_ctx, 0.125, w, bad.get("max_new", 60), status=st)
+        torch.cuda.synchronize()
+        assert int(st.item()) == api.LL_DEV_BAD_POSITION
+        assert torch.equal(w[0], base[0]) or bad.get("cu", [0])[0] != -1
+    narrow, st = base[..., :70].contiguous(), api.new_status()
+    api.paged_attention_weights(q, i32(cu), c.k, c.d_table, c.d_ctx, 0.125, narrow, 30, status=st)
+    check_status(st, api.LL_DEV_BAD_POSITION)
+    ref, bound = reference(c, f64(q), cu, 0.125, base[..., :70])
+    assert_weights(narrow, ref, bound)
+    w, st = base.clone(), api.new_status()
+    api.paged_attention_weights(q[:0], i32([0] * 5), c.k, c.d_table, c.d_ctx, 0.125, w, 3, status=st)
+    check_status(st)
+    assert torch.equal(w, base)
+
+
+def test_prompt_streams_and_graphs():
+    case = ([500, 300], [100, 90], 8, 2, 128, 64)
+    c, q, cu, base = prompt(case)
+    cu = i32(cu)
+    want = api.paged_attention_weights(q, cu, c.k, c.d_table, c.d_ctx, 0.1, base.clone(), 100)
+    torch.cuda.synchronize()
+    side, w = torch.cuda.Stream(), base.clone()
+    side.wait_stream(torch.cuda.current_stream())
+    api.paged_attention_weights(q, cu, c.k, c.d_table, c.d_ctx, 0.1, w, 100, stream=side)
+    side.synchronize()
+    assert torch.equal(w, want)
+    w, st = base.clone(), api.new_status()
+    ws = torch.empty(api.attention_weights_workspace_size(2, 190, 100, 8, 2, 128, c.table.shape[1], 64), dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        api.paged_attention_weights(q, cu, c.k, c.d_table, c.d_ctx, 0.1, w, 100, workspace=ws, status=st)
+    graph.replay()
+    check_status(st)
+    assert torch.equal(w, want)

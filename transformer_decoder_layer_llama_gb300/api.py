@@ -51,7 +51,8 @@ EXPORTED = [
     "ll_compact_blocks", "ll_workspace_size_f8", "ll_layer_prefill_f8", "ll_layer_decode_step_f8",
     "ll_norm_rope", "ll_norm_rope_backward_workspace_size", "ll_norm_rope_backward",
     "ll_attention_decode_weights_workspace_size", "ll_paged_attention_decode_weights",
-    "ll_paged_attention_decode_weights_q8", "ll_evict_rows",
+    "ll_paged_attention_decode_weights_q8", "ll_evict_rows", "ll_attention_weights_workspace_size",
+    "ll_paged_attention_weights",
 ]
 
 
@@ -171,6 +172,9 @@ def _load():
                                                              S, P, P]),
         "ll_paged_attention_decode_weights_q8": (ctypes.c_int, [P, ctypes.POINTER(ll_kv_pool_q8), P, I32, P, I32, I32, I32,
                                                                 I32, I32, F32, P, I32, P, P, S, P, P]),
+        "ll_attention_weights_workspace_size": (S, [I32, I32, I32, I32, I32, I32, I32, I32]),
+        "ll_paged_attention_weights": (ctypes.c_int, [P, P, I32, P, I32, P, I32, P, I32, I32, I32, I32, I32, I32, F32, P, I32, P,
+                                                      S, P, P]),
         "ll_evict_rows": (ctypes.c_int, [ctypes.POINTER(ll_row_tensor), I32, I32, I32, I32, P, I32, P, I32, P, I32, P, I32, I32,
                                          I32, P, P, P, P, P]),
         "ll_append_to_cache_f8": (ctypes.c_int, [P, P, I64, I64, P, I32, P, I32, I32, I32, I32, I32, poolf8, P, I32,
@@ -1067,6 +1071,44 @@ def paged_attention_decode_weights_q8(q, pool: PoolQ8, block_table, context_lens
     return _decode_weights("ll_paged_attention_decode_weights_q8", lib.ll_paged_attention_decode_weights_q8, pool.c(),
                            (pool.k, pool.v, pool.k_scale, pool.v_scale), q, block_table, context_lens, scale, weights, out,
                            workspace, status, stream)
+
+
+def attention_weights_workspace_size(batch, tokens, max_new, n_heads, n_kv_heads, head_dim, max_blocks, block_size):
+    return lib.ll_attention_weights_workspace_size(int(batch), int(tokens), int(max_new), int(n_heads), int(n_kv_heads),
+                                                   int(head_dim), int(max_blocks), int(block_size))
+
+
+def paged_attention_weights(q, cu_new, k_pool, block_table, context_lens, scale, weights, max_new, workspace=None, status=None,
+                            stream=None):
+    """ll_paged_attention_weights: adds the attention weights of query rows q BF16 [tokens, n_heads, head_dim] (sequence b's
+    in rows cu_new[b] .. cu_new[b + 1] - 1, at most max_new, at the end of its context; whole prompts, chunks or the last
+    rows) to `weights` (float32 [batch, n_kv_heads, width], in place).  k_pool BF16 [num_blocks, n_kv_heads, block_size,
+    head_dim] already holds the keys.  Returns weights."""
+    given = workspace, status
+    _need(k_pool, "k_pool", torch.bfloat16)
+    if k_pool.dim() != 4:
+        raise ValueError("k_pool must be [num_blocks, n_kv_heads, block_size, head_dim]")
+    nb, Hkv, bs, d = k_pool.shape
+    B = _paged_batch(block_table, context_lens)
+    _need(q, "q", torch.bfloat16)
+    if q.dim() != 3 or q.shape[2] != d:
+        raise ValueError(f"q must be [tokens, n_heads, {d}], got {tuple(q.shape)}")
+    _need(cu_new, "cu_new", torch.int32, shape=(B + 1,))
+    width = _weights(weights, B, Hkv)
+    T, Hq, mb = q.shape[0], q.shape[1], block_table.shape[1]
+    if workspace is None:
+        workspace = torch.empty(max(attention_weights_workspace_size(B, T, max_new, Hq, Hkv, d, mb, bs), 16), dtype=torch.uint8,
+                                device=q.device)
+    else:
+        _need(workspace, "workspace", torch.uint8)
+    status = new_status(q.device) if status is None else _status(status)
+    dev = _on(q, k_pool, cu_new, block_table, context_lens, weights, workspace, status)
+    if stream is not None:
+        _made(stream, dev, *(t if g is None else None for g, t in zip(given, (workspace, status))))
+    _call("ll_paged_attention_weights", lib.ll_paged_attention_weights, dev, stream, q.data_ptr(), cu_new.data_ptr(), T,
+          k_pool.data_ptr(), nb, block_table.data_ptr(), mb, context_lens.data_ptr(), B, int(max_new), Hq, Hkv, d, bs,
+          float(scale), weights.data_ptr(), width, workspace.data_ptr(), workspace.numel(), status.data_ptr())
+    return weights
 
 
 def evict_rows(pool, block_table, context_lens, weights, keep, max_keep=None, sinks=0, recent=0, weights_out=None,

@@ -547,6 +547,53 @@ int ll_paged_attention_prefill_f8(const void* q, const int32_t* cu_new, int32_t 
     return cuda_rc(ll::launch_attn_prefill_f8(a, workspace, static_cast<cudaStream_t>(stream)));
 }
 
+size_t ll_attention_weights_workspace_size(int32_t batch, int32_t tokens, int32_t max_new, int32_t n_heads, int32_t n_kv_heads,
+                                           int32_t head_dim, int32_t max_blocks, int32_t block_size) {
+    if (tokens < 0 || max_new <= 0 || paged_shape(batch, n_heads, n_kv_heads, head_dim, block_size, max_blocks) != LL_OK) return 0;
+    return align_up(std::max<size_t>(1, ll::observe_scratch_bytes(batch, tokens, std::min(max_new, tokens), n_heads, n_kv_heads,
+                                                                  max_blocks, block_size)));
+}
+
+int ll_paged_attention_weights(const void* q, const int32_t* cu_new, int32_t tokens, const void* k_pool, int32_t num_blocks,
+                               const int32_t* block_table, int32_t max_blocks, const int32_t* context_lens, int32_t batch,
+                               int32_t max_new, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim, int32_t block_size,
+                               float scale, float* weights, int32_t weights_width, void* workspace, size_t workspace_bytes,
+                               int32_t* status, void* stream) {
+    ll::clear_last_error();
+    if (!cu_new || !k_pool || num_blocks <= 0 || !block_table || !context_lens || !weights || weights_width <= 0 || !status ||
+        !(scale >= 0.f) || !std::isfinite(scale) || tokens < 0 || max_new <= 0)
+        return LL_ERR_INVALID_ARG;
+    const int rc = paged_shape(batch, n_heads, n_kv_heads, head_dim, block_size, max_blocks);
+    if (rc != LL_OK) return rc;
+    if (!aligned16(k_pool) || (reinterpret_cast<uintptr_t>(weights) & 3u) != 0) return LL_ERR_INVALID_ARG;
+    if (tokens > 0 && (!q || !aligned16(q))) return LL_ERR_INVALID_ARG;
+    // rows of the pool are TMA coordinates
+    if ((int64_t)num_blocks * n_kv_heads * block_size > (1LL << 31) - 1) return LL_ERR_UNSUPPORTED;
+    if (!ll::observe_fits(batch, std::min(max_new, tokens), n_heads, n_kv_heads, max_blocks, block_size)) return LL_ERR_UNSUPPORTED;
+    const size_t need = ll_attention_weights_workspace_size(batch, tokens, max_new, n_heads, n_kv_heads, head_dim, max_blocks, block_size);
+    if (!workspace || workspace_bytes < need || !aligned16(workspace)) return LL_ERR_WORKSPACE;
+    ll::ObserveArgs a{};
+    a.q = static_cast<const __nv_bfloat16*>(q);
+    a.k_pool = static_cast<const __nv_bfloat16*>(k_pool);
+    a.cu_new = cu_new;
+    a.context_lens = context_lens;
+    a.block_table = block_table;
+    a.tokens = tokens;
+    a.batch = batch;
+    a.max_new = std::min(max_new, tokens);
+    a.max_blocks = max_blocks;
+    a.num_blocks = num_blocks;
+    a.block_size = block_size;
+    a.n_heads = n_heads;
+    a.n_kv_heads = n_kv_heads;
+    a.head_dim = head_dim;
+    a.scale = scale;
+    a.weights = weights;
+    a.weights_width = weights_width;
+    a.status = status;
+    return cuda_rc(ll::launch_observe(a, workspace, static_cast<cudaStream_t>(stream)));
+}
+
 int ll_evict_rows(const ll_row_tensor* tensors, int32_t n_tensors, int32_t num_blocks, int32_t n_kv_heads, int32_t block_size,
                   const int32_t* block_table, int32_t max_blocks, const int32_t* context_lens, int32_t batch,
                   const float* weights, int32_t weights_width, const int32_t* keep, int32_t max_keep, int32_t sinks,

@@ -1011,6 +1011,30 @@ bool make_tmap_bf16_sw128(CUtensorMap* m, const void* ptr, uint64_t inner, uint6
     return true;
 }
 
+bool make_tmap_heads_sw128(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t heads, uint64_t tokens, uint32_t box_heads,
+                           uint32_t box_tokens) {
+    auto fn = encode_fn();
+    if (!fn) {
+        set_last_error("cuTensorMapEncodeTiled", "driver entry point not found");
+        return false;
+    }
+    cuuint64_t dims[3] = {inner, heads, tokens};
+    cuuint64_t strides[2] = {inner * 2, inner * heads * 2};
+    cuuint32_t box[3] = {(cuuint32_t)BK, box_heads, box_tokens};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) {
+        char msg[160];
+        snprintf(msg, sizeof(msg), "CUresult %d (heads %llu x %llu x %llu, box %u x %u)", (int)r, (unsigned long long)tokens,
+                 (unsigned long long)heads, (unsigned long long)inner, box_tokens, box_heads);
+        set_last_error("cuTensorMapEncodeTiled", msg);
+        return false;
+    }
+    return true;
+}
+
 bool make_tmap_u8_sw128(CUtensorMap* m, const void* ptr, uint64_t rows, uint32_t box_rows) {
     auto fn = encode_fn();
     if (!fn) {

@@ -99,6 +99,11 @@ cudaError_t launch_gemm(const GemmProblem& p, cudaStream_t stream);
 bool make_tmap_bf16_sw128(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t rows,
                           uint32_t box_rows);
 
+// Tensor map of BF16 heads [tokens, heads, inner] read in boxes of box_tokens x box_heads x 64 elements with the
+// 128-byte swizzle: the heads of a token follow each other as rows of the box.
+bool make_tmap_heads_sw128(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t heads, uint64_t tokens, uint32_t box_heads,
+                           uint32_t box_tokens);
+
 // Tensor map of 128-byte rows of bytes [rows, 128] (an INT8 K/V pool with head_dim
 // 128) read in boxes of box_rows full rows with the 128-byte swizzle.
 bool make_tmap_u8_sw128(CUtensorMap* m, const void* ptr, uint64_t rows, uint32_t box_rows);
@@ -286,6 +291,26 @@ cudaError_t launch_attn_decode_f8(AttnF8Args a, void* workspace, cudaStream_t st
 size_t attn_prefill_f8_scratch_bytes(int head_dim);
 cudaError_t launch_attn_prefill_f8(AttnF8Args a, void* workspace, cudaStream_t stream);
 bool attn_prefill_f8_fits(int batch, int max_new, int n_heads, int n_kv_heads);
+
+// Attention weights of query rows over a BF16 cache (attn_weights_tc.cu).
+struct ObserveArgs {
+    const __nv_bfloat16* q;        // [tokens][n_heads][head_dim]
+    const __nv_bfloat16* k_pool;
+    const int32_t* cu_new;         // [batch + 1]
+    const int32_t* context_lens;
+    const int32_t* block_table;
+    int tokens, batch, max_new, max_blocks, num_blocks, block_size, n_heads, n_kv_heads, head_dim;
+    float scale;
+    float* weights;                // [batch][n_kv_heads][weights_width], added to
+    int weights_width;
+    float* lse;                    // scratch: log2 of a row's softmax denominator [n_kv_heads][tokens][group]
+    float2* part;                  //          (max, sum) of the pieces of a row [..][pieces]
+    int pieces, key_ctas;          // set by the launcher
+    int32_t* status;
+};
+bool observe_fits(int batch, int max_new, int n_heads, int n_kv_heads, int max_blocks, int block_size);
+size_t observe_scratch_bytes(int batch, int tokens, int max_new, int n_heads, int n_kv_heads, int max_blocks, int block_size);
+cudaError_t launch_observe(ObserveArgs a, void* workspace, cudaStream_t stream);
 
 // Which cached rows stay, and their move to the front (evict.cu).
 constexpr int kEvictMaxTensors = 8;
