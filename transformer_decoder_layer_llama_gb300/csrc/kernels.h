@@ -243,10 +243,10 @@ struct NormRopeGradArgs {
     int tokens, n_heads, n_kv_heads, head_dim, rotary_dim, max_position;
     float eps;
     bool interleaved;
-    float* partials;               // scratch [CTAs][2][head_dim]
+    float* partials;               // scratch [kNormGradMaxCtas][head_dim]
     int32_t* status;
 };
-constexpr int kNormGradMaxCtas = 2 * 160;
+constexpr int kNormGradMaxCtas = 4 * 160;   // partial rows of head_dim
 size_t norm_rope_grad_scratch_bytes(int head_dim);
 cudaError_t launch_norm_rope_grad(const NormRopeGradArgs& a, bool f32, cudaStream_t stream);
 

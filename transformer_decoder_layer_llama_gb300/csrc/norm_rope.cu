@@ -17,24 +17,35 @@ namespace ll {
 namespace {
 
 constexpr int kNormThreads = 256;
-constexpr int kNormHeads = 3;          // of a thread, forward
-constexpr int kNormGradHeads = 2;      // of a thread, gradient (x and dy of each)
-constexpr int kNormGradCtasPerSm = 2;
-constexpr int kNormAnyWarps = 4;       // of the gradient's CTA for other shapes
+constexpr int kNormGradThreads = 128;
+constexpr int kNormGradCtasPerSm = 4;
+// Heads of a thread: 48 bytes a column on their way (16384 tokens of 64 + 8 BF16 heads: 105 us with six, 113 with three;
+// of 32 + 8 float32 heads: 103 with three, 109 with six); in the gradient, with x and dy, 32 (4096 tokens of 32 + 8: BF16
+// 37.5 us with four, 41.6 with one; float32 48 with two, 54 with four).
+template <typename T>
+constexpr int kNormHeads = sizeof(T) == 2 ? 6 : 3;
+template <typename T>
+constexpr int kNormGradHeads = sizeof(T) == 2 ? 4 : 2;
+constexpr int kNormAnyWarps = 4;       // of the gradient's CTA for heads that no group holds
 
-// How the threads of a vector kernel share a token's heads: a head is `lanes` threads of a group of W (a power of
-// two), each with two 16-byte columns; a token is `rows` groups, each with up to U heads at a time, in `parts` turns; a
-// CTA has `slots` tokens at a time.
+// How threads share a token's heads: a head is `lanes` threads of a group of W (a power of two), each with two columns
+// of N elements; a token is `rows` groups, each with up to U heads at a time, in `parts` turns; a CTA has `slots` tokens
+// at a time.
 struct HeadSplit {
     int lanes, width, rows, parts, slots, threads;
 };
 
-HeadSplit head_split(int head_dim, int n, int heads, int per_thread) {
+int head_lanes(int head_dim, int rotary_dim, int n, bool interleaved) {
+    const int turned = interleaved ? (rotary_dim + 2 * n - 1) / (2 * n) : (rotary_dim / 2 + n - 1) / n;
+    return turned + (head_dim - rotary_dim + 2 * n - 1) / (2 * n);
+}
+
+HeadSplit head_split(int lanes, int heads, int per_thread, int threads) {
     HeadSplit s;
-    s.lanes = head_dim / (2 * n);
+    s.lanes = lanes;
     s.width = 4;
     while (s.width < s.lanes) s.width *= 2;
-    const int most = kNormThreads / s.width;
+    const int most = threads / s.width;
     s.parts = (heads + per_thread * most - 1) / (per_thread * most);
     s.rows = (heads + per_thread * s.parts - 1) / (per_thread * s.parts);
     s.slots = std::max(1, most / s.rows);
@@ -42,46 +53,105 @@ HeadSplit head_split(int head_dim, int n, int heads, int per_thread) {
     return s;
 }
 
-// A thread's two columns: rotated half-split, they hold the two ends of its pairs; interleaved or behind the rotated
-// part, neighbouring elements.
-template <int N, bool HALF>
+// A thread's two columns, at e0 and e1, of n0 and n1 elements (N each where a head divides into whole columns: VEC):
+// rotated half-split, they hold the two ends of its pairs; interleaved or behind the rotated part, neighbours.
+template <int N, bool HALF, bool VEC>
 struct Columns {
-    int e0, e1;
+    int e0, e1, n0, n1;
     bool turn;
-    LL_DEVINL Columns(int lane, int rotary_dim) {
-        const int first = lane * 2 * N;
-        turn = first < rotary_dim;
-        e0 = HALF && turn ? lane * N : first;
-        e1 = HALF && turn ? e0 + (rotary_dim >> 1) : first + N;
+    LL_DEVINL Columns(int lane, int head_dim, int rotary_dim) {
+        const int half = rotary_dim >> 1, turned = HALF ? (half + N - 1) / N : (rotary_dim + 2 * N - 1) / (2 * N);
+        turn = lane < turned;
+        if (HALF && turn) {
+            e0 = lane * N;
+            e1 = half + e0;
+            n0 = n1 = min(N, half - e0);
+        } else {
+            e0 = turn ? lane * 2 * N : rotary_dim + (lane - turned) * 2 * N;
+            e1 = e0 + N;
+            const int end = turn ? rotary_dim : head_dim;
+            n0 = max(0, min(N, end - e0));
+            n1 = max(0, min(N, end - e1));
+        }
+        if (VEC) n0 = n1 = N;
     }
 };
 
-// Element pairs (2 i, 2 i + 1) of a 16-byte column.
-template <typename T>
-LL_DEVINL void unpack2(const uint4& w, float2 (&v)[Vec<T>::N / 2]) {
-    float f[Vec<T>::N];
-    Vec<T>::unpack(w, f);
-#pragma unroll
-    for (int i = 0; i < Vec<T>::N / 2; ++i) v[i] = make_float2(f[2 * i], f[2 * i + 1]);
-}
-template <typename T>
-LL_DEVINL uint4 pack2(const float2 (&v)[Vec<T>::N / 2]) {
-    float f[Vec<T>::N];
-#pragma unroll
-    for (int i = 0; i < Vec<T>::N / 2; ++i) {
-        f[2 * i] = v[i].x;
-        f[2 * i + 1] = v[i].y;
-    }
-    return Vec<T>::pack(f);
-}
+// N elements of T as they lie in memory.
+template <typename T, int N, bool VEC>
+struct Column {
+    static constexpr int WORDS = VEC ? N * (int)sizeof(T) / 4 : N;
+    uint32_t w[WORDS];
 
-template <int M>
-LL_DEVINL void load2(const float* p, float2 (&v)[M]) {
+    LL_DEVINL void zero() {
 #pragma unroll
-    for (int i = 0; i < M / 2; ++i) {
-        const float4 x = __ldg(reinterpret_cast<const float4*>(p) + i);
-        v[2 * i] = make_float2(x.x, x.y);
-        v[2 * i + 1] = make_float2(x.z, x.w);
+        for (int i = 0; i < WORDS; ++i) w[i] = 0u;
+    }
+    LL_DEVINL void load(const T* p, int n) {
+        if constexpr (VEC && WORDS == 2) {
+            const uint2 x = *reinterpret_cast<const uint2*>(p);
+            w[0] = x.x; w[1] = x.y;
+        } else if constexpr (VEC) {
+#pragma unroll
+            for (int i = 0; i < WORDS / 4; ++i) {
+                const uint4 x = reinterpret_cast<const uint4*>(p)[i];
+                w[4 * i] = x.x; w[4 * i + 1] = x.y; w[4 * i + 2] = x.z; w[4 * i + 3] = x.w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                if constexpr (sizeof(T) == 2) w[i] = i < n ? reinterpret_cast<const unsigned short*>(p)[i] : 0u;
+                else w[i] = i < n ? reinterpret_cast<const uint32_t*>(p)[i] : 0u;
+            }
+        }
+    }
+    LL_DEVINL void unpack(float2 (&v)[N / 2]) const {
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+            if constexpr (sizeof(T) == 4) v[i] = make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+            else if constexpr (VEC) v[i] = make_float2(bf16_lo(w[i]), bf16_hi(w[i]));
+            else v[i] = make_float2(__uint_as_float(w[2 * i] << 16), __uint_as_float(w[2 * i + 1] << 16));
+        }
+    }
+    static LL_DEVINL void store(T* p, const float2 (&v)[N / 2], int n) {
+        if constexpr (VEC) {
+            uint32_t o[WORDS];
+#pragma unroll
+            for (int i = 0; i < N / 2; ++i) {
+                if constexpr (sizeof(T) == 2) {
+                    o[i] = pack_bf16x2(v[i].x, v[i].y);
+                } else {
+                    o[2 * i] = __float_as_uint(v[i].x);
+                    o[2 * i + 1] = __float_as_uint(v[i].y);
+                }
+            }
+            if constexpr (WORDS == 2) *reinterpret_cast<uint2*>(p) = make_uint2(o[0], o[1]);
+            else {
+#pragma unroll
+                for (int i = 0; i < WORDS / 4; ++i)
+                    reinterpret_cast<uint4*>(p)[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (i < n) Vec<T>::put(p + i, i & 1 ? v[i / 2].y : v[i / 2].x);
+        }
+    }
+};
+
+// Gains of a column (0 behind its elements).
+template <int N, bool VEC>
+LL_DEVINL void load_gains(const float* p, int n, float2 (&v)[N / 2]) {
+    if (VEC) {
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i) {
+            const float4 x = __ldg(reinterpret_cast<const float4*>(p) + i);
+            v[2 * i] = make_float2(x.x, x.y);
+            v[2 * i + 1] = make_float2(x.z, x.w);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) v[i] = make_float2(2 * i < n ? __ldg(p + 2 * i) : 0.f, 2 * i + 1 < n ? __ldg(p + 2 * i + 1) : 0.f);
     }
 }
 
@@ -104,15 +174,24 @@ LL_DEVINL int norm_position(const int32_t* positions, int t, int max_position, i
 
 // The (cos, sin) entries of a thread's two columns, as whole pairs of elements: half-split, c[i], s[i] belong to
 // elements 2 i and 2 i + 1 of both columns; interleaved, to pair i of the thread's N, with s = (-sin, sin).
-template <int N, bool HALF>
+template <int N, bool HALF, bool VEC>
 struct Turn {
     static constexpr int M = HALF ? N / 2 : N;
     float2 c[M], s[M];
-    LL_DEVINL void load(const float2* table, int pos, int half, int e0) {
-        const float4* cs = reinterpret_cast<const float4*>(table + (size_t)pos * half + (HALF ? e0 : e0 / 2));
+    LL_DEVINL void load(const float2* table, int pos, int half, const Columns<N, HALF, VEC>& col) {
+        const float2* cs = table + (size_t)pos * half + (HALF ? col.e0 : col.e0 / 2);
 #pragma unroll
         for (int i = 0; i < N / 2; ++i) {               // two pairs of the head at a time
-            const float4 x = __ldg(cs + i);
+            float4 x;
+            if (VEC) {
+                x = __ldg(reinterpret_cast<const float4*>(cs) + i);
+            } else {
+                // pairs 2 i, 2 i + 1 of the thread: of elements in the column (half), or in either column (interleaved)
+                const int have = HALF ? col.n0 : (col.n0 + col.n1) / 2;
+                const float2 a = 2 * i < have ? __ldg(cs + 2 * i) : make_float2(1.f, 0.f);
+                const float2 b = 2 * i + 1 < have ? __ldg(cs + 2 * i + 1) : make_float2(1.f, 0.f);
+                x = make_float4(a.x, a.y, b.x, b.y);
+            }
             if (HALF) {
                 c[i] = make_float2(x.x, x.z);
                 s[i] = make_float2(x.y, x.w);
@@ -128,30 +207,32 @@ struct Turn {
 
 // Forward.  The gains are taken into the factors of the rotation once for a thread's U heads of a token: with a, b
 // the columns of x,  a' = r (a fa + b ga),  b' = r (b fb + a gb)  (interleaved: a' = r (a fa + swapped(a) ga), b' likewise).
-template <typename T, bool HALF, int W>
-__global__ void __launch_bounds__(kNormThreads, 3) norm_rope_vec_kernel(const NormRopeArgs a, const HeadSplit hs, float inv_d) {
-    constexpr int N = Vec<T>::N, P = N / 2, U = kNormHeads;
+template <typename T, int N, bool HALF, int W, bool VEC>
+__global__ void __launch_bounds__(kNormThreads) norm_rope_kernel(const NormRopeArgs a, const HeadSplit hs, float inv_d) {
+    using Col = Column<T, N, VEC>;
+    constexpr int P = N / 2, U = kNormHeads<T>;
     pdl_wait();
     pdl_trigger();
     const int group = threadIdx.x / W, lane = threadIdx.x % W;
     const int slot = group / hs.rows, row = group - slot * hs.rows;
     const int t = blockIdx.x * hs.slots + slot;
     const bool here = slot < hs.slots && t < a.tokens, mine = here && lane < hs.lanes;
-    const Columns<N, HALF> col(lane, a.rotary_dim);
+    const Columns<N, HALF, VEC> col(lane, a.head_dim, a.rotary_dim);
     const int H = a.n_heads + a.n_kv_heads, gap = col.e1 - col.e0;
     const int h0 = blockIdx.y * hs.rows * U + row;
     const int pos_read = here ? a.positions[t] : 0;
     const T* q = static_cast<const T*>(a.q) + (size_t)t * a.q_stride + col.e0;
     const T* k = static_cast<const T*>(a.k) + (size_t)t * a.k_stride + col.e0 - (long long)a.n_heads * a.head_dim;
-    uint4 w0[U], w1[U];
+    Col w0[U], w1[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {                       // (on their way before the position is there)
         const int h = h0 + u * hs.rows;
-        w0[u] = w1[u] = make_uint4(0u, 0u, 0u, 0u);
+        w0[u].zero();
+        w1[u].zero();
         if (mine && h < H) {
             const T* src = (h < a.n_heads ? q : k) + (size_t)h * a.head_dim;
-            w0[u] = *reinterpret_cast<const uint4*>(src);
-            w1[u] = *reinterpret_cast<const uint4*>(src + gap);
+            w0[u].load(src, col.n0);
+            w1[u].load(src + gap, col.n1);
         }
     }
     const bool known = pos_read >= 0 && pos_read < a.max_position;
@@ -159,11 +240,11 @@ __global__ void __launch_bounds__(kNormThreads, 3) norm_rope_vec_kernel(const No
     const bool live = known && mine;                    // (every thread takes part in the shuffles)
     float2 fa[P], ga[P], fb[P], gb[P];
     const auto factors = [&](const float* gain) {
-        load2<P>(gain + col.e0, fa);
-        load2<P>(gain + col.e1, fb);
+        load_gains<N, VEC>(gain + col.e0, col.n0, fa);
+        load_gains<N, VEC>(gain + col.e1, col.n1, fb);
         if (!col.turn) return;
-        Turn<N, HALF> turn;
-        turn.load(a.table, pos_read, a.rotary_dim >> 1, col.e0);
+        Turn<N, HALF, VEC> turn;
+        turn.load(a.table, pos_read, a.rotary_dim >> 1, col);
 #pragma unroll
         for (int i = 0; i < P; ++i) {
             if (HALF) {
@@ -172,7 +253,7 @@ __global__ void __launch_bounds__(kNormThreads, 3) norm_rope_vec_kernel(const No
                 fa[i] = mul2(fa[i], turn.c[i]);
                 fb[i] = mul2(fb[i], turn.c[i]);
             } else {
-                constexpr int M = Turn<N, HALF>::M;
+                constexpr int M = Turn<N, HALF, VEC>::M;
                 ga[i] = mul2(swapped(fa[i]), turn.s[i]);
                 gb[i] = mul2(swapped(fb[i]), turn.s[(P + i) % M]);
                 fa[i] = mul2(fa[i], turn.c[i]);
@@ -188,8 +269,8 @@ __global__ void __launch_bounds__(kNormThreads, 3) norm_rope_vec_kernel(const No
     for (int u = 0; u < U; ++u) {
         const int h = h0 + u * hs.rows;
         float2 x[P], y[P], sum = make_float2(0.f, 0.f);
-        unpack2<T>(w0[u], x);
-        unpack2<T>(w1[u], y);
+        w0[u].unpack(x);
+        w1[u].unpack(y);
 #pragma unroll
         for (int i = 0; i < P; ++i) sum = fma2(y[i], y[i], fma2(x[i], x[i], sum));
         const float total = group_sum<W>(sum.x + sum.y);
@@ -213,8 +294,8 @@ __global__ void __launch_bounds__(kNormThreads, 3) norm_rope_vec_kernel(const No
             }
         }
         T* dst = (isq ? q_out : k_out) + (size_t)h * a.head_dim;
-        *reinterpret_cast<uint4*>(dst) = pack2<T>(x);
-        *reinterpret_cast<uint4*>(dst + gap) = pack2<T>(y);
+        Col::store(dst, x, col.n0);
+        Col::store(dst + gap, y, col.n1);
     }
 }
 
@@ -230,7 +311,7 @@ LL_DEVINL void unit_elements(int u, int rotary_dim, bool interleaved, int& i0, i
     }
 }
 
-// Any even rotary_dim, any element-aligned pointers and strides: a warp per head.
+// Heads that no group of threads holds: a warp per head, two passes over it.
 template <typename T>
 __global__ void __launch_bounds__(kNormThreads) norm_rope_any_kernel(const NormRopeArgs a) {
     using V = Vec<T>;
@@ -284,10 +365,11 @@ struct HeadRows {
 // their way before the first is used, the token's position read a turn ahead.  A thread keeps the gain gradients of its
 // columns over all its tokens.  The sums of a CTA's groups meet in shared memory in a fixed order, those of the CTAs in a
 // second kernel: the same bits every time.
-template <typename T, bool HALF, int W>
-__global__ void __launch_bounds__(kNormThreads, kNormGradCtasPerSm)
-    norm_rope_grad_vec_kernel(const NormRopeGradArgs a, const HeadSplit q_split, const HeadSplit k_split, int q_ctas, float inv_d) {
-    constexpr int N = Vec<T>::N, P = N / 2, U = kNormGradHeads;
+template <typename T, int N, bool HALF, int W, bool VEC>
+__global__ void __launch_bounds__(kNormGradThreads, N == 4 ? kNormGradCtasPerSm : 2)
+    norm_rope_grad_kernel(const NormRopeGradArgs a, const HeadSplit q_split, const HeadSplit k_split, int q_ctas, float inv_d) {
+    using Col = Column<T, N, VEC>;
+    constexpr int P = N / 2, U = kNormGradHeads<T>;
     extern __shared__ float s_dg[];                       // [groups][head_dim]
     pdl_wait();
     pdl_trigger();
@@ -306,7 +388,7 @@ __global__ void __launch_bounds__(kNormThreads, kNormGradCtasPerSm)
     const int parts = isq ? q_split.parts : k_split.parts;
     const int group = threadIdx.x / W, lane = threadIdx.x % W;
     const int slot = group / rows, row = group - slot * rows;
-    const Columns<N, HALF> col(lane, a.rotary_dim);
+    const Columns<N, HALF, VEC> col(lane, a.head_dim, a.rotary_dim);
     const int gap = col.e1 - col.e0;
     const bool worker = slot < slots && lane < q_split.lanes;
     float2 dg0[P], dg1[P];
@@ -325,34 +407,33 @@ __global__ void __launch_bounds__(kNormThreads, kNormGradCtasPerSm)
         const bool live = here && known && worker;
         for (int part = 0; part < parts; ++part) {
             const int h0 = part * rows * U + row;
-            uint4 wx0[U], wx1[U], wy0[U], wy1[U];
+            Col wx0[U], wx1[U], wy0[U], wy1[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int h = h0 + u * rows;
-                wx0[u] = wx1[u] = wy0[u] = wy1[u] = make_uint4(0u, 0u, 0u, 0u);
                 if (live && h < m.heads) {
                     const T* x = m.x + t * m.x_stride + h * a.head_dim + col.e0;
                     const T* dy = m.dy + t * m.dy_stride + h * a.head_dim + col.e0;
-                    wx0[u] = *reinterpret_cast<const uint4*>(x);
-                    wx1[u] = *reinterpret_cast<const uint4*>(x + gap);
-                    wy0[u] = *reinterpret_cast<const uint4*>(dy);
-                    wy1[u] = *reinterpret_cast<const uint4*>(dy + gap);
+                    wx0[u].load(x, col.n0);
+                    wx1[u].load(x + gap, col.n1);
+                    wy0[u].load(dy, col.n0);
+                    wy1[u].load(dy + gap, col.n1);
                 }
             }
-            Turn<N, HALF> turn;
-            if (live && col.turn) turn.load(a.table, pos, a.rotary_dim >> 1, col.e0);
+            Turn<N, HALF, VEC> turn;
+            if (live && col.turn) turn.load(a.table, pos, a.rotary_dim >> 1, col);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int h = h0 + u * rows;
                 const bool on = live && h < m.heads;
                 float2 x0[P], x1[P], y0[P], y1[P], g0[P], g1[P], sq = make_float2(0.f, 0.f), dot = sq;
                 if (on) {
-                    unpack2<T>(wx0[u], x0);
-                    unpack2<T>(wx1[u], x1);
-                    unpack2<T>(wy0[u], y0);
-                    unpack2<T>(wy1[u], y1);
-                    load2<P>(m.gain + col.e0, g0);
-                    load2<P>(m.gain + col.e1, g1);
+                    wx0[u].unpack(x0);
+                    wx1[u].unpack(x1);
+                    wy0[u].unpack(y0);
+                    wy1[u].unpack(y1);
+                    load_gains<N, VEC>(m.gain + col.e0, col.n0, g0);
+                    load_gains<N, VEC>(m.gain + col.e1, col.n1, g1);
 #pragma unroll
                     for (int i = 0; i < P; ++i) {
                         if (col.turn) {                   // dn = R^T dy
@@ -361,7 +442,7 @@ __global__ void __launch_bounds__(kNormThreads, kNormGradCtasPerSm)
                                 y1[i] = fma2(y1[i], turn.c[i], mul2(y0[i], make_float2(-turn.s[i].x, -turn.s[i].y)));
                                 y0[i] = n0;
                             } else {                      // (s swapped is -s)
-                                constexpr int M = Turn<N, HALF>::M;
+                                constexpr int M = Turn<N, HALF, VEC>::M;
                                 y0[i] = fma2(y0[i], turn.c[i], mul2(swapped(y0[i]), swapped(turn.s[i])));
                                 y1[i] = fma2(y1[i], turn.c[(P + i) % M], mul2(swapped(y1[i]), swapped(turn.s[(P + i) % M])));
                             }
@@ -383,18 +464,18 @@ __global__ void __launch_bounds__(kNormThreads, kNormGradCtasPerSm)
                     x1[i] = mul2(fma2(x1[i], both(f), g1[i]), both(r));
                 }
                 T* dst = m.dx + t * m.dx_stride + h * a.head_dim + col.e0;
-                *reinterpret_cast<uint4*>(dst) = pack2<T>(x0);
-                *reinterpret_cast<uint4*>(dst + gap) = pack2<T>(x1);
+                Col::store(dst, x0, col.n0);
+                Col::store(dst + gap, x1, col.n1);
             }
         }
     }
     if (worker) {
-        float2* s0 = reinterpret_cast<float2*>(s_dg + group * a.head_dim + col.e0);
-        float2* s1 = reinterpret_cast<float2*>(s_dg + group * a.head_dim + col.e1);
+        float* s0 = s_dg + group * a.head_dim + col.e0;
+        float* s1 = s_dg + group * a.head_dim + col.e1;
 #pragma unroll
-        for (int i = 0; i < P; ++i) {
-            s0[i] = dg0[i];
-            s1[i] = dg1[i];
+        for (int i = 0; i < N; ++i) {
+            if (i < col.n0) s0[i] = i & 1 ? dg0[i / 2].y : dg0[i / 2].x;
+            if (i < col.n1) s1[i] = i & 1 ? dg1[i / 2].y : dg1[i / 2].x;
         }
     }
     __syncthreads();
@@ -406,7 +487,7 @@ __global__ void __launch_bounds__(kNormThreads, kNormGradCtasPerSm)
     }
 }
 
-// Any shape: a warp per head, the gain gradients of a warp in shared memory (a lane adds to its own elements only).
+// Heads that no group holds: a warp per head, the gain gradients of a warp in shared memory (a lane adds to its own elements only).
 template <typename T>
 __global__ void __launch_bounds__(kNormAnyWarps * 32) norm_rope_grad_any_kernel(const NormRopeGradArgs a) {
     using V = Vec<T>;
@@ -492,41 +573,56 @@ __global__ void __launch_bounds__(1024) norm_rope_gains_kernel(const float* part
     if (lane == 0 && e < head_dim) out[e] = total;
 }
 
-bool rows16(const void* p, long long stride, int esz) {
-    return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && stride * esz % 16 == 0;
+// f(N, W, VEC) with the constants of a call: columns of four elements, of eight where a head then needs more than a warp
+// (and no group for longer heads: a warp takes two passes over each).  Whole, aligned columns take vector loads (4096
+// tokens of 32 + 8 BF16 heads of 128, gradient: 42 us; element by element, 98 of 128 rotated, 111; a warp per head 300).
+// BF16, 16384 tokens of 32 + 8 heads of 128: 64 us with columns of four, 76 with eight (twice the registers).
+struct NormShape {
+    int n, lanes;
+    bool vec;
+};
+
+bool rows_on(const void* p, long long stride, int esz, int bytes) {
+    return reinterpret_cast<uintptr_t>(p) % bytes == 0 && stride * esz % bytes == 0;
 }
 
-// f with the width of a group as a constant.
-template <typename F>
-cudaError_t for_width(int width, F&& f) {
-    switch (width) {
-        case 4: return f(std::integral_constant<int, 4>{});
-        case 8: return f(std::integral_constant<int, 8>{});
-        case 16: return f(std::integral_constant<int, 16>{});
-        default: return f(std::integral_constant<int, 32>{});
+// n 0: a head does not fit a warp.
+NormShape norm_shape(int head_dim, int rotary_dim, bool interleaved) {
+    for (int n : {4, 8}) {
+        const int lanes = head_lanes(head_dim, rotary_dim, n, interleaved);
+        if (lanes <= 32) return {n, lanes, head_dim % (2 * n) == 0 && rotary_dim % (2 * n) == 0};
     }
+    return {0, 0, false};
 }
 
-// 16-byte columns, two to a thread, a head within a warp: every row and the gains start on 16 bytes.
-bool vec_shape(int head_dim, int rotary_dim, int n) {
-    return head_dim % (2 * n) == 0 && rotary_dim % (2 * n) == 0 && head_dim / (2 * n) <= 32;
+template <typename F>
+cudaError_t for_shape(const NormShape& s, F&& f) {
+    const auto with = [&](auto n, auto w) { return s.vec ? f(n, w, std::true_type{}) : f(n, w, std::false_type{}); };
+    using Four = std::integral_constant<int, 4>;
+    if (s.n == 8) return with(std::integral_constant<int, 8>{}, std::integral_constant<int, 32>{});
+    if (s.lanes <= 4) return with(Four{}, std::integral_constant<int, 4>{});
+    if (s.lanes <= 8) return with(Four{}, std::integral_constant<int, 8>{});
+    if (s.lanes <= 16) return with(Four{}, std::integral_constant<int, 16>{});
+    return with(Four{}, std::integral_constant<int, 32>{});
 }
 
 template <typename T>
 cudaError_t norm_rope_for(const NormRopeArgs& a, cudaStream_t stream) {
-    constexpr int N = Vec<T>::N, E = (int)sizeof(T);
+    constexpr int E = (int)sizeof(T);
     const int H = a.n_heads + a.n_kv_heads;
-    const bool vec = vec_shape(a.head_dim, a.rotary_dim, N) &&
-                     (a.n_heads == 0 || (rows16(a.q, a.q_stride, E) && rows16(a.q_out, a.q_out_stride, E) && rows16(a.q_gain, 0, 4))) &&
-                     (a.n_kv_heads == 0 || (rows16(a.k, a.k_stride, E) && rows16(a.k_out, a.k_out_stride, E) && rows16(a.k_gain, 0, 4)));
+    NormShape s = norm_shape(a.head_dim, a.rotary_dim, a.interleaved);
+    const int bytes = std::min(16, s.n * E);
+    s.vec = s.vec &&
+            (a.n_heads == 0 || (rows_on(a.q, a.q_stride, E, bytes) && rows_on(a.q_out, a.q_out_stride, E, bytes) && rows_on(a.q_gain, 0, 4, 16))) &&
+            (a.n_kv_heads == 0 || (rows_on(a.k, a.k_stride, E, bytes) && rows_on(a.k_out, a.k_out_stride, E, bytes) && rows_on(a.k_gain, 0, 4, 16)));
     trace_before("norm_rope", stream);
     cudaError_t e;
-    if (vec) {
-        const HeadSplit hs = head_split(a.head_dim, N, H, kNormHeads);
+    if (s.n) {
+        HeadSplit hs = head_split(s.lanes, H, kNormHeads<T>, kNormThreads);
         const dim3 grid((unsigned)((a.tokens + hs.slots - 1) / hs.slots), (unsigned)hs.parts);
-        e = for_width(hs.width, [&](auto w) {
-            return launch_pdl(a.interleaved ? norm_rope_vec_kernel<T, false, w.value> : norm_rope_vec_kernel<T, true, w.value>, grid,
-                              dim3(hs.threads), 0, stream, 1, a, hs, 1.f / (float)a.head_dim);
+        e = for_shape(s, [&](auto n, auto w, auto vec) {
+            return launch_pdl(a.interleaved ? norm_rope_kernel<T, n.value, false, w.value, vec.value> : norm_rope_kernel<T, n.value, true, w.value, vec.value>,
+                              grid, dim3(hs.threads), 0, stream, 1, a, hs, 1.f / (float)a.head_dim);
         });
     } else {
         const unsigned y = (unsigned)std::min(16, (H + kNormThreads / 32 - 1) / (kNormThreads / 32));
@@ -539,19 +635,21 @@ cudaError_t norm_rope_for(const NormRopeArgs& a, cudaStream_t stream) {
 
 template <typename T>
 cudaError_t norm_rope_grad_for(const NormRopeGradArgs& a, cudaStream_t stream) {
-    constexpr int N = Vec<T>::N, E = (int)sizeof(T);
+    constexpr int E = (int)sizeof(T);
     const int most = std::min(kNormGradMaxCtas, std::max(1, device_sm_count()) * kNormGradCtasPerSm);
-    const bool vec = vec_shape(a.head_dim, a.rotary_dim, N) &&
-                     (a.n_heads == 0 || (rows16(a.q, a.q_stride, E) && rows16(a.dq, a.dq_stride, E) && rows16(a.q_grad, a.q_grad_stride, E) && rows16(a.q_gain, 0, 4))) &&
-                     (a.n_kv_heads == 0 || (rows16(a.k, a.k_stride, E) && rows16(a.dk, a.dk_stride, E) && rows16(a.k_grad, a.k_grad_stride, E) && rows16(a.k_gain, 0, 4)));
+    NormShape s = norm_shape(a.head_dim, a.rotary_dim, a.interleaved);
+    const int bytes = std::min(16, s.n * E);
+    s.vec = s.vec &&
+            (a.n_heads == 0 || (rows_on(a.q, a.q_stride, E, bytes) && rows_on(a.dq, a.dq_stride, E, bytes) && rows_on(a.q_grad, a.q_grad_stride, E, bytes) && rows_on(a.q_gain, 0, 4, 16))) &&
+            (a.n_kv_heads == 0 || (rows_on(a.k, a.k_stride, E, bytes) && rows_on(a.dk, a.dk_stride, E, bytes) && rows_on(a.k_grad, a.k_grad_stride, E, bytes) && rows_on(a.k_gain, 0, 4, 16)));
     int q_rows = 0, k_rows = 0;                           // of partials
     cudaError_t e = cudaSuccess;
     trace_before("norm_rope_grad", stream);
     if (a.tokens == 0) {                                  // the gains' gradients are zeros
-    } else if (vec) {
+    } else if (s.n) {
         // CTAs for q and for k, as many as their tokens ask for, in proportion to their heads up to what runs at once
-        const HeadSplit qs = head_split(a.head_dim, N, std::max(a.n_heads, 1), kNormGradHeads);
-        const HeadSplit ks = head_split(a.head_dim, N, std::max(a.n_kv_heads, 1), kNormGradHeads);
+        const HeadSplit qs = head_split(s.lanes, std::max(a.n_heads, 1), kNormGradHeads<T>, kNormGradThreads);
+        const HeadSplit ks = head_split(s.lanes, std::max(a.n_kv_heads, 1), kNormGradHeads<T>, kNormGradThreads);
         q_rows = a.n_heads ? (a.tokens + qs.slots - 1) / qs.slots : 0;
         k_rows = a.n_kv_heads ? (a.tokens + ks.slots - 1) / ks.slots : 0;
         if (q_rows + k_rows > most) {
@@ -560,14 +658,14 @@ cudaError_t norm_rope_grad_for(const NormRopeGradArgs& a, cudaStream_t stream) {
             q_rows = std::min(q_rows, q_part);
             k_rows = std::min(k_rows, most - q_rows);
         }
-        const size_t smem = (size_t)std::max(qs.slots * qs.rows, ks.slots * ks.rows) * a.head_dim * sizeof(float);   // at most 16 KB
-        e = for_width(qs.width, [&](auto w) {
-            return launch_pdl(a.interleaved ? norm_rope_grad_vec_kernel<T, false, w.value> : norm_rope_grad_vec_kernel<T, true, w.value>,
-                              dim3(q_rows + k_rows), dim3(kNormThreads), smem, stream, 1, a, qs, ks, q_rows, 1.f / (float)a.head_dim);
+        const size_t smem = (size_t)std::max(qs.slots * qs.rows, ks.slots * ks.rows) * a.head_dim * sizeof(float);   // at most 8 KB
+        e = for_shape(s, [&](auto n, auto w, auto vec) {
+            return launch_pdl(a.interleaved ? norm_rope_grad_kernel<T, n.value, false, w.value, vec.value> : norm_rope_grad_kernel<T, n.value, true, w.value, vec.value>,
+                              dim3(q_rows + k_rows), dim3(kNormGradThreads), smem, stream, 1, a, qs, ks, q_rows, 1.f / (float)a.head_dim);
         });
     } else {
         const long long rows = (long long)a.tokens * (a.n_heads + a.n_kv_heads);
-        q_rows = k_rows = (int)std::min<long long>(most, (rows + kNormAnyWarps - 1) / kNormAnyWarps);
+        q_rows = k_rows = (int)std::min<long long>(most / 2, (rows + kNormAnyWarps - 1) / kNormAnyWarps);
         const size_t smem = (size_t)kNormAnyWarps * 2 * a.head_dim * sizeof(float);    // 32 KB at head_dim 1024
         e = launch_pdl(norm_rope_grad_any_kernel<T>, dim3(q_rows), dim3(kNormAnyWarps * 32), smem, stream, 1, a);
     }
@@ -588,7 +686,7 @@ cudaError_t launch_norm_rope(const NormRopeArgs& a, bool f32, cudaStream_t strea
     return f32 ? norm_rope_for<float>(a, stream) : norm_rope_for<__nv_bfloat16>(a, stream);
 }
 
-size_t norm_rope_grad_scratch_bytes(int head_dim) { return (size_t)kNormGradMaxCtas * 2 * head_dim * sizeof(float); }
+size_t norm_rope_grad_scratch_bytes(int head_dim) { return (size_t)kNormGradMaxCtas * head_dim * sizeof(float); }
 
 cudaError_t launch_norm_rope_grad(const NormRopeGradArgs& a, bool f32, cudaStream_t stream) {
     return f32 ? norm_rope_grad_for<float>(a, stream) : norm_rope_grad_for<__nv_bfloat16>(a, stream);
