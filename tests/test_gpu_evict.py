@@ -209,3 +209,38 @@ def test_streams_and_graphs():
     graph.replay()
     check_status(st)
     assert torch.equal(kc, kept) and torch.equal(wa, wc) and all(torch.equal(bits(x), bits(y)) for x, y in zip(a.tensors, c.tensors))
+
+
+def test_rows_of_weights_beyond_shared_memory():
+    """A table so wide that the choice reads the weights from memory again; many heads and sequences, so no clusters."""
+    c = Cache([60000, 70, 1000, 16], 48, 64, 256, 8, spare=150)
+    w = make_weights("spread", 4, 48, c.width, torch.Generator().manual_seed(3))
+    run(c, w, 64, 4, 10)
+
+
+@pytest.mark.parametrize("separate", [False, True])
+def test_one_very_long_row_of_weights(separate):
+    c = Cache([420000], 1, 64, 256, 5, spare=0)
+    w = make_weights("ties", 1, 1, c.width, torch.Generator().manual_seed(3))
+    g = W.keep_rows
+    before = [bits(t).clone() for t in c.tensors]
+    wd, st = w.cuda(), api.new_status()
+    out = torch.zeros_like(wd) if separate else None
+    kept, lens = api.evict_rows(c.pool, c.d_table, c.d_ctx, wd, 5000, sinks=7, recent=11, weights_out=out, status=st)
+    check_status(st)
+    rows = g(w[0, 0, :420000].numpy(), 5000, 7, 11)
+    assert (kept[0, 0].cpu().numpy() == rows).all() and lens.tolist() == [5000]
+    at = np.arange(5000)
+    for t, old in zip(c.tensors, before):
+        assert torch.equal(bits(t)[c.table[0, at // 256], 0, at % 256], old[c.table[0, rows // 256], 0, rows % 256])
+    got = (out if separate else wd)[0, 0].cpu()
+    assert torch.equal(got[:5000], w[0, 0, rows]) and (got[5000:420000] == 0).all()
+
+
+@pytest.mark.parametrize("weights", ["spread", "ties", "zeros", "odd"])
+@pytest.mark.parametrize("ctx,block,keep", [([1024, 1023, 900, 31], 256, 33), ([2048, 2047, 1500, 1025], 256, 1024), ([1008, 640, 32, 64], 16, 640),
+                                            ([2000, 1999, 2], 16, 1998)])
+def test_rows_at_the_size_of_a_warp(ctx, block, keep, weights):
+    """A table as wide as a warp's registers, and one block less."""
+    c = Cache(ctx, 3, 64, block, keep, spare=0)
+    run(c, make_weights(weights, len(ctx), 3, c.width, torch.Generator().manual_seed(keep)), keep, 3, 17)

@@ -318,7 +318,8 @@ struct EvictArgs {
     void* data[kEvictMaxTensors];              // [num_blocks][n_kv_heads][block_size][row_bytes]
     int row_bytes[kEvictMaxTensors];
     bool wide[kEvictMaxTensors];               // rows in pieces of 16 bytes, else 4
-    int slices[kEvictMaxTensors];              // set by the launcher
+    int slices[kEvictMaxTensors];              // set by the launcher, with block_shift
+    int block_shift;
     int n_tensors, num_blocks, n_kv_heads, block_size, max_blocks, batch;
     const int32_t* block_table;
     const int32_t* context_lens;
