@@ -893,14 +893,14 @@ __global__ void attn_decode_combine_kernel(const AttnDecodeArgs a, int max_split
 }
 
 // The outputs, as attn_decode_combine_kernel (blocks x >= spans: one query head of the group each), and the
-// attention weights of 256 E cached tokens per block x < spans:
+// attention weights of 1024 cached tokens per block x < spans:
 //   weights[b][hk][p] += sum over the group's heads of 2^(score_h[p] - lse_h),  lse_h = M + log2 sum_s 2^(m_s - M) l_s.
 // The scores are float32, 4 bytes a query head and key beside the 4 head_dim bytes of a key and KV head, and mostly
 // still in L2 when they are read here.  One kernel for both, so that a step has no launch more than without weights.
-// A thread has E positions and the scores of AHEAD heads on their way at once, before the normalisers are there.
+// A thread has four positions and the scores of AHEAD heads on their way at once, before the normalisers are there.
 constexpr int kFinishThreads = 256;
 
-template <int E, int AHEAD>
+template <int AHEAD>
 __global__ void __launch_bounds__(kFinishThreads) attn_decode_finish_kernel(const AttnDecodeArgs a, int max_splits, int spans) {
     __shared__ float s_lse[16];
     pdl_wait();
@@ -926,28 +926,30 @@ __global__ void __launch_bounds__(kFinishThreads) attn_decode_finish_kernel(cons
         }
         return;
     }
+    constexpr int E = 4;
     const long long span0 = (long long)blockIdx.x * (E * kFinishThreads);
     if (span0 >= ctx) return;
-    const int p0 = (int)span0, p1 = min(ctx, p0 + E * kFinishThreads);
+    const int p1 = (int)min((long long)ctx, span0 + E * kFinishThreads);
     if (p1 > a.weights_width && threadIdx.x == 0) flag_status(a.status, LL_DEV_BAD_POSITION);
     const int end = min(p1, a.weights_width);
-    const float* scores = a.scores + ((size_t)b * a.n_heads + (size_t)hk * G) * a.score_stride;
-    float* weights = a.weights + ((size_t)b * a.n_kv_heads + hk) * a.weights_width;
-    float sum[E], next[AHEAD][E];
-    const auto fetch = [&](int h, float (&v)[E]) {
+    const int p = (int)span0 + E * threadIdx.x;                   // this thread's four; rows of scores are multiples of 16
+    const bool here = p < end;
+    const float* scores = a.scores + ((size_t)b * a.n_heads + (size_t)hk * G) * a.score_stride + p;
+    float* weights = a.weights + ((size_t)b * a.n_kv_heads + hk) * a.weights_width + p;
+    const bool wide = p + E <= end && (reinterpret_cast<uintptr_t>(weights) & 15u) == 0;
+    const float4 none = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+    float4 next[AHEAD], sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const int p = p0 + e * kFinishThreads + threadIdx.x;
-            v[e] = h < G && p < end ? __ldcs(scores + (size_t)h * a.score_stride + p) : -INFINITY;
-        }
-    };
-#pragma unroll
-    for (int e = 0; e < E; ++e) {                                 // the sums so far and the first heads, before the normalisers
-        const int p = p0 + e * kFinishThreads + threadIdx.x;
-        sum[e] = p < end ? weights[p] : 0.f;
+    for (int j = 0; j < AHEAD; ++j)                               // the first heads and the sums so far, before the normalisers
+        next[j] = here && j < G ? __ldcs(reinterpret_cast<const float4*>(scores + (size_t)j * a.score_stride)) : none;
+    if (wide) {
+        sum = *reinterpret_cast<const float4*>(weights);
+    } else {
+        if (p < end) sum.x = weights[0];
+        if (p + 1 < end) sum.y = weights[1];
+        if (p + 2 < end) sum.z = weights[2];
+        if (p + 3 < end) sum.w = weights[3];
     }
-#pragma unroll
-    for (int j = 0; j < AHEAD; ++j) fetch(j, next[j]);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     for (int h = warp; h < G; h += kFinishThreads / 32) {
         const float* ml = a.part_ml + 2 * (first + (size_t)h * max_splits);
@@ -963,22 +965,29 @@ __global__ void __launch_bounds__(kFinishThreads) attn_decode_finish_kernel(cons
         if (lane == 0) s_lse[h] = den == 0.f ? INFINITY : mb + log2f(den);
     }
     __syncthreads();
-    float add[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) add[e] = 0.f;
+    if (!here) return;
+    float4 add = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int h0 = 0; h0 < G; h0 += AHEAD) {
 #pragma unroll
         for (int j = 0; j < AHEAD; ++j) {
-            const float lse = h0 + j < G ? s_lse[h0 + j] : INFINITY;
-#pragma unroll
-            for (int e = 0; e < E; ++e) add[e] += exp2f(next[j][e] - lse);
-            fetch(h0 + AHEAD + j, next[j]);
+            if (h0 + j >= G) break;
+            const float lse = s_lse[h0 + j];
+            add.x += ex2_approx(next[j].x - lse);
+            add.y += ex2_approx(next[j].y - lse);
+            add.z += ex2_approx(next[j].z - lse);
+            add.w += ex2_approx(next[j].w - lse);
+            const int h = h0 + AHEAD + j;
+            if (h < G) next[j] = __ldcs(reinterpret_cast<const float4*>(scores + (size_t)h * a.score_stride));
         }
     }
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        const int p = p0 + e * kFinishThreads + threadIdx.x;
-        if (p < end) weights[p] = sum[e] + add[e];
+    // (scores behind the context, in the last four, are whatever was there: only p < end is written)
+    if (wide) {
+        *reinterpret_cast<float4*>(weights) = make_float4(sum.x + add.x, sum.y + add.y, sum.z + add.z, sum.w + add.w);
+    } else {
+        weights[0] = sum.x + add.x;
+        if (p + 1 < end) weights[1] = sum.y + add.y;
+        if (p + 2 < end) weights[2] = sum.z + add.z;
+        if (p + 3 < end) weights[3] = sum.w + add.w;
     }
 }
 
@@ -988,12 +997,10 @@ cudaError_t launch_join(const AttnDecodeArgs& a, int max_splits, cudaStream_t st
     if (a.weights) {
         trace_before("attn_decode_finish", stream);
         const int G = a.n_heads / a.n_kv_heads;
-        const auto finish = [&](auto kernel, int positions) {
-            const int spans = (int)((a.score_stride + positions * kFinishThreads - 1) / (positions * kFinishThreads));
-            return launch_pdl(kernel, dim3(spans + G, a.n_kv_heads, a.batch), dim3(kFinishThreads), 0, stream, 1, a, max_splits, spans);
-        };
-        e = G == 1 ? finish(attn_decode_finish_kernel<8, 1>, 8) : G == 2 ? finish(attn_decode_finish_kernel<8, 2>, 8) :
-            G <= 4 ? finish(attn_decode_finish_kernel<4, 4>, 4) : finish(attn_decode_finish_kernel<2, 8>, 2);
+        const int spans = (int)((a.score_stride + 4 * kFinishThreads - 1) / (4 * kFinishThreads));
+        const auto kernel = G == 1 ? attn_decode_finish_kernel<1> : G == 2 ? attn_decode_finish_kernel<2> :
+                            G <= 4 ? attn_decode_finish_kernel<4> : attn_decode_finish_kernel<8>;
+        e = launch_pdl(kernel, dim3(spans + G, a.n_kv_heads, a.batch), dim3(kFinishThreads), 0, stream, 1, a, max_splits, spans);
     } else {
         trace_before("attn_decode_combine", stream);
         e = launch_pdl(attn_decode_combine_kernel, dim3(a.n_heads, a.batch), dim3(a.head_dim), 0, stream, 1, a, max_splits);
