@@ -299,10 +299,50 @@ def test_prompt_edges():
     check_status(st, api.LL_DEV_BAD_POSITION)
     ref, bound = reference(c, f64(q), cu, 0.125, base[..., :70])
     assert_weights(narrow, ref, bound)
+    w, st = torch.zeros_like(base), api.new_status()                    # a scale of 0: equal weights
+    api.paged_attention_weights(q, i32(cu), c.k, c.d_table, c.d_ctx, 0.0, w, 30, status=st)
+    check_status(st)
+    for b, n in enumerate(c.ctx):
+        m = case[1][b]
+        want = sum(np.where(np.arange(n) <= n - m + i, 2 / (n - m + i + 1), 0) for i in range(m))
+        assert np.allclose(f64(w[b, :, :n]), want, rtol=1e-5) and (w[b, :, n:] == 0).all()
     w, st = base.clone(), api.new_status()
     api.paged_attention_weights(q[:0], i32([0] * 5), c.k, c.d_table, c.d_ctx, 0.125, w, 3, status=st)
     check_status(st)
     assert torch.equal(w, base)
+
+
+@pytest.mark.parametrize("which", ["a query row", "a key"])
+def test_nan_reaches_what_it_is_a_score_of(which):
+    """A NaN in a row's query: every position that the row sees.  In a key: every position, of every row that sees it."""
+    ctx, new, H, Hkv, d, block = [700], [300], 4, 2, 64, 64
+    for at in (0, 5, 123, 299):
+        c, q, cu, base = prompt((ctx, new, H, Hkv, d, block))
+        if which == "a query row":
+            q[at, 1, 7] = math.nan
+            hit = [0], range(400 + at + 1)                   # its KV head; the positions that it sees
+        else:
+            key = 400 + at
+            c.k[c.table[0, key // block], 1, key % block, 3] = math.nan
+            hit = [1], range(700)                            # rows from `at` on see it, the last of them all
+        w, st = base.clone(), api.new_status()
+        api.paged_attention_weights(q, i32(cu), c.k, c.d_table, c.d_ctx, 0.125, w, 300, status=st)
+        check_status(st)
+        nan = np.zeros(w.shape, dtype=bool)
+        for h in hit[0]:
+            nan[0, h, list(hit[1])] = True
+        assert (np.isnan(f64(w)) == nan).all()
+
+
+def test_prompt_far_below_its_largest_score():
+    """Scores far apart: what is far below the largest adds nothing to speak of, and no noise to the rest."""
+    ctx, new, H, Hkv, d, block = [520], [40], 2, 1, 64, 64
+    c, q, cu, _ = prompt((ctx, new, H, Hkv, d, block))
+    w, st = torch.zeros(1, 1, c.table.shape[1] * block).cuda(), api.new_status()
+    api.paged_attention_weights(q, i32(cu), c.k, c.d_table, c.d_ctx, 40.0, w, 40, status=st)
+    check_status(st)
+    ref, bound = reference(c, f64(q), cu, 40.0, torch.zeros(w.shape))
+    assert_weights(w, ref, bound)
 
 
 def test_prompt_streams_and_graphs():

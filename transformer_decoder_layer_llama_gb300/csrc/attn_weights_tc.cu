@@ -7,33 +7,41 @@
 //         its scores with a running maximum and sum.  Long rows are split into `pieces` and joined by a small kernel.
 //   COLS  128 keys in the lanes, query rows in the columns: a thread has a key, adds 2^(score - lse of the column) and at
 //         the end adds its sum to the weight.  One thread per weight: no atomics, the same bits every time.
-// Both are one kernel: two tiles of 128 rows stay in shared memory (A), tiles of 128 rows stream past them (B), and each
-// streamed tile meets both, which halves the traffic from L2 per score.  Warp 0 loads (TMA), warp 1 issues the MMAs, two
-// groups of four warps take the scores of one A tile each from TMEM, two buffers a tile so that the next product runs
-// beside the exponentials.  Every wait is bounded.
+// Both are one persistent kernel.  Two tiles of 128 rows (A) stay in shared memory while tiles of 256 rows (B) stream past
+// them; each meets both, which halves the traffic from L2 per score, and an MMA of M 128 N 256 takes 160 clocks where two of
+// N 128 take 200 to 300 (operands in shared memory).  A tile's scores fill half of TMEM: while its four warps take their
+// exponentials, the other tile's product runs.  A warp looks up the items ahead of the others, so that the
+// next item's tiles load while the last one's scores are summed.  Every wait is bounded.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
 
 #include "common.cuh"
 #include "kernels.h"
+#include "vec16.cuh"
 
 namespace ll {
 
 namespace {
 
-constexpr int kTile = 128;
-constexpr int kObsThreads = 320;
+constexpr int kTile = 128;               // rows of an A tile
+constexpr int kWide = 256;               // rows of a B tile, and of a pair of A tiles
+constexpr int kObsThreads = 352;         // TMA, MMA, four warps for each A tile's scores, items
+constexpr int kObsItemWarp = 10;
 constexpr float kLog2eObs = 1.4426950408889634f;
-constexpr int kObsPieceTiles = 4;        // at least, of a piece of a row
+constexpr int kObsPieceTiles = 2;        // at least, of a piece of a row (2048 rows of 32 heads: 33 us, 46 with 4)
+constexpr int kObsLoad = 64;             // columns of one load from TMEM (8192 rows of 64 heads over 8: rows 461 us, keys 538; 32: 584, 620)
+constexpr int kObsItems = 4;             // looked up ahead
 
-template <int D, bool ROWS>
+// FEW (COLS only): no sequence has more rows than one B tile, which then stays for all of an item's keys.
+template <int D, bool FEW>
 struct ObsLayout {
-    static constexpr uint32_t TILE = kTile * D * 2;          // [D / 64][128 rows][128 B], 128-byte swizzle
-    static constexpr int A_BUFS = ROWS ? 1 : 2;              // of two tiles
-    static constexpr int STAGES = ROWS ? 4 : 2;
-    static constexpr uint32_t OFF_B = A_BUFS * 2 * TILE;
-    static constexpr uint32_t TOTAL = OFF_B + STAGES * TILE;
+    static constexpr uint32_t A_TILE = kTile * D * 2;        // [D / 64][128 rows][128 B], 128-byte swizzle
+    static constexpr uint32_t B_TILE = kWide * D * 2;        // [D / 64][256 rows][128 B]
+    static constexpr int A_BUFS = FEW ? 2 : 1;               // of two tiles
+    static constexpr int STAGES = FEW ? 1 : 2;
+    static constexpr uint32_t OFF_B = A_BUFS * 2 * A_TILE;
+    static constexpr uint32_t TOTAL = OFF_B + STAGES * B_TILE;
 };
 
 // What a sequence brings: its first query row, their number, the context (0 rows: nothing to do).
@@ -44,10 +52,10 @@ struct ObsSeq {
 LL_DEVINL ObsSeq obs_sequence(const ObserveArgs& a, int b, bool flag) {
     ObsSeq s;
     s.row0 = a.cu_new[b];
-    s.n = a.cu_new[b + 1] - s.row0;
-    s.ctx = a.context_lens[b];
     const long long end = (long long)a.cu_new[b + 1];
-    if (s.row0 < 0 || end < s.row0 || end > a.tokens || s.n > a.max_new || s.ctx < s.n ||
+    s.ctx = a.context_lens[b];
+    s.n = (int)max(-1ll, min(end - s.row0, (long long)a.max_new + 1));
+    if (s.row0 < 0 || s.n < 0 || s.n > a.max_new || end > a.tokens || s.ctx < s.n ||
         (long long)s.ctx > (long long)a.max_blocks * a.block_size) {
         if (flag) flag_status(a.status, LL_DEV_BAD_POSITION);
         s.n = 0;
@@ -55,57 +63,69 @@ LL_DEVINL ObsSeq obs_sequence(const ObserveArgs& a, int b, bool flag) {
     return s;
 }
 
-// The steps of a CTA: groups of two A tiles, and for each the B tiles first .. last - 1.
-template <bool ROWS>
-struct ObsWork {
-    ObsSeq s;
-    int b, hk, G, Tq;                    // heads per KV head, query tokens per tile
+// An item of a CTA: pairs of A tiles, and for each the B tiles first(pair) .. last - 1.
+struct ObsItem {
+    int row0, n, ctx, b, hk;
     int pair, pair_step, pairs;          // A tiles 2 pair and 2 pair + 1, pair += pair_step while below pairs
     int piece, j0, j1;                   // ROWS: key tiles of this piece
-    int nq;                              // COLS: query tiles of the sequence
+    int kind;                            // kObsEnd, kObsWork, or (not handed on) kObsNone, kObsEmpty
+};
+constexpr int kObsEnd = 0, kObsWork = 1, kObsNone = 2, kObsEmpty = 3;
 
-    LL_DEVINL int first(int p) const {
-        if (ROWS) return j0;
-        const int behind = 2 * kTile * p - (s.ctx - s.n);    // tokens of the call before the first key
-        return behind <= 0 ? 0 : behind / Tq;
+template <bool ROWS>
+struct ObsSteps {
+    int first0, Tb, pair_keys, last_;    // COLS: positions before the call's first row, its tokens per B tile
+    LL_DEVINL ObsSteps(const ObsItem& w, int G) {
+        Tb = kWide / G;
+        first0 = ROWS ? w.j0 : w.ctx - w.n;
+        last_ = ROWS ? w.j1 : (w.n + Tb - 1) / Tb;
     }
-    LL_DEVINL int last() const { return ROWS ? j1 : nq; }
+    LL_DEVINL int first(int pair) const {
+        if (ROWS) return first0;
+        const int behind = kWide * pair - first0;            // tokens of the call before the pair's first key
+        return behind <= 0 ? 0 : behind / Tb;
+    }
+    LL_DEVINL int last() const { return last_; }
 };
 
 template <bool ROWS>
-LL_DEVINL bool obs_work(const ObserveArgs& a, ObsWork<ROWS>& w) {
-    w.G = a.n_heads / a.n_kv_heads;
-    w.Tq = kTile / w.G;
-    int idx = blockIdx.x;
-    w.hk = idx % a.n_kv_heads;
+LL_DEVINL ObsItem obs_item(const ObserveArgs& a, long long idx, int G) {
+    ObsItem w;
+    w.kind = kObsNone;
+    w.hk = (int)(idx % a.n_kv_heads);
     idx /= a.n_kv_heads;
-    w.b = idx % a.batch;
-    idx /= a.batch;
-    w.s = obs_sequence(a, w.b, ROWS && threadIdx.x == 0 && w.hk == 0 && idx == 0);
-    if (w.s.n <= 0) return false;
-    w.nq = (w.s.n + w.Tq - 1) / w.Tq;
+    w.b = (int)(idx % a.batch);
+    const int sub = (int)(idx / a.batch);
+    const ObsSeq s = obs_sequence(a, w.b, ROWS && w.hk == 0 && sub == 0);
+    w.row0 = s.row0;
+    w.n = s.n;
+    w.ctx = s.ctx;
+    w.piece = w.j0 = w.j1 = 0;
+    if (s.n <= 0) return w;
     if (ROWS) {
-        w.piece = idx % a.pieces;
-        const int most = (a.max_new + 2 * w.Tq - 1) / (2 * w.Tq);
-        w.pair = most - 1 - idx / a.pieces;                  // the pairs with the most keys first
+        const int Tq = kTile / G;
+        w.piece = sub % a.pieces;
+        const int most = (a.max_new + 2 * Tq - 1) / (2 * Tq);
+        w.pair = most - 1 - sub / a.pieces;                  // the pairs with the most keys first
         w.pairs = w.pair + 1;
         w.pair_step = 1;
-        if (2 * w.pair >= w.nq) return false;
-        const int end = min(w.s.n, (2 * w.pair + 2) * w.Tq);            // tokens of the pair end here
-        const int tiles = (w.s.ctx - w.s.n + end - 1) / kTile + 1;
+        if (w.pair * 2ll * Tq >= s.n) return w;
+        const int end = (int)min((long long)s.n, (w.pair + 1) * 2ll * Tq);     // tokens of the pair end here
+        const int tiles = (s.ctx - s.n + end - 1) / kWide + 1;
         const int len = max(kObsPieceTiles, (tiles + a.pieces - 1) / a.pieces);
         w.j0 = min(tiles, w.piece * len);
         w.j1 = min(tiles, w.j0 + len);
+        w.kind = w.j0 < w.j1 ? kObsWork : kObsEmpty;
     } else {
-        w.pair = idx;
+        w.pair = sub;
         w.pair_step = a.key_ctas;
-        w.pairs = (w.s.ctx + 2 * kTile - 1) / (2 * kTile);
-        if (w.pair >= w.pairs) return false;
+        w.pairs = (s.ctx + kWide - 1) / kWide;
+        w.kind = w.pair < w.pairs ? kObsWork : kObsNone;
     }
-    return true;
+    return w;
 }
 
-// Barrier of a group of four warps, with an OR of `pred` for all its threads.
+// Barrier of the four warps of an A tile, with an OR of `pred` for all its threads.
 LL_DEVINL bool group_bar_any(int id, bool pred) {
     uint32_t r;
     asm volatile(
@@ -125,59 +145,54 @@ LL_DEVINL void tma_load_3d(void* smem_dst, const void* tmap, int32_t c0, int32_t
         : "memory");
 }
 
-template <int D, bool ROWS>
+LL_DEVINL float max3(float a, float b, float c) {          // NaN if there is one
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+LL_DEVINL void add_exp2(float2 x, float2& sum) { sum = add2(sum, make_float2(ex2_approx(x.x), ex2_approx(x.y))); }
+
+// tmQ: boxes of 128 / G tokens (ROWS: A tiles) or 256 / G (COLS: B tiles).
+template <int D, bool ROWS, bool FEW>
 __global__ void __launch_bounds__(kObsThreads, 1)
-    attn_weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK, const ObserveArgs a) {
-    using L = ObsLayout<D, ROWS>;
-    constexpr int STAGES = L::STAGES, ABUFS = L::A_BUFS;
+    attn_weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK, const ObserveArgs a,
+                        long long items) {
+    using L = ObsLayout<D, FEW>;
+    constexpr int STAGES = L::STAGES, ABUFS = L::A_BUFS, LOAD = kObsLoad;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    __shared__ uint64_t a_full[2], a_empty[2], b_full[STAGES], b_empty[STAGES], s_full[2][2], s_empty[2][2], drain;
-    __shared__ __align__(16) float s_lse[2][2][kTile];                     // COLS: [group][step parity][column]
+    __shared__ uint64_t a_full[2], a_empty[2], b_full[2], b_empty[2], s_full[2], s_empty[2], i_full[kObsItems], i_empty[kObsItems], drain;
+    __shared__ __align__(16) float s_lse[2][2][kWide];       // COLS: [tile][step parity][column]
+    __shared__ ObsItem s_item[kObsItems];
     __shared__ uint32_t tmem_base_s;
     __shared__ int abort_s;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int G = a.n_heads / a.n_kv_heads, Tq = (ROWS ? kTile : kWide) / G;      // query tokens per tile
     int32_t* status = a.status;
-    pdl_wait();
-    pdl_trigger();
-    ObsWork<ROWS> w;
-    if (!obs_work<ROWS>(a, w)) return;
-    const int32_t* table = a.block_table + (size_t)w.b * a.max_blocks;
-    const int64_t lse0 = ((int64_t)w.hk * a.tokens + w.s.row0) * w.G;      // this sequence and KV head among the rows of normalisers
-
-    if (ROWS && w.j0 >= w.j1) {                              // nothing left for this piece
-        for (int r = threadIdx.x; r < 2 * w.Tq * w.G; r += kObsThreads) {
-            const int64_t i = (int64_t)2 * w.pair * w.Tq * w.G + r;
-            if (i < (int64_t)w.s.n * w.G) a.part[(lse0 + i) * a.pieces + w.piece] = make_float2(-INFINITY, 0.f);
-        }
-        return;
-    }
-    // COLS with few query tiles: they stay in their stages for all of the CTA's keys
-    const bool resident = !ROWS && w.nq <= STAGES;
-
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&a_full[i], 1);
             mbar_init(&a_empty[i], 1);
-            for (int g = 0; g < 2; ++g) {
-                mbar_init(&s_full[g][i], 1);
-                mbar_init(&s_empty[g][i], 128);
-            }
-        }
-        for (int i = 0; i < STAGES; ++i) {
             mbar_init(&b_full[i], 1);
             mbar_init(&b_empty[i], 1);
+            mbar_init(&s_full[i], 1);
+            mbar_init(&s_empty[i], 128);
+        }
+        for (int i = 0; i < kObsItems; ++i) {
+            mbar_init(&i_full[i], 1);
+            mbar_init(&i_empty[i], 10);                      // TMA, MMA, eight warps
         }
         mbar_init(&drain, 1);
         abort_s = 0;
         fence_mbar_init();
     }
-    if (!ROWS) {                                             // columns behind the tile's last row: zeros, for finite scores
-        const int used = w.Tq * w.G, rows = kTile - used;
+    if (!ROWS) {                                             // columns behind a tile's last row: zeros, for finite scores
+        const int used = Tq * G, rows = kWide - used;
         for (int i = threadIdx.x; i < STAGES * (D / 64) * rows * 8; i += kObsThreads) {
             const int c = i & 7, r = used + (i >> 3) % rows, half = (i >> 3) / rows;     // half: of a stage
-            *reinterpret_cast<uint4*>(smem + L::OFF_B + half * (kTile * 128) + r * 128 + c * 16) = make_uint4(0u, 0u, 0u, 0u);
+            *reinterpret_cast<uint4*>(smem + L::OFF_B + half * (kWide * 128) + r * 128 + c * 16) = make_uint4(0u, 0u, 0u, 0u);
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
@@ -189,122 +204,189 @@ __global__ void __launch_bounds__(kObsThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_base_s;
+    pdl_wait();
+    pdl_trigger();
 
-    if (warp == 0) {
+    // The k-th item of this CTA for a role's warp or thread, and its return.
+    const auto take = [&](int k, ObsItem& w) {
+        if (!mbar_wait_bounded(&i_full[k % kObsItems], (uint32_t)(k / kObsItems) & 1u, &abort_s, status)) return false;
+        w = s_item[k % kObsItems];
+        return w.kind == kObsWork;
+    };
+
+    if (warp == kObsItemWarp) {
+        // ---------------------------------------------------- items: 32 at a time are looked up, those with work handed on
+        int k = 0;
+        bool ok = true;
+        for (long long round = 0; ok; round += 32) {
+            // every other round reversed: a CTA with one of the longest items has one of the shortest next
+            const long long turn = round + lane, idx = turn * gridDim.x + (turn & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+            ObsItem w;
+            w.kind = turn * gridDim.x < items ? kObsNone : kObsEnd;
+            if (idx < items) w = obs_item<ROWS>(a, idx, G);
+            uint32_t todo = __ballot_sync(0xffffffffu, w.kind != kObsNone);
+            if (todo == 0) continue;
+            while (todo && ok) {
+                const int l = __ffs(todo) - 1;
+                todo &= todo - 1;
+                const int kind = __shfl_sync(0xffffffffu, w.kind, l);
+                if (ROWS && kind == kObsEmpty) {             // nothing is left for this piece of the rows
+                    const int pair = __shfl_sync(0xffffffffu, w.pair, l), n = __shfl_sync(0xffffffffu, w.n, l);
+                    const int hk = __shfl_sync(0xffffffffu, w.hk, l), row0 = __shfl_sync(0xffffffffu, w.row0, l);
+                    const int piece = __shfl_sync(0xffffffffu, w.piece, l);
+                    const int64_t lse0 = ((int64_t)hk * a.tokens + row0) * G;
+                    for (int r = lane; r < 2 * Tq * G; r += 32) {
+                        const int64_t i = (int64_t)2 * pair * Tq * G + r;
+                        if (i < (int64_t)n * G) a.part[(lse0 + i) * a.pieces + piece] = make_float2(-INFINITY, 0.f);
+                    }
+                    continue;
+                }
+                const int slot = k % kObsItems;
+                ok = __all_sync(0xffffffffu, mbar_wait_bounded(&i_empty[slot], ((uint32_t)(k / kObsItems) & 1u) ^ 1u, &abort_s, status));
+                if (ok && lane == l) {
+                    s_item[slot] = w;
+                    mbar_arrive(&i_full[slot]);              // (releases the item)
+                }
+                __syncwarp();
+                ++k;
+                if (kind == kObsEnd) ok = false;
+            }
+        }
+    } else if (warp == 0) {
+        // ---------------------------------------------------- TMA: the whole warp, a lane for each box of keys
         if (lane == 0) {
-            // ------------------------------------------------ TMA
             tma_prefetch_desc(&tmQ);
             tma_prefetch_desc(&tmK);
-            const int br = min(a.block_size, kTile);
-            const auto load_queries = [&](uint8_t* dst, int tile, uint64_t* bar) {
-#pragma unroll
-                for (int hh = 0; hh < D / 64; ++hh)
-                    tma_load_3d(dst + hh * (kTile * 128), &tmQ, hh * 64, w.hk * w.G, w.s.row0 + tile * w.Tq, bar);
+        }
+        const int br = min(a.block_size, kTile), boxes = kWide / br;
+        uint32_t a_issued[2] = {0, 0}, b_issued[2] = {0, 0};
+        int g = 0, step = 0;
+        bool ok = true;
+        ObsItem w;
+        for (int k = 0; ok; ++k) {
+            if (!__all_sync(0xffffffffu, take(k, w))) break;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&i_empty[k % kObsItems]);
+            const int32_t* table = a.block_table + (size_t)w.b * a.max_blocks;
+            const ObsSteps<ROWS> steps(w, G);
+            // the block of this lane's box of the 256 keys from key0 on, -1: none to load
+            const auto block = [&](int key0) {
+                const int p = key0 + lane * br;
+                return lane < boxes && p < w.ctx ? table[p / a.block_size] : -1;
             };
-            const uint32_t query_bytes = (uint32_t)(w.Tq * w.G) * D * 2;
-            const auto key_bytes = [&](int tile) {
-                uint32_t bytes = 0;
-                for (int p = tile * kTile; p < tile * kTile + kTile && p < w.s.ctx; p += br) {
-                    const int blk = table[p / a.block_size];
-                    if (blk >= 0 && blk < a.num_blocks) bytes += (uint32_t)(D / 64) * br * 128u;
-                }
-                return bytes;
-            };
-            const auto load_keys = [&](uint8_t* dst, int tile, uint64_t* bar) {
-                for (int p = tile * kTile, sb = 0; p < tile * kTile + kTile && p < w.s.ctx; p += br, ++sb) {
-                    const int blk = table[p / a.block_size];
-                    if (blk < 0 || blk >= a.num_blocks) {
-                        flag_status(status, LL_DEV_BAD_BLOCK);
-                        continue;
-                    }
+            // 256 keys from key0 on: rows 0 .. 255 of a B tile, or of two A tiles
+            const auto load_keys = [&](uint8_t* dst, int key0, int blk, bool split, uint64_t* bar) {
+                const int p = key0 + lane * br, r = lane * br;
+                const bool there = blk >= 0 && blk < a.num_blocks;
+                if (lane < boxes && p < w.ctx && !there) flag_status(status, LL_DEV_BAD_BLOCK);
+                const uint32_t n = __popc(__ballot_sync(0xffffffffu, there));
+                if (lane == 0) mbar_arrive_expect_tx(bar, n * (uint32_t)(D / 64) * br * 128u);
+                __syncwarp();
+                if (there) {
                     const int row = (blk * a.n_kv_heads + w.hk) * a.block_size + p % a.block_size;
+                    uint8_t* to = split ? dst + (r / kTile) * L::A_TILE + (r % kTile) * 128 : dst + r * 128;
 #pragma unroll
                     for (int hh = 0; hh < D / 64; ++hh)
-                        tma_load_2d(dst + hh * (kTile * 128) + sb * br * 128, &tmK, hh * 64, row, bar);
+                        tma_load_2d(to + hh * (split ? kTile : kWide) * 128, &tmK, hh * 64, row, bar);
                 }
             };
-            uint32_t a_issued[2] = {0, 0}, b_issued[STAGES];
-            for (int i = 0; i < STAGES; ++i) b_issued[i] = 0;
-            int g = 0, step = 0;
-            bool ok = true;
+            int ahead = ROWS ? block(w.j0 * kWide) : block(w.pair * kWide);
             for (int pair = w.pair; pair < w.pairs && ok; pair += w.pair_step, ++g) {
                 const int buf = g % ABUFS;
-                if (!mbar_wait_bounded(&a_empty[buf], ((uint32_t)(g / ABUFS) & 1u) ^ 1u, &abort_s, status)) break;
-                uint8_t* dst = smem + buf * 2 * L::TILE;
+                ok = __all_sync(0xffffffffu, mbar_wait_bounded(&a_empty[buf], ((uint32_t)(g / ABUFS) & 1u) ^ 1u, &abort_s, status));
+                if (!ok) break;
+                uint8_t* dst = smem + buf * 2 * L::A_TILE;
                 if (ROWS) {
-                    const bool second = 2 * pair + 1 < w.nq;
-                    mbar_arrive_expect_tx(&a_full[buf], second ? 2 * query_bytes : query_bytes);
-                    load_queries(dst, 2 * pair, &a_full[buf]);
-                    if (second) load_queries(dst + L::TILE, 2 * pair + 1, &a_full[buf]);
+                    const bool second = (2 * pair + 1) * Tq < w.n;
+                    if (lane == 0) {
+                        const uint32_t bytes = (uint32_t)(Tq * G) * D * 2;
+                        mbar_arrive_expect_tx(&a_full[buf], second ? 2 * bytes : bytes);
+                        for (int h = 0; h < (second ? 2 : 1); ++h)
+#pragma unroll
+                            for (int hh = 0; hh < D / 64; ++hh)
+                                tma_load_3d(dst + h * L::A_TILE + hh * (kTile * 128), &tmQ, hh * 64, w.hk * G, w.row0 + (2 * pair + h) * Tq,
+                                            &a_full[buf]);
+                    }
                 } else {
-                    mbar_arrive_expect_tx(&a_full[buf], key_bytes(2 * pair) + key_bytes(2 * pair + 1));
-                    load_keys(dst, 2 * pair, &a_full[buf]);
-                    load_keys(dst + L::TILE, 2 * pair + 1, &a_full[buf]);
+                    const int blk = ahead;
+                    if (pair + w.pair_step < w.pairs) ahead = block((pair + w.pair_step) * kWide);
+                    load_keys(dst, pair * kWide, blk, true, &a_full[buf]);
                 }
                 ++a_issued[buf];
-                if (resident && g > 0) continue;
-                for (int j = w.first(pair); j < w.last(); ++j, ++step) {
-                    const int st = resident ? j : step % STAGES;
-                    if (!resident && !mbar_wait_bounded(&b_empty[st], ((uint32_t)(step / STAGES) & 1u) ^ 1u, &abort_s, status)) {
-                        ok = false;
-                        break;
-                    }
-                    uint8_t* to = smem + L::OFF_B + st * L::TILE;
+                if (FEW && pair != w.pair) continue;         // (the rows are there)
+                for (int j = steps.first(pair); j < steps.last(); ++j, ++step) {
+                    const int st = step % STAGES;
+                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(&b_empty[st], ((uint32_t)(step / STAGES) & 1u) ^ 1u, &abort_s, status));
+                    if (!ok) break;
+                    uint8_t* to = smem + L::OFF_B + st * L::B_TILE;
                     if (ROWS) {
-                        mbar_arrive_expect_tx(&b_full[st], key_bytes(j));
-                        load_keys(to, j, &b_full[st]);
-                    } else {
-                        mbar_arrive_expect_tx(&b_full[st], query_bytes);
-                        load_queries(to, j, &b_full[st]);
+                        const int blk = ahead;
+                        if (j + 1 < steps.last()) ahead = block((j + 1) * kWide);
+                        load_keys(to, j * kWide, blk, false, &b_full[st]);
+                    } else if (lane == 0) {
+                        mbar_arrive_expect_tx(&b_full[st], (uint32_t)(Tq * G) * D * 2);
+#pragma unroll
+                        for (int hh = 0; hh < D / 64; ++hh)
+                            tma_load_3d(to + hh * (kWide * 128), &tmQ, hh * 64, w.hk * G, w.row0 + j * Tq, &b_full[st]);
                     }
                     ++b_issued[st];
                 }
             }
-            if (abort_s) {                                   // wait (bounded) for the copies in flight before the CTA leaves
-                volatile int never = 0;
-                for (int i = 0; i < 2; ++i)
-                    if (a_issued[i]) mbar_wait_bounded(&a_full[i], (a_issued[i] - 1) & 1u, &never, nullptr);
-                for (int i = 0; i < STAGES; ++i)
-                    if (b_issued[i]) mbar_wait_bounded(&b_full[i], (b_issued[i] - 1) & 1u, &never, nullptr);
+        }
+        if (abort_s && lane == 0) {                          // wait (bounded) for the copies in flight before the CTA leaves
+            volatile int never = 0;
+            for (int i = 0; i < 2; ++i) {
+                if (a_issued[i]) mbar_wait_bounded(&a_full[i], (a_issued[i] - 1) & 1u, &never, nullptr);
+                if (b_issued[i]) mbar_wait_bounded(&b_full[i], (b_issued[i] - 1) & 1u, &never, nullptr);
             }
         }
         __syncwarp();
     } else if (warp == 1) {
         if (lane == 0) {
             // ------------------------------------------------ MMA: S[group] = A[group] B^T for every step
-            const uint32_t idesc = umma_idesc_bf16(kTile, kTile);
-            int g = 0, step = 0;
+            const uint32_t idesc = umma_idesc_bf16(kTile, kWide);
+            int g = 0, bstep = 0, step = 0;
             bool ok = true;
-            for (int pair = w.pair; pair < w.pairs && ok; pair += w.pair_step, ++g) {
-                const int buf = g % ABUFS;
-                if (!mbar_wait_bounded(&a_full[buf], (uint32_t)(g / ABUFS) & 1u, &abort_s, status)) break;
-                const uint32_t sa = smem_u32(smem + buf * 2 * L::TILE);
-                for (int j = w.first(pair); j < w.last() && ok; ++j, ++step) {
-                    const int st = resident ? j : step % STAGES;
-                    if (!mbar_wait_bounded(&b_full[st], resident ? 0u : (uint32_t)(step / STAGES) & 1u, &abort_s, status)) {
+            ObsItem w;
+            for (int k = 0; ok && take(k, w); ++k) {
+                mbar_arrive(&i_empty[k % kObsItems]);
+                const ObsSteps<ROWS> steps(w, G);
+                for (int pair = w.pair; pair < w.pairs && ok; pair += w.pair_step, ++g) {
+                    const int buf = g % ABUFS;
+                    if (!mbar_wait_bounded(&a_full[buf], (uint32_t)(g / ABUFS) & 1u, &abort_s, status)) {
                         ok = false;
                         break;
                     }
-                    const uint32_t sb = smem_u32(smem + L::OFF_B + st * L::TILE);
-                    const int par = step & 1;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        if (!mbar_wait_bounded(&s_empty[h][par], ((uint32_t)(step >> 1) & 1u) ^ 1u, &abort_s, status)) {
+                    const uint32_t sa = smem_u32(smem + buf * 2 * L::A_TILE);
+                    for (int j = steps.first(pair); j < steps.last() && ok; ++j, ++step) {
+                        const int st = bstep % STAGES;
+                        if (!mbar_wait_bounded(&b_full[st], (uint32_t)(bstep / STAGES) & 1u, &abort_s, status)) {
                             ok = false;
                             break;
                         }
-                        tc_fence_after();
-                        const uint32_t d = tmem + (uint32_t)(h * 2 + par) * kTile;
+                        const uint32_t sb = smem_u32(smem + L::OFF_B + st * L::B_TILE);
 #pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk) {
-                            const uint32_t off = (uint32_t)(kk >> 2) * (kTile * 128) + (uint32_t)(kk & 3) * 32;
-                            tc_mma_bf16(d, umma_desc_sw128(sa + h * L::TILE + off), umma_desc_sw128(sb + off), idesc, kk > 0 ? 1u : 0u);
+                        for (int h = 0; h < 2; ++h) {
+                            if (!mbar_wait_bounded(&s_empty[h], ((uint32_t)step & 1u) ^ 1u, &abort_s, status)) {
+                                ok = false;
+                                break;
+                            }
+                            tc_fence_after();
+#pragma unroll
+                            for (int kk = 0; kk < D / 16; ++kk) {
+                                const uint32_t in = (uint32_t)(kk & 3) * 32;
+                                tc_mma_bf16(tmem + h * kWide, umma_desc_sw128(sa + h * L::A_TILE + (kk >> 2) * (kTile * 128) + in),
+                                            umma_desc_sw128(sb + (kk >> 2) * (kWide * 128) + in), idesc, kk > 0 ? 1u : 0u);
+                            }
+                            tc_commit(&s_full[h]);
                         }
-                        tc_commit(&s_full[h][par]);
+                        if (!FEW || pair + w.pair_step >= w.pairs) {
+                            tc_commit(&b_empty[st]);
+                            ++bstep;
+                        }
                     }
-                    if (!resident) tc_commit(&b_empty[st]);
+                    tc_commit(&a_empty[buf]);
                 }
-                tc_commit(&a_empty[buf]);
             }
             tc_commit(&drain);
             volatile int never = 0;
@@ -312,120 +394,175 @@ __global__ void __launch_bounds__(kObsThreads, 1)
         }
         __syncwarp();
     } else {
-        // ---------------------------------------------------- the scores of A tile `h` of every group
+        // ---------------------------------------------------- the scores of A tile `h` of every pair
         const int h = (warp - 2) >> 2, r = (warp & 3) * 32 + lane;       // r: TMEM lane = row of the A tile
-        const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-        const float sl2 = a.scale * kLog2eObs;
-        const int before = w.s.ctx - w.s.n;                  // positions before the call's first row
+        const uint32_t scores = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)h * kWide;
+        // (a scale of 0 as the smallest number: masked scores stay -infinity, others are 0 in effect)
+        const float sl2 = a.scale > 0.f ? a.scale * kLog2eObs : __uint_as_float(1u);
         int step = 0;
-        if (ROWS) {
-            const int tile = 2 * w.pair + h, tok = tile * w.Tq + r / w.G;
-            const bool valid = r < w.Tq * w.G && tok < w.s.n;
-            const int pos = valid ? before + tok : -1;
-            const int tile_pos = before + tile * w.Tq;       // the lowest position of the tile's rows
-            float m = -INFINITY, l = 0.f;
+        ObsItem w, nw;
+        bool more = __all_sync(0xffffffffu, take(0, w));
+        if constexpr (ROWS) {
             // which 16-key runs of a key tile have a block, a tile ahead
-            const auto runs = [&](int j) {
-                const int p = j * kTile + (lane & 7) * 16;
-                const int blk = p < w.s.ctx ? table[p / a.block_size] : -1;
+            constexpr uint32_t kRuns = (1u << (LOAD / 16)) - 1u;
+            const auto runs = [&](const ObsItem& w, int j) {
+                const int p = j * kWide + (lane & 15) * 16;
+                const int blk = p < w.ctx ? a.block_table[(size_t)w.b * a.max_blocks + p / a.block_size] : -1;
                 return blk >= 0 && blk < a.num_blocks;
             };
-            bool run_ok = runs(w.j0);
-            for (int j = w.j0; j < w.j1; ++j, ++step) {
-                const uint32_t ok8 = __ballot_sync(0xffffffffu, run_ok) & 0xffu;
-                if (j + 1 < w.j1) run_ok = runs(j + 1);
-                const int par = step & 1, key0 = j * kTile;
-                if (!mbar_wait_bounded(&s_full[h][par], (uint32_t)(step >> 1) & 1u, &abort_s, status)) break;
-                tc_fence_after();
-                const bool plain = ok8 == 0xffu && key0 + kTile - 1 <= tile_pos;       // the same for the whole group
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    float v[64];
-                    tmem_ld64(tmem + lane_base + (uint32_t)(h * 2 + par) * kTile + half * 64, v);
-                    if (half == 1) {
-                        tc_fence_before();
-                        mbar_arrive(&s_empty[h][par]);
+            bool run_ok = more && runs(w, w.j0);
+            for (int k = 0; more; ++k) {
+                const int tok = (2 * w.pair + h) * Tq + r / G, before = w.ctx - w.n;
+                const bool valid = r < Tq * G && tok < w.n;
+                const int pos = valid ? before + tok : -1;
+                // the lowest and highest position of the tile's rows
+                const int tile_lo = before + (2 * w.pair + h) * Tq, tile_hi = before + min(w.n, (2 * w.pair + h + 1) * Tq) - 1;
+                const bool any = (2 * w.pair + h) * Tq < w.n;
+                float m = -INFINITY, l = 0.f;
+                bool next_more = false;
+                for (int j = w.j0; j < w.j1; ++j, ++step) {
+                    const uint32_t ok16 = __ballot_sync(0xffffffffu, run_ok) & 0xffffu;
+                    if (j + 1 < w.j1) {
+                        run_ok = runs(w, j + 1);
+                    } else {                                 // the next item, and what its first tile needs
+                        next_more = __all_sync(0xffffffffu, take(k + 1, nw));
+                        run_ok = next_more && runs(nw, nw.j0);
                     }
-                    if (!plain) {
+                    const int key0 = j * kWide;
+                    if (!mbar_wait_bounded(&s_full[h], (uint32_t)step & 1u, &abort_s, status)) break;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < kWide; c += LOAD) {
+                        const int k0 = key0 + c;
+                        // (the same for the whole tile: nothing to see, or everything)
+                        const bool none = !any || k0 > tile_hi, plain = ((ok16 >> (c / 16)) & kRuns) == kRuns && k0 + LOAD - 1 <= tile_lo;
+                        float v[LOAD];
+                        if (!none) tmem_ld64(scores + c, v);
+                        if (c + LOAD == kWide) {
+                            tc_fence_before();
+                            mbar_arrive(&s_empty[h]);
+                        }
+                        if (none) continue;
+                        if (!plain) {
 #pragma unroll
-                        for (int c = 0; c < 64; ++c)
-                            if (!((ok8 >> (half * 4 + c / 16)) & 1u) || key0 + half * 64 + c > pos) v[c] = -INFINITY;
+                            for (int i = 0; i < LOAD; ++i)
+                                if (!((ok16 >> (c / 16 + i / 16)) & 1u) || k0 + i > pos) v[i] = -INFINITY;
+                        }
+                        float mx[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+                        for (int i = 4; i < LOAD - 4; i += 2) mx[i / 2 & 3] = max3(mx[i / 2 & 3], v[i], v[i + 1]);
+                        const float top = max3(max3(mx[0], mx[1], v[LOAD - 4]), max3(mx[2], mx[3], v[LOAD - 3]), max3(v[LOAD - 2], v[LOAD - 1], v[LOAD - 1])) * sl2;
+                        if (!(top <= m)) {                   // (NaN too: it stays)
+                            l *= ex2_approx(m - top);        // (0 from -infinity)
+                            m = top;
+                        }
+                        const float base = m == -INFINITY ? 0.f : m;
+                        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                        const float2 f = make_float2(sl2, sl2), n = make_float2(-base, -base);
+#pragma unroll
+                        for (int i = 0; i < LOAD; i += 2) {
+                            const float2 e = fma2(make_float2(v[i], v[i + 1]), f, n);
+                            add_exp2(e, sum[i / 2 & 1]);
+                        }
+                        l += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
                     }
-                    float mx[4] = {v[0], v[1], v[2], v[3]};
-#pragma unroll
-                    for (int c = 4; c < 64; ++c) mx[c & 3] = fmaxf(mx[c & 3], v[c]);
-                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
-                    if (top > m) {
-                        l *= ex2_approx(m - top);            // (0 from -infinity)
-                        m = top;
-                    }
-                    const float base = m == -INFINITY ? 0.f : m;
-                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int c = 0; c < 64; ++c) sum[c & 3] += ex2_approx(fmaf(v[c], sl2, -base));
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                 }
-            }
-            if (valid && !abort_s) {
-                const int64_t i = lse0 + (int64_t)tile * w.Tq * w.G + r;
-                if (a.pieces == 1) a.lse[i] = l == 0.f ? INFINITY : m + log2f(l);
-                else a.part[i * a.pieces + w.piece] = make_float2(m, l);
+                if (valid && !abort_s) {
+                    const int64_t i = ((int64_t)w.hk * a.tokens + w.row0) * G + (int64_t)(2 * w.pair + h) * Tq * G + r;
+                    if (a.pieces == 1) a.lse[i] = m == -INFINITY ? INFINITY : m + log2f(l);
+                    else a.part[i * a.pieces + w.piece] = make_float2(m, l);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&i_empty[k % kObsItems]);
+                w = nw;
+                more = next_more;
             }
         } else {
-            // the normaliser of column r of query tile j (+infinity: adds nothing)
-            const auto column = [&](int j) {
-                const int tok = j * w.Tq + r / w.G;
-                return r < w.Tq * w.G && tok < w.s.n ? __ldg(a.lse + lse0 + (int64_t)j * w.Tq * w.G + r) : INFINITY;
+            // the normaliser of column c of query tile j (+infinity: adds nothing)
+            const auto column = [&](const ObsItem& w, int j, int c) {
+                const int tok = j * Tq + c / G;
+                return c < Tq * G && tok < w.n ? __ldg(a.lse + ((int64_t)w.hk * a.tokens + w.row0) * G + (int64_t)j * Tq * G + c) : INFINITY;
             };
-            float* weights = a.weights + ((size_t)w.b * a.n_kv_heads + w.hk) * a.weights_width;
-            float next = column(w.first(w.pair));
+            float next[2];                                   // of the columns r and r + 128, which this thread brings
+            const auto columns = [&](const ObsItem& w, int j) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) next[i] = column(w, j, r + i * 128);
+            };
+            if (more) columns(w, ObsSteps<ROWS>(w, G).first(w.pair));
             bool stop = false;
-            for (int pair = w.pair; pair < w.pairs && !stop; pair += w.pair_step) {
-                const int tile0 = (2 * pair + h) * kTile, key = tile0 + r;
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
-                for (int j = w.first(pair); j < w.last(); ++j, ++step) {
-                    const int par = step & 1;
-                    s_lse[h][par][r] = next;
-                    stop = group_bar_any(2 + h, abort_s != 0);
-                    if (stop) break;
-                    if (j + 1 < w.last()) next = column(j + 1);
-                    else if (pair + w.pair_step < w.pairs) next = column(w.first(pair + w.pair_step));
-                    // (a thread whose wait runs out has set abort_s: all leave at the next barrier)
-                    const bool got = mbar_wait_bounded(&s_full[h][par], (uint32_t)(step >> 1) & 1u, &abort_s, status);
-                    if (!__all_sync(0xffffffffu, got)) continue;
-                    tc_fence_after();
-                    const int tok0 = j * w.Tq;
-                    const bool plain = tok0 + w.Tq <= w.s.n && tile0 + kTile - 1 <= before + tok0;
-                    // columns from `lo` on see this key, up to the sequence's last row
-                    const int lo = max(0, key - before - tok0) * w.G, hi = min(w.Tq, w.s.n - tok0) * w.G;
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        float v[64];
-                        tmem_ld64(tmem + lane_base + (uint32_t)(h * 2 + par) * kTile + half * 64, v);
-                        if (half == 1) {
-                            tc_fence_before();
-                            mbar_arrive(&s_empty[h][par]);
+            for (int k = 0; more && !stop; ++k) {
+                const ObsSteps<ROWS> steps(w, G);
+                const int before = w.ctx - w.n;
+                float* weights = a.weights + ((size_t)w.b * a.n_kv_heads + w.hk) * a.weights_width;
+                bool next_more = false;
+                for (int pair = w.pair; pair < w.pairs && !stop; pair += w.pair_step) {
+                    const int tile0 = (2 * pair + h) * kTile, key = tile0 + r;
+                    // the weight so far, and whether its key has a block, on their way beside the first scores
+                    const bool in = key < w.ctx, wide = key < a.weights_width;
+                    const int blk = in ? a.block_table[(size_t)w.b * a.max_blocks + key / a.block_size] : -1;
+                    const float so_far = in && wide ? weights[key] : 0.f;
+                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                    for (int j = steps.first(pair); j < steps.last(); ++j, ++step) {
+                        float* lse = s_lse[h][step & 1];
+                        lse[r] = -next[0];
+                        lse[r + 128] = -next[1];
+                        // (a thread whose wait has run out has set abort_s: all leave here)
+                        stop = group_bar_any(2 + h, abort_s != 0);
+                        if (stop) break;
+                        const bool last_step = j + 1 == steps.last(), last_pair = pair + w.pair_step >= w.pairs;
+                        if (last_step && last_pair) {        // the next item, and what its first step needs
+                            next_more = __all_sync(0xffffffffu, take(k + 1, nw));
+                            if (next_more) columns(nw, ObsSteps<ROWS>(nw, G).first(nw.pair));
+                        } else {
+                            columns(w, last_step ? steps.first(pair + w.pair_step) : j + 1);
                         }
-                        const float4* lse = reinterpret_cast<const float4*>(&s_lse[h][par][half * 64]);
-#pragma unroll
-                        for (int c = 0; c < 64; c += 4) {
-                            const float4 n = lse[c / 4];
-                            float e[4] = {fmaf(v[c], sl2, -n.x), fmaf(v[c + 1], sl2, -n.y), fmaf(v[c + 2], sl2, -n.z), fmaf(v[c + 3], sl2, -n.w)};
-                            if (!plain) {
-#pragma unroll
-                                for (int i = 0; i < 4; ++i)
-                                    if (half * 64 + c + i < lo || half * 64 + c + i >= hi) e[i] = -INFINITY;
+                        const bool got = mbar_wait_bounded(&s_full[h], (uint32_t)step & 1u, &abort_s, status);
+                        if (!__all_sync(0xffffffffu, got)) continue;
+                        tc_fence_after();
+                        const int tok0 = j * Tq, full_to = min(Tq, w.n - tok0) * G;      // columns with a row
+                        // columns from `lo` on see this key; all of the tile's keys from `all` on, any from `some` on
+                        const int lo = max(0, key - before - tok0) * G;
+                        const int some = max(0, tile0 - before - tok0) * G, all = max(0, tile0 + kTile - 1 - before - tok0) * G;
+#pragma unroll 1
+                        for (int c = 0; c < kWide; c += LOAD) {
+                            const bool none = c >= full_to || c + LOAD <= some || tile0 >= w.ctx;
+                            const bool plain = c >= all && (c + LOAD <= full_to || full_to == Tq * G);
+                            float v[LOAD];
+                            if (!none) tmem_ld64(scores + c, v);
+                            if (c + LOAD == kWide) {
+                                tc_fence_before();
+                                mbar_arrive(&s_empty[h]);
                             }
+                            if (none) continue;
+                            const float4* n4 = reinterpret_cast<const float4*>(lse + c);      // (negated)
+                            const float2 f = make_float2(sl2, sl2);
+                            if (plain) {
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) sum[i] += ex2_approx(e[i]);
+                                for (int i = 0; i < LOAD; i += 4) {
+                                    const float4 n = n4[i / 4];
+                                    add_exp2(fma2(make_float2(v[i], v[i + 1]), f, make_float2(n.x, n.y)), sum[0]);
+                                    add_exp2(fma2(make_float2(v[i + 2], v[i + 3]), f, make_float2(n.z, n.w)), sum[1]);
+                                }
+                            } else {                         // (masked behind the product: the normaliser may be NaN)
+#pragma unroll
+                                for (int i = 0; i < LOAD; ++i) {
+                                    const float e = fmaf(v[i], sl2, reinterpret_cast<const float*>(n4)[i]);
+                                    sum[0].x += ex2_approx(c + i < lo || c + i >= full_to ? -INFINITY : e);
+                                }
+                            }
                         }
                     }
+                    if (stop) break;
+                    const float total = (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
+                    if (in) {
+                        if (!wide) flag_status(status, LL_DEV_BAD_POSITION);
+                        else if (blk >= 0 && blk < a.num_blocks) weights[key] = so_far + total;
+                    }
                 }
-                if (!stop && key < w.s.ctx) {
-                    const int blk = table[key / a.block_size];
-                    if (key >= a.weights_width) flag_status(status, LL_DEV_BAD_POSITION);
-                    else if (blk >= 0 && blk < a.num_blocks) weights[key] += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&i_empty[k % kObsItems]);
+                w = nw;
+                more = next_more;
             }
         }
     }
@@ -441,37 +578,60 @@ __global__ void __launch_bounds__(256) attn_weights_join_kernel(const float2* pa
     const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
     if (i >= rows) return;
     float M = -INFINITY, den = 0.f;
-    for (int p = 0; p < pieces; ++p) M = fmaxf(M, part[i * pieces + p].x);
+    for (int p = 0; p < pieces; ++p) M = max3(M, part[i * pieces + p].x, part[i * pieces + p].x);
     const float base = M == -INFINITY ? 0.f : M;
     for (int p = 0; p < pieces; ++p) {
         const float2 x = part[i * pieces + p];
         den += exp2f(x.x - base) * x.y;
     }
-    lse[i] = den == 0.f ? INFINITY : base + log2f(den);
+    lse[i] = M == -INFINITY ? INFINITY : base + log2f(den);
+}
+
+// Pieces of a row and parts of a KV head's keys: a few items per SM where the batch alone gives fewer.
+struct ObsSplit {
+    long long row_items, key_items;
+    int pieces, key_ctas;
+};
+
+ObsSplit obs_split(int batch, int max_new, int n_heads, int n_kv_heads, int max_blocks, int block_size) {
+    constexpr int kRowItems = 4 * 152, kKeyItems = 6 * 152;
+    const long long Tq = kTile / (n_heads / n_kv_heads), bh = (long long)batch * n_kv_heads;
+    const long long items = (max_new + 2 * Tq - 1) / (2 * Tq) * bh;
+    const long long tiles = ((long long)max_blocks * block_size + kWide - 1) / kWide;
+    ObsSplit s;
+    s.pieces = (int)std::max<long long>(1, std::min<long long>({16, (kRowItems + items - 1) / items, (tiles + kObsPieceTiles - 1) / kObsPieceTiles}));
+    s.key_ctas = (int)std::max<long long>(1, std::min<long long>((kKeyItems + bh - 1) / bh, tiles));
+    s.row_items = items * s.pieces;
+    s.key_items = bh * s.key_ctas;
+    return s;
+}
+
+template <int D, bool ROWS, bool FEW>
+cudaError_t launch_pass(const ObserveArgs& a, const CUtensorMap& tmK, long long items, cudaStream_t stream) {
+    const int G = a.n_heads / a.n_kv_heads;
+    CUtensorMap tmQ;
+    if (!make_tmap_heads_sw128(&tmQ, a.q, D, (uint64_t)a.n_heads, (uint64_t)a.tokens, (uint32_t)G, (uint32_t)((ROWS ? kTile : kWide) / G)))
+        return cudaErrorInvalidValue;
+    const auto kernel = attn_weights_kernel<D, ROWS, FEW>;
+    const size_t smem = ObsLayout<D, FEW>::TOTAL + 1024;
+    cudaError_t e = ensure_func_attr((const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem,
+                                     "cudaFuncSetAttribute(attn_weights_kernel)");
+    if (e != cudaSuccess) return e;
+    const unsigned grid = (unsigned)std::min<long long>(items, std::max(1, device_sm_count()));
+    trace_before(ROWS ? "attn_weights_rows" : "attn_weights_cols", stream);
+    e = launch_pdl(kernel, dim3(grid), dim3(kObsThreads), smem, stream, 1, tmQ, tmK, a, items);
+    trace_after(stream);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    return record(e, "attn_weights_kernel launch");
 }
 
 template <int D>
-cudaError_t observe_for(const ObserveArgs& a, cudaStream_t stream) {
-    CUtensorMap tmQ, tmK;
-    const int G = a.n_heads / a.n_kv_heads, Tq = kTile / G;
+cudaError_t observe_for(const ObserveArgs& a, const ObsSplit& s, cudaStream_t stream) {
+    CUtensorMap tmK;
     const uint64_t rows = (uint64_t)a.num_blocks * a.n_kv_heads * a.block_size;
-    if (!make_tmap_bf16_sw128(&tmK, a.k_pool, D, rows, (uint32_t)std::min(a.block_size, kTile)) ||
-        !make_tmap_heads_sw128(&tmQ, a.q, D, (uint64_t)a.n_heads, (uint64_t)a.tokens, (uint32_t)G, (uint32_t)Tq))
-        return cudaErrorInvalidValue;
-    const size_t smem_rows = ObsLayout<D, true>::TOTAL + 1024, smem_cols = ObsLayout<D, false>::TOTAL + 1024;
-    cudaError_t e = ensure_func_attr((const void*)attn_weights_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     (int)smem_rows, "cudaFuncSetAttribute(attn_weights_kernel)");
-    if (e == cudaSuccess)
-        e = ensure_func_attr((const void*)attn_weights_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)smem_cols, "cudaFuncSetAttribute(attn_weights_kernel)");
+    if (!make_tmap_bf16_sw128(&tmK, a.k_pool, D, rows, (uint32_t)std::min(a.block_size, kTile))) return cudaErrorInvalidValue;
+    cudaError_t e = launch_pass<D, true, false>(a, tmK, s.row_items, stream);
     if (e != cudaSuccess) return e;
-    const int pairs = (a.max_new + 2 * Tq - 1) / (2 * Tq);
-    trace_before("attn_weights_rows", stream);
-    e = launch_pdl(attn_weights_kernel<D, true>, dim3((unsigned)((long long)pairs * a.pieces * a.batch * a.n_kv_heads)), dim3(kObsThreads),
-                   smem_rows, stream, 1, tmQ, tmK, a);
-    trace_after(stream);
-    if (e == cudaSuccess) e = cudaGetLastError();
-    if (e != cudaSuccess) return record(e, "attn_weights_kernel launch");
     if (a.pieces > 1) {
         const long long n = (long long)a.tokens * a.n_heads;
         trace_before("attn_weights_join", stream);
@@ -481,31 +641,9 @@ cudaError_t observe_for(const ObserveArgs& a, cudaStream_t stream) {
         if (e == cudaSuccess) e = cudaGetLastError();
         if (e != cudaSuccess) return record(e, "attn_weights_join launch");
     }
-    trace_before("attn_weights_cols", stream);
-    e = launch_pdl(attn_weights_kernel<D, false>, dim3((unsigned)((long long)a.key_ctas * a.batch * a.n_kv_heads)), dim3(kObsThreads),
-                   smem_cols, stream, 1, tmQ, tmK, a);
-    trace_after(stream);
-    if (e == cudaSuccess) e = cudaGetLastError();
-    return record(e, "attn_weights_kernel launch");
-}
-
-// Pieces of a row and CTAs of a KV head's keys: about four CTAs per SM where the batch alone gives fewer.
-struct ObsSplit {
-    long long row_items, key_items;      // CTAs of the two passes
-    int pieces, key_ctas;
-};
-
-ObsSplit obs_split(int batch, int max_new, int n_heads, int n_kv_heads, int max_blocks, int block_size) {
-    constexpr int kCtas = 4 * 152;
-    const long long Tq = kTile / (n_heads / n_kv_heads), bh = (long long)batch * n_kv_heads;
-    const long long items = (max_new + 2 * Tq - 1) / (2 * Tq) * bh;
-    const long long tiles = ((long long)max_blocks * block_size + kTile - 1) / kTile;
-    ObsSplit s;
-    s.pieces = (int)std::max<long long>(1, std::min<long long>({16, (kCtas + items - 1) / items, (tiles + kObsPieceTiles - 1) / kObsPieceTiles}));
-    s.key_ctas = (int)std::max<long long>(1, std::min<long long>((kCtas + bh - 1) / bh, (tiles + 1) / 2));
-    s.row_items = items * s.pieces;
-    s.key_items = bh * s.key_ctas;
-    return s;
+    // rows of one B tile at most: they stay, and the keys' tiles are the ones with two buffers
+    return a.max_new <= kWide / (a.n_heads / a.n_kv_heads) ? launch_pass<D, false, true>(a, tmK, s.key_items, stream)
+                                                           : launch_pass<D, false, false>(a, tmK, s.key_items, stream);
 }
 
 }  // namespace
@@ -529,7 +667,7 @@ cudaError_t launch_observe(ObserveArgs a, void* workspace, cudaStream_t stream) 
     a.key_ctas = s.key_ctas;
     a.lse = static_cast<float*>(workspace);
     a.part = reinterpret_cast<float2*>(static_cast<char*>(workspace) + ((size_t)a.tokens * a.n_heads * 4 + 15) / 16 * 16);
-    return a.head_dim == 128 ? observe_for<128>(a, stream) : observe_for<64>(a, stream);
+    return a.head_dim == 128 ? observe_for<128>(a, s, stream) : observe_for<64>(a, s, stream);
 }
 
 }  // namespace ll
