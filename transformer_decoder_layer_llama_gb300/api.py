@@ -720,15 +720,19 @@ def _norm_args(q, k, q_gain, k_gain, positions, table, layout, name):
         raise TypeError("q and k must be bfloat16 or float32 tensors")
     if layout not in LL_ROPE_LAYOUTS:
         raise ValueError(f"layout must be one of {sorted(LL_ROPE_LAYOUTS)}, got {layout!r}")
-    if torch.is_grad_enabled() and any(getattr(t, "requires_grad", False) for t in (q, k, q_gain, k_gain)):
-        raise ValueError(f"{name} is not recorded by autograd: use torch.no_grad(), and norm_rope_backward for the gradient")
+    if torch.is_grad_enabled():
+        for t in (q, k, q_gain, k_gain):
+            if t is not None and t.requires_grad:
+                raise ValueError(f"{name} is not recorded by autograd: use torch.no_grad(), and norm_rope_backward for "
+                                 "the gradient")
     qh, kh = _heads(q, "q", x.dtype), _heads(k, "k", x.dtype)
     T, _, d = x.shape
-    if k is not None and (k.shape[0] != T or k.shape[2] != d):
-        raise ValueError(f"k must be [{T}, n_kv_heads, {d}], got {tuple(k.shape)}")
-    for t, gain, n in ((q, q_gain, "q_gain"), (k, k_gain, "k_gain")):
-        if t is not None:
-            _need(gain, n, torch.float32, shape=(d,))
+    if q is not None:
+        _need(q_gain, "q_gain", torch.float32, shape=(d,))
+    if k is not None:
+        if k.shape[0] != T or k.shape[2] != d:
+            raise ValueError(f"k must be [{T}, n_kv_heads, {d}], got {tuple(k.shape)}")
+        _need(k_gain, "k_gain", torch.float32, shape=(d,))
     _need(positions, "positions", torch.int32, shape=(T,))
     _need(table, "table", torch.float32)
     rows = table.shape
@@ -737,9 +741,15 @@ def _norm_args(q, k, q_gain, k_gain, positions, table, layout, name):
     return x.dtype, T, d, qh, kh
 
 
-def _like(t, out):
-    """`out`, or a new contiguous tensor of t's shape; None for None."""
-    return out if out is not None or t is None else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+def _head_out(t, out, name):
+    """(`out`, or a new contiguous tensor of t's shape, and its ll_head_rows); None for None."""
+    if t is None:
+        return None, ll_head_rows(None, 0, 0)
+    if out is not None:
+        return out, _heads(out, name, t.dtype, t.shape)
+    shape = t.shape
+    out = torch.empty(shape, dtype=t.dtype, device=t.device)
+    return out, ll_head_rows(out.data_ptr(), shape[1] * shape[2], shape[1])
 
 
 def norm_rope(q, k, q_gain, k_gain, positions, table, eps=1e-5, layout="half", q_out=None, k_out=None, status=None,
@@ -750,20 +760,22 @@ def norm_rope(q, k, q_gain, k_gain, positions, table, eps=1e-5, layout="half", q
     Not recorded by autograd: norm_rope_backward is the gradient.  Returns (q_out, k_out)."""
     dtype, T, d, qh, kh = _norm_args(q, k, q_gain, k_gain, positions, table, layout, "norm_rope")
     given = q_out, k_out, status
-    q_out, k_out = _like(q, q_out), _like(k, k_out)
-    qo = _heads(q_out, "q_out", dtype, q.shape) if q is not None else ll_head_rows(None, 0, 0)
-    ko = _heads(k_out, "k_out", dtype, k.shape) if k is not None else ll_head_rows(None, 0, 0)
+    q_out, qo = _head_out(q, q_out, "q_out")
+    k_out, ko = _head_out(k, k_out, "k_out")
     x = q if q is not None else k
     status = new_status(x.device) if status is None else _status(status)
-    dev = _on(x, k, q_out, k_out, q_gain if q is not None else None, k_gain if k is not None else None, positions, table,
-              status)
+    if q is None:
+        q_gain = None
+    if k is None:
+        k_gain = None
+    dev = _on(x, k, q_out, k_out, q_gain, k_gain, positions, table, status)
     if stream is not None:
         _made(stream, dev, *(t if g is None else None for g, t in zip(given, (q_out, k_out, status))))
-    _call("ll_norm_rope", lib.ll_norm_rope, dev, stream, qh, kh, LL_F32 if dtype == torch.float32 else LL_BF16,
+    _call("ll_norm_rope", lib.ll_norm_rope, dev, stream, qh, kh, LL_F32 if dtype is torch.float32 else LL_BF16,
           q_gain.data_ptr() if q is not None else None, k_gain.data_ptr() if k is not None else None, eps,
           positions.data_ptr(), T, d, 2 * table.shape[1], LL_ROPE_LAYOUTS[layout], table.data_ptr(), table.shape[0], qo, ko,
           status.data_ptr())
-    return (q_out if q is not None else None), (k_out if k is not None else None)
+    return q_out, k_out
 
 
 def norm_rope_backward_workspace_size(head_dim: int) -> int:
@@ -779,21 +791,22 @@ def norm_rope_backward(dq, dk, q, k, q_gain, k_gain, positions, table, eps=1e-5,
     if (dq is None) != (q is None) or (dk is None) != (k is None):
         raise ValueError("dq and dk go with q and k")
     given = q_grad, k_grad, q_gain_grad, k_gain_grad, workspace, status
-    none = ll_head_rows(None, 0, 0)
     x = q if q is not None else k
+    dqh = _heads(dq, "dq", dtype, q.shape if q is not None else None)
+    dkh = _heads(dk, "dk", dtype, k.shape if k is not None else None)
+    q_grad, qo = _head_out(q, q_grad, "q_grad")
+    k_grad, ko = _head_out(k, k_grad, "k_grad")
     if q is None:
-        q_grad = q_gain_grad = q_gain = None
-        dqh = qo = none
+        q_gain = q_gain_grad = None
+    elif q_gain_grad is None:
+        q_gain_grad = torch.empty((d,), dtype=torch.float32, device=x.device)
     else:
-        q_grad, q_gain_grad = _like(q, q_grad), _like(q_gain, q_gain_grad)
-        dqh, qo = _heads(dq, "dq", dtype, q.shape), _heads(q_grad, "q_grad", dtype, q.shape)
         _need(q_gain_grad, "q_gain_grad", torch.float32, shape=(d,))
     if k is None:
-        k_grad = k_gain_grad = k_gain = None
-        dkh = ko = none
+        k_gain = k_gain_grad = None
+    elif k_gain_grad is None:
+        k_gain_grad = torch.empty((d,), dtype=torch.float32, device=x.device)
     else:
-        k_grad, k_gain_grad = _like(k, k_grad), _like(k_gain, k_gain_grad)
-        dkh, ko = _heads(dk, "dk", dtype, k.shape), _heads(k_grad, "k_grad", dtype, k.shape)
         _need(k_gain_grad, "k_gain_grad", torch.float32, shape=(d,))
     if workspace is None:
         workspace = torch.empty(max(norm_rope_backward_workspace_size(d), 16), dtype=torch.uint8, device=x.device)
@@ -805,7 +818,7 @@ def norm_rope_backward(dq, dk, q, k, q_gain, k_gain, positions, table, eps=1e-5,
     if stream is not None:
         _made(stream, dev, *(t if g is None else None for g, t in zip(given, (*outs, workspace, status))))
     _call("ll_norm_rope_backward", lib.ll_norm_rope_backward, dev, stream, dqh, dkh, qh, kh,
-          LL_F32 if dtype == torch.float32 else LL_BF16, q_gain.data_ptr() if q is not None else None,
+          LL_F32 if dtype is torch.float32 else LL_BF16, q_gain.data_ptr() if q is not None else None,
           k_gain.data_ptr() if k is not None else None, eps, positions.data_ptr(), T, d, 2 * table.shape[1],
           LL_ROPE_LAYOUTS[layout], table.data_ptr(), table.shape[0], qo, ko,
           q_gain_grad.data_ptr() if q is not None else None, k_gain_grad.data_ptr() if k is not None else None,
