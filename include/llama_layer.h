@@ -585,6 +585,25 @@ int ll_paged_attention_weights(const void* q, const int32_t* cu_new, int32_t tok
                                float scale, float* weights, int32_t weights_width, void* workspace, size_t workspace_bytes,
                                int32_t* status, void* stream);
 
+/* Workspace bytes for ll_layer_decode_step_weights(_q8) (sizes as for ll_workspace_size;
+ * the checkpoints of ll_workspace_checkpoints hold in it). */
+size_t ll_workspace_size_weights(const ll_config* cfg, int32_t max_tokens, int32_t max_blocks);
+
+/* ll_layer_decode_step (and _q8) that adds its attention weights as
+ * ll_paged_attention_decode_weights does, and can rotate by positions of the uncut sequence:
+ * positions int32 [batch] are the new tokens' rotary positions (NULL: context_lens[b] - 1),
+ * context_lens[b] - 1 stays the place in the cache; a position beyond the table sets
+ * LL_DEV_BAD_POSITION as there.  y as that call's for the same positions.  Limits of both
+ * calls. */
+int ll_layer_decode_step_weights(const ll_config* cfg, const void* packed, const void* x, const ll_kv_pool* pool,
+                                 const int32_t* block_table, int32_t max_blocks, const int32_t* context_lens,
+                                 const int32_t* positions, int32_t batch, float* weights, int32_t weights_width, void* y,
+                                 void* workspace, size_t workspace_bytes, int32_t* status, void* stream);
+int ll_layer_decode_step_weights_q8(const ll_config* cfg, const void* packed, const void* x, const ll_kv_pool_q8* pool,
+                                    const int32_t* block_table, int32_t max_blocks, const int32_t* context_lens,
+                                    const int32_t* positions, int32_t batch, float* weights, int32_t weights_width, void* y,
+                                    void* workspace, size_t workspace_bytes, int32_t* status, void* stream);
+
 /* One tensor of a paged pool, by the bytes of a cached row (K or V rows, codes, scales). */
 typedef struct {
     void* data;           /* device, [num_blocks][n_kv_heads][block_size][row_bytes], 4-byte aligned (16: faster) */

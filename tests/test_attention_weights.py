@@ -123,3 +123,56 @@ OBSERVE = dict(q=FAKE, cu=FAKE, tokens=16, k=FAKE, num_blocks=8, table=FAKE, max
     (dict(batch=65535, n_kv_heads=128, n_heads=128, tokens=1 << 24, max_new=1 << 24), UNSUPPORTED)])
 def test_observe_refusals(bad, code):
     assert api.lib.ll_paged_attention_weights(*{**OBSERVE, **bad}.values(), NULL) == code
+
+
+STEP = dict(packed=FAKE, x=FAKE, pool=pool(), table=FAKE, max_blocks=8, ctx=FAKE, positions=0, batch=2, weights=FAKE, width=128,
+            y=2 * FAKE, ws=FAKE, ws_bytes=1 << 40, status=FAKE)
+
+
+@pytest.mark.parametrize("bad,code", [
+    (dict(packed=0), INVALID), (dict(x=0), INVALID), (dict(table=0), INVALID), (dict(max_blocks=0), INVALID), (dict(ctx=0), INVALID),
+    (dict(batch=0), INVALID), (dict(batch=70000), UNSUPPORTED), (dict(weights=0), INVALID), (dict(weights=FAKE + 2), INVALID),
+    (dict(width=0), INVALID), (dict(y=0), INVALID), (dict(y=FAKE), INVALID), (dict(ws=0), WORKSPACE), (dict(ws_bytes=1000), WORKSPACE),
+    (dict(status=0), INVALID), (dict(pool=pool(v=0)), INVALID), (dict(max_blocks=1 << 27), UNSUPPORTED),
+    (dict(pool=pool(num_blocks=1 << 28)), UNSUPPORTED)])
+def test_layer_step_refusals(bad, code):
+    from transformer_decoder_layer_llama_gb300 import synth
+    cfg = api.make_config(synth.DIMS_TINY, 128)
+    a = {**STEP, **bad}
+    assert api.lib.ll_layer_decode_step_weights(ctypes.byref(cfg), *a.values(), NULL) == code
+    c7 = api.make_config(synth.DIMS_7B, 128)
+    if "pool" not in bad:
+        assert api.lib.ll_layer_decode_step_weights_q8(ctypes.byref(c7), *{**a, "pool": pool_q8()}.values(), NULL) == code
+    assert api.lib.ll_layer_decode_step_weights_q8(ctypes.byref(cfg), *{**STEP, "pool": pool_q8()}.values(), NULL) == UNSUPPORTED
+    n = api.lib.ll_workspace_size_weights(ctypes.byref(c7), 4, 16)
+    assert n >= api.workspace_size(c7, 4, 16) + 4 * 32 * 16 * 128 * 4
+    assert api.lib.ll_workspace_size_weights(ctypes.byref(c7), 0, 16) == 0
+
+
+def test_the_scheduler_cuts_a_request():
+    from transformer_decoder_layer_llama_gb300.serving import BlockAllocator, Scheduler
+    sch = Scheduler(3, 16, 8, BlockAllocator(30, seed=3), seed=1)
+    for s in range(2):
+        sch.start_resident(s, 70 + s)
+    free = sch.alloc.free_count()
+    assert sch.positions().tolist() == [69, 70, -1]
+    blocks = list(sch.slots[0].blocks)
+    sch.cut(0, 33)
+    assert sch.slots[0].blocks == blocks[:3] and sch.alloc.free_count() == free + 2
+    assert sch.table[0].tolist() == blocks[:3] + [-1] * 5 and sch.positions().tolist() == [69, 70, -1]
+    sch.fork(0, 2)
+    assert sch.positions().tolist() == [69, 70, 69]
+    assert sch.grow_for_decode().tolist() == [34, 72, 34] and sch.positions().tolist() == [70, 71, 70]
+    with pytest.raises(ValueError, match="shared"):
+        sch.own_blocks(0)
+    sch.own_blocks(1)
+    for bad in ((0, 35), (0, -1)):
+        with pytest.raises(ValueError):
+            sch.cut(*bad)
+    sch.retire(2)
+    sch.own_blocks(0)
+    for call in (lambda: sch.own_blocks(2), lambda: sch.cut(2, 0)):
+        with pytest.raises(ValueError):
+            call()
+    sch.cut(1, 0)
+    assert sch.slots[1].blocks == [] and sch.held_outside() == []

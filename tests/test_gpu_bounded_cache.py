@@ -1,0 +1,317 @@
+"""Normed heads, cache, attention weights and evictions together, as a server with a bounded cache uses them."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import cache_ops as C
+from oracle import weight_ops as W
+from tests.helpers import bits, f64
+from transformer_decoder_layer_llama_gb300 import synth
+
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    from transformer_decoder_layer_llama_gb300 import api
+
+DIMS = synth.LayerDims(512, 8, 2, 128, 688, 16)
+
+
+def i32(x):
+    return torch.as_tensor(np.asarray(x), dtype=torch.int32).cuda()
+
+
+def check_status(st, want=0):
+    torch.cuda.synchronize()
+    assert int(st.item()) == want
+
+
+@pytest.mark.parametrize("int8", [False, True])
+def test_a_served_batch_with_a_bounded_cache(int8):
+    """Prompts: norm and rotate, write, weigh the rows; steps: norm and rotate at the uncut position, write, attend and
+    weigh; whenever a sequence passes the bound, evict.  The reference keeps its own list of rows for each head and
+    sequence; weights and outputs within 2^-6 of the largest value (BF16 heads and cache rows, 2^-8 each, and INT8 codes
+    are taken from the library's own; what is compared is attention over the same rows)."""
+    H, Hkv, d, bs, B, bound, sinks, recent = 8, 2, 128, 16, 3, 48, 2, 8
+    G, mb, nb = H // Hkv, 6, 20
+    g = torch.Generator().manual_seed(4)
+    perm = torch.randperm(nb, generator=g).tolist()
+    table = np.array([[perm.pop() for _ in range(mb)] for _ in range(B)])
+    dt = i32(table)
+    k_pool, v_pool = (torch.full((nb, Hkv, bs, d), math.nan).bfloat16().cuda() for _ in range(2))
+    q8 = api.PoolQ8.empty(nb, Hkv, bs, d)
+    gains = [(1 + 0.2 * torch.randn(d, generator=g)).cuda() for _ in range(2)]
+    rope = api.rope_table(api.make_rope_config(d), 256)
+    freq, _ = C.inv_freq(d)
+    weights, st, scale = torch.zeros(B, Hkv, mb * bs).cuda(), api.new_status(), 1 / math.sqrt(d)
+    ref_w = [[np.zeros(0) for _ in range(Hkv)] for _ in range(B)]
+    lens, seen = [40, 33, 47], [40, 33, 47]                     # rows in the cache, tokens so far
+
+    def heads(tokens, pos):
+        x = torch.randn(tokens, (H + 2 * Hkv) * d, generator=g).bfloat16().cuda()
+        q, k, v = x[:, :H * d].view(tokens, H, d), x[:, H * d:(H + Hkv) * d].view(tokens, Hkv, d), x[:, (H + Hkv) * d:].view(tokens, Hkv, d)
+        q1, k1 = api.norm_rope(q, k, *gains, i32(pos), rope, status=st)
+        ref = W.norm_rope(f64(k), f64(gains[1]), np.asarray(pos), freq, 1e-5, "half")
+        assert (np.abs(f64(k1) - ref) <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -12).all()
+        return q1, k1, v.contiguous()
+
+    def write(k, v, seqs, places):
+        slots = i32([table[b, p // bs] * bs + p % bs for b, p in zip(seqs, places)])
+        if int8:
+            api.reshape_and_cache_q8(k, v, slots, q8, status=st)
+        api.reshape_and_cache(k, v, slots, k_pool, v_pool, status=st)      # (the prompts are weighed over BF16 keys)
+
+    def rows(b, h, n):
+        at = np.arange(n)
+        blk = table[b, at // bs]
+        if int8:
+            codes, s = (t.cpu().numpy()[blk, h, at % bs] for t in (q8.k, q8.k_scale))
+            vc, vs = (t.cpu().numpy()[blk, h, at % bs] for t in (q8.v, q8.v_scale))
+            return codes.astype(np.float64) * s[:, None], vc.astype(np.float64) * vs[:, None]
+        return f64(k_pool)[blk, h, at % bs], f64(v_pool)[blk, h, at % bs]
+
+    def compare():
+        for b in range(B):
+            for h in range(Hkv):
+                got = f64(weights[b, h])
+                assert np.abs(got[:lens[b]] - ref_w[b][h]).max() <= 2.0 ** -6 * ref_w[b][h].max()
+                assert (got[lens[b]:] == 0).all()
+
+    # the prompts
+    cu = np.cumsum([0] + lens)
+    q, k, v = heads(cu[-1], np.concatenate([np.arange(n) for n in lens]))
+    write(k, v, np.repeat(np.arange(B), lens), np.concatenate([np.arange(n) for n in lens]))
+    api.paged_attention_weights(q, i32(cu), k_pool, dt, i32(lens), scale, weights, max(lens), status=st)
+    for b in range(B):
+        for h in range(Hkv):
+            keys = f64(k_pool)[table[b, np.arange(lens[b]) // bs], h, np.arange(lens[b]) % bs]
+            ref_w[b][h] = W.probabilities(f64(q[cu[b]:cu[b + 1], h * G:(h + 1) * G]), keys, scale, 0).sum((0, 1))
+    check_status(st)
+    compare()
+    # steps, with evictions on the way
+    for step in range(20):
+        q, k, v = heads(B, seen)
+        write(k, v, range(B), lens)
+        lens, seen = [n + 1 for n in lens], [n + 1 for n in seen]
+        if int8:
+            out = api.paged_attention_decode_weights_q8(q, q8, dt, i32(lens), scale, weights, status=st)
+        else:
+            out = api.paged_attention_decode_weights(q, k_pool, v_pool, dt, i32(lens), scale, weights, status=st)
+        check_status(st)
+        for b in range(B):
+            for h in range(Hkv):
+                kk, vv = rows(b, h, lens[b])
+                p = W.probabilities(f64(q[b, h * G:(h + 1) * G])[None], kk, scale, lens[b] - 1)[0]
+                ref_w[b][h] = np.append(ref_w[b][h], 0.0) + p.sum(0)
+                ref = p @ vv
+                assert np.abs(f64(out[b, h * G:(h + 1) * G]) - ref).max() <= 2.0 ** -6 * np.abs(vv).max()
+        compare()
+        if max(lens) > bound:
+            held = [[rows(b, h, lens[b]) for h in range(Hkv)] for b in range(B)]
+            before = weights.clone()
+            pool = q8 if int8 else (k_pool, v_pool)
+            kept, new = api.evict_rows(pool, dt, i32(lens), weights, bound - 8, sinks=sinks, recent=recent, status=st)
+            check_status(st)
+            assert new.tolist() == [min(n, bound - 8) for n in lens]
+            for b in range(B):
+                for h in range(Hkv):
+                    keep = W.keep_rows(before[b, h, :lens[b]].cpu().numpy(), bound - 8, sinks, recent)
+                    assert (kept[b, h, :len(keep)].cpu().numpy() == keep).all()
+                    ref_w[b][h] = ref_w[b][h][keep]
+                    for a, o in zip(rows(b, h, len(keep)), held[b][h]):
+                        assert (a == o[keep]).all()
+            lens = new.tolist()
+            compare()
+    assert max(seen) > max(lens) and lens[0] <= bound
+
+
+def layer(dims, seed, max_position=512):
+    cfg = api.make_config(dims, max_position=max_position)
+    return cfg, api.pack_weights(cfg, {k: v.cuda() for k, v in synth.make_weights(dims, 0.02, seed=seed).items()})
+
+
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("B", [3, 40, 300])
+def test_layer_step_with_weights(B, int8):
+    """The step's output and cache are those of the plain step; its weights those of the attention over its own queries;
+    other rotary positions are those of a step at that place.  (300 sequences take the prefill's form of the products.)"""
+    dims, mb = DIMS, 5
+    cfg, packed = layer(dims, 3)
+    g = torch.Generator().manual_seed(B)
+    ctx = torch.randint(1, mb * 16 + 1, (B,), generator=g).tolist()
+    table, nb = synth.make_block_table([mb * 16] * B, 16, seed=1)
+    table = table.cuda()
+    x = synth.make_x(B, dims.hidden, seed=2).cuda()
+
+    def pool():
+        k, v = (t.cuda() for t in synth.make_pool(nb, dims, seed=5))
+        if not int8:
+            return k, v
+        p = api.PoolQ8.empty(nb, 2, 16, 128)
+        slots = torch.arange(nb * 16, dtype=torch.int32).cuda()
+        flat = [t.transpose(1, 2).reshape(nb * 16, 2, 128).contiguous() for t in (k, v)]
+        api.reshape_and_cache_q8(*flat, slots, p)
+        return p
+    tensors = lambda p: [p.k, p.v, p.k_scale, p.v_scale] if int8 else list(p)  # noqa: E731
+    base = torch.rand(B, 2, mb * 16 + 7, generator=g).cuda()
+    a, b, st = pool(), pool(), api.new_status()
+    w, ws = base.clone(), api.new_workspace_weights(cfg, B, mb)
+    y = api.layer_decode_step_weights(cfg, packed, x, a, table, i32(ctx), w, workspace=ws, status=st)
+    if int8:
+        want = api.layer_decode_step_q8(cfg, packed, x, b, table, i32(ctx))
+    else:
+        want = api.layer_decode_step(cfg, packed, x, *b, table, i32(ctx))
+    check_status(st)
+    assert torch.equal(y, want) and all(torch.equal(s, t) for s, t in zip(tensors(a), tensors(b)))
+    q = api.checkpoints(cfg, ws, B, mb, B)["q"].view(B, 8, 128).clone()
+    again = base.clone()
+    if int8:
+        api.paged_attention_decode_weights_q8(q, a, table, i32(ctx), 1 / math.sqrt(128), again)
+    else:
+        api.paged_attention_decode_weights(q, *a, table, i32(ctx), 1 / math.sqrt(128), again)
+    assert torch.equal(again, w)
+    # other positions: q and the new K are those of a step that stands there
+    pos = [(c - 1 + 17) % (mb * 16) for c in ctx]
+    a, b, w = pool(), pool(), base.clone()
+    api.layer_decode_step_weights(cfg, packed, x, a, table, i32(ctx), w, positions=i32(pos), workspace=ws, status=st)
+    q = api.checkpoints(cfg, ws, B, mb, B)["q"].clone()
+    ws2 = api.new_workspace_weights(cfg, B, mb)
+    api.layer_decode_step_weights(cfg, packed, x, b, table, i32([p + 1 for p in pos]), base.clone(), workspace=ws2, status=st)
+    check_status(st)
+    assert torch.equal(q, api.checkpoints(cfg, ws2, B, mb, B)["q"])
+    place = lambda p, at: [t[table[torch.arange(B), torch.tensor(at) // 16].long(), :, torch.tensor(at) % 16] for t in tensors(p)]  # noqa: E731
+    assert all(torch.equal(s, t) for s, t in zip(place(a, [c - 1 for c in ctx]), place(b, pos)))
+    # a position beyond the table is flagged
+    st = api.new_status()
+    api.layer_decode_step_weights(cfg, packed, x, a, table, i32(ctx), w, positions=i32([512] + pos[1:]), workspace=ws, status=st)
+    check_status(st, api.LL_DEV_BAD_POSITION)
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_stack_with_a_bounded_cache(captured):
+    """A two-layer stack that evicts, against the same layer calls and evictions by hand."""
+    from transformer_decoder_layer_llama_gb300.serving import BlockAllocator, Scheduler, StackEngine
+    d, L, nb, mb, slots, prompt, keep = synth.DIMS_TINY, 2, 40, 5, 3, 40, 48
+    layers = [layer(d, 60 + l) for l in range(L)]
+    cfg, packed = layers[0][0], [p for _, p in layers]
+    sch = Scheduler(slots, d.block_size, mb, BlockAllocator(nb, seed=5), seed=6, prompt_len=prompt)
+    pools = [tuple(t.cuda() for t in synth.make_pool(nb, d, seed=l)) for l in range(L)]
+    own = [tuple(t.clone() for t in p) for p in pools]
+    eng = StackEngine(api, [cfg] * L, packed, pools, slots, mb, slots * prompt, track_weights=True)
+    stream = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    if captured:
+        eng.ctx.fill_(1)
+        torch.cuda.synchronize()
+        eng.capture_decode(stream)                            # (table of -1: flagged, nothing is written)
+        stream.synchronize()
+        eng.status.zero_()
+        eng.start_weights(range(slots), stream)
+    for s in range(slots):
+        sch.start_resident(s, prompt + s)
+    weights = [torch.zeros(slots, d.n_kv_heads, mb * d.block_size).cuda() for _ in range(L)]
+    st, cuts = api.new_status(), 0
+    stream.synchronize()
+    for i in range(30):
+        ctx = sch.grow_for_decode()
+        eng.table.copy_(torch.from_numpy(sch.table))
+        eng.ctx.copy_(torch.from_numpy(ctx))
+        eng.pos.copy_(torch.from_numpy(sch.positions()))
+        assert sch.positions().tolist() == [prompt + s + i for s in range(slots)]
+        x = synth.make_x(slots, d.hidden, seed=i)
+        eng.x.copy_(x)
+        torch.cuda.synchronize()
+        y = eng.decode(stream)
+        stream.synchronize()
+        h = x.cuda()
+        for l in range(L):
+            h = api.layer_decode_step_weights(cfg, packed[l], h, own[l], i32(sch.table), i32(ctx), weights[l],
+                                              positions=i32(sch.positions()), status=st)
+        check_status(st)
+        assert torch.equal(h, y) and all(torch.equal(a, b) for a, b in zip(weights, eng.weights))
+        if max(r.ctx for r in sch.slots) > keep:
+            table, lens = i32(sch.table), [r.ctx for r in sch.slots]
+            done = eng.evict(sch, keep - 10, stream, sinks=2, recent=5)
+            stream.synchronize()
+            assert done == list(range(slots)) and [r.ctx for r in sch.slots] == [min(n, keep - 10) for n in lens]
+            for l in range(L):
+                api.evict_rows(own[l], table, i32(lens), weights[l], keep - 10, sinks=2, recent=5, status=st)
+            check_status(st)
+            assert all(torch.equal(a, b) for p, o in zip(pools, own) for a, b in zip(p, o))
+            assert all(torch.equal(a, b) for a, b in zip(weights, eng.weights))
+            assert all(len(r.blocks) == -(-r.ctx // d.block_size) for r in sch.slots)
+            cuts += 1
+    assert cuts >= 2 and int(eng.status.item()) == 0
+    assert eng.evict(sch, 10 ** 6, stream) == []
+    eng.start_weights([1], stream)
+    eng.copy_weights(0, 2, stream)
+    stream.synchronize()
+    assert all((w[1] == 0).all() and torch.equal(w[0], w[2]) for w in eng.weights)
+
+
+def test_a_shared_block_is_not_moved_into():
+    from transformer_decoder_layer_llama_gb300.serving import BlockAllocator, Scheduler, StackEngine
+    d, nb, mb, slots = synth.DIMS_TINY, 40, 5, 3
+    cfg, packed = layer(d, 9)
+    sch = Scheduler(slots, d.block_size, mb, BlockAllocator(nb, seed=5), seed=6)
+    pools = [tuple(t.cuda() for t in synth.make_pool(nb, d, seed=1))]
+    eng = StackEngine(api, [cfg], [packed], pools, slots, mb, 64, track_weights=True)
+    sch.start_resident(0, 60)
+    sch.start_resident(1, 60)
+    sch.fork(0, 2)
+    before, held = [bits(t) for t in pools[0]], [list(r.blocks) for r in sch.slots]
+    stream = torch.cuda.Stream()
+    with pytest.raises(ValueError, match="shared"):
+        eng.evict(sch, 32, stream)
+    stream.synchronize()
+    assert all((a == bits(t)).all() for a, t in zip(before, pools[0])) and held == [list(r.blocks) for r in sch.slots]
+    with pytest.raises(ValueError, match="track_weights"):
+        StackEngine(api, [cfg], [packed], pools, slots, mb, 64).evict(sch, 32, stream)
+
+
+@pytest.mark.parametrize("observe", [None, 0, 1, 7, 33])
+def test_stack_prompts_start_the_weights(observe):
+    """The weights after a prefill are those of the prompts' last queries over the keys the layers wrote, within 2^-6 of the
+    largest (rows of BF16 queries and keys as they are); other slots keep theirs."""
+    from transformer_decoder_layer_llama_gb300.serving import StackEngine
+    d, L, nb, mb, S, T = synth.DIMS_TINY, 2, 30, 5, 4, 33
+    layers = [layer(d, 70 + l) for l in range(L)]
+    cfg, packed = layers[0][0], [p for _, p in layers]
+    pools = [tuple(t.cuda() for t in synth.make_pool(nb, d, seed=l)) for l in range(L)]
+    plain = [tuple(t.clone() for t in p) for p in pools]
+    eng = StackEngine(api, [cfg] * L, packed, pools, S, mb, 2 * T, track_weights=True)
+    ref = StackEngine(api, [cfg] * L, packed, plain, S, mb, 2 * T)
+    table = torch.randperm(nb, generator=torch.Generator().manual_seed(1))[:2 * mb].view(2, mb)
+    stream = torch.cuda.Stream()
+    for e in (eng, ref):
+        e.pf_table[:2] = i32(table)
+        e.pf_pos[:2 * T] = torch.arange(T, dtype=torch.int32).repeat(2).cuda()
+        e.pf_x[:2 * T] = synth.make_x(2 * T, d.hidden, seed=3).cuda()
+    for w in eng.weights:
+        w.fill_(3.0)
+    torch.cuda.synchronize()
+    y = eng.prefill(2, T, stream, slots=[2, 0], observe=observe)
+    want = ref.prefill(2, T, stream)
+    stream.synchronize()
+    assert torch.equal(y, want) and int(eng.status.item()) == 0
+    assert all(torch.equal(a, b) for p, o in zip(pools, plain) for a, b in zip(p, o))
+    n = T if observe is None else observe
+    G = d.n_heads // d.n_kv_heads
+    for l in range(L):
+        got = f64(eng.weights[l])
+        assert (got[[1, 3]] == 3).all() and (got[[0, 2]][:, :, T:] == 0).all()
+        if l == L - 1 and n:
+            q = f64(api.checkpoints(cfg, eng.ws, 2 * T, mb, 2 * T)["q"]).reshape(2, T, d.n_heads, d.head_dim)
+            for i, s in enumerate((2, 0)):
+                for h in range(d.n_kv_heads):
+                    keys = f64(pools[l][0])[table[i].numpy()[np.arange(T) // d.block_size], h, np.arange(T) % d.block_size]
+                    p = W.probabilities(q[i, T - n:, h * G:(h + 1) * G], keys, d.head_dim ** -0.5, T - n).sum((0, 1))
+                    assert np.abs(got[s, h, :T] - p).max() <= 2.0 ** -6 * p.max()
+        total = got[[0, 2]].sum(-1)
+        assert (np.abs(total - n * G) <= 1e-4 * n * G).all()
+    for bad in (dict(slots=[0]), dict(slots=[0, 0]), dict(slots=[0, S]), dict(slots=[0, 1], observe=T + 1)):
+        with pytest.raises(ValueError):
+            eng.prefill(2, T, stream, **bad)
+    with pytest.raises(ValueError, match="track_weights"):
+        ref.prefill(2, T, stream, slots=[0, 1])

@@ -52,7 +52,8 @@ EXPORTED = [
     "ll_norm_rope", "ll_norm_rope_backward_workspace_size", "ll_norm_rope_backward",
     "ll_attention_decode_weights_workspace_size", "ll_paged_attention_decode_weights",
     "ll_paged_attention_decode_weights_q8", "ll_evict_rows", "ll_attention_weights_workspace_size",
-    "ll_paged_attention_weights",
+    "ll_paged_attention_weights", "ll_workspace_size_weights", "ll_layer_decode_step_weights",
+    "ll_layer_decode_step_weights_q8",
 ]
 
 
@@ -175,6 +176,10 @@ def _load():
         "ll_attention_weights_workspace_size": (S, [I32, I32, I32, I32, I32, I32, I32, I32]),
         "ll_paged_attention_weights": (ctypes.c_int, [P, P, I32, P, I32, P, I32, P, I32, I32, I32, I32, I32, I32, F32, P, I32, P,
                                                       S, P, P]),
+        "ll_workspace_size_weights": (S, [cfgp, I32, I32]),
+        "ll_layer_decode_step_weights": (ctypes.c_int, [cfgp, P, P, poolp, P, I32, P, P, I32, P, I32, P, P, S, P, P]),
+        "ll_layer_decode_step_weights_q8": (ctypes.c_int, [cfgp, P, P, ctypes.POINTER(ll_kv_pool_q8), P, I32, P, P, I32, P, I32,
+                                                           P, P, S, P, P]),
         "ll_evict_rows": (ctypes.c_int, [ctypes.POINTER(ll_row_tensor), I32, I32, I32, I32, P, I32, P, I32, P, I32, P, I32, I32,
                                          I32, P, P, P, P, P]),
         "ll_append_to_cache_f8": (ctypes.c_int, [P, P, I64, I64, P, I32, P, I32, I32, I32, I32, I32, poolf8, P, I32,
@@ -1122,6 +1127,54 @@ def paged_attention_weights(q, cu_new, k_pool, block_table, context_lens, scale,
           k_pool.data_ptr(), nb, block_table.data_ptr(), mb, context_lens.data_ptr(), B, int(max_new), Hq, Hkv, d, bs,
           float(scale), weights.data_ptr(), width, workspace.data_ptr(), workspace.numel(), status.data_ptr())
     return weights
+
+
+def new_workspace_weights(cfg, batch, max_blocks, device=None):
+    """A workspace for layer_decode_step_weights of up to `batch` sequences."""
+    n = lib.ll_workspace_size_weights(ctypes.byref(cfg), int(batch), int(max_blocks))
+    if n == 0:
+        raise LayerError("ll_workspace_size_weights", LL_ERR_INVALID_ARG)
+    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def layer_decode_step_weights(cfg, packed, x, pool, block_table, context_lens, weights, positions=None, y=None, workspace=None,
+                              status=None, stream=None):
+    """ll_layer_decode_step_weights (_q8 where `pool` is a PoolQ8; else a (K, V) pair of BF16 pools): the layer's decode
+    step that adds its attention weights to `weights` (float32 [batch, n_kv_heads, width], in place).  positions int32
+    [batch]: the new tokens' rotary positions where the cache has been cut (None: context_lens - 1).  Returns y."""
+    given = y, workspace, status
+    q8 = isinstance(pool, PoolQ8)
+    if q8:
+        k, cpool = pool.k, pool.c()
+    else:
+        cpool = _pool(*pool)
+        k = pool[0]
+    B = _paged_batch(block_table, context_lens)
+    _need(packed, "packed", torch.uint8)
+    _need(x, "x", torch.bfloat16, shape=(B, cfg.hidden))
+    if tuple(k.shape[1:]) != (cfg.n_kv_heads, cfg.block_size, cfg.head_dim):
+        raise ValueError(f"the pool must be [num_blocks, {cfg.n_kv_heads}, {cfg.block_size}, {cfg.head_dim}]")
+    width = _weights(weights, B, cfg.n_kv_heads)
+    if positions is not None:
+        _need(positions, "positions", torch.int32, shape=(B,))
+    if y is None:
+        y = torch.empty_like(x)
+    else:
+        _need(y, "y", torch.bfloat16, shape=(B, cfg.hidden))
+    mb = block_table.shape[1]
+    if workspace is None:
+        workspace = new_workspace_weights(cfg, B, mb, x.device)
+    else:
+        _need(workspace, "workspace", torch.uint8)
+    status = new_status(x.device) if status is None else _status(status)
+    dev = _on(x, packed, k, block_table, context_lens, weights, positions, y, workspace, status)
+    if stream is not None:
+        _made(stream, dev, *(t if g is None else None for g, t in zip(given, (y, workspace, status))))
+    name = "ll_layer_decode_step_weights_q8" if q8 else "ll_layer_decode_step_weights"
+    _call(name, getattr(lib, name), dev, stream, ctypes.byref(cfg), packed.data_ptr(), x.data_ptr(), cpool,
+          block_table.data_ptr(), mb, context_lens.data_ptr(), positions.data_ptr() if positions is not None else None, B,
+          weights.data_ptr(), width, y.data_ptr(), workspace.data_ptr(), workspace.numel(), status.data_ptr())
+    return y
 
 
 def evict_rows(pool, block_table, context_lens, weights, keep, max_keep=None, sinks=0, recent=0, weights_out=None,

@@ -170,14 +170,27 @@ bool pool_ok(const ll_kv_pool* p) {
     return p && p->k && p->v && p->num_blocks > 0 && aligned16(p->k) && aligned16(p->v);
 }
 
+// What a decode step over a BF16 or INT8 pool adds its attention weights to, and the tokens' rotary positions.
+struct StepWeights {
+    const int32_t* positions;      // or null: context_lens - 1
+    float* weights;
+    int32_t width;
+};
+
+// Bytes of the scores that such a step keeps behind its workspace.
+size_t step_scores_bytes(const ll_config* c, int T, int max_blocks) {
+    return align_up((size_t)T * c->n_heads * max_blocks * c->block_size * sizeof(float));
+}
+
 int run_layer(const ll_config* cfg, const void* packed, const void* x, const int32_t* positions,
               const int32_t* context_lens, int T, int seq_len, int batch, const ll_kv_pool* pool,
               const int32_t* block_table, int max_blocks, void* y, void* workspace,
               size_t workspace_bytes, int32_t* status, cudaStream_t stream, bool decode,
-              const ll_kv_pool_q8* pq8 = nullptr, const ll_kv_pool_f8* pf8 = nullptr) {
+              const ll_kv_pool_q8* pq8 = nullptr, const ll_kv_pool_f8* pf8 = nullptr, const StepWeights* sw = nullptr) {
     WsLayout L = ws_layout(cfg, T, max_blocks);
     const WsF8Layout LF = pf8 ? ws_f8_layout(cfg, T, max_blocks) : WsF8Layout{};
-    if (!workspace || workspace_bytes < (pf8 ? LF.total : L.total) || !aligned16(workspace)) return LL_ERR_WORKSPACE;
+    const size_t need = pf8 ? LF.total : L.total + (sw ? step_scores_bytes(cfg, T, max_blocks) : 0);
+    if (!workspace || workspace_bytes < need || !aligned16(workspace)) return LL_ERR_WORKSPACE;
     Packed P = packed_view(cfg, packed);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     auto* xh = reinterpret_cast<__nv_bfloat16*>(ws + L.xh);
@@ -223,6 +236,7 @@ int run_layer(const ll_config* cfg, const void* packed, const void* x, const int
     g.ep.q_out = q;
     g.ep.positions = decode ? nullptr : positions;
     g.ep.context_lens = decode ? context_lens : nullptr;
+    g.ep.rope_positions = sw ? sw->positions : nullptr;
     g.ep.block_table = block_table;
     g.ep.max_blocks = max_blocks;
     g.ep.seq_len = seq_len;
@@ -348,6 +362,12 @@ int run_layer(const ll_config* cfg, const void* packed, const void* x, const int
         at.part_o = reinterpret_cast<float*>(ws + L.attn);
         at.part_ml = at.part_o + rows * d;
         at.status = status;
+        if (sw) {
+            at.weights = sw->weights;
+            at.weights_width = sw->width;
+            at.scores = reinterpret_cast<float*>(ws + L.total);
+            at.score_stride = (long long)max_blocks * cfg->block_size;
+        }
         if ((e = pq8 ? ll::launch_attn_decode_q8(at, stream) : ll::launch_attn_decode(at, stream)) != cudaSuccess)
             return LL_ERR_CUDA;
     }
@@ -850,6 +870,52 @@ int ll_layer_decode_step_q8(const ll_config* cfg, const void* packed, const void
     if (!aligned16(packed) || !aligned16(x) || !aligned16(y)) return LL_ERR_INVALID_ARG;
     return run_layer(cfg, packed, x, nullptr, context_lens, batch, 1, batch, nullptr, block_table, max_blocks, y,
                      workspace, workspace_bytes, status, static_cast<cudaStream_t>(stream), true, pool);
+}
+
+size_t ll_workspace_size_weights(const ll_config* cfg, int32_t max_tokens, int32_t max_blocks) {
+    if (config_supported(cfg) != LL_OK || max_tokens <= 0 || max_blocks <= 0) return 0;
+    return ws_layout(cfg, max_tokens, max_blocks).total + step_scores_bytes(cfg, max_tokens, max_blocks);
+}
+
+static int step_weights(const ll_config* cfg, const void* packed, const void* x, const ll_kv_pool* pool, const ll_kv_pool_q8* pq8,
+                        const int32_t* block_table, int32_t max_blocks, const int32_t* context_lens, const int32_t* positions,
+                        int32_t batch, float* weights, int32_t weights_width, void* y, void* workspace, size_t workspace_bytes,
+                        int32_t* status, void* stream) {
+    if (!packed || !x || !context_lens || !block_table || !y || !status || !weights || weights_width <= 0) return LL_ERR_INVALID_ARG;
+    if (batch <= 0 || max_blocks <= 0 || x == y) return LL_ERR_INVALID_ARG;
+    if (!aligned16(packed) || !aligned16(x) || !aligned16(y) || (reinterpret_cast<uintptr_t>(weights) & 3u) != 0) return LL_ERR_INVALID_ARG;
+    const int64_t nb = pq8 ? pq8->num_blocks : pool->num_blocks;
+    if (batch > 65535 || (int64_t)max_blocks * cfg->block_size > (1LL << 30) ||
+        nb * cfg->n_kv_heads * cfg->block_size > (1LL << 31) - 1)
+        return LL_ERR_UNSUPPORTED;
+    const StepWeights sw = {positions, weights, weights_width};
+    return run_layer(cfg, packed, x, nullptr, context_lens, batch, 1, batch, pool, block_table, max_blocks, y, workspace,
+                     workspace_bytes, status, static_cast<cudaStream_t>(stream), true, pq8, nullptr, &sw);
+}
+
+int ll_layer_decode_step_weights(const ll_config* cfg, const void* packed, const void* x, const ll_kv_pool* pool,
+                                 const int32_t* block_table, int32_t max_blocks, const int32_t* context_lens,
+                                 const int32_t* positions, int32_t batch, float* weights, int32_t weights_width, void* y,
+                                 void* workspace, size_t workspace_bytes, int32_t* status, void* stream) {
+    ll::clear_last_error();
+    const int rc = config_supported(cfg);
+    if (rc != LL_OK) return rc;
+    if (!pool_ok(pool)) return LL_ERR_INVALID_ARG;
+    return step_weights(cfg, packed, x, pool, nullptr, block_table, max_blocks, context_lens, positions, batch, weights,
+                        weights_width, y, workspace, workspace_bytes, status, stream);
+}
+
+int ll_layer_decode_step_weights_q8(const ll_config* cfg, const void* packed, const void* x, const ll_kv_pool_q8* pool,
+                                    const int32_t* block_table, int32_t max_blocks, const int32_t* context_lens,
+                                    const int32_t* positions, int32_t batch, float* weights, int32_t weights_width, void* y,
+                                    void* workspace, size_t workspace_bytes, int32_t* status, void* stream) {
+    ll::clear_last_error();
+    const int rc = config_supported(cfg);
+    if (rc != LL_OK) return rc;
+    if (cfg->head_dim != 128) return LL_ERR_UNSUPPORTED;
+    if (!pool_q8_ok(pool)) return LL_ERR_INVALID_ARG;
+    return step_weights(cfg, packed, x, nullptr, pool, block_table, max_blocks, context_lens, positions, batch, weights,
+                        weights_width, y, workspace, workspace_bytes, status, stream);
 }
 
 size_t ll_workspace_size_f8(const ll_config* cfg, int32_t max_tokens, int32_t max_blocks) {

@@ -64,7 +64,7 @@ struct GemmArgs {
 };
 
 struct TokenSlot {
-    int pos;         // -1 if invalid
+    int pos;         // of the rotation; -1 if invalid
     long long kv_row;  // row index (blk * Hkv) * bs + off of head 0, or -1
 };
 
@@ -76,6 +76,14 @@ LL_DEVINL TokenSlot token_slot(const EpiParams& ep, int t) {
         return s;
     }
     s.pos = pos;
+    if (ep.rope_positions) {
+        s.pos = ep.rope_positions[t];
+        if (s.pos < 0 || s.pos >= ep.max_position) {
+            flag_status(ep.status, LL_DEV_BAD_POSITION);
+            s.pos = -1;
+            return s;
+        }
+    }
     if (ep.kv_stage) {                           // staging rows [token][kv head]
         s.kv_row = (long long)t * ep.n_kv_heads;
         return s;

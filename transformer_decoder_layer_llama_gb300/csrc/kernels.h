@@ -59,6 +59,7 @@ struct EpiParams {
     int kv_stage;
     const int32_t* positions;      // prefill: position of each token (null in decode)
     const int32_t* context_lens;   // decode: position = context_lens[token] - 1
+    const int32_t* rope_positions; // angle of each token, or null: its position in the cache
     const int32_t* block_table;
     int max_blocks;
     int seq_len;                   // tokens per sequence (decode: 1)

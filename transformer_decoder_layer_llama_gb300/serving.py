@@ -98,6 +98,7 @@ class Request:
     ctx: int              # tokens in the cache
     budget: int           # decode tokens still to produce
     blocks: list
+    dropped: int = 0      # tokens that have been cut from its cache
 
 
 class Scheduler:
@@ -168,11 +169,37 @@ class Scheduler:
         full = r.ctx // self.bs
         last = self.alloc.alloc(1) if r.ctx % self.bs else []
         self.alloc.share(r.blocks[:full])
-        nr = Request(self.next_rid, r.ctx, r.budget, r.blocks[:full] + last)
+        nr = Request(self.next_rid, r.ctx, r.budget, r.blocks[:full] + last, r.dropped)
         self.next_rid += 1
         self.slots[dst] = nr
         self._set_blocks(dst, nr.blocks)
         return [(r.blocks[full], last[0])] if last else []
+
+    def positions(self) -> np.ndarray:
+        """The rotary position of each slot's last token, which its cache may be too short to tell (int32; -1: empty)."""
+        return np.array([r.ctx - 1 + r.dropped if r is not None else -1 for r in self.slots], np.int32)
+
+    def own_blocks(self, slot: int) -> None:
+        """Raises ValueError where somebody else holds a block of the request in a slot: its rows cannot be moved."""
+        r = self.slots[slot]
+        if r is None:
+            raise ValueError(f"slot {slot} is empty")
+        shared = [b for b in r.blocks if self.alloc.holders(b) > 1]
+        if shared:
+            raise ValueError(f"blocks {shared[:8]} of slot {slot} are shared: copy them before rows move in them")
+
+    def cut(self, slot: int, ctx: int) -> None:
+        """The cache of the request in a slot now has its first `ctx` places only (as an eviction leaves it): the blocks
+        behind them are let go, positions() goes on from the uncut sequence."""
+        r = self.slots[slot]
+        if r is None or not 0 <= ctx <= r.ctx:
+            raise ValueError(f"slot {slot} holds no {ctx} tokens")
+        left = -(-ctx // self.bs)
+        self.alloc.free(r.blocks[left:])
+        r.dropped += r.ctx - ctx
+        r.ctx = ctx
+        self._set_blocks(slot, r.blocks[:left])
+        r.blocks = r.blocks[:left]
 
     def held_outside(self) -> list:
         """Blocks in use that somebody besides the requests in the slots holds (a prefix kept with share, blocks
@@ -216,10 +243,12 @@ class Scheduler:
 
 class StackEngine:
     """The GPU side: L layers (packed weights, K/V pools) and device copies of the tables.  A layer's pool is
-    a (K, V) pair of BF16 tensors or an api.PoolF8; all layers have the same kind."""
+    a (K, V) pair of BF16 tensors or an api.PoolF8; all layers have the same kind.  With track_weights (BF16 pools)
+    every decode step adds up the attention weights of the cached tokens, for evict(); it then reads the tokens' rotary
+    positions from `pos`, as it reads the context lengths from `ctx`."""
 
     def __init__(self, api, cfgs, packed, pools, n_slots, max_blocks, max_prefill_tokens,
-                 device="cuda"):
+                 device="cuda", track_weights=False):
         self.api = api
         self.cfgs, self.packed, self.pools = cfgs, packed, pools
         self.n_slots = n_slots
@@ -228,8 +257,15 @@ class StackEngine:
         self.table = torch.full((n_slots, max_blocks), -1, dtype=torch.int32, device=device)
         self.ctx = torch.zeros(n_slots, dtype=torch.int32, device=device)
         self.f8 = isinstance(pools[0], api.PoolF8)
+        if track_weights and self.f8:
+            raise ValueError("attention weights are tracked over BF16 pools")
         self.ws = (api.new_workspace_f8 if self.f8 else api.new_workspace)(cfg, max(n_slots, max_prefill_tokens),
                                                                            max_blocks, device)
+        self.weights = None
+        if track_weights:
+            self.weights = [torch.zeros(n_slots, cfg.n_kv_heads, max_blocks * cfg.block_size, device=device) for _ in cfgs]
+            self.pos = torch.zeros(n_slots, dtype=torch.int32, device=device)
+            self.step_ws = api.new_workspace_weights(cfg, n_slots, max_blocks, device)
         self._blocks = None
         self.status = api.new_status(device)
         self.x = torch.zeros(n_slots, self.H, dtype=torch.bfloat16, device=device)
@@ -245,11 +281,24 @@ class StackEngine:
         # the buffers are filled on the stream that is current here, and used on the caller's from now on
         torch.cuda.current_stream(self.table.device).synchronize()
 
-    def prefill(self, n_req, prompt_len, stream):
+    def prefill(self, n_req, prompt_len, stream, slots=None, observe=None):
         """All layers over the n_req requests whose rows are in pf_table[:n_req] and whose
         inputs are in pf_x[:n_req * prompt_len]; their positions in pf_pos (BF16 pools) or their
-        context lengths, which count the prompt, in pf_ctx (e4m3 pools)."""
+        context lengths, which count the prompt, in pf_ctx (e4m3 pools).  With track_weights, `slots` names
+        the requests' slots: their attention weights start as those of the last `observe` tokens (None: all) of
+        each prompt."""
         T = n_req * prompt_len
+        if slots is not None:
+            if self.weights is None:
+                raise ValueError("slots are for track_weights")
+            if len(slots) != n_req or len(set(slots)) != n_req or not all(0 <= s < self.n_slots for s in slots):
+                raise ValueError(f"slots must name {n_req} of the {self.n_slots} slots")
+            observe = prompt_len if observe is None else observe
+            if not 0 <= observe <= prompt_len:
+                raise ValueError(f"observe must be in 0..{prompt_len}")
+            if observe == 0:
+                self.start_weights(slots, stream)
+                slots = None
         src = self.pf_x[:T]
         for l in range(len(self.cfgs)):
             dst = self.pf_bufs[l & 1][:T]
@@ -263,8 +312,24 @@ class StackEngine:
             self.api.layer_prefill(self.cfgs[l], self.packed[l], src, self.pf_pos[:T], n_req, prompt_len,
                                    k, v, self.pf_table[:n_req], y=dst, workspace=self.ws,
                                    status=self.status, stream=stream)
+            if slots is not None:
+                self._observe(l, n_req, prompt_len, observe, slots, stream)
             src = dst
         return src
+
+    def _observe(self, l, n_req, prompt_len, observe, slots, stream):
+        """The attention weights of the last `observe` tokens of the prompts that layer l has just been over."""
+        cfg, dev, T = self.cfgs[l], self.table.device, n_req * prompt_len
+        with torch.cuda.stream(stream):
+            q = self.api.checkpoints(cfg, self.ws, T, self.table.shape[1], T)["q"]
+            q = q.view(n_req, prompt_len, cfg.n_heads, cfg.head_dim)[:, prompt_len - observe:].contiguous()
+            cu = torch.arange(0, (n_req + 1) * observe, observe, dtype=torch.int32, device=dev)
+            ctx = self.pf_pos[:T].view(n_req, prompt_len)[:, -1] + 1
+            w = self.weights[l].new_zeros(n_req, *self.weights[l].shape[1:])
+            self.api.paged_attention_weights(q.flatten(0, 1), cu, self.pools[l][0], self.pf_table[:n_req],
+                                             ctx, cfg.head_dim ** -0.5, w, observe, status=self.status)
+            for i, s in enumerate(slots):
+                self.weights[l][s].copy_(w[i])
 
     def _decode_layers(self, stream):
         src = self.x
@@ -273,6 +338,12 @@ class StackEngine:
             if self.f8:
                 self.api.layer_decode_step_f8(self.cfgs[l], self.packed[l], src, self.pools[l], self.table, self.ctx,
                                               y=dst, workspace=self.ws, status=self.status, stream=stream)
+                src = dst
+                continue
+            if self.weights is not None:
+                self.api.layer_decode_step_weights(self.cfgs[l], self.packed[l], src, self.pools[l], self.table, self.ctx,
+                                                   self.weights[l], positions=self.pos, y=dst, workspace=self.step_ws,
+                                                   status=self.status, stream=stream)
                 src = dst
                 continue
             k, v = self.pools[l]
@@ -318,6 +389,44 @@ class StackEngine:
             block_map, counts = block_map.cpu().numpy(), counts.tolist()
         scheduler.apply_map(block_map)
         return counts[1]
+
+    def start_weights(self, slots, stream):
+        """The requests in `slots` are new: their tokens have no attention weight yet."""
+        with torch.cuda.stream(stream):
+            for w in self.weights:
+                for s in slots:
+                    w[s].zero_()
+
+    def copy_weights(self, src, dst, stream):
+        """The request in slot `dst` is a fork of that in `src` (beside copy_blocks)."""
+        with torch.cuda.stream(stream):
+            for w in self.weights:
+                w[dst].copy_(w[src])
+
+    def evict(self, scheduler: Scheduler, keep, stream, sinks=0, recent=0) -> list:
+        """Cuts every request with more than `keep` cached tokens down to `keep` in every layer: each KV head keeps the
+        first `sinks`, the last `recent`, and of the others those of the largest attention weight.  Frees the blocks
+        behind them in the scheduler; returns the slots that were cut.  Where such a request shares a block, ValueError
+        before anything is moved."""
+        if self.weights is None:
+            raise ValueError("evict needs track_weights")
+        slots = [s for s, r in enumerate(scheduler.slots) if r is not None and r.ctx > keep]
+        for s in slots:
+            scheduler.own_blocks(s)
+        if not slots:
+            return slots
+        lens = np.array([r.ctx if r is not None else 0 for r in scheduler.slots], np.int32)
+        lens[lens <= keep] = 0                                # (nothing of the others is looked at)
+        stream.wait_stream(torch.cuda.current_stream(self.table.device))
+        with torch.cuda.stream(stream):                       # behind the steps that still read the table
+            self.table.copy_(torch.from_numpy(scheduler.table))
+            ctx = torch.from_numpy(lens).to(self.table.device)
+            for l in range(len(self.cfgs)):
+                self.api.evict_rows(self.pools[l], self.table, ctx, self.weights[l], keep, sinks=sinks, recent=recent,
+                                    status=self.status)
+        for s in slots:
+            scheduler.cut(s, keep)
+        return slots
 
     def capture_decode(self, stream):
         """Records the all-layer decode step once as a CUDA graph (replayed by decode())."""
