@@ -5,7 +5,7 @@
 // Two kernels.  The choice: a CTA (a cluster where there are few rows of weights) per sequence and KV head finds the
 // weight of the last kept row digit by digit in histograms (11, 11 and 10 bits of an order-preserving integer), then
 // every warp counts, and after one exchange of counts writes, its own stretch of positions: no sort, five passes over
-// weights that stay in L2.  The move: kept[j] >= j ascending, so a row's place is never the source of a later one.  A CTA
+// weights in shared memory, or in L2 where they are too long for it.  Short rows take a warp each, with the keys in registers.  The move: kept[j] >= j ascending, so a row's place is never the source of a later one.  A CTA
 // goes through its rows in order and writes a run of them when all its threads have read theirs; heads, tensors
 // and slices of a row's bytes do not meet, so they are what is spread over CTAs.  Bound by the bytes of the rows.
 #include <algorithm>
@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
 
 // Short rows of weights, at most 32 V: a warp per sequence and KV head, the keys in registers.  The last kept row's key is
 // found bit by bit (32 counts at most; it ends when a count is what is needed), without a barrier.  2048 rows of 1150
-// weights: %s us, in a CTA each 48.
+// weights: 29 us, in a CTA each 48.
 template <int V>
 __global__ void __launch_bounds__(kWarpSelectThreads) evict_select_warp_kernel(const EvictArgs a) {
     pdl_wait();
@@ -510,8 +510,8 @@ cudaError_t launch_evict(const EvictArgs& args, cudaStream_t stream) {
     const long long most = (long long)a.max_blocks * a.block_size;
     const int sms = std::max(1, device_sm_count());
     trace_before("evict_select", stream);
-    // Few rows of weights are spread over clusters, as many CTAs as run at once (65536 positions of 8 heads: %s us
-    // with eight CTAs each, %s with one); weights that fit lie in shared memory.
+    // Few rows of weights are spread over clusters, as many CTAs as run at once (65536 positions of 8 heads: 23 us
+    // with eight CTAs each, 101 with one); weights that fit lie in shared memory.
     const int nc = most < 4096 ? 1 : rows * 8 <= 2 * sms ? 8 : rows * 4 <= 2 * sms ? 4 : rows * 2 <= 2 * sms ? 2 : 1;
     const int threads = nc == 8 ? 1024 : 512;            // (alone on its SM or not)
     const int warps = nc * threads / 32;
