@@ -592,9 +592,10 @@ size_t ll_workspace_size_weights(const ll_config* cfg, int32_t max_tokens, int32
 /* ll_layer_decode_step (and _q8) that adds its attention weights as
  * ll_paged_attention_decode_weights does, and can rotate by positions of the uncut sequence:
  * positions int32 [batch] are the new tokens' rotary positions (NULL: context_lens[b] - 1),
- * context_lens[b] - 1 stays the place in the cache; a position beyond the table sets
- * LL_DEV_BAD_POSITION as there.  y as that call's for the same positions.  Limits of both
- * calls. */
+ * context_lens[b] - 1 stays the place in the cache.  A position beyond the table sets
+ * LL_DEV_BAD_POSITION: that token's K and V are not written, and its sequence's y and what is
+ * added to its weights are unspecified.  y as that call's for the same positions.  Limits of
+ * both calls. */
 int ll_layer_decode_step_weights(const ll_config* cfg, const void* packed, const void* x, const ll_kv_pool* pool,
                                  const int32_t* block_table, int32_t max_blocks, const int32_t* context_lens,
                                  const int32_t* positions, int32_t batch, float* weights, int32_t weights_width, void* y,
@@ -622,7 +623,9 @@ typedef struct {
  *   weights_out                         as weights: its rows [0, m) the kept ones', [m, n) zeros,
  *                                       the rest as it was; weights itself or memory apart from it
  * Blocks behind the last one that m rows need are free for the caller to reuse; a block that
- * a moved row is written to must not be part of another sequence (fork it with ll_copy_blocks first).
+ * a moved row is written to must not be part of another sequence (fork it with ll_copy_blocks first)
+ * or stand twice in the table.  Tensors and outputs that share memory with each other or with
+ * weights, context_lens or keep are refused (LL_ERR_INVALID_ARG).
  * Cached keys keep the rotary positions they were written with: go on with positions of the
  * uncut sequence, not with the cut length.
  * Sizes that do not fit (n < 0 or beyond the table or weights_width, keep[b] < 0, m >

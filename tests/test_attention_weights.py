@@ -79,7 +79,7 @@ def rows(*pairs):
     return (api.ll_row_tensor * max(len(pairs), 1))(*pairs)
 
 
-EVICT = dict(tensors=rows((FAKE, 256), (FAKE, 256)), n=2, num_blocks=8, n_kv_heads=2, block=16, table=FAKE, max_blocks=8, ctx=FAKE,
+EVICT = dict(tensors=rows((6 * FAKE, 256), (5 * FAKE, 256)), n=2, num_blocks=8, n_kv_heads=2, block=16, table=FAKE, max_blocks=8, ctx=FAKE,
              batch=2, weights=2 * FAKE, width=128, keep=0, max_keep=64, sinks=1, recent=2, weights_out=2 * FAKE, kept=3 * FAKE,
              new_lens=4 * FAKE, status=FAKE)
 
@@ -91,10 +91,12 @@ EVICT = dict(tensors=rows((FAKE, 256), (FAKE, 256)), n=2, num_blocks=8, n_kv_hea
     (dict(max_keep=0), INVALID), (dict(sinks=-1), INVALID), (dict(recent=-1), INVALID), (dict(weights_out=0), INVALID),
     (dict(weights_out=2 * FAKE + 128), INVALID), (dict(kept=0), INVALID), (dict(kept=2 * FAKE + 256), INVALID), (dict(new_lens=0), INVALID),
     (dict(new_lens=FAKE + 4), INVALID), (dict(new_lens=3 * FAKE + 16), INVALID), (dict(keep=4 * FAKE), INVALID), (dict(status=0), INVALID),
-    (dict(tensors=rows((FAKE, 256), (FAKE, 6))), INVALID), (dict(tensors=rows((FAKE, 256), (FAKE, 0))), INVALID),
-    (dict(tensors=rows((FAKE, 256), (0, 256))), INVALID), (dict(tensors=rows((FAKE, 256), (FAKE + 2, 256))), INVALID),
-    (dict(tensors=rows((FAKE, 256), (FAKE, 4100))), UNSUPPORTED), (dict(num_blocks=1 << 26), UNSUPPORTED), (dict(max_blocks=1 << 27), UNSUPPORTED),
-    (dict(n_kv_heads=40000), UNSUPPORTED)])
+    (dict(tensors=rows((6 * FAKE, 256), (5 * FAKE, 6))), INVALID), (dict(tensors=rows((6 * FAKE, 256), (5 * FAKE, 0))), INVALID),
+    (dict(tensors=rows((6 * FAKE, 256), (0, 256))), INVALID), (dict(tensors=rows((6 * FAKE, 256), (5 * FAKE + 2, 256))), INVALID),
+    (dict(tensors=rows((6 * FAKE, 256), (5 * FAKE, 4100))), UNSUPPORTED), (dict(num_blocks=1 << 26), UNSUPPORTED), (dict(max_blocks=1 << 27), UNSUPPORTED),
+    (dict(n_kv_heads=40000), UNSUPPORTED), (dict(tensors=rows((6 * FAKE, 256), (6 * FAKE, 256))), INVALID),
+    (dict(tensors=rows((6 * FAKE, 256), (6 * FAKE + 8 * 2 * 16 * 256 - 4, 4))), INVALID), (dict(tensors=rows((6 * FAKE, 256), (2 * FAKE, 256))), INVALID),
+    (dict(new_lens=2 * FAKE + 64), INVALID), (dict(kept=5 * FAKE), INVALID)])
 def test_evict_refusals(bad, code):
     assert api.lib.ll_evict_rows(*{**EVICT, **bad}.values(), NULL) == code
 

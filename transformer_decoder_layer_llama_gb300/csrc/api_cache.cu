@@ -608,13 +608,6 @@ int ll_evict_rows(const ll_row_tensor* tensors, int32_t n_tensors, int32_t num_b
     if (n_tensors > ll::kEvictMaxTensors || !ll::block_size_ok(block_size) || batch > 65535 || n_kv_heads > 32767 ||
         (int64_t)max_blocks * block_size > kMaxPositions || (int64_t)num_blocks * n_kv_heads * block_size > (1LL << 31) - 1)
         return LL_ERR_UNSUPPORTED;
-    const size_t rows = (size_t)batch * n_kv_heads, weight_bytes = rows * weights_width * 4, kept_bytes = rows * max_keep * 4;
-    if (weights_out != weights && overlap(weights_out, weight_bytes, weights, weight_bytes)) return LL_ERR_INVALID_ARG;
-    if (overlap(kept, kept_bytes, weights, weight_bytes) || overlap(kept, kept_bytes, weights_out, weight_bytes) ||
-        overlap(new_lens, (size_t)batch * 4, context_lens, (size_t)batch * 4) ||
-        (keep && overlap(new_lens, (size_t)batch * 4, keep, (size_t)batch * 4)) ||
-        overlap(new_lens, (size_t)batch * 4, kept, kept_bytes))
-        return LL_ERR_INVALID_ARG;
     ll::EvictArgs a{};
     for (int32_t t = 0; t < n_tensors; ++t) {
         const ll_row_tensor& x = tensors[t];
@@ -624,6 +617,21 @@ int ll_evict_rows(const ll_row_tensor* tensors, int32_t n_tensors, int32_t num_b
         a.row_bytes[t] = (int)x.row_bytes;
         a.wide[t] = x.row_bytes % 16 == 0 && aligned16(x.data);
     }
+    // what is written: the tensors, weights_out (weights itself, or apart), kept, new_lens; apart from each other and what is read
+    const size_t rows = (size_t)batch * n_kv_heads, pool_rows = (size_t)num_blocks * n_kv_heads * block_size;
+    struct { const void* p; size_t bytes; } use[ll::kEvictMaxTensors + 6];
+    int written = 0;
+    for (; written < n_tensors; ++written) use[written] = {tensors[written].data, pool_rows * tensors[written].row_bytes};
+    use[written++] = {kept, rows * max_keep * 4};
+    use[written++] = {new_lens, (size_t)batch * 4};
+    use[written++] = {weights_out, rows * weights_width * 4};
+    int used = written;
+    if (weights != weights_out) use[used++] = {weights, rows * weights_width * 4};
+    use[used++] = {context_lens, (size_t)batch * 4};
+    if (keep) use[used++] = {keep, (size_t)batch * 4};
+    for (int i = 0; i < written; ++i)
+        for (int j = i + 1; j < used; ++j)
+            if (overlap(use[i].p, use[i].bytes, use[j].p, use[j].bytes)) return LL_ERR_INVALID_ARG;
     a.n_tensors = n_tensors;
     a.num_blocks = num_blocks;
     a.n_kv_heads = n_kv_heads;
