@@ -208,6 +208,44 @@ def test_unaligned_and_wide_rows_take_the_same_values():
     assert (np.abs(f64(a) - f64(b)) <= 2 * (2.0 ** -8 * np.abs(ref) + 2.0 ** -18)).all()
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("case,pad", [((3001, 32, 8, 128, 128), 0), ((3001, 32, 8, 128, 64), 4), ((2500, 70, 3, 64, 32), 0), ((2500, 3, 40, 256, 64), 0),
+                                      ((901, 5, 2, 128, 128), 4), ((901, 5, 2, 64, 64), 3)])
+def test_gradient_of_many_tokens(case, pad, layout, dtype):
+    """Many turns of a CTA; rows on 16 bytes, on 8 and on an element's (pad: elements before and between rows).  A chain
+    of a gain's sum: 3001 tokens x 40 heads over 600 CTAs, with the joins below 200."""
+    T, H, Hk, d, rot = case
+    gen, _, q, k, gains, pos, table, freq = setup(case, dtype, seed=5)
+
+    def place(x):
+        wide = torch.zeros(T, x.shape[1] * d + 8 + pad, dtype=dtype).cuda()
+        view = wide[:, pad:pad + x.shape[1] * d].view(T, x.shape[1], d)
+        view.copy_(x)
+        return view
+
+    q, k = place(q), place(k)
+    dq, dk = (place(torch.randn(x.shape, generator=gen).to(dtype).cuda()) for x in (q, k))
+    st = api.new_status()
+    outs = api.norm_rope_backward(dq, dk, q, k, *gains, pos.cuda(), table, eps=EPS, layout=layout, status=st)
+    check_status(st)
+    for x, dy, gain, dx, dg in zip((q, k), (dq, dk), gains, outs[:2], outs[2:]):
+        xn, dn, g = f64(x), f64(dy), f64(gain)
+        rx, rg = W.norm_rope_backward(dn, xn, g, pos.numpy(), freq, EPS, layout)
+        bx, bg = gradient_bounds(dn, xn, g, pos.numpy(), freq, rot, layout)
+        assert (np.abs(f64(dx) - rx) <= bx + UNIT[dtype] * np.abs(rx) + TINY).all()
+        assert (np.abs(f64(dg) - rg) <= bg + TINY).all()
+    bad = pos.clone()
+    bad[::7] = -1                                             # their rows stay as they were, the others do not change
+    over = api.norm_rope_backward(dq, dk, q, k, *gains, bad.cuda(), table, eps=EPS, layout=layout, q_grad=dq.clone(), k_grad=dk.clone(), status=st)
+    check_status(st, api.LL_DEV_BAD_POSITION)
+    for got, dx, dy in zip(over[:2], outs[:2], (dq, dk)):
+        assert torch.equal(got[::7], dy[::7])
+        keep = torch.ones(T, dtype=torch.bool)
+        keep[::7] = False
+        assert torch.equal(got[keep.cuda()], dx[keep.cuda()])
+
+
 def test_streams_and_graphs():
     case = (40, 8, 2, 128, 128)
     gen, _, q, k, gains, pos, table, _ = setup(case, torch.bfloat16)

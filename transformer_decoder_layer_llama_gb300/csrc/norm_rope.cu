@@ -361,6 +361,45 @@ struct HeadRows {
     int heads;
 };
 
+// A head's columns x0, x1 and dy in y0, y1, the gains in g0, g1: turns y into dn, g into g dn, and adds to the sums.
+template <int N, bool HALF, typename TURN>
+LL_DEVINL void grad_sums(const float2 (&x0)[N / 2], const float2 (&x1)[N / 2], float2 (&y0)[N / 2], float2 (&y1)[N / 2],
+                         float2 (&g0)[N / 2], float2 (&g1)[N / 2], bool turned, const TURN& turn, float2& sq, float2& dot) {
+    constexpr int P = N / 2, M = TURN::M;
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        if (turned) {                                     // dn = R^T dy
+            if (HALF) {
+                const float2 n0 = fma2(y0[i], turn.c[i], mul2(y1[i], turn.s[i]));
+                y1[i] = fma2(y1[i], turn.c[i], mul2(y0[i], make_float2(-turn.s[i].x, -turn.s[i].y)));
+                y0[i] = n0;
+            } else {                                      // (s swapped is -s)
+                y0[i] = fma2(y0[i], turn.c[i], mul2(swapped(y0[i]), swapped(turn.s[i])));
+                y1[i] = fma2(y1[i], turn.c[(P + i) % M], mul2(swapped(y1[i]), swapped(turn.s[(P + i) % M])));
+            }
+        }
+        g0[i] = mul2(y0[i], g0[i]);
+        g1[i] = mul2(y1[i], g1[i]);
+        sq = fma2(x1[i], x1[i], fma2(x0[i], x0[i], sq));
+        dot = fma2(g1[i], x1[i], fma2(g0[i], x0[i], dot));
+    }
+}
+
+// With the sums over the head: x0, x1 become dx, and dn x r goes to the gains' gradients.
+template <int N>
+LL_DEVINL void grad_values(float sum_sq, float sum_dot, float inv_d, float eps, float2 (&x0)[N / 2], float2 (&x1)[N / 2],
+                           const float2 (&y0)[N / 2], const float2 (&y1)[N / 2], const float2 (&g0)[N / 2], const float2 (&g1)[N / 2],
+                           float2 (&dg0)[N / 2], float2 (&dg1)[N / 2]) {
+    const float r = rsqrtf(sum_sq * inv_d + eps), f = -(sum_dot * inv_d * r * r);
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+        dg0[i] = fma2(y0[i], mul2(x0[i], both(r)), dg0[i]);
+        dg1[i] = fma2(y1[i], mul2(x1[i], both(r)), dg1[i]);
+        x0[i] = mul2(fma2(x0[i], both(f), g0[i]), both(r));
+        x1[i] = mul2(fma2(x1[i], both(f), g1[i]), both(r));
+    }
+}
+
 // The tokens go round the CTAs of a tensor (q's, then k's); a group has U heads of a token at a time, its loads all on
 // their way before the first is used, the token's position read a turn ahead.  A thread keeps the gain gradients of its
 // columns over all its tokens.  The sums of a CTA's groups meet in shared memory in a fixed order, those of the CTAs in a
@@ -434,35 +473,11 @@ __global__ void __launch_bounds__(kNormGradThreads, N == 4 ? kNormGradCtasPerSm 
                     wy1[u].unpack(y1);
                     load_gains<N, VEC>(m.gain + col.e0, col.n0, g0);
                     load_gains<N, VEC>(m.gain + col.e1, col.n1, g1);
-#pragma unroll
-                    for (int i = 0; i < P; ++i) {
-                        if (col.turn) {                   // dn = R^T dy
-                            if (HALF) {
-                                const float2 n0 = fma2(y0[i], turn.c[i], mul2(y1[i], turn.s[i]));
-                                y1[i] = fma2(y1[i], turn.c[i], mul2(y0[i], make_float2(-turn.s[i].x, -turn.s[i].y)));
-                                y0[i] = n0;
-                            } else {                      // (s swapped is -s)
-                                constexpr int M = Turn<N, HALF, VEC>::M;
-                                y0[i] = fma2(y0[i], turn.c[i], mul2(swapped(y0[i]), swapped(turn.s[i])));
-                                y1[i] = fma2(y1[i], turn.c[(P + i) % M], mul2(swapped(y1[i]), swapped(turn.s[(P + i) % M])));
-                            }
-                        }
-                        g0[i] = mul2(y0[i], g0[i]);
-                        g1[i] = mul2(y1[i], g1[i]);
-                        sq = fma2(x1[i], x1[i], fma2(x0[i], x0[i], sq));
-                        dot = fma2(g1[i], x1[i], fma2(g0[i], x0[i], dot));
-                    }
+                    grad_sums<N, HALF>(x0, x1, y0, y1, g0, g1, col.turn, turn, sq, dot);
                 }
                 const float sum_sq = group_sum<W>(sq.x + sq.y), sum_dot = group_sum<W>(dot.x + dot.y);
                 if (!on) continue;
-                const float r = rsqrtf(sum_sq * inv_d + a.eps), f = -(sum_dot * inv_d * r * r);
-#pragma unroll
-                for (int i = 0; i < P; ++i) {
-                    dg0[i] = fma2(y0[i], mul2(x0[i], both(r)), dg0[i]);
-                    dg1[i] = fma2(y1[i], mul2(x1[i], both(r)), dg1[i]);
-                    x0[i] = mul2(fma2(x0[i], both(f), g0[i]), both(r));
-                    x1[i] = mul2(fma2(x1[i], both(f), g1[i]), both(r));
-                }
+                grad_values<N>(sum_sq, sum_dot, inv_d, a.eps, x0, x1, y0, y1, g0, g1, dg0, dg1);
                 T* dst = m.dx + t * m.dx_stride + h * a.head_dim + col.e0;
                 Col::store(dst, x0, col.n0);
                 Col::store(dst + gap, x1, col.n1);
@@ -484,6 +499,147 @@ __global__ void __launch_bounds__(kNormGradThreads, N == 4 ? kNormGradCtasPerSm 
 #pragma unroll 8
         for (int i = 0; i < slots * rows; ++i) sum += s_dg[i * a.head_dim + e];
         a.partials[(size_t)blockIdx.x * a.head_dim + e] = sum;
+    }
+}
+
+// The same for BF16 rows that start on 16 bytes: a turn's heads (a token's, or those of several tokens with few heads)
+// come by bulk copies into shared memory while the turn before is worked on.  4096 tokens of 32 + 8 heads of 128: 31 us,
+// with loads into registers 37.5; of 256: 50 and 62; three stages 33, five or six CTAs per SM 33 and 35.  (float32, with
+// twice the bytes for the same work: no faster than loads into registers.)
+constexpr int kGradStages = 2;
+constexpr int kGradTurnBytes = kNormGradThreads * 8 * kNormGradHeads<__nv_bfloat16> * 2;       // of x, and of dy, at most
+
+template <bool HALF, int W>
+__global__ void __launch_bounds__(kNormGradThreads, kNormGradCtasPerSm)
+    norm_rope_grad_bulk_kernel(const NormRopeGradArgs a, const HeadSplit q_split, const HeadSplit k_split, int q_ctas, float inv_d) {
+    using T = __nv_bfloat16;
+    using Col = Column<T, 4, true>;
+    constexpr int P = 2, U = kNormGradHeads<T>, BYTES = kGradTurnBytes;
+    extern __shared__ __align__(128) uint8_t s_turn[];    // [kGradStages][x, dy]; then the groups' gain gradients
+    __shared__ uint64_t full[kGradStages];
+    __shared__ int abort_s;
+    const bool isq = (int)blockIdx.x < q_ctas;
+    const int ctas = isq ? q_ctas : gridDim.x - q_ctas, cta = isq ? blockIdx.x : blockIdx.x - q_ctas;
+    HeadRows<T> m;
+    m.x = static_cast<const T*>(isq ? a.q : a.k);
+    m.dy = static_cast<const T*>(isq ? a.dq : a.dk);
+    m.dx = static_cast<T*>(isq ? a.q_grad : a.k_grad);
+    m.x_stride = isq ? a.q_stride : a.k_stride;
+    m.dy_stride = isq ? a.dq_stride : a.dk_stride;
+    m.dx_stride = isq ? a.q_grad_stride : a.k_grad_stride;
+    m.gain = isq ? a.q_gain : a.k_gain;
+    m.heads = isq ? a.n_heads : a.n_kv_heads;
+    const int rows = isq ? q_split.rows : k_split.rows, slots = isq ? q_split.slots : k_split.slots;
+    const int parts = isq ? q_split.parts : k_split.parts, d = a.head_dim;
+    const int group = threadIdx.x / W, lane = threadIdx.x % W;
+    const int slot = group / rows, row = group - slot * rows;
+    const Columns<4, HALF, true> col(lane, d, a.rotary_dim);
+    const int gap = col.e1 - col.e0;
+    const bool worker = slot < slots && lane < q_split.lanes;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kGradStages; ++i) mbar_init(&full[i], 1);
+        abort_s = 0;
+        fence_mbar_init();
+    }
+    __syncthreads();
+    pdl_wait();
+    pdl_trigger();
+    const int t_step = ctas * slots;
+    const int rounds = a.tokens > cta * slots ? (a.tokens - cta * slots + t_step - 1) / t_step : 0, turns = rounds * parts;
+    // turn n: heads [part rows U, + rows U) of tokens t0 .. t0 + slots - 1; warp 0
+    const auto issue = [&](int n) {
+        const int t0 = cta * slots + n / parts * t_step, h0 = n % parts * rows * U, st = n % kGradStages;
+        const int count = min(slots, a.tokens - t0);
+        const uint32_t bytes = (uint32_t)(min(rows * U, m.heads - h0) * d * (int)sizeof(T));
+        if (threadIdx.x == 0) mbar_arrive_expect_tx(&full[st], 2 * count * bytes);
+        __syncwarp();
+        for (int i = threadIdx.x; i < 2 * count; i += 32) {
+            const int s = i >> 1, t = t0 + s;
+            const T* from = i & 1 ? m.dy + t * m.dy_stride : m.x + t * m.x_stride;
+            bulk_load(s_turn + (st * 2 + (i & 1)) * BYTES + s * rows * U * d * (int)sizeof(T), from + h0 * d, bytes, &full[st]);
+        }
+    };
+    int issued = 0;
+    if (threadIdx.x < 32)
+        for (; issued < min(kGradStages, turns); ++issued) issue(issued);
+    float2 g0[P], g1[P], dg0[P], dg1[P];
+#pragma unroll
+    for (int i = 0; i < P; ++i) g0[i] = g1[i] = dg0[i] = dg1[i] = make_float2(0.f, 0.f);
+    if (worker) {
+        load_gains<4, true>(m.gain + col.e0, 4, g0);
+        load_gains<4, true>(m.gain + col.e1, 4, g1);
+    }
+    int t = cta * slots + slot, n = 0;
+    int pos_next = slot < slots && t < a.tokens ? a.positions[t] : 0;
+    bool stop = false;
+    for (int round = 0; round < rounds && !stop; ++round, t += t_step) {
+        const int pos = pos_next;
+        pos_next = slot < slots && t + t_step < a.tokens ? a.positions[t + t_step] : 0;
+        const bool here = slot < slots && t < a.tokens, known = pos >= 0 && pos < a.max_position;
+        if (here && !known && lane == 0 && row == 0) flag_status(a.status, LL_DEV_BAD_POSITION);
+        const bool live = here && known && worker;
+        Turn<4, HALF, true> turn;
+        if (live && col.turn) turn.load(a.table, pos, a.rotary_dim >> 1, col);
+        for (int part = 0; part < parts; ++part, ++n) {
+            const int st = n % kGradStages, h0 = part * rows * U + row;
+            const T* sx = reinterpret_cast<const T*>(s_turn + st * 2 * BYTES) + (slot * rows * U + row) * d + col.e0;
+            mbar_wait_bounded(&full[st], (uint32_t)(n / kGradStages) & 1u, &abort_s, a.status);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int h = h0 + u * rows;
+                const bool on = live && h < m.heads;
+                float2 x0[P], x1[P], y0[P], y1[P], z0[P], z1[P], sq = make_float2(0.f, 0.f), dot = sq;
+                if (on) {
+                    Col c;
+                    const T* x = sx + u * rows * d;
+                    const T* dy = x + BYTES / sizeof(T);
+                    c.load(x, 4);
+                    c.unpack(x0);
+                    c.load(x + gap, 4);
+                    c.unpack(x1);
+                    c.load(dy, 4);
+                    c.unpack(y0);
+                    c.load(dy + gap, 4);
+                    c.unpack(y1);
+#pragma unroll
+                    for (int i = 0; i < P; ++i) {
+                        z0[i] = g0[i];
+                        z1[i] = g1[i];
+                    }
+                    grad_sums<4, HALF>(x0, x1, y0, y1, z0, z1, col.turn, turn, sq, dot);
+                }
+                const float sum_sq = group_sum<W>(sq.x + sq.y), sum_dot = group_sum<W>(dot.x + dot.y);
+                if (!on) continue;
+                grad_values<4>(sum_sq, sum_dot, inv_d, a.eps, x0, x1, y0, y1, z0, z1, dg0, dg1);
+                T* dst = m.dx + t * m.dx_stride + h * d + col.e0;
+                Col::store(dst, x0, 4);
+                Col::store(dst + gap, x1, 4);
+            }
+            stop = __syncthreads_or(abort_s);             // everyone has read the turn
+            if (stop) break;
+            if (threadIdx.x < 32 && issued < turns) issue(issued++);
+        }
+    }
+    if (stop && threadIdx.x == 0) {                       // wait (bounded) for the copies in flight before the CTA leaves
+        volatile int never = 0;
+        for (int i = max(0, issued - kGradStages); i < issued; ++i)
+            mbar_wait_bounded(&full[i % kGradStages], (uint32_t)(i / kGradStages) & 1u, &never, nullptr);
+    }
+    __syncthreads();
+    float* s_dg = reinterpret_cast<float*>(s_turn);       // [groups][head_dim], all turns have been read
+    if (worker) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            s_dg[group * d + col.e0 + i] = i & 1 ? dg0[i / 2].y : dg0[i / 2].x;
+            s_dg[group * d + col.e1 + i] = i & 1 ? dg1[i / 2].y : dg1[i / 2].x;
+        }
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < d; e += blockDim.x) {
+        float sum = 0.f;
+#pragma unroll 8
+        for (int i = 0; i < slots * rows; ++i) sum += s_dg[i * d + e];
+        a.partials[(size_t)blockIdx.x * d + e] = sum;
     }
 }
 
@@ -633,6 +789,22 @@ cudaError_t norm_rope_for(const NormRopeArgs& a, cudaStream_t stream) {
     return record(e, "norm_rope launch");
 }
 
+// f(W) for a HeadSplit's width.
+template <typename F>
+cudaError_t for_width(int width, F&& f) {
+    if (width == 4) return f(std::integral_constant<int, 4>{});
+    if (width == 8) return f(std::integral_constant<int, 8>{});
+    if (width == 16) return f(std::integral_constant<int, 16>{});
+    return f(std::integral_constant<int, 32>{});
+}
+
+template <typename K, typename... Args>
+cudaError_t launch_staged(K kernel, dim3 grid, dim3 block, int bytes, cudaStream_t stream, const Args&... args) {
+    const cudaError_t e = ensure_func_attr((const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes,
+                                           "cudaFuncSetAttribute(norm_rope_grad_bulk_kernel)");
+    return e != cudaSuccess ? e : launch_pdl(kernel, grid, block, bytes, stream, 1, args...);
+}
+
 template <typename T>
 cudaError_t norm_rope_grad_for(const NormRopeGradArgs& a, cudaStream_t stream) {
     constexpr int E = (int)sizeof(T);
@@ -642,6 +814,9 @@ cudaError_t norm_rope_grad_for(const NormRopeGradArgs& a, cudaStream_t stream) {
     s.vec = s.vec &&
             (a.n_heads == 0 || (rows_on(a.q, a.q_stride, E, bytes) && rows_on(a.dq, a.dq_stride, E, bytes) && rows_on(a.q_grad, a.q_grad_stride, E, bytes) && rows_on(a.q_gain, 0, 4, 16))) &&
             (a.n_kv_heads == 0 || (rows_on(a.k, a.k_stride, E, bytes) && rows_on(a.dk, a.dk_stride, E, bytes) && rows_on(a.k_grad, a.k_grad_stride, E, bytes) && rows_on(a.k_gain, 0, 4, 16)));
+    const bool bulk = E == 2 && s.vec && s.n == 4 &&
+                      (a.n_heads == 0 || (rows_on(a.q, a.q_stride, E, 16) && rows_on(a.dq, a.dq_stride, E, 16))) &&
+                      (a.n_kv_heads == 0 || (rows_on(a.k, a.k_stride, E, 16) && rows_on(a.dk, a.dk_stride, E, 16)));
     int q_rows = 0, k_rows = 0;                           // of partials
     cudaError_t e = cudaSuccess;
     trace_before("norm_rope_grad", stream);
@@ -659,7 +834,13 @@ cudaError_t norm_rope_grad_for(const NormRopeGradArgs& a, cudaStream_t stream) {
             k_rows = std::min(k_rows, most - q_rows);
         }
         const size_t smem = (size_t)std::max(qs.slots * qs.rows, ks.slots * ks.rows) * a.head_dim * sizeof(float);   // at most 8 KB
-        e = for_shape(s, [&](auto n, auto w, auto vec) {
+        if (bulk) {
+            e = for_width(qs.width, [&](auto w) {
+                const auto kernel = a.interleaved ? norm_rope_grad_bulk_kernel<false, w.value> : norm_rope_grad_bulk_kernel<true, w.value>;
+                return launch_staged(kernel, dim3(q_rows + k_rows), dim3(kNormGradThreads), 2 * kGradStages * kGradTurnBytes, stream, a, qs, ks,
+                                     q_rows, 1.f / (float)a.head_dim);
+            });
+        } else e = for_shape(s, [&](auto n, auto w, auto vec) {
             return launch_pdl(a.interleaved ? norm_rope_grad_kernel<T, n.value, false, w.value, vec.value> : norm_rope_grad_kernel<T, n.value, true, w.value, vec.value>,
                               dim3(q_rows + k_rows), dim3(kNormGradThreads), smem, stream, 1, a, qs, ks, q_rows, 1.f / (float)a.head_dim);
         });
