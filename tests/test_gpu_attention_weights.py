@@ -257,6 +257,15 @@ def test_prompt(case):
         assert more > max(new) or torch.equal(again, w)
 
 
+@pytest.mark.parametrize("case", [
+    ([(37 * i) % 900 for i in range(70)], [min((37 * i) % 900, i % 5) for i in range(70)], 4, 1, 64, 16), ([39000], [20], 8, 1, 128, 256),
+    ([9000] + [300] * 90, [1] * 91, 16, 8, 64, 64), ([300] * 40 + [0, 7000], [2] * 40 + [0, 64], 4, 2, 128, 128), ([500], [84], 3, 1, 128, 32),
+    ([500, 600], [85, 3], 3, 1, 128, 32), ([2600] * 5, [16] * 5, 32, 32, 64, 128)])
+def test_windows(case):
+    """Few rows: every CTA has a share of all sequences' and heads' keys, so that a head's may lie in many parts."""
+    test_prompt(case)
+
+
 def test_prompt_equals_its_single_tokens():
     """A chunk's weights are those of its rows as decode steps, but for rounding."""
     case = ([150, 90], [7, 3], 8, 2, 128, 32)

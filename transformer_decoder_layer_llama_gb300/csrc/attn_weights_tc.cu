@@ -4,7 +4,8 @@
 // A column sum of P needs every row's normaliser first, and the scores of all pairs are too many to keep (4 bytes a
 // pair), so they are computed twice:
 //   ROWS  128 query rows (tokens x heads of a KV head) in the lanes, keys in the columns: a thread has a row and runs over
-//         its scores with a running maximum and sum.  Long rows are split into `pieces` and joined by a small kernel.
+//         its scores with a running maximum and sum.  Long rows are split into `pieces`, which a small kernel joins, or
+//         COLS itself where a sequence has few rows.
 //   COLS  128 keys in the lanes, query rows in the columns: a thread has a key, adds 2^(score - lse of the column) and at
 //         the end adds its sum to the weight.  One thread per weight: no atomics, the same bits every time.
 // Both are one persistent kernel.  Two tiles of 128 rows (A) stay in shared memory while tiles of 256 rows (B) stream past
@@ -33,7 +34,8 @@ constexpr int kObsPieceTiles = 2;        // at least, of a piece of a row (2048 
 constexpr int kObsLoad = 64;             // columns of one load from TMEM (8192 rows of 64 heads over 8: rows 461 us, keys 538; 32: 584, 620)
 constexpr int kObsItems = 4;             // looked up ahead
 
-// FEW (COLS only): no sequence has more rows than one B tile, which then stays for all of an item's keys.
+// FEW: no sequence has more rows than two A tiles.  They then stay: in ROWS beside the keys of a CTA's whole share, in COLS
+// as the B tile that all of its keys meet.
 template <int D, bool FEW>
 struct ObsLayout {
     static constexpr uint32_t A_TILE = kTile * D * 2;        // [D / 64][128 rows][128 B], 128-byte swizzle
@@ -68,13 +70,14 @@ struct ObsItem {
     int row0, n, ctx, b, hk;
     int pair, pair_step, pairs;          // A tiles 2 pair and 2 pair + 1, pair += pair_step while below pairs
     int piece, j0, j1;                   // ROWS: key tiles of this piece
+    int pieces;                          // FEW: of these rows
     int kind;                            // kObsEnd, kObsWork, or (not handed on) kObsNone, kObsEmpty
 };
 constexpr int kObsEnd = 0, kObsWork = 1, kObsNone = 2, kObsEmpty = 3;
 
 template <bool ROWS>
 struct ObsSteps {
-    int first0, Tb, pair_keys, last_;    // COLS: positions before the call's first row, its tokens per B tile
+    int first0, Tb, last_;               // COLS: positions before the call's first row, its tokens per B tile
     LL_DEVINL ObsSteps(const ObsItem& w, int G) {
         Tb = kWide / G;
         first0 = ROWS ? w.j0 : w.ctx - w.n;
@@ -125,6 +128,43 @@ LL_DEVINL ObsItem obs_item(const ObserveArgs& a, long long idx, int G) {
     return w;
 }
 
+// FEW: the key tiles of all sequences and heads, and how many of them each CTA has (so many that no head's are in more than
+// a.pieces parts).  A warp.
+struct ObsShare {
+    long long total, each;
+};
+
+LL_DEVINL ObsShare obs_share(const ObserveArgs& a, bool flag) {
+    long long sum = 0;
+    int most = 0;
+    for (int b = threadIdx.x & 31; b < a.batch; b += 32) {
+        const ObsSeq s = obs_sequence(a, b, flag);
+        const int tiles = s.n > 0 ? (s.ctx + kWide - 1) / kWide : 0;
+        sum += tiles;
+        most = max(most, tiles);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    most = __reduce_max_sync(0xffffffffu, most);
+    ObsShare sh;
+    sh.total = sum * a.n_kv_heads;
+    sh.each = max(max(1ll, (sh.total + gridDim.x - 1) / gridDim.x), (long long)((most + a.pieces - 2) / (a.pieces - 1)));
+    return sh;
+}
+
+// The sum of x over the lanes before this one; adds that of all to `total`.
+LL_DEVINL long long scan_before(long long x, long long& total) {
+    const int lane = threadIdx.x & 31;
+    long long run = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, run, o);
+        if (lane >= o) run += y;
+    }
+    total += __shfl_sync(0xffffffffu, run, 31);
+    return run - x;
+}
+
 // Barrier of the four warps of an A tile, with an OR of `pred` for all its threads.
 LL_DEVINL bool group_bar_any(int id, bool pred) {
     uint32_t r;
@@ -158,7 +198,7 @@ template <int D, bool ROWS, bool FEW>
 __global__ void __launch_bounds__(kObsThreads, 1)
     attn_weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK, const ObserveArgs a,
                         long long items) {
-    using L = ObsLayout<D, FEW>;
+    using L = ObsLayout<D, FEW && !ROWS>;
     constexpr int STAGES = L::STAGES, ABUFS = L::A_BUFS, LOAD = kObsLoad;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -215,41 +255,88 @@ __global__ void __launch_bounds__(kObsThreads, 1)
     };
 
     if (warp == kObsItemWarp) {
-        // ---------------------------------------------------- items: 32 at a time are looked up, those with work handed on
+        // ---------------------------------------------------- items
         int k = 0;
         bool ok = true;
-        for (long long round = 0; ok; round += 32) {
-            // every other round reversed: a CTA with one of the longest items has one of the shortest next
-            const long long turn = round + lane, idx = turn * gridDim.x + (turn & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-            ObsItem w;
-            w.kind = turn * gridDim.x < items ? kObsNone : kObsEnd;
-            if (idx < items) w = obs_item<ROWS>(a, idx, G);
-            uint32_t todo = __ballot_sync(0xffffffffu, w.kind != kObsNone);
-            if (todo == 0) continue;
-            while (todo && ok) {
-                const int l = __ffs(todo) - 1;
-                todo &= todo - 1;
-                const int kind = __shfl_sync(0xffffffffu, w.kind, l);
-                if (ROWS && kind == kObsEmpty) {             // nothing is left for this piece of the rows
-                    const int pair = __shfl_sync(0xffffffffu, w.pair, l), n = __shfl_sync(0xffffffffu, w.n, l);
-                    const int hk = __shfl_sync(0xffffffffu, w.hk, l), row0 = __shfl_sync(0xffffffffu, w.row0, l);
-                    const int piece = __shfl_sync(0xffffffffu, w.piece, l);
-                    const int64_t lse0 = ((int64_t)hk * a.tokens + row0) * G;
-                    for (int r = lane; r < 2 * Tq * G; r += 32) {
-                        const int64_t i = (int64_t)2 * pair * Tq * G + r;
-                        if (i < (int64_t)n * G) a.part[(lse0 + i) * a.pieces + piece] = make_float2(-INFINITY, 0.f);
+        // hands an item on, from lane l
+        const auto hand_on = [&](const ObsItem& w, int l) {
+            const int slot = k % kObsItems;
+            ok = __all_sync(0xffffffffu, mbar_wait_bounded(&i_empty[slot], ((uint32_t)(k / kObsItems) & 1u) ^ 1u, &abort_s, status));
+            if (ok && lane == l) {
+                s_item[slot] = w;
+                mbar_arrive(&i_full[slot]);                  // (releases the item)
+            }
+            __syncwarp();
+            ++k;
+        };
+        if constexpr (FEW) {
+            // every CTA has an equal share of all sequences' and heads' key tiles, one after another (32 rows of 8 contexts to
+            // 16384: 52 + 53 us; 56 + 63 with items of equal parts of a context, whose rows come anew for each; one row of
+            // 16 contexts to 32768: 128 + 121, 185 + 145)
+            const ObsShare sh = obs_share(a, ROWS && blockIdx.x == 0);
+            const long long g0 = sh.each * blockIdx.x, g1 = min(sh.total, g0 + sh.each);
+            long long before = 0;                            // tiles of the sequences before
+            for (int b0 = 0; ok && b0 < a.batch && before < g1; b0 += 32) {
+                const ObsSeq s = b0 + lane < a.batch ? obs_sequence(a, b0 + lane, false) : ObsSeq{0, 0, 0};
+                const int tiles = s.n > 0 ? (s.ctx + kWide - 1) / kWide : 0;
+                const long long all = (long long)tiles * a.n_kv_heads, first = before, start = first + scan_before(all, before);
+                uint32_t todo = __ballot_sync(0xffffffffu, all > 0 && start < g1 && start + all > g0);
+                while (todo && ok) {
+                    const int l = __ffs(todo) - 1;
+                    todo &= todo - 1;
+                    const long long from = __shfl_sync(0xffffffffu, start, l);
+                    const int t = __shfl_sync(0xffffffffu, tiles, l);
+                    for (int hk = (int)(max(0ll, g0 - from) / t); ok && hk < a.n_kv_heads && from + (long long)hk * t < g1; ++hk) {
+                        const long long own = from + (long long)hk * t;          // this head's first tile
+                        ObsItem w;
+                        w.row0 = s.row0;
+                        w.n = s.n;
+                        w.ctx = s.ctx;
+                        w.b = b0 + l;
+                        w.hk = hk;
+                        w.j0 = (int)(max(g0, own) - own);
+                        w.j1 = (int)(min(g1, own + t) - own);
+                        w.pair = ROWS ? 0 : w.j0;
+                        w.pairs = ROWS ? 1 : w.j1;
+                        w.pair_step = 1;
+                        w.piece = (int)(blockIdx.x - own / sh.each);
+                        w.pieces = (int)((own + t - 1) / sh.each - own / sh.each) + 1;
+                        w.kind = kObsWork;
+                        hand_on(w, l);
                     }
-                    continue;
                 }
-                const int slot = k % kObsItems;
-                ok = __all_sync(0xffffffffu, mbar_wait_bounded(&i_empty[slot], ((uint32_t)(k / kObsItems) & 1u) ^ 1u, &abort_s, status));
-                if (ok && lane == l) {
-                    s_item[slot] = w;
-                    mbar_arrive(&i_full[slot]);              // (releases the item)
+            }
+            ObsItem end;
+            end.kind = kObsEnd;
+            if (ok) hand_on(end, 0);
+        } else {
+            // 32 at a time are looked up, those with work handed on
+            for (long long round = 0; ok; round += 32) {
+                // every other round reversed: a CTA with one of the longest items has one of the shortest next
+                const long long turn = round + lane, idx = turn * gridDim.x + (turn & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+                ObsItem w;
+                w.kind = turn * gridDim.x < items ? kObsNone : kObsEnd;
+                if (idx < items) w = obs_item<ROWS>(a, idx, G);
+                uint32_t todo = __ballot_sync(0xffffffffu, w.kind != kObsNone);
+                if (todo == 0) continue;
+                while (todo && ok) {
+                    const int l = __ffs(todo) - 1;
+                    todo &= todo - 1;
+                    const int kind = __shfl_sync(0xffffffffu, w.kind, l);
+                    if (ROWS && kind == kObsEmpty) {             // nothing is left for this piece of the rows
+                        const int pair = __shfl_sync(0xffffffffu, w.pair, l), n = __shfl_sync(0xffffffffu, w.n, l);
+                        const int hk = __shfl_sync(0xffffffffu, w.hk, l), row0 = __shfl_sync(0xffffffffu, w.row0, l);
+                        const int piece = __shfl_sync(0xffffffffu, w.piece, l);
+                        const int64_t lse0 = ((int64_t)hk * a.tokens + row0) * G;
+                        for (int r = lane; r < 2 * Tq * G; r += 32) {
+                            const int64_t i = (int64_t)2 * pair * Tq * G + r;
+                            if (i < (int64_t)n * G) a.part[(lse0 + i) * a.pieces + piece] = make_float2(-INFINITY, 0.f);
+                        }
+                        continue;
+                    }
+                    hand_on(w, l);
+                    if (kind == kObsEnd) ok = false;
                 }
-                __syncwarp();
-                ++k;
-                if (kind == kObsEnd) ok = false;
             }
         }
     } else if (warp == 0) {
@@ -313,7 +400,7 @@ __global__ void __launch_bounds__(kObsThreads, 1)
                     load_keys(dst, pair * kWide, blk, true, &a_full[buf]);
                 }
                 ++a_issued[buf];
-                if (FEW && pair != w.pair) continue;         // (the rows are there)
+                if (FEW && !ROWS && pair != w.pair) continue;   // (the rows are there)
                 for (int j = steps.first(pair); j < steps.last(); ++j, ++step) {
                     const int st = step % STAGES;
                     ok = __all_sync(0xffffffffu, mbar_wait_bounded(&b_empty[st], ((uint32_t)(step / STAGES) & 1u) ^ 1u, &abort_s, status));
@@ -380,7 +467,7 @@ __global__ void __launch_bounds__(kObsThreads, 1)
                             }
                             tc_commit(&s_full[h]);
                         }
-                        if (!FEW || pair + w.pair_step >= w.pairs) {
+                        if (!FEW || ROWS || pair + w.pair_step >= w.pairs) {
                             tc_commit(&b_empty[st]);
                             ++bstep;
                         }
@@ -469,7 +556,7 @@ __global__ void __launch_bounds__(kObsThreads, 1)
                 }
                 if (valid && !abort_s) {
                     const int64_t i = ((int64_t)w.hk * a.tokens + w.row0) * G + (int64_t)(2 * w.pair + h) * Tq * G + r;
-                    if (a.pieces == 1) a.lse[i] = m == -INFINITY ? INFINITY : m + log2f(l);
+                    if (!FEW && a.pieces == 1) a.lse[i] = m == -INFINITY ? INFINITY : m + log2f(l);
                     else a.part[i * a.pieces + w.piece] = make_float2(m, l);
                 }
                 __syncwarp();
@@ -478,10 +565,21 @@ __global__ void __launch_bounds__(kObsThreads, 1)
                 more = next_more;
             }
         } else {
-            // the normaliser of column c of query tile j (+infinity: adds nothing)
+            // the normaliser of column c of query tile j (+infinity: adds nothing).  FEW: from its pieces, once per item.  (More
+            // rows have theirs read a tile ahead, which joining on the way would hold up: 8192 rows 671 us for 538.)
             const auto column = [&](const ObsItem& w, int j, int c) {
                 const int tok = j * Tq + c / G;
-                return c < Tq * G && tok < w.n ? __ldg(a.lse + ((int64_t)w.hk * a.tokens + w.row0) * G + (int64_t)j * Tq * G + c) : INFINITY;
+                if (c >= Tq * G || tok >= w.n) return INFINITY;
+                const int64_t i = ((int64_t)w.hk * a.tokens + w.row0) * G + (int64_t)j * Tq * G + c;
+                if (!FEW) return __ldg(a.lse + i);
+                const float2* part = a.part + i * a.pieces;
+                float2 x = __ldg(part);
+                for (int p = 1; p < w.pieces; ++p) {
+                    const float2 y = __ldg(part + p);
+                    const float m = max3(x.x, y.x, y.x), base = m == -INFINITY ? 0.f : m;
+                    x = make_float2(m, ex2_approx(x.x - base) * x.y + ex2_approx(y.x - base) * y.y);
+                }
+                return x.x == -INFINITY ? INFINITY : x.x + log2f(x.y);
             };
             float next[2];                                   // of the columns r and r + 128, which this thread brings
             const auto columns = [&](const ObsItem& w, int j) {
@@ -513,7 +611,7 @@ __global__ void __launch_bounds__(kObsThreads, 1)
                         if (last_step && last_pair) {        // the next item, and what its first step needs
                             next_more = __all_sync(0xffffffffu, take(k + 1, nw));
                             if (next_more) columns(nw, ObsSteps<ROWS>(nw, G).first(nw.pair));
-                        } else {
+                        } else if (!FEW) {                   // (FEW: the same rows for every pair)
                             columns(w, last_step ? steps.first(pair + w.pair_step) : j + 1);
                         }
                         const bool got = mbar_wait_bounded(&s_full[h], (uint32_t)step & 1u, &abort_s, status);
@@ -591,6 +689,7 @@ __global__ void __launch_bounds__(256) attn_weights_join_kernel(const float2* pa
 struct ObsSplit {
     long long row_items, key_items;
     int pieces, key_ctas;
+    bool few;
 };
 
 ObsSplit obs_split(int batch, int max_new, int n_heads, int n_kv_heads, int max_blocks, int block_size) {
@@ -603,6 +702,12 @@ ObsSplit obs_split(int batch, int max_new, int n_heads, int n_kv_heads, int max_
     s.key_ctas = (int)std::max<long long>(1, std::min<long long>((kKeyItems + bh - 1) / bh, tiles));
     s.row_items = items * s.pieces;
     s.key_items = bh * s.key_ctas;
+    s.few = max_new <= 2 * Tq;
+    if (s.few) {                                             // shares: a head's keys in at most so many parts
+        const long long n = std::max(1, device_sm_count());
+        s.pieces = (int)std::max<long long>(2, std::min({(n + n_kv_heads - 1) / n_kv_heads + 1, 4 * n / bh + 2, tiles}));
+        s.row_items = s.key_items = bh * tiles;
+    }
     return s;
 }
 
@@ -613,7 +718,7 @@ cudaError_t launch_pass(const ObserveArgs& a, const CUtensorMap& tmK, long long 
     if (!make_tmap_heads_sw128(&tmQ, a.q, D, (uint64_t)a.n_heads, (uint64_t)a.tokens, (uint32_t)G, (uint32_t)((ROWS ? kTile : kWide) / G)))
         return cudaErrorInvalidValue;
     const auto kernel = attn_weights_kernel<D, ROWS, FEW>;
-    const size_t smem = ObsLayout<D, FEW>::TOTAL + 1024;
+    const size_t smem = ObsLayout<D, FEW && !ROWS>::TOTAL + 1024;
     cudaError_t e = ensure_func_attr((const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem,
                                      "cudaFuncSetAttribute(attn_weights_kernel)");
     if (e != cudaSuccess) return e;
@@ -630,6 +735,10 @@ cudaError_t observe_for(const ObserveArgs& a, const ObsSplit& s, cudaStream_t st
     CUtensorMap tmK;
     const uint64_t rows = (uint64_t)a.num_blocks * a.n_kv_heads * a.block_size;
     if (!make_tmap_bf16_sw128(&tmK, a.k_pool, D, rows, (uint32_t)std::min(a.block_size, kTile))) return cudaErrorInvalidValue;
+    if (s.few) {
+        const cudaError_t e = launch_pass<D, true, true>(a, tmK, s.row_items, stream);
+        return e != cudaSuccess ? e : launch_pass<D, false, true>(a, tmK, s.key_items, stream);
+    }
     cudaError_t e = launch_pass<D, true, false>(a, tmK, s.row_items, stream);
     if (e != cudaSuccess) return e;
     if (a.pieces > 1) {
@@ -641,23 +750,21 @@ cudaError_t observe_for(const ObserveArgs& a, const ObsSplit& s, cudaStream_t st
         if (e == cudaSuccess) e = cudaGetLastError();
         if (e != cudaSuccess) return record(e, "attn_weights_join launch");
     }
-    // rows of one B tile at most: they stay, and the keys' tiles are the ones with two buffers
-    return a.max_new <= kWide / (a.n_heads / a.n_kv_heads) ? launch_pass<D, false, true>(a, tmK, s.key_items, stream)
-                                                           : launch_pass<D, false, false>(a, tmK, s.key_items, stream);
+    return launch_pass<D, false, false>(a, tmK, s.key_items, stream);
 }
 
 }  // namespace
 
 bool observe_fits(int batch, int max_new, int n_heads, int n_kv_heads, int max_blocks, int block_size) {
     const ObsSplit s = obs_split(batch, std::max(max_new, 1), n_heads, n_kv_heads, max_blocks, block_size);
-    return s.row_items < (1LL << 31) && s.key_items < (1LL << 31);
+    return s.few || (s.row_items < (1LL << 31) && s.key_items < (1LL << 31));
 }
 
 size_t observe_scratch_bytes(int batch, int tokens, int max_new, int n_heads, int n_kv_heads, int max_blocks, int block_size) {
-    // the normalisers, and room for the pieces of rows
+    // the normalisers, and a (max, sum) for each piece of a row
     const size_t rows = (size_t)tokens * n_heads;
-    const ObsSplit s = obs_split(batch, std::max(max_new, 1), n_heads, n_kv_heads, max_blocks, block_size);
-    return (rows * 4 + 15) / 16 * 16 + (s.pieces > 1 ? rows * s.pieces * 8 : 0);
+    return (rows * sizeof(float) + 15) / 16 * 16 +
+           rows * obs_split(batch, std::max(max_new, 1), n_heads, n_kv_heads, max_blocks, block_size).pieces * sizeof(float2);
 }
 
 cudaError_t launch_observe(ObserveArgs a, void* workspace, cudaStream_t stream) {

@@ -305,7 +305,7 @@ struct ObserveArgs {
     float* weights;                // [batch][n_kv_heads][weights_width], added to
     int weights_width;
     float* lse;                    // scratch: log2 of a row's softmax denominator [n_kv_heads][tokens][group]
-    float2* part;                  //          (max, sum) of the pieces of a row [..][pieces]
+    float2* part;                  //          (max, sum of 2^(score - max)) of the pieces of a row [..][pieces]
     int pieces, key_ctas;          // set by the launcher
     int32_t* status;
 };
