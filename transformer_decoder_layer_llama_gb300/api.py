@@ -228,7 +228,14 @@ def _stream(stream):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+_Tensor = torch.Tensor
+
+
 def _need(t, name, dtype, device=True, shape=None):
+    # (what holds in nearly every call first: the checks of a call of few tokens take as long as its kernels)
+    if isinstance(t, _Tensor) and t.dtype is dtype and t.is_contiguous() and (t.is_cuda or not device) and \
+            (shape is None or t.shape == shape):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
     if t.dtype != dtype:
@@ -577,7 +584,7 @@ def _rows3(t, name, dtype):
 def _status(t):
     """A status word that the caller passed: the kernels set its bits as an int32."""
     _need(t, "status", torch.int32)
-    if t.numel() < 1:
+    if not t.numel():
         raise ValueError("status must hold one number")
     return t
 
@@ -711,9 +718,13 @@ def _heads(t, name, dtype, shape=None):
     if t is None:
         return ll_head_rows(None, 0, 0)
     stride = _rows3(t, name, dtype)
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    return ll_head_rows(t.data_ptr(), stride, t.shape[1])
+    own = t.shape
+    if shape is not None and own != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(own)}")
+    return ll_head_rows(t.data_ptr(), stride, own[1])
+
+
+_NORM_DTYPES = {torch.bfloat16: LL_BF16, torch.float32: LL_F32}
 
 
 def _norm_args(q, k, q_gain, k_gain, positions, table, layout, name):
@@ -721,7 +732,7 @@ def _norm_args(q, k, q_gain, k_gain, positions, table, layout, name):
     x = q if q is not None else k
     if x is None:
         raise ValueError("q and k are both None")
-    if not isinstance(x, torch.Tensor) or x.dtype not in (torch.bfloat16, torch.float32):
+    if not isinstance(x, _Tensor) or x.dtype not in _NORM_DTYPES:
         raise TypeError("q and k must be bfloat16 or float32 tensors")
     if layout not in LL_ROPE_LAYOUTS:
         raise ValueError(f"layout must be one of {sorted(LL_ROPE_LAYOUTS)}, got {layout!r}")
@@ -730,20 +741,23 @@ def _norm_args(q, k, q_gain, k_gain, positions, table, layout, name):
             if t is not None and t.requires_grad:
                 raise ValueError(f"{name} is not recorded by autograd: use torch.no_grad(), and norm_rope_backward for "
                                  "the gradient")
-    qh, kh = _heads(q, "q", x.dtype), _heads(k, "k", x.dtype)
+    dtype = x.dtype
+    qh, kh = _heads(q, "q", dtype), _heads(k, "k", dtype)
     T, _, d = x.shape
     if q is not None:
-        _need(q_gain, "q_gain", torch.float32, shape=(d,))
+        _need(q_gain, "q_gain", torch.float32, True, (d,))
     if k is not None:
-        if k.shape[0] != T or k.shape[2] != d:
-            raise ValueError(f"k must be [{T}, n_kv_heads, {d}], got {tuple(k.shape)}")
-        _need(k_gain, "k_gain", torch.float32, shape=(d,))
-    _need(positions, "positions", torch.int32, shape=(T,))
+        if q is not None:
+            Tk, _, dk = k.shape
+            if Tk != T or dk != d:
+                raise ValueError(f"k must be [{T}, n_kv_heads, {d}], got {tuple(k.shape)}")
+        _need(k_gain, "k_gain", torch.float32, True, (d,))
+    _need(positions, "positions", torch.int32, True, (T,))
     _need(table, "table", torch.float32)
     rows = table.shape
     if len(rows) != 3 or rows[2] != 2 or not 2 <= 2 * rows[1] <= d:
         raise ValueError("table must be [max_position, rotary_dim / 2, 2] with rotary_dim <= head_dim")
-    return x.dtype, T, d, qh, kh
+    return dtype, T, d, qh, kh
 
 
 def _head_out(t, out, name):
@@ -776,7 +790,7 @@ def norm_rope(q, k, q_gain, k_gain, positions, table, eps=1e-5, layout="half", q
     dev = _on(x, k, q_out, k_out, q_gain, k_gain, positions, table, status)
     if stream is not None:
         _made(stream, dev, *(t if g is None else None for g, t in zip(given, (q_out, k_out, status))))
-    _call("ll_norm_rope", lib.ll_norm_rope, dev, stream, qh, kh, LL_F32 if dtype is torch.float32 else LL_BF16,
+    _call("ll_norm_rope", lib.ll_norm_rope, dev, stream, qh, kh, _NORM_DTYPES[dtype],
           q_gain.data_ptr() if q is not None else None, k_gain.data_ptr() if k is not None else None, eps,
           positions.data_ptr(), T, d, 2 * table.shape[1], LL_ROPE_LAYOUTS[layout], table.data_ptr(), table.shape[0], qo, ko,
           status.data_ptr())
@@ -822,8 +836,8 @@ def norm_rope_backward(dq, dk, q, k, q_gain, k_gain, positions, table, eps=1e-5,
     dev = _on(x, k, dq, dk, *outs, q_gain, k_gain, positions, table, workspace, status)
     if stream is not None:
         _made(stream, dev, *(t if g is None else None for g, t in zip(given, (*outs, workspace, status))))
-    _call("ll_norm_rope_backward", lib.ll_norm_rope_backward, dev, stream, dqh, dkh, qh, kh,
-          LL_F32 if dtype is torch.float32 else LL_BF16, q_gain.data_ptr() if q is not None else None,
+    _call("ll_norm_rope_backward", lib.ll_norm_rope_backward, dev, stream, dqh, dkh, qh, kh, _NORM_DTYPES[dtype],
+          q_gain.data_ptr() if q is not None else None,
           k_gain.data_ptr() if k is not None else None, eps, positions.data_ptr(), T, d, 2 * table.shape[1],
           LL_ROPE_LAYOUTS[layout], table.data_ptr(), table.shape[0], qo, ko,
           q_gain_grad.data_ptr() if q is not None else None, k_gain_grad.data_ptr() if k is not None else None,
@@ -1226,7 +1240,7 @@ def evict_rows(pool, block_table, context_lens, weights, keep, max_keep=None, si
     if stream is not None:
         _made(stream, dev, *(t if g is None else None for g, t in zip(given, (kept, new_lens, status))))
     rows = (ll_row_tensor * len(tensors))(
-        *((t.data_ptr(), t.element_size() * (t.shape[3] if t.dim() == 4 else 1)) for t in tensors))
+        *[(t.data_ptr(), t.element_size() * (t.shape[3] if t.dim() == 4 else 1)) for t in tensors])
     _call("ll_evict_rows", lib.ll_evict_rows, dev, stream, rows, len(tensors), nb, Hkv, bs, block_table.data_ptr(),
           block_table.shape[1], context_lens.data_ptr(), B, weights.data_ptr(), width,
           per.data_ptr() if per is not None else None, max_keep, int(sinks), int(recent), weights_out.data_ptr(),
