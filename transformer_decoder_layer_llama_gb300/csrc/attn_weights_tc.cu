@@ -30,7 +30,7 @@ constexpr int kWide = 256;               // rows of a B tile, and of a pair of A
 constexpr int kObsThreads = 352;         // TMA, MMA, four warps for each A tile's scores, items
 constexpr int kObsItemWarp = 10;
 constexpr float kLog2eObs = 1.4426950408889634f;
-constexpr int kObsPieceTiles = 2;        // at least, of a piece of a row (2048 rows of 32 heads: 33 us, 46 with 4)
+constexpr int kObsPieceTiles = 2;        // at least, of a piece of a row (the rows are fetched for each)
 constexpr int kObsLoad = 64;             // columns of one load from TMEM (8192 rows of 64 heads over 8: rows 461 us, keys 538; 32: 584, 620)
 constexpr int kObsItems = 4;             // looked up ahead
 
@@ -685,7 +685,10 @@ __global__ void __launch_bounds__(256) attn_weights_join_kernel(const float2* pa
     lse[i] = M == -INFINITY ? INFINITY : base + log2f(den);
 }
 
-// Pieces of a row and parts of a KV head's keys: a few items per SM where the batch alone gives fewer.
+// Pieces of a row and parts of a KV head's keys: a few items per SM where the batch alone gives fewer.  Rows of whole prompts
+// (no more than as many positions again in the table) are items of 1, 2, .. tiles, which fill the SMs without pieces once there
+// are enough: 2048 rows of 32 heads 31 + 29 us, in three pieces 33 + 6 for the join + 29; behind longer contexts pieces even
+// out what differs: 100 to 700 rows of two contexts to 8000, 8 heads, 60 + 6 us for the rows, 76 in one piece.
 struct ObsSplit {
     long long row_items, key_items;
     int pieces, key_ctas;
@@ -693,12 +696,13 @@ struct ObsSplit {
 };
 
 ObsSplit obs_split(int batch, int max_new, int n_heads, int n_kv_heads, int max_blocks, int block_size) {
-    constexpr int kRowItems = 4 * 152, kKeyItems = 6 * 152;
+    constexpr int kRowItems = 4 * 152, kPromptItems = 152, kKeyItems = 6 * 152;
+    const int row_items = 2LL * max_new >= (long long)max_blocks * block_size ? kPromptItems : kRowItems;
     const long long Tq = kTile / (n_heads / n_kv_heads), bh = (long long)batch * n_kv_heads;
     const long long items = (max_new + 2 * Tq - 1) / (2 * Tq) * bh;
     const long long tiles = ((long long)max_blocks * block_size + kWide - 1) / kWide;
     ObsSplit s;
-    s.pieces = (int)std::max<long long>(1, std::min<long long>({16, (kRowItems + items - 1) / items, (tiles + kObsPieceTiles - 1) / kObsPieceTiles}));
+    s.pieces = (int)std::max<long long>(1, std::min<long long>({16, (row_items + items - 1) / items, (tiles + kObsPieceTiles - 1) / kObsPieceTiles}));
     s.key_ctas = (int)std::max<long long>(1, std::min<long long>((kKeyItems + bh - 1) / bh, tiles));
     s.row_items = items * s.pieces;
     s.key_items = bh * s.key_ctas;
