@@ -124,6 +124,24 @@ def test_long_rows_of_weights(ctx, keep, weights):
     run(c, make_weights(weights, len(ctx), 2, c.width, torch.Generator().manual_seed(keep)), keep, 4, min(keep, 100))
 
 
+@pytest.mark.parametrize("weights", ["spread", "ties", "zeros", "some odd"])
+@pytest.mark.parametrize("ctx,H,keep,spare,extra", [
+    ([5000], 5, 1700, 1, 0), ([5000, 300], 10, 1234, 1, 1), ([4999] * 3, 20, 4000, 1, 2), ([5003] * 2, 50, 900, 1, 3), ([4100, 700], 100, 2000, 1, 0),
+    ([300, 64], 2, 50, 900, 1), ([3000], 80, 1200, 3300, 0)])
+def test_forms_of_the_choice(ctx, H, keep, spare, extra, weights):
+    """Rows of weights in clusters of eight, four and two CTAs, in one with all or half of its threads, too long for shared
+    memory by the table (and short in it), on 16 bytes or not; warps with and without odd values; part of the rows and outputs
+    apart."""
+    c = Cache(ctx, H, 16, 16, keep, spare=spare)
+    g = torch.Generator().manual_seed(H)
+    w = make_weights("spread" if weights == "some odd" else weights, len(ctx), H, c.width + extra, g)
+    if weights == "some odd":                                 # few places, most warps have none
+        odd = make_weights("odd", len(ctx), H, w.shape[2], g)
+        w = torch.where(torch.rand(w.shape, generator=g) < 0.001, odd, w)
+        w = torch.where(torch.rand(w.shape, generator=g) < 0.05, 0.0, w)
+    run(c, w, keep, 4, min(keep, 100), separate=extra == 1)
+
+
 def test_a_number_for_each_sequence():
     c = Cache([50, 60, 70, 16], 2, 64, 16, 1)
     w = make_weights("spread", 4, 2, c.width, torch.Generator().manual_seed(1))

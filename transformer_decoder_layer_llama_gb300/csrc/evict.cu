@@ -69,6 +69,25 @@ LL_DEVINL Budget evict_budget(const EvictArgs& a, int b, bool flag) {
     return g;
 }
 
+// n weights to shared memory, by cp.async; and zeros.  A CTA's threads, 16 bytes each where the row lies for it.
+LL_DEVINL void copy_weights(float* dst, const float* src, int n) {
+    const bool wide = (reinterpret_cast<uintptr_t>(src) & 15u) == 0;
+    const int whole = wide ? n & ~3 : 0;
+    for (int i = 4 * threadIdx.x; i < whole; i += 4 * blockDim.x)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst + i)), "l"(src + i) : "memory");
+    for (int i = whole + threadIdx.x; i < n; i += blockDim.x)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst + i)), "l"(src + i) : "memory");
+}
+
+// w[j0 .. n) of a row, thread `at` of `all`.
+LL_DEVINL void zero_weights(float* w, int j0, int n, int at, int all) {
+    const int lead = min(n, j0 + (int)((16u - (uint32_t)(reinterpret_cast<uintptr_t>(w + j0) & 15u)) / 4u & 3u));      // up to 16 bytes' start
+    const int whole = lead + ((n - lead) & ~3);
+    if (at < lead - j0) w[j0 + at] = 0.f;
+    for (int j = lead + 4 * at; j < whole; j += 4 * all) *reinterpret_cast<float4*>(w + j) = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (at < n - whole) w[whole + at] = 0.f;
+}
+
 // The sum of v over the lanes before this one in the list s[0 .. n), n <= 32, that each warp reads by itself: the value for
 // entry `at`, and the total.
 LL_DEVINL int before_in(const int* s, int n, int at, int& total) {
@@ -119,8 +138,7 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
     };
     bool skip = g.skip;
     if (CACHED && !skip && g.left < n)
-        for (int p = c0 + tid; p < c1; p += threads)       // all on their way at once
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(s_w + (p - c0))), "l"(w + p) : "memory");
+        copy_weights(s_w, w + c0, c1 - c0);                // all on their way at once
     if (!skip && g.left < n) {                             // rows will move: every block must be there
         bool bad = false;
         const int blocks = (n + a.block_size - 1) / a.block_size;
@@ -150,6 +168,10 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
     // the key of the last row that stays, digit by digit: `prefix` in the bits above `shift`, `need` rows of that prefix
     uint32_t prefix = 0;
     int need = rest;
+    // whether this warp's weights between the first and last rows are neither negative (-0 too) nor NaN, as sums of
+    // probabilities are: their keys are their bits with the top one set (16 sequences of 4096 to 32768 rows: 31 us, 42 without)
+    bool plain = rest > 0;
+    constexpr uint32_t kInfinity = 0x7f800000u;
     if (rest > 0) {
         constexpr int kShift[3] = {21, 10, 0};
 #pragma unroll
@@ -157,23 +179,48 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
             const int shift = kShift[pass];
             const uint32_t above = pass == 0 ? 0u : 0xffffffffu << kShift[pass - 1 < 0 ? 0 : pass - 1];
             const uint32_t mask = pass == 2 ? 1023u : 2047u;
-            // a lane adds up runs of one bin (zeros, say) before it adds them to the histogram
-            int run_bin = -1, run_len = 0;
+            // a lane adds up runs of one bin before it adds them to the histogram, and zeros
+            int run_bin = -1, run_len = 0, zeros = 0;
+            const auto count = [&](int bin) {
+                if (bin != run_bin) {
+                    if (run_len) atomicAdd(&s_hist[pass][run_bin], run_len);
+                    run_bin = bin;
+                    run_len = 0;
+                }
+                ++run_len;
+            };
             for (int p0 = w0 + 4 * lane; p0 < w1; p0 += kSpan) {
                 float v[4];
                 four(p0, v);
+                if (p0 >= p_lo && p0 + 4 <= p_hi && (pass == 0 || plain)) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const uint32_t key = weight_key(v[e]);
-                    if (p0 + e < p_lo || p0 + e >= p_hi || (key & above) != prefix) continue;
-                    const int bin = (int)((key >> shift) & mask);
-                    if (bin != run_bin) {
-                        if (run_len) atomicAdd(&s_hist[pass][run_bin], run_len);
-                        run_bin = bin;
-                        run_len = 0;
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t u = __float_as_uint(v[e]), key = u | 0x80000000u;
+                        if (pass > 0) {
+                            if ((key & above) == prefix) count((int)((key >> shift) & mask));
+                        } else if (u == 0u) {
+                            ++zeros;
+                        } else if (u <= kInfinity) {
+                            atomicAdd(&s_hist[0][key >> shift], 1);
+                        } else {
+                            plain = false;
+                            count((int)(weight_key(v[e]) >> shift));
+                        }
                     }
-                    ++run_len;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t key = weight_key(v[e]);
+                        if (p0 + e < p_lo || p0 + e >= p_hi || (key & above) != prefix) continue;
+                        if (pass == 0 && __float_as_uint(v[e]) > kInfinity) plain = false;
+                        count((int)((key >> shift) & mask));
+                    }
                 }
+            }
+            if (pass == 0) {
+                zeros = __reduce_add_sync(0xffffffffu, zeros);
+                if (lane == 0 && zeros) atomicAdd(&s_hist[0][1024], zeros);
+                plain = __all_sync(0xffffffffu, plain);
             }
             if (run_len) atomicAdd(&s_hist[pass][run_bin], run_len);
             // (a cluster's histograms meet in its first CTA, bin by bin where there is something, and that one picks)
@@ -238,6 +285,15 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
     for (int p0 = w0 + 4 * lane; p0 < w1; p0 += kSpan) {
         float v[4];
         four(p0, v);
+        if (plain && p0 >= p_lo && p0 + 4 <= p_hi) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t key = __float_as_uint(v[e]) | 0x80000000u;
+                gt += key > prefix ? 1 : 0;
+                eq += key == prefix ? 1 : 0;
+            }
+            continue;
+        }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             bool tie;
@@ -272,6 +328,35 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
         bool in[4], tie[4];
         int g_rank = gt_before, e_rank = eq_before;        // before this lane's four
         if (p0 < w1) four(p0, v);
+        if (plain && q0 >= p_lo && q0 + kSpan <= p_hi) {   // (the same for the warp)
+            uint32_t gts[4], some = 0;
+            bool same = false;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t key = __float_as_uint(v[e]) | 0x80000000u;
+                in[e] = key > prefix;
+                same = same || key == prefix;
+                gts[e] = __ballot_sync(0xffffffffu, in[e]);
+                some |= gts[e];
+            }
+            if (!__any_sync(0xffffffffu, same)) {          // no ties
+                if (some == 0u) continue;
+                int j = gt_before + min(eq_before, need);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    j += __popc(gts[e] & below);
+                    gt_before += __popc(gts[e]);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (!in[e]) continue;
+                    kept[j] = p0 + e;
+                    if (CACHED) w_out[j] = v[e];           // (w_out may be w: all of it has been read)
+                    ++j;
+                }
+                continue;
+            }
+        }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             in[e] = stays(p0 + e, p0 < w1 ? v[e] : 0.f, tie[e]);
@@ -294,7 +379,7 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
     }
     for (int j = g.left + at; j < a.max_keep; j += all) kept[j] = -1;
     if (CACHED) {
-        for (int j = g.left + at; j < n; j += all) w_out[j] = 0.f;
+        zero_weights(w_out, g.left, n, at, all);
         sync_all<NC>();                                    // (counts of this CTA's may still be read)
         return;
     }
@@ -510,10 +595,11 @@ cudaError_t launch_evict(const EvictArgs& args, cudaStream_t stream) {
     const long long most = (long long)a.max_blocks * a.block_size;
     const int sms = std::max(1, device_sm_count());
     trace_before("evict_select", stream);
-    // Few rows of weights are spread over clusters, as many CTAs as run at once (65536 positions of 8 heads: 23 us
-    // with eight CTAs each, 101 with one); weights that fit lie in shared memory.
-    const int nc = most < 4096 ? 1 : rows * 8 <= 2 * sms ? 8 : rows * 4 <= 2 * sms ? 4 : rows * 2 <= 2 * sms ? 2 : 1;
-    const int threads = nc == 8 ? 1024 : 512;            // (alone on its SM or not)
+    // Few rows of weights are spread over clusters, as many CTAs as run at once, one on an SM (65536 positions of 8 heads: 21
+    // us with eight CTAs each, 101 with one; of 32 heads 27 with four, 54 with eight in two turns; clusters of eight fill about
+    // half of the SMs at once, 16 of them take 38).  Weights that fit lie in shared memory.
+    const int nc = most < 4096 ? 1 : rows * 16 <= sms ? 8 : rows * 4 <= sms ? 4 : rows * 2 <= sms ? 2 : 1;
+    const int threads = most >= 4096 && rows * nc <= sms ? 1024 : 512;
     const int warps = nc * threads / 32;
     const long long stretch = (most + warps - 1) / warps + kSpan - 1;    // of a warp, in whole spans
     const size_t smem = (size_t)(stretch / kSpan * kSpan) * (threads / 32) * sizeof(float);
