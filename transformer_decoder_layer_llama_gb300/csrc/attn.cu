@@ -893,12 +893,13 @@ __global__ void attn_decode_combine_kernel(const AttnDecodeArgs a, int max_split
 }
 
 // The outputs, as attn_decode_combine_kernel (blocks x >= spans: one query head of the group each), and the
-// attention weights of 1024 cached tokens per block x < spans:
+// attention weights of 2048 cached tokens per block x < spans:
 //   weights[b][hk][p] += sum over the group's heads of 2^(score_h[p] - lse_h),  lse_h = M + log2 sum_s 2^(m_s - M) l_s.
 // The scores are float32, 4 bytes a query head and key beside the 4 head_dim bytes of a key and KV head, and mostly
-// still in L2 when they are read here.  One kernel for both, so that a step has no launch more than without weights.
-// A thread has four positions and the scores of AHEAD heads on their way at once, before the normalisers are there.
+// still in L2 when they are read here (not where there are 75 MB of them beside 600 MB of K and V).  One kernel for both, so that a step has no launch more than without weights.
+// A thread has twice four positions and the scores of AHEAD heads on their way at once, before the normalisers are there.
 constexpr int kFinishThreads = 256;
+constexpr int kFinishFours = 2;          // of a thread (64 sequences of 512 to 4096, 32 heads: 20.4 us, 22.4 with one, 20.4 with four)
 
 template <int AHEAD>
 __global__ void __launch_bounds__(kFinishThreads) attn_decode_finish_kernel(const AttnDecodeArgs a, int max_splits, int spans) {
@@ -926,29 +927,36 @@ __global__ void __launch_bounds__(kFinishThreads) attn_decode_finish_kernel(cons
         }
         return;
     }
-    constexpr int E = 4;
-    const long long span0 = (long long)blockIdx.x * (E * kFinishThreads);
+    constexpr int E = 4, K = kFinishFours, kSpan = E * kFinishThreads;
+    const long long span0 = (long long)blockIdx.x * (K * kSpan);
     if (span0 >= ctx) return;
-    const int p1 = (int)min((long long)ctx, span0 + E * kFinishThreads);
+    const int p1 = (int)min((long long)ctx, span0 + K * kSpan);
     if (p1 > a.weights_width && threadIdx.x == 0) flag_status(a.status, LL_DEV_BAD_POSITION);
     const int end = min(p1, a.weights_width);
-    const int p = (int)span0 + E * threadIdx.x;                   // this thread's four; rows of scores are multiples of 16
-    const bool here = p < end;
-    const float* scores = a.scores + ((size_t)b * a.n_heads + (size_t)hk * G) * a.score_stride + p;
-    float* weights = a.weights + ((size_t)b * a.n_kv_heads + hk) * a.weights_width + p;
-    const bool wide = p + E <= end && (reinterpret_cast<uintptr_t>(weights) & 15u) == 0;
+    const int p0 = (int)span0 + E * threadIdx.x;                  // this thread's first four; rows of scores are multiples of 16
+    const float* scores = a.scores + ((size_t)b * a.n_heads + (size_t)hk * G) * a.score_stride + p0;
+    float* weights = a.weights + ((size_t)b * a.n_kv_heads + hk) * a.weights_width + p0;
+    const bool aligned = (reinterpret_cast<uintptr_t>(weights) & 15u) == 0;
     const float4 none = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-    float4 next[AHEAD], sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    float4 next[K][AHEAD], sum[K];
 #pragma unroll
-    for (int j = 0; j < AHEAD; ++j)                               // the first heads and the sums so far, before the normalisers
-        next[j] = here && j < G ? __ldcs(reinterpret_cast<const float4*>(scores + (size_t)j * a.score_stride)) : none;
-    if (wide) {
-        sum = *reinterpret_cast<const float4*>(weights);
-    } else {
-        if (p < end) sum.x = weights[0];
-        if (p + 1 < end) sum.y = weights[1];
-        if (p + 2 < end) sum.z = weights[2];
-        if (p + 3 < end) sum.w = weights[3];
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j)                           // the first heads and the sums so far, before the normalisers
+            next[k][j] = p0 + k * kSpan < end && j < G ? __ldcs(reinterpret_cast<const float4*>(scores + (size_t)j * a.score_stride + k * kSpan)) : none;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int p = p0 + k * kSpan;
+        const float* w = weights + k * kSpan;
+        sum[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (aligned && p + E <= end) {
+            sum[k] = *reinterpret_cast<const float4*>(w);
+        } else {
+            if (p < end) sum[k].x = w[0];
+            if (p + 1 < end) sum[k].y = w[1];
+            if (p + 2 < end) sum[k].z = w[2];
+            if (p + 3 < end) sum[k].w = w[3];
+        }
     }
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     for (int h = warp; h < G; h += kFinishThreads / 32) {
@@ -965,29 +973,40 @@ __global__ void __launch_bounds__(kFinishThreads) attn_decode_finish_kernel(cons
         if (lane == 0) s_lse[h] = den == 0.f ? INFINITY : mb + log2f(den);
     }
     __syncthreads();
-    if (!here) return;
-    float4 add = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (p0 >= end) return;
+    float4 add[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) add[k] = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int h0 = 0; h0 < G; h0 += AHEAD) {
 #pragma unroll
         for (int j = 0; j < AHEAD; ++j) {
             if (h0 + j >= G) break;
             const float lse = s_lse[h0 + j];
-            add.x += ex2_approx(next[j].x - lse);
-            add.y += ex2_approx(next[j].y - lse);
-            add.z += ex2_approx(next[j].z - lse);
-            add.w += ex2_approx(next[j].w - lse);
             const int h = h0 + AHEAD + j;
-            if (h < G) next[j] = __ldcs(reinterpret_cast<const float4*>(scores + (size_t)h * a.score_stride));
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                add[k].x += ex2_approx(next[k][j].x - lse);
+                add[k].y += ex2_approx(next[k][j].y - lse);
+                add[k].z += ex2_approx(next[k][j].z - lse);
+                add[k].w += ex2_approx(next[k][j].w - lse);
+                if (h < G && p0 + k * kSpan < end)
+                    next[k][j] = __ldcs(reinterpret_cast<const float4*>(scores + (size_t)h * a.score_stride + k * kSpan));
+            }
         }
     }
     // (scores behind the context, in the last four, are whatever was there: only p < end is written)
-    if (wide) {
-        *reinterpret_cast<float4*>(weights) = make_float4(sum.x + add.x, sum.y + add.y, sum.z + add.z, sum.w + add.w);
-    } else {
-        weights[0] = sum.x + add.x;
-        if (p + 1 < end) weights[1] = sum.y + add.y;
-        if (p + 2 < end) weights[2] = sum.z + add.z;
-        if (p + 3 < end) weights[3] = sum.w + add.w;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int p = p0 + k * kSpan;
+        float* w = weights + k * kSpan;
+        if (aligned && p + E <= end) {
+            *reinterpret_cast<float4*>(w) = make_float4(sum[k].x + add[k].x, sum[k].y + add[k].y, sum[k].z + add[k].z, sum[k].w + add[k].w);
+        } else {
+            if (p < end) w[0] = sum[k].x + add[k].x;
+            if (p + 1 < end) w[1] = sum[k].y + add[k].y;
+            if (p + 2 < end) w[2] = sum[k].z + add[k].z;
+            if (p + 3 < end) w[3] = sum[k].w + add[k].w;
+        }
     }
 }
 
@@ -997,9 +1016,9 @@ cudaError_t launch_join(const AttnDecodeArgs& a, int max_splits, cudaStream_t st
     if (a.weights) {
         trace_before("attn_decode_finish", stream);
         const int G = a.n_heads / a.n_kv_heads;
-        const int spans = (int)((a.score_stride + 4 * kFinishThreads - 1) / (4 * kFinishThreads));
-        const auto kernel = G == 1 ? attn_decode_finish_kernel<1> : G == 2 ? attn_decode_finish_kernel<2> :
-                            G <= 4 ? attn_decode_finish_kernel<4> : attn_decode_finish_kernel<8>;
+        constexpr int kTokens = 4 * kFinishThreads * kFinishFours;
+        const int spans = (int)((a.score_stride + kTokens - 1) / kTokens);
+        const auto kernel = G == 1 ? attn_decode_finish_kernel<1> : G == 2 ? attn_decode_finish_kernel<2> : attn_decode_finish_kernel<4>;
         e = launch_pdl(kernel, dim3(spans + G, a.n_kv_heads, a.batch), dim3(kFinishThreads), 0, stream, 1, a, max_splits, spans);
     } else {
         trace_before("attn_decode_combine", stream);
