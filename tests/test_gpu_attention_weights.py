@@ -321,6 +321,51 @@ def test_prompt_edges():
     assert torch.equal(w, base)
 
 
+def test_prompt_edges_of_many_rows():
+    """As above where a sequence has more rows than stay beside its keys."""
+    case = ([300, 350, 420, 40], [200, 150, 300, 5], 4, 2, 64, 16)
+    c, q, cu, base = prompt(case)
+    pad = torch.full((9, 4, 64), math.nan).bfloat16().cuda()
+    wide, cu9 = torch.cat([pad, q, pad]), [x + 9 for x in cu]
+    table = c.table.copy()
+    table[2, [1, 20]] = 10 ** 6, -1
+    w, st = base.clone(), api.new_status()
+    api.paged_attention_weights(wide, i32(cu9), c.k, i32(table), i32([300, 149, 420, 40]), 0.125, w, 300, status=st)   # 149 < 150 rows
+    check_status(st, api.LL_DEV_BAD_POSITION | api.LL_DEV_BAD_BLOCK)
+    ref, bound = reference(c, f64(q), cu, 0.125, base, {2: (1, 20)})
+    for b in (0, 2, 3):
+        assert (np.abs(f64(w[b]) - ref[b]) <= bound[b] + 2.0 ** -24 * np.abs(ref[b])).all()
+    assert torch.equal(w[1], base[1]) and torch.equal(w[2, :, 16:32], base[2, :, 16:32]) and torch.equal(w[2, :, 320:336], base[2, :, 320:336])
+    w, st = torch.zeros_like(base), api.new_status()                    # a scale of 0: equal weights
+    api.paged_attention_weights(q, i32(cu), c.k, c.d_table, c.d_ctx, 0.0, w, 300, status=st)
+    check_status(st)
+    for b, n in enumerate(c.ctx):
+        m = case[1][b]
+        want = sum(np.where(np.arange(n) <= n - m + i, 2 / (n - m + i + 1), 0) for i in range(m))
+        assert np.allclose(f64(w[b, :, :n]), want, rtol=1e-5) and (w[b, :, n:] == 0).all()
+
+
+@pytest.mark.parametrize("which", ["a query row", "a key"])
+def test_nan_in_a_window(which):
+    """As below for few rows: their keys lie in several CTAs' shares."""
+    n, m = 2900, 20
+    for at in (0, 7, 19):
+        c, q, cu, base = prompt(([n], [m], 4, 2, 64, 64))
+        if which == "a query row":
+            q[at, 1, 7] = math.nan
+            head, end = 0, n - m + at + 1                     # its KV head; the positions that it sees
+        else:
+            key = n - m + at
+            c.k[c.table[0, key // 64], 1, key % 64, 3] = math.nan
+            head, end = 1, n                                  # rows from `at` on see it, the last of them all
+        w, st = base.clone(), api.new_status()
+        api.paged_attention_weights(q, i32(cu), c.k, c.d_table, c.d_ctx, 0.125, w, m, status=st)
+        check_status(st)
+        nan = np.zeros(w.shape, dtype=bool)
+        nan[0, head, :end] = True
+        assert (np.isnan(f64(w)) == nan).all()
+
+
 @pytest.mark.parametrize("which", ["a query row", "a key"])
 def test_nan_reaches_what_it_is_a_score_of(which):
     """A NaN in a row's query: every position that the row sees.  In a key: every position, of every row that sees it."""
