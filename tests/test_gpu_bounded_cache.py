@@ -315,3 +315,28 @@ def test_stack_prompts_start_the_weights(observe):
             eng.prefill(2, T, stream, **bad)
     with pytest.raises(ValueError, match="track_weights"):
         ref.prefill(2, T, stream, slots=[0, 1])
+
+
+def test_weights_beyond_32_bits():
+    """Weights of 2.7e9 elements: the last sequences' lie behind 2^31.  The same bits as with narrow ones."""
+    B, H, Hkv, d, bs, n, wide = 40, 16, 8, 64, 16, 300, 1 << 23
+    g = torch.Generator().manual_seed(2)
+    mb = -(-n // bs)
+    table = i32(torch.randperm(B * mb, generator=g).view(B, mb))
+    pools = [tuple(torch.randn(B * mb, Hkv, bs, d, generator=g).bfloat16().cuda() for _ in range(2))]
+    pools.append(tuple(t.clone() for t in pools[0]))
+    q, rows = torch.randn(B, H, d, generator=g).bfloat16().cuda(), torch.randn(B * 5, H, d, generator=g).bfloat16().cuda()
+    ctx, cu, st = i32([n] * B), i32(range(0, 5 * B + 1, 5)), api.new_status()
+    out = []
+    for pool, width in zip(pools, (mb * bs, wide)):
+        w = torch.zeros(B, Hkv, width, device="cuda")
+        api.paged_attention_weights(rows, cu, pool[0], table, ctx, 0.125, w, 5, status=st)
+        o = api.paged_attention_decode_weights(q, *pool, table, ctx, 0.125, w, status=st)
+        kept, lens = api.evict_rows(pool, table, ctx, w, 200, sinks=2, recent=20, status=st)
+        check_status(st)
+        assert width < wide or (w[::13, :, mb * bs:] == 0).all()
+        out.append((o, kept, lens, w[:, :, :mb * bs].clone()))
+        del w
+    assert all(torch.equal(a, b) for a, b in zip(*out)) and all(torch.equal(a, b) for a, b in zip(*pools))
+    assert (out[0][3][-1, -1, :200] > 0).all()
+    torch.cuda.empty_cache()
