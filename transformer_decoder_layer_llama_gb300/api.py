@@ -771,12 +771,58 @@ def _head_out(t, out, name):
     return out, ll_head_rows(out.data_ptr(), shape[1] * shape[2], shape[1])
 
 
+def _norm_usual(q, k, q_gain, k_gain, positions, table, layout, status):
+    """What nearly every call of norm_rope and its gradient is, in one look: q and k with their gains, rows, a status word,
+    all on the current device.  Returns (device index, tokens, n_heads, n_kv_heads, head_dim, strides of q and k), or None:
+    then the checks below say what is wrong, or do what is unusual.  (A call of few tokens takes 15.4 us so, 18.6 without; the gradient 24.7, 32.)"""
+    for t in (q, k, q_gain, k_gain, positions, table, status):
+        if not isinstance(t, _Tensor):
+            return None
+    dtype, dev = q.dtype, torch.cuda.current_device()
+    if dtype not in _NORM_DTYPES or k.dtype is not dtype or q.dim() != 3 or k.dim() != 3 or layout not in LL_ROPE_LAYOUTS:
+        return None
+    T, H, d = q.shape
+    Tk, Hk, dk = k.shape
+    st, sh, sd = q.stride()
+    kt, kh, kd = k.stride()
+    if T == 1:
+        st, kt = H * d, Hk * d
+    if T < 1 or Tk != T or dk != d or sd != 1 or kd != 1 or sh != d or kh != d or st < H * d or kt < Hk * d or \
+            q_gain.dtype is not torch.float32 or k_gain.dtype is not torch.float32 or table.dtype is not torch.float32 or \
+            positions.dtype is not torch.int32 or status.dtype is not torch.int32 or q_gain.shape != (d,) or \
+            k_gain.shape != (d,) or positions.shape != (T,) or table.dim() != 3 or not status.numel():
+        return None
+    if not (q.get_device() == dev and k.get_device() == dev and q_gain.get_device() == dev and k_gain.get_device() == dev and
+            positions.get_device() == dev and table.get_device() == dev and status.get_device() == dev and
+            q_gain.is_contiguous() and k_gain.is_contiguous() and positions.is_contiguous() and table.is_contiguous() and
+            status.is_contiguous()):
+        return None
+    if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or q_gain.requires_grad or k_gain.requires_grad):
+        return None
+    _, half, two = table.shape
+    return (dev, T, H, Hk, d, st, kt) if two == 2 and 2 <= 2 * half <= d else None
+
+
 def norm_rope(q, k, q_gain, k_gain, positions, table, eps=1e-5, layout="half", q_out=None, k_out=None, status=None,
               stream=None):
     """ll_norm_rope: RMS norm of every head of q [tokens, n_heads, head_dim] and k [tokens, n_kv_heads, head_dim] with
     the gains (float32 [head_dim]), then the rotary positions of rope(), in one pass.  q and k are BF16 or float32,
     heads contiguous within a token; either may be None (its gain too).  Pass q_out=q (k_out=k) to work in place.
     Not recorded by autograd: norm_rope_backward is the gradient.  Returns (q_out, k_out)."""
+    usual = _norm_usual(q, k, q_gain, k_gain, positions, table, layout, status) if stream is None and q_out is None and \
+        k_out is None else None
+    if usual is not None:
+        dev, T, H, Hk, d, st, kt = usual
+        dtype, device = q.dtype, q.device
+        q_out = torch.empty((T, H, d), dtype=dtype, device=device)
+        k_out = torch.empty((T, Hk, d), dtype=dtype, device=device)
+        rc = lib.ll_norm_rope(ll_head_rows(q.data_ptr(), st, H), ll_head_rows(k.data_ptr(), kt, Hk), _NORM_DTYPES[dtype],
+                              q_gain.data_ptr(), k_gain.data_ptr(), eps, positions.data_ptr(), T, d, 2 * table.shape[1],
+                              LL_ROPE_LAYOUTS[layout], table.data_ptr(), table.shape[0], ll_head_rows(q_out.data_ptr(), H * d, H),
+                              ll_head_rows(k_out.data_ptr(), Hk * d, Hk), status.data_ptr(), _raw_stream(dev))
+        if rc != LL_OK:
+            raise LayerError("ll_norm_rope", rc)
+        return q_out, k_out
     dtype, T, d, qh, kh = _norm_args(q, k, q_gain, k_gain, positions, table, layout, "norm_rope")
     given = q_out, k_out, status
     q_out, qo = _head_out(q, q_out, "q_out")
@@ -806,6 +852,34 @@ def norm_rope_backward(dq, dk, q, k, q_gain, k_gain, positions, table, eps=1e-5,
     """ll_norm_rope_backward: the gradients of norm_rope's inputs q, k and gains, from the gradients dq, dk of its
     outputs.  Pass q_grad=dq (k_grad=dk) to overwrite those.  Returns (q_grad, k_grad, q_gain_grad, k_gain_grad), the
     gains' in float32; None for a tensor that is None."""
+    usual = _norm_usual(q, k, q_gain, k_gain, positions, table, layout, status) if stream is None and q_grad is None and \
+        k_grad is None and q_gain_grad is None and k_gain_grad is None and isinstance(dq, _Tensor) and \
+        isinstance(dk, _Tensor) and isinstance(workspace, _Tensor) else None
+    if usual is not None:
+        dev, T, H, Hk, d, st, kt = usual
+        dtype, device = q.dtype, q.device
+        if dq.dtype is dtype and dk.dtype is dtype and dq.shape == q.shape and dk.shape == k.shape and \
+                workspace.dtype is torch.uint8 and workspace.is_contiguous() and dq.get_device() == dev and \
+                dk.get_device() == dev and workspace.get_device() == dev:
+            dst, dsh, dsd = dq.stride()
+            dkt, dkh, dkd = dk.stride()
+            if T == 1:
+                dst, dkt = H * d, Hk * d
+            if dsd == 1 and dkd == 1 and dsh == d and dkh == d and dst >= H * d and dkt >= Hk * d:
+                q_grad = torch.empty((T, H, d), dtype=dtype, device=device)
+                k_grad = torch.empty((T, Hk, d), dtype=dtype, device=device)
+                q_gain_grad = torch.empty((d,), dtype=torch.float32, device=device)
+                k_gain_grad = torch.empty((d,), dtype=torch.float32, device=device)
+                rc = lib.ll_norm_rope_backward(
+                    ll_head_rows(dq.data_ptr(), dst, H), ll_head_rows(dk.data_ptr(), dkt, Hk), ll_head_rows(q.data_ptr(), st, H),
+                    ll_head_rows(k.data_ptr(), kt, Hk), _NORM_DTYPES[dtype], q_gain.data_ptr(), k_gain.data_ptr(), eps,
+                    positions.data_ptr(), T, d, 2 * table.shape[1], LL_ROPE_LAYOUTS[layout], table.data_ptr(), table.shape[0],
+                    ll_head_rows(q_grad.data_ptr(), H * d, H), ll_head_rows(k_grad.data_ptr(), Hk * d, Hk),
+                    q_gain_grad.data_ptr(), k_gain_grad.data_ptr(), workspace.data_ptr(), workspace.numel(), status.data_ptr(),
+                    _raw_stream(dev))
+                if rc != LL_OK:
+                    raise LayerError("ll_norm_rope_backward", rc)
+                return q_grad, k_grad, q_gain_grad, k_gain_grad
     dtype, T, d, qh, kh = _norm_args(q, k, q_gain, k_gain, positions, table, layout, "norm_rope_backward")
     if (dq is None) != (q is None) or (dk is None) != (k is None):
         raise ValueError("dq and dk go with q and k")
