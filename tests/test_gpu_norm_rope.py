@@ -272,3 +272,40 @@ def test_streams_and_graphs():
         graph.replay()
         check_status(st)
         assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+def test_what_the_binding_refuses():
+    """One thing wrong at a time, with all that a usual call has."""
+    T, H, Hk, d = 6, 4, 2, 64
+    ok = dict(q=torch.ones(T, H, d).bfloat16(), k=torch.ones(T, Hk, d).bfloat16(), q_gain=torch.ones(d), k_gain=torch.ones(d),
+              positions=torch.zeros(T, dtype=torch.int32), table=torch.zeros(8, d // 2, 2), status=torch.zeros(1, dtype=torch.int32))
+    ok = {n: t.cuda() for n, t in ok.items()}
+    ws = torch.empty(api.norm_rope_backward_workspace_size(d), dtype=torch.uint8, device="cuda")
+    wide = torch.ones(T, H, 2 * d).bfloat16().cuda()
+    bad = [dict(q=ok["q"].half()), dict(k=ok["k"].float()), dict(q=ok["q"][0]), dict(k=ok["k"][:5]), dict(k=wide[..., :d // 2]), dict(q=wide[..., :d]),
+           dict(q=wide[..., ::2]), dict(q=ok["q"].transpose(0, 1)), dict(q_gain=ok["q_gain"][:60]), dict(k_gain=ok["k_gain"].bfloat16()),
+           dict(q_gain=torch.ones(2 * d).cuda()[::2]), dict(positions=ok["positions"].long()), dict(positions=ok["positions"][:5]),
+           dict(positions=ok["positions"].cpu()), dict(table=ok["table"][..., 0]), dict(table=torch.zeros(8, d, 2).cuda()), dict(table=ok["table"].cpu()),
+           dict(table=torch.zeros(8, d // 2, 4).cuda()[..., ::2]), dict(status=torch.zeros(1).cuda()), dict(status=ok["status"][:0]),
+           dict(layout="quarter"), dict(q=ok["q"].clone().requires_grad_()), dict(k_gain=ok["k_gain"].clone().requires_grad_()), dict(q=None, k=None)]
+    for change in bad:
+        a = {**ok, **change}
+        with pytest.raises((ValueError, TypeError)):
+            api.norm_rope(**a)
+        dq, dk = (torch.ones(T, n, d).bfloat16().cuda() for n in (H, Hk))
+        with pytest.raises((ValueError, TypeError)):
+            api.norm_rope_backward(dq, dk, workspace=ws, **a)
+    dq, dk = torch.ones_like(ok["q"]), torch.ones_like(ok["k"])
+    for change in (dict(dq=dq.float()), dict(dk=dk[:5]), dict(dq=wide[..., :d]), dict(dq=None), dict(dk=dk.cpu()), dict(workspace=ws.float()),
+                   dict(workspace=ws.cpu())):
+        with pytest.raises((ValueError, TypeError)):
+            api.norm_rope_backward(**{**dict(dq=dq, dk=dk, workspace=ws), **ok, **change})
+    with pytest.raises(api.LayerError):
+        api.norm_rope_backward(dq, dk, workspace=ws[:64], **ok)
+    with pytest.raises(api.LayerError):
+        api.norm_rope(**ok, eps=0.0)
+    check_status(ok["status"])
+    with torch.no_grad():                                     # a leaf that wants a gradient, where none is recorded
+        api.norm_rope(**{**ok, "q": ok["q"].clone().requires_grad_()})
+    one = {n: t if n in ("q_gain", "k_gain", "table", "status") else t[:1] for n, t in ok.items()}
+    assert torch.equal(api.norm_rope(**one)[0], api.norm_rope(**ok)[0][:1])

@@ -105,3 +105,8 @@ def test_binding_refusals():
         api.norm_rope(x.half(), None, g, None, pos, tab)
     with pytest.raises(ValueError, match="layout"):
         api.norm_rope(x, None, g, None, pos, tab, layout="quarter")
+    status, ws = torch.zeros(1, dtype=torch.int32), torch.zeros(1 << 20, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="GPU"):
+        api.norm_rope(x, x, g, g, pos, tab, status=status)
+    with pytest.raises(ValueError, match="GPU"):
+        api.norm_rope_backward(x, x, x, x, g, g, pos, tab, workspace=ws, status=status)

@@ -778,6 +778,8 @@ def _norm_usual(q, k, q_gain, k_gain, positions, table, layout, status):
     for t in (q, k, q_gain, k_gain, positions, table, status):
         if not isinstance(t, _Tensor):
             return None
+    if not q.is_cuda:
+        return None
     dtype, dev = q.dtype, torch.cuda.current_device()
     if dtype not in _NORM_DTYPES or k.dtype is not dtype or q.dim() != 3 or k.dim() != 3 or layout not in LL_ROPE_LAYOUTS:
         return None
