@@ -515,23 +515,23 @@ __global__ void __launch_bounds__(kWarpSelectThreads) evict_select_warp_kernel(c
 }
 
 // Moves the rows of one (tensor, slice of its rows' bytes, KV head, sequence).  T: the piece a thread moves at a time.
-template <typename T, int ROWS>
+template <typename T, int ROWS, int THREADS>
 LL_DEVINL void move_rows(const EvictArgs& a, char* data, int row_bytes, int slice0, int pieces, int hk, int b, int2* s_place) {
-    constexpr int PER = ROWS / kMoveThreads;
+    constexpr int PER = ROWS / THREADS;
     const int* kept = a.kept + ((size_t)b * a.n_kv_heads + hk) * a.max_keep;
     const int32_t* table = a.block_table + (size_t)b * a.max_blocks;
-    const int run = kMoveThreads * kMovePieces / pieces;          // rows between two barriers
-    const int u = threadIdx.x % pieces, r0 = threadIdx.x / pieces, stride = kMoveThreads / pieces;
+    const int run = THREADS * kMovePieces / pieces;          // rows between two barriers
+    const int u = threadIdx.x % pieces, r0 = threadIdx.x / pieces, stride = THREADS / pieces;
     int src[PER], from[PER], to[PER];                             // rows of the next lookup, and the blocks they are in
     const auto look = [&](int base) {
 #pragma unroll
         for (int e = 0; e < PER; ++e) {
-            const int j = base + e * kMoveThreads + threadIdx.x;
+            const int j = base + e * THREADS + threadIdx.x;
             src[e] = j < a.max_keep ? kept[j] : -1;
         }
 #pragma unroll
         for (int e = 0; e < PER; ++e) {
-            const int j = base + e * kMoveThreads + threadIdx.x;
+            const int j = base + e * THREADS + threadIdx.x;
             from[e] = src[e] > j ? table[src[e] >> a.block_shift] : 0;
             to[e] = src[e] > j ? table[j >> a.block_shift] : 0;
         }
@@ -542,7 +542,7 @@ LL_DEVINL void move_rows(const EvictArgs& a, char* data, int row_bytes, int slic
         bool any = false;
 #pragma unroll
         for (int e = 0; e < PER; ++e) {
-            const int i = e * kMoveThreads + threadIdx.x, j = base + i;
+            const int i = e * THREADS + threadIdx.x, j = base + i;
             any = any || src[e] >= 0;
             s_place[i] = src[e] <= j ? make_int2(-1, -1)
                                      : make_int2(((from[e] * a.n_kv_heads + hk) << a.block_shift) + (src[e] & (a.block_size - 1)),
@@ -571,9 +571,10 @@ LL_DEVINL void move_rows(const EvictArgs& a, char* data, int row_bytes, int slic
 
 // ROWS: whose places a CTA looks up at a time, while the ones before them move.  Where there are many CTAs few (their
 // registers are another CTA's: 64 sequences to 1024 rows of 32 heads 313 us with 512, 350 with 2048), where all run at once
-// many (a document of 65536 tokens to 8192 rows 25 us with 2048, 37 with 512).
-template <int ROWS>
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArgs a) {
+// more, and with the SM to itself still more and twice the threads (8192 of 65536 rows of 128 bytes, 8 heads: 20 us with
+// 4096, 24 with 2048 and 256 threads).
+template <int ROWS, int THREADS>
+__global__ void __launch_bounds__(THREADS) evict_move_kernel(const EvictArgs a) {
     __shared__ int2 s_place[ROWS];
     pdl_wait();
     pdl_trigger();
@@ -581,8 +582,8 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArg
     while (slice >= a.slices[t]) slice -= a.slices[t++];
     const int bytes = a.row_bytes[t] / a.slices[t];
     char* data = static_cast<char*>(a.data[t]);
-    if (a.wide[t]) move_rows<uint4, ROWS>(a, data, a.row_bytes[t], slice * bytes, bytes / 16, blockIdx.y, blockIdx.z, s_place);
-    else move_rows<uint32_t, ROWS>(a, data, a.row_bytes[t], slice * bytes, bytes / 4, blockIdx.y, blockIdx.z, s_place);
+    if (a.wide[t]) move_rows<uint4, ROWS, THREADS>(a, data, a.row_bytes[t], slice * bytes, bytes / 16, blockIdx.y, blockIdx.z, s_place);
+    else move_rows<uint32_t, ROWS, THREADS>(a, data, a.row_bytes[t], slice * bytes, bytes / 4, blockIdx.y, blockIdx.z, s_place);
 }
 
 }  // namespace
@@ -634,14 +635,20 @@ cudaError_t launch_evict(const EvictArgs& args, cudaStream_t stream) {
     trace_after(stream);
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) return record(e, "evict_select launch");
-    // whole rows where that gives every SM a few CTAs, else slices of at least 16 bytes
+    // Whole rows where that gives every SM a few CTAs, else slices of 64 bytes, and where those leave half of the SMs idle
+    // smaller ones, down to a piece.  (8192 of 65536 rows of 128 bytes, K and V of 8 heads: 8 sequences 61 us with 64 bytes,
+    // 115 with 16; one 27 and 20.)
     int slices = 0;
     for (int t = 0; t < a.n_tensors; ++t) {
         const int piece = a.wide[t] ? 16 : 4;
         a.slices[t] = 1;
         // pieces of a slice divide a CTA's threads: slices halve the row while that leaves whole pieces
         int n = a.row_bytes[t] / piece;
-        while (n > kMoveThreads || kMoveThreads % n != 0 || (rows * a.n_tensors * a.slices[t] < 4 * sms && n % 2 == 0)) {
+        const auto more = [&] {
+            const long long ctas = rows * a.n_tensors * a.slices[t];
+            return n % 2 == 0 && (n * piece >= 128 ? ctas < 4 * sms : 2 * ctas < sms);
+        };
+        while (n > kMoveThreads || kMoveThreads % n != 0 || more()) {
             int f = 2;
             while (n % f != 0) ++f;                        // the smallest factor
             n /= f;
@@ -650,8 +657,11 @@ cudaError_t launch_evict(const EvictArgs& args, cudaStream_t stream) {
         slices += a.slices[t];
     }
     trace_before("evict_move", stream);
-    e = launch_pdl(rows * slices <= 2 * sms ? evict_move_kernel<2048> : evict_move_kernel<512>, dim3(slices, a.n_kv_heads, a.batch),
-                   dim3(kMoveThreads), 0, stream, 1, a);
+    const dim3 grid(slices, a.n_kv_heads, a.batch);
+    const long long ctas = rows * slices;
+    e = ctas <= sms       ? launch_pdl(evict_move_kernel<4096, 2 * kMoveThreads>, grid, dim3(2 * kMoveThreads), 0, stream, 1, a)
+        : ctas <= 2 * sms ? launch_pdl(evict_move_kernel<2048, kMoveThreads>, grid, dim3(kMoveThreads), 0, stream, 1, a)
+                          : launch_pdl(evict_move_kernel<512, kMoveThreads>, grid, dim3(kMoveThreads), 0, stream, 1, a);
     trace_after(stream);
     if (e == cudaSuccess) e = cudaGetLastError();
     return record(e, "evict_move launch");

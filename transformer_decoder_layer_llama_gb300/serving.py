@@ -406,8 +406,8 @@ class StackEngine:
     def evict(self, scheduler: Scheduler, keep, stream, sinks=0, recent=0) -> list:
         """Cuts every request with more than `keep` cached tokens down to `keep` in every layer: each KV head keeps the
         first `sinks`, the last `recent`, and of the others those of the largest attention weight.  Frees the blocks
-        behind them in the scheduler (what reuses them must come behind this on `stream`); returns the slots that were cut.  Where such a request shares a block, ValueError
-        before anything is moved."""
+        behind them in the scheduler (what reuses them must come behind this on `stream`); returns the slots that were
+        cut.  Where such a request shares a block, ValueError before anything is moved."""
         if self.weights is None:
             raise ValueError("evict needs track_weights")
         slots = [s for s, r in enumerate(scheduler.slots) if r is not None and r.ctx > keep]
