@@ -211,7 +211,8 @@ def test_unaligned_and_wide_rows_take_the_same_values():
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("layout", ["half", "interleaved"])
 @pytest.mark.parametrize("case,pad", [((3001, 32, 8, 128, 128), 0), ((3001, 32, 8, 128, 64), 4), ((2500, 70, 3, 64, 32), 0), ((2500, 3, 40, 256, 64), 0),
-                                      ((901, 5, 2, 128, 128), 4), ((901, 5, 2, 64, 64), 3)])
+                                      ((901, 5, 2, 128, 128), 4), ((901, 5, 2, 64, 64), 3),
+                                      ((901, 5, 2, 128, 128), 2), ((700, 6, 2, 96, 36), 2), ((700, 6, 2, 256, 128), 2)])
 def test_gradient_of_many_tokens(case, pad, layout, dtype):
     """Many turns of a CTA; rows on 16 bytes, on 8 and on an element's (pad: elements before and between rows).  A chain
     of a gain's sum: 3001 tokens x 40 heads over 600 CTAs, with the joins below 200."""
@@ -244,6 +245,31 @@ def test_gradient_of_many_tokens(case, pad, layout, dtype):
         keep = torch.ones(T, dtype=torch.bool)
         keep[::7] = False
         assert torch.equal(got[keep.cuda()], dx[keep.cuda()])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("pad", [1, 2, 4, 6, 8])
+@pytest.mark.parametrize("d,rot", [(128, 128), (128, 100), (128, 98), (256, 64), (66, 36), (1024, 16)])
+def test_rows_on_any_element(d, rot, pad, layout, dtype):
+    """Rows on one, two, four or eight elements, gains on one: what is loaded at a time goes by that."""
+    T, H, Hk = 37, 3, 2
+    _, _, q, k, gains, pos, table, freq = setup((T, H, Hk, d, rot), dtype)
+    wide = torch.zeros(T, (H + Hk) * d + 2 * pad, dtype=dtype).cuda()
+    views = [wide[:, pad:pad + H * d].view(T, H, d), wide[:, pad + H * d:pad + (H + Hk) * d].view(T, Hk, d)]
+    moved = torch.zeros(2, 2 * d).cuda()
+    for v, x in zip(views, (q, k)):
+        v.copy_(x)
+    odd = [moved[i, pad:pad + d].copy_(gain) for i, gain in enumerate(gains)]
+    st = api.new_status()
+    out = api.norm_rope(*views, *odd, pos.cuda(), table, eps=EPS, layout=layout, q_out=views[0], k_out=views[1], status=st)
+    check_status(st)
+    for x, gain, got in zip((q, k), gains, out):
+        xn, g = f64(x), f64(gain)
+        ref = W.norm_rope(xn, g, pos.numpy(), freq, EPS, layout)
+        n = xn / np.sqrt((xn * xn).mean(-1, keepdims=True) + EPS) * g
+        assert (np.abs(f64(got) - ref) <= 30 * U * pair_sum(n, rot, layout) + UNIT[dtype] * np.abs(ref) + TINY).all()
+    assert (wide[:, :pad] == 0).all() and (wide[:, pad + (H + Hk) * d:] == 0).all()
 
 
 def test_streams_and_graphs():

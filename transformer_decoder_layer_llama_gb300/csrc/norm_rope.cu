@@ -22,10 +22,11 @@ constexpr int kNormGradCtasPerSm = 4;
 // Heads of a thread: 48 bytes a column on their way (16384 tokens of 64 + 8 BF16 heads: 105 us with six, 113 with three;
 // of 32 + 8 float32 heads: 103 with three, 109 with six); in the gradient, with x and dy, 32 (4096 tokens of 32 + 8: BF16
 // 37.5 us with four, 41.6 with one; float32 48 with two, 54 with four).
-template <typename T>
-constexpr int kNormHeads = sizeof(T) == 2 ? 6 : 3;
-template <typename T>
-constexpr int kNormGradHeads = sizeof(T) == 2 ? 4 : 2;
+// Element by element or in pairs a column takes more registers: 98 of 128 rotated, BF16, 385 us with six, 236 with three.
+template <typename T, int VEC = 2>
+constexpr int kNormHeads = VEC < 2 || sizeof(T) == 4 ? 3 : 6;
+template <typename T, int VEC = 2>
+constexpr int kNormGradHeads = VEC < 2 || sizeof(T) == 4 ? 2 : 4;
 constexpr int kNormAnyWarps = 4;       // of the gradient's CTA for heads that no group holds
 
 // How threads share a token's heads: a head is `lanes` threads of a group of W (a power of two), each with two columns
@@ -53,9 +54,10 @@ HeadSplit head_split(int lanes, int heads, int per_thread, int threads) {
     return s;
 }
 
-// A thread's two columns, at e0 and e1, of n0 and n1 elements (N each where a head divides into whole columns: VEC):
+// A thread's two columns, at e0 and e1, of n0 and n1 elements (N each where a head divides into whole columns: VEC 2; VEC 1:
+// an even number, which lie for loads of two; VEC 0: element by element):
 // rotated half-split, they hold the two ends of its pairs; interleaved or behind the rotated part, neighbours.
-template <int N, bool HALF, bool VEC>
+template <int N, bool HALF, int VEC>
 struct Columns {
     int e0, e1, n0, n1;
     bool turn;
@@ -73,14 +75,14 @@ struct Columns {
             n0 = max(0, min(N, end - e0));
             n1 = max(0, min(N, end - e1));
         }
-        if (VEC) n0 = n1 = N;
+        if (VEC == 2) n0 = n1 = N;
     }
 };
 
 // N elements of T as they lie in memory.
-template <typename T, int N, bool VEC>
+template <typename T, int N, int VEC>
 struct Column {
-    static constexpr int WORDS = VEC ? N * (int)sizeof(T) / 4 : N;
+    static constexpr int WORDS = VEC > 0 ? N * (int)sizeof(T) / 4 : N;
     uint32_t w[WORDS];
 
     LL_DEVINL void zero() {
@@ -88,10 +90,20 @@ struct Column {
         for (int i = 0; i < WORDS; ++i) w[i] = 0u;
     }
     LL_DEVINL void load(const T* p, int n) {
-        if constexpr (VEC && WORDS == 2) {
+        if constexpr (VEC == 1) {
+#pragma unroll
+            for (int i = 0; i < N / 2; ++i) {
+                if constexpr (sizeof(T) == 2) {
+                    w[i] = 2 * i < n ? reinterpret_cast<const uint32_t*>(p)[i] : 0u;
+                } else {
+                    const uint2 x = 2 * i < n ? reinterpret_cast<const uint2*>(p)[i] : make_uint2(0u, 0u);
+                    w[2 * i] = x.x; w[2 * i + 1] = x.y;
+                }
+            }
+        } else if constexpr (VEC == 2 && WORDS == 2) {
             const uint2 x = *reinterpret_cast<const uint2*>(p);
             w[0] = x.x; w[1] = x.y;
-        } else if constexpr (VEC) {
+        } else if constexpr (VEC == 2) {
 #pragma unroll
             for (int i = 0; i < WORDS / 4; ++i) {
                 const uint4 x = reinterpret_cast<const uint4*>(p)[i];
@@ -109,12 +121,19 @@ struct Column {
 #pragma unroll
         for (int i = 0; i < N / 2; ++i) {
             if constexpr (sizeof(T) == 4) v[i] = make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
-            else if constexpr (VEC) v[i] = make_float2(bf16_lo(w[i]), bf16_hi(w[i]));
+            else if constexpr (VEC > 0) v[i] = make_float2(bf16_lo(w[i]), bf16_hi(w[i]));
             else v[i] = make_float2(__uint_as_float(w[2 * i] << 16), __uint_as_float(w[2 * i + 1] << 16));
         }
     }
     static LL_DEVINL void store(T* p, const float2 (&v)[N / 2], int n) {
-        if constexpr (VEC) {
+        if constexpr (VEC == 1) {
+#pragma unroll
+            for (int i = 0; i < N / 2; ++i) {
+                if (2 * i >= n) continue;
+                if constexpr (sizeof(T) == 2) reinterpret_cast<uint32_t*>(p)[i] = pack_bf16x2(v[i].x, v[i].y);
+                else reinterpret_cast<float2*>(p)[i] = v[i];
+            }
+        } else if constexpr (VEC == 2) {
             uint32_t o[WORDS];
 #pragma unroll
             for (int i = 0; i < N / 2; ++i) {
@@ -140,9 +159,12 @@ struct Column {
 };
 
 // Gains of a column (0 behind its elements).
-template <int N, bool VEC>
+template <int N, int VEC>
 LL_DEVINL void load_gains(const float* p, int n, float2 (&v)[N / 2]) {
-    if (VEC) {
+    if (VEC == 1) {
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) v[i] = 2 * i < n ? __ldg(reinterpret_cast<const float2*>(p) + i) : make_float2(0.f, 0.f);
+    } else if (VEC == 2) {
 #pragma unroll
         for (int i = 0; i < N / 4; ++i) {
             const float4 x = __ldg(reinterpret_cast<const float4*>(p) + i);
@@ -174,7 +196,7 @@ LL_DEVINL int norm_position(const int32_t* positions, int t, int max_position, i
 
 // The (cos, sin) entries of a thread's two columns, as whole pairs of elements: half-split, c[i], s[i] belong to
 // elements 2 i and 2 i + 1 of both columns; interleaved, to pair i of the thread's N, with s = (-sin, sin).
-template <int N, bool HALF, bool VEC>
+template <int N, bool HALF, int VEC>
 struct Turn {
     static constexpr int M = HALF ? N / 2 : N;
     float2 c[M], s[M];
@@ -183,8 +205,10 @@ struct Turn {
 #pragma unroll
         for (int i = 0; i < N / 2; ++i) {               // two pairs of the head at a time
             float4 x;
-            if (VEC) {
+            if (VEC == 2) {
                 x = __ldg(reinterpret_cast<const float4*>(cs) + i);
+            } else if (VEC == 1 && HALF) {
+                x = 2 * i < col.n0 ? __ldg(reinterpret_cast<const float4*>(cs) + i) : make_float4(1.f, 0.f, 1.f, 0.f);
             } else {
                 // pairs 2 i, 2 i + 1 of the thread: of elements in the column (half), or in either column (interleaved)
                 const int have = HALF ? col.n0 : (col.n0 + col.n1) / 2;
@@ -207,10 +231,10 @@ struct Turn {
 
 // Forward.  The gains are taken into the factors of the rotation once for a thread's U heads of a token: with a, b
 // the columns of x,  a' = r (a fa + b ga),  b' = r (b fb + a gb)  (interleaved: a' = r (a fa + swapped(a) ga), b' likewise).
-template <typename T, int N, bool HALF, int W, bool VEC>
+template <typename T, int N, bool HALF, int W, int VEC>
 __global__ void __launch_bounds__(kNormThreads) norm_rope_kernel(const NormRopeArgs a, const HeadSplit hs, float inv_d) {
     using Col = Column<T, N, VEC>;
-    constexpr int P = N / 2, U = kNormHeads<T>;
+    constexpr int P = N / 2, U = kNormHeads<T, VEC>;
     pdl_wait();
     pdl_trigger();
     const int group = threadIdx.x / W, lane = threadIdx.x % W;
@@ -404,11 +428,11 @@ LL_DEVINL void grad_values(float sum_sq, float sum_dot, float inv_d, float eps, 
 // their way before the first is used, the token's position read a turn ahead.  A thread keeps the gain gradients of its
 // columns over all its tokens.  The sums of a CTA's groups meet in shared memory in a fixed order, those of the CTAs in a
 // second kernel: the same bits every time.
-template <typename T, int N, bool HALF, int W, bool VEC>
+template <typename T, int N, bool HALF, int W, int VEC>
 __global__ void __launch_bounds__(kNormGradThreads, N == 4 ? kNormGradCtasPerSm : 2)
     norm_rope_grad_kernel(const NormRopeGradArgs a, const HeadSplit q_split, const HeadSplit k_split, int q_ctas, float inv_d) {
     using Col = Column<T, N, VEC>;
-    constexpr int P = N / 2, U = kNormGradHeads<T>;
+    constexpr int P = N / 2, U = kNormGradHeads<T, VEC>;
     extern __shared__ float s_dg[];                       // [groups][head_dim]
     pdl_wait();
     pdl_trigger();
@@ -513,7 +537,7 @@ template <bool HALF, int W>
 __global__ void __launch_bounds__(kNormGradThreads, kNormGradCtasPerSm)
     norm_rope_grad_bulk_kernel(const NormRopeGradArgs a, const HeadSplit q_split, const HeadSplit k_split, int q_ctas, float inv_d) {
     using T = __nv_bfloat16;
-    using Col = Column<T, 4, true>;
+    using Col = Column<T, 4, 2>;
     constexpr int P = 2, U = kNormGradHeads<T>, BYTES = kGradTurnBytes;
     extern __shared__ __align__(128) uint8_t s_turn[];    // [kGradStages][x, dy]; then the groups' gain gradients
     __shared__ uint64_t full[kGradStages];
@@ -533,7 +557,7 @@ __global__ void __launch_bounds__(kNormGradThreads, kNormGradCtasPerSm)
     const int parts = isq ? q_split.parts : k_split.parts, d = a.head_dim;
     const int group = threadIdx.x / W, lane = threadIdx.x % W;
     const int slot = group / rows, row = group - slot * rows;
-    const Columns<4, HALF, true> col(lane, d, a.rotary_dim);
+    const Columns<4, HALF, 2> col(lane, d, a.rotary_dim);
     const int gap = col.e1 - col.e0;
     const bool worker = slot < slots && lane < q_split.lanes;
     if (threadIdx.x == 0) {
@@ -566,8 +590,8 @@ __global__ void __launch_bounds__(kNormGradThreads, kNormGradCtasPerSm)
 #pragma unroll
     for (int i = 0; i < P; ++i) g0[i] = g1[i] = dg0[i] = dg1[i] = make_float2(0.f, 0.f);
     if (worker) {
-        load_gains<4, true>(m.gain + col.e0, 4, g0);
-        load_gains<4, true>(m.gain + col.e1, 4, g1);
+        load_gains<4, 2>(m.gain + col.e0, 4, g0);
+        load_gains<4, 2>(m.gain + col.e1, 4, g1);
     }
     int t = cta * slots + slot, n = 0;
     int pos_next = slot < slots && t < a.tokens ? a.positions[t] : 0;
@@ -578,7 +602,7 @@ __global__ void __launch_bounds__(kNormGradThreads, kNormGradCtasPerSm)
         const bool here = slot < slots && t < a.tokens, known = pos >= 0 && pos < a.max_position;
         if (here && !known && lane == 0 && row == 0) flag_status(a.status, LL_DEV_BAD_POSITION);
         const bool live = here && known && worker;
-        Turn<4, HALF, true> turn;
+        Turn<4, HALF, 2> turn;
         if (live && col.turn) turn.load(a.table, pos, a.rotary_dim >> 1, col);
         for (int part = 0; part < parts; ++part, ++n) {
             const int st = n % kGradStages, h0 = part * rows * U + row;
@@ -730,12 +754,12 @@ __global__ void __launch_bounds__(1024) norm_rope_gains_kernel(const float* part
 }
 
 // f(N, W, VEC) with the constants of a call: columns of four elements, of eight where a head then needs more than a warp
-// (and no group for longer heads: a warp takes two passes over each).  Whole, aligned columns take vector loads (4096
-// tokens of 32 + 8 BF16 heads of 128, gradient: 42 us; element by element, 98 of 128 rotated, 111; a warp per head 300).
-// BF16, 16384 tokens of 32 + 8 heads of 128: 64 us with columns of four, 76 with eight (twice the registers).
+// (and no group for longer heads: a warp takes two passes over each).  Whole, aligned columns take vector loads, others loads
+// of two elements where they lie for it (BF16, 32 + 8 heads of 128, 16384 tokens, and the gradient of 4096: all of a head
+// rotated 62 and 37 us; 100 elements, in pairs, 159 and 70; 98 half-split, element by element, 236 and 75; a warp per head
+// took 300 for the gradient).  16384 tokens: 64 us with columns of four, 76 with eight (twice the registers).
 struct NormShape {
-    int n, lanes;
-    bool vec;
+    int n, lanes, vec;
 };
 
 bool rows_on(const void* p, long long stride, int esz, int bytes) {
@@ -746,14 +770,26 @@ bool rows_on(const void* p, long long stride, int esz, int bytes) {
 NormShape norm_shape(int head_dim, int rotary_dim, bool interleaved) {
     for (int n : {4, 8}) {
         const int lanes = head_lanes(head_dim, rotary_dim, n, interleaved);
-        if (lanes <= 32) return {n, lanes, head_dim % (2 * n) == 0 && rotary_dim % (2 * n) == 0};
+        if (lanes <= 32)
+            return {n, lanes, head_dim % (2 * n) == 0 && rotary_dim % (2 * n) == 0 ? 2 : head_dim % 2 == 0 && (interleaved || rotary_dim % 4 == 0) ? 1 : 0};
     }
-    return {0, 0, false};
+    return {0, 0, 0};
+}
+
+// The widest loads that a shape allows and its tensors lie for: lies(bytes of a column's load, bytes of a gain's).
+template <typename F>
+int load_form(const NormShape& s, int esz, F&& lies) {
+    const bool pairs = s.vec > 0 && lies(2 * esz, 8);
+    return s.vec == 2 && lies(std::min(16, s.n * esz), 16) ? 2 : pairs ? 1 : 0;
 }
 
 template <typename F>
 cudaError_t for_shape(const NormShape& s, F&& f) {
-    const auto with = [&](auto n, auto w) { return s.vec ? f(n, w, std::true_type{}) : f(n, w, std::false_type{}); };
+    const auto with = [&](auto n, auto w) {
+        return s.vec == 2   ? f(n, w, std::integral_constant<int, 2>{})
+               : s.vec == 1 ? f(n, w, std::integral_constant<int, 1>{})
+                            : f(n, w, std::integral_constant<int, 0>{});
+    };
     using Four = std::integral_constant<int, 4>;
     if (s.n == 8) return with(std::integral_constant<int, 8>{}, std::integral_constant<int, 32>{});
     if (s.lanes <= 4) return with(Four{}, std::integral_constant<int, 4>{});
@@ -767,14 +803,16 @@ cudaError_t norm_rope_for(const NormRopeArgs& a, cudaStream_t stream) {
     constexpr int E = (int)sizeof(T);
     const int H = a.n_heads + a.n_kv_heads;
     NormShape s = norm_shape(a.head_dim, a.rotary_dim, a.interleaved);
-    const int bytes = std::min(16, s.n * E);
-    s.vec = s.vec &&
-            (a.n_heads == 0 || (rows_on(a.q, a.q_stride, E, bytes) && rows_on(a.q_out, a.q_out_stride, E, bytes) && rows_on(a.q_gain, 0, 4, 16))) &&
-            (a.n_kv_heads == 0 || (rows_on(a.k, a.k_stride, E, bytes) && rows_on(a.k_out, a.k_out_stride, E, bytes) && rows_on(a.k_gain, 0, 4, 16)));
+    // on `bytes` and gains on `gain`
+    const auto lies = [&](int bytes, int gain) {
+        return (a.n_heads == 0 || (rows_on(a.q, a.q_stride, E, bytes) && rows_on(a.q_out, a.q_out_stride, E, bytes) && rows_on(a.q_gain, 0, 4, gain))) &&
+               (a.n_kv_heads == 0 || (rows_on(a.k, a.k_stride, E, bytes) && rows_on(a.k_out, a.k_out_stride, E, bytes) && rows_on(a.k_gain, 0, 4, gain)));
+    };
+    s.vec = load_form(s, E, lies);
     trace_before("norm_rope", stream);
     cudaError_t e;
     if (s.n) {
-        HeadSplit hs = head_split(s.lanes, H, kNormHeads<T>, kNormThreads);
+        HeadSplit hs = head_split(s.lanes, H, s.vec == 2 ? kNormHeads<T> : kNormHeads<T, 0>, kNormThreads);
         const dim3 grid((unsigned)((a.tokens + hs.slots - 1) / hs.slots), (unsigned)hs.parts);
         e = for_shape(s, [&](auto n, auto w, auto vec) {
             return launch_pdl(a.interleaved ? norm_rope_kernel<T, n.value, false, w.value, vec.value> : norm_rope_kernel<T, n.value, true, w.value, vec.value>,
@@ -810,11 +848,12 @@ cudaError_t norm_rope_grad_for(const NormRopeGradArgs& a, cudaStream_t stream) {
     constexpr int E = (int)sizeof(T);
     const int most = std::min(kNormGradMaxCtas, std::max(1, device_sm_count()) * kNormGradCtasPerSm);
     NormShape s = norm_shape(a.head_dim, a.rotary_dim, a.interleaved);
-    const int bytes = std::min(16, s.n * E);
-    s.vec = s.vec &&
-            (a.n_heads == 0 || (rows_on(a.q, a.q_stride, E, bytes) && rows_on(a.dq, a.dq_stride, E, bytes) && rows_on(a.q_grad, a.q_grad_stride, E, bytes) && rows_on(a.q_gain, 0, 4, 16))) &&
-            (a.n_kv_heads == 0 || (rows_on(a.k, a.k_stride, E, bytes) && rows_on(a.dk, a.dk_stride, E, bytes) && rows_on(a.k_grad, a.k_grad_stride, E, bytes) && rows_on(a.k_gain, 0, 4, 16)));
-    const bool bulk = E == 2 && s.vec && s.n == 4 &&
+    const auto lies = [&](int bytes, int gain) {
+        return (a.n_heads == 0 || (rows_on(a.q, a.q_stride, E, bytes) && rows_on(a.dq, a.dq_stride, E, bytes) && rows_on(a.q_grad, a.q_grad_stride, E, bytes) && rows_on(a.q_gain, 0, 4, gain))) &&
+               (a.n_kv_heads == 0 || (rows_on(a.k, a.k_stride, E, bytes) && rows_on(a.dk, a.dk_stride, E, bytes) && rows_on(a.k_grad, a.k_grad_stride, E, bytes) && rows_on(a.k_gain, 0, 4, gain)));
+    };
+    s.vec = load_form(s, E, lies);
+    const bool bulk = E == 2 && s.vec == 2 && s.n == 4 &&
                       (a.n_heads == 0 || (rows_on(a.q, a.q_stride, E, 16) && rows_on(a.dq, a.dq_stride, E, 16))) &&
                       (a.n_kv_heads == 0 || (rows_on(a.k, a.k_stride, E, 16) && rows_on(a.dk, a.dk_stride, E, 16)));
     int q_rows = 0, k_rows = 0;                           // of partials
@@ -823,8 +862,9 @@ cudaError_t norm_rope_grad_for(const NormRopeGradArgs& a, cudaStream_t stream) {
     if (a.tokens == 0) {                                  // the gains' gradients are zeros
     } else if (s.n) {
         // CTAs for q and for k, as many as their tokens ask for, in proportion to their heads up to what runs at once
-        const HeadSplit qs = head_split(s.lanes, std::max(a.n_heads, 1), kNormGradHeads<T>, kNormGradThreads);
-        const HeadSplit ks = head_split(s.lanes, std::max(a.n_kv_heads, 1), kNormGradHeads<T>, kNormGradThreads);
+        const int per_thread = s.vec == 2 ? kNormGradHeads<T> : kNormGradHeads<T, 0>;
+        const HeadSplit qs = head_split(s.lanes, std::max(a.n_heads, 1), per_thread, kNormGradThreads);
+        const HeadSplit ks = head_split(s.lanes, std::max(a.n_kv_heads, 1), per_thread, kNormGradThreads);
         q_rows = a.n_heads ? (a.tokens + qs.slots - 1) / qs.slots : 0;
         k_rows = a.n_kv_heads ? (a.tokens + ks.slots - 1) / ks.slots : 0;
         if (q_rows + k_rows > most) {
