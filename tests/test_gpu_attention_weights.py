@@ -419,3 +419,70 @@ def test_prompt_streams_and_graphs():
     graph.replay()
     check_status(st)
     assert torch.equal(w, want)
+
+
+# ---------------------------------------------------------------- calls that follow each other on one stream
+
+@pytest.mark.parametrize("int8", [False, True])
+def test_calls_of_a_stream_share_a_workspace(int8):
+    """Prompts' weights and then a step's, and steps of other batches, over one workspace without a wait between: the same
+    bits as with workspaces of their own.  (The step's first kernel starts before the one in front has ended.)"""
+    H, Hkv, d, block = 8, 2, 128, 64
+    long = Paged([1900], Hkv, d, block, 1)                               # the normalisers of its rows: 1900 x 8
+    wide = Paged([700, 9000, 65, 3000, 1024, 8000], Hkv, d, block, 2, int8)
+    few = Paged([8300, 20], Hkv, d, block, 3, int8)                      # (nine splits: BF16 calls have a dispatch order too)
+    one = Paged([40], Hkv, d, block, 4, True)                            # one split: its dispatch order lies far in front
+    g = torch.Generator().manual_seed(5)
+    q = {n: torch.randn(n, H, d, generator=g).bfloat16().cuda() for n in (1, 2, 6, 1900)}
+    cu, scale, st = i32([0, 1900]), 1 / math.sqrt(d), api.new_status()
+
+    def step(c, w, ws):
+        x = q[len(c.ctx)]
+        if c.int8:
+            return api.paged_attention_decode_weights_q8(x, c.pool, c.d_table, c.d_ctx, scale, w, workspace=ws, status=st)
+        return api.paged_attention_decode_weights(x, c.k, c.v, c.d_table, c.d_ctx, scale, w, workspace=ws, status=st)
+
+    def chain(ws):
+        cases = (long, one, wide, few, wide, one, long)
+        w = [torch.zeros(len(c.ctx), Hkv, c.table.shape[1] * block, device="cuda") for c in cases]
+        torch.cuda.synchronize()
+        out = []
+        for c, x in zip(cases, w):
+            if c is long:
+                api.paged_attention_weights(q[1900], cu, c.k, c.d_table, c.d_ctx, scale, x, 1900, workspace=ws, status=st)
+            else:
+                out.append(step(c, x, ws))
+        check_status(st)
+        return w + out
+
+    want = chain(None)
+    size = max([api.attention_decode_weights_workspace_size(len(c.ctx), H, Hkv, d, c.table.shape[1], block) for c in (one, wide, few)] +
+               [api.attention_weights_workspace_size(1, 1900, 1900, H, Hkv, d, long.table.shape[1], block)])
+    ws = torch.full((size,), 255, dtype=torch.uint8, device="cuda")
+    for _ in range(20):
+        assert all(torch.equal(a, b) for a, b in zip(chain(ws), want))
+
+
+@pytest.mark.parametrize("int8", [False, True])
+def test_context_lengths_from_the_kernel_in_front(int8):
+    """The lengths are written by the kernel in front of the call, as a server's `ctx += 1` does: the call sees them."""
+    H, Hkv, d, block = 8, 2, 128, 64
+    c = Paged([8300, 8200], Hkv, d, block, 6, int8)
+    q = torch.randn(2, H, d, generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
+    scale, st, ctx = 1 / math.sqrt(d), api.new_status(), i32([0, 0])
+    zero = lambda: torch.zeros(2, Hkv, c.table.shape[1] * block, device="cuda")  # noqa: E731
+
+    def call(ctx, w):
+        if int8:
+            return api.paged_attention_decode_weights_q8(q, c.pool, c.d_table, ctx, scale, w, status=st)
+        return api.paged_attention_decode_weights(q, c.k, c.v, c.d_table, ctx, scale, w, status=st)
+
+    lens = [(8300, 8200), (1, 8193), (8300, 40), (0, 0), (8256, 8200)]
+    for n in lens * 4:
+        a, b, new = zero(), zero(), i32(n)
+        torch.cuda.synchronize()
+        ctx.copy_(new)
+        out = call(ctx, a)
+        check_status(st)
+        assert torch.equal(out, call(new, b)) and torch.equal(a, b)
+        ctx.zero_()

@@ -362,6 +362,8 @@ int run_layer(const ll_config* cfg, const void* packed, const void* x, const int
         at.part_o = reinterpret_cast<float*>(ws + L.attn);
         at.part_ml = at.part_o + rows * d;
         at.status = status;
+        // (in front is the QKV product's or the INT8 cache write's kernel, which started behind all before this call)
+        at.order_early = true;
         if (sw) {
             at.weights = sw->weights;
             at.weights_width = sw->width;

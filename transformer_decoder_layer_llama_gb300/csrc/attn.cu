@@ -84,6 +84,9 @@ __global__ void __launch_bounds__(kOrderThreads) attn_decode_order_kernel(const 
     extern __shared__ int s_ord[];             // [batch] context, [batch] full-split prefix, [batch] partial slot -> sequence
     __shared__ long long s_warp[32];
     pdl_trigger();
+    // The kernel in front may still read the memory that the table goes to (another call over the same workspace, or over
+    // memory that the caller has just let go), or be the one that writes the context lengths.
+    if (!a.order_early) pdl_wait();
     const int B = a.batch, Hkv = a.n_kv_heads;
     const int max_ctx = a.max_blocks * a.block_size;
     int* s_c = s_ord;
@@ -151,7 +154,7 @@ __global__ void __launch_bounds__(kOrderThreads) attn_decode_order_kernel(const 
         a.order[L] = e;
     }
     // the split kernel waits for this grid only: keep it ordered after the kernel before
-    pdl_wait();
+    if (a.order_early) pdl_wait();
 }
 
 // The work of this CTA of the split grid: from the dispatch order when there is one, else

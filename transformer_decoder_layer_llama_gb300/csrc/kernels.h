@@ -183,6 +183,7 @@ struct AttnDecodeArgs {
     const float* k_scale;          // ... and their scales [num_blocks, n_kv_heads, block_size]
     const float* v_scale;
     int4* order;                   // dispatch order of the split grid, in the scratch (set by the launcher)
+    bool order_early;              // the kernel in front neither uses the scratch nor writes context_lens: no wait for it
     float* weights;                // attention weights to add to, [batch][n_kv_heads][weights_width], or null
     int weights_width;
     float* scores;                 // with weights: scratch [batch][n_heads][score_stride]
