@@ -335,3 +335,17 @@ def test_what_the_binding_refuses():
         api.norm_rope(**{**ok, "q": ok["q"].clone().requires_grad_()})
     one = {n: t if n in ("q_gain", "k_gain", "table", "status") else t[:1] for n, t in ok.items()}
     assert torch.equal(api.norm_rope(**one)[0], api.norm_rope(**ok)[0][:1])
+
+
+# Q alone with so many heads that the last turn of a token has groups without one (the smallest such sizes of their forms:
+# float32 or loads of two elements with a head in 32 and in 16 lanes, whole BF16 columns likewise), and K alone.
+ALONE = [(3, 127, 0, 256, 256), (2, 541, 0, 128, 100), (2, 295, 0, 256, 256), (1, 1261, 0, 128, 128), (3, 0, 127, 256, 256),
+         (2, 0, 541, 128, 98), (1, 1400, 0, 80, 50), (2, 126, 1, 256, 10), (2, 127, 1, 256, 256), (2, 300, 0, 33, 32)]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("case", ALONE)
+def test_many_heads_of_one_kind(case, layout, dtype):
+    test_forward(case, layout, dtype)
+    test_gradient(case, layout, dtype)

@@ -316,8 +316,8 @@ int ll_norm_rope(const ll_head_rows* q, const ll_head_rows* k, int32_t dtype, co
     a.k_stride = k->stride;
     a.q_out_stride = q_out->stride;
     a.k_out_stride = k_out->stride;
-    a.q_gain = q_gain;
-    a.k_gain = k_gain;
+    a.q_gain = q->n_heads > 0 ? q_gain : k_gain;          // (no null pointer for heads that are not there)
+    a.k_gain = k->n_heads > 0 ? k_gain : q_gain;
     a.positions = positions;
     a.table = static_cast<const float2*>(table);
     a.tokens = tokens;

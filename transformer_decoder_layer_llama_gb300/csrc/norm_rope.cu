@@ -9,6 +9,7 @@
 #include <type_traits>
 
 #include "common.cuh"
+#include "head_split.h"
 #include "kernels.h"
 #include "vec16.cuh"
 
@@ -29,29 +30,9 @@ template <typename T, int VEC = 2>
 constexpr int kNormGradHeads = VEC < 2 || sizeof(T) == 4 ? 2 : 4;
 constexpr int kNormAnyWarps = 4;       // of the gradient's CTA for heads that no group holds
 
-// How threads share a token's heads: a head is `lanes` threads of a group of W (a power of two), each with two columns
-// of N elements; a token is `rows` groups, each with up to U heads at a time, in `parts` turns; a CTA has `slots` tokens
-// at a time.
-struct HeadSplit {
-    int lanes, width, rows, parts, slots, threads;
-};
-
 int head_lanes(int head_dim, int rotary_dim, int n, bool interleaved) {
     const int turned = interleaved ? (rotary_dim + 2 * n - 1) / (2 * n) : (rotary_dim / 2 + n - 1) / n;
     return turned + (head_dim - rotary_dim + 2 * n - 1) / (2 * n);
-}
-
-HeadSplit head_split(int lanes, int heads, int per_thread, int threads) {
-    HeadSplit s;
-    s.lanes = lanes;
-    s.width = 4;
-    while (s.width < s.lanes) s.width *= 2;
-    const int most = threads / s.width;
-    s.parts = (heads + per_thread * most - 1) / (per_thread * most);
-    s.rows = (heads + per_thread * s.parts - 1) / (per_thread * s.parts);
-    s.slots = std::max(1, most / s.rows);
-    s.threads = (s.slots * s.rows * s.width + 31) / 32 * 32;
-    return s;
 }
 
 // A thread's two columns, at e0 and e1, of n0 and n1 elements (N each where a head divides into whole columns: VEC 2; VEC 1:
@@ -243,7 +224,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_rope_kernel(const NormRopeA
     const bool here = slot < hs.slots && t < a.tokens, mine = here && lane < hs.lanes;
     const Columns<N, HALF, VEC> col(lane, a.head_dim, a.rotary_dim);
     const int H = a.n_heads + a.n_kv_heads, gap = col.e1 - col.e0;
-    const int h0 = blockIdx.y * hs.rows * U + row;
+    const int h0 = first_head(hs, blockIdx.y, row, U);
     const int pos_read = here ? a.positions[t] : 0;
     const T* q = static_cast<const T*>(a.q) + (size_t)t * a.q_stride + col.e0;
     const T* k = static_cast<const T*>(a.k) + (size_t)t * a.k_stride + col.e0 - (long long)a.n_heads * a.head_dim;
@@ -286,7 +267,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_rope_kernel(const NormRopeA
         }
     };
     bool gain_q = h0 < a.n_heads;
-    if (live) factors(gain_q ? a.q_gain : a.k_gain);
+    if (live && h0 < H) factors(gain_q ? a.q_gain : a.k_gain);      // (no head, no gain: Q alone has no k_gain)
     T* q_out = static_cast<T*>(a.q_out) + (size_t)t * a.q_out_stride + col.e0;
     T* k_out = static_cast<T*>(a.k_out) + (size_t)t * a.k_out_stride + col.e0 - (long long)a.n_heads * a.head_dim;
 #pragma unroll
