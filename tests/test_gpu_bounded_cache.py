@@ -340,3 +340,61 @@ def test_weights_beyond_32_bits():
     assert all(torch.equal(a, b) for a, b in zip(*out)) and all(torch.equal(a, b) for a, b in zip(*pools))
     assert (out[0][3][-1, -1, :200] > 0).all()
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("kind", ["weights", "bf16", "e4m3"])
+def test_capturing_between_steps_changes_nothing(kind):
+    """Prompts, steps, the capture, steps: pools, weights, status and the last outputs are the same bits before and after
+    capture_decode, whatever lies in x by then, and the replayed steps are those of an engine that captures nothing."""
+    from transformer_decoder_layer_llama_gb300.serving import BlockAllocator, Scheduler, StackEngine
+    d, L, nb, mb, slots, prompt = synth.DIMS_TINY, 2, 40, 5, 3, 21
+    layers = [layer(d, 80 + l) for l in range(L)]
+    cfg, packed = layers[0][0], [p for _, p in layers]
+    results = []
+    for captured in (False, True):
+        sch = Scheduler(slots, d.block_size, mb, BlockAllocator(nb, seed=5), seed=6, prompt_len=prompt)
+        if kind == "e4m3":
+            pools = [api.PoolF8.empty(nb, d.n_kv_heads, d.block_size, d.head_dim) for _ in range(L)]
+            parts = [t.view(torch.uint8) for p in pools for t in (p.k, p.v)] + [t for p in pools for t in (p.k_scale, p.v_scale)]
+        else:
+            pools = [tuple(t.cuda() for t in synth.make_pool(nb, d, seed=l)) for l in range(L)]
+            parts = [t for p in pools for t in p]
+        eng = StackEngine(api, [cfg] * L, packed, pools, slots, mb, slots * prompt, track_weights=kind == "weights")
+        state = parts + (eng.weights or []) + [eng.status]
+        for s in range(slots):
+            sch.start_resident(s, prompt)
+        eng.pf_table.copy_(torch.from_numpy(sch.table))
+        eng.pf_ctx.fill_(prompt)
+        eng.pf_pos.copy_(torch.arange(prompt, dtype=torch.int32).repeat(slots))
+        eng.pf_x.copy_(synth.make_x(slots * prompt, d.hidden, seed=1))
+        stream = torch.cuda.Stream()
+        torch.cuda.synchronize()
+        eng.prefill(slots, prompt, stream, **({"slots": [0, 1, 2]} if kind == "weights" else {}))
+        ys = []
+        for i in range(6):
+            stream.synchronize()
+            if captured and i in (0, 3):
+                eng.x.copy_(synth.make_x(slots, d.hidden, seed=99))
+                torch.cuda.synchronize()
+                before, y = [t.clone() for t in state], None if i == 0 else eng.y.clone()
+                torch.cuda.synchronize()
+                eng.capture_decode(stream)
+                stream.synchronize()
+                assert all(torch.equal(a, b) for a, b in zip(before, state))
+                assert y is None or torch.equal(y, eng.y)
+                if i == 0:
+                    eng.graph = None                          # (the next steps as plain calls)
+            ctx = sch.grow_for_decode()
+            eng.table.copy_(torch.from_numpy(sch.table))
+            eng.ctx.copy_(torch.from_numpy(ctx))
+            if kind == "weights":
+                eng.pos.copy_(torch.from_numpy(sch.positions()))
+            eng.x.copy_(synth.make_x(slots, d.hidden, seed=10 + i))
+            torch.cuda.synchronize()
+            eng.decode(stream)
+            stream.synchronize()
+            ys.append(eng.y.clone())
+        torch.cuda.synchronize()
+        assert int(eng.status.item()) == 0
+        results.append(ys + [t.clone() for t in state])
+    assert all(torch.equal(a, b) for a, b in zip(*results))

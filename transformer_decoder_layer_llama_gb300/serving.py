@@ -429,9 +429,18 @@ class StackEngine:
         return slots
 
     def capture_decode(self, stream):
-        """Records the all-layer decode step once as a CUDA graph (replayed by decode())."""
+        """Records the all-layer decode step once as a CUDA graph (replayed by decode()).  Pools, attention weights, status
+        and the last step's outputs stay as they are, so it can be called at any place between steps."""
+        held = self.ctx, self.status, self.bufs
         with torch.cuda.stream(stream):
-            self.y = self._decode_layers(stream)      # warm-up outside the capture
+            # warm-up outside the capture: over empty contexts it writes no row and adds no weight, and what it flags
+            # and puts out goes elsewhere
+            self.ctx, self.status = torch.zeros_like(self.ctx), torch.zeros_like(self.status)
+            self.bufs = [torch.empty_like(b) for b in self.bufs]
+            try:
+                self._decode_layers(stream)
+            finally:
+                self.ctx, self.status, self.bufs = held
         stream.synchronize()
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g, stream=stream):
