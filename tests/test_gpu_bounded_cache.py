@@ -398,3 +398,65 @@ def test_capturing_between_steps_changes_nothing(kind):
         assert int(eng.status.item()) == 0
         results.append(ys + [t.clone() for t in state])
     assert all(torch.equal(a, b) for a, b in zip(*results))
+
+
+def test_a_slot_starts_anew():
+    """A request in the slot of one that has ended: its sums are those of a fresh engine's, and a prefill that does not say
+    whose slots it fills is refused before anything is written; so are steps whose positions were never given."""
+    from transformer_decoder_layer_llama_gb300.serving import BlockAllocator, Scheduler, StackEngine
+    d, nb, mb, slots, prompt = synth.DIMS_TINY, 40, 5, 2, 25
+    cfg, packed = layer(d, 90)
+    stream = torch.cuda.Stream()
+
+    def serve(before):
+        """Weights and kept rows of the second request of slot 0; `before`: there was a first one."""
+        pools = [tuple(t.cuda() for t in synth.make_pool(nb, d, seed=3))]
+        sch = Scheduler(slots, d.block_size, mb, BlockAllocator(nb, seed=5), seed=6, prompt_len=prompt)
+        eng = StackEngine(api, [cfg], [packed], pools, slots, mb, slots * prompt, track_weights=True)
+        sch.start_resident(1, 3)
+        for turn in range(2 if before else 1):
+            sch.start_resident(0, prompt)
+            eng.pf_table[:1].copy_(torch.from_numpy(sch.table[:1]))
+            eng.pf_pos[:prompt].copy_(torch.arange(prompt, dtype=torch.int32))
+            eng.pf_x[:prompt].copy_(synth.make_x(prompt, d.hidden, seed=7 + (before and turn == 0)))
+            torch.cuda.synchronize()
+            held = [t.clone() for t in (*pools[0], *eng.weights)]
+            with pytest.raises(ValueError, match="slots"):
+                eng.prefill(1, prompt, stream)
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(held, (*pools[0], *eng.weights)))
+            eng.prefill(1, prompt, stream, slots=[0], observe=9)
+            kept = eng.weights[0].clone()
+            eng.prefill(1, prompt, stream, slots=[])          # (leaves the weights)
+            stream.synchronize()
+            assert torch.equal(kept[0], eng.weights[0][0])
+            for i in range(7):
+                ctx = sch.grow_for_decode()
+                eng.table.copy_(torch.from_numpy(sch.table))
+                eng.ctx.copy_(torch.from_numpy(ctx))
+                eng.pos.copy_(torch.from_numpy(sch.positions()))
+                eng.x.copy_(synth.make_x(slots, d.hidden, seed=30 + i))
+                torch.cuda.synchronize()
+                eng.decode(stream)
+                stream.synchronize()
+            w = eng.weights[0][0].clone()
+            assert eng.evict(sch, 20, stream, sinks=1, recent=3) == [0]
+            stream.synchronize()
+            rows = [t[torch.tensor(sch.slots[0].blocks).cuda()].transpose(1, 2).flatten(0, 1)[:20].clone() for t in pools[0]]
+            if turn + 1 < (2 if before else 1):
+                sch.retire(0)
+        return [w, eng.weights[0][0].clone(), *rows]
+
+    assert all(torch.equal(a, b) for a, b in zip(serve(True), serve(False)))
+    # positions that nobody gave
+    pools = [tuple(t.cuda() for t in synth.make_pool(nb, d, seed=3))]
+    sch = Scheduler(slots, d.block_size, mb, BlockAllocator(nb, seed=5), seed=6, prompt_len=prompt)
+    eng = StackEngine(api, [cfg], [packed], pools, slots, mb, slots * prompt, track_weights=True)
+    for s in range(slots):
+        sch.start_resident(s, prompt)
+    eng.table.copy_(torch.from_numpy(sch.table))
+    eng.ctx.copy_(torch.from_numpy(sch.grow_for_decode()))
+    torch.cuda.synchronize()
+    eng.decode(stream)
+    stream.synchronize()
+    assert int(eng.status.item()) == api.LL_DEV_BAD_POSITION

@@ -264,7 +264,7 @@ class StackEngine:
         self.weights = None
         if track_weights:
             self.weights = [torch.zeros(n_slots, cfg.n_kv_heads, max_blocks * cfg.block_size, device=device) for _ in cfgs]
-            self.pos = torch.zeros(n_slots, dtype=torch.int32, device=device)
+            self.pos = torch.full((n_slots,), -1, dtype=torch.int32, device=device)      # (flagged by a step until it is filled)
             self.step_ws = api.new_workspace_weights(cfg, n_slots, max_blocks, device)
         self._blocks = None
         self.status = api.new_status(device)
@@ -286,8 +286,12 @@ class StackEngine:
         inputs are in pf_x[:n_req * prompt_len]; their positions in pf_pos (BF16 pools) or their
         context lengths, which count the prompt, in pf_ctx (e4m3 pools).  With track_weights, `slots` names
         the requests' slots: their attention weights start as those of the last `observe` tokens (None: all) of
-        each prompt."""
+        each prompt.  (An empty `slots` leaves all weights as they are, those of the slots' last requests among them.)"""
         T = n_req * prompt_len
+        if self.weights is not None and slots is None:
+            raise ValueError("with track_weights, slots must name the requests' slots: their weights are the last requests'")
+        if slots is not None and self.weights is not None and len(slots) == 0:
+            slots = None
         if slots is not None:
             if self.weights is None:
                 raise ValueError("slots are for track_weights")
