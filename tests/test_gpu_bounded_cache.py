@@ -460,3 +460,57 @@ def test_a_slot_starts_anew():
     eng.decode(stream)
     stream.synchronize()
     assert int(eng.status.item()) == api.LL_DEV_BAD_POSITION
+
+
+@pytest.mark.parametrize("kind", ["bf16", "int8"])
+@pytest.mark.parametrize("why", ["too far", "negative", "cache"])
+def test_a_refused_token_leaves_its_row(why, kind):
+    """A step whose token has no rotary position (behind the table, negative, or its place in the cache behind the table with
+    none given): flagged, and codes, scales and rows of that place stay byte for byte, whatever an earlier call has left in the
+    workspace; the other sequences' rows and outputs are those of a step without it."""
+    dims, mb, B, far = DIMS, 5, 6, 2
+    cfg, packed = layer(dims, 3, max_position=64)              # (the table of blocks reaches to 80)
+    table, nb = synth.make_block_table([mb * 16] * B, 16, seed=1)
+    table = table.cuda()
+    ctx = [9, 64, 50, 17, 33, 1]
+    if why == "cache":
+        ctx[far] = 70
+    pos = {"too far": 64, "negative": -1}
+    positions = None if why == "cache" else i32([pos[why] if b == far else c - 1 for b, c in enumerate(ctx)])
+
+    def pool():
+        k, v = (t.cuda() for t in synth.make_pool(nb, dims, seed=5))
+        if kind == "bf16":
+            return k, v
+        p = api.PoolQ8.empty(nb, 2, 16, 128)
+        api.reshape_and_cache_q8(*(t.transpose(1, 2).reshape(nb * 16, 2, 128).contiguous() for t in (k, v)),
+                                 torch.arange(nb * 16, dtype=torch.int32).cuda(), p)
+        return p
+    tensors = lambda p: [p.k, p.v, p.k_scale, p.v_scale] if kind == "int8" else list(p)  # noqa: E731
+    ws = api.new_workspace_weights(cfg, B, mb)
+    w = torch.zeros(B, 2, mb * 16, device="cuda")
+    x, other = (synth.make_x(B, dims.hidden, seed=s).cuda() for s in (2, 3))
+    # the workspace holds another step's rows
+    api.layer_decode_step_weights(cfg, packed, other, pool(), table, i32([5] * B), w, workspace=ws)
+    p, want, st = pool(), pool(), api.new_status()
+    before = [t.clone() for t in tensors(p)]
+    y = api.layer_decode_step_weights(cfg, packed, x, p, table, i32(ctx), w.zero_(), positions=positions, workspace=ws, status=st)
+    check_status(st, api.LL_DEV_BAD_POSITION)
+    good = api.new_status()
+    ref = api.layer_decode_step_weights(cfg, packed, x, want, table, i32([5 if b == far else c for b, c in enumerate(ctx)]),
+                                        torch.zeros_like(w), status=good)
+    check_status(good)
+    rest = [b for b in range(B) if b != far]
+    assert torch.equal(y[rest], ref[rest])
+    for a, old, new in zip(tensors(p), before, tensors(want)):
+        assert torch.equal(a[table[far].long()], old[table[far].long()])
+        assert torch.equal(a[table[rest].long()], new[table[rest].long()])
+    if why == "cache":                                         # the step without weights likewise
+        p, st = pool(), api.new_status()
+        if kind == "int8":
+            api.layer_decode_step_q8(cfg, packed, x, p, table, i32(ctx), workspace=ws, status=st)
+        else:
+            api.layer_decode_step(cfg, packed, x, *p, table, i32(ctx), workspace=ws, status=st)
+        check_status(st, api.LL_DEV_BAD_POSITION)
+        for a, old in zip(tensors(p), before):
+            assert torch.equal(a[table[far].long()], old[table[far].long()])

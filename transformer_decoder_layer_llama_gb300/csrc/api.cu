@@ -261,7 +261,8 @@ int run_layer(const ll_config* cfg, const void* packed, const void* x, const int
     if ((e = ll::launch_gemm(g, stream)) != cudaSuccess) return LL_ERR_CUDA;
     if (pq8 &&
         (e = ll::launch_reshape_and_cache_q8(g.ep.k_pool, g.ep.v_pool, nullptr, decode ? nullptr : positions,
-                                             decode ? context_lens : nullptr, block_table, max_blocks, seq_len, T,
+                                             decode ? context_lens : nullptr, g.ep.rope_positions, cfg->max_position,
+                                             block_table, max_blocks, seq_len, T,
                                              cfg->n_kv_heads, d, cfg->block_size, static_cast<int8_t*>(pq8->k),
                                              static_cast<int8_t*>(pq8->v), pq8->k_scale, pq8->v_scale,
                                              pq8->num_blocks, status, stream)) != cudaSuccess)
@@ -801,7 +802,7 @@ int ll_reshape_and_cache_q8(const void* k, const void* v, const int32_t* slot_ma
     if (head_dim % 32 != 0 || head_dim > 256) return LL_ERR_UNSUPPORTED;
     return cuda_rc(ll::launch_reshape_and_cache_q8(
         static_cast<const __nv_bfloat16*>(k), static_cast<const __nv_bfloat16*>(v), slot_mapping, nullptr,
-        nullptr, nullptr, 0, 1, tokens, n_kv_heads, head_dim, block_size, static_cast<int8_t*>(pool->k),
+        nullptr, nullptr, 0, nullptr, 0, 1, tokens, n_kv_heads, head_dim, block_size, static_cast<int8_t*>(pool->k),
         static_cast<int8_t*>(pool->v), pool->k_scale, pool->v_scale, pool->num_blocks, status,
         static_cast<cudaStream_t>(stream)));
 }

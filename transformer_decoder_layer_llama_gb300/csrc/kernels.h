@@ -138,9 +138,11 @@ cudaError_t launch_rmsnorm_f32(const float* x, const float* g, __nv_bfloat16* ou
 // ReshapeAndCache into an INT8 pool (one warp per token and KV head: absmax, float32
 // scale = absmax / 127, round-half-even codes).  A token's slot comes from `slots`
 // when non-null, else from its position (positions[t], or context_lens[t / seq_len] - 1
-// when positions is null) through block_table (sequence t / seq_len).
+// when positions is null) through block_table (sequence t / seq_len); it is then skipped where that
+// position, or its rotary one (rope_positions[t], where given), is not below max_position.
 cudaError_t launch_reshape_and_cache_q8(const __nv_bfloat16* k, const __nv_bfloat16* v, const int32_t* slots,
                                         const int32_t* positions, const int32_t* context_lens,
+                                        const int32_t* rope_positions, int max_position,
                                         const int32_t* block_table, int max_blocks, int seq_len, int tokens,
                                         int n_kv_heads, int head_dim, int block_size, int8_t* k_pool,
                                         int8_t* v_pool, float* k_scale, float* v_scale, int num_blocks,

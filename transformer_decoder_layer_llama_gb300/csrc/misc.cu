@@ -183,6 +183,7 @@ template <int E>
 __global__ void reshape_and_cache_q8_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __restrict__ v,
                                             const int32_t* __restrict__ slots, const int32_t* __restrict__ positions,
                                             const int32_t* __restrict__ context_lens,
+                                            const int32_t* __restrict__ rope_positions, int max_position,
                                             const int32_t* __restrict__ block_table, int max_blocks, int seq_len,
                                             int tokens, int n_kv_heads, int block_size, int8_t* __restrict__ k_pool,
                                             int8_t* __restrict__ v_pool, float* __restrict__ k_scale,
@@ -200,10 +201,12 @@ __global__ void reshape_and_cache_q8_kernel(const __nv_bfloat16* __restrict__ k,
     } else {
         const int seq = t / seq_len;
         const int pos = positions ? positions[t] : context_lens[seq] - 1;
-        if (pos < 0 || pos / block_size >= max_blocks) {
+        // (a token that the QKV epilogue has refused has no rows in k and v: whatever lies there)
+        if (pos < 0 || pos >= max_position || pos / block_size >= max_blocks) {
             if (h == 0 && lane == 0) flag_status(status, LL_DEV_BAD_POSITION);
             return;
         }
+        if (rope_positions && (rope_positions[t] < 0 || rope_positions[t] >= max_position)) return;
         const int blk = block_table[(size_t)seq * max_blocks + pos / block_size];
         slot = blk < 0 ? (long long)num_blocks * block_size : (long long)blk * block_size + pos % block_size;
     }
@@ -496,6 +499,7 @@ cudaError_t launch_reshape_and_cache(const __nv_bfloat16* k, const __nv_bfloat16
 
 cudaError_t launch_reshape_and_cache_q8(const __nv_bfloat16* k, const __nv_bfloat16* v, const int32_t* slots,
                                         const int32_t* positions, const int32_t* context_lens,
+                                        const int32_t* rope_positions, int max_position,
                                         const int32_t* block_table, int max_blocks, int seq_len, int tokens,
                                         int n_kv_heads, int head_dim, int block_size, int8_t* k_pool,
                                         int8_t* v_pool, float* k_scale, float* v_scale, int num_blocks,
@@ -506,8 +510,8 @@ cudaError_t launch_reshape_and_cache_q8(const __nv_bfloat16* k, const __nv_bfloa
     cudaError_t e = cudaErrorInvalidValue;
 #define LL_Q8_LAUNCH(E_)                                                                                    \
     e = launch_pdl(reshape_and_cache_q8_kernel<E_>, dim3(blocks_for(threads, 256)), dim3(256), 0, stream, 1, \
-                   k, v, slots, positions, context_lens, block_table, max_blocks, seq_len, tokens,            \
-                   n_kv_heads, block_size, k_pool, v_pool, k_scale, v_scale, num_blocks, status)
+                   k, v, slots, positions, context_lens, rope_positions, max_position, block_table,           \
+                   max_blocks, seq_len, tokens, n_kv_heads, block_size, k_pool, v_pool, k_scale, v_scale, num_blocks, status)
     switch (head_dim) {
         case 32: LL_Q8_LAUNCH(1); break;
         case 64: LL_Q8_LAUNCH(2); break;
