@@ -486,3 +486,34 @@ def test_context_lengths_from_the_kernel_in_front(int8):
         check_status(st)
         assert torch.equal(out, call(new, b)) and torch.equal(a, b)
         ctx.zero_()
+
+
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("group", [1, 2, 7])
+def test_a_query_of_nan_reaches_what_it_sees_alone(group, int8):
+    """A NaN query gives NaN to its sequence's and KV head's positions; those without a valid block, behind the context and of
+    other heads and sequences keep their values, as in the prompts' call."""
+    Hkv, d, block = 2, 128, 32
+    c = Paged([1300, 90], Hkv, d, block, 8, int8)
+    q = torch.randn(2, Hkv * group, d, generator=torch.Generator().manual_seed(1)).bfloat16()
+    q[0, group + group // 2, 5] = math.nan                    # sequence 0, KV head 1
+    table = c.table.copy()
+    table[0, [1, 35]] = 10 ** 6, -1
+    table[1, 2] = -1
+    q, base, st = q.cuda(), torch.rand(2, Hkv, c.table.shape[1] * block + 3, generator=torch.Generator().manual_seed(2)).cuda(), api.new_status()
+    w = base.clone()
+    if int8:
+        api.paged_attention_decode_weights_q8(q, c.pool, i32(table), c.d_ctx, 0.1, w, status=st)
+    else:
+        api.paged_attention_decode_weights(q, c.k, c.v, i32(table), c.d_ctx, 0.1, w, status=st)
+    check_status(st, api.LL_DEV_BAD_BLOCK)
+    hole = torch.zeros(1300, dtype=torch.bool)
+    hole[32:64] = hole[35 * 32:36 * 32] = True
+    assert torch.equal(w[0, 1].cpu()[:1300].isnan(), ~hole) and torch.equal(w[0, 1].cpu()[:1300][hole], base[0, 1].cpu()[:1300][hole])
+    assert torch.equal(w[0, :, 1300:], base[0, :, 1300:]) and torch.equal(w[1, :, 64:], base[1, :, 64:])
+    assert torch.equal(w[0, 0, 32:64], base[0, 0, 32:64]) and not w[0, 0].isnan().any() and not w[1].isnan().any()
+    if not int8:                                               # the prompts' call on the same query: the same places
+        again = base.clone()
+        api.paged_attention_weights(q, i32([0, 1, 2]), c.k, i32(table), c.d_ctx, 0.1, again, 1, status=st)
+        check_status(st, api.LL_DEV_BAD_BLOCK)
+        assert torch.equal(again.isnan(), w.isnan())

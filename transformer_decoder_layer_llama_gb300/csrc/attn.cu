@@ -978,6 +978,7 @@ __global__ void __launch_bounds__(kFinishThreads) attn_decode_finish_kernel(cons
     __syncthreads();
     if (p0 >= end) return;
     float4 add[K];
+    bool nan = false;                                             // of a query: its masked scores' sums are NaN too
 #pragma unroll
     for (int k = 0; k < K; ++k) add[k] = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int h0 = 0; h0 < G; h0 += AHEAD) {
@@ -986,6 +987,7 @@ __global__ void __launch_bounds__(kFinishThreads) attn_decode_finish_kernel(cons
             if (h0 + j >= G) break;
             const float lse = s_lse[h0 + j];
             const int h = h0 + AHEAD + j;
+            nan = nan || lse != lse;
 #pragma unroll
             for (int k = 0; k < K; ++k) {
                 add[k].x += ex2_approx(next[k][j].x - lse);
@@ -1002,6 +1004,10 @@ __global__ void __launch_bounds__(kFinishThreads) attn_decode_finish_kernel(cons
     for (int k = 0; k < K; ++k) {
         const int p = p0 + k * kSpan;
         float* w = weights + k * kSpan;
+        if (nan && p < end) {                                     // (all four are in one block: without a valid one nothing is added)
+            const int blk = a.block_table[(size_t)b * a.max_blocks + p / a.block_size];
+            if (blk < 0 || blk >= a.num_blocks) continue;
+        }
         if (aligned && p + E <= end) {
             *reinterpret_cast<float4*>(w) = make_float4(sum[k].x + add[k].x, sum[k].y + add[k].y, sum[k].z + add[k].z, sum[k].w + add[k].w);
         } else {
