@@ -565,7 +565,9 @@ int ll_paged_attention_decode_weights_q8(const void* q, const ll_kv_pool_q8* poo
                                          int32_t head_dim, int32_t block_size, float scale, float* weights, int32_t weights_width,
                                          void* out, void* workspace, size_t workspace_bytes, int32_t* status, void* stream);
 
-/* Workspace bytes for ll_paged_attention_weights (0 for sizes that it refuses). */
+/* Workspace bytes for ll_paged_attention_weights (0 for sizes that it refuses), on the
+ * current device.  Enough for calls of fewer sequences, tokens, rows of a sequence
+ * (max_new) or blocks too: the size does not depend on batch and max_new. */
 size_t ll_attention_weights_workspace_size(int32_t batch, int32_t tokens, int32_t max_new, int32_t n_heads, int32_t n_kv_heads,
                                            int32_t head_dim, int32_t max_blocks, int32_t block_size);
 

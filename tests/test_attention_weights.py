@@ -178,3 +178,14 @@ def test_the_scheduler_cuts_a_request():
             call()
     sch.cut(1, 0)
     assert sch.slots[1].blocks == [] and sch.held_outside() == []
+
+
+def test_a_workspace_is_enough_for_smaller_calls():
+    """One workspace, of the largest call, for calls of fewer rows, tokens, sequences and blocks (which are cut into more pieces)."""
+    size = api.attention_weights_workspace_size
+    for heads, kv in ((64, 8), (32, 32), (16, 1), (7, 7)):
+        most = size(8, 2048, 2048, heads, kv, 128, 256, 128)
+        assert most >= 2048 * heads * 4
+        for batch, tokens, new, blocks in ((8, 2048, 256, 256), (8, 2048, 32, 256), (8, 2048, 1, 256), (1, 2048, 2048, 256), (1, 33, 33, 256),
+                                           (3, 2000, 700, 8), (8, 0, 5, 1)):
+            assert 0 < size(batch, tokens, new, heads, kv, 128, blocks, 128) <= most

@@ -517,3 +517,25 @@ def test_a_query_of_nan_reaches_what_it_sees_alone(group, int8):
         api.paged_attention_weights(q, i32([0, 1, 2]), c.k, i32(table), c.d_ctx, 0.1, again, 1, status=st)
         check_status(st, api.LL_DEV_BAD_BLOCK)
         assert torch.equal(again.isnan(), w.isnan())
+
+
+@pytest.mark.parametrize("heads,kv", [(16, 2), (4, 4), (8, 1)])
+def test_one_workspace_for_smaller_calls(heads, kv):
+    """A workspace of the largest call's size serves calls of fewer sequences, rows and tokens: the same bits as with their own."""
+    ctx, d, block, most = [3000, 2000, 700, 3000, 90, 1500], 64, 32, 300
+    c = Paged(ctx, kv, d, block, 9)
+    wide = c.table.shape[1]
+    q = torch.randn(6 * most, heads, d, generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
+    st, n = api.new_status(), api.attention_weights_workspace_size(6, 6 * most, most, heads, kv, d, wide, block)
+    ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+    for batch in (6, 2, 1):
+        for new in (90, 70, 64, 17, 1):
+            cu = i32([new * b for b in range(batch + 1)])
+            args = (q[:batch * new], cu, c.k, c.d_table[:batch].contiguous(), c.d_ctx[:batch].contiguous(), 0.125)
+            a, b = (torch.zeros(batch, kv, wide * block, device="cuda") for _ in range(2))
+            api.paged_attention_weights(*args, a, new, workspace=ws, status=st)
+            api.paged_attention_weights(*args, b, new, status=st)
+            assert torch.equal(a, b) and api.attention_weights_workspace_size(batch, batch * new, new, heads, kv, d, wide, block) <= n
+    with pytest.raises(api.LayerError):
+        api.paged_attention_weights(*args, a, 1, workspace=ws[:16], status=st)
+    check_status(st)

@@ -550,8 +550,7 @@ int ll_paged_attention_prefill_f8(const void* q, const int32_t* cu_new, int32_t 
 size_t ll_attention_weights_workspace_size(int32_t batch, int32_t tokens, int32_t max_new, int32_t n_heads, int32_t n_kv_heads,
                                            int32_t head_dim, int32_t max_blocks, int32_t block_size) {
     if (tokens < 0 || max_new <= 0 || paged_shape(batch, n_heads, n_kv_heads, head_dim, block_size, max_blocks) != LL_OK) return 0;
-    return align_up(std::max<size_t>(1, ll::observe_scratch_bytes(batch, tokens, std::min(max_new, tokens), n_heads, n_kv_heads,
-                                                                  max_blocks, block_size)));
+    return align_up(std::max<size_t>(1, ll::observe_workspace_bytes(tokens, n_heads, n_kv_heads, max_blocks, block_size)));
 }
 
 int ll_paged_attention_weights(const void* q, const int32_t* cu_new, int32_t tokens, const void* k_pool, int32_t num_blocks,
@@ -570,7 +569,8 @@ int ll_paged_attention_weights(const void* q, const int32_t* cu_new, int32_t tok
     // rows of the pool are TMA coordinates
     if ((int64_t)num_blocks * n_kv_heads * block_size > (1LL << 31) - 1) return LL_ERR_UNSUPPORTED;
     if (!ll::observe_fits(batch, std::min(max_new, tokens), n_heads, n_kv_heads, max_blocks, block_size)) return LL_ERR_UNSUPPORTED;
-    const size_t need = ll_attention_weights_workspace_size(batch, tokens, max_new, n_heads, n_kv_heads, head_dim, max_blocks, block_size);
+    const size_t need = std::max<size_t>(1, ll::observe_scratch_bytes(batch, tokens, std::min(max_new, tokens), n_heads, n_kv_heads,
+                                                                      max_blocks, block_size));
     if (!workspace || workspace_bytes < need || !aligned16(workspace)) return LL_ERR_WORKSPACE;
     ll::ObserveArgs a{};
     a.q = static_cast<const __nv_bfloat16*>(q);

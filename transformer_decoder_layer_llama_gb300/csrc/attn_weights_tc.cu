@@ -33,6 +33,7 @@ constexpr float kLog2eObs = 1.4426950408889634f;
 constexpr int kObsPieceTiles = 2;        // at least, of a piece of a row (the rows are fetched for each)
 constexpr int kObsLoad = 64;             // columns of one load from TMEM (8192 rows of 64 heads over 8: rows 461 us, keys 538; 32: 584, 620)
 constexpr int kObsItems = 4;             // looked up ahead
+constexpr int kObsMostPieces = 16;       // of a row, where sequences have more rows than two A tiles
 
 // FEW: no sequence has more rows than two A tiles.  They then stay: in ROWS beside the keys of a CTA's whole share, in COLS
 // as the B tile that all of its keys meet.
@@ -696,19 +697,18 @@ struct ObsSplit {
 };
 
 ObsSplit obs_split(int batch, int max_new, int n_heads, int n_kv_heads, int max_blocks, int block_size) {
-    constexpr int kRowItems = 4 * 152, kPromptItems = 152, kKeyItems = 6 * 152;
-    const int row_items = 2LL * max_new >= (long long)max_blocks * block_size ? kPromptItems : kRowItems;
+    const long long n = std::max(1, device_sm_count()), key_items = 6 * n;
+    const long long row_items = 2LL * max_new >= (long long)max_blocks * block_size ? n : 4 * n;
     const long long Tq = kTile / (n_heads / n_kv_heads), bh = (long long)batch * n_kv_heads;
     const long long items = (max_new + 2 * Tq - 1) / (2 * Tq) * bh;
     const long long tiles = ((long long)max_blocks * block_size + kWide - 1) / kWide;
     ObsSplit s;
-    s.pieces = (int)std::max<long long>(1, std::min<long long>({16, (row_items + items - 1) / items, (tiles + kObsPieceTiles - 1) / kObsPieceTiles}));
-    s.key_ctas = (int)std::max<long long>(1, std::min<long long>((kKeyItems + bh - 1) / bh, tiles));
+    s.pieces = (int)std::max<long long>(1, std::min<long long>({kObsMostPieces, (row_items + items - 1) / items, (tiles + kObsPieceTiles - 1) / kObsPieceTiles}));
+    s.key_ctas = (int)std::max<long long>(1, std::min<long long>((key_items + bh - 1) / bh, tiles));
     s.row_items = items * s.pieces;
     s.key_items = bh * s.key_ctas;
     s.few = max_new <= 2 * Tq;
     if (s.few) {                                             // shares: a head's keys in at most so many parts
-        const long long n = std::max(1, device_sm_count());
         s.pieces = (int)std::max<long long>(2, std::min({(n + n_kv_heads - 1) / n_kv_heads + 1, 4 * n / bh + 2, tiles}));
         s.row_items = s.key_items = bh * tiles;
     }
@@ -764,11 +764,21 @@ bool observe_fits(int batch, int max_new, int n_heads, int n_kv_heads, int max_b
     return s.few || (s.row_items < (1LL << 31) && s.key_items < (1LL << 31));
 }
 
-size_t observe_scratch_bytes(int batch, int tokens, int max_new, int n_heads, int n_kv_heads, int max_blocks, int block_size) {
-    // the normalisers, and a (max, sum) for each piece of a row
+// The normalisers, and a (max, sum) for each piece of a row.
+static size_t observe_bytes(int tokens, int n_heads, long long pieces) {
     const size_t rows = (size_t)tokens * n_heads;
-    return (rows * sizeof(float) + 15) / 16 * 16 +
-           rows * obs_split(batch, std::max(max_new, 1), n_heads, n_kv_heads, max_blocks, block_size).pieces * sizeof(float2);
+    return (rows * sizeof(float) + 15) / 16 * 16 + rows * pieces * sizeof(float2);
+}
+
+size_t observe_scratch_bytes(int batch, int tokens, int max_new, int n_heads, int n_kv_heads, int max_blocks, int block_size) {
+    return observe_bytes(tokens, n_heads, obs_split(batch, std::max(max_new, 1), n_heads, n_kv_heads, max_blocks, block_size).pieces);
+}
+
+size_t observe_workspace_bytes(int tokens, int n_heads, int n_kv_heads, int max_blocks, int block_size) {
+    // (fewer rows and sequences are cut into more pieces: the most that obs_split gives any)
+    const long long n = std::max(1, device_sm_count()), tiles = ((long long)max_blocks * block_size + kWide - 1) / kWide;
+    const long long few = (n + n_kv_heads - 1) / n_kv_heads + 1;
+    return observe_bytes(tokens, n_heads, std::max<long long>(2, std::min(tiles, std::max<long long>(few, kObsMostPieces))));
 }
 
 cudaError_t launch_observe(ObserveArgs a, void* workspace, cudaStream_t stream) {

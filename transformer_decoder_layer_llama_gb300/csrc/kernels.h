@@ -313,7 +313,9 @@ struct ObserveArgs {
     int32_t* status;
 };
 bool observe_fits(int batch, int max_new, int n_heads, int n_kv_heads, int max_blocks, int block_size);
+// What a call needs, and what is enough for it and every call of fewer sequences, tokens, rows of a sequence or blocks.
 size_t observe_scratch_bytes(int batch, int tokens, int max_new, int n_heads, int n_kv_heads, int max_blocks, int block_size);
+size_t observe_workspace_bytes(int tokens, int n_heads, int n_kv_heads, int max_blocks, int block_size);
 cudaError_t launch_observe(ObserveArgs a, void* workspace, cudaStream_t stream);
 
 // Which cached rows stay, and their move to the front (evict.cu).
