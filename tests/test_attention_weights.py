@@ -189,3 +189,29 @@ def test_a_workspace_is_enough_for_smaller_calls():
         for batch, tokens, new, blocks in ((8, 2048, 256, 256), (8, 2048, 32, 256), (8, 2048, 1, 256), (1, 2048, 2048, 256), (1, 33, 33, 256),
                                            (3, 2000, 700, 8), (8, 0, 5, 1)):
             assert 0 < size(batch, tokens, new, heads, kv, 128, blocks, 128) <= most
+
+
+def test_the_scheduler_unshares_a_request():
+    from transformer_decoder_layer_llama_gb300.serving import BlockAllocator, Scheduler
+    sch = Scheduler(3, 16, 8, BlockAllocator(14, seed=3), seed=1)
+    sch.start_resident(0, 70)
+    sch.start_resident(1, 20)
+    sch.fork(0, 2)
+    first, second, free = list(sch.slots[0].blocks), list(sch.slots[2].blocks), sch.alloc.free_count()
+    assert sch.unshare(1) == [] and first[:4] == second[:4]
+    pairs = sch.unshare(2)
+    assert [a for a, _ in pairs] == first[:4] and sch.slots[2].blocks == [b for _, b in pairs] + second[4:]
+    assert sch.table[2].tolist() == sch.slots[2].blocks + [-1] * 3 and sch.slots[0].blocks == first
+    assert not set(sch.slots[2].blocks) & set(first) and sch.alloc.free_count() == free - 4
+    for s in range(3):
+        sch.own_blocks(s)
+        assert sch.unshare(s) == []
+    sch.retire(1)
+    sch.fork(0, 1)
+    held, free = list(sch.slots[1].blocks), sch.alloc.free_count()
+    with pytest.raises(MemoryError):
+        sch.unshare(1)
+    assert held == sch.slots[1].blocks and sch.alloc.free_count() == free and sch.held_outside() == []
+    sch.retire(1)
+    with pytest.raises(ValueError):
+        sch.unshare(1)

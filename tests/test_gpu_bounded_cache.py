@@ -514,3 +514,46 @@ def test_a_refused_token_leaves_its_row(why, kind):
         check_status(st, api.LL_DEV_BAD_POSITION)
         for a, old in zip(tensors(p), before):
             assert torch.equal(a[table[far].long()], old[table[far].long()])
+
+
+def test_a_forked_request_is_cut_once_it_has_its_own_blocks():
+    """A fork: the other requests can still be cut, by name; with its blocks copied it can be, too, and the request that it
+    shared them with keeps every byte."""
+    from transformer_decoder_layer_llama_gb300.serving import BlockAllocator, Scheduler, StackEngine
+    d, L, nb, mb, slots = synth.DIMS_TINY, 2, 40, 5, 3
+    cfg, packed = layer(d, 9)
+    sch = Scheduler(slots, d.block_size, mb, BlockAllocator(nb, seed=5), seed=6)
+    pools = [tuple(t.cuda() for t in synth.make_pool(nb, d, seed=l)) for l in range(L)]
+    eng = StackEngine(api, [cfg] * L, [packed] * L, pools, slots, mb, 64, track_weights=True)
+    g = torch.Generator().manual_seed(1)
+    for w in eng.weights:
+        w.copy_(torch.rand(w.shape, generator=g))
+    stream = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    sch.start_resident(0, 60)
+    sch.start_resident(1, 60)
+    eng.copy_blocks(sch.fork(0, 2), stream)
+    eng.copy_weights(0, 2, stream)
+
+    def rows(slot, n):
+        stream.synchronize()
+        return [t[torch.tensor(sch.slots[slot].blocks).cuda()].transpose(1, 2).flatten(0, 1)[:n].clone() for p in pools for t in p]
+    first, other = rows(0, 60), [w.clone() for w in eng.weights]
+    assert all(torch.equal(a, b) for a, b in zip(first, rows(2, 60)))
+    with pytest.raises(ValueError, match="shared"):
+        eng.evict(sch, 32, stream, sinks=2, recent=5)
+    assert eng.evict(sch, 32, stream, sinks=2, recent=5, slots=[1]) == [1] and [r.ctx for r in sch.slots] == [60, 32, 60]
+    assert all(torch.equal(a, b) for s in (0, 2) for a, b in zip(first, rows(s, 60)))
+    eng.copy_blocks(sch.unshare(2), stream)
+    assert all(torch.equal(a, b) for s in (0, 2) for a, b in zip(first, rows(s, 60)))
+    assert eng.evict(sch, 32, stream, sinks=2, recent=5, slots=[1, 2]) == [2] and [r.ctx for r in sch.slots] == [60, 32, 32]
+    assert all(torch.equal(a, b) for a, b in zip(first, rows(0, 60)))
+    got = rows(2, 32)
+    for l in range(L):
+        for h in range(d.n_kv_heads):
+            keep = torch.from_numpy(W.keep_rows(other[l][2, h, :60].cpu().numpy(), 32, 2, 5)).cuda()
+            for i in range(2):
+                assert torch.equal(got[2 * l + i][:, h], first[2 * l + i][keep, h])
+            assert torch.equal(eng.weights[l][2, h, :32], other[l][2, h, keep]) and (eng.weights[l][2, h, 32:60] == 0).all()
+        assert torch.equal(eng.weights[l][0], other[l][0])
+    assert eng.evict(sch, 32, stream, sinks=2, recent=5) == [0] and int(eng.status.item()) == 0

@@ -186,7 +186,22 @@ class Scheduler:
             raise ValueError(f"slot {slot} is empty")
         shared = [b for b in r.blocks if self.alloc.holders(b) > 1]
         if shared:
-            raise ValueError(f"blocks {shared[:8]} of slot {slot} are shared: copy them before rows move in them")
+            raise ValueError(f"blocks {shared[:8]} of slot {slot} are shared: unshare the slot before rows move in them")
+
+    def unshare(self, slot: int) -> list:
+        """Gives the request in a slot blocks of its own in the place of those that somebody else holds too.  Returns the
+        (from, to) block pairs to copy in every pool (StackEngine.copy_blocks) before the request goes on; with too few
+        free blocks MemoryError, and nothing is changed."""
+        r = self.slots[slot]
+        if r is None:
+            raise ValueError(f"slot {slot} is empty")
+        at = [i for i, b in enumerate(r.blocks) if self.alloc.holders(b) > 1]
+        pairs = [(r.blocks[i], b) for i, b in zip(at, self.alloc.alloc(len(at)))]
+        self.alloc.free(b for b, _ in pairs)
+        for i, (_, b) in zip(at, pairs):
+            r.blocks[i] = b
+        self._set_blocks(slot, r.blocks)
+        return pairs
 
     def cut(self, slot: int, ctx: int) -> None:
         """The cache of the request in a slot now has its first `ctx` places only (as an eviction leaves it): the blocks
@@ -407,20 +422,21 @@ class StackEngine:
             for w in self.weights:
                 w[dst].copy_(w[src])
 
-    def evict(self, scheduler: Scheduler, keep, stream, sinks=0, recent=0) -> list:
-        """Cuts every request with more than `keep` cached tokens down to `keep` in every layer: each KV head keeps the
-        first `sinks`, the last `recent`, and of the others those of the largest attention weight.  Frees the blocks
-        behind them in the scheduler (what reuses them must come behind this on `stream`); returns the slots that were
-        cut.  Where such a request shares a block, ValueError before anything is moved."""
+    def evict(self, scheduler: Scheduler, keep, stream, sinks=0, recent=0, slots=None) -> list:
+        """Cuts every request (of those in `slots`, where given) with more than `keep` cached tokens down to `keep` in every
+        layer: each KV head keeps the first `sinks`, the last `recent`, and of the others those of the largest attention
+        weight.  Frees the blocks behind them in the scheduler (what reuses them must come behind this on `stream`);
+        returns the slots that were cut.  Where such a request shares a block (Scheduler.unshare), ValueError before
+        anything is moved."""
         if self.weights is None:
             raise ValueError("evict needs track_weights")
-        slots = [s for s, r in enumerate(scheduler.slots) if r is not None and r.ctx > keep]
+        slots = [s for s, r in enumerate(scheduler.slots) if r is not None and r.ctx > keep and (slots is None or s in slots)]
         for s in slots:
             scheduler.own_blocks(s)
         if not slots:
             return slots
-        lens = np.array([r.ctx if r is not None else 0 for r in scheduler.slots], np.int32)
-        lens[lens <= keep] = 0                                # (nothing of the others is looked at)
+        lens = np.zeros(self.n_slots, np.int32)               # (nothing of the others is looked at)
+        lens[slots] = [scheduler.slots[s].ctx for s in slots]
         stream.wait_stream(torch.cuda.current_stream(self.table.device))
         with torch.cuda.stream(stream):                       # behind the steps that still read the table
             self.table.copy_(torch.from_numpy(scheduler.table))
