@@ -559,7 +559,9 @@ int ll_paged_attention_decode_weights(const void* q, const ll_kv_pool* pool, con
                                       int32_t head_dim, int32_t block_size, float scale, float* weights, int32_t weights_width,
                                       void* out, void* workspace, size_t workspace_bytes, int32_t* status, void* stream);
 
-/* The same over an INT8 pool (output as ll_paged_attention_decode_q8; head_dim 128). */
+/* The same over an INT8 pool (output as ll_paged_attention_decode_q8; head_dim 128).  Queries
+ * enter the scores, and so the weights, as FP16 there: exact between 2^-14 and 65504 in
+ * size, in steps of 2^-24 below; an element beyond is infinite. */
 int ll_paged_attention_decode_weights_q8(const void* q, const ll_kv_pool_q8* pool, const int32_t* block_table, int32_t max_blocks,
                                          const int32_t* context_lens, int32_t batch, int32_t n_heads, int32_t n_kv_heads,
                                          int32_t head_dim, int32_t block_size, float scale, float* weights, int32_t weights_width,

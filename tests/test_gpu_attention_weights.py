@@ -539,3 +539,32 @@ def test_one_workspace_for_smaller_calls(heads, kv):
     with pytest.raises(api.LayerError):
         api.paged_attention_weights(*args, a, 1, workspace=ws[:16], status=st)
     check_status(st)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "int8", "noalloc"])
+def test_plain_decode_calls_of_a_stream_share_a_workspace(kind):
+    """The calls without weights, of batches whose dispatch orders lie in each other's partials, without a wait between."""
+    H, Hkv, d, block, scale = 8, 2, 128, 64, 0.09
+    cases = [Paged(ctx, Hkv, d, block, 20 + i, kind == "int8") for i, ctx in enumerate(([8200, 9000, 8700], [8300], [8500, 8193], [700], [9000] * 4))]
+    if kind != "int8":
+        cases = [c for c in cases if c.table.shape[1] * block > 7 * 1024]       # (with a dispatch order)
+    g = torch.Generator().manual_seed(6)
+    q, st = [torch.randn(len(c.ctx), H, d, generator=g).bfloat16().cuda() for c in cases], api.new_status()
+    size = max(api.attention_workspace_size(len(c.ctx), H, d, c.table.shape[1], block) for c in cases)
+    ws = torch.full((size,), 255, dtype=torch.uint8, device="cuda")
+
+    def call(c, x, **kw):
+        if kind == "int8":
+            return api.paged_attention_decode_q8(x, c.pool, c.d_table, c.d_ctx, scale, status=st, **kw)
+        if kind == "noalloc" and kw:
+            return api.paged_attention_decode_noalloc(x, c.k, c.v, c.d_table, c.d_ctx, scale, status=st)
+        return api.paged_attention_decode(x, c.k, c.v, c.d_table, c.d_ctx, scale, status=st, **kw)
+
+    want = []
+    for c, x in zip(cases, q):
+        want.append(call(c, x))
+        check_status(st)
+    for _ in range(30):
+        got = [call(c, x, workspace=ws) for c, x in zip(cases, q)]
+        check_status(st)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
