@@ -430,7 +430,8 @@ class StackEngine:
         anything is moved."""
         if self.weights is None:
             raise ValueError("evict needs track_weights")
-        slots = [s for s, r in enumerate(scheduler.slots) if r is not None and r.ctx > keep and (slots is None or s in slots)]
+        asked = range(self.n_slots) if slots is None else set(slots)
+        slots = [s for s, r in enumerate(scheduler.slots) if r is not None and r.ctx > keep and s in asked]
         for s in slots:
             scheduler.own_blocks(s)
         if not slots:
